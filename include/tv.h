@@ -54,7 +54,8 @@ typedef enum {
   TV_ERR_CUDA = -4,         /* a CUDA runtime/driver call failed (see tv_last_error) */
   TV_ERR_TIMEOUT = -5,      /* a bounded device-side wait gave up (device status only) */
   TV_ERR_WORKSPACE = -6,    /* workspace missing or smaller than the size query asked for */
-  TV_ERR_BOUNDS = -7        /* prefix_len[b] + Q exceeds the cache geometry (device) */
+  TV_ERR_BOUNDS = -7,       /* prefix_len[b] + Q exceeds the cache geometry (device) */
+  TV_ERR_NO_PAGES = -8      /* too few free pages in the pool (device status only) */
 } tv_status;
 
 typedef enum { TV_F32 = 0, TV_BF16 = 1 } tv_dtype;
@@ -392,6 +393,178 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
                   int64_t kpe_row_stride, int d_latent, int d_rope,
                   const tv_cache_layout* cache, const int32_t* prefix_len, const int32_t* path,
                   const int32_t* accept_len, int B, int Q, int32_t* new_prefix_len,
+                  int32_t* status, void* stream);
+
+/*
+ * tv_tree_sample -- sampled acceptance of a verified draft tree.
+ *
+ * The counterpart of tv_tree_accept for a target that is sampled from: every emitted token
+ * is distributed as the target's own p = softmax(logits[b,n] / T_b) at its node n, whatever
+ * the drafter proposed.  The random numbers are inputs.  From the root, the children of the
+ * current node are tested in index order with their own uniform numbers; with unnormalised
+ * weights w = p and W = sum w:
+ *   draft_probs NULL (candidates chosen without chance, as by tv_build_tree):
+ *       child c is accepted iff  uniforms[b,c] * W < w[x_c]; else w[x_c] = 0.
+ *   draft_probs given (the children of a node are a draw without replacement from the
+ *   drafter's distribution g there, in index order; G = 1 at first):
+ *       child c is accepted iff  uniforms[b,c] * g[x_c] * W < w[x_c] * G; else
+ *       w = max(w - g * W/G, 0), G = G - g[x_c], g[x_c] = 0; no child is tested any more
+ *       once G <= 0, and if no weight is left after a rejection the child is accepted
+ *       after all (w and g are then equal but for rounding).
+ * With no child accepted (any more) the walk ends and the bonus token is the smallest v
+ * with w[0] + .. + w[v] > uniforms[b,0] * W.  T_b = 0 is greedy: w is 1 at the largest
+ * logit (the smallest index among equals) and 0 elsewhere; the result then equals
+ * tv_tree_accept's.
+ *
+ * Weights are integers in units of 2^-44 of the row's largest and their sums are exact, so
+ * results do not depend on how a row is split, and equal those of the rule in 64-bit
+ * arithmetic unless a uniform number falls within about 2^-38 of a boundary.
+ */
+typedef enum { TV_DRAFT_BY_DEPTH = 0, TV_DRAFT_BY_NODE = 1 } tv_draft_mode;
+
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_sample_args): ABI check */
+  int32_t B, Q;              /* sequences, tree nodes (1..64) */
+  int64_t vocab;             /* 1 .. 2^18 */
+  const void* logits;        /* device [B, Q, vocab], row (b,i) at logits +
+                                (b*Q+i)*logits_row_stride elements.  -inf masks a token. */
+  tv_dtype logits_dt;        /* F32 or BF16 */
+  int64_t logits_row_stride; /* >= vocab */
+  const float* temperature;  /* device [B], >= 0; nullable (1 for every sequence) */
+  const int32_t* parent;     /* device [B, Q] draft tree */
+  const int32_t* tokens;     /* device [B, Q] draft tokens (entry 0 is not read; a token
+                                outside [0, vocab) is never accepted and not tested) */
+  const float* uniforms;     /* device [B, Q] in [0, 1) (clamped into it; a NaN counts as 0):
+                                entry i > 0 tests node i, entry 0 draws the bonus token */
+  const float* draft_probs;  /* device [B, draft_rows, vocab] float32, rows that sum to 1;
+                                nullable */
+  int64_t draft_row_stride;  /* elements between rows, >= vocab (a sequence's rows follow
+                                the previous one's) */
+  int32_t draft_rows;        /* rows per sequence */
+  int32_t draft_mode;        /* tv_draft_mode: the children of node n were drawn from row
+                                depth(n) (TV_DRAFT_BY_DEPTH) or n (TV_DRAFT_BY_NODE) */
+  int32_t* accept_len;       /* device [B] out, as tv_tree_accept */
+  int32_t* path;             /* device [B, Q] out, as tv_tree_accept */
+  int32_t* new_tokens;       /* device [B, Q] out, as tv_tree_accept */
+  int32_t* status;           /* device int32, nullable.  TV_ERR_INVALID_TREE: invalid parent
+                                array (A = 0, path [0, -1, ..], new_tokens all -1).
+                                TV_ERR_INVALID_ARG: a negative or NaN temperature (same
+                                outputs), or a visited row with a NaN, a +inf or nothing
+                                but -inf (the walk ends there without a bonus token: -1).
+                                TV_ERR_BOUNDS: depth(n) >= draft_rows at a visited node
+                                with children (they are not tested). */
+} tv_sample_args;
+
+/* Returns TV_ERR_UNSUPPORTED for Q > 64 or vocab > 2^18, TV_ERR_INVALID_ARG for bad sizes,
+ * strides, modes or pointers (draft_rows < Q with TV_DRAFT_BY_NODE among them). */
+int tv_tree_sample(const tv_sample_args* a, void* stream);
+
+/*
+ * Pages of a cache: a pool that is kept on the device.
+ *
+ * Rows are the scheduler's sequence slots.  Row r holds the pages page_table[r, 0 ..
+ * n_pages[r]-1]; entries behind them are -1.  refcount[p] counts the table entries that
+ * name page p; 0 means free.  The same page numbers serve every layer's c_kv and k_pe
+ * arrays.  An empty pool has n_pages = 0, refcount = 0 and page_table = -1.  Calls on one
+ * pool that are not ordered by a stream race.  Every per-row argument has one entry for
+ * each of the `rows` slots, so that no row can be named twice.
+ */
+typedef struct {
+  int32_t* page_table; /* device [rows, max_pages] */
+  int32_t* n_pages;    /* device [rows] */
+  int32_t* refcount;   /* device [num_pages] */
+  int32_t rows;        /* 1 .. 4096 */
+  int32_t max_pages;   /* pages per row at most */
+  int32_t num_pages;   /* pages in the pool, < 2^24 */
+  int32_t page_size;   /* tokens per page */
+} tv_page_pool;
+
+/*
+ * tv_pages_reserve -- give rows the pages of the keys they are about to write.
+ *
+ * Row r, holding length[r] keys, is to hold new_length[r]: it gets pages up to
+ * ceil(new_length / page_size), and the pages that keys length .. new_length-1 fall into
+ * become its own.  A shared one (refcount > 1) is replaced by a fresh page, unless every
+ * holder writes it in this call and r is the lowest of them, which keeps it.  If such a
+ * page already holds keys of the row (length % page_size of them), copies[r] says what to
+ * copy.  Fresh pages are dealt in order of (row, page index): the i-th takes the i-th
+ * lowest free page.  Rows with new_length[r] <= length[r] are left alone.
+ *
+ * length, new_length : device [rows] int32.
+ * copies : device [rows, 3] int32 out: {source page, new page, keys to copy}, or {-1, -1,
+ *          0}; the list tv_pages_copy takes (run it for every layer before the keys are
+ *          written).
+ * status : TV_ERR_NO_PAGES: too few free pages; TV_ERR_BOUNDS: a row needs more than
+ *          max_pages, has length > n_pages * page_size or length < 0, or its table names a
+ *          page outside the pool.  In both cases nothing is changed (copies: all {-1, -1, 0}).
+ * workspace : device memory of tv_pages_workspace_size(pool) bytes, 256-byte aligned.
+ */
+size_t tv_pages_workspace_size(const tv_page_pool* pool);
+int tv_pages_reserve(const tv_page_pool* pool, const int32_t* length, const int32_t* new_length,
+                     int32_t* copies, int32_t* status, void* workspace, size_t ws_bytes,
+                     void* stream);
+
+/*
+ * tv_pages_fork -- rows that share another row's first keys.
+ *
+ * fork_from : device [rows] int32: the row to fork from, or -1 for rows left alone.
+ * length    : device [rows] int32: row r shares the first ceil(length[r] / page_size)
+ *             pages of row fork_from[r].  No key is copied; tv_pages_reserve does that for
+ *             the one page that is written again.
+ * status    : TV_ERR_BOUNDS (that row is left alone): the row holds pages already, its
+ *             source is not a row, is itself forked into by this call, or has fewer pages.
+ */
+int tv_pages_fork(const tv_page_pool* pool, const int32_t* fork_from, const int32_t* length,
+                  int32_t* status, void* stream);
+
+/*
+ * tv_pages_release -- drop the pages behind a row's first keys.
+ *
+ * keep   : device [rows] int32: the row keeps its first ceil(keep[r] / page_size) pages (0:
+ *          none); a negative entry, or one that covers every page, leaves the row alone.
+ *          A page that no row names any more is free.
+ * status : TV_ERR_BOUNDS: a dropped entry named no page of the pool, or a free one (the
+ *          entry is dropped, no count changes).
+ */
+int tv_pages_release(const tv_page_pool* pool, const int32_t* keep, int32_t* status, void* stream);
+
+/*
+ * tv_pages_compact -- move the pages in use to the front of the pool.
+ *
+ * With U pages in use, the k-th page in use at U or above (in ascending order) moves to the
+ * k-th free page below U; tables and counts are rewritten, and pages U .. num_pages-1 are
+ * free afterwards.
+ *
+ * moves   : device [num_pages, 3] int32 out: {from, to, page_size}, n_moves entries (the
+ *           rest is left as it was); the list tv_pages_copy takes.  No page is both a
+ *           source and a target.
+ * n_moves : device int32 out.
+ * status  : TV_ERR_BOUNDS: a table entry below n_pages names no page of the pool (it is left
+ *           as it is).
+ * workspace : as for tv_pages_reserve.
+ */
+int tv_pages_compact(const tv_page_pool* pool, int32_t* moves, int32_t* n_moves, int32_t* status,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * tv_pages_copy -- copy pages of the cache arrays as a list says.
+ *
+ * Entry {s, d, n} copies rows s*page_size .. s*page_size+n-1 to rows d*page_size .. of
+ * c_kv and of k_pe (nullable when d_rope is 0) in each of n_layers layers.  Entries with a negative source
+ * or n = 0 are skipped, and so are those whose pages lie outside num_rows rows or whose n
+ * exceeds page_size (TV_ERR_BOUNDS).  No page may be both a source and a target, nor a
+ * target twice.
+ *
+ * c_kv, k_pe : rows of d_latent / d_rope elements at the given row strides, layers at the
+ *              given layer strides (elements; ignored for one layer).  Row sizes, strides
+ *              and pointers are multiples of 16 bytes.
+ * list       : device [n_list, 3] int32.  count: device int32, nullable: only the first
+ *              *count entries (at most n_list).
+ */
+int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride,
+                  int64_t kpe_row_stride, int d_latent, int d_rope, int n_layers,
+                  int64_t ckv_layer_stride, int64_t kpe_layer_stride, int page_size,
+                  int64_t num_rows, const int32_t* list, const int32_t* count, int n_list,
                   int32_t* status, void* stream);
 
 /* Text for a tv_status code (static storage). */

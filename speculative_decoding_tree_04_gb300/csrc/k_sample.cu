@@ -1,0 +1,614 @@
+// k_sample.cu -- sampled acceptance of a verified draft tree (tv_tree_sample).
+//
+// The walk starts at the root.  At node n the target's distribution is
+// p = softmax(logits[n] / T).  The children of n are tested in index order with their own
+// uniform numbers; with weights w (w = p at first, W their sum)
+//   no draft probabilities:  accept child c iff  u_c W < w[x_c]; else w[x_c] = 0
+//   draft probabilities g (G = 1 at first):
+//                            accept child c iff  u_c g[x_c] W < w[x_c] G;
+//                            else w = max(w - g W/G, 0), G -= g[x_c], g[x_c] = 0
+// and when no child is accepted the bonus token is the first v with
+// sum_{i<=v} w_i > u_0 W.  Both rules leave every emitted token distributed as p: the first
+// because "accept c with the probability that p has left for x_c" is a draw from p in
+// disguise, the second because w + (accepted part of g) = p term by term.
+//
+// Subtractions of positive amounts compose, max(max(w - a, 0) - b, 0) = max(w - a - b, 0),
+// so the residual after any number of rejections is max(w - g S, 0) with one scalar S, the
+// sum of the W/G so far; it is recomputed from the logits when it is needed and never
+// stored.  A rejected token's own weight is zero from then on (u < 1).
+//
+// Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
+// that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
+// are as many boundaries as tokens.  Weights are therefore held as integers in units of
+// 2^-44 of the row's largest (rounded from an exponential good to about 2^-38, built from
+// pairs of floats: this part's double-precision units are slow).  Their sums are exact,
+// whatever order they are taken in, so splits, tests and the final search agree with one
+// another to the last unit.  A vocabulary of 2^18 tokens sums to below 2^63.
+//
+// Work.  Only the visited rows are read: accepted length + 1 of Q.  One cluster of CTAs
+// per sequence shares a row; every CTA takes a contiguous slice, sums are exchanged through
+// distributed shared memory, and every CTA takes the same decisions from the same numbers.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "sm100_ptx.h"
+#include "tv_internal.h"
+
+namespace tv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
+constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
+constexpr int kTable = 64;
+
+// 2^(j/64) as the sum of two floats, from the exponential's Taylor series in double.
+struct ExpTable {
+  float hi[kTable], lo[kTable];
+};
+constexpr ExpTable make_exp_table() {
+  ExpTable t{};
+  for (int j = 0; j < kTable; ++j) {
+    const double x = 0.693147180559945309417 * j / kTable;
+    double term = 1.0, sum = 1.0;
+    for (int k = 1; k < 24; ++k) {
+      term *= x / k;
+      sum += term;
+    }
+    t.hi[j] = (float)sum;
+    t.lo[j] = (float)(sum - (double)t.hi[j]);
+  }
+  return t;
+}
+__constant__ ExpTable c_exp = make_exp_table();
+
+struct SampleParams {
+  const void* logits;
+  int64_t V, stride;
+  const float* temperature;
+  const int32_t* parent;
+  const int32_t* tokens;
+  const float* uniforms;
+  const float* draft;
+  int64_t draft_stride;
+  int32_t draft_rows, by_node;
+  int B, Q;
+  int32_t* accept_len;
+  int32_t* path;
+  int32_t* new_tokens;
+  int32_t* status;
+};
+
+// What the walk does next, decided by thread 0 of every CTA alike.
+enum : int { kAccept = 0, kResidual = 1, kDraw = 2 };
+
+struct Shared {
+  float2 exp2_table[kTable];
+  int64_t sums[2][kMaxCluster];   // exchanged slice sums, two phases
+  uint64_t keys[2][kMaxCluster];  // exchanged slice maxima
+  int64_t warp_sum[kWarps];       // of this CTA's slice, by warp
+  uint64_t warp_key[kWarps];
+  int64_t e[64];                  // weight of node i's token in its parent's row
+  float q[64];                    // its draft probability
+  int32_t parent[64], token[64];
+  float u[64];
+  int32_t rejected[64];           // tokens refused at this node, and their weights
+  int64_t rejected_e[64];
+  int n_rejected, cmd, next;
+  float s_hi, s_lo;               // S as a pair of floats
+  int64_t target;                 // the draw's place in the sums, and the vectors it is in
+  int range0, range1;
+};
+
+// 2^((x - m) c) in units of 2^-44, as a float pair until the final rounding.  c = ch + cl.
+// With y = (x - m) c = k/64 + f: 2^y = 2^(k/64) e^(f ln 2), the first factor from the
+// table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).
+__device__ __forceinline__ int64_t weight(float x, float m, float ch, float cl,
+                                          const float2* __restrict__ table) {
+  const float dh = x - m;
+  float yh = dh * ch;
+  if (!(yh > -46.f)) return 0;  // below half a unit; -inf (masked) too
+  const float bb = dh - x;
+  const float dl = (x - (dh - bb)) - (m + bb);
+  const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+  const float k = rintf(yh * (float)kTable);
+  const float f = fmaf(k, -1.f / kTable, yh);  // exact
+  constexpr float ln2h = 0.693147182464599609375f, ln2l = -1.90465429995776804525e-9f;
+  const float zh = f * ln2h;
+  const float zl = fmaf(f, ln2h, -zh) + fmaf(f, ln2l, yl * ln2h);
+  const float p =
+      zh * zh * fmaf(zh, fmaf(zh, fmaf(zh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
+  const float el = fmaf(zh, zl, zl) + p;
+  const int ki = (int)k;
+  const float2 t = table[ki & (kTable - 1)];
+  const float ph = t.x * zh;
+  const float pl = fmaf(t.x, zh, -ph) + fmaf(t.x, el, t.y);
+  const float hi = t.x + ph;
+  const float lo = ((t.x - hi) + ph) + pl;
+  const float scale = __int_as_float(((ki >> 6) + 44 + 127) << 23);
+  return __float2ll_rn(hi * scale) + (int64_t)__float2int_rn(lo * scale);
+}
+
+// max(e - q S, 0) in the same units.
+__device__ __forceinline__ int64_t residual(int64_t e, float q, float sh, float sl) {
+  const float p = q * sh;
+  if (!(p > 0.f)) return e;
+  if (p > 2.f) return 0;  // a weight is at most 1
+  const float pe = fmaf(q, sh, -p) + q * sl;
+  const int64_t r = e - __float2ll_rn(p * kUnit) - __float2ll_rn(pe * kUnit);
+  return r > 0 ? r : 0;
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ static void unpack(const uint4& w, float* x) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+  __device__ static float one(const float* p) { return __ldg(p); }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static void unpack(const uint4& w, float* x) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+};
+
+// A row as 16-byte vectors on 16-byte boundaries: vector j holds elements j*N - off ..,
+// where the row starts `off` elements past a boundary.  Elements outside the row read as
+// -inf, whose weight is zero.
+template <typename T>
+struct Row {
+  const T* x;
+  int64_t V;
+  int off, n_vec;
+  __device__ Row(const T* row, int64_t vocab) : x(row), V(vocab) {
+    off = (int)(((uintptr_t)row & 15u) / sizeof(T));
+    n_vec = (int)((V + off + Vec<T>::N - 1) / Vec<T>::N);
+  }
+  __device__ int vector_of(int64_t v) const { return (int)((v + off) / Vec<T>::N); }
+  __device__ int64_t first(int j) const { return (int64_t)j * Vec<T>::N - off; }
+  __device__ bool whole(int j) const { return first(j) >= 0 && first(j) + Vec<T>::N <= V; }
+  __device__ void load(int j, float* v) const {
+    const int64_t a = first(j);
+    if (whole(j)) {
+      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(x + a)), v);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i)
+      v[i] = a + i >= 0 && a + i < V ? Vec<T>::one(x + a + i) : -INFINITY;
+  }
+};
+
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ void st_cluster_u64(const void* local, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "l"(v)
+               : "memory");
+}
+
+// What turns a row's logits into weights: the row's maximum, the scale 1/T (of log2) and,
+// after rejections under draft probabilities, the drafter's row and S.
+struct Scale {
+  float m, ch, cl;
+  const float* q;
+  float s_hi, s_lo;
+  const float2* table;
+};
+
+// The weights of vector j.
+template <typename T>
+__device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j, int64_t* e) {
+  float v[Vec<T>::N];
+  row.load(j, v);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; ++i) {
+    e[i] = weight(v[i], c.m, c.ch, c.cl, c.table);
+    if (c.s_hi > 0.f && e[i] > 0)
+      e[i] = residual(e[i], __ldg(c.q + row.first(j) + i), c.s_hi, c.s_lo);
+  }
+}
+
+// Sum of the weights of vectors [j0, j1), by one warp.
+template <typename T>
+__device__ __forceinline__ int64_t sum_range(const Row<T>& row, const Scale& c, int j0, int j1) {
+  int64_t s = 0;
+  for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
+    int64_t e[Vec<T>::N];
+    weights(row, c, j, e);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) s += e[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, int C) {
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int b = blockIdx.x / C, Q = p.Q;
+  if (tid < kTable) sh.exp2_table[tid] = make_float2(c_exp.hi[tid], c_exp.lo[tid]);
+  bool ok_tree = true;
+  if (tid < Q) {
+    const int par = p.parent[(int64_t)b * Q + tid];
+    sh.parent[tid] = par;
+    sh.token[tid] = p.tokens[(int64_t)b * Q + tid];
+    // outside [0, 1): the nearest number inside (NaN: 0)
+    sh.u[tid] = fminf(fmaxf(p.uniforms[(int64_t)b * Q + tid], 0.f), 0x1.fffffep-1f);
+    ok_tree = tid == 0 ? par == -1 : (par >= 0 && par < tid);
+  }
+  const float T0 = p.temperature ? p.temperature[b] : 1.f;
+  const bool ok_temp = T0 >= 0.f;  // a NaN is not
+  const bool any_bad = __syncthreads_or(!ok_tree);
+  int32_t* path = p.path + (int64_t)b * Q;
+  int32_t* emit = p.new_tokens + (int64_t)b * Q;
+  if (rank == 0)
+    for (int i = tid; i < Q; i += kThreads) {
+      path[i] = i == 0 ? 0 : -1;
+      emit[i] = -1;
+    }
+  if (any_bad || !ok_temp) {  // the whole cluster alike
+    if (rank == 0 && tid == 0) {
+      p.accept_len[b] = 0;
+      report(p.status, any_bad ? TV_ERR_INVALID_TREE : TV_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  __syncthreads();  // the -1 fill is ordered before the entries written below
+  const bool greedy = T0 == 0.f;
+  // 1/T in units of log2 as a pair of floats; the clamp keeps 0 * inf out of the weights
+  const float cq = 1.44269502162933349609375f / T0;
+  const float ch = fminf(fmaxf(cq, 1e-30f), 1e30f);
+  const float cl =
+      ch == cq ? (fmaf(-cq, T0, 1.44269502162933349609375f) + 1.925963033500011e-8f) / T0 : 0.f;
+
+  int node = 0, count = 0, phase = 0;
+  for (;;) {
+    const Row<T> row((const T*)p.logits + ((int64_t)b * Q + node) * p.stride, p.V);
+    const int per = (row.n_vec + C - 1) / C;
+    const int c0 = min(row.n_vec, (int)rank * per), c1 = min(row.n_vec, c0 + per);
+    const int per_w = (per + kWarps - 1) / kWarps;
+    const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
+    // the children's logits, while the row streams in
+    float child = 0.f;
+    const bool is_child = tid < Q && tid > node && sh.parent[tid] == node &&
+                          sh.token[tid] >= 0 && sh.token[tid] < p.V;
+    const float* q = nullptr;
+    bool has_q = false;
+    if (p.draft) {
+      const int r = p.by_node ? node : count;
+      has_q = r < p.draft_rows;
+      q = p.draft + ((int64_t)b * p.draft_rows + min(r, p.draft_rows - 1)) * p.draft_stride;
+    }
+    if (is_child) {
+      child = Vec<T>::one(row.x + sh.token[tid]);
+      if (has_q) sh.q[tid] = __ldg(q + sh.token[tid]);
+    }
+    // ---- the row's maximum (and, among equal values, its first index) ----
+    uint64_t key = 0;
+    uint32_t nan_bits = 0;
+    for (int j = w0 + lane; j < w1; j += 32 * kUnroll) {
+      float v[kUnroll][Vec<T>::N];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (j + 32 * k < w1) row.load(j + 32 * k, v[k]);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (j + 32 * k >= w1) continue;
+        float m = v[k][0];
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) {
+          nan_bits = max(nan_bits, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+          if (v[k][i] > m) {
+            m = v[k][i];
+            at = i;
+          }
+        }
+        const uint64_t kk = ((uint64_t)ordered(m) << 32) |
+                            (uint32_t)(0xFFFFFFFFu - (uint32_t)(row.first(j + 32 * k) + at));
+        if (m > -INFINITY && kk > key) key = kk;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
+    }
+    // a NaN anywhere beats every value: the largest key of all
+    if (__any_sync(0xffffffffu, nan_bits > 0x7F800000u)) key = ~0ull;
+    if (lane == 0) sh.warp_key[warp] = key;
+    __syncthreads();
+    if (tid < C) {
+      uint64_t k = sh.warp_key[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) k = max(k, sh.warp_key[w]);
+      if (C > 1)
+        st_cluster_u64(&sh.keys[phase][rank], (uint32_t)tid, k);
+      else
+        sh.keys[phase][0] = k;
+    }
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    key = 0;
+    for (int r = 0; r < C; ++r) key = max(key, sh.keys[phase][r]);
+    phase ^= 1;
+    const float m = unordered((uint32_t)(key >> 32));
+    const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
+    if (key == 0 || key == ~0ull || m == INFINITY) {  // nothing to draw from
+      if (rank == 0 && tid == 0) report(p.status, TV_ERR_INVALID_ARG);
+      break;
+    }
+    if (greedy) {
+      if (tid == 0) {
+        int next = -1;
+        for (int i = node + 1; i < Q && next < 0; ++i)
+          if (sh.parent[i] == node && sh.token[i] == top) next = i;
+        sh.next = next;
+      }
+      __syncthreads();
+      const int next = sh.next;
+      if (rank == 0 && tid == 0) emit[count] = top;
+      if (next < 0) break;
+      ++count;
+      if (rank == 0 && tid == 0) path[count] = next;
+      node = next;
+      continue;
+    }
+    // ---- the sum of the weights, the tests, and residual sums after rejections ----
+    Scale sc{m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
+    if (is_child) sh.e[tid] = weight(child, m, ch, cl, sh.exp2_table);
+    // thread 0's: S and G, the child to test next, and whether the residual that is being
+    // summed belongs to the rejection of child at - 1
+    double S = 0.0, G = 1.0;
+    int at = node + 1;
+    bool rejecting = false;
+    if (tid == 0) sh.n_rejected = 0;
+    for (;;) {
+      const int64_t ws = sum_range(row, sc, w0, w1);
+      if (lane == 0) sh.warp_sum[warp] = ws;
+      __syncthreads();
+      if (tid < C) {
+        int64_t t = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sh.warp_sum[w];
+        if (C > 1)
+          st_cluster_u64(&sh.sums[phase][rank], (uint32_t)tid, (uint64_t)t);
+        else
+          sh.sums[phase][0] = t;
+      }
+      if (C > 1) cluster_sync();
+      else __syncthreads();
+      if (tid == 0) {
+        int64_t W = 0;
+        for (int r = 0; r < C; ++r) W += sh.sums[phase][r];
+        int cmd = kDraw, next = -1;
+        if (rejecting && W == 0) {
+          // the drafter covers all that p has left: the two are equal but for rounding
+          cmd = kAccept;
+          next = at - 1;
+        }
+        for (; cmd == kDraw && at < Q; ++at) {
+          if (sh.parent[at] != node || sh.token[at] < 0 || sh.token[at] >= p.V) continue;
+          if (p.draft && !has_q) {  // no drafter's row for this depth: no test
+            if (rank == 0) report(p.status, TV_ERR_BOUNDS);
+            at = Q;
+            break;
+          }
+          if (p.draft && !(G > 0.0)) break;  // nothing left that could have been drawn
+          bool again = false;  // a token refused before has no weight left
+          for (int r = 0; r < sh.n_rejected; ++r) again |= sh.rejected[r] == sh.token[at];
+          const double u = sh.u[at], g = !p.draft ? 1.0 : again ? 0.0 : (double)sh.q[at];
+          const int64_t w = again       ? 0
+                            : !p.draft ? sh.e[at]
+                                       : residual(sh.e[at], sh.q[at], sc.s_hi, sc.s_lo);
+          if (u * g * (double)W < (double)w * G) {
+            cmd = kAccept;
+            next = at;
+            break;
+          }
+          if (!again) {
+            sh.rejected[sh.n_rejected] = sh.token[at];
+            sh.rejected_e[sh.n_rejected++] = w;
+          }
+          if (!p.draft) {
+            W -= w;
+            continue;
+          }
+          cmd = kResidual;
+          rejecting = true;
+          S += (double)W * (1.0 / (double)kUnit) / G;
+          G -= g;
+          sh.s_hi = (float)S;
+          sh.s_lo = (float)(S - (double)(float)S);
+          ++at;
+          break;
+        }
+        if (cmd == kDraw) sh.target = min((int64_t)((double)sh.u[0] * (double)W), W - 1);
+        sh.cmd = cmd;
+        sh.next = next;
+      }
+      __syncthreads();
+      if (sh.cmd != kResidual) break;
+      sc.s_hi = sh.s_hi;
+      sc.s_lo = sh.s_lo;
+      phase ^= 1;
+    }
+    if (sh.cmd == kAccept) {
+      node = sh.next;
+      if (rank == 0 && tid == 0) {
+        emit[count] = sh.token[node];
+        path[count + 1] = node;
+      }
+      ++count;
+      phase ^= 1;
+      continue;
+    }
+    // ---- the draw: the slice, the warp's part, a sixteenth of it, the vector, the token ----
+    const int n_out = p.draft ? 0 : sh.n_rejected;  // weights still in the sums
+    if (tid == 0) {
+      int64_t t = sh.target;
+      int owner = 0, w = 0;
+      for (; owner < C - 1; ++owner) {
+        int64_t s = sh.sums[phase][owner];
+        for (int r = 0; r < n_out; ++r)
+          if (row.vector_of(sh.rejected[r]) / per == owner) s -= sh.rejected_e[r];
+        if (t < s) break;
+        t -= s;
+      }
+      if (owner == (int)rank) {
+        for (; w < kWarps - 1; ++w) {
+          int64_t s = sh.warp_sum[w];
+          for (int r = 0; r < n_out; ++r) {
+            const int j = row.vector_of(sh.rejected[r]) - c0;
+            if (j >= 0 && j < c1 - c0 && j / per_w == w) s -= sh.rejected_e[r];
+          }
+          if (t < s) break;
+          t -= s;
+        }
+        sh.range0 = min(c1, c0 + w * per_w);
+        sh.range1 = min(c1, sh.range0 + per_w);
+        sh.target = t;
+      }
+      sh.next = owner;
+    }
+    __syncthreads();
+    if (sh.next != (int)rank) break;
+    const int r0 = sh.range0, r1 = sh.range1, per_r = (r1 - r0 + kWarps - 1) / kWarps;
+    const int x0 = min(r1, r0 + warp * per_r), x1 = min(r1, x0 + per_r);
+    int64_t part = sum_range(row, sc, x0, x1);
+    for (int r = 0; r < n_out; ++r) {
+      const int j = row.vector_of(sh.rejected[r]);
+      if (j >= x0 && j < x1) part -= sh.rejected_e[r];
+    }
+    __syncthreads();  // thread 0 has read the sums of the parts before
+    if (lane == 0) sh.warp_sum[warp] = part;
+    __syncthreads();
+    if (warp == 0) {
+      int64_t t = sh.target;
+      int w = 0;
+      for (; w < kWarps - 1 && t >= sh.warp_sum[w]; ++w) t -= sh.warp_sum[w];
+      const int y0 = min(r1, r0 + w * per_r), y1 = min(r1, y0 + per_r);
+      for (int j = y0; j < y1; j += 32) {
+        int64_t e[Vec<T>::N], s = 0;
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) e[i] = 0;
+        if (j + lane < y1) weights(row, sc, j + lane, e);
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) {
+          for (int r = 0; r < n_out; ++r)
+            if (row.first(j + lane) + i == sh.rejected[r]) e[i] = 0;
+          s += e[i];
+        }
+        int64_t up_to = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
+          if (lane >= o) up_to += below;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, up_to > t);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            t -= up_to - s;
+            int at_v = 0;
+#pragma unroll
+            for (int i = 0; i < Vec<T>::N; ++i) {
+              if (t >= e[i]) ++at_v;
+              else break;
+              t -= e[i];
+            }
+            emit[count] = (int32_t)(row.first(j + lane) + at_v);
+          }
+          break;
+        }
+        t -= __shfl_sync(0xffffffffu, up_to, 31);
+      }
+    }
+    break;
+  }
+  if (rank == 0 && tid == 0) p.accept_len[b] = count;
+  if (C > 1) cluster_sync();  // no CTA leaves while another may still write to it
+}
+
+template <typename T>
+cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.B * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (C > 8) {
+    cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<T>,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T>, p, C);
+}
+
+}  // namespace
+
+// CTAs per sequence: as many as fill the GPU once, at most 16 and at least about 2048
+// vocabulary entries each.
+int sample_cluster(int B, int64_t V, int sm_count) {
+  int C = kMaxCluster;
+  while (C > 1 && ((int64_t)B * C > sm_count || V < 2048ll * C)) C /= 2;
+  return C;
+}
+
+cudaError_t launch_tree_sample(const tv_sample_args* a, int sm_count, cudaStream_t st) {
+  if (a->B == 0) return cudaSuccess;
+  SampleParams p{};
+  p.logits = a->logits;
+  p.V = a->vocab;
+  p.stride = a->logits_row_stride;
+  p.temperature = a->temperature;
+  p.parent = a->parent;
+  p.tokens = a->tokens;
+  p.uniforms = a->uniforms;
+  p.draft = a->draft_probs;
+  p.draft_stride = a->draft_row_stride;
+  p.draft_rows = a->draft_rows;
+  p.by_node = a->draft_mode == TV_DRAFT_BY_NODE;
+  p.B = a->B;
+  p.Q = a->Q;
+  p.accept_len = a->accept_len;
+  p.path = a->path;
+  p.new_tokens = a->new_tokens;
+  p.status = a->status;
+  const int C = sample_cluster(a->B, a->vocab, sm_count);
+  return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, C, st) : launch<float>(p, C, st);
+}
+
+}  // namespace tv

@@ -123,6 +123,7 @@ const char* tv_status_string(int code) {
     case TV_ERR_TIMEOUT: return "device wait timed out";
     case TV_ERR_WORKSPACE: return "workspace missing or too small";
     case TV_ERR_BOUNDS: return "prefix length outside the cache geometry";
+    case TV_ERR_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }
@@ -347,6 +348,145 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
                                      accept_len, B, Q, new_prefix_len, status,
                                      (cudaStream_t)stream);
   return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_compact_kv");
+}
+
+int tv_tree_sample(const tv_sample_args* a, void* stream) {
+  g_last_error.clear();
+  if (!a) return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: args is NULL%s");
+  if (a->struct_size != sizeof(tv_sample_args))
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: struct_size mismatch (ABI)%s");
+  if (a->B < 0 || a->Q < 1 || a->vocab < 1)
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: bad B, Q or vocab%s");
+  if (a->Q > 64) return fail(TV_ERR_UNSUPPORTED, "tv_tree_sample: Q > 64 not supported%s");
+  if (a->vocab > (1 << 18))
+    return fail(TV_ERR_UNSUPPORTED, "tv_tree_sample: vocab > 2^18 not supported%s");
+  if (a->B >= (1 << 24)) return fail(TV_ERR_UNSUPPORTED, "tv_tree_sample: B must be below 2^24%s");
+  if (!(a->logits_dt == TV_F32 || a->logits_dt == TV_BF16))
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: logits must be F32 or BF16%s");
+  if (a->logits_row_stride < a->vocab)
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: row stride smaller than the row%s");
+  if (a->draft_probs) {
+    if (a->draft_mode != TV_DRAFT_BY_DEPTH && a->draft_mode != TV_DRAFT_BY_NODE)
+      return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: bad draft_mode%s");
+    if (a->draft_row_stride < a->vocab || a->draft_rows < 1 ||
+        (a->draft_mode == TV_DRAFT_BY_NODE && a->draft_rows < a->Q))
+      return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: bad draft_rows or draft_row_stride%s");
+    if ((uintptr_t)a->draft_probs % 4)
+      return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: draft_probs not aligned to 4 bytes%s");
+  }
+  if (a->B == 0) return TV_OK;
+  if (!a->logits || !a->parent || !a->tokens || !a->uniforms || !a->accept_len || !a->path ||
+      !a->new_tokens)
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: NULL pointer%s");
+  const uintptr_t es = a->logits_dt == TV_BF16 ? 2 : 4;
+  if ((uintptr_t)a->logits % es)
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: logits not aligned to its element size%s");
+  cudaError_t e = tv::launch_tree_sample(a, sm_count(), (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_tree_sample");
+}
+
+static int check_pool(const tv_page_pool* p, const char* who) {
+  if (!p) return fail(TV_ERR_INVALID_ARG, "%s: pool is NULL", who);
+  if (p->rows < 1 || p->max_pages < 1 || p->num_pages < 1 || p->page_size < 1)
+    return fail(TV_ERR_INVALID_ARG, "%s: bad rows, max_pages, num_pages or page_size", who);
+  if (p->rows > 4096 || p->num_pages >= (1 << 24) ||
+      (int64_t)p->max_pages * p->page_size >= (1ll << 31))
+    return fail(TV_ERR_UNSUPPORTED,
+                "%s: needs rows <= 4096, num_pages < 2^24, max_pages * page_size < 2^31", who);
+  if (!p->page_table || !p->n_pages || !p->refcount)
+    return fail(TV_ERR_INVALID_ARG, "%s: NULL pool array", who);
+  return TV_OK;
+}
+
+static int check_pool_workspace(const tv_page_pool* p, void* ws, size_t ws_bytes,
+                                const char* who) {
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < tv::pages_workspace(*p))
+    return fail(TV_ERR_WORKSPACE,
+                "%s: workspace missing, misaligned or smaller than tv_pages_workspace_size()", who);
+  return TV_OK;
+}
+
+size_t tv_pages_workspace_size(const tv_page_pool* p) {
+  g_last_error.clear();
+  return check_pool(p, "tv_pages_workspace_size") == TV_OK ? tv::pages_workspace(*p) : 0;
+}
+
+int tv_pages_reserve(const tv_page_pool* p, const int32_t* length, const int32_t* new_length,
+                     int32_t* copies, int32_t* status, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  g_last_error.clear();
+  int rc = check_pool(p, "tv_pages_reserve");
+  if (rc != TV_OK) return rc;
+  if (!length || !new_length || !copies)
+    return fail(TV_ERR_INVALID_ARG, "tv_pages_reserve: NULL pointer%s");
+  rc = check_pool_workspace(p, workspace, ws_bytes, "tv_pages_reserve");
+  if (rc != TV_OK) return rc;
+  cudaError_t e = tv::launch_pages_reserve(*p, length, new_length, copies, status, workspace,
+                                           (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_reserve");
+}
+
+int tv_pages_fork(const tv_page_pool* p, const int32_t* fork_from, const int32_t* length,
+                  int32_t* status, void* stream) {
+  g_last_error.clear();
+  const int rc = check_pool(p, "tv_pages_fork");
+  if (rc != TV_OK) return rc;
+  if (!fork_from || !length) return fail(TV_ERR_INVALID_ARG, "tv_pages_fork: NULL pointer%s");
+  cudaError_t e = tv::launch_pages_fork(*p, fork_from, length, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_fork");
+}
+
+int tv_pages_release(const tv_page_pool* p, const int32_t* keep, int32_t* status, void* stream) {
+  g_last_error.clear();
+  const int rc = check_pool(p, "tv_pages_release");
+  if (rc != TV_OK) return rc;
+  if (!keep) return fail(TV_ERR_INVALID_ARG, "tv_pages_release: NULL pointer%s");
+  cudaError_t e = tv::launch_pages_release(*p, keep, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_release");
+}
+
+int tv_pages_compact(const tv_page_pool* p, int32_t* moves, int32_t* n_moves, int32_t* status,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  int rc = check_pool(p, "tv_pages_compact");
+  if (rc != TV_OK) return rc;
+  if (!moves || !n_moves) return fail(TV_ERR_INVALID_ARG, "tv_pages_compact: NULL pointer%s");
+  rc = check_pool_workspace(p, workspace, ws_bytes, "tv_pages_compact");
+  if (rc != TV_OK) return rc;
+  cudaError_t e = tv::launch_pages_compact(*p, moves, n_moves, status, workspace,
+                                           (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_compact");
+}
+
+int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride,
+                  int64_t kpe_row_stride, int d_latent, int d_rope, int n_layers,
+                  int64_t ckv_layer_stride, int64_t kpe_layer_stride, int page_size,
+                  int64_t num_rows, const int32_t* list, const int32_t* count, int n_list,
+                  int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (d_latent < 1 || d_rope < 0 || n_layers < 1 || page_size < 1 || num_rows < 0 || n_list < 0)
+    return fail(TV_ERR_INVALID_ARG, "tv_pages_copy: bad sizes%s");
+  if (d_latent > 65536 || d_rope > 65536 || page_size > 65536)
+    return fail(TV_ERR_UNSUPPORTED, "tv_pages_copy: rows and pages of at most 65536%s");
+  if (!(kv_dt == TV_F32 || kv_dt == TV_BF16))
+    return fail(TV_ERR_INVALID_ARG, "tv_pages_copy: bad dtype%s");
+  if (n_list == 0) return TV_OK;
+  if (!c_kv || (d_rope > 0 && !k_pe) || !list)
+    return fail(TV_ERR_INVALID_ARG, "tv_pages_copy: NULL pointer%s");
+  const int64_t es = kv_dt == TV_BF16 ? 2 : 4;
+  if (n_layers == 1) ckv_layer_stride = kpe_layer_stride = 0;
+  if (ckv_row_stride < d_latent || (d_rope > 0 && kpe_row_stride < d_rope) ||
+      ckv_layer_stride < 0 || kpe_layer_stride < 0 || (d_latent * es) % 16 || (d_rope * es) % 16 ||
+      (ckv_row_stride * es) % 16 || (ckv_layer_stride * es) % 16 || !aligned16(c_kv) ||
+      (d_rope > 0 &&
+       ((kpe_row_stride * es) % 16 || (kpe_layer_stride * es) % 16 || !aligned16(k_pe))))
+    return fail(TV_ERR_INVALID_ARG,
+                "tv_pages_copy: rows, strides and pointers must be 16-byte multiples%s");
+  cudaError_t e = tv::launch_pages_copy(
+      c_kv, k_pe, ckv_row_stride * es, kpe_row_stride * es, (int)(d_latent * es),
+      (int)(d_rope * es), n_layers, ckv_layer_stride * es, kpe_layer_stride * es, page_size,
+      num_rows, list, count, n_list, status, (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_copy");
 }
 
 }  // extern "C"

@@ -103,6 +103,28 @@ cudaError_t launch_build_tree(const float* lp, const int32_t* tok, const int32_t
                               int L, int K, int budget, int32_t* parent, int32_t* tokens,
                               int32_t* depth, float* score, int32_t* status, cudaStream_t st);
 
+// Sampled tree acceptance (k_sample.cu).
+int sample_cluster(int B, int64_t V, int sm_count);
+cudaError_t launch_tree_sample(const tv_sample_args* a, int sm_count, cudaStream_t st);
+
+// Pages of the cache (k_pages.cu).
+size_t pages_workspace(const tv_page_pool& p);
+cudaError_t launch_pages_reserve(const tv_page_pool& p, const int32_t* length,
+                                 const int32_t* new_length, int32_t* copies, int32_t* status,
+                                 void* ws, cudaStream_t st);
+cudaError_t launch_pages_fork(const tv_page_pool& p, const int32_t* fork_from,
+                              const int32_t* length, int32_t* status, cudaStream_t st);
+cudaError_t launch_pages_release(const tv_page_pool& p, const int32_t* keep, int32_t* status,
+                                 cudaStream_t st);
+cudaError_t launch_pages_compact(const tv_page_pool& p, int32_t* moves, int32_t* n_moves,
+                                 int32_t* status, void* ws, cudaStream_t st);
+// Strides and row sizes in bytes, multiples of 16.
+cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_t kpe_stride,
+                              int ckv_row, int kpe_row, int n_layers, int64_t ckv_layer,
+                              int64_t kpe_layer, int page_size, int64_t num_rows,
+                              const int32_t* list, const int32_t* count, int n_list,
+                              int32_t* status, cudaStream_t st);
+
 // Set the thread-local text returned by tv_last_error() (defined in tv_api.cu).
 void set_last_error(const char* msg);
 

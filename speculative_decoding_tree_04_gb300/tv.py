@@ -12,6 +12,10 @@ this module raises.
     build_tree(logprobs, cand_tokens, budget, parent, tokens, root=None, depth=None, ...)
     tree_accept(logits, parent, tokens, accept_len, path, new_tokens, target=None, ...)
     compact_kv(c_kv, k_pe, cache, prefix_len, path, accept_len, new_prefix_len, ...)
+    tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens, ...)
+    pages_reserve(pool, length, new_length, copies, ...), pages_fork(pool, fork_from, length),
+    pages_release(pool, keep), pages_compact(pool, moves, n_moves),
+    pages_copy(c_kv, k_pe, page_size, copies, ...)
 """
 from __future__ import annotations
 
@@ -27,10 +31,12 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "tv.h")
 
 TV_OK, TV_ERR_INVALID_ARG, TV_ERR_INVALID_TREE, TV_ERR_UNSUPPORTED = 0, -1, -2, -3
 TV_ERR_CUDA, TV_ERR_TIMEOUT, TV_ERR_WORKSPACE, TV_ERR_BOUNDS = -4, -5, -6, -7
+TV_ERR_NO_PAGES = -8
 TV_F32, TV_BF16 = 0, 1
 PATH_AUTO, PATH_SIMT, PATH_TCGEN05 = 0, 1, 2
 PAGED_AUTO, PAGED_STEP_MAPS, PAGED_GATHER = 0, 1, 2
 MASK_TREE, MASK_CAUSAL = 0, 1
+DRAFT_BY_DEPTH, DRAFT_BY_NODE = 0, 1
 
 
 class TVError(RuntimeError):
@@ -86,6 +92,33 @@ class PrologueArgs(ctypes.Structure):
     ]
 
 
+class SampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("B", ctypes.c_int32), ("Q", ctypes.c_int32),
+        ("vocab", ctypes.c_int64),
+        ("logits", ctypes.c_void_p), ("logits_dt", ctypes.c_int),
+        ("logits_row_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_void_p),
+        ("parent", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+        ("uniforms", ctypes.c_void_p),
+        ("draft_probs", ctypes.c_void_p), ("draft_row_stride", ctypes.c_int64),
+        ("draft_rows", ctypes.c_int32), ("draft_mode", ctypes.c_int32),
+        ("accept_len", ctypes.c_void_p), ("path", ctypes.c_void_p),
+        ("new_tokens", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -122,6 +155,16 @@ def load():
                                    ctypes.c_size_t, P]
     lib.tv_compact_kv.argtypes = [P, P, i32, i64, i64, i32, i32, ctypes.POINTER(CacheLayout),
                                   P, P, P, i32, i32, P, P, P]
+    lib.tv_tree_sample.argtypes = [ctypes.POINTER(SampleArgs), P]
+    POOL, sz = ctypes.POINTER(PagePool), ctypes.c_size_t
+    lib.tv_pages_workspace_size.argtypes = [POOL]
+    lib.tv_pages_workspace_size.restype = sz
+    lib.tv_pages_reserve.argtypes = [POOL, P, P, P, P, P, sz, P]
+    lib.tv_pages_fork.argtypes = [POOL, P, P, P, P]
+    lib.tv_pages_release.argtypes = [POOL, P, P, P]
+    lib.tv_pages_compact.argtypes = [POOL, P, P, P, P, sz, P]
+    lib.tv_pages_copy.argtypes = [P, P, i32, i64, i64, i32, i32, i32, i64, i64, i32, i64, P, P,
+                                  i32, P, P]
     _lib = lib
     return lib
 
@@ -406,3 +449,205 @@ def verify_prologue(parent, prefix_len, q_pe_in, q_pe_out, kpe_tree, ckv_tree, c
     a.status = None if status is None else status.data_ptr()
     rc = load().tv_verify_prologue(ctypes.byref(a), _stream(stream))
     _check(rc, "tv_verify_prologue")
+
+
+def _on_device(*ts):
+    """Check that every tensor given lives on one CUDA device, and return that device."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libtv takes CUDA tensors only")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+class _launch:
+    """The stream to launch on (default: the tensors' device's current one), with that
+    device current meanwhile.  A stream of another device is refused."""
+
+    def __init__(self, dev, stream):
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"tensors on {dev}, stream on {stream.device}")
+        self.stream = stream
+        self.handle = ctypes.c_void_p(stream.cuda_stream)
+        self.other = dev.index if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.other is not None:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.other)
+        return self
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _scratch(kind, dev, stream, need):
+    """Workspace of `need` bytes for one call on `stream`: one buffer per device, stream
+    and kind of call, grown when needed.  During a capture the buffer is the graph's own:
+    graphs that share one could replay at the same time, and it must outlive them."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    key = (kind, dev, stream.cuda_stream)
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws.record_stream(stream)  # a smaller one that it replaces may still be in use there
+        _ws_cache[key] = ws
+    return ws
+
+
+def _i32(name, t, shape):
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be contiguous int32 of shape {tuple(shape)}")
+
+
+def _status_arg(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
+
+
+def tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
+                temperature=None, draft_probs=None, draft_mode=DRAFT_BY_DEPTH, status=None,
+                stream=None):
+    """Sampled acceptance: logits [B,Q,V] (float32 or bf16), a draft tree parent and tokens
+    [B,Q] int32, uniforms [B,Q] float32 -> accept_len [B], path and new_tokens [B,Q] int32.
+
+    temperature [B] float32 (0 = greedy).  draft_probs [B,R,V] float32: the distributions
+    the children were drawn from, by depth or by node (draft_mode); None when the candidates
+    were chosen without chance."""
+    dev = _on_device(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
+                     temperature, draft_probs, status)
+    B, Q, V = logits.shape
+    if B and (logits.stride(2) != 1 or (B > 1 and logits.stride(0) != Q * logits.stride(1))):
+        raise ValueError("logits rows must be contiguous and uniformly strided over (B, Q)")
+    for name, t, shape in (("parent", parent, (B, Q)), ("tokens", tokens, (B, Q)),
+                           ("accept_len", accept_len, (B,)), ("path", path, (B, Q)),
+                           ("new_tokens", new_tokens, (B, Q))):
+        _i32(name, t, shape)
+    for name, t, shape in (("uniforms", uniforms, (B, Q)), ("temperature", temperature, (B,))):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
+                              tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be contiguous float32 of shape {shape}")
+    _status_arg(status)
+    a = SampleArgs()
+    a.struct_size = ctypes.sizeof(SampleArgs)
+    a.B, a.Q, a.vocab = B, Q, V
+    a.logits, a.logits_dt = logits.data_ptr(), _dt(logits)
+    a.logits_row_stride = logits.stride(1) if Q > 1 or B > 1 else V
+    a.temperature = None if temperature is None else temperature.data_ptr()
+    a.parent, a.tokens = parent.data_ptr(), tokens.data_ptr()
+    a.uniforms = uniforms.data_ptr()
+    if draft_probs is not None:
+        d = draft_probs
+        if d.dtype != torch.float32 or d.dim() != 3 or d.shape[0] != B or d.shape[2] != V:
+            raise ValueError("draft_probs must be float32 [B, rows, V]")
+        R = d.shape[1]
+        if B and (d.stride(2) != 1 or (B > 1 and d.stride(0) != R * d.stride(1))):
+            raise ValueError("draft_probs rows must be contiguous and uniformly strided")
+        a.draft_probs = d.data_ptr()
+        a.draft_row_stride = d.stride(1) if R > 1 or B > 1 else V
+        a.draft_rows, a.draft_mode = R, int(draft_mode)
+    a.accept_len, a.path = accept_len.data_ptr(), path.data_ptr()
+    a.new_tokens = new_tokens.data_ptr()
+    a.status = None if status is None else status.data_ptr()
+    with _launch(dev, stream) as st:
+        rc = load().tv_tree_sample(ctypes.byref(a), st.handle)
+    _check(rc, "tv_tree_sample")
+
+
+def make_page_pool(refcount, page_table, n_pages, page_size) -> PagePool:
+    """A pool over refcount [pages], page_table [rows, max_pages] and n_pages [rows] int32
+    (empty: 0, -1 and 0); the tensors are kept alive by it and changed in place."""
+    dev = _on_device(refcount, page_table, n_pages)
+    rows, most = page_table.shape
+    _i32("refcount", refcount, (refcount.numel(),))
+    _i32("page_table", page_table, (rows, most))
+    _i32("n_pages", n_pages, (rows,))
+    p = PagePool(page_table.data_ptr(), n_pages.data_ptr(), refcount.data_ptr(), rows, most,
+                 refcount.numel(), int(page_size))
+    p.tensors, p.device = (refcount, page_table, n_pages), dev
+    return p
+
+
+def pages_workspace_size(pool: PagePool) -> int:
+    return int(load().tv_pages_workspace_size(ctypes.byref(pool)))
+
+
+def _pool_call(name, pool, per_row, others, status, stream, workspace=None, scratch=False):
+    """Marshal one pool call: per-row int32 arguments, other device arguments, status."""
+    dev = _on_device(*(t for _, t in per_row), *others, status, workspace)
+    if dev != pool.device:
+        raise ValueError(f"pool on {pool.device}, arguments on {dev}")
+    for what, t in per_row:
+        _i32(what, t, (pool.rows,))
+    _status_arg(status)
+    args = [_ptr(t) for _, t in per_row] + [_ptr(t) for t in others] + [_ptr(status)]
+    with _launch(dev, stream) as st:
+        if scratch:
+            if workspace is None:
+                workspace = _scratch("pages", dev, st.stream, pages_workspace_size(pool))
+            args += [_ptr(workspace), workspace.numel() * workspace.element_size()]
+        rc = getattr(load(), name)(ctypes.byref(pool), *args, st.handle)
+    _check(rc, name)
+
+
+def pages_reserve(pool: PagePool, length, new_length, copies, status=None, workspace=None,
+                  stream=None):
+    """Give every row the pages of keys length .. new_length-1 for itself; copies [rows,3]
+    int32 becomes the list pages_copy takes."""
+    _i32("copies", copies, (pool.rows, 3))
+    _pool_call("tv_pages_reserve", pool, (("length", length), ("new_length", new_length)),
+               (copies,), status, stream, workspace, True)
+
+
+def pages_fork(pool: PagePool, fork_from, length, status=None, stream=None):
+    """Row r shares the pages of the first length[r] keys of row fork_from[r] (-1: none)."""
+    _pool_call("tv_pages_fork", pool, (("fork_from", fork_from), ("length", length)), (),
+               status, stream)
+
+
+def pages_release(pool: PagePool, keep, status=None, stream=None):
+    """Row r keeps the pages of its first keep[r] keys (negative: left alone)."""
+    _pool_call("tv_pages_release", pool, (("keep", keep),), (), status, stream)
+
+
+def pages_compact(pool: PagePool, moves, n_moves, status=None, workspace=None, stream=None):
+    """Move the pages in use to the front of the pool: tables and counts now, the cache's
+    rows by pages_copy with moves [num_pages,3] and count=n_moves [1] (int32)."""
+    _i32("moves", moves, (pool.num_pages, 3))
+    _i32("n_moves", n_moves, (1,))
+    _pool_call("tv_pages_compact", pool, (), (moves, n_moves), status, stream, workspace, True)
+
+
+def pages_copy(c_kv, k_pe, page_size, copies, count=None, status=None, stream=None):
+    """Copy the listed pages' rows in c_kv [rows, DL] and k_pe [rows, DR], or in every layer
+    of [layers, rows, DL] and [layers, rows, DR].  copies [n,3] int32 as pages_reserve or
+    pages_compact wrote it; count [1]: only its first count entries."""
+    dev = _on_device(c_kv, k_pe, copies, count, status)
+    c3 = c_kv if c_kv.dim() == 3 else c_kv.unsqueeze(0)
+    k3 = k_pe if k_pe.dim() == 3 else k_pe.unsqueeze(0)
+    if c3.shape[:2] != k3.shape[:2] or c_kv.dtype != k_pe.dtype:
+        raise ValueError("c_kv and k_pe must have the same layers, rows and dtype")
+    if c3.stride(2) != 1 or k3.stride(2) != 1:
+        raise ValueError("cache rows must be contiguous")
+    n = copies.shape[0]
+    _i32("copies", copies, (n, 3))
+    if count is not None:
+        _i32("count", count, (1,))
+    _status_arg(status)
+    layers, rows, DL = c3.shape
+    with _launch(dev, stream) as st:
+        rc = load().tv_pages_copy(_ptr(c_kv), _ptr(k_pe), _dt(c_kv), c3.stride(1), k3.stride(1),
+                                  DL, k3.shape[2], layers, c3.stride(0), k3.stride(0),
+                                  int(page_size), rows, _ptr(copies), _ptr(count), n,
+                                  _ptr(status), st.handle)
+    _check(rc, "tv_pages_copy")

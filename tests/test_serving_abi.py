@@ -1,0 +1,114 @@
+"""Refusals of the serving calls (CPU only: arguments are checked on the host and the
+placeholder pointers are never followed)."""
+import ctypes
+
+import pytest
+
+from speculative_decoding_tree_04_gb300 import tv
+
+FAKE = 1 << 20
+
+
+def sample_args(**kw):
+    a = tv.SampleArgs()
+    a.struct_size = ctypes.sizeof(tv.SampleArgs)
+    a.B, a.Q, a.vocab = 2, 9, 1000
+    a.logits, a.logits_dt, a.logits_row_stride = FAKE, tv.TV_F32, 1000
+    a.parent = a.tokens = a.uniforms = a.accept_len = a.path = a.new_tokens = FAKE
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(struct_size=8), tv.TV_ERR_INVALID_ARG),
+    (dict(B=-1), tv.TV_ERR_INVALID_ARG),
+    (dict(Q=0), tv.TV_ERR_INVALID_ARG),
+    (dict(Q=65), tv.TV_ERR_UNSUPPORTED),
+    (dict(vocab=0), tv.TV_ERR_INVALID_ARG),
+    (dict(vocab=(1 << 18) + 1, logits_row_stride=1 << 19), tv.TV_ERR_UNSUPPORTED),
+    (dict(logits_dt=2), tv.TV_ERR_INVALID_ARG),
+    (dict(logits_row_stride=999), tv.TV_ERR_INVALID_ARG),
+    (dict(logits=None), tv.TV_ERR_INVALID_ARG),
+    (dict(logits=FAKE + 2), tv.TV_ERR_INVALID_ARG),
+    (dict(uniforms=None), tv.TV_ERR_INVALID_ARG),
+    (dict(path=None), tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE, draft_row_stride=999, draft_rows=9), tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=0), tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=9, draft_mode=2),
+     tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=8, draft_mode=1),
+     tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE + 2, draft_row_stride=1000, draft_rows=9), tv.TV_ERR_INVALID_ARG),
+    (dict(B=0, logits=None), tv.TV_OK),
+])
+def test_tree_sample_arguments(tvlib, kw, code):
+    assert tv.load().tv_tree_sample(ctypes.byref(sample_args(**kw)), None) == code
+    assert (code == tv.TV_OK) == (not tv.load().tv_last_error())
+
+
+def pool(**kw):
+    p = tv.PagePool(FAKE, FAKE, FAKE, 8, 16, 100, 64)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), tv.TV_ERR_INVALID_ARG),
+    (dict(rows=4097), tv.TV_ERR_UNSUPPORTED),
+    (dict(max_pages=0), tv.TV_ERR_INVALID_ARG),
+    (dict(num_pages=0), tv.TV_ERR_INVALID_ARG),
+    (dict(num_pages=1 << 24), tv.TV_ERR_UNSUPPORTED),
+    (dict(page_size=0), tv.TV_ERR_INVALID_ARG),
+    (dict(max_pages=1 << 25), tv.TV_ERR_UNSUPPORTED),
+    (dict(refcount=None), tv.TV_ERR_INVALID_ARG),
+    (dict(page_table=None), tv.TV_ERR_INVALID_ARG),
+])
+def test_pool_arguments(tvlib, kw, code):
+    lib, p = tv.load(), ctypes.byref(pool(**kw))
+    assert lib.tv_pages_workspace_size(p) == 0
+    assert lib.tv_pages_reserve(p, FAKE, FAKE, FAKE, None, FAKE, 1 << 20, None) == code
+    assert lib.tv_pages_fork(p, FAKE, FAKE, None, None) == code
+    assert lib.tv_pages_release(p, FAKE, None, None) == code
+    assert lib.tv_pages_compact(p, FAKE, FAKE, None, FAKE, 1 << 20, None) == code
+    assert lib.tv_last_error()
+
+
+def test_pool_pointers_and_workspace(tvlib):
+    lib, p = tv.load(), ctypes.byref(pool())
+    need = lib.tv_pages_workspace_size(p)
+    assert need > 0 and need % 256 == 0
+    bad, short = tv.TV_ERR_INVALID_ARG, tv.TV_ERR_WORKSPACE
+    assert lib.tv_pages_reserve(None, FAKE, FAKE, FAKE, None, FAKE, need, None) == bad
+    assert lib.tv_pages_reserve(p, None, FAKE, FAKE, None, FAKE, need, None) == bad
+    assert lib.tv_pages_reserve(p, FAKE, FAKE, FAKE, None, None, need, None) == short
+    assert lib.tv_pages_reserve(p, FAKE, FAKE, FAKE, None, FAKE + 16, need, None) == short
+    assert lib.tv_pages_reserve(p, FAKE, FAKE, FAKE, None, FAKE, need - 1, None) == short
+    assert lib.tv_pages_fork(p, None, FAKE, None, None) == bad
+    assert lib.tv_pages_release(p, None, None, None) == bad
+    assert lib.tv_pages_compact(p, None, FAKE, None, FAKE, need, None) == bad
+    assert lib.tv_pages_compact(p, FAKE, FAKE, None, FAKE, need - 1, None) == short
+
+
+def test_pages_copy_arguments(tvlib):
+    ok = dict(c=FAKE, k=FAKE, dt=1, cs=512, ks=64, dl=512, dr=64, layers=2, cl=1 << 20,
+              kl=1 << 18, ps=64, rows=6400, lst=FAKE, n=4)
+
+    def call(**kw):
+        p = dict(ok, **kw)
+        return tv.load().tv_pages_copy(p["c"], p["k"], p["dt"], p["cs"], p["ks"], p["dl"],
+                                       p["dr"], p["layers"], p["cl"], p["kl"], p["ps"],
+                                       p["rows"], p["lst"], None, p["n"], None, None)
+
+    assert call(n=0) == tv.TV_OK
+    for kw in (dict(c=None), dict(k=None), dict(lst=None), dict(dt=3), dict(dl=0), dict(dr=-1),
+               dict(cs=511), dict(ks=56), dict(dl=508), dict(dr=4), dict(cs=516), dict(ks=68),
+               dict(c=FAKE + 8), dict(k=FAKE + 8), dict(layers=0), dict(cl=-8), dict(cl=1004),
+               dict(ps=0), dict(rows=-1), dict(n=-1)):
+        assert call(**kw) == tv.TV_ERR_INVALID_ARG, kw
+    assert call(ps=65537) == tv.TV_ERR_UNSUPPORTED
+
+
+def test_new_status_has_a_text(tvlib):
+    assert tv.load().tv_status_string(tv.TV_ERR_NO_PAGES) == b"too few free pages"
