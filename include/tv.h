@@ -567,6 +567,62 @@ int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
                   int64_t num_rows, const int32_t* list, const int32_t* count, int n_list,
                   int32_t* status, void* stream);
 
+/*
+ * tv_prefill_attn -- causal latent attention of prompts in its expanded form.
+ *
+ * With W_uk[h], W_uv[h] the rows 0 .. d_nope-1 and d_nope .. of w_kv[h], key j of a
+ * sequence is k_j = W_uk[h] c_kv_j for head h, with the rope part k_pe_j that all heads
+ * share, and its value v_j = W_uv[h] c_kv_j.  Query i of sequence b, at logical key
+ * prefix_len[b] + i, takes
+ *     s_j = scale * ( q_nope[i,h] . k_j + q_pe[i,h] . k_pe_j ),   0 <= j <= prefix_len[b] + i
+ *     out[i,h] = sum_j softmax(s)_j v_j.
+ * This is the attention that tv_verify_attn with TV_MASK_CAUSAL computes in the latent
+ * space (q_latent = q_nope W_uk, and W_uv applied to its output) at 640 instead of 2176
+ * flop per (query, key, head), plus 2 * d_latent * (d_nope + d_v) flop per key and head for
+ * the expansion; it is the cheaper form from about 170 queries on, tv_verify_attn for
+ * fewer (a draft tree, single tokens).
+ *
+ * The sequences' queries are packed: sequence b has rows q_start[b] .. q_start[b+1]-1 of
+ * q_nope, q_pe and out.  Its keys 0 .. prefix_len[b] + q_len - 1 are all in the cache (the
+ * prompt's own rows included).  Expanded keys and values, and the softmax weights, are
+ * rounded to bf16 for the tensor cores; sums and statistics are 32-bit.  Values in the
+ * inputs must be finite.
+ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_prefill_args): ABI check */
+  int32_t B, H, T;           /* sequences, heads, rows of q_nope, q_pe and out */
+  int32_t d_latent;          /* a multiple of 64 */
+  int32_t d_nope, d_rope, d_v; /* 128, 64, 128 */
+  float scale;               /* > 0 */
+  tv_dtype dt;               /* TV_BF16 */
+  const void* q_nope;        /* device [T, H, d_nope] contiguous */
+  const void* q_pe;          /* device [T, H, d_rope] contiguous, RoPE applied */
+  const void* w_kv;          /* device [H, d_nope + d_v, d_latent] contiguous */
+  const void* c_kv;          /* cache rows, as tv_attn_args */
+  const void* k_pe;          /* cache rows, RoPE applied */
+  int64_t ckv_row_stride, kpe_row_stride;
+  tv_cache_layout cache;     /* 64-token pages, or contiguous; num_rows > 0, < 2^31 */
+  const int32_t* q_start;    /* device [B + 1], ascending, 0 .. T */
+  const int32_t* prefix_len; /* device [B] */
+  int32_t max_q_len;         /* host bounds: queries of one sequence, */
+  int32_t max_kv_len;        /* prefix_len + queries of one sequence, */
+  int64_t total_kv;          /* and that summed over the sequences with queries */
+  void* out;                 /* device [T, H, d_v] bf16 out, 32-byte aligned.  Rows of no
+                                sequence are left as they were. */
+  int32_t* status;           /* device int32, nullable.  TV_ERR_BOUNDS: a sequence outside
+                                the bounds above, with a negative prefix_len, or whose
+                                q_start is negative, above its end or below an earlier one
+                                (its rows are left as they were), or a page of
+                                it outside the cache (that page reads as zeros). */
+} tv_prefill_args;
+
+/* Bytes of workspace (the expanded keys and values: about 512 * H + 128 bytes per key);
+ * depends on B, H, T and total_kv.  0 for invalid arguments. */
+size_t tv_prefill_attn_workspace_size(const tv_prefill_args* a);
+
+/* workspace: device memory of at least that size, 256-byte aligned; scratch. */
+int tv_prefill_attn(const tv_prefill_args* a, void* workspace, size_t ws_bytes, void* stream);
+
 /* Text for a tv_status code (static storage). */
 const char* tv_status_string(int code);
 

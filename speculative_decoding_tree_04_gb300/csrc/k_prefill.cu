@@ -1,0 +1,806 @@
+// k_prefill.cu -- causal latent attention of prompts in its expanded form (tv_prefill_attn).
+//
+// For head h, key j of a sequence is k_j = W_uk[h] c_j (d_nope) with the rope part k_pe_j
+// that all heads share, and value j is v_j = W_uv[h] c_j.  Query i (at key P + i) takes
+//   out_i = sum_{j <= P+i} softmax_j( scale (q_nope.k_j + q_pe.k_pe_j) ) v_j.
+// Per (query, key) pair and head that is 2 (128 + 64 + 128) = 640 flop, against
+// 2 (2*512 + 64) = 2176 with the query absorbed into the latent space (tv_verify_attn);
+// the expansion costs 2*512*256 flop per key and head once, whatever the number of queries.
+// So it pays from about 170 queries per key sweep on; below that the absorbed form is
+// cheaper.
+//
+// Three kernels:
+//   plan     one block: where each sequence's expanded keys go, the tiles of the other two;
+//   expand   [K | V] = C W^T for every sequence and head, a GEMM of 128 keys x 256 outputs
+//            x d_latent, rounded to bf16 into the workspace (the precision the tensor cores
+//            read); rows behind a sequence's last key are zero, so that masked weights
+//            (zero) times them is zero;
+//   attend   per head and 256 queries, an online softmax over 128 keys at a time.
+//
+// Both tensor-core kernels are warp-specialised: one thread issues TMA loads into a ring of
+// 128-byte-swizzled tiles, one issues tcgen05.mma with accumulators in TMEM, whole warps
+// read TMEM (thread = row).  Every wait is bounded by a wall-clock deadline, after which the
+// kernel records TV_ERR_TIMEOUT, waits for its own copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include "sm100_ptx.h"
+#include "tv_internal.h"
+
+namespace tv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kDN = 128, kDR = 64, kDV = 128;   // per-head widths
+constexpr int kKV = kDN + kDV;                  // outputs of the expansion per head
+constexpr int kBlock = 128;                     // keys per block, queries per tile
+constexpr int kPair = 2 * kBlock;               // queries per CTA
+constexpr int kChunk = kBlock * 128;            // 128 rows of 64 bf16: 16 KB
+constexpr uint64_t kDeadlineNs = 2000000000ull;
+constexpr float kRescale = 8.0f;                // log2: see attend_kernel
+
+// ---- workspace --------------------------------------------------------------------------
+// counts {query tiles, key tiles}; query tiles {first row of q, rows left, position of the
+// first row, first expanded key}; key tiles {sequence, first key, expanded row, rows left};
+// then K [H][cap][128], V [H][cap][128] and the rope keys [cap][64], bf16.
+struct Layout {
+  int64_t cap;               // expanded key rows
+  int64_t max_q, max_k;      // tiles at most
+  size_t q_tiles, k_tiles, k, v, kr, total;
+};
+size_t align1k(size_t n) { return (n + 1023) / 1024 * 1024; }
+Layout layout(const tv_prefill_args* a) {
+  Layout l{};
+  l.cap = (a->total_kv + (int64_t)(kBlock - 1) * a->B + kBlock - 1) / kBlock * kBlock;
+  l.max_k = l.cap / kBlock;
+  l.max_q = a->T / kPair + a->B;
+  size_t n = 1024;
+  l.q_tiles = n;
+  n += align1k((size_t)l.max_q * sizeof(int4));
+  l.k_tiles = n;
+  n += align1k((size_t)l.max_k * sizeof(int4));
+  l.k = n;
+  n += (size_t)l.cap * a->H * kDN * 2;
+  l.v = n;
+  n += (size_t)l.cap * a->H * kDV * 2;
+  l.kr = n;
+  n += (size_t)l.cap * kDR * 2;
+  l.total = n;
+  return l;
+}
+
+// ---- plan -------------------------------------------------------------------------------
+struct PlanArgs {
+  const int32_t* q_start;
+  const int32_t* prefix_len;
+  int32_t B, T, max_q_len, max_kv_len;
+  int32_t max_q, max_k;
+  int32_t* counts;
+  int4* q_tiles;
+  int4* k_tiles;
+  int32_t* status;
+};
+
+__global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
+  __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost;
+  __shared__ int s_weight[1024];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    s_base_q = s_base_k = 0;
+    s_base_max = INT_MIN;
+  }
+  for (int b0 = 0; b0 < p.B; b0 += 1024) {
+    const int b = b0 + tid;
+    int nq = 0, nk = 0, q0 = 0, n = 0, P = 0;
+    // a sequence that starts below an earlier start would share rows with another one
+    int top = b < p.B ? p.q_start[b] : INT_MIN;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_up_sync(0xffffffffu, top, o));
+    if (lane == 31) s_max[warp] = top;
+    __syncthreads();
+    top = max(top, s_base_max);
+    for (int w = 0; w < warp; ++w) top = max(top, s_max[w]);
+    __syncthreads();
+    if (tid == 1023) s_base_max = top;
+    if (b < p.B) {
+      const int64_t s = p.q_start[b], e = p.q_start[b + 1], pre = p.prefix_len[b];
+      // a bad sequence is left out: its rows stay as they were
+      if (s < 0 || s < top || e < s || e > p.T || pre < 0 || e - s > p.max_q_len ||
+          (e > s && pre + e - s > p.max_kv_len)) {
+        report(p.status, TV_ERR_BOUNDS);
+      } else if (e > s) {
+        q0 = (int)s;
+        n = (int)(e - s);
+        P = (int)pre;
+        nq = (n + kPair - 1) / kPair;
+        nk = (P + n + kBlock - 1) / kBlock;
+      }
+    }
+    int cq = nq, ck = nk;  // inclusive sums within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int uq = __shfl_up_sync(0xffffffffu, cq, o), uk = __shfl_up_sync(0xffffffffu, ck, o);
+      if (lane >= o) {
+        cq += uq;
+        ck += uk;
+      }
+    }
+    if (lane == 31) {
+      s_q[warp] = cq;
+      s_k[warp] = ck;
+    }
+    __syncthreads();
+    int bq = s_base_q + cq - nq, bk = s_base_k + ck - nk;
+    for (int w = 0; w < warp; ++w) {
+      bq += s_q[w];
+      bk += s_k[w];
+    }
+    __syncthreads();
+    if (tid == 1023) {
+      s_base_q = bq + nq;
+      s_base_k = bk + nk;
+    }
+    // past the caller's bounds: left out (and, counts being cumulative, all after it too)
+    const bool fits = bq + nq <= p.max_q && bk + nk <= p.max_k;
+    if (nq > 0 && !fits) report(p.status, TV_ERR_BOUNDS);
+    if (nq > 0 && fits) {
+      for (int i = 0; i < nq; ++i)
+        p.q_tiles[bq + i] = make_int4(q0 + i * kPair, n - i * kPair, P + i * kPair, bk * kBlock);
+      for (int i = 0; i < nk; ++i)
+        p.k_tiles[bk + i] =
+            make_int4(b, i * kBlock, (bk + i) * kBlock, P + n - i * kBlock);
+    }
+    const uint32_t lost = __ballot_sync(0xffffffffu, nq > 0 && !fits);
+    // the counts end at the first sequence that does not fit
+    if (tid == 0) s_lost = INT_MAX;
+    __syncthreads();
+    if (lost && lane == __ffs(lost) - 1) atomicMin(&s_lost, b);
+    __syncthreads();
+    if (s_lost != INT_MAX) {
+      if (b == s_lost) {
+        s_base_q = bq;
+        s_base_k = bk;
+      }
+      __syncthreads();
+      break;
+    }
+  }
+  __syncthreads();
+  const int total_q = s_base_q, total_k = s_base_k;
+  if (tid == 0) {
+    p.counts[0] = total_q;
+    p.counts[1] = total_k;
+  }
+  // longest sweeps first, so that the short ones fill the end (up to 1024 tiles)
+  if (total_q > 1024) return;
+  int4 mine = make_int4(0, 0, 0, 0);
+  if (tid < total_q) {
+    mine = p.q_tiles[tid];
+    s_weight[tid] = mine.z + min(mine.y, kPair);
+  }
+  __syncthreads();
+  if (tid < total_q) {
+    int rank = 0;
+    const int w = s_weight[tid];
+    for (int i = 0; i < total_q; ++i)
+      rank += s_weight[i] > w || (s_weight[i] == w && i < tid);
+    p.q_tiles[rank] = mine;
+  }
+}
+
+// ---- bounded waits ------------------------------------------------------------------------
+struct Abort {
+  volatile int flag;
+  int32_t* status;
+};
+
+__device__ __noinline__ bool wait_slow(Abort& ab, uint32_t a, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait_cta(a, parity)) return true;
+    if (ab.flag) return false;
+    if (globaltimer() - t0 > kDeadlineNs) {
+      ab.flag = 1;
+      report(ab.status, TV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_for(Abort& ab, uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_cta(a, parity)) return true;
+  return wait_slow(ab, a, parity);
+}
+// Whether or not the kernel is giving up: a copy or MMA in flight has to land first.
+__device__ __noinline__ void drain(Abort& ab, uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait_cta(a, parity))
+    if (globaltimer() - t0 > kDeadlineNs) {
+      report(ab.status, TV_ERR_TIMEOUT);
+      return;
+    }
+}
+__device__ __forceinline__ void drain_ring(Abort& ab, uint64_t* full, uint32_t stages,
+                                           uint32_t count) {
+  for (uint32_t k = 0; k < stages && k < count; ++k) {
+    const uint32_t u = count - 1 - k;
+    drain(ab, &full[u % stages], (u / stages) & 1);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// 32 bytes in one store (sm_100)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// ---- expand -------------------------------------------------------------------------------
+constexpr int kExpThreads = 256;
+constexpr int kExpStages = 4;
+constexpr int kExpA = kChunk, kExpB = kKV * 128;  // 16 KB of keys, 32 KB of weights
+constexpr int kExpStage = kExpA + kExpB;
+constexpr uint32_t kIdescExp = idesc_bf16_f32(kBlock, kKV, 0, 0);
+
+struct ExpandShared {
+  uint64_t full[kExpStages], empty[kExpStages], acc_full[2], acc_empty[2], last;
+  uint32_t tmem;
+  Abort abort;
+};
+constexpr int kExpSmem = kExpStages * kExpStage + (int)sizeof(ExpandShared) + 1024;
+
+struct ExpandArgs {
+  const int32_t* counts;
+  const int4* k_tiles;
+  const int32_t* page_table;  // null: contiguous
+  int32_t max_pages, H, k_chunks;
+  int64_t kv_stride_b, num_rows, cap;
+  const __nv_bfloat16* k_pe;
+  int64_t kpe_stride;
+  __nv_bfloat16 *K, *V, *KR;
+  int32_t* status;
+};
+
+// First cache row of 64 keys, or a row past the end (TMA then reads zeros) for a page that
+// is not in the cache.
+__device__ __forceinline__ int64_t cache_row64(const ExpandArgs& p, int b, int64_t key) {
+  if (!p.page_table) return (int64_t)b * p.kv_stride_b + key;
+  const int64_t row = (int64_t)__ldg(p.page_table + (int64_t)b * p.max_pages + key / 64) * 64;
+  return row >= 0 && row + 64 <= p.num_rows ? row : p.num_rows;
+}
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+    expand_kernel(ExpandArgs p, const __grid_constant__ CUtensorMap map_c,
+                  const __grid_constant__ CUtensorMap map_w) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  ExpandShared& sh = *(ExpandShared*)(smem + kExpStages * kExpStage);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_k = p.counts[1];
+  const int64_t n_tiles = (int64_t)n_k * p.H;
+  if (blockIdx.x >= n_tiles) return;
+  if (tid == 0) {
+    for (int i = 0; i < kExpStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], 4);
+    }
+    mbar_init(&sh.last, 1);
+    sh.abort.flag = 0;
+    sh.abort.status = p.status;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t u = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+      const int h = (int)(t / n_k);
+      const int4 kt = __ldg(p.k_tiles + (t - (int64_t)h * n_k));
+      // the second half may hold no key: read past the end then (its page may not exist)
+      const int row0 = (int)min(cache_row64(p, kt.x, kt.y), p.num_rows);
+      const int row1 = kt.w > 64 ? (int)min(cache_row64(p, kt.x, kt.y + 64), p.num_rows)
+                                 : (int)p.num_rows;
+      for (int c = 0; c < p.k_chunks; ++c, ++u) {
+        const uint32_t s = u % kExpStages;
+        if (!wait_for(sh.abort, &sh.empty[s], ((u / kExpStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&sh.full[s], kExpStage);
+        unsigned char* a = smem + s * kExpStage;
+        tma_load_2d(a, &map_c, 64 * c, row0, &sh.full[s]);
+        tma_load_2d(a + kExpA / 2, &map_c, 64 * c, row1, &sh.full[s]);
+        tma_load_2d(a + kExpA, &map_w, 64 * c, h * kKV, &sh.full[s]);
+      }
+    }
+    drain_ring(sh.abort, sh.full, kExpStages, u);
+  } else if (warp == 1 && lane == 0) {
+    uint32_t u = 0, i = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < n_tiles; t += gridDim.x, ++i) {
+      const uint32_t buf = i & 1;
+      ok = wait_for(sh.abort, &sh.acc_empty[buf], ((i >> 1) & 1) ^ 1);
+      tc_fence_after();
+      for (int c = 0; ok && c < p.k_chunks; ++c, ++u) {
+        const uint32_t s = u % kExpStages;
+        if (!wait_for(sh.abort, &sh.full[s], (u / kExpStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * kExpStage);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + buf * kKV, smem_desc(a + 32 * k, 16, 1024, 2),
+                 smem_desc(a + kExpA + 32 * k, 16, 1024, 2), kIdescExp, (c | k) != 0);
+        mma_commit(&sh.empty[s]);
+      }
+      if (ok) mma_commit(&sh.acc_full[buf]);
+    }
+    mma_commit(&sh.last);
+    drain(sh.abort, &sh.last, 0);
+  } else if (warp >= 4) {
+    const int r = tid - 128;  // row of the tile = TMEM lane
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane field << 16
+    uint32_t i = 0;
+    for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++i) {
+      const int h = (int)(t / n_k);
+      const int4 kt = __ldg(p.k_tiles + (t - (int64_t)h * n_k));
+      const bool live = r < kt.w;
+      if (h == 0) {  // the rope keys, once per key tile
+        uint4 v[8] = {};
+        if (live) {
+          const int64_t row = cache_row64(p, kt.x, kt.y + (r & 64)) + (r & 63);
+          if (row < p.num_rows) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.k_pe + row * p.kpe_stride);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __ldg(src + k);
+          } else {
+            report(p.status, TV_ERR_BOUNDS);
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(p.KR + ((int64_t)kt.z + r) * kDR);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = v[k];
+      }
+      const uint32_t buf = i & 1;
+      if (!__all_sync(0xffffffffu, wait_for(sh.abort, &sh.acc_full[buf], (i >> 1) & 1))) break;
+      tc_fence_after();
+      const int64_t at = (int64_t)h * p.cap + kt.z + r;
+#pragma unroll
+      for (int c = 0; c < kKV; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(tmem + lanes + buf * kKV + c, x);
+        tmem_wait_ld_regs(x);
+        uint32_t y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          y[k] = live ? pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])) : 0u;
+        __nv_bfloat16* dst = c < kDN ? p.K + at * kDN + c : p.V + at * kDV + (c - kDN);
+        st_global_32(dst, y);
+        st_global_32(dst + 16, y + 8);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---- attend -------------------------------------------------------------------------------
+// A CTA takes one head and up to 256 queries as two 128-row tiles that share every key
+// block.  TMEM (512 columns): S0, S1 (128 each; P, in bf16, overwrites the first half of
+// its S) and O0, O1.  While one tile's softmax runs, the tensor cores work for the other:
+// per tile and block 12 MMAs of 128x128x16 for S and 8 for O, 1280 clocks at the full rate,
+// against 16384 exponentials.
+constexpr int kAttThreads = 384;
+constexpr int kRing = 8;  // 16 KB chunks, 5 per key block
+constexpr int kQBytes = 3 * kChunk;
+constexpr uint32_t kTmS = 0, kTmO = 256;
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
+constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1);
+
+struct AttendShared {
+  uint64_t full[kRing], empty[kRing], q_full, s_full[2], p_full[2], o_full[2], last;
+  uint32_t tmem;
+  Abort abort;
+};
+constexpr int kAttSmem = 2 * kQBytes + kRing * kChunk + (int)sizeof(AttendShared) + 1024;
+static_assert(kAttSmem <= 232448, "shared memory of an SM");
+
+struct AttendArgs {
+  const int32_t* counts;
+  const int4* q_tiles;
+  int32_t H;
+  float scale_log2;
+  __nv_bfloat16* out;
+  int32_t* status;
+};
+
+__global__ void __launch_bounds__(kAttThreads, 1)
+    attend_kernel(AttendArgs p, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_qr,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v,
+                  const __grid_constant__ CUtensorMap map_kr) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = smem + 2 * kQBytes;
+  AttendShared& sh = *(AttendShared*)(ring + kRing * kChunk);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = blockIdx.x / p.H, h = blockIdx.x - tile * p.H;
+  if (tile >= p.counts[0]) return;
+  const int4 qt = __ldg(p.q_tiles + tile);
+  const int rows = min(qt.y, kPair), pos0 = qt.z, key0 = qt.w;
+  const int tiles = rows > kBlock ? 2 : 1;
+  // key blocks that the tiles' last rows see
+  const int n0 = (pos0 + min(rows, kBlock) + kBlock - 1) / kBlock;
+  const int n1 = tiles > 1 ? (pos0 + rows + kBlock - 1) / kBlock : 0;
+  const int n = max(n0, n1);
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    mbar_init(&sh.last, 1);
+    sh.abort.flag = 0;
+    sh.abort.status = p.status;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0 && lane == 0) {
+    mbar_arrive_expect_tx(&sh.q_full, tiles * kQBytes);
+    for (int t = 0; t < tiles; ++t) {
+      unsigned char* q = smem + t * kQBytes;
+      const int row = qt.x + t * kBlock;
+      tma_load_3d(q, &map_q, 0, h, row, &sh.q_full);
+      tma_load_3d(q + kChunk, &map_q, 64, h, row, &sh.q_full);
+      tma_load_3d(q + 2 * kChunk, &map_qr, 0, h, row, &sh.q_full);
+    }
+    uint32_t u = 0;
+    bool ok = true;
+    for (int j = 0; ok && j < n; ++j) {
+      const int key = key0 + j * kBlock;
+      for (int c = 0; c < 5; ++c, ++u) {
+        const uint32_t s = u % kRing;
+        if (!wait_for(sh.abort, &sh.empty[s], ((u / kRing) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&sh.full[s], kChunk);
+        unsigned char* dst = ring + s * kChunk;
+        if (c < 2) tma_load_3d(dst, &map_k, 64 * c, key, h, &sh.full[s]);
+        else if (c == 2) tma_load_2d(dst, &map_kr, 0, key, &sh.full[s]);
+        else tma_load_4d(dst, &map_v, 0, key + 64 * (c - 3), 0, h, &sh.full[s]);
+      }
+    }
+    drain_ring(sh.abort, sh.full, kRing, u);
+    drain(sh.abort, &sh.q_full, 0);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t q = smem_u32(smem), r = smem_u32(ring);
+    // block j's chunks are ring entries 5j .. 5j+4: K nope, K nope, K rope (128 keys of 64
+    // elements each), V, V (64 keys of 128 elements each, as two 64-wide column pieces)
+    auto chunk = [&](uint32_t u) { return r + (u % kRing) * kChunk; };
+    auto arrived = [&](uint32_t u) {
+      return wait_for(sh.abort, &sh.full[u % kRing], (u / kRing) & 1);
+    };
+    auto scores = [&](int t, int j) {
+#pragma unroll 1
+      for (int c = 0; c < 3; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + kTmS + 128 * t, smem_desc(q + t * kQBytes + c * kChunk + 32 * k, 16, 1024, 2),
+                 smem_desc(chunk(5 * j + c) + 32 * k, 16, 1024, 2), kIdescS, (c | k) != 0);
+      mma_commit(&sh.s_full[t]);
+    };
+    auto keys_here = [&](int j) {
+      const bool ok = arrived(5 * j) && arrived(5 * j + 1) && arrived(5 * j + 2);
+      tc_fence_after();
+      return ok;
+    };
+    auto release = [&](uint32_t u, int k) {
+      for (int i = 0; i < k; ++i) mma_commit(&sh.empty[(u + i) % kRing]);
+    };
+    bool ok = wait_for(sh.abort, &sh.q_full, 0) && keys_here(0);
+    if (ok) {
+      scores(0, 0);
+      if (tiles > 1) scores(1, 0);
+      release(0, 3);
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      bool have_v = false, have_k = false;
+      for (int t = 0; ok && t < tiles; ++t) {
+        const int nt = t ? n1 : n0;
+        if (j >= nt) continue;
+        ok = wait_for(sh.abort, &sh.p_full[t], j & 1);
+        if (ok && !have_v) ok = have_v = arrived(5 * j + 3) && arrived(5 * j + 4);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)  // the keys are the contraction: V is an MN-major B
+          mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + 8 * k,
+                 smem_desc(chunk(5 * j + 3 + (k >> 2)) + 2048 * (k & 3), kChunk / 2, 1024, 2),
+                 kIdescO, (j | k) != 0);
+        if (j + 1 < nt) {
+          if (!have_k) ok = have_k = keys_here(j + 1);
+          if (!ok) break;
+          scores(t, j + 1);
+        } else {
+          mma_commit(&sh.o_full[t]);
+        }
+      }
+      if (!ok) break;
+      release(5 * j + 3, 2);
+      if (have_k) release(5 * (j + 1), 3);
+    }
+    mma_commit(&sh.last);
+    drain(sh.abort, &sh.last, 0);
+  } else if (warp >= 4) {
+    const int t = warp >= 8 ? 1 : 0;
+    const int row = tid - 128 - 128 * t;  // of the tile
+    const int nt = t ? n1 : n0;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tmem + lanes + kTmS + 128 * t, to = tmem + lanes + kTmO + 128 * t;
+    const int last_key = pos0 + t * kBlock + row;      // the row sees keys 0 .. last_key
+    const int tile_first = pos0 + t * kBlock;          // ... and every row these
+    const float c = p.scale_log2;
+    float m = 0.f, l = 0.f;  // running maximum (of scores times c) and sum
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.s_full[t], j & 1));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_wait_ld_regs(s + 32 * k);
+      const int k0 = j * kBlock;
+      if (k0 + kBlock - 1 > tile_first) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k0 + k > last_key) s[k] = 0xFF800000u;
+      }
+      float bm = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+#pragma unroll
+      for (int k = 2; k < 128; k += 2)
+        bm = fmax3(bm, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+      bm *= c;
+      // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
+      // the accumulator is rescaled rarely.  Key 0 is visible to every row, so the first
+      // block always has a maximum.
+      if (j == 0) {
+        m = bm;
+      } else if (__any_sync(0xffffffffu, bm > m + kRescale)) {
+        const float mn = bm > m + kRescale ? bm : m;
+        const float f = ex2(m - mn);
+        m = mn;
+        l *= f;
+        // S of block j was issued after the O of block j - 1: O is complete
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * k, o);
+          tmem_wait_ld_regs(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st32(to + 32 * k, o);
+        }
+        tmem_wait_st();
+      }
+      const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float x, y;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[64 * half + 2 * k]),
+                                   __uint_as_float(s[64 * half + 2 * k + 1])),
+                           c2, m2),
+                    x, y);
+          x = ex2(x);
+          y = ex2(y);
+          l0 += x;
+          l1 += y;
+          pk[k] = pack_bf16(x, y);  // the tensor cores take bf16: 2^-9 of a weight at most
+        }
+        tmem_st32(ts + 32 * half, pk);
+      }
+      l += l0 + l1;  // the sum is that of the unrounded weights
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[t]);
+    }
+    if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.o_full[t], 0));
+    if (ok && nt > 0) {
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const int q = t * kBlock + row;
+      __nv_bfloat16* dst = p.out + ((int64_t)(qt.x + q) * p.H + h) * kDV;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * k, o);
+        tmem_wait_ld_regs(o);
+        uint32_t y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          y[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+        if (q < rows) {
+          st_global_32(dst + 32 * k, y);
+          st_global_32(dst + 32 * k + 16, y + 8);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---- host ---------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+std::mutex g_mu;
+bool g_ready[64] = {};
+
+cudaError_t setup() {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return cudaErrorNotSupported;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_ready[dev]) {
+    e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttSmem);
+    if (e != cudaSuccess) return e;
+    g_ready[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+// A 2-D to 4-D view of bf16 data, inner extent 64 per box, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* stride_bytes, const uint32_t* box) {
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], e[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = stride_bytes[i];
+  }
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, e,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
+          uint32_t box_rows) {
+  const uint64_t d[2] = {inner, rows}, s[1] = {stride};
+  const uint32_t b[2] = {64, box_rows};
+  return make_map(m, base, 2, d, s, b);
+}
+
+}  // namespace
+
+size_t prefill_workspace(const tv_prefill_args* a) { return layout(a).total; }
+
+cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cudaStream_t st) {
+  cudaError_t e = setup();
+  if (e != cudaSuccess) return e;
+  const Layout l = layout(a);
+  char* base = (char*)ws;
+  int32_t* counts = (int32_t*)base;
+  int4* q_tiles = (int4*)(base + l.q_tiles);
+  int4* k_tiles = (int4*)(base + l.k_tiles);
+  const uint64_t H = a->H, T = a->T, cap = (uint64_t)l.cap;
+
+  PlanArgs pa{a->q_start, a->prefix_len, a->B,    a->T,    a->max_q_len, a->max_kv_len,
+              (int)l.max_q, (int)l.max_k, counts, q_tiles, k_tiles,      a->status};
+  plan_kernel<<<1, 1024, 0, st>>>(pa);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  CUtensorMap m_c, m_w, m_q, m_qr, m_k, m_v, m_kr;
+  const uint64_t dq[3] = {kDN, H, T}, sq[2] = {kDN * 2, H * kDN * 2};
+  const uint64_t dqr[3] = {kDR, H, T}, sqr[2] = {kDR * 2, H * kDR * 2};
+  const uint32_t bq[3] = {64, 1, kBlock};
+  const uint64_t dk[3] = {kDN, cap, H}, sk[2] = {kDN * 2, cap * kDN * 2};
+  const uint32_t bk[3] = {64, kBlock, 1};
+  const uint64_t dv[4] = {64, cap, kDV / 64, H}, sv[3] = {kDV * 2, 128, cap * kDV * 2};
+  const uint32_t bv[4] = {64, 64, kDV / 64, 1};
+  if (!map2(&m_c, a->c_kv, a->d_latent, (uint64_t)a->cache.num_rows,
+            (uint64_t)a->ckv_row_stride * 2, 64) ||
+      !map2(&m_w, a->w_kv, a->d_latent, H * kKV, (uint64_t)a->d_latent * 2, kKV) ||
+      !make_map(&m_q, a->q_nope, 3, dq, sq, bq) || !make_map(&m_qr, a->q_pe, 3, dqr, sqr, bq) ||
+      !make_map(&m_k, base + l.k, 3, dk, sk, bk) || !make_map(&m_v, base + l.v, 4, dv, sv, bv) ||
+      !map2(&m_kr, base + l.kr, kDR, cap, kDR * 2, kBlock))
+    return cudaErrorInvalidValue;
+
+  ExpandArgs xa{};
+  xa.counts = counts;
+  xa.k_tiles = k_tiles;
+  xa.page_table = a->cache.page_table;
+  xa.max_pages = a->cache.max_pages;
+  xa.H = a->H;
+  xa.k_chunks = a->d_latent / 64;
+  xa.kv_stride_b = a->cache.kv_stride_b;
+  xa.num_rows = a->cache.num_rows;
+  xa.cap = l.cap;
+  xa.k_pe = (const __nv_bfloat16*)a->k_pe;
+  xa.kpe_stride = a->kpe_row_stride;
+  xa.K = (__nv_bfloat16*)(base + l.k);
+  xa.V = (__nv_bfloat16*)(base + l.v);
+  xa.KR = (__nv_bfloat16*)(base + l.kr);
+  xa.status = a->status;
+  const int64_t exp_tiles = l.max_k * a->H;
+  expand_kernel<<<(unsigned)std::min<int64_t>(exp_tiles, sm_count), kExpThreads, kExpSmem, st>>>(
+      xa, m_c, m_w);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  AttendArgs aa{counts, q_tiles, a->H, (float)((double)a->scale * 1.4426950408889634),
+                (__nv_bfloat16*)a->out, a->status};
+  attend_kernel<<<(unsigned)(l.max_q * a->H), kAttThreads, kAttSmem, st>>>(aa, m_q, m_qr, m_k, m_v,
+                                                                          m_kr);
+  return cudaGetLastError();
+}
+
+}  // namespace tv

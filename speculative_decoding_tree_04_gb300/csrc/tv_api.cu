@@ -489,4 +489,63 @@ int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
   return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_pages_copy");
 }
 
+static int check_prefill(const tv_prefill_args* a) {
+  if (!a) return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: args is NULL%s");
+  if (a->struct_size != sizeof(tv_prefill_args))
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: struct_size mismatch (ABI)%s");
+  if (a->B < 0 || a->H < 1 || a->T < 0 || a->max_q_len < 0 || a->max_kv_len < 0 ||
+      a->total_kv < 0 || a->d_latent < 1)
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: bad B, H, T, d_latent or bounds%s");
+  if (!(a->scale > 0.f) || a->scale > 1e30f)
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: scale must be positive%s");
+  if (a->dt != TV_BF16) return fail(TV_ERR_UNSUPPORTED, "tv_prefill_attn: bf16 only%s");
+  if (a->d_nope != 128 || a->d_rope != 64 || a->d_v != 128 || a->d_latent % 64)
+    return fail(TV_ERR_UNSUPPORTED,
+                "tv_prefill_attn: needs d_nope 128, d_rope 64, d_v 128, d_latent a multiple of 64%s");
+  if (a->B == 0 || a->T == 0) return TV_OK;
+  if (a->H > 65535 || a->B >= (1 << 20) ||
+      ((int64_t)a->T / 256 + a->B) * a->H >= (1ll << 31) ||
+      (int64_t)a->B * (a->max_kv_len / 128 + 1) >= (1ll << 31) ||
+      a->total_kv + 128ll * a->B >= (1ll << 31) || a->d_latent > 65536)
+    return fail(TV_ERR_UNSUPPORTED, "tv_prefill_attn: sizes past 32-bit tile counts%s");
+  if (!a->q_nope || !a->q_pe || !a->w_kv || !a->c_kv || !a->k_pe || !a->q_start ||
+      !a->prefix_len || !a->out)
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: NULL pointer%s");
+  if (a->cache.num_rows <= 0 || a->cache.num_rows >= (1ll << 31) - 64)
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: cache.num_rows is required, below 2^31%s");
+  if (a->ckv_row_stride < a->d_latent || a->kpe_row_stride < a->d_rope ||
+      (a->ckv_row_stride * 2) % 16 || (a->kpe_row_stride * 2) % 16 || !aligned16(a->c_kv) ||
+      !aligned16(a->k_pe) || !aligned16(a->q_nope) || !aligned16(a->q_pe) ||
+      !aligned16(a->w_kv) || ((uintptr_t)a->out & 31u))
+    return fail(TV_ERR_INVALID_ARG,
+                "tv_prefill_attn: tensors and rows must be 16-byte aligned (out: 32)%s");
+  if (a->cache.page_table) {
+    if (a->cache.page_size != 64)
+      return fail(TV_ERR_UNSUPPORTED, "tv_prefill_attn: needs 64-token pages%s");
+    if (a->cache.max_pages <= 0 || a->max_kv_len > 64ll * a->cache.max_pages)
+      return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: max_kv_len exceeds max_pages * 64%s");
+  } else if (a->cache.kv_stride_b < a->max_kv_len) {
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: kv_stride_b < max_kv_len%s");
+  }
+  return TV_OK;
+}
+
+size_t tv_prefill_attn_workspace_size(const tv_prefill_args* a) {
+  g_last_error.clear();
+  if (check_prefill(a) != TV_OK || a->B == 0 || a->T == 0) return 0;
+  return tv::prefill_workspace(a);
+}
+
+int tv_prefill_attn(const tv_prefill_args* a, void* workspace, size_t ws_bytes, void* stream) {
+  g_last_error.clear();
+  const int rc = check_prefill(a);
+  if (rc != TV_OK) return rc;
+  if (a->B == 0 || a->T == 0) return TV_OK;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < tv::prefill_workspace(a))
+    return fail(TV_ERR_WORKSPACE, "tv_prefill_attn: workspace missing, misaligned or smaller than "
+                                  "tv_prefill_attn_workspace_size()%s");
+  cudaError_t e = tv::launch_prefill(a, workspace, sm_count(), (cudaStream_t)stream);
+  return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_prefill_attn");
+}
+
 }  // extern "C"

@@ -16,6 +16,7 @@ this module raises.
     pages_reserve(pool, length, new_length, copies, ...), pages_fork(pool, fork_from, length),
     pages_release(pool, keep), pages_compact(pool, moves, n_moves),
     pages_copy(c_kv, k_pe, page_size, copies, ...)
+    prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, ...)
 """
 from __future__ import annotations
 
@@ -110,6 +111,24 @@ class SampleArgs(ctypes.Structure):
     ]
 
 
+class PrefillArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32), ("d_nope", ctypes.c_int32),
+        ("d_rope", ctypes.c_int32), ("d_v", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("dt", ctypes.c_int),
+        ("q_nope", ctypes.c_void_p), ("q_pe", ctypes.c_void_p), ("w_kv", ctypes.c_void_p),
+        ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("ckv_row_stride", ctypes.c_int64), ("kpe_row_stride", ctypes.c_int64),
+        ("cache", CacheLayout),
+        ("q_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+        ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32),
+        ("total_kv", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
 class PagePool(ctypes.Structure):
     _fields_ = [
         ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_void_p),
@@ -165,6 +184,9 @@ def load():
     lib.tv_pages_compact.argtypes = [POOL, P, P, P, P, sz, P]
     lib.tv_pages_copy.argtypes = [P, P, i32, i64, i64, i32, i32, i32, i64, i64, i32, i64, P, P,
                                   i32, P, P]
+    lib.tv_prefill_attn_workspace_size.argtypes = [ctypes.POINTER(PrefillArgs)]
+    lib.tv_prefill_attn_workspace_size.restype = sz
+    lib.tv_prefill_attn.argtypes = [ctypes.POINTER(PrefillArgs), P, sz, P]
     _lib = lib
     return lib
 
@@ -651,3 +673,59 @@ def pages_copy(c_kv, k_pe, page_size, copies, count=None, status=None, stream=No
                                   int(page_size), rows, _ptr(copies), _ptr(count), n,
                                   _ptr(status), st.handle)
     _check(rc, "tv_pages_copy")
+
+
+def prefill_args(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, max_q_len,
+                 max_kv_len, total_kv, page_table=None, page_size=64, kv_stride_b=0,
+                 status=None) -> PrefillArgs:
+    T, H, DN = q_nope.shape
+    B, DR, DL = prefix_len.shape[0], q_pe.shape[2], w_kv.shape[2]
+    DV = w_kv.shape[1] - DN
+    for name, t, shape in (("q_nope", q_nope, (T, H, DN)), ("q_pe", q_pe, (T, H, DR)),
+                           ("w_kv", w_kv, (H, DN + DV, DL)), ("out", out, (T, H, DV))):
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != q_nope.dtype:
+            raise ValueError(f"{name} must be contiguous {q_nope.dtype} of shape {shape}")
+    for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
+        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype != q_nope.dtype:
+            raise ValueError(f"{name} must be rows of {d} contiguous {q_nope.dtype}")
+    _i32("q_start", q_start, (B + 1,))
+    _i32("prefix_len", prefix_len, (B,))
+    if page_table is not None:
+        _i32("page_table", page_table, (B, page_table.shape[1]))
+    _status_arg(status)
+    a = PrefillArgs()
+    a.struct_size = ctypes.sizeof(PrefillArgs)
+    a.B, a.H, a.T, a.d_latent, a.d_nope, a.d_rope, a.d_v = B, H, T, DL, DN, DR, DV
+    a.scale, a.dt = float(scale), _dt(q_nope)
+    a.q_nope, a.q_pe, a.w_kv = q_nope.data_ptr(), q_pe.data_ptr(), w_kv.data_ptr()
+    a.c_kv, a.k_pe = c_kv.data_ptr(), k_pe.data_ptr()
+    a.ckv_row_stride, a.kpe_row_stride = c_kv.stride(0), k_pe.stride(0)
+    a.cache = make_cache(page_table, page_size, kv_stride_b, min(c_kv.shape[0], k_pe.shape[0]))
+    a.q_start, a.prefix_len = q_start.data_ptr(), prefix_len.data_ptr()
+    a.max_q_len, a.max_kv_len, a.total_kv = int(max_q_len), int(max_kv_len), int(total_kv)
+    a.out = out.data_ptr()
+    a.status = None if status is None else status.data_ptr()
+    return a
+
+
+def prefill_workspace_size(a: PrefillArgs) -> int:
+    return int(load().tv_prefill_attn_workspace_size(ctypes.byref(a)))
+
+
+def prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, max_q_len,
+                 max_kv_len, total_kv, page_table=None, page_size=64, kv_stride_b=0,
+                 status=None, workspace=None, stream=None):
+    """Causal attention of packed prompts in the expanded form: q_nope [T,H,128], q_pe
+    [T,H,64], w_kv [H,256,DL], cache rows c_kv [rows,DL] and k_pe [rows,64], q_start [B+1]
+    and prefix_len [B] int32 -> out [T,H,128] (all bf16).  max_q_len, max_kv_len and
+    total_kv bound a sequence's queries, its keys, and all sequences' keys together."""
+    dev = _on_device(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, page_table,
+                     status, workspace)
+    a = prefill_args(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, max_q_len,
+                     max_kv_len, total_kv, page_table, page_size, kv_stride_b, status)
+    with _launch(dev, stream) as st:
+        if workspace is None:
+            workspace = _scratch("prefill", dev, st.stream, max(1, prefill_workspace_size(a)))
+        rc = load().tv_prefill_attn(ctypes.byref(a), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), st.handle)
+    _check(rc, "tv_prefill_attn")

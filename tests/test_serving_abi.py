@@ -112,3 +112,63 @@ def test_pages_copy_arguments(tvlib):
 
 def test_new_status_has_a_text(tvlib):
     assert tv.load().tv_status_string(tv.TV_ERR_NO_PAGES) == b"too few free pages"
+
+
+def prefill_args(**kw):
+    a = tv.PrefillArgs()
+    a.struct_size = ctypes.sizeof(tv.PrefillArgs)
+    a.B, a.H, a.T, a.d_latent, a.d_nope, a.d_rope, a.d_v = 2, 16, 100, 512, 128, 64, 128
+    a.scale, a.dt = 0.07, tv.TV_BF16
+    a.q_nope = a.q_pe = a.w_kv = a.c_kv = a.k_pe = a.q_start = a.prefix_len = a.out = FAKE
+    a.ckv_row_stride, a.kpe_row_stride = 512, 64
+    a.cache = tv.CacheLayout(FAKE, 64, 10, 0, 6400)
+    a.max_q_len, a.max_kv_len, a.total_kv = 64, 640, 1000
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(struct_size=8), tv.TV_ERR_INVALID_ARG),
+    (dict(B=-1), tv.TV_ERR_INVALID_ARG),
+    (dict(H=0), tv.TV_ERR_INVALID_ARG),
+    (dict(T=-1), tv.TV_ERR_INVALID_ARG),
+    (dict(total_kv=-1), tv.TV_ERR_INVALID_ARG),
+    (dict(scale=0.0), tv.TV_ERR_INVALID_ARG),
+    (dict(scale=-1.0), tv.TV_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), tv.TV_ERR_INVALID_ARG),
+    (dict(dt=tv.TV_F32), tv.TV_ERR_UNSUPPORTED),
+    (dict(d_nope=64), tv.TV_ERR_UNSUPPORTED),
+    (dict(d_rope=32), tv.TV_ERR_UNSUPPORTED),
+    (dict(d_v=64), tv.TV_ERR_UNSUPPORTED),
+    (dict(d_latent=520, ckv_row_stride=520), tv.TV_ERR_UNSUPPORTED),
+    (dict(H=65536), tv.TV_ERR_UNSUPPORTED),
+    (dict(B=1 << 19, H=1 << 14), tv.TV_ERR_UNSUPPORTED),
+    (dict(total_kv=1 << 31), tv.TV_ERR_UNSUPPORTED),
+    (dict(q_nope=None), tv.TV_ERR_INVALID_ARG),
+    (dict(q_start=None), tv.TV_ERR_INVALID_ARG),
+    (dict(w_kv=FAKE + 8), tv.TV_ERR_INVALID_ARG),
+    (dict(out=FAKE + 16), tv.TV_ERR_INVALID_ARG),
+    (dict(ckv_row_stride=511), tv.TV_ERR_INVALID_ARG),
+    (dict(kpe_row_stride=68), tv.TV_ERR_INVALID_ARG),
+    (dict(max_kv_len=641), tv.TV_ERR_INVALID_ARG),
+    (dict(cache=tv.CacheLayout(FAKE, 32, 20, 0, 6400)), tv.TV_ERR_UNSUPPORTED),
+    (dict(cache=tv.CacheLayout(FAKE, 64, 10, 0, 0)), tv.TV_ERR_INVALID_ARG),
+    (dict(cache=tv.CacheLayout(None, 64, 0, 639, 6400)), tv.TV_ERR_INVALID_ARG),
+])
+def test_prefill_arguments(tvlib, kw, code):
+    lib, a = tv.load(), prefill_args(**kw)
+    assert lib.tv_prefill_attn_workspace_size(ctypes.byref(a)) == 0
+    assert lib.tv_prefill_attn(ctypes.byref(a), FAKE, 1 << 40, None) == code
+    assert lib.tv_last_error()
+
+
+def test_prefill_workspace(tvlib):
+    lib, a = tv.load(), prefill_args()
+    need = lib.tv_prefill_attn_workspace_size(ctypes.byref(a))
+    assert need >= 1000 * (16 * 512 + 128)
+    for ws, size in ((None, need), (FAKE + 64, need), (FAKE, need - 1)):
+        assert lib.tv_prefill_attn(ctypes.byref(a), ws, size, None) == tv.TV_ERR_WORKSPACE
+    for kw in (dict(B=0), dict(T=0)):
+        empty = prefill_args(**kw)
+        assert lib.tv_prefill_attn(ctypes.byref(empty), None, 0, None) == tv.TV_OK
