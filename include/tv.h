@@ -584,9 +584,10 @@ int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  *
  * The sequences' queries are packed: sequence b has rows q_start[b] .. q_start[b+1]-1 of
  * q_nope, q_pe and out.  Its keys 0 .. prefix_len[b] + q_len - 1 are all in the cache (the
- * prompt's own rows included).  Expanded keys and values, and the softmax weights, are
- * rounded to bf16 for the tensor cores; sums and statistics are 32-bit.  Values in the
- * inputs must be finite.
+ * prompt's own rows included).  For the tensor cores expanded keys are rounded to bf16,
+ * expanded values and the softmax weights to fp16 (so a value's magnitude must stay within
+ * 65504: a larger one is clamped and reported); sums and statistics are 32-bit.  The inputs
+ * must be finite.
  */
 typedef struct {
   uint32_t struct_size;      /* sizeof(tv_prefill_args): ABI check */
@@ -613,7 +614,8 @@ typedef struct {
                                 the bounds above, with a negative prefix_len, or whose
                                 q_start is negative, above its end or below an earlier one
                                 (its rows are left as they were), or a page of
-                                it outside the cache (that page reads as zeros). */
+                                it outside the cache (that page reads as zeros), or an expanded
+                                value past 65504. */
 } tv_prefill_args;
 
 /* Bytes of workspace (the expanded keys and values: about 512 * H + 128 bytes per key);

@@ -12,9 +12,10 @@
 // Three kernels:
 //   plan     one block: where each sequence's expanded keys go, the tiles of the other two;
 //   expand   [K | V] = C W^T for every sequence and head, a GEMM of 128 keys x 256 outputs
-//            x d_latent, rounded to bf16 into the workspace (the precision the tensor cores
-//            read); rows behind a sequence's last key are zero, so that masked weights
-//            (zero) times them is zero;
+//            x d_latent, rounded into the workspace to 16 bits (what the tensor cores read):
+//            K to bf16, the type of the queries it meets, V to fp16 (three bits more); rows
+//            behind a sequence's last key are zero, so that masked weights (zero) times them
+//            is zero;
 //   attend   per head and 256 queries, an online softmax over 128 keys at a time.
 //
 // Both tensor-core kernels are warp-specialised: one thread issues TMA loads into a ring of
@@ -23,6 +24,7 @@
 // kernel records TV_ERR_TIMEOUT, waits for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -44,11 +46,12 @@ constexpr int kPair = 2 * kBlock;               // queries per CTA
 constexpr int kChunk = kBlock * 128;            // 128 rows of 64 bf16: 16 KB
 constexpr uint64_t kDeadlineNs = 2000000000ull;
 constexpr float kRescale = 8.0f;                // log2: see attend_kernel
+constexpr float kMaxV = 65504.f;                // the largest fp16
 
 // ---- workspace --------------------------------------------------------------------------
 // counts {query tiles, key tiles}; query tiles {first row of q, rows left, position of the
 // first row, first expanded key}; key tiles {sequence, first key, expanded row, rows left};
-// then K [H][cap][128], V [H][cap][128] and the rope keys [cap][64], bf16.
+// then K [H][cap][128] in bf16, V [H][cap][128] in fp16 and the rope keys [cap][64].
 struct Layout {
   int64_t cap;               // expanded key rows
   int64_t max_q, max_k;      // tiles at most
@@ -241,6 +244,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
 // 32 bytes in one store (sm_100)
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
@@ -270,7 +277,8 @@ struct ExpandArgs {
   int64_t kv_stride_b, num_rows, cap;
   const __nv_bfloat16* k_pe;
   int64_t kpe_stride;
-  __nv_bfloat16 *K, *V, *KR;
+  __nv_bfloat16 *K, *KR;
+  __half* V;
   int32_t* status;
 };
 
@@ -392,6 +400,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       if (!__all_sync(0xffffffffu, wait_for(sh.abort, &sh.acc_full[buf], (i >> 1) & 1))) break;
       tc_fence_after();
       const int64_t at = (int64_t)h * p.cap + kt.z + r;
+      float big = 0.f;
 #pragma unroll
       for (int c = 0; c < kKV; c += 32) {
         uint32_t x[32];
@@ -399,12 +408,20 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         tmem_wait_ld_regs(x);
         uint32_t y[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          y[k] = live ? pack_bf16(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])) : 0u;
-        __nv_bfloat16* dst = c < kDN ? p.K + at * kDN + c : p.V + at * kDV + (c - kDN);
+        for (int k = 0; k < 16; ++k) {
+          float a = __uint_as_float(x[2 * k]), b = __uint_as_float(x[2 * k + 1]);
+          if (c >= kDN) {
+            big = fmax3(big, fabsf(a), fabsf(b));
+            a = fminf(fmaxf(a, -kMaxV), kMaxV);
+            b = fminf(fmaxf(b, -kMaxV), kMaxV);
+          }
+          y[k] = !live ? 0u : c < kDN ? pack_bf16(a, b) : pack_f16(a, b);
+        }
+        void* dst = c < kDN ? (void*)(p.K + at * kDN + c) : (void*)(p.V + at * kDV + (c - kDN));
         st_global_32(dst, y);
-        st_global_32(dst + 16, y + 8);
+        st_global_32((char*)dst + 32, y + 8);
       }
+      if (live && big > kMaxV) report(p.status, TV_ERR_BOUNDS);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
@@ -418,7 +435,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 
 // ---- attend -------------------------------------------------------------------------------
 // A CTA takes one head and up to 256 queries as two 128-row tiles that share every key
-// block.  TMEM (512 columns): S0, S1 (128 each; P, in bf16, overwrites the first half of
+// block.  TMEM (512 columns): S0, S1 (128 each; P, in fp16, overwrites the first half of
 // its S) and O0, O1.  While one tile's softmax runs, the tensor cores work for the other:
 // per tile and block 12 MMAs of 128x128x16 for S and 8 for O, 1280 clocks at the full rate,
 // against 16384 exponentials.
@@ -427,7 +444,8 @@ constexpr int kRing = 8;  // 16 KB chunks, 5 per key block
 constexpr int kQBytes = 3 * kChunk;
 constexpr uint32_t kTmS = 0, kTmO = 256;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
-constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1);
+// the same with fp16 operands (type fields 0)
+constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1) & ~((1u << 7) | (1u << 10));
 
 struct AttendShared {
   uint64_t full[kRing], empty[kRing], q_full, s_full[2], p_full[2], o_full[2], last;
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           y = ex2(y);
           l0 += x;
           l1 += y;
-          pk[k] = pack_bf16(x, y);  // the tensor cores take bf16: 2^-9 of a weight at most
+          pk[k] = pack_f16(x, y);  // V's type; weights stay below 2^8
         }
         tmem_st32(ts + 32 * half, pk);
       }
@@ -787,7 +805,7 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   xa.k_pe = (const __nv_bfloat16*)a->k_pe;
   xa.kpe_stride = a->kpe_row_stride;
   xa.K = (__nv_bfloat16*)(base + l.k);
-  xa.V = (__nv_bfloat16*)(base + l.v);
+  xa.V = (__half*)(base + l.v);
   xa.KR = (__nv_bfloat16*)(base + l.kr);
   xa.status = a->status;
   const int64_t exp_tiles = l.max_k * a->H;

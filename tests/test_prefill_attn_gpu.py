@@ -2,8 +2,8 @@
 in 64 bits.
 
 Tolerance.  A rounding to bf16 is off by at most h = 2^-8 relative.  The kernel rounds the
-expanded keys, the expanded values, the softmax weights and the output (everything else is
-32-bit, below 1e-5 of it at these sizes).  With A = sum_j p_j |v_j| per output element, and
+expanded keys and the output to bf16, the expanded values and the softmax weights to fp16
+(2^-11, counted as h here; everything else is 32-bit, below 1e-5 of it at these sizes).  With A = sum_j p_j |v_j| per output element, and
 D = max_j scale sum_d |q_d k_jd| h the most a score moves (so that a weight moves by at most
 e^(2D)), the output is within
     A (e^(2D) (1 + h)^2 - 1) + h |out| (1 + ..) + 1e-5 A.
@@ -260,6 +260,18 @@ def test_pages_outside_the_cache_read_as_zeros(page):
         s[k] = torch.cat([s[k], torch.zeros((1, s[k].shape[1]), dtype=torch.bfloat16)])
     s["rows"][0][64:128] = len(s["c_kv"]) - 1
     close(s, out, 0, rms=False)
+
+
+def test_values_past_the_fp16_range_are_clamped_and_reported():
+    s = make(18, 2, [40], [100], DL=64)
+    s["w_kv"][1, 128 + 5] = 512.0
+    s["c_kv"][s["rows"][0][77]] = 4.0      # 64 * 4 * 512 = 131072
+    out = run(s, tv.TV_ERR_BOUNDS)
+    one = dict(s, H=1, q_nope=s["q_nope"][:, :1], q_pe=s["q_pe"][:, :1], w_kv=s["w_kv"][:1])
+    close(one, out[:, :1], 0, rms=False)   # the other head is untouched
+    assert np.isfinite(out).all() and out[:, 1, 5].max() <= 65504
+    s["c_kv"][s["rows"][0][77]] = 1.9921875  # 65280: in range
+    run(s)
 
 
 def test_captured_and_replayed_with_other_lengths():
