@@ -222,6 +222,15 @@ __device__ __forceinline__ bool wait_for(Abort& ab, uint64_t* bar, uint32_t pari
   if (mbar_try_wait_cta(a, parity)) return true;
   return wait_slow(ab, a, parity);
 }
+// The same without suspension, for the waits on the critical chain (a suspended waiter takes
+// hundreds of clocks to wake).
+__device__ __forceinline__ bool spin_for(Abort& ab, uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 4096; ++i)
+    if (mbar_test(a, parity)) return true;
+  return wait_slow(ab, a, parity);
+}
 // Whether or not the kernel is giving up: a copy or MMA in flight has to land first.
 __device__ __noinline__ void drain(Abort& ab, uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
@@ -267,7 +276,7 @@ struct ExpandShared {
   uint32_t tmem;
   Abort abort;
 };
-constexpr int kExpSmem = kExpStages * kExpStage + (int)sizeof(ExpandShared) + 1024;
+constexpr int kExpSmem = kExpStages * kExpStage + (int)sizeof(ExpandShared);
 
 struct ExpandArgs {
   const int32_t* counts;
@@ -293,8 +302,11 @@ __device__ __forceinline__ int64_t cache_row64(const ExpandArgs& p, int b, int64
 __global__ void __launch_bounds__(kExpThreads, 1)
     expand_kernel(ExpandArgs p, const __grid_constant__ CUtensorMap map_c,
                   const __grid_constant__ CUtensorMap map_w) {
-  extern __shared__ unsigned char raw[];
-  unsigned char* smem = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
+    if (threadIdx.x == 0) report(p.status, TV_ERR_UNSUPPORTED);
+    return;
+  }
   ExpandShared& sh = *(ExpandShared*)(smem + kExpStages * kExpStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_k = p.counts[1];
@@ -439,20 +451,23 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 // its S) and O0, O1.  While one tile's softmax runs, the tensor cores work for the other:
 // per tile and block 12 MMAs of 128x128x16 for S and 8 for O, 1280 clocks at the full rate,
 // against 16384 exponentials.
-constexpr int kAttThreads = 384;
-constexpr int kRing = 8;  // 16 KB chunks, 5 per key block
+constexpr int kAttThreads = 640;
+constexpr int kRing = 8;  // 16 KB chunks, 5 per key block: K and V of 1.6 blocks
 constexpr int kQBytes = 3 * kChunk;
 constexpr uint32_t kTmS = 0, kTmO = 256;
+constexpr uint32_t kGaveUp = 0x7FC0DEADu;  // in place of a maximum: this half's wait ran out
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
 // the same with fp16 operands (type fields 0)
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1) & ~((1u << 7) | (1u << 10));
 
 struct AttendShared {
-  uint64_t full[kRing], empty[kRing], q_full, s_full[2], p_full[2], o_full[2], last;
+  uint64_t k_full[2], v_full[2], k_done[2], v_done[2];  // of a block, by its parity
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], last;
   uint32_t tmem;
   Abort abort;
+  float row[2][2][kBlock];  // a tile's row statistics, by half
 };
-constexpr int kAttSmem = 2 * kQBytes + kRing * kChunk + (int)sizeof(AttendShared) + 1024;
+constexpr int kAttSmem = 2 * kQBytes + kRing * kChunk + (int)sizeof(AttendShared);
 static_assert(kAttSmem <= 232448, "shared memory of an SM");
 
 struct AttendArgs {
@@ -470,8 +485,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                   const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ CUtensorMap map_kr) {
-  extern __shared__ unsigned char raw[];
-  unsigned char* smem = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles need it
+    if (threadIdx.x == 0) report(p.status, TV_ERR_UNSUPPORTED);
+    return;
+  }
   unsigned char* ring = smem + 2 * kQBytes;
   AttendShared& sh = *(AttendShared*)(ring + kRing * kChunk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -485,17 +503,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const int n1 = tiles > 1 ? (pos0 + rows + kBlock - 1) / kBlock : 0;
   const int n = max(n0, n1);
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
-    }
     mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.last, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.k_done[i], 1);
+      mbar_init(&sh.v_done[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
     }
-    mbar_init(&sh.last, 1);
     sh.abort.flag = 0;
     sh.abort.status = p.status;
     fence_mbar_init();
@@ -518,181 +536,219 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       tma_load_3d(q + kChunk, &map_q, 64, h, row, &sh.q_full);
       tma_load_3d(q + 2 * kChunk, &map_qr, 0, h, row, &sh.q_full);
     }
-    uint32_t u = 0;
+    // block j's chunks are ring entries 5j .. 5j+4: K nope, K nope, K rope (128 keys of 64
+    // elements each), V, V (64 keys of 128 elements each, as two 64-wide column pieces).
+    // An entry is free again when the block it last held a part of is done with.
     bool ok = true;
+    int armed_k = 0, armed_v = 0;
     for (int j = 0; ok && j < n; ++j) {
       const int key = key0 + j * kBlock;
-      for (int c = 0; c < 5; ++c, ++u) {
-        const uint32_t s = u % kRing;
-        if (!wait_for(sh.abort, &sh.empty[s], ((u / kRing) & 1) ^ 1)) {
-          ok = false;
-          break;
+      for (int c = 0; c < 5; ++c) {
+        const int u = 5 * j + c, before = u - kRing;
+        if (ok && before >= 0) {
+          const int bj = before / 5;
+          uint64_t* done = before - 5 * bj < 3 ? &sh.k_done[bj & 1] : &sh.v_done[bj & 1];
+          ok = wait_for(sh.abort, done, (bj >> 1) & 1);
         }
-        mbar_arrive_expect_tx(&sh.full[s], kChunk);
-        unsigned char* dst = ring + s * kChunk;
-        if (c < 2) tma_load_3d(dst, &map_k, 64 * c, key, h, &sh.full[s]);
-        else if (c == 2) tma_load_2d(dst, &map_kr, 0, key, &sh.full[s]);
-        else tma_load_4d(dst, &map_v, 0, key + 64 * (c - 3), 0, h, &sh.full[s]);
+        // giving up, but what a barrier has been armed for still has to come
+        if (!ok && (c == 0 || c == 3)) break;
+        unsigned char* dst = ring + (u % kRing) * kChunk;
+        uint64_t* kb = &sh.k_full[j & 1];
+        uint64_t* vb = &sh.v_full[j & 1];
+        if (c == 0) {
+          mbar_arrive_expect_tx(kb, 3 * kChunk);
+          ++armed_k;
+        } else if (c == 3) {
+          mbar_arrive_expect_tx(vb, 2 * kChunk);
+          ++armed_v;
+        }
+        if (c < 2) tma_load_3d(dst, &map_k, 64 * c, key, h, kb);
+        else if (c == 2) tma_load_2d(dst, &map_kr, 0, key, kb);
+        else tma_load_4d(dst, &map_v, 0, key + 64 * (c - 3), 0, h, vb);
       }
     }
-    drain_ring(sh.abort, sh.full, kRing, u);
     drain(sh.abort, &sh.q_full, 0);
+    drain_ring(sh.abort, sh.k_full, 2, armed_k);
+    drain_ring(sh.abort, sh.v_full, 2, armed_v);
   } else if (warp == 1 && lane == 0) {
+    // one issuing thread, so that the tiles take turns: a tile's MMAs run while the other
+    // tile's softmax does
     const uint32_t q = smem_u32(smem), r = smem_u32(ring);
-    // block j's chunks are ring entries 5j .. 5j+4: K nope, K nope, K rope (128 keys of 64
-    // elements each), V, V (64 keys of 128 elements each, as two 64-wide column pieces)
-    auto chunk = [&](uint32_t u) { return r + (u % kRing) * kChunk; };
-    auto arrived = [&](uint32_t u) {
-      return wait_for(sh.abort, &sh.full[u % kRing], (u / kRing) & 1);
-    };
+    auto chunk = [&](int u) { return r + (uint32_t)(u % kRing) * kChunk; };
     auto scores = [&](int t, int j) {
-#pragma unroll 1
-      for (int c = 0; c < 3; ++c)
+      const uint32_t qt = q + t * kQBytes;
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint64_t dq = smem_desc(qt + c * kChunk, 16, 1024, 2);
+        const uint64_t dk = smem_desc(chunk(5 * j + c), 16, 1024, 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + kTmS + 128 * t, smem_desc(q + t * kQBytes + c * kChunk + 32 * k, 16, 1024, 2),
-                 smem_desc(chunk(5 * j + c) + 32 * k, 16, 1024, 2), kIdescS, (c | k) != 0);
+          mma_ss(tmem + kTmS + 128 * t, dq + 2 * k, dk + 2 * k, kIdescS, (c | k) != 0);
+      }
       mma_commit(&sh.s_full[t]);
     };
-    auto keys_here = [&](int j) {
-      const bool ok = arrived(5 * j) && arrived(5 * j + 1) && arrived(5 * j + 2);
-      tc_fence_after();
-      return ok;
-    };
-    auto release = [&](uint32_t u, int k) {
-      for (int i = 0; i < k; ++i) mma_commit(&sh.empty[(u + i) % kRing]);
-    };
-    bool ok = wait_for(sh.abort, &sh.q_full, 0) && keys_here(0);
+    bool ok = wait_for(sh.abort, &sh.q_full, 0) && wait_for(sh.abort, &sh.k_full[0], 0);
     if (ok) {
+      tc_fence_after();
       scores(0, 0);
       if (tiles > 1) scores(1, 0);
-      release(0, 3);
+      mma_commit(&sh.k_done[0]);
     }
     for (int j = 0; ok && j < n; ++j) {
       bool have_v = false, have_k = false;
       for (int t = 0; ok && t < tiles; ++t) {
         const int nt = t ? n1 : n0;
         if (j >= nt) continue;
-        ok = wait_for(sh.abort, &sh.p_full[t], j & 1);
-        if (ok && !have_v) ok = have_v = arrived(5 * j + 3) && arrived(5 * j + 4);
+        ok = spin_for(sh.abort, &sh.p_full[t], j & 1) &&
+             (have_v || wait_for(sh.abort, &sh.v_full[j & 1], (j >> 1) & 1));
         if (!ok) break;
+        have_v = true;
         tc_fence_after();
+        const uint64_t dv0 = smem_desc(chunk(5 * j + 3), kChunk / 2, 1024, 2);
+        const uint64_t dv1 = smem_desc(chunk(5 * j + 4), kChunk / 2, 1024, 2);
 #pragma unroll
         for (int k = 0; k < 8; ++k)  // the keys are the contraction: V is an MN-major B
           mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + 8 * k,
-                 smem_desc(chunk(5 * j + 3 + (k >> 2)) + 2048 * (k & 3), kChunk / 2, 1024, 2),
-                 kIdescO, (j | k) != 0);
+                 (k < 4 ? dv0 : dv1) + 128 * (k & 3), kIdescO, (j | k) != 0);
         if (j + 1 < nt) {
-          if (!have_k) ok = have_k = keys_here(j + 1);
-          if (!ok) break;
+          if (!have_k) {
+            ok = have_k = wait_for(sh.abort, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
           scores(t, j + 1);
         } else {
           mma_commit(&sh.o_full[t]);
         }
       }
       if (!ok) break;
-      release(5 * j + 3, 2);
-      if (have_k) release(5 * (j + 1), 3);
+      mma_commit(&sh.v_done[j & 1]);
+      if (have_k) mma_commit(&sh.k_done[(j + 1) & 1]);
     }
     mma_commit(&sh.last);
     drain(sh.abort, &sh.last, 0);
   } else if (warp >= 4) {
-    const int t = warp >= 8 ? 1 : 0;
-    const int row = tid - 128 - 128 * t;  // of the tile
+    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
+    const int row = (warp & 3) * 32 + lane;  // of the tile = TMEM lane
     const int nt = t ? n1 : n0;
+    const uint32_t pair = 1 + 4 * t + (warp & 3);  // barrier of the two warps of these rows
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + kTmS + 128 * t, to = tmem + lanes + kTmO + 128 * t;
-    const int last_key = pos0 + t * kBlock + row;      // the row sees keys 0 .. last_key
-    const int tile_first = pos0 + t * kBlock;          // ... and every row these
+    const uint32_t ts = tmem + lanes + kTmS + 128 * t + 64 * half;
+    const uint32_t tp = tmem + lanes + kTmS + 128 * t + 32 * half;
+    const uint32_t to = tmem + lanes + kTmO + 128 * t + 64 * half;
+    const int tile_first = pos0 + t * kBlock;  // every row of the tile sees keys 0 .. this
+    const int last_key = tile_first + row;     // ... and this row 0 .. this
     const float c = p.scale_log2;
-    float m = 0.f, l = 0.f;  // running maximum (of scores times c) and sum
+    float m = 0.f, l = 0.f;  // running maximum (of scores times c); sum over this half
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
-      ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.s_full[t], j & 1));
-      if (!ok) break;
+      ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.s_full[t], j & 1));
       tc_fence_after();
-      uint32_t s[128];
+      uint32_t s[64];
+      if (ok) {
+        tmem_ld32(ts, s);
+        tmem_ld32(ts + 32, s + 32);
+        tmem_wait_ld_regs(s);
+        tmem_wait_ld_regs(s + 32);
+      }
+      const int k0 = j * kBlock + 64 * half;
+      if (k0 + 63 > tile_first) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_wait_ld_regs(s + 32 * k);
-      const int k0 = j * kBlock;
-      if (k0 + kBlock - 1 > tile_first) {
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
+        for (int k = 0; k < 64; ++k)
           if (k0 + k > last_key) s[k] = 0xFF800000u;
       }
-      float bm = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+      float b0 = __uint_as_float(s[0]), b1 = __uint_as_float(s[1]), b2 = __uint_as_float(s[2]),
+            b3 = __uint_as_float(s[3]);
 #pragma unroll
-      for (int k = 2; k < 128; k += 2)
-        bm = fmax3(bm, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-      bm *= c;
+      for (int k = 4; k < 60; k += 8) {
+        b0 = fmax3(b0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+        b1 = fmax3(b1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+        b2 = fmax3(b2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+        b3 = fmax3(b3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+      }
+      b0 = fmax3(b0, __uint_as_float(s[60]), __uint_as_float(s[61]));
+      b1 = fmax3(b1, __uint_as_float(s[62]), __uint_as_float(s[63]));
+      const float bm = fmax3(fmaxf(b0, b1), b2, b3) * c;
       // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
       // the accumulator is rescaled rarely.  Key 0 is visible to every row, so the first
-      // block always has a maximum.
-      if (j == 0) {
-        m = bm;
-      } else if (__any_sync(0xffffffffu, bm > m + kRescale)) {
-        const float mn = bm > m + kRescale ? bm : m;
-        const float f = ex2(m - mn);
-        m = mn;
-        l *= f;
-        // S of block j was issued after the O of block j - 1: O is complete
+      // block always has a maximum.  This barrier also orders both halves' reads of S
+      // before either writes P over it.
+      if (named_sync_or(pair, 64, !ok || j == 0 || bm > m + kRescale)) {
+        sh.row[t][half][row] = ok ? bm : __uint_as_float(kGaveUp);
+        named_sync(pair, 64);
+        const float other = sh.row[t][half ^ 1][row];
+        ok = !__any_sync(0xffffffffu, !ok || __float_as_uint(other) == kGaveUp);
+        if (!ok) break;
+        const float both = fmaxf(bm, other);
+        if (j == 0) {
+          m = both;
+        } else {
+          const float mn = both > m + kRescale ? both : m;
+          const float f = ex2(m - mn);
+          m = mn;
+          l *= f;
+          // S of block j was issued after the O of block j - 1: O is complete
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * k, o);
-          tmem_wait_ld_regs(o);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * k, o);
+            tmem_wait_ld_regs16(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32(to + 32 * k, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to + 16 * k, o);
+          }
         }
-        tmem_wait_st();
       }
       const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
-      float l0 = 0.f, l1 = 0.f;
+      uint64_t l2 = 0;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           float x, y;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[64 * half + 2 * k]),
-                                   __uint_as_float(s[64 * half + 2 * k + 1])),
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * q + 2 * k]),
+                                   __uint_as_float(s[32 * q + 2 * k + 1])),
                            c2, m2),
                     x, y);
           x = ex2(x);
           y = ex2(y);
-          l0 += x;
-          l1 += y;
+          l2 = f2_add(l2, f2_pack(x, y));
           pk[k] = pack_f16(x, y);  // V's type; weights stay below 2^8
         }
-        tmem_st32(ts + 32 * half, pk);
+        tmem_st16(tp + 16 * q, pk);
       }
-      l += l0 + l1;  // the sum is that of the unrounded weights
+      float la, lb;
+      f2_unpack(l2, la, lb);
+      l += la + lb;  // the sum is that of the unrounded weights
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[t]);
     }
-    if (ok && nt > 0) ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.o_full[t], 0));
-    if (ok && nt > 0) {
-      tc_fence_after();
-      const float inv = 1.f / l;
+    if (nt > 0 && ok) {
+      ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.o_full[t], 0));
+      sh.row[t][half][row] = l;
+      named_sync(pair, 64);
+      const float inv = 1.f / (l + sh.row[t][half ^ 1][row]);
       const int q = t * kBlock + row;
-      __nv_bfloat16* dst = p.out + ((int64_t)(qt.x + q) * p.H + h) * kDV;
+      if (ok) {
+        tc_fence_after();
+        __nv_bfloat16* dst = p.out + ((int64_t)(qt.x + q) * p.H + h) * kDV + 64 * half;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[32];
-        tmem_ld32(to + 32 * k, o);
-        tmem_wait_ld_regs(o);
-        uint32_t y[16];
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * k, o);
+          tmem_wait_ld_regs(o);
+          uint32_t y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          y[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-        if (q < rows) {
-          st_global_32(dst + 32 * k, y);
-          st_global_32(dst + 32 * k + 16, y + 8);
+          for (int i = 0; i < 16; ++i)
+            y[i] =
+                pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+          if (q < rows) {
+            st_global_32(dst + 32 * k, y);
+            st_global_32(dst + 32 * k + 16, y + 8);
+          }
         }
       }
     }
