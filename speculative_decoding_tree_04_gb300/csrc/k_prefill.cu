@@ -446,26 +446,26 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 }
 
 // ---- attend -------------------------------------------------------------------------------
-// A CTA takes one head and up to 256 queries as two 128-row tiles that share every key
-// block.  TMEM (512 columns): S0, S1 (128 each; P, in fp16, overwrites the first half of
-// its S) and O0, O1.  While one tile's softmax runs, the tensor cores work for the other:
-// per tile and block 12 MMAs of 128x128x16 for S and 8 for O, 1280 clocks at the full rate,
-// against 16384 exponentials.
+// Persistent CTAs; an item of work is one head and up to 256 queries as two 128-row tiles
+// that share every key block.  TMEM (512 columns): S0, S1 (128 each; P, in fp16, overwrites
+// the first half of its S) and O0, O1.  One thread issues all MMAs, so that the tiles take
+// turns: a tile's MMAs run while the other tile's softmax does.  Per tile and block these
+// are 12 of 128x128x16 for S and 8 for O, 1280 clocks at the full rate, against 16384
+// exponentials.  Sixteen warps do the softmax, eight per tile, 16 rows each: the 16x256b
+// TMEM shape spreads a row over four lanes, which meet in two shuffles.
 constexpr int kAttThreads = 640;
 constexpr int kRing = 8;  // 16 KB chunks, 5 per key block: K and V of 1.6 blocks
 constexpr int kQBytes = 3 * kChunk;
 constexpr uint32_t kTmS = 0, kTmO = 256;
-constexpr uint32_t kGaveUp = 0x7FC0DEADu;  // in place of a maximum: this half's wait ran out
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
 // the same with fp16 operands (type fields 0)
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1) & ~((1u << 7) | (1u << 10));
 
 struct AttendShared {
   uint64_t k_full[2], v_full[2], k_done[2], v_done[2];  // of a block, by its parity
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], last;
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], o_free[2], last;
   uint32_t tmem;
   Abort abort;
-  float row[2][2][kBlock];  // a tile's row statistics, by half
 };
 constexpr int kAttSmem = 2 * kQBytes + kRing * kChunk + (int)sizeof(AttendShared);
 static_assert(kAttSmem <= 232448, "shared memory of an SM");
@@ -478,6 +478,56 @@ struct AttendArgs {
   __nv_bfloat16* out;
   int32_t* status;
 };
+
+// The r-th item of this CTA.  Items are listed longest first and dealt in rounds of
+// alternating direction.
+struct Item {
+  bool some;
+  int h, row0, rows, pos0, key0, tiles, n0, n1;  // n: key blocks that a tile's last row sees
+};
+__device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int r) {
+  Item it;
+  const int64_t i =
+      (int64_t)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  it.some = i < total;
+  if (!it.some) return it;
+  const int tile = (int)i / p.H;
+  it.h = (int)i - tile * p.H;
+  const int4 qt = __ldg(p.q_tiles + tile);
+  it.row0 = qt.x;
+  it.rows = min(qt.y, kPair);
+  it.pos0 = qt.z;
+  it.key0 = qt.w;
+  it.tiles = it.rows > kBlock ? 2 : 1;
+  it.n0 = (it.pos0 + min(it.rows, kBlock) + kBlock - 1) / kBlock;
+  it.n1 = it.tiles > 1 ? (it.pos0 + it.rows + kBlock - 1) / kBlock : 0;
+  return it;
+}
+
+// Among the four lanes that share rows: lane q gives its words x[2 d], x[2 d + 1] to lane d
+// and gets y[r], y[4 + r] from lane r.
+__device__ __forceinline__ void exchange4(uint32_t* x, uint32_t* y) {
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = (i & 2) * 2 + (i & 1), b = a + 2;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, (q & 1) ? x[a] : x[b], 1);
+    if (q & 1) x[a] = got;
+    else x[b] = got;
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int b = a + 4;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, (q & 2) ? x[a] : x[b], 2);
+    if (q & 2) x[a] = got;
+    else x[b] = got;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    y[r] = x[2 * r];
+    y[4 + r] = x[2 * r + 1];
+  }
+}
 
 __global__ void __launch_bounds__(kAttThreads, 1)
     attend_kernel(AttendArgs p, const __grid_constant__ CUtensorMap map_q,
@@ -493,15 +543,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   unsigned char* ring = smem + 2 * kQBytes;
   AttendShared& sh = *(AttendShared*)(ring + kRing * kChunk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tile = blockIdx.x / p.H, h = blockIdx.x - tile * p.H;
-  if (tile >= p.counts[0]) return;
-  const int4 qt = __ldg(p.q_tiles + tile);
-  const int rows = min(qt.y, kPair), pos0 = qt.z, key0 = qt.w;
-  const int tiles = rows > kBlock ? 2 : 1;
-  // key blocks that the tiles' last rows see
-  const int n0 = (pos0 + min(rows, kBlock) + kBlock - 1) / kBlock;
-  const int n1 = tiles > 1 ? (pos0 + rows + kBlock - 1) / kBlock : 0;
-  const int n = max(n0, n1);
+  const int total = p.counts[0] * p.H;
+  if ((int)blockIdx.x >= total) return;
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.last, 1);
@@ -513,6 +556,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.o_free[i], 8);
     }
     sh.abort.flag = 0;
     sh.abort.status = p.status;
@@ -528,229 +572,274 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const uint32_t tmem = sh.tmem;
 
   if (warp == 0 && lane == 0) {
-    mbar_arrive_expect_tx(&sh.q_full, tiles * kQBytes);
-    for (int t = 0; t < tiles; ++t) {
-      unsigned char* q = smem + t * kQBytes;
-      const int row = qt.x + t * kBlock;
-      tma_load_3d(q, &map_q, 0, h, row, &sh.q_full);
-      tma_load_3d(q + kChunk, &map_q, 64, h, row, &sh.q_full);
-      tma_load_3d(q + 2 * kChunk, &map_qr, 0, h, row, &sh.q_full);
-    }
-    // block j's chunks are ring entries 5j .. 5j+4: K nope, K nope, K rope (128 keys of 64
-    // elements each), V, V (64 keys of 128 elements each, as two 64-wide column pieces).
-    // An entry is free again when the block it last held a part of is done with.
+    // Block g (counted over all items) has the ring entries 5g .. 5g+4: K nope, K nope, K
+    // rope (128 keys of 64 elements each), V, V (64 keys of 128 elements each, as two
+    // 64-wide column pieces).  An entry is free again when the block it last held a part of
+    // is done with.
     bool ok = true;
-    int armed_k = 0, armed_v = 0;
-    for (int j = 0; ok && j < n; ++j) {
-      const int key = key0 + j * kBlock;
-      for (int c = 0; c < 5; ++c) {
-        const int u = 5 * j + c, before = u - kRing;
-        if (ok && before >= 0) {
-          const int bj = before / 5;
-          uint64_t* done = before - 5 * bj < 3 ? &sh.k_done[bj & 1] : &sh.v_done[bj & 1];
-          ok = wait_for(sh.abort, done, (bj >> 1) & 1);
+    int g = 0, items = 0, armed_k = 0, armed_v = 0;
+    for (int r = 0; ok; ++r) {
+      const Item it = item_of(p, total, r);
+      if (!it.some) break;
+      // the last block of scores of the item before frees the queries
+      if (g > 0) ok = wait_for(sh.abort, &sh.k_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      if (!ok) break;
+      mbar_arrive_expect_tx(&sh.q_full, it.tiles * kQBytes);
+      ++items;
+      for (int t = 0; t < it.tiles; ++t) {
+        unsigned char* q = smem + t * kQBytes;
+        const int row = it.row0 + t * kBlock;
+        tma_load_3d(q, &map_q, 0, it.h, row, &sh.q_full);
+        tma_load_3d(q + kChunk, &map_q, 64, it.h, row, &sh.q_full);
+        tma_load_3d(q + 2 * kChunk, &map_qr, 0, it.h, row, &sh.q_full);
+      }
+      const int n = max(it.n0, it.n1);
+      for (int j = 0; ok && j < n; ++j, ++g) {
+        const int key = it.key0 + j * kBlock;
+        uint64_t* kb = &sh.k_full[g & 1];
+        uint64_t* vb = &sh.v_full[g & 1];
+#pragma unroll 1
+        for (int c = 0; c < 5; ++c) {
+          const uint32_t u = 5u * g + c;
+          if (ok && u >= (uint32_t)kRing) {
+            const uint32_t before = u - kRing, gb = before / 5;
+            uint64_t* done = before - 5 * gb < 3 ? &sh.k_done[gb & 1] : &sh.v_done[gb & 1];
+            ok = wait_for(sh.abort, done, (gb >> 1) & 1);
+          }
+          // giving up, but what a barrier has been armed for still has to come
+          if (!ok && (c == 0 || c == 3)) break;
+          unsigned char* dst = ring + (u % kRing) * kChunk;
+          if (c == 0) {
+            mbar_arrive_expect_tx(kb, 3 * kChunk);
+            ++armed_k;
+          } else if (c == 3) {
+            mbar_arrive_expect_tx(vb, 2 * kChunk);
+            ++armed_v;
+          }
+          if (c < 2) tma_load_3d(dst, &map_k, 64 * c, key, it.h, kb);
+          else if (c == 2) tma_load_2d(dst, &map_kr, 0, key, kb);
+          else tma_load_4d(dst, &map_v, 0, key + 64 * (c - 3), 0, it.h, vb);
         }
-        // giving up, but what a barrier has been armed for still has to come
-        if (!ok && (c == 0 || c == 3)) break;
-        unsigned char* dst = ring + (u % kRing) * kChunk;
-        uint64_t* kb = &sh.k_full[j & 1];
-        uint64_t* vb = &sh.v_full[j & 1];
-        if (c == 0) {
-          mbar_arrive_expect_tx(kb, 3 * kChunk);
-          ++armed_k;
-        } else if (c == 3) {
-          mbar_arrive_expect_tx(vb, 2 * kChunk);
-          ++armed_v;
-        }
-        if (c < 2) tma_load_3d(dst, &map_k, 64 * c, key, h, kb);
-        else if (c == 2) tma_load_2d(dst, &map_kr, 0, key, kb);
-        else tma_load_4d(dst, &map_v, 0, key + 64 * (c - 3), 0, h, vb);
       }
     }
-    drain(sh.abort, &sh.q_full, 0);
+    if (items > 0) drain(sh.abort, &sh.q_full, (items - 1) & 1);
     drain_ring(sh.abort, sh.k_full, 2, armed_k);
     drain_ring(sh.abort, sh.v_full, 2, armed_v);
   } else if (warp == 1 && lane == 0) {
-    // one issuing thread, so that the tiles take turns: a tile's MMAs run while the other
-    // tile's softmax does
-    const uint32_t q = smem_u32(smem), r = smem_u32(ring);
-    auto chunk = [&](int u) { return r + (uint32_t)(u % kRing) * kChunk; };
-    auto scores = [&](int t, int j) {
+    const uint32_t q = smem_u32(smem), ring0 = smem_u32(ring);
+    int g = 0;             // blocks before this item
+    int sc[2] = {0, 0};    // softmax turns of a tile before this item
+    int oc[2] = {0, 0};    // items of a tile
+    auto chunk = [&](uint32_t u) { return ring0 + (u % kRing) * kChunk; };
+    auto scores = [&](int t, int gj) {
       const uint32_t qt = q + t * kQBytes;
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
         const uint64_t dq = smem_desc(qt + c * kChunk, 16, 1024, 2);
-        const uint64_t dk = smem_desc(chunk(5 * j + c), 16, 1024, 2);
+        const uint64_t dk = smem_desc(chunk(5u * gj + c), 16, 1024, 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_ss(tmem + kTmS + 128 * t, dq + 2 * k, dk + 2 * k, kIdescS, (c | k) != 0);
       }
       mma_commit(&sh.s_full[t]);
     };
-    bool ok = wait_for(sh.abort, &sh.q_full, 0) && wait_for(sh.abort, &sh.k_full[0], 0);
-    if (ok) {
+    bool ok = true;
+    for (int r = 0; ok; ++r) {
+      const Item it = item_of(p, total, r);
+      if (!it.some) break;
+      const int n = max(it.n0, it.n1);
+      ok = wait_for(sh.abort, &sh.q_full, r & 1) &&
+           wait_for(sh.abort, &sh.k_full[g & 1], (g >> 1) & 1);
+      if (!ok) break;
       tc_fence_after();
-      scores(0, 0);
-      if (tiles > 1) scores(1, 0);
-      mma_commit(&sh.k_done[0]);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      bool have_v = false, have_k = false;
-      for (int t = 0; ok && t < tiles; ++t) {
-        const int nt = t ? n1 : n0;
-        if (j >= nt) continue;
-        ok = spin_for(sh.abort, &sh.p_full[t], j & 1) &&
-             (have_v || wait_for(sh.abort, &sh.v_full[j & 1], (j >> 1) & 1));
-        if (!ok) break;
-        have_v = true;
-        tc_fence_after();
-        const uint64_t dv0 = smem_desc(chunk(5 * j + 3), kChunk / 2, 1024, 2);
-        const uint64_t dv1 = smem_desc(chunk(5 * j + 4), kChunk / 2, 1024, 2);
+      scores(0, g);
+      if (it.tiles > 1) scores(1, g);
+      mma_commit(&sh.k_done[g & 1]);
+      for (int j = 0; ok && j < n; ++j) {
+        const int gj = g + j;
+        bool have_v = false, have_k = false;
+        for (int t = 0; ok && t < it.tiles; ++t) {
+          const int nt = t ? it.n1 : it.n0;
+          if (j >= nt) continue;
+          ok = spin_for(sh.abort, &sh.p_full[t], (sc[t] + j) & 1) &&
+               (have_v || wait_for(sh.abort, &sh.v_full[gj & 1], (gj >> 1) & 1)) &&
+               (j > 0 || oc[t] == 0 || wait_for(sh.abort, &sh.o_free[t], (oc[t] - 1) & 1));
+          if (!ok) break;
+          have_v = true;
+          tc_fence_after();
+          const uint64_t dv0 = smem_desc(chunk(5u * gj + 3), kChunk / 2, 1024, 2);
+          const uint64_t dv1 = smem_desc(chunk(5u * gj + 4), kChunk / 2, 1024, 2);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)  // the keys are the contraction: V is an MN-major B
-          mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + 8 * k,
-                 (k < 4 ? dv0 : dv1) + 128 * (k & 3), kIdescO, (j | k) != 0);
-        if (j + 1 < nt) {
-          if (!have_k) {
-            ok = have_k = wait_for(sh.abort, &sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
+          for (int k = 0; k < 8; ++k)  // the keys are the contraction: V is an MN-major B
+            mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + 8 * k,
+                   (k < 4 ? dv0 : dv1) + 128 * (k & 3), kIdescO, (j | k) != 0);
+          // the last tile is the longest: with it the block's values are done
+          if (t == it.tiles - 1) mma_commit(&sh.v_done[gj & 1]);
+          if (j + 1 < nt) {
+            if (!have_k) {
+              ok = have_k = wait_for(sh.abort, &sh.k_full[(gj + 1) & 1], ((gj + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(t, gj + 1);
+            if (t == it.tiles - 1) mma_commit(&sh.k_done[(gj + 1) & 1]);
+          } else {
+            mma_commit(&sh.o_full[t]);
           }
-          scores(t, j + 1);
-        } else {
-          mma_commit(&sh.o_full[t]);
         }
       }
-      if (!ok) break;
-      mma_commit(&sh.v_done[j & 1]);
-      if (have_k) mma_commit(&sh.k_done[(j + 1) & 1]);
+      g += n;
+      sc[0] += it.n0;
+      sc[1] += it.n1;
+      ++oc[0];
+      oc[1] += it.tiles - 1;
     }
     mma_commit(&sh.last);
     drain(sh.abort, &sh.last, 0);
   } else if (warp >= 4) {
-    const int t = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
-    const int row = (warp & 3) * 32 + lane;  // of the tile = TMEM lane
-    const int nt = t ? n1 : n0;
-    const uint32_t pair = 1 + 4 * t + (warp & 3);  // barrier of the two warps of these rows
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + kTmS + 128 * t + 64 * half;
-    const uint32_t tp = tmem + lanes + kTmS + 128 * t + 32 * half;
-    const uint32_t to = tmem + lanes + kTmO + 128 * t + 64 * half;
-    const int tile_first = pos0 + t * kBlock;  // every row of the tile sees keys 0 .. this
-    const int last_key = tile_first + row;     // ... and this row 0 .. this
+    const int t = (warp - 4) >> 3, sub = ((warp - 4) >> 2) & 1;
+    const int base = (warp & 3) * 32 + 16 * sub;  // first of this warp's rows = TMEM lanes
+    const int ra = base + (lane >> 2);            // this thread's rows: ra and ra + 8
+    const int col = 2 * (lane & 3);               // its columns: 8 i + col, 8 i + col + 1
+    const uint32_t ts = tmem + ((uint32_t)base << 16) + kTmS + 128 * t;
+    const uint32_t to = tmem + ((uint32_t)base << 16) + kTmO + 128 * t;
     const float c = p.scale_log2;
-    float m = 0.f, l = 0.f;  // running maximum (of scores times c); sum over this half
+    const uint64_t c2 = f2_pack(c, c);
+    int sc = 0, oc = 0;
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.s_full[t], j & 1));
-      tc_fence_after();
-      uint32_t s[64];
-      if (ok) {
-        tmem_ld32(ts, s);
-        tmem_ld32(ts + 32, s + 32);
+    for (int r = 0; ok; ++r) {
+      const Item it = item_of(p, total, r);
+      if (!it.some) break;
+      const int nt = t ? it.n1 : it.n0;
+      if (nt == 0) continue;
+      const int tile_first = it.pos0 + t * kBlock;  // every row of the tile sees keys 0 .. this
+      float ma = 0.f, mb = 0.f;                     // running maxima (of scores times c)
+      float la = 0.f, lb = 0.f;                     // sums over this thread's columns
+      for (int j = 0; j < nt; ++j, ++sc) {
+        ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.s_full[t], sc & 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[64];  // s[4 i + e]: row ra (e < 2) or ra + 8, column 8 i + col + (e & 1)
+        tmem_ld_16x256b_x8(ts, s);
+        tmem_ld_16x256b_x8(ts + 64, s + 32);
         tmem_wait_ld_regs(s);
         tmem_wait_ld_regs(s + 32);
-      }
-      const int k0 = j * kBlock + 64 * half;
-      if (k0 + 63 > tile_first) {
+        const int k0 = j * kBlock;
+        if (k0 + kBlock - 1 > tile_first) {
+          const int lim = tile_first + ra - k0 - col;  // row ra sees columns 8 i + e up to it
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (k0 + k > last_key) s[k] = 0xFF800000u;
-      }
-      float b0 = __uint_as_float(s[0]), b1 = __uint_as_float(s[1]), b2 = __uint_as_float(s[2]),
-            b3 = __uint_as_float(s[3]);
+          for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int k = 4; k < 60; k += 8) {
-        b0 = fmax3(b0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-        b1 = fmax3(b1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-        b2 = fmax3(b2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
-        b3 = fmax3(b3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
-      }
-      b0 = fmax3(b0, __uint_as_float(s[60]), __uint_as_float(s[61]));
-      b1 = fmax3(b1, __uint_as_float(s[62]), __uint_as_float(s[63]));
-      const float bm = fmax3(fmaxf(b0, b1), b2, b3) * c;
-      // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
-      // the accumulator is rescaled rarely.  Key 0 is visible to every row, so the first
-      // block always has a maximum.  This barrier also orders both halves' reads of S
-      // before either writes P over it.
-      if (named_sync_or(pair, 64, !ok || j == 0 || bm > m + kRescale)) {
-        sh.row[t][half][row] = ok ? bm : __uint_as_float(kGaveUp);
-        named_sync(pair, 64);
-        const float other = sh.row[t][half ^ 1][row];
-        ok = !__any_sync(0xffffffffu, !ok || __float_as_uint(other) == kGaveUp);
-        if (!ok) break;
-        const float both = fmaxf(bm, other);
+            for (int e = 0; e < 4; ++e)
+              if (8 * i + (e & 1) > lim + 8 * (e >> 1)) s[4 * i + e] = 0xFF800000u;
+        }
+        float xa = -INFINITY, ya = -INFINITY, xb = -INFINITY, yb = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          xa = fmax3(xa, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+          xb = fmax3(xb, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+          ya = fmax3(ya, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
+          yb = fmax3(yb, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
+        }
+        xa = fmaxf(xa, ya);
+        xb = fmaxf(xb, yb);
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
+        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)) * c;
+        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)) * c;
+        // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
+        // the accumulator is rescaled rarely.  Key 0 is visible to every row, so the first
+        // block always has a maximum.
         if (j == 0) {
-          m = both;
-        } else {
-          const float mn = both > m + kRescale ? both : m;
-          const float f = ex2(m - mn);
-          m = mn;
-          l *= f;
+          ma = xa;
+          mb = xb;
+        } else if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
+          const float na = xa > ma + kRescale ? xa : ma, nb = xb > mb + kRescale ? xb : mb;
+          const float fa = ex2(ma - na), fb = ex2(mb - nb);
+          ma = na;
+          mb = nb;
+          la *= fa;
+          lb *= fb;
           // S of block j was issued after the O of block j - 1: O is complete
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t o[16];
-            tmem_ld16(to + 16 * k, o);
+            tmem_ld_16x256b_x4(to + 32 * k, o);
             tmem_wait_ld_regs16(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(to + 16 * k, o);
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * ((i & 2) ? fb : fa));
+            tmem_st_16x256b_x4(to + 32 * k, o);
           }
         }
-      }
-      const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
-      uint64_t l2 = 0;
+        const uint64_t m2a = f2_pack(-ma, -ma), m2b = f2_pack(-mb, -mb);
+        uint64_t l2a = 0, l2b = 0;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pk[16];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[16];  // V's type; weights stay below 2^8
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x, y;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * q + 2 * k]),
-                                   __uint_as_float(s[32 * q + 2 * k + 1])),
-                           c2, m2),
-                    x, y);
-          x = ex2(x);
-          y = ex2(y);
-          l2 = f2_add(l2, f2_pack(x, y));
-          pk[k] = pack_f16(x, y);  // V's type; weights stay below 2^8
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t* x = s + 32 * half + 4 * i;
+            float a0, a1, b0, b1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, m2a), a0,
+                      a1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2]), __uint_as_float(x[3])), c2, m2b), b0,
+                      b1);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            b0 = ex2(b0);
+            b1 = ex2(b1);
+            l2a = f2_add(l2a, f2_pack(a0, a1));
+            l2b = f2_add(l2b, f2_pack(b0, b1));
+            pk[2 * i] = pack_f16(a0, a1);
+            pk[2 * i + 1] = pack_f16(b0, b1);
+          }
+          tmem_st_16x128b_x8(ts + 32 * half, pk);
         }
-        tmem_st16(tp + 16 * q, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        float u, v;  // the sums are those of the unrounded weights
+        f2_unpack(l2a, u, v);
+        la += u + v;
+        f2_unpack(l2b, u, v);
+        lb += u + v;
       }
-      float la, lb;
-      f2_unpack(l2, la, lb);
-      l += la + lb;  // the sum is that of the unrounded weights
-      tmem_wait_st();
+      if (!ok) break;
+      la += __shfl_xor_sync(0xffffffffu, la, 1);
+      lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+      la += __shfl_xor_sync(0xffffffffu, la, 2);
+      lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+      ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.o_full[t], oc & 1));
+      if (!ok) break;
+      ++oc;
+      tc_fence_after();
+      const float ia = 1.f / la, ib = 1.f / lb;
+      const int q = t * kBlock + ra;
+      __nv_bfloat16* dst =
+          p.out + ((int64_t)(it.row0 + q) * p.H + it.h) * kDV + 16 * (lane & 3);
+      const int64_t down = (int64_t)8 * p.H * kDV;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        uint32_t o[32];
+        tmem_ld_16x256b_x8(to + 64 * k, o);
+        tmem_wait_ld_regs(o);
+        uint32_t x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = pack_bf16(__uint_as_float(o[4 * i]) * ia, __uint_as_float(o[4 * i + 1]) * ia);
+        exchange4(x, y);
+        if (q < it.rows) st_global_32(dst + 64 * k, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = pack_bf16(__uint_as_float(o[4 * i + 2]) * ib, __uint_as_float(o[4 * i + 3]) * ib);
+        exchange4(x, y);
+        if (q + 8 < it.rows) st_global_32(dst + down + 64 * k, y);
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[t]);
-    }
-    if (nt > 0 && ok) {
-      ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.o_full[t], 0));
-      sh.row[t][half][row] = l;
-      named_sync(pair, 64);
-      const float inv = 1.f / (l + sh.row[t][half ^ 1][row]);
-      const int q = t * kBlock + row;
-      if (ok) {
-        tc_fence_after();
-        __nv_bfloat16* dst = p.out + ((int64_t)(qt.x + q) * p.H + h) * kDV + 64 * half;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * k, o);
-          tmem_wait_ld_regs(o);
-          uint32_t y[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            y[i] =
-                pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          if (q < rows) {
-            st_global_32(dst + 32 * k, y);
-            st_global_32(dst + 32 * k + 16, y + 8);
-          }
-        }
-      }
+      if (lane == 0) mbar_arrive(&sh.o_free[t]);
     }
   }
   tc_fence_before();
@@ -872,7 +961,7 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
 
   AttendArgs aa{counts, q_tiles, a->H, (float)((double)a->scale * 1.4426950408889634),
                 (__nv_bfloat16*)a->out, a->status};
-  attend_kernel<<<(unsigned)(l.max_q * a->H), kAttThreads, kAttSmem, st>>>(aa, m_q, m_qr, m_k, m_v,
+  attend_kernel<<<(unsigned)std::min<int64_t>(l.max_q * a->H, sm_count), kAttThreads, kAttSmem, st>>>(aa, m_q, m_qr, m_k, m_v,
                                                                           m_kr);
   return cudaGetLastError();
 }
