@@ -20,7 +20,7 @@
 //
 // Both tensor-core kernels are warp-specialised: one thread issues TMA loads into a ring of
 // 128-byte-swizzled tiles, one issues tcgen05.mma with accumulators in TMEM, whole warps
-// read TMEM (thread = row).  Every wait is bounded by a wall-clock deadline, after which the
+// read TMEM (thread = row).  Every wait is bounded by a deadline, after which the
 // kernel records TV_ERR_TIMEOUT, waits for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,7 +44,7 @@ constexpr int kKV = kDN + kDV;                  // outputs of the expansion per 
 constexpr int kBlock = 128;                     // keys per block, queries per tile
 constexpr int kPair = 2 * kBlock;               // queries per CTA
 constexpr int kChunk = kBlock * 128;            // 128 rows of 64 bf16: 16 KB
-constexpr uint64_t kDeadlineNs = 2000000000ull;
+constexpr long long kDeadline = 4000000000ll;   // clocks of a wait: about 2 s
 constexpr float kRescale = 8.0f;                // log2: see attend_kernel
 constexpr float kMaxV = 65504.f;                // the largest fp16
 
@@ -204,13 +204,14 @@ struct Abort {
 };
 
 __device__ __noinline__ bool wait_slow(Abort& ab, uint32_t a, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
+  // the SM's own clock: reading the global timer takes about as long as these waits do
+  const long long t0 = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_cta(a, parity)) return true;
+      if (mbar_try_wait_plain(a, parity)) return true;
     if (ab.flag) return false;
-    if (globaltimer() - t0 > kDeadlineNs) {
+    if (clock64() - t0 > kDeadline) {
       ab.flag = 1;
       report(ab.status, TV_ERR_TIMEOUT);
       return false;
@@ -219,24 +220,15 @@ __device__ __noinline__ bool wait_slow(Abort& ab, uint32_t a, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_for(Abort& ab, uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_cta(a, parity)) return true;
-  return wait_slow(ab, a, parity);
-}
-// The same without suspension, for the waits on the critical chain (a suspended waiter takes
-// hundreds of clocks to wake).
-__device__ __forceinline__ bool spin_for(Abort& ab, uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-  for (int i = 0; i < 4096; ++i)
-    if (mbar_test(a, parity)) return true;
+  if (mbar_try_wait_plain(a, parity)) return true;
   return wait_slow(ab, a, parity);
 }
 // Whether or not the kernel is giving up: a copy or MMA in flight has to land first.
 __device__ __noinline__ void drain(Abort& ab, uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_cta(a, parity))
-    if (globaltimer() - t0 > kDeadlineNs) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait_plain(a, parity))
+    if (clock64() - t0 > kDeadline) {
       report(ab.status, TV_ERR_TIMEOUT);
       return;
     }
@@ -448,14 +440,15 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 // ---- attend -------------------------------------------------------------------------------
 // Persistent CTAs; an item of work is one head and up to 256 queries as two 128-row tiles
 // that share every key block.  TMEM (512 columns): S0, S1 (128 each; P, in fp16, overwrites
-// the first half of its S) and O0, O1.  One thread issues all MMAs, so that the tiles take
-// turns: a tile's MMAs run while the other tile's softmax does.  Per tile and block these
+// the first half of its S) and O0, O1.  The tiles take turns at the tensor cores: a tile's MMAs
+// run while the other tile's softmax does.  Per tile and block these
 // are 12 of 128x128x16 for S and 8 for O, 1280 clocks at the full rate, against 16384
 // exponentials.  Sixteen warps do the softmax, eight per tile, 16 rows each: the 16x256b
 // TMEM shape spreads a row over four lanes, which meet in two shuffles.
 constexpr int kAttThreads = 640;
 constexpr int kRing = 8;  // 16 KB chunks, 5 per key block: K and V of 1.6 blocks
 constexpr int kQBytes = 3 * kChunk;
+constexpr int kPassAt = 2;  // of the three chunks of a block of scores
 constexpr uint32_t kTmS = 0, kTmO = 256;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
 // the same with fp16 operands (type fields 0)
@@ -463,7 +456,7 @@ constexpr uint32_t kIdescO = idesc_bf16_f32(128, 128, 0, 1) & ~((1u << 7) | (1u 
 
 struct AttendShared {
   uint64_t k_full[2], v_full[2], k_done[2], v_done[2];  // of a block, by its parity
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], o_free[2], last;
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], o_free[2], turn[2], last[2];
   uint32_t tmem;
   Abort abort;
 };
@@ -547,12 +540,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   if ((int)blockIdx.x >= total) return;
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.last, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.k_done[i], 1);
-      mbar_init(&sh.v_done[i], 1);
+      mbar_init(&sh.k_done[i], 2);  // one for each tile
+      mbar_init(&sh.v_done[i], 2);
+      mbar_init(&sh.turn[i], 1);
+      mbar_init(&sh.last[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 8);
       mbar_init(&sh.o_full[i], 1);
@@ -625,77 +619,116 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (items > 0) drain(sh.abort, &sh.q_full, (items - 1) & 1);
     drain_ring(sh.abort, sh.k_full, 2, armed_k);
     drain_ring(sh.abort, sh.v_full, 2, armed_v);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t q = smem_u32(smem), ring0 = smem_u32(ring);
-    int g = 0;             // blocks before this item
-    int sc[2] = {0, 0};    // softmax turns of a tile before this item
-    int oc[2] = {0, 0};    // items of a tile
+  } else if (warp == 1 || warp == 2) {
+    // One issuing warp per tile; they hand each other the turn, so that a tile's MMAs run
+    // while the other tile's softmax does, and a warp's own waits and commits fall into the
+    // other's turn.  The warp stays in step, its counters and descriptors uniform; one lane
+    // issues.
+    const int t = warp - 1;
+    const uint32_t lead = lane == 0;
+    const uint32_t q = smem_u32(smem) + t * kQBytes, ring0 = smem_u32(ring);
+    const uint32_t ts = kTmS + 128 * t, to = kTmO + 128 * t;
+    int g = 0;      // blocks before this item
+    int sc = 0;     // this tile's softmax turns before this item
+    int oc = 0;     // items with this tile
+    int turns = 0;  // turns taken
     auto chunk = [&](uint32_t u) { return ring0 + (u % kRing) * kChunk; };
-    auto scores = [&](int t, int gj) {
-      const uint32_t qt = q + t * kQBytes;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for(sh.abort, bar, parity)) != 0;
+    };
+    auto take_turn = [&](bool shared) {
+      if (!shared) return true;
+      ++turns;
+      return t == 0 ? turns == 1 || wait(&sh.turn[0], (turns - 2) & 1)
+                    : wait(&sh.turn[1], (turns - 1) & 1);
+    };
+    auto pass_turn = [&](bool shared) {
+      if (shared && lead) mbar_arrive(&sh.turn[t ^ 1]);
+    };
+    auto scores = [&](int gj, bool both) {
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        const uint64_t dq = smem_desc(qt + c * kChunk, 16, 1024, 2);
+        if (c == kPassAt) pass_turn(both);  // its way there takes about as long as the rest
+        const uint64_t dq = smem_desc(q + c * kChunk, 16, 1024, 2);
         const uint64_t dk = smem_desc(chunk(5u * gj + c), 16, 1024, 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + kTmS + 128 * t, dq + 2 * k, dk + 2 * k, kIdescS, (c | k) != 0);
+          mma_ss_lead(lead, ts, dq + 2 * k, dk + 2 * k, kIdescS, (c | k) != 0);
       }
-      mma_commit(&sh.s_full[t]);
+      mma_commit_lead(lead, &sh.s_full[t]);
     };
-    bool ok = true;
+    // this tile is done with a block's keys or values (an item's only tile counts twice)
+    auto done = [&](uint64_t* bar, bool only) {
+      mma_commit_lead(lead, bar);
+      if (only) mma_commit_lead(lead, bar);
+    };
+    bool ok = tmem == 0;  // 512 of 512 columns: the addresses above are absolute
     for (int r = 0; ok; ++r) {
       const Item it = item_of(p, total, r);
       if (!it.some) break;
-      const int n = max(it.n0, it.n1);
-      ok = wait_for(sh.abort, &sh.q_full, r & 1) &&
-           wait_for(sh.abort, &sh.k_full[g & 1], (g >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      scores(0, g);
-      if (it.tiles > 1) scores(1, g);
-      mma_commit(&sh.k_done[g & 1]);
-      for (int j = 0; ok && j < n; ++j) {
-        const int gj = g + j;
-        bool have_v = false, have_k = false;
-        for (int t = 0; ok && t < it.tiles; ++t) {
-          const int nt = t ? it.n1 : it.n0;
-          if (j >= nt) continue;
-          ok = spin_for(sh.abort, &sh.p_full[t], (sc[t] + j) & 1) &&
-               (have_v || wait_for(sh.abort, &sh.v_full[gj & 1], (gj >> 1) & 1)) &&
-               (j > 0 || oc[t] == 0 || wait_for(sh.abort, &sh.o_free[t], (oc[t] - 1) & 1));
+      const int n0 = __reduce_max_sync(0xffffffffu, it.n0);
+      const int n1 = __reduce_max_sync(0xffffffffu, it.n1);
+      const int nt = t ? n1 : n0, n = max(n0, n1);
+      const bool both = n1 > 0;
+      if (nt > 0) {
+        ok = wait(&sh.q_full, r & 1) && wait(&sh.k_full[g & 1], (g >> 1) & 1) && take_turn(both);
+        if (!ok) break;
+        tc_fence_after();
+        scores(g, both);
+        done(&sh.k_done[g & 1], !both);
+        for (int j = 0; ok && j < nt; ++j) {
+          const int gj = g + j;
+          ok = wait(&sh.v_full[gj & 1], (gj >> 1) & 1) &&
+               (j > 0 || oc == 0 || wait(&sh.o_free[t], (oc - 1) & 1)) &&
+               wait(&sh.p_full[t], (sc + j) & 1) && take_turn(both);
           if (!ok) break;
-          have_v = true;
           tc_fence_after();
           const uint64_t dv0 = smem_desc(chunk(5u * gj + 3), kChunk / 2, 1024, 2);
           const uint64_t dv1 = smem_desc(chunk(5u * gj + 4), kChunk / 2, 1024, 2);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // the keys are the contraction: V is an MN-major B
-            mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + 8 * k,
-                   (k < 4 ? dv0 : dv1) + 128 * (k & 3), kIdescO, (j | k) != 0);
-          // the last tile is the longest: with it the block's values are done
-          if (t == it.tiles - 1) mma_commit(&sh.v_done[gj & 1]);
+            mma_ts_lead(lead, to, ts + 8 * k, (k < 4 ? dv0 : dv1) + 128 * (k & 3), kIdescO,
+                        (j | k) != 0);
           if (j + 1 < nt) {
-            if (!have_k) {
-              ok = have_k = wait_for(sh.abort, &sh.k_full[(gj + 1) & 1], ((gj + 1) >> 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            scores(t, gj + 1);
-            if (t == it.tiles - 1) mma_commit(&sh.k_done[(gj + 1) & 1]);
+            done(&sh.v_done[gj & 1], !both);
+            ok = wait(&sh.k_full[(gj + 1) & 1], ((gj + 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(gj + 1, both);
+            done(&sh.k_done[(gj + 1) & 1], !both);
           } else {
-            mma_commit(&sh.o_full[t]);
+            mma_commit_lead(lead, &sh.o_full[t]);
+            pass_turn(both);
+            done(&sh.v_done[gj & 1], !both);
+          }
+        }
+        // The first tile may end a block early: it passes its turn and lets go of that
+        // block.  Its barriers' phase before (two blocks back) has to be over, or the
+        // arrival would count for that one.
+        for (int j = nt; ok && j < n; ++j) {
+          const int gj = g + j;
+          ok = take_turn(both) &&
+               (gj < 2 || (wait(&sh.k_done[gj & 1], ((gj >> 1) & 1) ^ 1) &&
+                           wait(&sh.v_done[gj & 1], ((gj >> 1) & 1) ^ 1)));
+          if (!ok) break;
+          pass_turn(both);
+          if (lead) {
+            mbar_arrive(&sh.k_done[gj & 1]);
+            mbar_arrive(&sh.v_done[gj & 1]);
           }
         }
       }
       g += n;
-      sc[0] += it.n0;
-      sc[1] += it.n1;
-      ++oc[0];
-      oc[1] += it.tiles - 1;
+      sc += nt;
+      oc += nt > 0;
     }
-    mma_commit(&sh.last);
-    drain(sh.abort, &sh.last, 0);
+    if (tmem != 0 && lane == 0) {
+      report(p.status, TV_ERR_CUDA);
+      sh.abort.flag = 1;
+    }
+    mma_commit_lead(lead, &sh.last[t]);
+    if (lane == 0) drain(sh.abort, &sh.last[t], 0);
+    __syncwarp();
   } else if (warp >= 4) {
     const int t = (warp - 4) >> 3, sub = ((warp - 4) >> 2) & 1;
     const int base = (warp & 3) * 32 + 16 * sub;  // first of this warp's rows = TMEM lanes
@@ -716,7 +749,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       float ma = 0.f, mb = 0.f;                     // running maxima (of scores times c)
       float la = 0.f, lb = 0.f;                     // sums over this thread's columns
       for (int j = 0; j < nt; ++j, ++sc) {
-        ok = __all_sync(0xffffffffu, spin_for(sh.abort, &sh.s_full[t], sc & 1));
+        ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.s_full[t], sc & 1));
         if (!ok) break;
         tc_fence_after();
         uint32_t s[64];  // s[4 i + e]: row ra (e < 2) or ra + 8, column 8 i + col + (e & 1)

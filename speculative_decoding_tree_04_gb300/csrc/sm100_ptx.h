@@ -127,11 +127,11 @@ __device__ __forceinline__ bool mbar_try_wait_cta(uint32_t addr, uint32_t parity
   return ok != 0;
 }
 
-// One probe without suspension.
-__device__ __forceinline__ bool mbar_test(uint32_t addr, uint32_t parity) {
+// Without a hint of its own: the hardware's default.
+__device__ __forceinline__ bool mbar_try_wait_plain(uint32_t addr, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; "
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; "
       "selp.u32 %0, 1, 0, p; }"
       : "=r"(ok)
       : "r"(addr), "r"(parity)
@@ -320,6 +320,35 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
+      : "memory");
+}
+// The same three for a whole warp in step, of which only the lane with `lead` set issues.  The
+// operands are then warp-uniform values that stay in uniform registers, where a single thread
+// in a branch of its own has them moved there for every MMA.
+__device__ __forceinline__ void mma_ss_lead(uint32_t lead, uint32_t d_tmem, uint64_t a_desc,
+                                            uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lead(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                            uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, e; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %5, 0; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.b32 e, %1, 0; "
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 // Completion of this thread's earlier tensor-core ops arrives on the barrier at the same
