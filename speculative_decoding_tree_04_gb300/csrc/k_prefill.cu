@@ -40,6 +40,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kDN = 128, kDR = 64, kDV = 128;   // per-head widths
+static_assert(kDN == kDV, "K and V of the workspace have one shape");
 constexpr int kKV = kDN + kDV;                  // outputs of the expansion per head
 constexpr int kBlock = 128;                     // keys per block, queries per tile
 constexpr int kPair = 2 * kBlock;               // queries per CTA
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
   __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost;
   __shared__ int s_weight[1024];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();  // the expansion may set itself up meanwhile
   if (tid == 0) {
     s_base_q = s_base_k = 0;
     s_base_max = INT_MIN;
@@ -301,9 +303,6 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   }
   ExpandShared& sh = *(ExpandShared*)(smem + kExpStages * kExpStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_k = p.counts[1];
-  const int64_t n_tiles = (int64_t)n_k * p.H;
-  if (blockIdx.x >= n_tiles) return;
   if (tid == 0) {
     for (int i = 0; i < kExpStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -326,13 +325,18 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  griddep_launch_dependents();
+  griddep_wait();  // the plan
+  const int n_k = p.counts[1];
+  const int64_t n_tiles = (int64_t)n_k * p.H;
 
   if (warp == 0 && lane == 0) {
+    fence_proxy_async_global();
     uint32_t u = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
       const int h = (int)(t / n_k);
-      const int4 kt = __ldg(p.k_tiles + (t - (int64_t)h * n_k));
+      const int4 kt = p.k_tiles[t - (int64_t)h * n_k];
       // the second half may hold no key: read past the end then (its page may not exist)
       const int row0 = (int)min(cache_row64(p, kt.x, kt.y), p.num_rows);
       const int row1 = kt.w > 64 ? (int)min(cache_row64(p, kt.x, kt.y + 64), p.num_rows)
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     uint32_t i = 0;
     for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++i) {
       const int h = (int)(t / n_k);
-      const int4 kt = __ldg(p.k_tiles + (t - (int64_t)h * n_k));
+      const int4 kt = p.k_tiles[t - (int64_t)h * n_k];
       const bool live = r < kt.w;
       if (h == 0) {  // the rope keys, once per key tile
         uint4 v[8] = {};
@@ -486,7 +490,7 @@ __device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int r) {
   if (!it.some) return it;
   const int tile = (int)i / p.H;
   it.h = (int)i - tile * p.H;
-  const int4 qt = __ldg(p.q_tiles + tile);
+  const int4 qt = p.q_tiles[tile];
   it.row0 = qt.x;
   it.rows = min(qt.y, kPair);
   it.pos0 = qt.z;
@@ -536,8 +540,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   unsigned char* ring = smem + 2 * kQBytes;
   AttendShared& sh = *(AttendShared*)(ring + kRing * kChunk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int total = p.counts[0] * p.H;
-  if ((int)blockIdx.x >= total) return;
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
     for (int i = 0; i < 2; ++i) {
@@ -564,8 +566,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  griddep_wait();  // the plan and the expanded keys
+  const int total = p.counts[0] * p.H;
 
   if (warp == 0 && lane == 0) {
+    fence_proxy_async_global();
     // Block g (counted over all items) has the ring entries 5g .. 5g+4: K nope, K nope, K
     // rope (128 keys of 64 elements each), V, V (64 keys of 128 elements each, as two
     // 64-wide column pieces).  An entry is free again when the block it last held a part of
@@ -979,24 +984,33 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   xa.k_chunks = a->d_latent / 64;
   xa.kv_stride_b = a->cache.kv_stride_b;
   xa.num_rows = a->cache.num_rows;
-  xa.cap = l.cap;
   xa.k_pe = (const __nv_bfloat16*)a->k_pe;
   xa.kpe_stride = a->kpe_row_stride;
+  xa.cap = l.cap;
   xa.K = (__nv_bfloat16*)(base + l.k);
   xa.V = (__half*)(base + l.v);
   xa.KR = (__nv_bfloat16*)(base + l.kr);
   xa.status = a->status;
-  const int64_t exp_tiles = l.max_k * a->H;
-  expand_kernel<<<(unsigned)std::min<int64_t>(exp_tiles, sm_count), kExpThreads, kExpSmem, st>>>(
-      xa, m_c, m_w);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-
   AttendArgs aa{counts, q_tiles, a->H, (float)((double)a->scale * 1.4426950408889634),
                 (__nv_bfloat16*)a->out, a->status};
-  attend_kernel<<<(unsigned)std::min<int64_t>(l.max_q * a->H, sm_count), kAttThreads, kAttSmem, st>>>(aa, m_q, m_qr, m_k, m_v,
-                                                                          m_kr);
-  return cudaGetLastError();
+
+  // each kernel's set-up runs beside the one before it (programmatic dependent launch)
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(l.max_k * a->H, sm_count));
+  cfg.blockDim = dim3(kExpThreads);
+  cfg.dynamicSmemBytes = kExpSmem;
+  e = cudaLaunchKernelEx(&cfg, expand_kernel, xa, m_c, m_w);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(l.max_q * a->H, sm_count));
+  cfg.blockDim = dim3(kAttThreads);
+  cfg.dynamicSmemBytes = kAttSmem;
+  return cudaLaunchKernelEx(&cfg, attend_kernel, aa, m_q, m_qr, m_k, m_v, m_kr);
 }
 
 }  // namespace tv
