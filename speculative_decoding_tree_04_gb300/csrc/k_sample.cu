@@ -17,6 +17,12 @@
 // sum of the W/G so far; it is recomputed from the logits when it is needed and never
 // stored.  A rejected token's own weight is zero from then on (u < 1).
 //
+// Passes.  A visited row is streamed once for its maximum and a float sum of exponentials
+// relative to a running one.  That sum is within 1e-5 of the row's, and it decides every test
+// whose two sides differ by more; only a closer one (two in 10^5), the draw at the end of the
+// walk, and what follows a rejection under draft probabilities take the exact sums below, from
+// L2 by then.
+//
 // Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
 // that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
 // are as many boundaries as tokens.  Weights are therefore held as integers in units of
@@ -40,12 +46,13 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
 constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
 constexpr int kTable = 64;
+constexpr int kCopies = 16;     // of the table, one for each lane of a half warp: no conflicts
 
 // 2^(j/64) as the sum of two floats, from the exponential's Taylor series in double.
 struct ExpTable {
@@ -88,11 +95,13 @@ struct SampleParams {
 enum : int { kAccept = 0, kResidual = 1, kDraw = 2 };
 
 struct Shared {
-  float2 exp2_table[kTable];
+  float2 exp2_table[kTable * kCopies];
   int64_t sums[2][kMaxCluster];   // exchanged slice sums, two phases
   uint64_t keys[2][kMaxCluster];  // exchanged slice maxima
   int64_t warp_sum[kWarps];       // of this CTA's slice, by warp
   uint64_t warp_key[kWarps];
+  float approx[2][kMaxCluster];   // exchanged float sums, relative to the slice's maximum
+  float warp_approx[kWarps];
   int64_t e[64];                  // weight of node i's token in its parent's row
   float q[64];                    // its draft probability
   int32_t parent[64], token[64];
@@ -105,34 +114,45 @@ struct Shared {
   int range0, range1;
 };
 
-// 2^((x - m) c) in units of 2^-44, as a float pair until the final rounding.  c = ch + cl.
+// 2^((x - m) c) in units of 2^-44, as high * 2^22 + low; c = ch + cl.
 // With y = (x - m) c = k/64 + f: 2^y = 2^(k/64) e^(f ln 2), the first factor from the
-// table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).
-__device__ __forceinline__ int64_t weight(float x, float m, float ch, float cl,
-                                          const float2* __restrict__ table) {
+// table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).  Floats
+// become integers by adding 1.5 * 2^23, whose last place is 1: conversions run at a quarter
+// of the rate.
+struct Weight {
+  int high, low;
+};
+__device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
+                                         const float2* __restrict__ table) {
   const float dh = x - m;
-  float yh = dh * ch;
-  if (!(yh > -46.f)) return 0;  // below half a unit; -inf (masked) too
+  const float yh = dh * ch;
+  if (!(yh > -46.f)) return {0, 0};  // below half a unit; -inf (masked) too
   const float bb = dh - x;
   const float dl = (x - (dh - bb)) - (m + bb);
   const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-  const float k = rintf(yh * (float)kTable);
-  const float f = fmaf(k, -1.f / kTable, yh);  // exact
+  constexpr float magic = 12582912.f;
+  const float kr = fmaf(yh, (float)kTable, magic);
+  const int ki = __float_as_int(kr) - __float_as_int(magic);
+  const float f = fmaf(kr - magic, -1.f / kTable, yh);  // exact
   constexpr float ln2h = 0.693147182464599609375f, ln2l = -1.90465429995776804525e-9f;
   const float zh = f * ln2h;
   const float zl = fmaf(f, ln2h, -zh) + fmaf(f, ln2l, yl * ln2h);
   const float p =
       zh * zh * fmaf(zh, fmaf(zh, fmaf(zh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
   const float el = fmaf(zh, zl, zl) + p;
-  const int ki = (int)k;
-  const float2 t = table[ki & (kTable - 1)];
+  const float2 t = table[(ki & (kTable - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
   const float ph = t.x * zh;
   const float pl = fmaf(t.x, zh, -ph) + fmaf(t.x, el, t.y);
   const float hi = t.x + ph;
   const float lo = ((t.x - hi) + ph) + pl;
-  const float scale = __int_as_float(((ki >> 6) + 44 + 127) << 23);
-  return __float2ll_rn(hi * scale) + (int64_t)__float2int_rn(lo * scale);
+  const int e = (ki >> 6) << 23;
+  const float a = hi * __int_as_float(e + ((22 + 127) << 23));
+  const float ra = a + magic;
+  const float rb = fmaf(a - (ra - magic), 4194304.f,
+                        lo * __int_as_float(e + ((44 + 127) << 23))) + magic;
+  return {__float_as_int(ra) - __float_as_int(magic), __float_as_int(rb) - __float_as_int(magic)};
 }
+__device__ __forceinline__ int64_t units(Weight w) { return ((int64_t)w.high << 22) + w.low; }
 
 // max(e - q S, 0) in the same units.
 __device__ __forceinline__ int64_t residual(int64_t e, float q, float sh, float sl) {
@@ -206,6 +226,10 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "f"(v)
+               : "memory");
+}
 __device__ __forceinline__ void st_cluster_u64(const void* local, uint32_t rank, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "l"(v)
                : "memory");
@@ -227,25 +251,44 @@ __device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j
   row.load(j, v);
 #pragma unroll
   for (int i = 0; i < Vec<T>::N; ++i) {
-    e[i] = weight(v[i], c.m, c.ch, c.cl, c.table);
+    e[i] = units(weight(v[i], c.m, c.ch, c.cl, c.table));
     if (c.s_hi > 0.f && e[i] > 0)
       e[i] = residual(e[i], __ldg(c.q + row.first(j) + i), c.s_hi, c.s_lo);
   }
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 // Sum of the weights of vectors [j0, j1), by one warp.
 template <typename T>
 __device__ __forceinline__ int64_t sum_range(const Row<T>& row, const Scale& c, int j0, int j1) {
   int64_t s = 0;
-  for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
-    int64_t e[Vec<T>::N];
-    weights(row, c, j, e);
+  if (c.s_hi > 0.f) {
+    for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
+      int64_t e[Vec<T>::N];
+      weights(row, c, j, e);
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) s += e[i];
+      for (int i = 0; i < Vec<T>::N; ++i) s += e[i];
+    }
+    return warp_sum(s);
   }
+  for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
+    float v[Vec<T>::N];
+    row.load(j, v);
+    int high = 0, low = 0;  // eight of at most 2^22 each
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+    for (int i = 0; i < Vec<T>::N; ++i) {
+      const Weight w = weight(v[i], c.m, c.ch, c.cl, c.table);
+      high += w.high;
+      low += w.low;
+    }
+    s += units({high, low});
+  }
+  return warp_sum(s);
 }
 
 template <typename T>
@@ -254,7 +297,8 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = C > 1 ? cluster_rank() : 0u;
   const int b = blockIdx.x / C, Q = p.Q;
-  if (tid < kTable) sh.exp2_table[tid] = make_float2(c_exp.hi[tid], c_exp.lo[tid]);
+  for (int i = tid; i < kTable * kCopies; i += kThreads)
+    sh.exp2_table[i] = make_float2(c_exp.hi[i / kCopies], c_exp.lo[i / kCopies]);
   bool ok_tree = true;
   if (tid < Q) {
     const int par = p.parent[(int64_t)b * Q + tid];
@@ -311,57 +355,95 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
       child = Vec<T>::one(row.x + sh.token[tid]);
       if (has_q) sh.q[tid] = __ldg(q + sh.token[tid]);
     }
-    // ---- the row's maximum (and, among equal values, its first index) ----
-    uint64_t key = 0;
+    // ---- the row's maximum (among equal values its first index) and the float sum ----
+    float best = -INFINITY, sum = 0.f;
+    int best_at = 0;
     uint32_t nan_bits = 0;
     for (int j = w0 + lane; j < w1; j += 32 * kUnroll) {
       float v[kUnroll][Vec<T>::N];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (j + 32 * k < w1) row.load(j + 32 * k, v[k]);
-#pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        if (j + 32 * k >= w1) continue;
-        float m = v[k][0];
-        int at = 0;
+        if (j + 32 * k < w1) {
+          row.load(j + 32 * k, v[k]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < Vec<T>::N; ++i) v[k][i] = -INFINITY;
+        }
+      }
+      float m = v[0][0];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
 #pragma unroll
         for (int i = 0; i < Vec<T>::N; ++i) {
           nan_bits = max(nan_bits, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
-          if (v[k][i] > m) {
-            m = v[k][i];
-            at = i;
-          }
+          m = fmaxf(m, v[k][i]);
         }
-        const uint64_t kk = ((uint64_t)ordered(m) << 32) |
-                            (uint32_t)(0xFFFFFFFFu - (uint32_t)(row.first(j + 32 * k) + at));
-        if (m > -INFINITY && kk > key) key = kk;
+      if (m > best) {
+        sum *= ex2((best - m) * ch);  // (from -inf: 0)
+        best = m;
+        best_at = -1;
+#pragma unroll
+        for (int k = kUnroll - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = Vec<T>::N - 1; i >= 0; --i)
+            if (v[k][i] == m) best_at = (int)row.first(j + 32 * k) + i;
+      }
+      if (best > -INFINITY) {
+        float part = 0.f;
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          float four = 0.f;
+#pragma unroll
+          for (int i = 0; i < Vec<T>::N; ++i) four += ex2((v[k][i] - best) * ch);
+          part += four;
+        }
+        sum += part;
       }
     }
+    // order-preserving value bits, then the complemented index: the largest key is the
+    // largest value's first place; a NaN anywhere beats every value
+    uint64_t key = best > -INFINITY ? ((uint64_t)ordered(best) << 32) |
+                                          (uint32_t)(0xFFFFFFFFu - (uint32_t)best_at)
+                                    : 0ull;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
       key = other > key ? other : key;
     }
-    // a NaN anywhere beats every value: the largest key of all
+    sum = key ? sum * ex2((best - unordered((uint32_t)(key >> 32))) * ch) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (__any_sync(0xffffffffu, nan_bits > 0x7F800000u)) key = ~0ull;
-    if (lane == 0) sh.warp_key[warp] = key;
+    if (lane == 0) {
+      sh.warp_key[warp] = key;
+      sh.warp_approx[warp] = sum;
+    }
     __syncthreads();
     if (tid < C) {
       uint64_t k = sh.warp_key[0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) k = max(k, sh.warp_key[w]);
-      if (C > 1)
+      const float top = unordered((uint32_t)(k >> 32));
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (sh.warp_key[w])
+          t += sh.warp_approx[w] * ex2((unordered((uint32_t)(sh.warp_key[w] >> 32)) - top) * ch);
+      if (C > 1) {
         st_cluster_u64(&sh.keys[phase][rank], (uint32_t)tid, k);
-      else
+        st_cluster_f32(&sh.approx[phase][rank], (uint32_t)tid, t);
+      } else {
         sh.keys[phase][0] = k;
+        sh.approx[phase][0] = t;
+      }
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
     key = 0;
     for (int r = 0; r < C; ++r) key = max(key, sh.keys[phase][r]);
-    phase ^= 1;
     const float m = unordered((uint32_t)(key >> 32));
     const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
+    phase ^= 1;
     if (key == 0 || key == ~0ull || m == INFINITY) {  // nothing to draw from
       if (rank == 0 && tid == 0) report(p.status, TV_ERR_INVALID_ARG);
       break;
@@ -384,13 +466,53 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
     }
     // ---- the sum of the weights, the tests, and residual sums after rejections ----
     Scale sc{m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
-    if (is_child) sh.e[tid] = weight(child, m, ch, cl, sh.exp2_table);
+    if (is_child) sh.e[tid] = units(weight(child, m, ch, cl, sh.exp2_table));
+    __syncthreads();
+    if (tid == 0) {
+      // by the float sum, as far as it decides: up to an accepted child, without a draft
+      // probability refused before it
+      double Z = 0.0;
+      for (int r = 0; r < C; ++r)
+        if (sh.keys[phase ^ 1][r])
+          Z += sh.approx[phase ^ 1][r] *
+               ex2((unordered((uint32_t)(sh.keys[phase ^ 1][r] >> 32)) - m) * ch);
+      double W = Z;
+      int next = -1;
+      sh.n_rejected = 0;
+      for (int i = node + 1; i < Q && !(p.draft && !has_q); ++i) {
+        if (sh.parent[i] != node || sh.token[i] < 0 || sh.token[i] >= p.V) continue;
+        bool again = false;
+        for (int r = 0; r < sh.n_rejected; ++r) again |= sh.rejected[r] == sh.token[i];
+        const double g = p.draft ? (double)sh.q[i] : 1.0;
+        const double w = again ? 0.0 : (double)sh.e[i] * (1.0 / (double)kUnit);
+        const double over = (double)sh.u[i] * g * W - w, error = 1e-5 * g * Z;
+        if (over < -error) {
+          next = i;
+          break;
+        }
+        if (p.draft || (over < error && w > 0.0)) break;
+        W -= w;
+        sh.rejected[sh.n_rejected++] = sh.token[i];
+      }
+      sh.next = next;
+      sh.n_rejected = 0;
+    }
+    __syncthreads();
+    if (sh.next >= 0) {
+      node = sh.next;
+      if (rank == 0 && tid == 0) {
+        emit[count] = sh.token[node];
+        path[count + 1] = node;
+      }
+      ++count;
+      __syncthreads();  // sh.next is read before the next node's tests write it
+      continue;
+    }
     // thread 0's: S and G, the child to test next, and whether the residual that is being
     // summed belongs to the rejection of child at - 1
     double S = 0.0, G = 1.0;
     int at = node + 1;
     bool rejecting = false;
-    if (tid == 0) sh.n_rejected = 0;
     for (;;) {
       const int64_t ws = sum_range(row, sc, w0, w1);
       if (lane == 0) sh.warp_sum[warp] = ws;
@@ -471,7 +593,7 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
       phase ^= 1;
       continue;
     }
-    // ---- the draw: the slice, the warp's part, a sixteenth of it, the vector, the token ----
+    // ---- the draw: the slice, the warp's part, an eighth of it, the vector, the token ----
     const int n_out = p.draft ? 0 : sh.n_rejected;  // weights still in the sums
     if (tid == 0) {
       int64_t t = sh.target;
@@ -579,11 +701,11 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
 
 }  // namespace
 
-// CTAs per sequence: as many as fill the GPU once, at most 16 and at least about 2048
-// vocabulary entries each.
+// CTAs per sequence: at most 16, about 2048 vocabulary entries each at least, and no more than
+// four per SM in all.
 int sample_cluster(int B, int64_t V, int sm_count) {
   int C = kMaxCluster;
-  while (C > 1 && ((int64_t)B * C > sm_count || V < 2048ll * C)) C /= 2;
+  while (C > 1 && ((int64_t)B * C > 4 * (int64_t)sm_count || V < 2048ll * C)) C /= 2;
   return C;
 }
 
