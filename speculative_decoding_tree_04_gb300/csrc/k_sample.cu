@@ -46,8 +46,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 32;
 constexpr int kMaxCluster = 16;
 constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
 constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
@@ -72,7 +71,7 @@ constexpr ExpTable make_exp_table() {
   }
   return t;
 }
-__constant__ ExpTable c_exp = make_exp_table();
+__device__ const ExpTable d_exp = make_exp_table();
 
 struct SampleParams {
   const void* logits;
@@ -91,25 +90,21 @@ struct SampleParams {
   int32_t* status;
 };
 
-// What the walk does next, decided by thread 0 of every CTA alike.
-enum : int { kAccept = 0, kResidual = 1, kDraw = 2 };
+// What the walk does next, decided by warp 0 of every CTA alike.
+enum : int { kAccept = 0, kExact = 1, kResidual = 2, kDraw = 3 };
 
 struct Shared {
   float2 exp2_table[kTable * kCopies];
-  int64_t sums[2][kMaxCluster];   // exchanged slice sums, two phases
-  uint64_t keys[2][kMaxCluster];  // exchanged slice maxima
-  int64_t warp_sum[kWarps];       // of this CTA's slice, by warp
-  uint64_t warp_key[kWarps];
-  float approx[2][kMaxCluster];   // exchanged float sums, relative to the slice's maximum
-  float warp_approx[kWarps];
-  int64_t e[64];                  // weight of node i's token in its parent's row
-  float q[64];                    // its draft probability
-  int32_t parent[64], token[64];
-  float u[64];
-  int32_t rejected[64];           // tokens refused at this node, and their weights
+  uint64_t keys[2][kMaxCluster];  // exchanged slice maxima, two phases
+  float approx[2][kMaxCluster];   // and float sums, relative to the slice's maximum
+  int64_t sums[2][kMaxCluster];   // exchanged slice sums
+  uint64_t warp_key[kMaxWarps];   // of this CTA's slice, by warp
+  float warp_approx[kMaxWarps];
+  int64_t warp_sum[kMaxWarps];
+  int32_t rejected[64];           // tokens refused at this node whose weights are in the sums
   int64_t rejected_e[64];
-  int n_rejected, cmd, next;
-  float s_hi, s_lo;               // S as a pair of floats
+  int n_rejected, cmd, next, top;
+  float m, s_hi, s_lo;            // the row's maximum; S as a pair of floats
   int64_t target;                 // the draw's place in the sums, and the vectors it is in
   int range0, range1;
 };
@@ -125,8 +120,9 @@ struct Weight {
 __device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
                                          const float2* __restrict__ table) {
   const float dh = x - m;
-  const float yh = dh * ch;
-  if (!(yh > -46.f)) return {0, 0};  // below half a unit; -inf (masked) too
+  const float y0 = dh * ch;
+  const bool some = y0 > -46.f;  // else below half a unit; -inf (masked) too
+  const float yh = some ? y0 : 0.f;
   const float bb = dh - x;
   const float dl = (x - (dh - bb)) - (m + bb);
   const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
@@ -150,17 +146,22 @@ __device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
   const float ra = a + magic;
   const float rb = fmaf(a - (ra - magic), 4194304.f,
                         lo * __int_as_float(e + ((44 + 127) << 23))) + magic;
-  return {__float_as_int(ra) - __float_as_int(magic), __float_as_int(rb) - __float_as_int(magic)};
+  return {some ? __float_as_int(ra) - __float_as_int(magic) : 0,
+          some ? __float_as_int(rb) - __float_as_int(magic) : 0};
 }
 __device__ __forceinline__ int64_t units(Weight w) { return ((int64_t)w.high << 22) + w.low; }
 
 // max(e - q S, 0) in the same units.
 __device__ __forceinline__ int64_t residual(int64_t e, float q, float sh, float sl) {
+  constexpr float magic = 12582912.f;
   const float p = q * sh;
   if (!(p > 0.f)) return e;
-  if (p > 2.f) return 0;  // a weight is at most 1
+  if (p > 1.f) return 0;  // a weight is at most 1
   const float pe = fmaf(q, sh, -p) + q * sl;
-  const int64_t r = e - __float2ll_rn(p * kUnit) - __float2ll_rn(pe * kUnit);
+  const float a = p * 4194304.f, ra = a + magic;
+  const float rb = fmaf(a - (ra - magic), 4194304.f, pe * kUnit) + magic;
+  const int64_t r = e - units({__float_as_int(ra) - __float_as_int(magic),
+                               __float_as_int(rb) - __float_as_int(magic)});
   return r > 0 ? r : 0;
 }
 
@@ -291,41 +292,73 @@ __device__ __forceinline__ int64_t sum_range(const Row<T>& row, const Scale& c, 
   return warp_sum(s);
 }
 
-template <typename T>
+template <typename U>
+__device__ __forceinline__ U pick(const U* two, int i) {  // slot i / 32 of lane i % 32
+  return __shfl_sync(0xffffffffu, (i >> 5) ? two[1] : two[0], i & 31);
+}
+// Largest of one 64-bit key per lane.
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+  const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+  const uint32_t low =
+      __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == high ? (uint32_t)k : 0u);
+  return ((uint64_t)high << 32) | low;
+}
+// Where `target` lies among one part per lane: the lane, and what is left of the target there.
+// The last lane below `parts` takes what rounding might leave over.
+__device__ __forceinline__ int locate(int64_t part, int parts, int64_t* target) {
+  const int lane = threadIdx.x & 31;
+  int64_t up_to = lane < parts ? part : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
+    if (lane >= o) up_to += below;
+  }
+  const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && up_to > *target);
+  const int at = past ? __ffs(past) - 1 : parts - 1;
+  *target -= __shfl_sync(0xffffffffu, up_to - part, at);
+  return at;
+}
+
+template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, int C) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int rank = C > 1 ? (int)cluster_rank() : 0;
   const int b = blockIdx.x / C, Q = p.Q;
-  for (int i = tid; i < kTable * kCopies; i += kThreads)
-    sh.exp2_table[i] = make_float2(c_exp.hi[i / kCopies], c_exp.lo[i / kCopies]);
-  bool ok_tree = true;
-  if (tid < Q) {
-    const int par = p.parent[(int64_t)b * Q + tid];
-    sh.parent[tid] = par;
-    sh.token[tid] = p.tokens[(int64_t)b * Q + tid];
-    // outside [0, 1): the nearest number inside (NaN: 0)
-    sh.u[tid] = fminf(fmaxf(p.uniforms[(int64_t)b * Q + tid], 0.f), 0x1.fffffep-1f);
-    ok_tree = tid == 0 ? par == -1 : (par >= 0 && par < tid);
-  }
-  const float T0 = p.temperature ? p.temperature[b] : 1.f;
-  const bool ok_temp = T0 >= 0.f;  // a NaN is not
-  const bool any_bad = __syncthreads_or(!ok_tree);
   int32_t* path = p.path + (int64_t)b * Q;
   int32_t* emit = p.new_tokens + (int64_t)b * Q;
-  if (rank == 0)
-    for (int i = tid; i < Q; i += kThreads) {
-      path[i] = i == 0 ? 0 : -1;
-      emit[i] = -1;
+  // warp 0 holds the tree: node lane and node lane + 32
+  int par[2] = {-2, -2}, tok[2] = {-1, -1};
+  float uni[2] = {0.f, 0.f};
+  bool ok_tree = true;
+  if (warp == 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int i = lane + 32 * s;
+      if (i >= Q) continue;
+      par[s] = p.parent[(int64_t)b * Q + i];
+      tok[s] = p.tokens[(int64_t)b * Q + i];
+      // outside [0, 1): the nearest number inside (NaN: 0)
+      uni[s] = fminf(fmaxf(p.uniforms[(int64_t)b * Q + i], 0.f), 0x1.fffffep-1f);
+      ok_tree = ok_tree && (i == 0 ? par[s] == -1 : par[s] >= 0 && par[s] < i);
+      if (rank == 0) {
+        path[i] = i == 0 ? 0 : -1;
+        emit[i] = -1;
+      }
     }
-  if (any_bad || !ok_temp) {  // the whole cluster alike
+  }
+  const float T0 = p.temperature ? p.temperature[b] : 1.f;
+  for (int i = tid; i < kTable * kCopies; i += kThreads)
+    sh.exp2_table[i] = make_float2(d_exp.hi[i / kCopies], d_exp.lo[i / kCopies]);
+  const bool ok_temp = T0 >= 0.f;  // a NaN is not
+  if (__syncthreads_or(!ok_tree) || !ok_temp) {  // the whole cluster alike
     if (rank == 0 && tid == 0) {
       p.accept_len[b] = 0;
-      report(p.status, any_bad ? TV_ERR_INVALID_TREE : TV_ERR_INVALID_ARG);
+      report(p.status, ok_temp ? TV_ERR_INVALID_TREE : TV_ERR_INVALID_ARG);
     }
     return;
   }
-  __syncthreads();  // the -1 fill is ordered before the entries written below
   const bool greedy = T0 == 0.f;
   // 1/T in units of log2 as a pair of floats; the clamp keeps 0 * inf out of the weights
   const float cq = 1.44269502162933349609375f / T0;
@@ -337,13 +370,9 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
   for (;;) {
     const Row<T> row((const T*)p.logits + ((int64_t)b * Q + node) * p.stride, p.V);
     const int per = (row.n_vec + C - 1) / C;
-    const int c0 = min(row.n_vec, (int)rank * per), c1 = min(row.n_vec, c0 + per);
+    const int c0 = min(row.n_vec, rank * per), c1 = min(row.n_vec, c0 + per);
     const int per_w = (per + kWarps - 1) / kWarps;
     const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
-    // the children's logits, while the row streams in
-    float child = 0.f;
-    const bool is_child = tid < Q && tid > node && sh.parent[tid] == node &&
-                          sh.token[tid] >= 0 && sh.token[tid] < p.V;
     const float* q = nullptr;
     bool has_q = false;
     if (p.draft) {
@@ -351,9 +380,19 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
       has_q = r < p.draft_rows;
       q = p.draft + ((int64_t)b * p.draft_rows + min(r, p.draft_rows - 1)) * p.draft_stride;
     }
-    if (is_child) {
-      child = Vec<T>::one(row.x + sh.token[tid]);
-      if (has_q) sh.q[tid] = __ldg(q + sh.token[tid]);
+    // warp 0: the children, and their logits while the row streams in
+    uint64_t children = 0;
+    float child[2] = {-INFINITY, -INFINITY}, child_q[2] = {0.f, 0.f};
+    if (warp == 0) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bool is = par[s] == node && tok[s] >= 0 && tok[s] < p.V;
+        children |= (uint64_t)__ballot_sync(0xffffffffu, is) << (32 * s);
+        if (is) {
+          child[s] = Vec<T>::one(row.x + tok[s]);
+          if (has_q) child_q[s] = __ldg(q + tok[s]);
+        }
+      }
     }
     // ---- the row's maximum (among equal values its first index) and the float sum ----
     float best = -INFINITY, sum = 0.f;
@@ -405,11 +444,7 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
     uint64_t key = best > -INFINITY ? ((uint64_t)ordered(best) << 32) |
                                           (uint32_t)(0xFFFFFFFFu - (uint32_t)best_at)
                                     : 0ull;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other > key ? other : key;
-    }
+    key = warp_max(key);
     sum = key ? sum * ex2((best - unordered((uint32_t)(key >> 32))) * ch) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -419,267 +454,271 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
       sh.warp_approx[warp] = sum;
     }
     __syncthreads();
-    if (tid < C) {
-      uint64_t k = sh.warp_key[0];
+    if (warp == 0) {
+      const uint64_t mine = lane < kWarps ? sh.warp_key[lane] : 0ull;
+      key = warp_max(mine);
+      float t = mine ? sh.warp_approx[lane] * ex2((unordered((uint32_t)(mine >> 32)) -
+                                                   unordered((uint32_t)(key >> 32))) * ch)
+                     : 0.f;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) k = max(k, sh.warp_key[w]);
-      const float top = unordered((uint32_t)(k >> 32));
-      float t = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (sh.warp_key[w])
-          t += sh.warp_approx[w] * ex2((unordered((uint32_t)(sh.warp_key[w] >> 32)) - top) * ch);
-      if (C > 1) {
-        st_cluster_u64(&sh.keys[phase][rank], (uint32_t)tid, k);
-        st_cluster_f32(&sh.approx[phase][rank], (uint32_t)tid, t);
-      } else {
-        sh.keys[phase][0] = k;
-        sh.approx[phase][0] = t;
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (C == 1) {
+        if (lane == 0) {
+          sh.keys[phase][0] = key;
+          sh.approx[phase][0] = t;
+        }
+      } else if (lane < C) {
+        st_cluster_u64(&sh.keys[phase][rank], (uint32_t)lane, key);
+        st_cluster_f32(&sh.approx[phase][rank], (uint32_t)lane, t);
       }
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
-    key = 0;
-    for (int r = 0; r < C; ++r) key = max(key, sh.keys[phase][r]);
-    const float m = unordered((uint32_t)(key >> 32));
-    const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
-    phase ^= 1;
-    if (key == 0 || key == ~0ull || m == INFINITY) {  // nothing to draw from
-      if (rank == 0 && tid == 0) report(p.status, TV_ERR_INVALID_ARG);
-      break;
-    }
-    if (greedy) {
-      if (tid == 0) {
-        int next = -1;
-        for (int i = node + 1; i < Q && next < 0; ++i)
-          if (sh.parent[i] == node && sh.token[i] == top) next = i;
-        sh.next = next;
-      }
-      __syncthreads();
-      const int next = sh.next;
-      if (rank == 0 && tid == 0) emit[count] = top;
-      if (next < 0) break;
-      ++count;
-      if (rank == 0 && tid == 0) path[count] = next;
-      node = next;
-      continue;
-    }
-    // ---- the sum of the weights, the tests, and residual sums after rejections ----
-    Scale sc{m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
-    if (is_child) sh.e[tid] = units(weight(child, m, ch, cl, sh.exp2_table));
-    __syncthreads();
-    if (tid == 0) {
-      // by the float sum, as far as it decides: up to an accepted child, without a draft
-      // probability refused before it
-      double Z = 0.0;
-      for (int r = 0; r < C; ++r)
-        if (sh.keys[phase ^ 1][r])
-          Z += sh.approx[phase ^ 1][r] *
-               ex2((unordered((uint32_t)(sh.keys[phase ^ 1][r] >> 32)) - m) * ch);
-      double W = Z;
-      int next = -1;
-      sh.n_rejected = 0;
-      for (int i = node + 1; i < Q && !(p.draft && !has_q); ++i) {
-        if (sh.parent[i] != node || sh.token[i] < 0 || sh.token[i] >= p.V) continue;
-        bool again = false;
-        for (int r = 0; r < sh.n_rejected; ++r) again |= sh.rejected[r] == sh.token[i];
-        const double g = p.draft ? (double)sh.q[i] : 1.0;
-        const double w = again ? 0.0 : (double)sh.e[i] * (1.0 / (double)kUnit);
-        const double over = (double)sh.u[i] * g * W - w, error = 1e-5 * g * Z;
-        if (over < -error) {
-          next = i;
-          break;
-        }
-        if (p.draft || (over < error && w > 0.0)) break;
-        W -= w;
-        sh.rejected[sh.n_rejected++] = sh.token[i];
-      }
-      sh.next = next;
-      sh.n_rejected = 0;
-    }
-    __syncthreads();
-    if (sh.next >= 0) {
-      node = sh.next;
-      if (rank == 0 && tid == 0) {
-        emit[count] = sh.token[node];
-        path[count + 1] = node;
-      }
-      ++count;
-      __syncthreads();  // sh.next is read before the next node's tests write it
-      continue;
-    }
-    // thread 0's: S and G, the child to test next, and whether the residual that is being
-    // summed belongs to the rejection of child at - 1
-    double S = 0.0, G = 1.0;
-    int at = node + 1;
-    bool rejecting = false;
-    for (;;) {
-      const int64_t ws = sum_range(row, sc, w0, w1);
-      if (lane == 0) sh.warp_sum[warp] = ws;
-      __syncthreads();
-      if (tid < C) {
-        int64_t t = 0;
+    int64_t child_e[2] = {0, 0};
+    if (warp == 0) {
+      const uint64_t mine = lane < C ? sh.keys[phase][lane] : 0ull;
+      key = warp_max(mine);
+      const float m = unordered((uint32_t)(key >> 32));
+      const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
+      int next = -1, cmd = kExact;
+      if (key == 0 || key == ~0ull || m == INFINITY) {  // nothing to draw from
+        cmd = kDraw;
+        next = -2;
+      } else if (greedy) {
+        const uint32_t h0 = __ballot_sync(0xffffffffu, ((uint32_t)children >> lane & 1) && tok[0] == top);
+        const uint32_t h1 =
+            __ballot_sync(0xffffffffu, ((uint32_t)(children >> 32) >> lane & 1) && tok[1] == top);
+        next = h0 ? __ffs(h0) - 1 : h1 ? 31 + __ffs(h1) : -1;
+        cmd = next >= 0 ? kAccept : kDraw;
+      } else {
+        float Z = mine ? sh.approx[phase][lane] * ex2((unordered((uint32_t)(mine >> 32)) - m) * ch)
+                       : 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) t += sh.warp_sum[w];
-        if (C > 1)
-          st_cluster_u64(&sh.sums[phase][rank], (uint32_t)tid, (uint64_t)t);
-        else
-          sh.sums[phase][0] = t;
-      }
-      if (C > 1) cluster_sync();
-      else __syncthreads();
-      if (tid == 0) {
-        int64_t W = 0;
-        for (int r = 0; r < C; ++r) W += sh.sums[phase][r];
-        int cmd = kDraw, next = -1;
-        if (rejecting && W == 0) {
-          // the drafter covers all that p has left: the two are equal but for rounding
-          cmd = kAccept;
-          next = at - 1;
-        }
-        for (; cmd == kDraw && at < Q; ++at) {
-          if (sh.parent[at] != node || sh.token[at] < 0 || sh.token[at] >= p.V) continue;
-          if (p.draft && !has_q) {  // no drafter's row for this depth: no test
-            if (rank == 0) report(p.status, TV_ERR_BOUNDS);
-            at = Q;
-            break;
-          }
-          if (p.draft && !(G > 0.0)) break;  // nothing left that could have been drawn
-          bool again = false;  // a token refused before has no weight left
-          for (int r = 0; r < sh.n_rejected; ++r) again |= sh.rejected[r] == sh.token[at];
-          const double u = sh.u[at], g = !p.draft ? 1.0 : again ? 0.0 : (double)sh.q[at];
-          const int64_t w = again       ? 0
-                            : !p.draft ? sh.e[at]
-                                       : residual(sh.e[at], sh.q[at], sc.s_hi, sc.s_lo);
-          if (u * g * (double)W < (double)w * G) {
+        for (int o = 16; o > 0; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          child_e[s] = units(weight(child[s], m, ch, cl, sh.exp2_table));
+        // by the float sum, as far as it decides: up to an accepted child, without a draft
+        // probability refused before it
+        float W = Z;
+        const float ew[2] = {(float)child_e[0] * (1.f / kUnit), (float)child_e[1] * (1.f / kUnit)};
+        uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
+        while (left) {
+          const int i = __ffsll((long long)left) - 1;
+          left &= left - 1;
+          const int x = pick(tok, i);
+          const uint64_t same =
+              (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
+              (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+          const float g = p.draft ? pick(child_q, i) : 1.f;
+          const float w = same & refused ? 0.f : pick(ew, i);
+          const float over = pick(uni, i) * g * W - w, error = 1e-5f * g * Z;
+          if (over < -error) {
+            next = i;
             cmd = kAccept;
-            next = at;
             break;
           }
-          if (!again) {
-            sh.rejected[sh.n_rejected] = sh.token[at];
-            sh.rejected_e[sh.n_rejected++] = w;
-          }
-          if (!p.draft) {
-            W -= w;
-            continue;
-          }
-          cmd = kResidual;
-          rejecting = true;
-          S += (double)W * (1.0 / (double)kUnit) / G;
-          G -= g;
-          sh.s_hi = (float)S;
-          sh.s_lo = (float)(S - (double)(float)S);
-          ++at;
-          break;
+          if (p.draft || (over < error && w > 0.f)) break;
+          W -= w;
+          refused |= 1ull << i;
         }
-        if (cmd == kDraw) sh.target = min((int64_t)((double)sh.u[0] * (double)W), W - 1);
+      }
+      if (lane == 0) {
         sh.cmd = cmd;
         sh.next = next;
+        sh.m = m;
+        sh.top = top;
+        sh.n_rejected = 0;
       }
-      __syncthreads();
-      if (sh.cmd != kResidual) break;
-      sc.s_hi = sh.s_hi;
-      sc.s_lo = sh.s_lo;
-      phase ^= 1;
     }
-    if (sh.cmd == kAccept) {
-      node = sh.next;
-      if (rank == 0 && tid == 0) {
-        emit[count] = sh.token[node];
-        path[count + 1] = node;
+    __syncthreads();
+    phase ^= 1;
+    if (sh.cmd == kExact) {
+      // ---- exact sums of the weights, the tests by them, and residuals after rejections ----
+      Scale sc{sh.m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
+      // warp 0's: S and G, the children left, the tokens refused, the child whose rejection
+      // the residual that is being summed belongs to
+      double S = 0.0, G = 1.0;
+      uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
+      int refusing = -1;
+      if (warp == 0 && p.draft && !has_q && children && rank == 0 && lane == 0)
+        report(p.status, TV_ERR_BOUNDS);  // no drafter's row for this depth: no test
+      for (;;) {
+        const int64_t ws = sum_range(row, sc, w0, w1);
+        if (lane == 0) sh.warp_sum[warp] = ws;
+        __syncthreads();
+        if (warp == 0) {
+          const int64_t t = warp_sum(lane < kWarps ? sh.warp_sum[lane] : 0);
+          if (C == 1) {
+            if (lane == 0) sh.sums[phase][0] = t;
+          } else if (lane < C) {
+            st_cluster_u64(&sh.sums[phase][rank], (uint32_t)lane, (uint64_t)t);
+          }
+        }
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        if (warp == 0) {
+          int64_t W = warp_sum(lane < C ? sh.sums[phase][lane] : 0);
+          int cmd = kDraw, next = -1, n = 0;
+          if (refusing >= 0 && W == 0) {
+            // the drafter covers all that p has left: the two are equal but for rounding
+            cmd = kAccept;
+            next = refusing;
+          }
+          while (cmd == kDraw && left && (!p.draft || G > 0.0)) {
+            const int i = __ffsll((long long)left) - 1;
+            left &= left - 1;
+            const int x = pick(tok, i);
+            const uint64_t same =
+                (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
+                (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+            const bool again = same & refused;  // a token refused before has no weight left
+            const float qx = pick(child_q, i);
+            const double u = pick(uni, i), g = !p.draft ? 1.0 : again ? 0.0 : (double)qx;
+            int64_t w = pick(child_e, i);
+            if (again) w = 0;
+            else if (p.draft) w = residual(w, qx, sc.s_hi, sc.s_lo);
+            if (u * g * (double)W < (double)w * G) {
+              cmd = kAccept;
+              next = i;
+              break;
+            }
+            refused |= 1ull << i;
+            if (!p.draft) {
+              W -= w;
+              if (!again && lane == 0) {
+                sh.rejected[n] = x;
+                sh.rejected_e[n] = w;
+              }
+              n += !again;
+              continue;
+            }
+            cmd = kResidual;
+            refusing = i;
+            S += (double)W * (1.0 / (double)kUnit) / G;
+            G -= g;
+          }
+          if (lane == 0) {
+            if (cmd == kDraw) sh.target = min((int64_t)((double)uni[0] * (double)W), W - 1);
+            sh.s_hi = (float)S;
+            sh.s_lo = (float)(S - (double)(float)S);
+            sh.n_rejected = n;
+            sh.cmd = cmd;
+            sh.next = next;
+          }
+        }
+        __syncthreads();
+        if (sh.cmd != kResidual) break;
+        sc.s_hi = sh.s_hi;
+        sc.s_lo = sh.s_lo;
+        phase ^= 1;
       }
-      ++count;
-      phase ^= 1;
-      continue;
-    }
-    // ---- the draw: the slice, the warp's part, an eighth of it, the vector, the token ----
-    const int n_out = p.draft ? 0 : sh.n_rejected;  // weights still in the sums
-    if (tid == 0) {
-      int64_t t = sh.target;
-      int owner = 0, w = 0;
-      for (; owner < C - 1; ++owner) {
-        int64_t s = sh.sums[phase][owner];
-        for (int r = 0; r < n_out; ++r)
-          if (row.vector_of(sh.rejected[r]) / per == owner) s -= sh.rejected_e[r];
-        if (t < s) break;
-        t -= s;
-      }
-      if (owner == (int)rank) {
-        for (; w < kWarps - 1; ++w) {
-          int64_t s = sh.warp_sum[w];
+      if (sh.cmd == kDraw) {
+        // ---- the draw: the slice, the warp's part, an eighth of it, the vector, the token --
+        const int n_out = sh.n_rejected;  // weights that are in the sums still
+        if (warp == 0) {
+          int64_t t = sh.target;
+          int64_t part = lane < C ? sh.sums[phase][lane] : 0;
+          for (int r = 0; r < n_out; ++r)
+            if (row.vector_of(sh.rejected[r]) / per == lane) part -= sh.rejected_e[r];
+          const int owner = locate(part, C, &t);
+          part = lane < kWarps ? sh.warp_sum[lane] : 0;
           for (int r = 0; r < n_out; ++r) {
             const int j = row.vector_of(sh.rejected[r]) - c0;
-            if (j >= 0 && j < c1 - c0 && j / per_w == w) s -= sh.rejected_e[r];
+            if (j >= 0 && j < c1 - c0 && j / per_w == lane) part -= sh.rejected_e[r];
           }
-          if (t < s) break;
-          t -= s;
+          const int w = locate(part, kWarps, &t);  // (counts in the owner only)
+          if (lane == 0) {
+            sh.next = owner;
+            sh.target = t;
+            sh.range0 = min(c1, c0 + w * per_w);
+            sh.range1 = min(c1, sh.range0 + per_w);
+          }
         }
-        sh.range0 = min(c1, c0 + w * per_w);
-        sh.range1 = min(c1, sh.range0 + per_w);
-        sh.target = t;
-      }
-      sh.next = owner;
-    }
-    __syncthreads();
-    if (sh.next != (int)rank) break;
-    const int r0 = sh.range0, r1 = sh.range1, per_r = (r1 - r0 + kWarps - 1) / kWarps;
-    const int x0 = min(r1, r0 + warp * per_r), x1 = min(r1, x0 + per_r);
-    int64_t part = sum_range(row, sc, x0, x1);
-    for (int r = 0; r < n_out; ++r) {
-      const int j = row.vector_of(sh.rejected[r]);
-      if (j >= x0 && j < x1) part -= sh.rejected_e[r];
-    }
-    __syncthreads();  // thread 0 has read the sums of the parts before
-    if (lane == 0) sh.warp_sum[warp] = part;
-    __syncthreads();
-    if (warp == 0) {
-      int64_t t = sh.target;
-      int w = 0;
-      for (; w < kWarps - 1 && t >= sh.warp_sum[w]; ++w) t -= sh.warp_sum[w];
-      const int y0 = min(r1, r0 + w * per_r), y1 = min(r1, y0 + per_r);
-      for (int j = y0; j < y1; j += 32) {
-        int64_t e[Vec<T>::N], s = 0;
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) e[i] = 0;
-        if (j + lane < y1) weights(row, sc, j + lane, e);
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) {
-          for (int r = 0; r < n_out; ++r)
-            if (row.first(j + lane) + i == sh.rejected[r]) e[i] = 0;
-          s += e[i];
-        }
-        int64_t up_to = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
-          if (lane >= o) up_to += below;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, up_to > t);
-        if (past) {
-          if (lane == __ffs(past) - 1) {
-            t -= up_to - s;
-            int at_v = 0;
-#pragma unroll
-            for (int i = 0; i < Vec<T>::N; ++i) {
-              if (t >= e[i]) ++at_v;
-              else break;
-              t -= e[i];
+        __syncthreads();
+        if (sh.next == rank) {
+          int y0 = sh.range0, y1 = sh.range1;
+          if (y1 - y0 > 128) {  // long enough for all warps to share
+            const int per_r = (y1 - y0 + kWarps - 1) / kWarps;
+            const int x0 = min(y1, y0 + warp * per_r), x1 = min(y1, x0 + per_r);
+            int64_t part = sum_range(row, sc, x0, x1);
+            for (int r = 0; r < n_out; ++r) {
+              const int j = row.vector_of(sh.rejected[r]);
+              if (j >= x0 && j < x1) part -= sh.rejected_e[r];
             }
-            emit[count] = (int32_t)(row.first(j + lane) + at_v);
+            if (lane == 0) sh.warp_sum[warp] = part;
+            __syncthreads();
+            if (warp == 0) {
+              int64_t t = sh.target;
+              const int w = locate(lane < kWarps ? sh.warp_sum[lane] : 0, kWarps, &t);
+              __syncwarp();
+              if (lane == 0) sh.target = t;
+              y0 = min(y1, y0 + w * per_r);
+              y1 = min(y1, y0 + per_r);
+              __syncwarp();
+            }
           }
-          break;
+          if (warp == 0) {
+            int64_t t = sh.target;
+            for (int j = y0; j < y1; j += 32) {
+              int64_t e[Vec<T>::N], s = 0;
+#pragma unroll
+              for (int i = 0; i < Vec<T>::N; ++i) e[i] = 0;
+              if (j + lane < y1) weights(row, sc, j + lane, e);
+#pragma unroll
+              for (int i = 0; i < Vec<T>::N; ++i) {
+                for (int r = 0; r < n_out; ++r)
+                  if (row.first(j + lane) + i == sh.rejected[r]) e[i] = 0;
+                s += e[i];
+              }
+              const int64_t all = warp_sum(s);
+              if (t >= all && j + 32 < y1) {
+                t -= all;
+                continue;
+              }
+              const int at = locate(s, 32, &t);
+              if (lane == at) {
+                int k = 0;
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < Vec<T>::N; ++i) {
+                  found = found || t < e[i];
+                  if (!found) {
+                    t -= e[i];
+                    ++k;
+                  }
+                }
+                emit[count] = (int32_t)(row.first(j + lane) + k);
+              }
+              break;
+            }
+          }
         }
-        t -= __shfl_sync(0xffffffffu, up_to, 31);
+        break;
+      }
+      phase ^= 1;
+    } else if (sh.cmd == kDraw) {  // greedy, or a row without a distribution
+      if (rank == 0 && tid == 0) {
+        if (sh.next == -2) report(p.status, TV_ERR_INVALID_ARG);
+        else emit[count] = sh.top;
+      }
+      break;
+    }
+    node = sh.next;
+    ++count;
+    if (warp == 0 && rank == 0) {
+      const int x = pick(tok, node);
+      if (lane == 0) {
+        emit[count - 1] = x;
+        path[count] = node;
       }
     }
-    break;
   }
   if (rank == 0 && tid == 0) p.accept_len[b] = count;
   if (C > 1) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
-template <typename T>
+template <typename T, int kThreads>
 cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * C));
@@ -692,11 +731,21 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (C > 8) {
-    cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<T>,
+    cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<T, kThreads>,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T>, p, C);
+  return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T, kThreads>, p, C);
+}
+
+// Threads per CTA: 1024 or 512 where the CTAs leave an SM that much room and a thread still
+// has eight values to read.
+template <typename T>
+cudaError_t launch(const SampleParams& p, int C, int sm_count, cudaStream_t st) {
+  const int64_t ctas = (int64_t)p.B * C, slice = p.V / C;
+  if (ctas <= sm_count && slice >= 8192) return launch<T, 1024>(p, C, st);
+  if (ctas <= 2ll * sm_count && slice >= 4096) return launch<T, 512>(p, C, st);
+  return launch<T, 256>(p, C, st);
 }
 
 }  // namespace
@@ -730,7 +779,8 @@ cudaError_t launch_tree_sample(const tv_sample_args* a, int sm_count, cudaStream
   p.new_tokens = a->new_tokens;
   p.status = a->status;
   const int C = sample_cluster(a->B, a->vocab, sm_count);
-  return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, C, st) : launch<float>(p, C, st);
+  return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, C, sm_count, st)
+                                 : launch<float>(p, C, sm_count, st);
 }
 
 }  // namespace tv
