@@ -18,10 +18,13 @@
 // stored.  A rejected token's own weight is zero from then on (u < 1).
 //
 // Passes.  A visited row is streamed once for its maximum and a float sum of exponentials
-// relative to a running one.  That sum is within 1e-5 of the row's, and it decides every test
-// whose two sides differ by more; only a closer one (two in 10^5), the draw at the end of the
-// walk, and what follows a rejection under draft probabilities take the exact sums below, from
-// L2 by then.
+// relative to a running one; what else it takes (a residual's sum, the draw) reads it from L2.
+// Floats decide first: every sum carries a bound on its error (1e-5 of the row's sum), a test
+// whose two sides differ by more than the bounds is decided, and so is a draw that lands that
+// far inside a token.  Whatever is closer sends the node back to be done with the exact sums
+// below: two tests in 10^5, and as many draws as the distribution has mass near boundaries
+// (a few in 100 for a language model's, all of them for a flat one).  An exact weight costs
+// about eight times a float one.
 //
 // Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
 // that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
@@ -91,7 +94,7 @@ struct SampleParams {
 };
 
 // What the walk does next, decided by warp 0 of every CTA alike.
-enum : int { kAccept = 0, kExact = 1, kResidual = 2, kDraw = 3 };
+enum : int { kAccept = 0, kExact = 1, kResidual = 2, kDraw = 3, kStop = 4 };
 
 struct Shared {
   float2 exp2_table[kTable * kCopies];
@@ -101,11 +104,14 @@ struct Shared {
   uint64_t warp_key[kMaxWarps];   // of this CTA's slice, by warp
   float warp_approx[kMaxWarps];
   int64_t warp_sum[kMaxWarps];
+  float parts[2][kMaxCluster];    // exchanged slice sums, in floats
+  float warp_part[kMaxWarps];
   int32_t rejected[64];           // tokens refused at this node whose weights are in the sums
-  int64_t rejected_e[64];
-  int n_rejected, cmd, next, top;
+  int n_rejected, cmd, next;
+  int redo;                       // 1 + the node whose draw has to be done again
   float m, s_hi, s_lo;            // the row's maximum; S as a pair of floats
   int64_t target;                 // the draw's place in the sums, and the vectors it is in
+  float target_f, margin;
   int range0, range1;
 };
 
@@ -227,6 +233,10 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+__device__ __forceinline__ void st_cluster_u32(const void* local, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "r"(v)
+               : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "f"(v)
                : "memory");
@@ -245,7 +255,7 @@ struct Scale {
   const float2* table;
 };
 
-// The weights of vector j.
+// The weights of vector j: exact, in units, or as floats relative to the largest.
 template <typename T>
 __device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j, int64_t* e) {
   float v[Vec<T>::N];
@@ -257,37 +267,43 @@ __device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j
       e[i] = residual(e[i], __ldg(c.q + row.first(j) + i), c.s_hi, c.s_lo);
   }
 }
+template <typename T>
+__device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j, float* e) {
+  float v[Vec<T>::N];
+  row.load(j, v);
+  if (c.s_hi > 0.f) {
+    float g[Vec<T>::N];
+    const int64_t a = row.first(j);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i)
+      g[i] = a + i >= 0 && a + i < row.V ? __ldg(c.q + a + i) : 0.f;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i)
+      e[i] = fmaxf(fmaf(-g[i], c.s_hi, ex2((v[i] - c.m) * c.ch)), 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) e[i] = ex2((v[i] - c.m) * c.ch);
+  }
+}
 
-__device__ __forceinline__ int64_t warp_sum(int64_t s) {
+template <typename S>
+__device__ __forceinline__ S warp_sum(S s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
 // Sum of the weights of vectors [j0, j1), by one warp.
-template <typename T>
-__device__ __forceinline__ int64_t sum_range(const Row<T>& row, const Scale& c, int j0, int j1) {
-  int64_t s = 0;
-  if (c.s_hi > 0.f) {
-    for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
-      int64_t e[Vec<T>::N];
-      weights(row, c, j, e);
-#pragma unroll
-      for (int i = 0; i < Vec<T>::N; ++i) s += e[i];
-    }
-    return warp_sum(s);
-  }
+template <typename S, typename T>
+__device__ __forceinline__ S sum_range(const Row<T>& row, const Scale& c, int j0, int j1) {
+  S s = 0;
+#pragma unroll 2
   for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += 32) {
-    float v[Vec<T>::N];
-    row.load(j, v);
-    int high = 0, low = 0;  // eight of at most 2^22 each
+    S e[Vec<T>::N], part = 0;
+    weights(row, c, j, e);
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) {
-      const Weight w = weight(v[i], c.m, c.ch, c.cl, c.table);
-      high += w.high;
-      low += w.low;
-    }
-    s += units({high, low});
+    for (int i = 0; i < Vec<T>::N; ++i) part += e[i];
+    s += part;
   }
   return warp_sum(s);
 }
@@ -305,12 +321,13 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
 }
 // Where `target` lies among one part per lane: the lane, and what is left of the target there.
 // The last lane below `parts` takes what rounding might leave over.
-__device__ __forceinline__ int locate(int64_t part, int parts, int64_t* target) {
+template <typename S>
+__device__ __forceinline__ int locate(S part, int parts, S* target) {
   const int lane = threadIdx.x & 31;
-  int64_t up_to = lane < parts ? part : 0;
+  S up_to = lane < parts ? part : (S)0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
+    const S below = __shfl_up_sync(0xffffffffu, up_to, o);
     if (lane >= o) up_to += below;
   }
   const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && up_to > *target);
@@ -318,9 +335,83 @@ __device__ __forceinline__ int locate(int64_t part, int parts, int64_t* target) 
   *target -= __shfl_sync(0xffffffffu, up_to - part, at);
   return at;
 }
+__device__ __forceinline__ int64_t& target_of(Shared& sh, int64_t) { return sh.target; }
+__device__ __forceinline__ float& target_of(Shared& sh, float) { return sh.target_f; }
+__device__ __forceinline__ int64_t* warp_sums(Shared& sh, int64_t) { return sh.warp_sum; }
+__device__ __forceinline__ float* warp_sums(Shared& sh, float) { return sh.warp_part; }
+
+// The owner's part of a draw, by the whole CTA: the token at place target_of(sh) of vectors
+// range0 .. range1-1, found through the warps' shares of them, the vector and the element.
+// Returns it in warp 0's lane that found it (others -1); -2 where a float draw lands within
+// `margin` of a token's edge.
+template <typename S, int kWarps, typename T>
+__device__ __forceinline__ int draw(Shared& sh, const Row<T>& row, const Scale& sc) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_out = sh.n_rejected;
+  int y0 = sh.range0, y1 = sh.range1;
+  S t = target_of(sh, (S)0);
+  // the weights of one vector, without the tokens refused
+  auto load = [&](int j, S* e) {
+    S s = 0;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) e[i] = 0;
+    if (j < y1) weights(row, sc, j, e);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) {
+      for (int r = 0; r < n_out; ++r)
+        if (row.first(j) + i == sh.rejected[r]) e[i] = 0;
+      s += e[i];
+    }
+    return s;
+  };
+  if (y1 - y0 > 128) {  // long enough for all warps to share
+    const int per = (y1 - y0 + kWarps - 1) / kWarps;
+    const int x0 = min(y1, y0 + warp * per), x1 = min(y1, x0 + per);
+    S part = 0;
+    for (int j = x0 + lane; j < x1; j += 32) {
+      S e[Vec<T>::N];
+      part += load(j, e);
+    }
+    part = warp_sum(part);
+    if (lane == 0) warp_sums(sh, (S)0)[warp] = part;
+    __syncthreads();
+    if (warp != 0) return -1;
+    const int w = locate(lane < kWarps ? warp_sums(sh, (S)0)[lane] : (S)0, kWarps, &t);
+    y0 = min(y1, y0 + w * per);
+    y1 = min(y1, y0 + per);
+  }
+  if (warp != 0) return -1;
+  for (int j = y0; j < y1; j += 32) {
+    S e[Vec<T>::N];
+    const S s = load(j + lane, e);
+    const S all = warp_sum(s);
+    if (t >= all && j + 32 < y1) {
+      t -= all;
+      continue;
+    }
+    const int at = locate(s, 32, &t);
+    if (lane != at) return -1;
+    int k = 0;
+    S width = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) {
+      if (!found && t < e[i]) {
+        found = true;
+        width = e[i];
+        k = i;
+      }
+      if (!found) t -= e[i];
+    }
+    const float edge = fminf((float)t, (float)(width - t));
+    if (sizeof(S) == 4 && !(found && edge > sh.margin)) return -2;
+    return (int)row.first(j + at) + k;
+  }
+  return sizeof(S) == 4 && lane == 0 ? -2 : -1;
+}
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, int C) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
+    tree_sample_kernel(SampleParams p, int C) {
   constexpr int kWarps = kThreads / 32;
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -351,6 +442,7 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
   const float T0 = p.temperature ? p.temperature[b] : 1.f;
   for (int i = tid; i < kTable * kCopies; i += kThreads)
     sh.exp2_table[i] = make_float2(d_exp.hi[i / kCopies], d_exp.lo[i / kCopies]);
+  if (tid == 0) sh.redo = 0;  // (before the first cluster barrier: other CTAs set it)
   const bool ok_temp = T0 >= 0.f;  // a NaN is not
   if (__syncthreads_or(!ok_tree) || !ok_temp) {  // the whole cluster alike
     if (rank == 0 && tid == 0) {
@@ -474,77 +566,180 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
+    const uint64_t slice_key = lane < C ? sh.keys[phase][lane] : 0ull;
+    key = warp_max(slice_key);
+    const float m = unordered((uint32_t)(key >> 32));
+    Scale sc{m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
     int64_t child_e[2] = {0, 0};
-    if (warp == 0) {
-      const uint64_t mine = lane < C ? sh.keys[phase][lane] : 0ull;
-      key = warp_max(mine);
-      const float m = unordered((uint32_t)(key >> 32));
-      const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
-      int next = -1, cmd = kExact;
-      if (key == 0 || key == ~0ull || m == INFINITY) {  // nothing to draw from
-        cmd = kDraw;
-        next = -2;
-      } else if (greedy) {
-        const uint32_t h0 = __ballot_sync(0xffffffffu, ((uint32_t)children >> lane & 1) && tok[0] == top);
+    if (key == 0 || key == ~0ull || m == INFINITY || greedy) {
+      if (warp == 0) {
+        const int top = (int)(0xFFFFFFFFu - (uint32_t)key);
+        const bool none = key == 0 || key == ~0ull || m == INFINITY;  // nothing to draw from
+        const uint32_t h0 =
+            __ballot_sync(0xffffffffu, ((uint32_t)children >> lane & 1) && tok[0] == top);
         const uint32_t h1 =
             __ballot_sync(0xffffffffu, ((uint32_t)(children >> 32) >> lane & 1) && tok[1] == top);
-        next = h0 ? __ffs(h0) - 1 : h1 ? 31 + __ffs(h1) : -1;
-        cmd = next >= 0 ? kAccept : kDraw;
-      } else {
-        float Z = mine ? sh.approx[phase][lane] * ex2((unordered((uint32_t)(mine >> 32)) - m) * ch)
-                       : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          child_e[s] = units(weight(child[s], m, ch, cl, sh.exp2_table));
-        // by the float sum, as far as it decides: up to an accepted child, without a draft
-        // probability refused before it
-        float W = Z;
-        const float ew[2] = {(float)child_e[0] * (1.f / kUnit), (float)child_e[1] * (1.f / kUnit)};
-        uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
-        while (left) {
-          const int i = __ffsll((long long)left) - 1;
-          left &= left - 1;
-          const int x = pick(tok, i);
-          const uint64_t same =
-              (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
-              (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
-          const float g = p.draft ? pick(child_q, i) : 1.f;
-          const float w = same & refused ? 0.f : pick(ew, i);
-          const float over = pick(uni, i) * g * W - w, error = 1e-5f * g * Z;
-          if (over < -error) {
-            next = i;
-            cmd = kAccept;
-            break;
-          }
-          if (p.draft || (over < error && w > 0.f)) break;
-          W -= w;
-          refused |= 1ull << i;
+        const int next = none ? -1 : h0 ? __ffs(h0) - 1 : h1 ? 31 + __ffs(h1) : -1;
+        if (lane == 0) {
+          if (rank == 0 && none) report(p.status, TV_ERR_INVALID_ARG);
+          else if (rank == 0 && next < 0) emit[count] = top;
+          sh.next = next;
+          sh.cmd = next < 0 ? kStop : kAccept;
         }
       }
-      if (lane == 0) {
-        sh.cmd = cmd;
-        sh.next = next;
-        sh.m = m;
-        sh.top = top;
-        sh.n_rejected = 0;
+      __syncthreads();
+      phase ^= 1;
+    } else {
+      // ---- by floats, with bounds on their errors ----
+      float part = slice_key ? sh.approx[phase][lane] *
+                                   ex2((unordered((uint32_t)(slice_key >> 32)) - m) * ch)
+                             : 0.f;  // lane r: slice r's sum
+      phase ^= 1;
+      const float Z = warp_sum(part);
+      float W = Z, dW = 1e-5f * Z, S = 0.f, dS = 0.f, G = 1.f;
+      uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
+      float ew[2] = {0.f, 0.f};
+      if (warp == 0) {
+        if (p.draft && !has_q && children && rank == 0 && lane == 0)
+          report(p.status, TV_ERR_BOUNDS);  // no drafter's row for this depth: no test
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          child_e[s] = units(weight(child[s], m, ch, cl, sh.exp2_table));
+          ew[s] = (float)child_e[s] * (1.f / kUnit);
+        }
+      }
+      for (;;) {
+        if (warp == 0) {
+          int cmd = kDraw, next = -1, n = 0;
+          if (!(W > 16.f * dW)) cmd = kExact;
+          while (cmd == kDraw && left) {
+            const int i = __ffsll((long long)left) - 1;
+            left &= left - 1;
+            const int x = pick(tok, i);
+            const uint64_t same =
+                (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
+                (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+            const bool again = same & refused;  // a token refused before has no weight left
+            const float u = pick(uni, i), e = pick(ew, i);
+            const float g = !p.draft ? 1.f : again ? 0.f : pick(child_q, i);
+            const float w = again ? 0.f : p.draft ? fmaxf(fmaf(-g, S, e), 0.f) : e;
+            const float over = u * g * W - w * G;
+            const float error = u * g * dW + G * (1e-6f * e + g * (dS + 1e-6f * S));
+            if (over < -error) {
+              cmd = kAccept;
+              next = i;
+              break;
+            }
+            if (over < error && !again && e > 0.f) {
+              cmd = kExact;
+              break;
+            }
+            if (!p.draft) {
+              refused |= 1ull << i;
+              W -= w;
+              if (!again) {
+                const int j = row.vector_of(x);
+                if (j / per == lane) part -= w;
+                if (lane == 0) sh.rejected[n] = x;
+                ++n;
+              }
+              continue;
+            }
+            refused |= 1ull << i;
+            S += W / G;
+            dS += (dW + 1e-6f * W) / G;
+            G -= g;
+            cmd = G > 1e-3f ? kResidual : kExact;
+          }
+          if (cmd == kDraw) {
+            // which slice, and where in it; then (of use to that slice's CTA) which warp
+            if (!(W > 16.f * dW)) cmd = kExact;
+            float t = uni[0] * W;
+            t = __shfl_sync(0xffffffffu, t, 0);
+            const int owner = locate(part, C, &t);
+            float mine = 0.f;
+            if (lane < kWarps) {
+              mine = sh.warp_part[lane];
+              if (S == 0.f) {
+                const uint64_t k = sh.warp_key[lane];
+                mine = k ? sh.warp_approx[lane] * ex2((unordered((uint32_t)(k >> 32)) - m) * ch)
+                         : 0.f;
+              }
+            }
+            __syncwarp();
+            for (int r = 0; r < n; ++r) {
+              const int x = sh.rejected[r], j = row.vector_of(x) - c0;
+              const uint64_t same =
+                  (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
+                  (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+              const float w = pick(ew, __ffsll((long long)(same & refused)) - 1);
+              if (j >= 0 && j < c1 - c0 && j / per_w == lane) mine -= w;
+            }
+            const int w = locate(mine, kWarps, &t);
+            next = owner;
+            if (lane == 0) {
+              sh.target_f = t;
+              sh.margin = 4.f * dW;
+              sh.range0 = min(c1, c0 + w * per_w);
+              sh.range1 = min(c1, sh.range0 + per_w);
+            }
+          }
+          if (lane == 0) {
+            sh.s_hi = S;
+            sh.n_rejected = n;
+            sh.cmd = cmd;
+            sh.next = next;
+          }
+        }
+        __syncthreads();
+        if (sh.cmd != kResidual) break;
+        sc.s_hi = sh.s_hi;
+        const float ws = sum_range<float>(row, sc, w0, w1);
+        if (lane == 0) sh.warp_part[warp] = ws;
+        __syncthreads();
+        if (warp == 0) {
+          const float t = warp_sum(lane < kWarps ? sh.warp_part[lane] : 0.f);
+          if (C == 1) {
+            if (lane == 0) sh.parts[phase][0] = t;
+          } else if (lane < C) {
+            st_cluster_f32(&sh.parts[phase][rank], (uint32_t)lane, t);
+          }
+        }
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        if (warp == 0) {
+          part = lane < C ? sh.parts[phase][lane] : 0.f;
+          W = warp_sum(part);
+          dW = 1e-5f * (Z + S) + dS;
+        }
+        phase ^= 1;
+      }
+      if (sh.cmd == kDraw) {
+        if (sh.next == rank) {
+          const int token = draw<float, kWarps>(sh, row, sc);
+          if (token >= 0) emit[count] = token;
+          if (token == -2)  // tell every CTA of the cluster
+            for (int r = 0; r < C; ++r) {
+              if (C > 1) st_cluster_u32(&sh.redo, (uint32_t)r, (uint32_t)node + 1);
+              else sh.redo = node + 1;
+            }
+        }
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        if (tid == 0) sh.cmd = sh.redo == node + 1 ? kExact : kStop;
+        __syncthreads();
       }
     }
-    __syncthreads();
-    phase ^= 1;
     if (sh.cmd == kExact) {
       // ---- exact sums of the weights, the tests by them, and residuals after rejections ----
-      Scale sc{sh.m, ch, cl, q, 0.f, 0.f, sh.exp2_table};
+      sc.s_hi = 0.f;
       // warp 0's: S and G, the children left, the tokens refused, the child whose rejection
       // the residual that is being summed belongs to
       double S = 0.0, G = 1.0;
       uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
       int refusing = -1;
-      if (warp == 0 && p.draft && !has_q && children && rank == 0 && lane == 0)
-        report(p.status, TV_ERR_BOUNDS);  // no drafter's row for this depth: no test
       for (;;) {
-        const int64_t ws = sum_range(row, sc, w0, w1);
+        const int64_t ws = sum_range<int64_t>(row, sc, w0, w1);
         if (lane == 0) sh.warp_sum[warp] = ws;
         __syncthreads();
         if (warp == 0) {
@@ -558,7 +753,8 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
         if (C > 1) cluster_sync();
         else __syncthreads();
         if (warp == 0) {
-          int64_t W = warp_sum(lane < C ? sh.sums[phase][lane] : 0);
+          int64_t part = lane < C ? sh.sums[phase][lane] : 0;
+          int64_t W = warp_sum(part);
           int cmd = kDraw, next = -1, n = 0;
           if (refusing >= 0 && W == 0) {
             // the drafter covers all that p has left: the two are equal but for rounding
@@ -586,11 +782,11 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
             refused |= 1ull << i;
             if (!p.draft) {
               W -= w;
-              if (!again && lane == 0) {
-                sh.rejected[n] = x;
-                sh.rejected_e[n] = w;
+              if (!again) {
+                if (row.vector_of(x) / per == lane) part -= w;
+                if (lane == 0) sh.rejected[n] = x;
+                ++n;
               }
-              n += !again;
               continue;
             }
             cmd = kResidual;
@@ -598,8 +794,28 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
             S += (double)W * (1.0 / (double)kUnit) / G;
             G -= g;
           }
+          if (cmd == kDraw) {
+            int64_t t = min((int64_t)((double)uni[0] * (double)W), W - 1);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            next = locate(part, C, &t);
+            int64_t mine = lane < kWarps ? sh.warp_sum[lane] : 0;
+            __syncwarp();
+            for (int r = 0; r < n; ++r) {
+              const int x = sh.rejected[r], j = row.vector_of(x) - c0;
+              const uint64_t same =
+                  (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
+                  (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+              const int64_t w = pick(child_e, __ffsll((long long)(same & refused)) - 1);
+              if (j >= 0 && j < c1 - c0 && j / per_w == lane) mine -= w;
+            }
+            const int w = locate(mine, kWarps, &t);
+            if (lane == 0) {
+              sh.target = t;
+              sh.range0 = min(c1, c0 + w * per_w);
+              sh.range1 = min(c1, sh.range0 + per_w);
+            }
+          }
           if (lane == 0) {
-            if (cmd == kDraw) sh.target = min((int64_t)((double)uni[0] * (double)W), W - 1);
             sh.s_hi = (float)S;
             sh.s_lo = (float)(S - (double)(float)S);
             sh.n_rejected = n;
@@ -614,96 +830,15 @@ __global__ void __launch_bounds__(kThreads) tree_sample_kernel(SampleParams p, i
         phase ^= 1;
       }
       if (sh.cmd == kDraw) {
-        // ---- the draw: the slice, the warp's part, an eighth of it, the vector, the token --
-        const int n_out = sh.n_rejected;  // weights that are in the sums still
-        if (warp == 0) {
-          int64_t t = sh.target;
-          int64_t part = lane < C ? sh.sums[phase][lane] : 0;
-          for (int r = 0; r < n_out; ++r)
-            if (row.vector_of(sh.rejected[r]) / per == lane) part -= sh.rejected_e[r];
-          const int owner = locate(part, C, &t);
-          part = lane < kWarps ? sh.warp_sum[lane] : 0;
-          for (int r = 0; r < n_out; ++r) {
-            const int j = row.vector_of(sh.rejected[r]) - c0;
-            if (j >= 0 && j < c1 - c0 && j / per_w == lane) part -= sh.rejected_e[r];
-          }
-          const int w = locate(part, kWarps, &t);  // (counts in the owner only)
-          if (lane == 0) {
-            sh.next = owner;
-            sh.target = t;
-            sh.range0 = min(c1, c0 + w * per_w);
-            sh.range1 = min(c1, sh.range0 + per_w);
-          }
-        }
-        __syncthreads();
         if (sh.next == rank) {
-          int y0 = sh.range0, y1 = sh.range1;
-          if (y1 - y0 > 128) {  // long enough for all warps to share
-            const int per_r = (y1 - y0 + kWarps - 1) / kWarps;
-            const int x0 = min(y1, y0 + warp * per_r), x1 = min(y1, x0 + per_r);
-            int64_t part = sum_range(row, sc, x0, x1);
-            for (int r = 0; r < n_out; ++r) {
-              const int j = row.vector_of(sh.rejected[r]);
-              if (j >= x0 && j < x1) part -= sh.rejected_e[r];
-            }
-            if (lane == 0) sh.warp_sum[warp] = part;
-            __syncthreads();
-            if (warp == 0) {
-              int64_t t = sh.target;
-              const int w = locate(lane < kWarps ? sh.warp_sum[lane] : 0, kWarps, &t);
-              __syncwarp();
-              if (lane == 0) sh.target = t;
-              y0 = min(y1, y0 + w * per_r);
-              y1 = min(y1, y0 + per_r);
-              __syncwarp();
-            }
-          }
-          if (warp == 0) {
-            int64_t t = sh.target;
-            for (int j = y0; j < y1; j += 32) {
-              int64_t e[Vec<T>::N], s = 0;
-#pragma unroll
-              for (int i = 0; i < Vec<T>::N; ++i) e[i] = 0;
-              if (j + lane < y1) weights(row, sc, j + lane, e);
-#pragma unroll
-              for (int i = 0; i < Vec<T>::N; ++i) {
-                for (int r = 0; r < n_out; ++r)
-                  if (row.first(j + lane) + i == sh.rejected[r]) e[i] = 0;
-                s += e[i];
-              }
-              const int64_t all = warp_sum(s);
-              if (t >= all && j + 32 < y1) {
-                t -= all;
-                continue;
-              }
-              const int at = locate(s, 32, &t);
-              if (lane == at) {
-                int k = 0;
-                bool found = false;
-#pragma unroll
-                for (int i = 0; i < Vec<T>::N; ++i) {
-                  found = found || t < e[i];
-                  if (!found) {
-                    t -= e[i];
-                    ++k;
-                  }
-                }
-                emit[count] = (int32_t)(row.first(j + lane) + k);
-              }
-              break;
-            }
-          }
+          const int token = draw<int64_t, kWarps>(sh, row, sc);
+          if (token >= 0) emit[count] = token;
         }
         break;
       }
       phase ^= 1;
-    } else if (sh.cmd == kDraw) {  // greedy, or a row without a distribution
-      if (rank == 0 && tid == 0) {
-        if (sh.next == -2) report(p.status, TV_ERR_INVALID_ARG);
-        else emit[count] = sh.top;
-      }
-      break;
     }
+    if (sh.cmd == kStop) break;
     node = sh.next;
     ++count;
     if (warp == 0 && rank == 0) {
