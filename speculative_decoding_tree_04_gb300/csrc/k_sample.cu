@@ -51,7 +51,6 @@ using namespace ptx;
 
 constexpr int kMaxWarps = 32;
 constexpr int kMaxCluster = 16;
-constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
 constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
 constexpr int kTable = 64;
 constexpr int kCopies = 16;     // of the table, one for each lane of a half warp: no conflicts
@@ -175,7 +174,8 @@ template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int N = 4;
+  static constexpr int N = 4, kUnroll = 8;  // elements per 16 bytes, loads in flight
+  static constexpr uint32_t kMasked = 0xFF800000u;  // a word of -inf
   __device__ static void unpack(const uint4& w, float* x) {
     x[0] = __uint_as_float(w.x);
     x[1] = __uint_as_float(w.y);
@@ -186,7 +186,8 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8;
+  static constexpr int N = 8, kUnroll = 4;
+  static constexpr uint32_t kMasked = 0xFF80FF80u;
   __device__ static void unpack(const uint4& w, float* x) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -213,6 +214,12 @@ struct Row {
   __device__ int vector_of(int64_t v) const { return (int)((v + off) / Vec<T>::N); }
   __device__ int64_t first(int j) const { return (int64_t)j * Vec<T>::N - off; }
   __device__ bool whole(int j) const { return first(j) >= 0 && first(j) + Vec<T>::N <= V; }
+  // The vectors that lie in the row whole, [first_whole, end_whole).
+  __device__ int first_whole() const { return off > 0 ? 1 : 0; }
+  __device__ int end_whole() const { return (int)((V + off) / Vec<T>::N); }
+  __device__ uint4 raw(int j) const {  // of those
+    return __ldg(reinterpret_cast<const uint4*>(x + first(j)));
+  }
   __device__ void load(int j, float* v) const {
     const int64_t a = first(j);
     if (whole(j)) {
@@ -274,9 +281,20 @@ __device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j
   if (c.s_hi > 0.f) {
     float g[Vec<T>::N];
     const int64_t a = row.first(j);
+    if (row.whole(j) && ((uintptr_t)(c.q + a) & 15u) == 0) {
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i)
-      g[i] = a + i >= 0 && a + i < row.V ? __ldg(c.q + a + i) : 0.f;
+      for (int i = 0; i < Vec<T>::N; i += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(c.q + a + i));
+        g[i] = f.x;
+        g[i + 1] = f.y;
+        g[i + 2] = f.z;
+        g[i + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < Vec<T>::N; ++i)
+        g[i] = a + i >= 0 && a + i < row.V ? __ldg(c.q + a + i) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i)
       e[i] = fmaxf(fmaf(-g[i], c.s_hi, ex2((v[i] - c.m) * c.ch)), 0.f);
@@ -472,7 +490,74 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
       has_q = r < p.draft_rows;
       q = p.draft + ((int64_t)b * p.draft_rows + min(r, p.draft_rows - 1)) * p.draft_stride;
     }
-    // warp 0: the children, and their logits while the row streams in
+    // ---- the row's maximum, and the float sum or (greedy) the maximum's first index ----
+    // (a NaN ends up in the sum)
+    constexpr int N = Vec<T>::N, kUnroll = Vec<T>::kUnroll;
+    float best = -INFINITY, sum = 0.f;
+    int best_at = 0;
+    // the row's ends, where they are no whole vector: one value a lane
+    auto end_value = [&](int j) {
+      if (j < w0 || j >= w1) return;
+      const int64_t a = row.first(j) + lane;
+      const float v = lane < N && a >= 0 && a < p.V ? Vec<T>::one(row.x + a) : -INFINITY;
+      if (v != v) sum = v;
+      if (v > best) {
+        sum = (greedy ? sum : sum * ex2((best - v) * ch)) + 1.f;
+        best = v;
+        best_at = (int)a;
+      } else if (best > -INFINITY) {
+        sum += ex2((v - best) * ch);
+      }
+    };
+    const int e0 = row.first_whole(), e1 = row.end_whole();
+    if (e0 > 0) end_value(0);
+    const int v0 = max(w0, e0), v1 = min(w1, e1);
+    for (int j0 = v0; j0 < v1; j0 += 32 * kUnroll) {
+      const int j = j0 + lane;
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        w[k] = make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+        if (j + 32 * k < v1) w[k] = row.raw(j + 32 * k);
+      }
+      float m = best;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (j0 + 32 * k >= v1) break;  // no lane of the warp has one
+        float v[N];
+        Vec<T>::unpack(w[k], v);
+        if (!greedy) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) m = fmax3(m, v[i], v[i + 1]);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (v[i] != v[i]) sum = v[i];
+          if (v[i] > best) {
+            best = v[i];
+            best_at = (int)row.first(j + 32 * k) + i;
+          }
+        }
+      }
+      if (greedy) continue;
+      if (m > best) {
+        sum *= ex2((best - m) * ch);  // (from -inf: 0)
+        best = m;
+      }
+      const float at = best > -INFINITY ? best : 0.f;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (j0 + 32 * k >= v1) break;
+        float v[N], part = 0.f;
+        Vec<T>::unpack(w[k], v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) part += ex2((v[i] - at) * ch);
+        sum += part;
+      }
+    }
+    if (e1 < row.n_vec && e1 >= e0) end_value(e1);
+    // warp 0: the children and their logits, which the row has brought to L2
     uint64_t children = 0;
     float child[2] = {-INFINITY, -INFINITY}, child_q[2] = {0.f, 0.f};
     if (warp == 0) {
@@ -486,61 +571,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
         }
       }
     }
-    // ---- the row's maximum (among equal values its first index) and the float sum ----
-    float best = -INFINITY, sum = 0.f;
-    int best_at = 0;
-    uint32_t nan_bits = 0;
-    for (int j = w0 + lane; j < w1; j += 32 * kUnroll) {
-      float v[kUnroll][Vec<T>::N];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        if (j + 32 * k < w1) {
-          row.load(j + 32 * k, v[k]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < Vec<T>::N; ++i) v[k][i] = -INFINITY;
-        }
-      }
-      float m = v[0][0];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) {
-          nan_bits = max(nan_bits, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
-          m = fmaxf(m, v[k][i]);
-        }
-      if (m > best) {
-        sum *= ex2((best - m) * ch);  // (from -inf: 0)
-        best = m;
-        best_at = -1;
-#pragma unroll
-        for (int k = kUnroll - 1; k >= 0; --k)
-#pragma unroll
-          for (int i = Vec<T>::N - 1; i >= 0; --i)
-            if (v[k][i] == m) best_at = (int)row.first(j + 32 * k) + i;
-      }
-      if (best > -INFINITY) {
-        float part = 0.f;
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-          float four = 0.f;
-#pragma unroll
-          for (int i = 0; i < Vec<T>::N; ++i) four += ex2((v[k][i] - best) * ch);
-          part += four;
-        }
-        sum += part;
-      }
-    }
     // order-preserving value bits, then the complemented index: the largest key is the
     // largest value's first place; a NaN anywhere beats every value
     uint64_t key = best > -INFINITY ? ((uint64_t)ordered(best) << 32) |
                                           (uint32_t)(0xFFFFFFFFu - (uint32_t)best_at)
                                     : 0ull;
+    const bool is_nan = sum != sum && best < INFINITY;
     key = warp_max(key);
     sum = key ? sum * ex2((best - unordered((uint32_t)(key >> 32))) * ch) : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (__any_sync(0xffffffffu, nan_bits > 0x7F800000u)) key = ~0ull;
+    if (__any_sync(0xffffffffu, is_nan)) key = ~0ull;
     if (lane == 0) {
       sh.warp_key[warp] = key;
       sh.warp_approx[warp] = sum;
