@@ -474,67 +474,68 @@ def verify_prologue(parent, prefix_len, q_pe_in, q_pe_out, kpe_tree, ckv_tree, c
 
 
 def _on_device(*ts):
-    """Check that every tensor given lives on one CUDA device, and return that device."""
+    """Check that every tensor given lives on one CUDA device, and return its index."""
     dev = None
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("libtv takes CUDA tensors only")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("libtv takes CUDA tensors only")
+                if dev is not None:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d}")
+                dev = d
     return dev
 
 
-class _launch:
-    """The stream to launch on (default: the tensors' device's current one), with that
-    device current meanwhile.  A stream of another device is refused."""
-
-    def __init__(self, dev, stream):
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"tensors on {dev}, stream on {stream.device}")
-        self.stream = stream
-        self.handle = ctypes.c_void_p(stream.cuda_stream)
-        self.other = dev.index if dev.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.other is not None:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.other)
-        return self
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            torch.cuda.set_device(self.back)
+def _raw_stream(dev, stream):
+    """Handle of the stream to launch on (default: the tensors' device's current one)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"tensors on cuda:{dev}, stream on {stream.device}")
+    return stream.cuda_stream
 
 
-def _scratch(kind, dev, stream, need):
-    """Workspace of `need` bytes for one call on `stream`: one buffer per device, stream
+def _call(dev, name, *args):
+    """One library call with the tensors' device current; raises on a failure."""
+    fn = getattr(_lib or load(), name)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != TV_OK:
+        _check(rc, name)
+
+
+def _scratch(kind, dev, handle, need):
+    """Workspace of `need` bytes for one call on the stream: one buffer per device, stream
     and kind of call, grown when needed.  During a capture the buffer is the graph's own:
     graphs that share one could replay at the same time, and it must outlive them."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    key = (kind, dev, stream.cuda_stream)
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+    key = (kind, dev, handle)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws.record_stream(stream)  # a smaller one that it replaces may still be in use there
+        ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+        # a smaller one that it replaces may still be in use on that stream
+        ws.record_stream(torch.cuda.ExternalStream(handle, device=f"cuda:{dev}"))
         _ws_cache[key] = ws
     return ws
 
 
 def _i32(name, t, shape):
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 of shape {tuple(shape)}")
 
 
 def _status_arg(status):
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+    if status is None:
+        return None
+    if status.dtype is not torch.int32 or status.numel() < 1:
         raise ValueError("status must be an int32 tensor")
+    return status.data_ptr()
 
 
 def tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
@@ -556,34 +557,25 @@ def tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
                            ("new_tokens", new_tokens, (B, Q))):
         _i32(name, t, shape)
     for name, t, shape in (("uniforms", uniforms, (B, Q)), ("temperature", temperature, (B,))):
-        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
-                              tuple(t.shape) != shape):
+        if t is not None and (t.shape != shape or t.dtype is not torch.float32 or
+                              not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous float32 of shape {shape}")
-    _status_arg(status)
-    a = SampleArgs()
-    a.struct_size = ctypes.sizeof(SampleArgs)
-    a.B, a.Q, a.vocab = B, Q, V
-    a.logits, a.logits_dt = logits.data_ptr(), _dt(logits)
-    a.logits_row_stride = logits.stride(1) if Q > 1 or B > 1 else V
-    a.temperature = None if temperature is None else temperature.data_ptr()
-    a.parent, a.tokens = parent.data_ptr(), tokens.data_ptr()
-    a.uniforms = uniforms.data_ptr()
+    probs, p_stride, p_rows = None, 0, 0
     if draft_probs is not None:
         d = draft_probs
-        if d.dtype != torch.float32 or d.dim() != 3 or d.shape[0] != B or d.shape[2] != V:
+        if d.dtype is not torch.float32 or d.dim() != 3 or d.shape[0] != B or d.shape[2] != V:
             raise ValueError("draft_probs must be float32 [B, rows, V]")
-        R = d.shape[1]
-        if B and (d.stride(2) != 1 or (B > 1 and d.stride(0) != R * d.stride(1))):
+        p_rows = d.shape[1]
+        if B and (d.stride(2) != 1 or (B > 1 and d.stride(0) != p_rows * d.stride(1))):
             raise ValueError("draft_probs rows must be contiguous and uniformly strided")
-        a.draft_probs = d.data_ptr()
-        a.draft_row_stride = d.stride(1) if R > 1 or B > 1 else V
-        a.draft_rows, a.draft_mode = R, int(draft_mode)
-    a.accept_len, a.path = accept_len.data_ptr(), path.data_ptr()
-    a.new_tokens = new_tokens.data_ptr()
-    a.status = None if status is None else status.data_ptr()
-    with _launch(dev, stream) as st:
-        rc = load().tv_tree_sample(ctypes.byref(a), st.handle)
-    _check(rc, "tv_tree_sample")
+        probs, p_stride = d.data_ptr(), d.stride(1) if p_rows > 1 or B > 1 else V
+    a = SampleArgs(ctypes.sizeof(SampleArgs), B, Q, V, logits.data_ptr(), _dt(logits),
+                   logits.stride(1) if Q > 1 or B > 1 else V,
+                   None if temperature is None else temperature.data_ptr(),
+                   parent.data_ptr(), tokens.data_ptr(), uniforms.data_ptr(), probs, p_stride,
+                   p_rows, int(draft_mode), accept_len.data_ptr(), path.data_ptr(),
+                   new_tokens.data_ptr(), _status_arg(status))
+    _call(dev, "tv_tree_sample", ctypes.byref(a), _raw_stream(dev, stream))
 
 
 def make_page_pool(refcount, page_table, n_pages, page_size) -> PagePool:
@@ -596,7 +588,7 @@ def make_page_pool(refcount, page_table, n_pages, page_size) -> PagePool:
     _i32("n_pages", n_pages, (rows,))
     p = PagePool(page_table.data_ptr(), n_pages.data_ptr(), refcount.data_ptr(), rows, most,
                  refcount.numel(), int(page_size))
-    p.tensors, p.device = (refcount, page_table, n_pages), dev
+    p.tensors, p.device, p.row_shape = (refcount, page_table, n_pages), dev, (rows,)
     return p
 
 
@@ -606,20 +598,20 @@ def pages_workspace_size(pool: PagePool) -> int:
 
 def _pool_call(name, pool, per_row, others, status, stream, workspace=None, scratch=False):
     """Marshal one pool call: per-row int32 arguments, other device arguments, status."""
-    dev = _on_device(*(t for _, t in per_row), *others, status, workspace)
+    dev = _on_device(*per_row.values(), *others, status, workspace)
     if dev != pool.device:
-        raise ValueError(f"pool on {pool.device}, arguments on {dev}")
-    for what, t in per_row:
-        _i32(what, t, (pool.rows,))
-    _status_arg(status)
-    args = [_ptr(t) for _, t in per_row] + [_ptr(t) for t in others] + [_ptr(status)]
-    with _launch(dev, stream) as st:
-        if scratch:
-            if workspace is None:
-                workspace = _scratch("pages", dev, st.stream, pages_workspace_size(pool))
-            args += [_ptr(workspace), workspace.numel() * workspace.element_size()]
-        rc = getattr(load(), name)(ctypes.byref(pool), *args, st.handle)
-    _check(rc, name)
+        raise ValueError(f"pool on cuda:{pool.device}, arguments on cuda:{dev}")
+    for what, t in per_row.items():
+        _i32(what, t, pool.row_shape)
+    args = [t.data_ptr() for t in per_row.values()]
+    args += [t.data_ptr() for t in others]
+    args.append(_status_arg(status))
+    handle = _raw_stream(dev, stream)
+    if scratch:
+        if workspace is None:
+            workspace = _scratch("pages", dev, handle, pages_workspace_size(pool))
+        args += [workspace.data_ptr(), workspace.numel() * workspace.element_size()]
+    _call(dev, name, ctypes.byref(pool), *args, handle)
 
 
 def pages_reserve(pool: PagePool, length, new_length, copies, status=None, workspace=None,
@@ -627,19 +619,19 @@ def pages_reserve(pool: PagePool, length, new_length, copies, status=None, works
     """Give every row the pages of keys length .. new_length-1 for itself; copies [rows,3]
     int32 becomes the list pages_copy takes."""
     _i32("copies", copies, (pool.rows, 3))
-    _pool_call("tv_pages_reserve", pool, (("length", length), ("new_length", new_length)),
+    _pool_call("tv_pages_reserve", pool, {"length": length, "new_length": new_length},
                (copies,), status, stream, workspace, True)
 
 
 def pages_fork(pool: PagePool, fork_from, length, status=None, stream=None):
     """Row r shares the pages of the first length[r] keys of row fork_from[r] (-1: none)."""
-    _pool_call("tv_pages_fork", pool, (("fork_from", fork_from), ("length", length)), (),
-               status, stream)
+    _pool_call("tv_pages_fork", pool, {"fork_from": fork_from, "length": length}, (), status,
+               stream)
 
 
 def pages_release(pool: PagePool, keep, status=None, stream=None):
     """Row r keeps the pages of its first keep[r] keys (negative: left alone)."""
-    _pool_call("tv_pages_release", pool, (("keep", keep),), (), status, stream)
+    _pool_call("tv_pages_release", pool, {"keep": keep}, (), status, stream)
 
 
 def pages_compact(pool: PagePool, moves, n_moves, status=None, workspace=None, stream=None):
@@ -647,7 +639,7 @@ def pages_compact(pool: PagePool, moves, n_moves, status=None, workspace=None, s
     rows by pages_copy with moves [num_pages,3] and count=n_moves [1] (int32)."""
     _i32("moves", moves, (pool.num_pages, 3))
     _i32("n_moves", n_moves, (1,))
-    _pool_call("tv_pages_compact", pool, (), (moves, n_moves), status, stream, workspace, True)
+    _pool_call("tv_pages_compact", pool, {}, (moves, n_moves), status, stream, workspace, True)
 
 
 def pages_copy(c_kv, k_pe, page_size, copies, count=None, status=None, stream=None):
@@ -665,14 +657,11 @@ def pages_copy(c_kv, k_pe, page_size, copies, count=None, status=None, stream=No
     _i32("copies", copies, (n, 3))
     if count is not None:
         _i32("count", count, (1,))
-    _status_arg(status)
     layers, rows, DL = c3.shape
-    with _launch(dev, stream) as st:
-        rc = load().tv_pages_copy(_ptr(c_kv), _ptr(k_pe), _dt(c_kv), c3.stride(1), k3.stride(1),
-                                  DL, k3.shape[2], layers, c3.stride(0), k3.stride(0),
-                                  int(page_size), rows, _ptr(copies), _ptr(count), n,
-                                  _ptr(status), st.handle)
-    _check(rc, "tv_pages_copy")
+    _call(dev, "tv_pages_copy", c_kv.data_ptr(), k_pe.data_ptr(), _dt(c_kv), c3.stride(1),
+          k3.stride(1), DL, k3.shape[2], layers, c3.stride(0), k3.stride(0), int(page_size), rows,
+          copies.data_ptr(), None if count is None else count.data_ptr(), n, _status_arg(status),
+          _raw_stream(dev, stream))
 
 
 def prefill_args(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, max_q_len,
@@ -681,31 +670,27 @@ def prefill_args(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale
     T, H, DN = q_nope.shape
     B, DR, DL = prefix_len.shape[0], q_pe.shape[2], w_kv.shape[2]
     DV = w_kv.shape[1] - DN
+    dt = q_nope.dtype
     for name, t, shape in (("q_nope", q_nope, (T, H, DN)), ("q_pe", q_pe, (T, H, DR)),
                            ("w_kv", w_kv, (H, DN + DV, DL)), ("out", out, (T, H, DV))):
-        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != q_nope.dtype:
-            raise ValueError(f"{name} must be contiguous {q_nope.dtype} of shape {shape}")
+        if t.shape != shape or t.dtype is not dt or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dt} of shape {shape}")
     for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
-        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype != q_nope.dtype:
-            raise ValueError(f"{name} must be rows of {d} contiguous {q_nope.dtype}")
+        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
+            raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
     _i32("q_start", q_start, (B + 1,))
     _i32("prefix_len", prefix_len, (B,))
+    rows = min(c_kv.shape[0], k_pe.shape[0])
     if page_table is not None:
         _i32("page_table", page_table, (B, page_table.shape[1]))
-    _status_arg(status)
-    a = PrefillArgs()
-    a.struct_size = ctypes.sizeof(PrefillArgs)
-    a.B, a.H, a.T, a.d_latent, a.d_nope, a.d_rope, a.d_v = B, H, T, DL, DN, DR, DV
-    a.scale, a.dt = float(scale), _dt(q_nope)
-    a.q_nope, a.q_pe, a.w_kv = q_nope.data_ptr(), q_pe.data_ptr(), w_kv.data_ptr()
-    a.c_kv, a.k_pe = c_kv.data_ptr(), k_pe.data_ptr()
-    a.ckv_row_stride, a.kpe_row_stride = c_kv.stride(0), k_pe.stride(0)
-    a.cache = make_cache(page_table, page_size, kv_stride_b, min(c_kv.shape[0], k_pe.shape[0]))
-    a.q_start, a.prefix_len = q_start.data_ptr(), prefix_len.data_ptr()
-    a.max_q_len, a.max_kv_len, a.total_kv = int(max_q_len), int(max_kv_len), int(total_kv)
-    a.out = out.data_ptr()
-    a.status = None if status is None else status.data_ptr()
-    return a
+        cache = CacheLayout(page_table.data_ptr(), page_size, page_table.shape[1], 0, rows)
+    else:
+        cache = CacheLayout(None, page_size, 0, kv_stride_b, rows)
+    return PrefillArgs(ctypes.sizeof(PrefillArgs), B, H, T, DL, DN, DR, DV, float(scale),
+                       _dt(q_nope), q_nope.data_ptr(), q_pe.data_ptr(), w_kv.data_ptr(),
+                       c_kv.data_ptr(), k_pe.data_ptr(), c_kv.stride(0), k_pe.stride(0), cache,
+                       q_start.data_ptr(), prefix_len.data_ptr(), int(max_q_len),
+                       int(max_kv_len), int(total_kv), out.data_ptr(), _status_arg(status))
 
 
 def prefill_workspace_size(a: PrefillArgs) -> int:
@@ -723,9 +708,8 @@ def prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale
                      status, workspace)
     a = prefill_args(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, max_q_len,
                      max_kv_len, total_kv, page_table, page_size, kv_stride_b, status)
-    with _launch(dev, stream) as st:
-        if workspace is None:
-            workspace = _scratch("prefill", dev, st.stream, max(1, prefill_workspace_size(a)))
-        rc = load().tv_prefill_attn(ctypes.byref(a), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), st.handle)
-    _check(rc, "tv_prefill_attn")
+    handle = _raw_stream(dev, stream)
+    if workspace is None:
+        workspace = _scratch("prefill", dev, handle, max(1, prefill_workspace_size(a)))
+    _call(dev, "tv_prefill_attn", ctypes.byref(a), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), handle)
