@@ -8,9 +8,9 @@
 //
 // The table work is latency: a few dependent passes over 4 bytes per page (a pool of 62000
 // pages, one GPU's memory at 61 layers, is 250 KB).  One cluster of CTAs does it in one
-// launch, each CTA scanning its slice of the counts, with counts exchanged through
-// distributed shared memory and one warp per row for the tables.  The copies are the bytes:
-// 64 keys of 1152 bytes per page and layer.
+// launch, each CTA scanning its slice of the counts (a run of consecutive pages per thread,
+// whose free ones it keeps as bits), with sums exchanged through distributed shared memory.
+// The copies are the bytes: 64 keys of 1152 bytes per page and layer.
 #include <algorithm>
 #include <climits>
 
@@ -62,10 +62,26 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* part) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  int64_t s = 0;
+  return warp_sum(part[threadIdx.x & 31]);
+}
+static_assert(kWarps == 32, "one part per lane");
+
+// The same, with the sum of the threads before this one.
+__device__ __forceinline__ int64_t block_scan(int v, int64_t* part, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int up_to = v;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += part[w];
-  return s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int below = __shfl_up_sync(0xffffffffu, up_to, o);
+    if (lane >= o) up_to += below;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = up_to;
+  __syncthreads();
+  const int64_t mine = part[lane];
+  const int64_t before = warp_sum(lane < warp ? mine : 0);
+  *total = warp_sum(mine);
+  return before + up_to - v;
 }
 
 // This CTA's number into slot `rank` of every CTA; the sum of the slots below this rank and
@@ -87,28 +103,38 @@ __device__ __forceinline__ Offsets collect(const int64_t* slots) {
   return o;
 }
 
-// Ranks of the flagged elements of [p0, p1): f(p, rank) for each, ranks counted from
-// `base` in ascending order.  Ends early once the ranks pass `limit`.
-template <typename Flag, typename Fn>
-__device__ void ranked(int p0, int p1, int64_t base, int64_t limit, int64_t* part, Flag flag,
-                       Fn f) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int q = p0; q < p1 && base < limit; q += kThreads) {
-    const int p = q + (int)threadIdx.x;
-    const bool on = p < p1 && flag(p);
-    const uint32_t m = __ballot_sync(0xffffffffu, on);
-    __syncthreads();
-    if (lane == 0) part[warp] = __popc(m);
-    __syncthreads();
-    int64_t before = base, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      before += w < warp ? part[w] : 0;
-      all += part[w];
+// A thread's run of consecutive pages of this CTA's slice, with a bit for each flagged one
+// where the run has at most 64 pages (a pool of half a million); longer runs are read again.
+struct Run {
+  int p0, p1;
+  uint64_t bits;
+};
+__device__ __forceinline__ Run run_of(int num_pages) {
+  const int per = (num_pages + kCluster - 1) / kCluster;
+  const int s0 = min(num_pages, (int)cluster_rank() * per), s1 = min(num_pages, s0 + per);
+  const int each = (per + kThreads - 1) / kThreads;
+  const int p0 = min(s1, s0 + (int)threadIdx.x * each);
+  return {p0, min(s1, p0 + each), 0ull};
+}
+template <typename Flag>
+__device__ __forceinline__ int mark(Run& r, Flag flag) {
+  int n = 0;
+  r.bits = 0;
+#pragma unroll 4
+  for (int p = r.p0; p < r.p1; ++p)
+    if (flag(p)) {
+      ++n;
+      r.bits |= 1ull << ((p - r.p0) & 63);
     }
-    if (on) f(p, before + __popc(m & ((1u << lane) - 1)));
-    base += all;
-  }
+  return n;
+}
+// f(p, rank) for each flagged page of the run, ranks from `rank` on and below `limit`.
+template <typename Flag, typename Fn>
+__device__ __forceinline__ void emit(const Run& r, int64_t rank, int64_t limit, Flag flag, Fn f) {
+  const bool known = r.p1 - r.p0 <= 64;
+  if (known && r.bits == 0) return;
+  for (int p = r.p0; p < r.p1 && rank < limit; ++p)
+    if (known ? (r.bits >> (p - r.p0)) & 1 : flag(p)) f(p, rank++);
 }
 
 // ---- reserve --------------------------------------------------------------------------
@@ -137,145 +163,123 @@ __device__ __forceinline__ RowNeed row_need(const tv_page_pool& P, int r,
   return w;
 }
 
-// Whether page index k of row r gets a fresh page.  `old`: the page it holds, or -1.
-__device__ __forceinline__ bool takes(const tv_page_pool& P, const Workspace& W, const RowNeed& w,
-                                      int r, int k, int* old) {
-  *old = -1;
-  if (k >= w.n) return true;
-  const int p = ld(P.page_table + (int64_t)r * P.max_pages + k);
-  const int c = ld(P.refcount + p);
-  if (c <= 1) return false;
-  *old = p;
-  return !(ld(W.a + p) == c && ld(W.b + p) == r);
-}
-
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
     reserve_kernel(tv_page_pool P, Workspace W, const int32_t* __restrict__ length,
                    const int32_t* __restrict__ new_length, int32_t* __restrict__ copies,
                    int32_t* status) {
-  __shared__ int64_t s_free[kCluster], s_need[kCluster], s_bad[kCluster], s_part[kWarps];
-  __shared__ int64_t s_row[4096 / kCluster + 1];
-  __shared__ int s_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_rank();
-  const int per = (P.num_pages + kCluster - 1) / kCluster;
-  const int p0 = min(P.num_pages, rank * per), p1 = min(P.num_pages, p0 + per);
+  constexpr int kRows = 4096 / kCluster;  // of a CTA at most: one per thread
+  static_assert(kRows <= kThreads, "a thread per row");
+  __shared__ int64_t s_flags[kCluster], s_free[kCluster], s_need[kCluster], s_part[kWarps];
+  __shared__ int s_new[kRows], s_at[kRows], s_k[kRows];  // of the pages behind those held
+  const int tid = threadIdx.x;
   const int per_r = (P.rows + kCluster - 1) / kCluster;
-  const int r0 = min(P.rows, rank * per_r), r1 = min(P.rows, r0 + per_r);
-  if (tid == 0) s_flag = 0;
-  // free pages of this slice; scratch of the shared ones
-  int n_free = 0;
-  for (int p = p0 + tid; p < p1; p += kThreads) {
-    const int c = ld(P.refcount + p);
-    n_free += c == 0;
-    if (c > 1) {
-      W.a[p] = 0;
+  const int r0 = min(P.rows, (int)cluster_rank() * per_r), r1 = min(P.rows, r0 + per_r);
+  const int r = r0 + tid;
+  // the row, and its pages that are written again: [first, held)
+  RowNeed w{};
+  bool bad = false, shared = false;
+  if (r < r1) w = row_need(P, r, length, new_length, &bad);
+  int32_t* row = P.page_table + (int64_t)r * P.max_pages;
+  const int held = w.active ? min(w.need, w.n) : 0;
+  for (int k = w.first; k < held; ++k) {
+    const int p = ld(row + k);
+    const int c = p >= 0 && p < P.num_pages ? ld(P.refcount + p) : 0;
+    if (c < 1) {
+      bad = true;
+    } else if (c > 1) {
+      shared = true;
+      W.a[p] = 0;  // every writer the same
       W.b[p] = INT_MAX;
     }
   }
-  const int64_t free_here = block_sum(n_free, s_part);
+  // free pages of this slice
+  Run run = run_of(P.num_pages);
+  const auto is_free = [&](int p) { return ld(P.refcount + p) == 0; };
+  int64_t free_here;
+  const int64_t free_before = block_scan(mark(run, is_free), s_part, &free_here);
+  const int64_t flags = __syncthreads_or(bad) ? 1ll << 32 : 0;
+  post(s_flags, flags + (__syncthreads_or(shared) ? 1 : 0));
+  post(s_free, free_here);
   cluster_sync();
-  // who writes which shared page; what is wrong with a row
-  bool bad = false;
-  for (int r = r0 + warp; r < r1; r += kWarps) {
-    const RowNeed w = row_need(P, r, length, new_length, &bad);
-    for (int k = w.first + lane; w.active && k < min(w.need, w.n); k += 32) {
-      const int p = ld(P.page_table + (int64_t)r * P.max_pages + k);
-      const int c = p >= 0 && p < P.num_pages ? ld(P.refcount + p) : 0;
-      if (c < 1) {
-        bad = true;
-      } else if (c > 1) {
+  const int64_t all_flags = collect(s_flags).total;
+  const Offsets of = collect(s_free);
+  const bool any_bad = all_flags >> 32;
+  int swaps = 0;
+  if (!any_bad && all_flags) {  // somewhere a shared page is written
+    for (int k = w.first; k < held; ++k) {
+      const int p = ld(row + k);
+      if (ld(P.refcount + p) > 1) {
         atomicAdd(W.a + p, 1);
         atomicMin(W.b + p, r);
       }
     }
-  }
-  if (bad) s_flag = 1;
-  __syncthreads();
-  post(s_bad, s_flag);
-  cluster_sync();
-  const bool any_bad = collect(s_bad).total > 0;
-  // fresh pages per row
-  int64_t mine = 0;
-  if (!any_bad) {
-    for (int r = r0 + warp; r < r1; r += kWarps) {
-      bool unused = false;
-      const RowNeed w = row_need(P, r, length, new_length, &unused);
-      int n = 0, old;
-      for (int k = w.first + lane; w.active && k < w.need; k += 32)
-        n += takes(P, W, w, r, k, &old);
-      const int64_t t = warp_sum(n);
-      if (lane == 0) {
-        s_row[r - r0] = t;
-        mine += t;
+    cluster_sync();
+    for (int k = w.first; k < held; ++k) {
+      const int p = ld(row + k), c = ld(P.refcount + p);
+      if (c > 1 && !(ld(W.a + p) == c && ld(W.b + p) == r)) {
+        row[k] = ~p;  // to be replaced
+        ++swaps;
       }
     }
   }
-  const int64_t need_here = block_sum(mine, s_part);
-  post(s_free, free_here);
+  const int fresh_k = max(w.n, w.first);  // the first page index that the row does not hold
+  const int news = w.active ? max(0, w.need - fresh_k) : 0;
+  int64_t need_here, news_here;
+  const int64_t need_before = block_scan(swaps + news, s_part, &need_here);
+  const int64_t news_before = block_scan(news, s_part, &news_here);
   post(s_need, need_here);
   cluster_sync();
-  const Offsets of = collect(s_free), on = collect(s_need);
+  const Offsets on = collect(s_need);
   if (any_bad || on.total > of.total) {  // the whole cluster alike
+    for (int k = w.first; swaps > 0 && k < held; ++k) {
+      const int p = ld(row + k);
+      if (p < 0) row[k] = ~p;
+    }
     for (int i = r0 * 3 + tid; i < r1 * 3; i += kThreads) copies[i] = i % 3 == 2 ? 0 : -1;
-    if (rank == 0 && tid == 0) report(status, any_bad ? TV_ERR_BOUNDS : TV_ERR_NO_PAGES);
+    if (cluster_rank() == 0 && tid == 0) report(status, any_bad ? TV_ERR_BOUNDS : TV_ERR_NO_PAGES);
     return;
   }
   // the lowest free pages, by rank
-  ranked(
-      p0, p1, of.below, on.total, s_part, [&](int p) { return ld(P.refcount + p) == 0; },
-      [&](int p, int64_t i) {
-        if (i < on.total) W.c[i] = p;
-      });
-  // where each row's fresh pages start
-  __syncthreads();
-  if (tid == 0) {
-    int64_t at = on.below;
-    for (int r = 0; r < r1 - r0; ++r) {
-      const int64_t n = s_row[r];
-      s_row[r] = at;
-      at += n;
-    }
+  emit(run, of.below + free_before, on.total, is_free, [&](int p, int64_t i) { W.c[i] = p; });
+  int at = (int)(on.below + need_before);  // below num_pages
+  if (r < r1) {
+    s_new[tid] = (int)news_before;
+    s_at[tid] = at + swaps - (int)news_before;
+    s_k[tid] = fresh_k - (int)news_before;
   }
   cluster_sync();
-  for (int r = r0 + warp; r < r1; r += kWarps) {
-    bool unused = false;
-    const RowNeed w = row_need(P, r, length, new_length, &unused);
+  if (r < r1) {
     int src = -1, dst = -1;
-    int64_t at = s_row[r - r0];
-    for (int k0 = w.first; w.active && k0 < w.need; k0 += 32) {
-      const int k = k0 + lane;
-      int old = -1;
-      const bool take = k < w.need && takes(P, W, w, r, k, &old);
-      const uint32_t m = __ballot_sync(0xffffffffu, take);
-      if (take) {
-        const int fresh = ld(W.c + at + __popc(m & ((1u << lane) - 1)));
-        P.page_table[(int64_t)r * P.max_pages + k] = fresh;
-        P.refcount[fresh] = 1;
-        if (old >= 0 && k == w.first) {
-          src = old;
-          dst = fresh;
-        }
+    for (int k = w.first; swaps > 0 && k < held; ++k) {
+      const int p = ld(row + k);
+      if (p >= 0) continue;
+      const int fresh = ld(W.c + at++);
+      row[k] = fresh;
+      P.refcount[fresh] = 1;
+      atomicSub(P.refcount + ~p, 1);
+      if (k == w.first) {
+        src = ~p;
+        dst = fresh;
       }
-      at += __popc(m);
     }
-    if (lane == 0) {  // lane 0 has the first page written
-      const int n = w.active ? length[r] % P.page_size : 0;
-      const bool copy = src >= 0 && n > 0;
-      copies[r * 3] = copy ? src : -1;
-      copies[r * 3 + 1] = copy ? dst : -1;
-      copies[r * 3 + 2] = copy ? n : 0;
-      if (w.active && w.need > w.n) P.n_pages[r] = w.need;
-    }
+    const int n = w.active ? length[r] % P.page_size : 0;
+    const bool copy = src >= 0 && n > 0;
+    copies[r * 3] = copy ? src : -1;
+    copies[r * 3 + 1] = copy ? dst : -1;
+    copies[r * 3 + 2] = copy ? n : 0;
+    if (news > 0) P.n_pages[r] = w.need;
   }
-  cluster_sync();
-  // shared pages lose the holders that moved off
-  for (int p = p0 + tid; p < p1; p += kThreads) {
-    const int c = ld(P.refcount + p);
-    if (c > 1) {
-      const int n = ld(W.a + p);
-      if (n > 0) P.refcount[p] = n == c ? 1 : c - n;
+  // pages behind the ones held, all threads alike: their number differs from row to row
+  for (int i = tid; i < (int)news_here; i += kThreads) {
+    int x = 0, y = r1 - r0;  // the row x with s_new[x] <= i < s_new[x + 1]
+    while (y - x > 1) {
+      const int mid = (x + y) / 2;
+      if (s_new[mid] <= i) x = mid;
+      else y = mid;
     }
+    const int fresh = ld(W.c + s_at[x] + i);
+    P.page_table[(int64_t)(r0 + x) * P.max_pages + s_k[x] + i] = fresh;
+    P.refcount[fresh] = 1;
   }
 }
 
@@ -336,32 +340,37 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
                         int32_t* __restrict__ n_moves) {
   __shared__ int64_t s_used[kCluster], s_hole[kCluster], s_move[kCluster], s_part[kWarps];
   const int tid = threadIdx.x, rank = (int)cluster_rank();
-  const int per = (P.num_pages + kCluster - 1) / kCluster;
-  const int p0 = min(P.num_pages, rank * per), p1 = min(P.num_pages, p0 + per);
-  int n = 0;
-  for (int p = p0 + tid; p < p1; p += kThreads) n += ld(P.refcount + p) > 0;
-  const int64_t here = block_sum(n, s_part);
+  Run run = run_of(P.num_pages);
+  const auto is_used = [&](int p) { return ld(P.refcount + p) > 0; };
+  const int64_t here = block_sum(mark(run, is_used), s_part);
   post(s_used, here);
   cluster_sync();
   const int used = (int)collect(s_used).total;
-  int holes = 0, movers = 0;
-  for (int p = p0 + tid; p < p1; p += kThreads) {
-    const bool on = ld(P.refcount + p) > 0;
-    holes += !on && p < used;
-    movers += on && p >= used;
-    if (!on) W.c[p] = -1;
+  const auto is_hole = [&](int p) { return p < used && ld(P.refcount + p) <= 0; };
+  const auto moves_on = [&](int p) { return p >= used && ld(P.refcount + p) > 0; };
+  Run holes = run, movers = run;
+  if (run.p1 - run.p0 <= 64) {  // from the bits: those below `used`, and the others
+    const int n = max(0, min(run.p1, used) - run.p0);
+    const uint64_t low = n >= 64 ? ~0ull : (1ull << n) - 1;
+    const int m = run.p1 - run.p0;
+    holes.bits = ~run.bits & low & (m >= 64 ? ~0ull : m > 0 ? (1ull << m) - 1 : 0ull);
+    movers.bits = run.bits & ~low;
   }
-  const int64_t holes_here = block_sum(holes, s_part), movers_here = block_sum(movers, s_part);
+  const bool known = run.p1 - run.p0 <= 64;
+  int64_t holes_here, movers_here;
+  const int64_t hole0 = block_scan(known ? __popcll(holes.bits) : mark(holes, is_hole), s_part,
+                                   &holes_here);
+  const int64_t move0 = block_scan(known ? __popcll(movers.bits) : mark(movers, moves_on), s_part,
+                                   &movers_here);
+  // where a page goes: -1 for the free ones (a table that names one is wrong)
+  for (int p = max(run.p0, used); p < run.p1; ++p)
+    if (known ? !((run.bits >> (p - run.p0)) & 1) : !is_used(p)) W.c[p] = -1;
   post(s_hole, holes_here);
   post(s_move, movers_here);
   cluster_sync();
   const Offsets oh = collect(s_hole), om = collect(s_move);
-  ranked(
-      p0, min(p1, used), oh.below, LLONG_MAX, s_part,
-      [&](int p) { return ld(P.refcount + p) <= 0; }, [&](int p, int64_t i) { W.a[i] = p; });
-  ranked(
-      max(p0, used), p1, om.below, LLONG_MAX, s_part,
-      [&](int p) { return ld(P.refcount + p) > 0; }, [&](int p, int64_t i) { W.b[i] = p; });
+  emit(holes, oh.below + hole0, LLONG_MAX, is_hole, [&](int p, int64_t i) { W.a[i] = p; });
+  emit(movers, om.below + move0, LLONG_MAX, moves_on, [&](int p, int64_t i) { W.b[i] = p; });
   cluster_sync();
   const int total = (int)om.total;  // as many holes as pages that move
   for (int i = rank * kThreads + tid; i < total; i += kCluster * kThreads) {
@@ -393,8 +402,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- copy -------------------------------------------------------------------------------
-constexpr int kCopyThreads = 256;
+// A unit of 16 rows of 512 + 64 bf16 elements is four 16-byte words a thread.
+constexpr int kCopyThreads = 288;
 constexpr int kCopyRows = 16;  // rows per unit of work
+constexpr int kCopyUnroll = 4;
 
 struct CopyParams {
   uint4 *c_kv, *k_pe;
@@ -406,24 +417,6 @@ struct CopyParams {
   int n_list;
   int32_t* status;
 };
-
-__device__ __forceinline__ void copy_rows(uint4* x, int64_t stride, int words, int64_t src,
-                                          int64_t dst, int rows) {
-  const int total = rows * words;
-  for (int i = threadIdx.x; i < total; i += 4 * kCopyThreads) {
-    uint4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = i + u * kCopyThreads;
-      if (j < total) v[u] = x[(src + j / words) * stride + j % words];
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = i + u * kCopyThreads;
-      if (j < total) x[(dst + j / words) * stride + j % words] = v[u];
-    }
-  }
-}
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p) {
   const int n = p.count ? min(max(*p.count, 0), p.n_list) : p.n_list;
@@ -444,9 +437,28 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p) {
     const int at = chunk * kCopyRows, here = min(kCopyRows, rows - at);
     if (here <= 0) continue;
     const int64_t src = s * p.page_size + at, dst = d * p.page_size + at;
-    copy_rows(p.c_kv + layer * p.ckv_layer, p.ckv_stride, p.ckv_words, src, dst, here);
-    if (p.kpe_words > 0)
-      copy_rows(p.k_pe + layer * p.kpe_layer, p.kpe_stride, p.kpe_words, src, dst, here);
+    uint4* const c = p.c_kv + layer * p.ckv_layer;
+    uint4* const k = p.kpe_words > 0 ? p.k_pe + layer * p.kpe_layer : c;
+    // the rows' words, both arrays' in one
+    const int words = p.ckv_words + p.kpe_words, total = here * words;
+    for (int i = threadIdx.x; i < total; i += kCopyUnroll * kCopyThreads) {
+      uint4 v[kCopyUnroll];
+      uint4* to[kCopyUnroll];
+#pragma unroll
+      for (int e = 0; e < kCopyUnroll; ++e) {
+        const int j = i + e * kCopyThreads;
+        if (j >= total) continue;
+        const int r = j / words, x = j - r * words;
+        const bool latent = x < p.ckv_words;
+        uint4* const base = latent ? c + x : k + (x - p.ckv_words);
+        const int64_t stride = latent ? p.ckv_stride : p.kpe_stride;
+        v[e] = __ldcs(base + (src + r) * stride);
+        to[e] = base + (dst + r) * stride;
+      }
+#pragma unroll
+      for (int e = 0; e < kCopyUnroll; ++e)
+        if (i + e * kCopyThreads < total) __stcs(to[e], v[e]);
+    }
   }
 }
 
@@ -507,7 +519,7 @@ cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_
   p.n_list = n_list;
   p.status = status;
   const int64_t units = (int64_t)n_list * n_layers * p.chunks;
-  const int64_t grid = std::min<int64_t>(units, 8ll * current_sm_count());
+  const int64_t grid = std::min<int64_t>(units, 7ll * current_sm_count());
   copy_kernel<<<(unsigned)grid, kCopyThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
