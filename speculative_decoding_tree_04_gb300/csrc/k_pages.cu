@@ -519,7 +519,9 @@ cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_
   p.n_list = n_list;
   p.status = status;
   const int64_t units = (int64_t)n_list * n_layers * p.chunks;
-  const int64_t grid = std::min<int64_t>(units, 7ll * current_sm_count());
+  // 24 CTAs per SM, several waves of them: 3.9k pages of two layers (1.16 GB moved) took 192 us
+  // with 7, 179 with 12, 172 with 24 and 217 with a CTA per unit of the list's capacity
+  const int64_t grid = std::min<int64_t>(units, 24ll * current_sm_count());
   copy_kernel<<<(unsigned)grid, kCopyThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
