@@ -26,6 +26,27 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 
+// Every kernel here is launched as a programmatic dependent of the one before it on the
+// stream, so that its launch overlaps that one, and waits for it before anything else.
+__device__ __forceinline__ void begin() {
+  griddep_launch_dependents();
+  griddep_wait();
+}
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), int64_t grid, int block, cudaStream_t st,
+                   Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct Workspace {
   int32_t* a;     // reserve: writers of a shared page.   compact: holes by rank
   int32_t* b;     // reserve: its lowest writer.          compact: pages that move, by rank
@@ -171,6 +192,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
   static_assert(kRows <= kThreads, "a thread per row");
   __shared__ int64_t s_flags[kCluster], s_free[kCluster], s_need[kCluster], s_part[kWarps];
   __shared__ int s_new[kRows], s_at[kRows], s_k[kRows];  // of the pages behind those held
+  begin();
   const int tid = threadIdx.x;
   const int per_r = (P.rows + kCluster - 1) / kCluster;
   const int r0 = min(P.rows, (int)cluster_rank() * per_r), r1 = min(P.rows, r0 + per_r);
@@ -287,6 +309,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(128)
     fork_kernel(tv_page_pool P, const int32_t* __restrict__ fork_from,
                 const int32_t* __restrict__ length, int32_t* status) {
+  begin();
   const int r = blockIdx.x, src = fork_from[r];
   if (src < 0) return;
   const int64_t want = ((int64_t)length[r] + P.page_size - 1) / P.page_size;
@@ -313,6 +336,7 @@ __global__ void __launch_bounds__(128)
 
 __global__ void __launch_bounds__(128)
     release_kernel(tv_page_pool P, const int32_t* __restrict__ keep, int32_t* status) {
+  begin();
   const int r = blockIdx.x;
   if (keep[r] < 0) return;
   const int64_t kept = ((int64_t)keep[r] + P.page_size - 1) / P.page_size;
@@ -339,6 +363,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
     compact_plan_kernel(tv_page_pool P, Workspace W, int32_t* __restrict__ moves,
                         int32_t* __restrict__ n_moves) {
   __shared__ int64_t s_used[kCluster], s_hole[kCluster], s_move[kCluster], s_part[kWarps];
+  begin();
   const int tid = threadIdx.x, rank = (int)cluster_rank();
   Run run = run_of(P.num_pages);
   const auto is_used = [&](int p) { return ld(P.refcount + p) > 0; };
@@ -390,6 +415,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(256)
     compact_tables_kernel(tv_page_pool P, Workspace W, int32_t* status) {
+  begin();
   const int r = blockIdx.x, used = W.head[0];
   const int n = min(P.n_pages[r], P.max_pages);
   int32_t* row = P.page_table + (int64_t)r * P.max_pages;
@@ -419,6 +445,7 @@ struct CopyParams {
 };
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyParams p) {
+  begin();
   const int n = p.count ? min(max(*p.count, 0), p.n_list) : p.n_list;
   const int64_t units = (int64_t)n * p.n_layers * p.chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -469,31 +496,26 @@ size_t pages_workspace(const tv_page_pool& p) { return 3 * ws_array(p.num_pages)
 cudaError_t launch_pages_reserve(const tv_page_pool& p, const int32_t* length,
                                  const int32_t* new_length, int32_t* copies, int32_t* status,
                                  void* ws, cudaStream_t st) {
-  reserve_kernel<<<kCluster, kThreads, 0, st>>>(p, split(ws, p.num_pages), length, new_length,
-                                                copies, status);
-  return cudaGetLastError();
+  return launch(reserve_kernel, kCluster, kThreads, st, p, split(ws, p.num_pages), length,
+                new_length, copies, status);
 }
 
 cudaError_t launch_pages_fork(const tv_page_pool& p, const int32_t* fork_from,
                               const int32_t* length, int32_t* status, cudaStream_t st) {
-  fork_kernel<<<p.rows, 128, 0, st>>>(p, fork_from, length, status);
-  return cudaGetLastError();
+  return launch(fork_kernel, p.rows, 128, st, p, fork_from, length, status);
 }
 
 cudaError_t launch_pages_release(const tv_page_pool& p, const int32_t* keep, int32_t* status,
                                  cudaStream_t st) {
-  release_kernel<<<p.rows, 128, 0, st>>>(p, keep, status);
-  return cudaGetLastError();
+  return launch(release_kernel, p.rows, 128, st, p, keep, status);
 }
 
 cudaError_t launch_pages_compact(const tv_page_pool& p, int32_t* moves, int32_t* n_moves,
                                  int32_t* status, void* ws, cudaStream_t st) {
   const Workspace w = split(ws, p.num_pages);
-  compact_plan_kernel<<<kCluster, kThreads, 0, st>>>(p, w, moves, n_moves);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch(compact_plan_kernel, kCluster, kThreads, st, p, w, moves, n_moves);
   if (e != cudaSuccess) return e;
-  compact_tables_kernel<<<p.rows, 256, 0, st>>>(p, w, status);
-  return cudaGetLastError();
+  return launch(compact_tables_kernel, p.rows, 256, st, p, w, status);
 }
 
 cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_t kpe_stride,
@@ -522,8 +544,7 @@ cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_
   // 24 CTAs per SM, several waves of them: 3.9k pages of two layers (1.16 GB moved) took 192 us
   // with 7, 179 with 12, 172 with 24 and 217 with a CTA per unit of the list's capacity
   const int64_t grid = std::min<int64_t>(units, 24ll * current_sm_count());
-  copy_kernel<<<(unsigned)grid, kCopyThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch(copy_kernel, grid, kCopyThreads, st, p);
 }
 
 }  // namespace tv

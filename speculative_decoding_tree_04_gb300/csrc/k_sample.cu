@@ -437,6 +437,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
   const int b = blockIdx.x / C, Q = p.Q;
   int32_t* path = p.path + (int64_t)b * Q;
   int32_t* emit = p.new_tokens + (int64_t)b * Q;
+  // (launched as a programmatic dependent of the kernel before it)
+  griddep_launch_dependents();
+  griddep_wait();
   // warp 0 holds the tree: node lane and node lane + 32
   int par[2] = {-2, -2}, tok[2] = {-1, -1};
   float uni[2] = {0.f, 0.f};
@@ -900,12 +903,14 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)(p.B * C));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (C > 8) {
     cudaError_t e = cudaFuncSetAttribute(tree_sample_kernel<T, kThreads>,
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
