@@ -19,12 +19,16 @@
 //
 // Passes.  A visited row is streamed once for its maximum and a float sum of exponentials
 // relative to a running one; what else it takes (a residual's sum, the draw) reads it from L2.
-// Floats decide first: every sum carries a bound on its error (1e-5 of the row's sum), a test
-// whose two sides differ by more than the bounds is decided, and so is a draw that lands that
-// far inside a token.  Whatever is closer sends the node back to be done with the exact sums
-// below: two tests in 10^5, and as many draws as the distribution has mass near boundaries
-// (a few in 100 for a language model's, all of them for a flat one).  An exact weight costs
-// about eight times a float one.
+// Floats decide first: every sum carries a bound on its error (about 4e-6 of the row's sum), a
+// test whose two sides differ by more than the bounds is decided, and so is a draw that lands
+// that far inside a token.  Whatever is closer sends the node back to be done with the exact
+// sums below: a few tests in 10^6, and as many draws as the distribution has mass near
+// boundaries (one in 100 for a language model's, all of them for a flat one).  An exact weight
+// costs about eight times a float one.
+//   The bound: 2^((x - m) c) has a relative error of 2^-23 ln 2 |y| from the roundings of its
+// exponent y and 2^-22 from the exponential; a distribution's mean |y| is its entropy less
+// log2 Z, at most 18 (2^18 tokens), so that the sum's error is below 1.8e-6 of it; and every
+// addition on the way from a value to the row's sum adds 2^-24.
 //
 // Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
 // that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
@@ -211,7 +215,11 @@ struct Row {
     off = (int)(((uintptr_t)row & 15u) / sizeof(T));
     n_vec = (int)((V + off + Vec<T>::N - 1) / Vec<T>::N);
   }
-  __device__ int vector_of(int64_t v) const { return (int)((v + off) / Vec<T>::N); }
+  // Whether token v lies in the i-th of the parts of `per` vectors that start at `from`.
+  __device__ bool in_part(int64_t v, int per, int i, int from = 0) const {
+    const int j = (int)((v + off) / Vec<T>::N) - from;
+    return j >= i * per && j < (i + 1) * per;
+  }
   __device__ int64_t first(int j) const { return (int64_t)j * Vec<T>::N - off; }
   __device__ bool whole(int j) const { return first(j) >= 0 && first(j) + Vec<T>::N <= V; }
   // The vectors that lie in the row whole, [first_whole, end_whole).
@@ -359,13 +367,12 @@ __device__ __forceinline__ int64_t* warp_sums(Shared& sh, int64_t) { return sh.w
 __device__ __forceinline__ float* warp_sums(Shared& sh, float) { return sh.warp_part; }
 
 // The owner's part of a draw, by the whole CTA: the token at place target_of(sh) of vectors
-// range0 .. range1-1, found through the warps' shares of them, the vector and the element.
-// Returns it in warp 0's lane that found it (others -1); -2 where a float draw lands within
-// `margin` of a token's edge.
+// range0 .. range1-1, a vector per thread at a time.  Returns it in the thread that has it
+// (others -1), or -2 there where a float draw lands within `margin` of a token's edge.
 template <typename S, int kWarps, typename T>
 __device__ __forceinline__ int draw(Shared& sh, const Row<T>& row, const Scale& sc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_out = sh.n_rejected;
-  int y0 = sh.range0, y1 = sh.range1;
+  const int y0 = sh.range0, y1 = sh.range1;
   S t = target_of(sh, (S)0);
   // the weights of one vector, without the tokens refused
   auto load = [&](int j, S* e) {
@@ -381,33 +388,23 @@ __device__ __forceinline__ int draw(Shared& sh, const Row<T>& row, const Scale& 
     }
     return s;
   };
-  if (y1 - y0 > 128) {  // long enough for all warps to share
-    const int per = (y1 - y0 + kWarps - 1) / kWarps;
-    const int x0 = min(y1, y0 + warp * per), x1 = min(y1, x0 + per);
-    S part = 0;
-    for (int j = x0 + lane; j < x1; j += 32) {
-      S e[Vec<T>::N];
-      part += load(j, e);
-    }
-    part = warp_sum(part);
-    if (lane == 0) warp_sums(sh, (S)0)[warp] = part;
-    __syncthreads();
-    if (warp != 0) return -1;
-    const int w = locate(lane < kWarps ? warp_sums(sh, (S)0)[lane] : (S)0, kWarps, &t);
-    y0 = min(y1, y0 + w * per);
-    y1 = min(y1, y0 + per);
-  }
-  if (warp != 0) return -1;
-  for (int j = y0; j < y1; j += 32) {
+  S* sums = warp_sums(sh, (S)0);
+  for (int base = y0; base < y1; base += 32 * kWarps) {  // a vector per thread
+    const int j = base + 32 * warp + lane;
     S e[Vec<T>::N];
-    const S s = load(j + lane, e);
-    const S all = warp_sum(s);
-    if (t >= all && j + 32 < y1) {
+    const S s = load(j, e);
+    const S part = warp_sum(s);
+    __syncthreads();
+    if (lane == 0) sums[warp] = part;
+    __syncthreads();
+    const S mine = lane < kWarps ? sums[lane] : (S)0;
+    const S all = warp_sum(mine);
+    if (t >= all && base + 32 * kWarps < y1) {
       t -= all;
       continue;
     }
-    const int at = locate(s, 32, &t);
-    if (lane != at) return -1;
+    if (warp != locate(mine, kWarps, &t)) return -1;
+    if (lane != locate(s, 32, &t)) return -1;
     int k = 0;
     S width = 0;
     bool found = false;
@@ -422,19 +419,19 @@ __device__ __forceinline__ int draw(Shared& sh, const Row<T>& row, const Scale& 
     }
     const float edge = fminf((float)t, (float)(width - t));
     if (sizeof(S) == 4 && !(found && edge > sh.margin)) return -2;
-    return (int)row.first(j + at) + k;
+    return (int)row.first(j) + k;
   }
-  return sizeof(S) == 4 && lane == 0 ? -2 : -1;
+  return sizeof(S) == 4 && threadIdx.x == 0 ? -2 : -1;
 }
 
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
-    tree_sample_kernel(SampleParams p, int C) {
+    tree_sample_kernel(SampleParams p, int log2_C) {
   constexpr int kWarps = kThreads / 32;
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = 1 << log2_C, b = blockIdx.x >> log2_C, Q = p.Q;
   const int rank = C > 1 ? (int)cluster_rank() : 0;
-  const int b = blockIdx.x / C, Q = p.Q;
   int32_t* path = p.path + (int64_t)b * Q;
   int32_t* emit = p.new_tokens + (int64_t)b * Q;
   // (launched as a programmatic dependent of the kernel before it)
@@ -482,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
   int node = 0, count = 0, phase = 0;
   for (;;) {
     const Row<T> row((const T*)p.logits + ((int64_t)b * Q + node) * p.stride, p.V);
-    const int per = (row.n_vec + C - 1) / C;
+    const int per = (row.n_vec + C - 1) >> log2_C;
     const int c0 = min(row.n_vec, rank * per), c1 = min(row.n_vec, c0 + per);
     const int per_w = (per + kWarps - 1) / kWarps;
     const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
@@ -640,7 +637,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
                              : 0.f;  // lane r: slice r's sum
       phase ^= 1;
       const float Z = warp_sum(part);
-      float W = Z, dW = 1e-5f * Z, S = 0.f, dS = 0.f, G = 1.f;
+      // additions from a value to the row's sum: a vector, a thread, a warp, a CTA, a cluster
+      const float adds = 6e-8f * (float)(N + (per_w + 31) / 32 + 16);
+      float W = Z, dW = (1.8e-6f + adds) * Z, S = 0.f, dS = 0.f, G = 1.f;
       uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
       float ew[2] = {0.f, 0.f};
       if (warp == 0) {
@@ -682,8 +681,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
               refused |= 1ull << i;
               W -= w;
               if (!again) {
-                const int j = row.vector_of(x);
-                if (j / per == lane) part -= w;
+                if (row.in_part(x, per, lane)) part -= w;
                 if (lane == 0) sh.rejected[n] = x;
                 ++n;
               }
@@ -691,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             }
             refused |= 1ull << i;
             S += W / G;
-            dS += (dW + 1e-6f * W) / G;
+            dS += (dW + W * (1e-6f + 1e-6f / G)) / G + 1e-7f * S;
             G -= g;
             cmd = G > 1e-3f ? kResidual : kExact;
           }
@@ -712,18 +710,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             }
             __syncwarp();
             for (int r = 0; r < n; ++r) {
-              const int x = sh.rejected[r], j = row.vector_of(x) - c0;
+              const int x = sh.rejected[r];
               const uint64_t same =
                   (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
                   (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
               const float w = pick(ew, __ffsll((long long)(same & refused)) - 1);
-              if (j >= 0 && j < c1 - c0 && j / per_w == lane) mine -= w;
+              if (row.in_part(x, per, rank) && row.in_part(x, per_w, lane, c0)) mine -= w;
             }
             const int w = locate(mine, kWarps, &t);
             next = owner;
             if (lane == 0) {
               sh.target_f = t;
-              sh.margin = 4.f * dW;
+              sh.margin = 3.f * dW;  // the target's error and the sums' of both passes
               sh.range0 = min(c1, c0 + w * per_w);
               sh.range1 = min(c1, sh.range0 + per_w);
             }
@@ -754,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
         if (warp == 0) {
           part = lane < C ? sh.parts[phase][lane] : 0.f;
           W = warp_sum(part);
-          dW = 1e-5f * (Z + S) + dS;
+          dW = 1.9e-6f * Z + 1e-7f * S + adds * W + dS;
         }
         phase ^= 1;
       }
@@ -827,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             if (!p.draft) {
               W -= w;
               if (!again) {
-                if (row.vector_of(x) / per == lane) part -= w;
+                if (row.in_part(x, per, lane)) part -= w;
                 if (lane == 0) sh.rejected[n] = x;
                 ++n;
               }
@@ -845,12 +843,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             int64_t mine = lane < kWarps ? sh.warp_sum[lane] : 0;
             __syncwarp();
             for (int r = 0; r < n; ++r) {
-              const int x = sh.rejected[r], j = row.vector_of(x) - c0;
+              const int x = sh.rejected[r];
               const uint64_t same =
                   (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) |
                   (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
               const int64_t w = pick(child_e, __ffsll((long long)(same & refused)) - 1);
-              if (j >= 0 && j < c1 - c0 && j / per_w == lane) mine -= w;
+              if (row.in_part(x, per, rank) && row.in_part(x, per_w, lane, c0)) mine -= w;
             }
             const int w = locate(mine, kWarps, &t);
             if (lane == 0) {
@@ -916,7 +914,9 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
                                          cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T, kThreads>, p, C);
+  int log2_C = 0;
+  while ((1 << log2_C) < C) ++log2_C;
+  return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T, kThreads>, p, log2_C);
 }
 
 // Threads per CTA: 1024 or 512 where the CTAs leave an SM that much room and a thread still
