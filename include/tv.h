@@ -618,8 +618,8 @@ typedef struct {
                                 value past 65504. */
 } tv_prefill_args;
 
-/* Bytes of workspace (the expanded keys and values: about 512 * H + 128 bytes per key);
- * depends on B, H, T and total_kv.  0 for invalid arguments. */
+/* Bytes of workspace (the expanded keys and values: about 512 * H + 128 bytes per key, and up
+ * to 20 MB for small batches); depends on B, H, T and total_kv, and on the device.  0 for invalid arguments. */
 size_t tv_prefill_attn_workspace_size(const tv_prefill_args* a);
 
 /* workspace: device memory of at least that size, 256-byte aligned; scratch. */

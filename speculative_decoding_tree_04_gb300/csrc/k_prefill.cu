@@ -9,14 +9,16 @@
 // So it pays from about 170 queries per key sweep on; below that the absorbed form is
 // cheaper.
 //
-// Three kernels:
-//   plan     one block: where each sequence's expanded keys go, the tiles of the other two;
+// Four kernels:
+//   plan     one block: where each sequence's expanded keys go, the tiles of the others;
 //   expand   [K | V] = C W^T for every sequence and head, a GEMM of 128 keys x 256 outputs
 //            x d_latent, rounded into the workspace to 16 bits (what the tensor cores read):
 //            K to bf16, the type of the queries it meets, V to fp16 (three bits more); rows
 //            behind a sequence's last key are zero, so that masked weights (zero) times them
 //            is zero;
-//   attend   per head and 256 queries, an online softmax over 128 keys at a time.
+//   attend   per head and 256 queries, an online softmax over 128 keys at a time; where that
+//            leaves SMs idle, the keys are cut into pieces that
+//   join     puts together.
 //
 // Both tensor-core kernels are warp-specialised: one thread issues TMA loads into a ring of
 // 128-byte-swizzled tiles, one issues tcgen05.mma with accumulators in TMEM, whole warps
@@ -50,16 +52,19 @@ constexpr float kRescale = 8.0f;                // log2: see attend_kernel
 constexpr float kMaxV = 65504.f;                // the largest fp16
 
 // ---- workspace --------------------------------------------------------------------------
-// counts {query tiles, key tiles}; query tiles {first row of q, rows left, position of the
+// counts {query tiles, key tiles, pieces of an item}; query tiles {first row of q, rows left, position of the
 // first row, first expanded key}; key tiles {sequence, first key, expanded row, rows left};
-// then K [H][cap][128] in bf16, V [H][cap][128] in fp16 and the rope keys [cap][64].
+// then K [H][cap][128] in bf16, V [H][cap][128] in fp16 and the rope keys [cap][64]; and,
+// where items may be cut, a piece's unnormalised output [256][128] and its rows' maximum and
+// sum [256][2], in floats, for each SM.
 struct Layout {
   int64_t cap;               // expanded key rows
   int64_t max_q, max_k;      // tiles at most
-  size_t q_tiles, k_tiles, k, v, kr, total;
+  bool cut;                  // few items: their keys may be cut into pieces
+  size_t q_tiles, k_tiles, k, v, kr, part_o, part_ml, total;
 };
 size_t align1k(size_t n) { return (n + 1023) / 1024 * 1024; }
-Layout layout(const tv_prefill_args* a) {
+Layout layout(const tv_prefill_args* a, int sm_count) {
   Layout l{};
   l.cap = (a->total_kv + (int64_t)(kBlock - 1) * a->B + kBlock - 1) / kBlock * kBlock;
   l.max_k = l.cap / kBlock;
@@ -75,6 +80,11 @@ Layout layout(const tv_prefill_args* a) {
   n += (size_t)l.cap * a->H * kDV * 2;
   l.kr = n;
   n += (size_t)l.cap * kDR * 2;
+  l.cut = l.max_q * a->H < sm_count;
+  l.part_o = n;
+  if (l.cut) n += (size_t)sm_count * kPair * kDV * 4;
+  l.part_ml = n;
+  if (l.cut) n += (size_t)sm_count * kPair * 2 * 4;
   l.total = n;
   return l;
 }
@@ -84,7 +94,7 @@ struct PlanArgs {
   const int32_t* q_start;
   const int32_t* prefix_len;
   int32_t B, T, max_q_len, max_kv_len;
-  int32_t max_q, max_k;
+  int32_t max_q, max_k, H, slots;  // slots: SMs if items may be cut, else 0
   int32_t* counts;
   int4* q_tiles;
   int4* k_tiles;
@@ -92,7 +102,7 @@ struct PlanArgs {
 };
 
 __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
-  __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost;
+  __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost, s_longest;
   __shared__ int s_weight[1024];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();  // the expansion may set itself up meanwhile
@@ -181,8 +191,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
   if (tid == 0) {
     p.counts[0] = total_q;
     p.counts[1] = total_k;
+    s_longest = 0;
   }
   // longest sweeps first, so that the short ones fill the end (up to 1024 tiles)
+  __syncthreads();
+  for (int i = tid; p.slots && i < total_q; i += 1024) {
+    const int4 t = p.q_tiles[i];
+    atomicMax(&s_longest, (t.z + min(t.y, kPair) + kBlock - 1) / kBlock);
+  }
+  __syncthreads();
+  // pieces: one per SM, of at least four blocks in the longest item
+  if (tid == 0)
+    p.counts[2] = total_q > 0 && p.slots ? max(1, min(p.slots / (total_q * p.H), s_longest / 4)) : 1;
   if (total_q > 1024) return;
   int4 mine = make_int4(0, 0, 0, 0);
   if (tid < total_q) {
@@ -473,31 +493,41 @@ struct AttendArgs {
   int32_t H;
   float scale_log2;
   __nv_bfloat16* out;
+  float* part_o;   // [piece][256][128]
+  float* part_ml;  // [piece][256][2]
   int32_t* status;
 };
 
 // The r-th item of this CTA.  Items are listed longest first and dealt in rounds of
-// alternating direction.
+// alternating direction; an item that is cut is as many items, one a CTA.
 struct Item {
   bool some;
-  int h, row0, rows, pos0, key0, tiles, n0, n1;  // n: key blocks that a tile's last row sees
+  int slot;                       // its place in the list
+  int h, row0, rows, pos0, key0, tiles;
+  int j0, n0, n1;                 // first key block; blocks from there that a tile's rows see
 };
-__device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int r) {
+__device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int pieces, int r) {
   Item it;
   const int64_t i =
       (int64_t)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   it.some = i < total;
   if (!it.some) return it;
-  const int tile = (int)i / p.H;
-  it.h = (int)i - tile * p.H;
+  it.slot = (int)i;
+  const int whole = it.slot / pieces, piece = it.slot - whole * pieces;
+  const int tile = whole / p.H;
+  it.h = whole - tile * p.H;
   const int4 qt = p.q_tiles[tile];
   it.row0 = qt.x;
   it.rows = min(qt.y, kPair);
   it.pos0 = qt.z;
-  it.key0 = qt.w;
   it.tiles = it.rows > kBlock ? 2 : 1;
-  it.n0 = (it.pos0 + min(it.rows, kBlock) + kBlock - 1) / kBlock;
-  it.n1 = it.tiles > 1 ? (it.pos0 + it.rows + kBlock - 1) / kBlock : 0;
+  const int n0 = (it.pos0 + min(it.rows, kBlock) + kBlock - 1) / kBlock;
+  const int n1 = it.tiles > 1 ? (it.pos0 + it.rows + kBlock - 1) / kBlock : 0;
+  const int n = max(n0, n1), j1 = (int)((int64_t)n * (piece + 1) / pieces);
+  it.j0 = (int)((int64_t)n * piece / pieces);
+  it.n0 = max(0, min(n0, j1) - it.j0);
+  it.n1 = max(0, min(n1, j1) - it.j0);
+  it.key0 = qt.w + it.j0 * kBlock;
   return it;
 }
 
@@ -566,8 +596,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  griddep_launch_dependents();
   griddep_wait();  // the plan and the expanded keys
-  const int total = p.counts[0] * p.H;
+  const int pieces = p.counts[2], total = p.counts[0] * p.H * pieces;
 
   if (warp == 0 && lane == 0) {
     fence_proxy_async_global();
@@ -578,8 +609,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     bool ok = true;
     int g = 0, items = 0, armed_k = 0, armed_v = 0;
     for (int r = 0; ok; ++r) {
-      const Item it = item_of(p, total, r);
+      const Item it = item_of(p, total, pieces, r);
       if (!it.some) break;
+      if (max(it.n0, it.n1) == 0) continue;  // (a piece of a short item: one item a CTA then)
       // the last block of scores of the item before frees the queries
       if (g > 0) ok = wait_for(sh.abort, &sh.k_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       if (!ok) break;
@@ -669,18 +701,22 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     };
     bool ok = tmem == 0;  // 512 of 512 columns: the addresses above are absolute
     for (int r = 0; ok; ++r) {
-      const Item it = item_of(p, total, r);
+      const Item it = item_of(p, total, pieces, r);
       if (!it.some) break;
       const int n0 = __reduce_max_sync(0xffffffffu, it.n0);
       const int n1 = __reduce_max_sync(0xffffffffu, it.n1);
       const int nt = t ? n1 : n0, n = max(n0, n1);
       const bool both = n1 > 0;
-      if (nt > 0) {
+      if (t == 0 ? n > 0 : both) {
         ok = wait(&sh.q_full, r & 1) && wait(&sh.k_full[g & 1], (g >> 1) & 1) && take_turn(both);
         if (!ok) break;
         tc_fence_after();
-        scores(g, both);
-        done(&sh.k_done[g & 1], !both);
+        if (nt > 0) {
+          scores(g, both);
+          done(&sh.k_done[g & 1], !both);
+        } else {
+          pass_turn(both);
+        }
         for (int j = 0; ok && j < nt; ++j) {
           const int gj = g + j;
           ok = wait(&sh.v_full[gj & 1], (gj >> 1) & 1) &&
@@ -707,8 +743,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             done(&sh.v_done[gj & 1], !both);
           }
         }
-        // The first tile may end a block early: it passes its turn and lets go of that
-        // block.  Its barriers' phase before (two blocks back) has to be over, or the
+        // The first tile may end before the second: it passes its turns and lets go of those
+        // blocks.  Their barriers' phase before (two blocks back) has to be over, or the
         // arrival would count for that one.
         for (int j = nt; ok && j < n; ++j) {
           const int gj = g + j;
@@ -746,11 +782,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     int sc = 0, oc = 0;
     bool ok = true;
     for (int r = 0; ok; ++r) {
-      const Item it = item_of(p, total, r);
-      if (!it.some) break;
-      const int nt = t ? it.n1 : it.n0;
-      if (nt == 0) continue;
-      const int tile_first = it.pos0 + t * kBlock;  // every row of the tile sees keys 0 .. this
+      int nt, tile_first;  // every row of the tile sees the sweep's keys 0 .. tile_first
+      {
+        const Item it = item_of(p, total, pieces, r);
+        if (!it.some) break;
+        nt = t ? it.n1 : it.n0;
+        tile_first = it.pos0 + (t - it.j0) * kBlock;
+        if (nt == 0) {
+          if (pieces > 1 && t < it.tiles && (lane & 3) == 0) {  // nothing of these rows here
+            float* ml = p.part_ml + ((int64_t)it.slot * kPair + t * kBlock + ra) * 2;
+            ml[1] = ml[17] = 0.f;  // rows ra and ra + 8
+          }
+          continue;
+        }
+      }
       float ma = 0.f, mb = 0.f;                     // running maxima (of scores times c)
       float la = 0.f, lb = 0.f;                     // sums over this thread's columns
       for (int j = 0; j < nt; ++j, ++sc) {
@@ -786,14 +831,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)) * c;
         xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)) * c;
         // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
-        // the accumulator is rescaled rarely.  Key 0 is visible to every row, so the first
-        // block always has a maximum.
+        // the accumulator is rescaled rarely.  (A piece's first block may hide all its keys
+        // from a row: the maximum is -inf then, and taken as 0 for the weights, all zero.)
         if (j == 0) {
           ma = xa;
           mb = xb;
         } else if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
           const float na = xa > ma + kRescale ? xa : ma, nb = xb > mb + kRescale ? xb : mb;
-          const float fa = ex2(ma - na), fb = ex2(mb - nb);
+          const float fa = na == ma ? 1.f : ex2(ma - na), fb = nb == mb ? 1.f : ex2(mb - nb);
           ma = na;
           mb = nb;
           la *= fa;
@@ -810,7 +855,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             tmem_st_16x256b_x4(to + 32 * k, o);
           }
         }
-        const uint64_t m2a = f2_pack(-ma, -ma), m2b = f2_pack(-mb, -mb);
+        const float za = ma > -INFINITY ? -ma : 0.f, zb = mb > -INFINITY ? -mb : 0.f;
+        const uint64_t m2a = f2_pack(za, za), m2b = f2_pack(zb, zb);
         uint64_t l2a = 0, l2b = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -853,8 +899,30 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (!ok) break;
       ++oc;
       tc_fence_after();
+      const Item it = item_of(p, total, pieces, r);  // (again: not kept through the sweep)
+      const int q = t * kBlock + ra;                 // rows q and q + 8 of the item
+      if (pieces > 1) {
+        const int64_t at = (int64_t)it.slot * kPair + q;
+        if ((lane & 3) == 0) {
+          *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(ma, la);
+          *reinterpret_cast<float2*>(p.part_ml + (at + 8) * 2) = make_float2(mb, lb);
+        }
+        float* dst = p.part_o + at * kDV + col;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[16];
+          tmem_ld_16x256b_x4(to + 32 * k, o);
+          tmem_wait_ld_regs16(o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<uint2*>(dst + 32 * k + 8 * i) = make_uint2(o[4 * i], o[4 * i + 1]);
+            *reinterpret_cast<uint2*>(dst + 8 * kDV + 32 * k + 8 * i) =
+                make_uint2(o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        continue;  // (the CTA's only item)
+      }
       const float ia = 1.f / la, ib = 1.f / lb;
-      const int q = t * kBlock + ra;
       __nv_bfloat16* dst =
           p.out + ((int64_t)(it.row0 + q) * p.H + it.h) * kDV + 16 * (lane & 3);
       const int64_t down = (int64_t)8 * p.H * kDV;
@@ -884,6 +952,44 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---- join ---------------------------------------------------------------------------------
+// A warp per (item, query): the pieces' outputs weighted by 2^(m - M).  16 MB of partials at
+// most, from L2.
+__global__ void __launch_bounds__(256) join_kernel(AttendArgs p) {
+  griddep_wait();
+  const int pieces = p.counts[2];
+  if (pieces == 1) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)p.counts[0] * p.H * kPair;
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += 8 * gridDim.x) {
+    const int whole = (int)(u / kPair), q = (int)(u % kPair);
+    const int tile = whole / p.H, h = whole - tile * p.H;
+    const int4 qt = p.q_tiles[tile];
+    if (q >= qt.y) continue;
+    const int64_t at = (int64_t)whole * pieces * kPair + q;  // piece k: + k * kPair
+    float M = -INFINITY;
+    for (int k = 0; k < pieces; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * kPair) * 2);
+      if (ml.y > 0.f) M = fmaxf(M, ml.x);
+    }
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < pieces; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * kPair) * 2);
+      if (!(ml.y > 0.f)) continue;  // no key of it is visible (its output may not exist)
+      const float f = ex2(ml.x - M);
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + k * kPair) * kDV + 4 * lane);
+      l = fmaf(ml.y, f, l);
+      o[0] = fmaf(x.x, f, o[0]);
+      o[1] = fmaf(x.y, f, o[1]);
+      o[2] = fmaf(x.z, f, o[2]);
+      o[3] = fmaf(x.w, f, o[3]);
+    }
+    const float inv = 1.f / l;
+    *reinterpret_cast<uint2*>(p.out + ((int64_t)(qt.x + q) * p.H + h) * kDV + 4 * lane) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  }
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -941,12 +1047,14 @@ bool map2(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint6
 
 }  // namespace
 
-size_t prefill_workspace(const tv_prefill_args* a) { return layout(a).total; }
+size_t prefill_workspace(const tv_prefill_args* a, int sm_count) {
+  return layout(a, sm_count).total;
+}
 
 cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cudaStream_t st) {
   cudaError_t e = setup();
   if (e != cudaSuccess) return e;
-  const Layout l = layout(a);
+  const Layout l = layout(a, sm_count);
   char* base = (char*)ws;
   int32_t* counts = (int32_t*)base;
   int4* q_tiles = (int4*)(base + l.q_tiles);
@@ -954,7 +1062,7 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   const uint64_t H = a->H, T = a->T, cap = (uint64_t)l.cap;
 
   PlanArgs pa{a->q_start, a->prefix_len, a->B,    a->T,    a->max_q_len, a->max_kv_len,
-              (int)l.max_q, (int)l.max_k, counts, q_tiles, k_tiles,      a->status};
+              (int)l.max_q, (int)l.max_k, a->H, l.cut ? sm_count : 0, counts, q_tiles, k_tiles, a->status};
   plan_kernel<<<1, 1024, 0, st>>>(pa);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -992,7 +1100,8 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   xa.KR = (__nv_bfloat16*)(base + l.kr);
   xa.status = a->status;
   AttendArgs aa{counts, q_tiles, a->H, (float)((double)a->scale * 1.4426950408889634),
-                (__nv_bfloat16*)a->out, a->status};
+                (__nv_bfloat16*)a->out, (float*)(base + l.part_o), (float*)(base + l.part_ml),
+                a->status};
 
   // each kernel's set-up runs beside the one before it (programmatic dependent launch)
   cudaLaunchConfig_t cfg = {};
@@ -1007,10 +1116,15 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   cfg.dynamicSmemBytes = kExpSmem;
   e = cudaLaunchKernelEx(&cfg, expand_kernel, xa, m_c, m_w);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(l.max_q * a->H, sm_count));
+  cfg.gridDim = dim3((unsigned)(l.cut ? sm_count : std::min<int64_t>(l.max_q * a->H, sm_count)));
   cfg.blockDim = dim3(kAttThreads);
   cfg.dynamicSmemBytes = kAttSmem;
-  return cudaLaunchKernelEx(&cfg, attend_kernel, aa, m_q, m_qr, m_k, m_v, m_kr);
+  e = cudaLaunchKernelEx(&cfg, attend_kernel, aa, m_q, m_qr, m_k, m_v, m_kr);
+  if (e != cudaSuccess || !l.cut) return e;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(l.max_q * a->H * (kPair / 8), 4 * sm_count));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel, aa);
 }
 
 }  // namespace tv

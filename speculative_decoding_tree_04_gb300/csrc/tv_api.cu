@@ -533,7 +533,7 @@ static int check_prefill(const tv_prefill_args* a) {
 size_t tv_prefill_attn_workspace_size(const tv_prefill_args* a) {
   g_last_error.clear();
   if (check_prefill(a) != TV_OK || a->B == 0 || a->T == 0) return 0;
-  return tv::prefill_workspace(a);
+  return tv::prefill_workspace(a, sm_count());
 }
 
 int tv_prefill_attn(const tv_prefill_args* a, void* workspace, size_t ws_bytes, void* stream) {
@@ -541,7 +541,7 @@ int tv_prefill_attn(const tv_prefill_args* a, void* workspace, size_t ws_bytes, 
   const int rc = check_prefill(a);
   if (rc != TV_OK) return rc;
   if (a->B == 0 || a->T == 0) return TV_OK;
-  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < tv::prefill_workspace(a))
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < tv::prefill_workspace(a, sm_count()))
     return fail(TV_ERR_WORKSPACE, "tv_prefill_attn: workspace missing, misaligned or smaller than "
                                   "tv_prefill_attn_workspace_size()%s");
   cudaError_t e = tv::launch_prefill(a, workspace, sm_count(), (cudaStream_t)stream);

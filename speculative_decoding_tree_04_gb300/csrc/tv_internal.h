@@ -126,7 +126,7 @@ cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_
                               int32_t* status, cudaStream_t st);
 
 // Expanded-form attention of prompts (k_prefill.cu).
-size_t prefill_workspace(const tv_prefill_args* a);
+size_t prefill_workspace(const tv_prefill_args* a, int sm_count);
 cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cudaStream_t st);
 
 // Set the thread-local text returned by tv_last_error() (defined in tv_api.cu).

@@ -171,6 +171,22 @@ def test_long_prompt_sampled_rows():
         close(one, out, 0)
 
 
+@pytest.mark.parametrize("H", [1, 2, 5])
+@pytest.mark.parametrize("prefix", [1100, 5000])
+def test_few_items_are_cut_along_the_keys(H, prefix):
+    """A batch that leaves SMs idle: up to 38 pieces of an item, some of a short sequence
+    empty, some beginning at the diagonal with all their keys hidden from the first rows."""
+    check(make(19 + H, H, [256, 200, 1, 129, 300], [prefix, 100, 0, 200, 900], DL=64))
+
+
+def test_cut_items_rescale_and_repeat():
+    s = make(21, 2, [140], [2500], DL=64, q_scale=8.0)
+    ramp = torch.linspace(0.1, 2, 2640)[:, None]
+    s["c_kv"][s["rows"][0]] = (s["c_kv"][s["rows"][0]].float() * ramp).bfloat16()
+    out = check(s, rms=False)
+    assert np.array_equal(run(s), out)
+
+
 def test_sharp_softmax():
     s = make(6, 2, [300], [100], DL=128, q_scale=12.0)
     check(s, rms=False)
