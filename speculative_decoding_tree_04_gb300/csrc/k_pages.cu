@@ -88,12 +88,12 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* part) {
 static_assert(kWarps == 32, "one part per lane");
 
 // The same, with the sum of the threads before this one.
-__device__ __forceinline__ int64_t block_scan(int v, int64_t* part, int64_t* total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int up_to = v;
+  int64_t up_to = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int below = __shfl_up_sync(0xffffffffu, up_to, o);
+    const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
     if (lane >= o) up_to += below;
   }
   __syncthreads();
@@ -247,7 +247,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
   const int fresh_k = max(w.n, w.first);  // the first page index that the row does not hold
   const int news = w.active ? max(0, w.need - fresh_k) : 0;
   int64_t need_here, news_here;
-  const int64_t need_before = block_scan(swaps + news, s_part, &need_here);
+  const int64_t need_before = block_scan((int64_t)swaps + news, s_part, &need_here);
   const int64_t news_before = block_scan(news, s_part, &news_here);
   post(s_need, need_here);
   cluster_sync();

@@ -131,6 +131,19 @@ def test_pages_run_out_and_nothing_changes():
     b.reserve([0, 12, 0], [0, 28, 0])
 
 
+def test_more_pages_asked_for_than_32_bits_count():
+    rows, most = 40, 1 << 26
+    table = torch.empty((rows, most), dtype=torch.int32, device="cuda")
+    n, ref = Both.dev([0] * rows), Both.dev([0] * 100)
+    pool = tv.make_page_pool(ref, table, n, 16)
+    copies = torch.zeros((rows, 3), dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tv.pages_reserve(pool, Both.dev([0] * rows), Both.dev([1 << 30] * rows), copies, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == tv.TV_ERR_NO_PAGES
+    assert int(n.sum()) == 0 and int(ref.sum()) == 0
+
+
 @pytest.mark.parametrize("what", ["too_many", "length", "negative", "page", "low_page", "free",
                                   "n_pages"])
 def test_reserve_refuses_bad_rows_whole(what):
@@ -274,4 +287,21 @@ def test_captured_step_replays():
         assert torch.equal(t, e)
     b.m.fork([-1, 0, 0, 0], [0, 45, 45, 45])
     assert np.array_equal(b.m.reserve([45] * 4, [53] * 4), b.copies.cpu().numpy())
+    b.same()
+
+
+def test_capture_on_a_stream_given_explicitly_keeps_its_own_workspace():
+    b = Both(3, 4, 20, 16)
+    length, new = b.dev([0] * 3), b.dev([20, 0, 5])
+    side = torch.cuda.Stream()
+    tv.pages_reserve(b.pool, length, length, b.copies, stream=side)
+    torch.cuda.synchronize()
+    kept = dict(tv._ws_cache)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tv.pages_reserve(b.pool, length, new, b.copies, status=b.status,
+                         stream=torch.cuda.current_stream())
+    assert tv._ws_cache.keys() == kept.keys()
+    g.replay()
+    b.m.reserve([0] * 3, [20, 0, 5])
     b.same()
