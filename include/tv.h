@@ -456,7 +456,8 @@ typedef struct {
 } tv_sample_args;
 
 /* Returns TV_ERR_UNSUPPORTED for Q > 64 or vocab > 2^18, TV_ERR_INVALID_ARG for bad sizes,
- * strides, modes or pointers (draft_rows < Q with TV_DRAFT_BY_NODE among them). */
+ * strides, modes or pointers (draft_rows < Q with TV_DRAFT_BY_NODE, and outputs that share
+ * memory with inputs or each other, among them). */
 int tv_tree_sample(const tv_sample_args* a, void* stream);
 
 /*

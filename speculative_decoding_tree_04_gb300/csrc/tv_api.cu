@@ -350,6 +350,12 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
   return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_compact_kv");
 }
 
+// Whether two arrays of the given bytes share memory (a null one does not).
+static bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
 int tv_tree_sample(const tv_sample_args* a, void* stream) {
   g_last_error.clear();
   if (!a) return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: args is NULL%s");
@@ -381,6 +387,26 @@ int tv_tree_sample(const tv_sample_args* a, void* stream) {
   const uintptr_t es = a->logits_dt == TV_BF16 ? 2 : 4;
   if ((uintptr_t)a->logits % es)
     return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: logits not aligned to its element size%s");
+  // the CTAs of a sequence read the inputs each for itself: an output among them would have
+  // them disagree
+  const int64_t n = 4ll * a->B, nq = n * a->Q;
+  const int64_t nl = (((int64_t)a->B * a->Q - 1) * a->logits_row_stride + a->vocab) * (int64_t)es;
+  const int64_t nd =
+      4 * (((int64_t)a->B * a->draft_rows - 1) * a->draft_row_stride + a->vocab);
+  const struct {
+    const void* p;
+    int64_t n;
+  } outs[3] = {{a->accept_len, n}, {a->path, nq}, {a->new_tokens, nq}},
+    ins[6] = {{a->parent, nq},      {a->tokens, nq},  {a->uniforms, nq},
+              {a->temperature, n}, {a->logits, nl}, {a->draft_probs, nd}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 6; ++i)
+      if (overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n))
+        return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: an output overlaps an input%s");
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n))
+        return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: two outputs overlap%s");
+  }
   cudaError_t e = tv::launch_tree_sample(a, sm_count(), (cudaStream_t)stream);
   return e == cudaSuccess ? TV_OK : cuda_fail(e, "tv_tree_sample");
 }

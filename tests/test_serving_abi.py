@@ -14,7 +14,8 @@ def sample_args(**kw):
     a.struct_size = ctypes.sizeof(tv.SampleArgs)
     a.B, a.Q, a.vocab = 2, 9, 1000
     a.logits, a.logits_dt, a.logits_row_stride = FAKE, tv.TV_F32, 1000
-    a.parent = a.tokens = a.uniforms = a.accept_len = a.path = a.new_tokens = FAKE
+    a.parent, a.tokens, a.uniforms = FAKE + (1 << 20), FAKE + (2 << 20), FAKE + (3 << 20)
+    a.accept_len, a.path, a.new_tokens = FAKE + (4 << 20), FAKE + (5 << 20), FAKE + (6 << 20)
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -40,6 +41,13 @@ def sample_args(**kw):
     (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=8, draft_mode=1),
      tv.TV_ERR_INVALID_ARG),
     (dict(draft_probs=FAKE + 2, draft_row_stride=1000, draft_rows=9), tv.TV_ERR_INVALID_ARG),
+    (dict(new_tokens=FAKE + (2 << 20)), tv.TV_ERR_INVALID_ARG),        # in place over tokens
+    (dict(path=FAKE + (1 << 20) + 68), tv.TV_ERR_INVALID_ARG),         # parent's last entry
+    (dict(accept_len=FAKE + (5 << 20)), tv.TV_ERR_INVALID_ARG),        # and path
+    (dict(temperature=FAKE + (4 << 20) + 4), tv.TV_ERR_INVALID_ARG),
+    (dict(new_tokens=FAKE + 4 * (17 * 1000 + 999)), tv.TV_ERR_INVALID_ARG),  # the last logit
+    (dict(draft_probs=FAKE + (5 << 20) - 4 * 999, draft_row_stride=1000, draft_rows=9),
+     tv.TV_ERR_INVALID_ARG),
     (dict(B=0, logits=None), tv.TV_OK),
 ])
 def test_tree_sample_arguments(tvlib, kw, code):
