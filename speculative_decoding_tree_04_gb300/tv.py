@@ -509,25 +509,40 @@ def _call(dev, name, *args):
         _check(rc, name)
 
 
-def _scratch(kind, dev, handle, need):
-    """Workspace of `need` bytes for one call on the stream: one buffer per device, stream
+def _scratch(kind, dev, stream, handle, size_of, x):
+    """Workspace of size_of(x) bytes for one call on the stream: one buffer per device, stream
     and kind of call, grown when needed.  During a capture the buffer is the graph's own:
     graphs that share one could replay at the same time, and it must outlive them."""
+    if stream is not None or torch._C._cuda_getDevice() != dev:
+        # both the size and the allocation are the device's and the stream's: a block that the
+        # current stream has just given up may still be read by work queued there
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return _scratch(kind, dev, None, handle, size_of, x)
+    need = max(1, size_of(x))
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
     key = (kind, dev, handle)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
-        # a smaller one that it replaces may still be in use on that stream
-        ws.record_stream(torch.cuda.ExternalStream(handle, device=f"cuda:{dev}"))
-        _ws_cache[key] = ws
+        ws = _ws_cache[key] = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
     return ws
 
 
 def _i32(name, t, shape):
     if t.shape != shape or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 of shape {tuple(shape)}")
+
+
+def _row_stride(name, t):
+    """Elements between the rows of a [B, rows, V] tensor whose rows lie evenly spaced."""
+    B, n, V = t.shape
+    if t.numel() and t.stride(2) != 1 and V > 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if n == 1:
+        return t.stride(0) if B > 1 else V
+    if B > 1 and t.stride(0) != n * t.stride(1):
+        raise ValueError(f"{name} rows must be evenly spaced over its first two dimensions")
+    return t.stride(1)
 
 
 def _status_arg(status):
@@ -550,8 +565,7 @@ def tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
     dev = _on_device(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
                      temperature, draft_probs, status)
     B, Q, V = logits.shape
-    if B and (logits.stride(2) != 1 or (B > 1 and logits.stride(0) != Q * logits.stride(1))):
-        raise ValueError("logits rows must be contiguous and uniformly strided over (B, Q)")
+    l_stride = _row_stride("logits", logits)
     for name, t, shape in (("parent", parent, (B, Q)), ("tokens", tokens, (B, Q)),
                            ("accept_len", accept_len, (B,)), ("path", path, (B, Q)),
                            ("new_tokens", new_tokens, (B, Q))):
@@ -565,12 +579,8 @@ def tree_sample(logits, parent, tokens, uniforms, accept_len, path, new_tokens,
         d = draft_probs
         if d.dtype is not torch.float32 or d.dim() != 3 or d.shape[0] != B or d.shape[2] != V:
             raise ValueError("draft_probs must be float32 [B, rows, V]")
-        p_rows = d.shape[1]
-        if B and (d.stride(2) != 1 or (B > 1 and d.stride(0) != p_rows * d.stride(1))):
-            raise ValueError("draft_probs rows must be contiguous and uniformly strided")
-        probs, p_stride = d.data_ptr(), d.stride(1) if p_rows > 1 or B > 1 else V
-    a = SampleArgs(ctypes.sizeof(SampleArgs), B, Q, V, logits.data_ptr(), _dt(logits),
-                   logits.stride(1) if Q > 1 or B > 1 else V,
+        probs, p_stride, p_rows = d.data_ptr(), _row_stride("draft_probs", d), d.shape[1]
+    a = SampleArgs(ctypes.sizeof(SampleArgs), B, Q, V, logits.data_ptr(), _dt(logits), l_stride,
                    None if temperature is None else temperature.data_ptr(),
                    parent.data_ptr(), tokens.data_ptr(), uniforms.data_ptr(), probs, p_stride,
                    p_rows, int(draft_mode), accept_len.data_ptr(), path.data_ptr(),
@@ -609,7 +619,7 @@ def _pool_call(name, pool, per_row, others, status, stream, workspace=None, scra
     handle = _raw_stream(dev, stream)
     if scratch:
         if workspace is None:
-            workspace = _scratch("pages", dev, handle, pages_workspace_size(pool))
+            workspace = _scratch("pages", dev, stream, handle, pages_workspace_size, pool)
         args += [workspace.data_ptr(), workspace.numel() * workspace.element_size()]
     _call(dev, name, ctypes.byref(pool), *args, handle)
 
@@ -710,6 +720,6 @@ def prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale
                      max_kv_len, total_kv, page_table, page_size, kv_stride_b, status)
     handle = _raw_stream(dev, stream)
     if workspace is None:
-        workspace = _scratch("prefill", dev, handle, max(1, prefill_workspace_size(a)))
+        workspace = _scratch("prefill", dev, stream, handle, prefill_workspace_size, a)
     _call(dev, "tv_prefill_attn", ctypes.byref(a), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), handle)

@@ -271,6 +271,21 @@ def test_strided_and_unaligned_rows():
     assert st == 0 and all(np.array_equal(g, v) for g, v in zip(got, e))
 
 
+def test_first_nodes_of_longer_rows():
+    """One node per sequence, out of a tensor with more: rows a whole sequence apart."""
+    s = make(23, 4, 6, 333, draft="depth")
+    one = {k: v[:, :1] if isinstance(v, torch.Tensor) and v.dim() > 1 else v
+           for k, v in s.items()}
+    e = expect({k: v.contiguous() if isinstance(v, torch.Tensor) else v for k, v in one.items()})
+    dev = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+    out = outputs(4, 1)
+    tv.tree_sample(dev["logits"][:, :1], dev["parent"][:, :1].contiguous(),
+                   dev["tokens"][:, :1].contiguous(), dev["uniforms"][:, :1].contiguous(), *out,
+                   temperature=dev["temperature"], draft_probs=dev["draft"][:, :1])
+    torch.cuda.synchronize()
+    assert all(np.array_equal(t.cpu().numpy(), x) for t, x in zip(out, e))
+
+
 def test_captured_and_replayed_with_new_inputs():
     a, b = make(20, 4, 9, 3000, draft="depth"), make(21, 4, 9, 3000, draft="depth")
     dev = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in a.items()}
