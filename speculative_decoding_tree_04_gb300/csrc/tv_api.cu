@@ -369,12 +369,13 @@ int tv_tree_sample(const tv_sample_args* a, void* stream) {
   if (a->B >= (1 << 24)) return fail(TV_ERR_UNSUPPORTED, "tv_tree_sample: B must be below 2^24%s");
   if (!(a->logits_dt == TV_F32 || a->logits_dt == TV_BF16))
     return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: logits must be F32 or BF16%s");
-  if (a->logits_row_stride < a->vocab)
-    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: row stride smaller than the row%s");
+  if (a->logits_row_stride < a->vocab || a->logits_row_stride >= (1ll << 31))
+    return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: row stride below the row's size or past 2^31%s");
   if (a->draft_probs) {
     if (a->draft_mode != TV_DRAFT_BY_DEPTH && a->draft_mode != TV_DRAFT_BY_NODE)
       return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: bad draft_mode%s");
-    if (a->draft_row_stride < a->vocab || a->draft_rows < 1 ||
+    if (a->draft_row_stride < a->vocab || a->draft_row_stride >= (1ll << 31) ||
+        a->draft_rows < 1 || a->draft_rows > (1 << 20) ||
         (a->draft_mode == TV_DRAFT_BY_NODE && a->draft_rows < a->Q))
       return fail(TV_ERR_INVALID_ARG, "tv_tree_sample: bad draft_rows or draft_row_stride%s");
     if ((uintptr_t)a->draft_probs % 4)
@@ -550,8 +551,8 @@ static int check_prefill(const tv_prefill_args* a) {
       return fail(TV_ERR_UNSUPPORTED, "tv_prefill_attn: needs 64-token pages%s");
     if (a->cache.max_pages <= 0 || a->max_kv_len > 64ll * a->cache.max_pages)
       return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: max_kv_len exceeds max_pages * 64%s");
-  } else if (a->cache.kv_stride_b < a->max_kv_len) {
-    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: kv_stride_b < max_kv_len%s");
+  } else if (a->cache.kv_stride_b < a->max_kv_len || a->cache.kv_stride_b >= (1ll << 31)) {
+    return fail(TV_ERR_INVALID_ARG, "tv_prefill_attn: kv_stride_b < max_kv_len or past 2^31%s");
   }
   return TV_OK;
 }

@@ -30,12 +30,14 @@ def sample_args(**kw):
     (dict(vocab=(1 << 18) + 1, logits_row_stride=1 << 19), tv.TV_ERR_UNSUPPORTED),
     (dict(logits_dt=2), tv.TV_ERR_INVALID_ARG),
     (dict(logits_row_stride=999), tv.TV_ERR_INVALID_ARG),
+    (dict(logits_row_stride=1 << 60), tv.TV_ERR_INVALID_ARG),
     (dict(logits=None), tv.TV_ERR_INVALID_ARG),
     (dict(logits=FAKE + 2), tv.TV_ERR_INVALID_ARG),
     (dict(uniforms=None), tv.TV_ERR_INVALID_ARG),
     (dict(path=None), tv.TV_ERR_INVALID_ARG),
     (dict(draft_probs=FAKE, draft_row_stride=999, draft_rows=9), tv.TV_ERR_INVALID_ARG),
     (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=0), tv.TV_ERR_INVALID_ARG),
+    (dict(draft_probs=FAKE, draft_row_stride=1 << 60, draft_rows=9), tv.TV_ERR_INVALID_ARG),
     (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=9, draft_mode=2),
      tv.TV_ERR_INVALID_ARG),
     (dict(draft_probs=FAKE, draft_row_stride=1000, draft_rows=8, draft_mode=1),
@@ -163,6 +165,7 @@ def prefill_args(**kw):
     (dict(cache=tv.CacheLayout(FAKE, 32, 20, 0, 6400)), tv.TV_ERR_UNSUPPORTED),
     (dict(cache=tv.CacheLayout(FAKE, 64, 10, 0, 0)), tv.TV_ERR_INVALID_ARG),
     (dict(cache=tv.CacheLayout(None, 64, 0, 639, 6400)), tv.TV_ERR_INVALID_ARG),
+    (dict(cache=tv.CacheLayout(None, 64, 0, 1 << 62, 6400)), tv.TV_ERR_INVALID_ARG),
 ])
 def test_prefill_arguments(tvlib, kw, code):
     lib, a = tv.load(), prefill_args(**kw)
