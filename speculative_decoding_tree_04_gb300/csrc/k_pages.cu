@@ -11,6 +11,11 @@
 // launch, each CTA scanning its slice of the counts (a run of consecutive pages per thread,
 // whose free ones it keeps as bits), with sums exchanged through distributed shared memory.
 // The copies are the bytes: 64 keys of 1152 bytes per page and layer.
+//
+// Measured.  A cycle that forks each of 64 rows into 7 more, reserves and copies the written
+// pages and releases: 45 us, overlapped by programmatic launches (55 without).  Alone, reserve
+// takes 13.5 (23 with a CTA's rows one after another instead of a thread each), fork 5.5,
+// release 7.5 and the copies 27.  Compaction of 1.16 GB: plan 10, tables 4, copies 172.
 #include <algorithm>
 #include <climits>
 
@@ -192,6 +197,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
   static_assert(kRows <= kThreads, "a thread per row");
   __shared__ int64_t s_flags[kCluster], s_free[kCluster], s_need[kCluster], s_part[kWarps];
   __shared__ int s_new[kRows], s_at[kRows], s_k[kRows];  // of the pages behind those held
+  cluster_arrive();  // a CTA's shared memory may be written once it is known to have started
   begin();
   const int tid = threadIdx.x;
   const int per_r = (P.rows + kCluster - 1) / kCluster;
@@ -220,6 +226,7 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
   int64_t free_here;
   const int64_t free_before = block_scan(mark(run, is_free), s_part, &free_here);
   const int64_t flags = __syncthreads_or(bad) ? 1ll << 32 : 0;
+  cluster_wait();
   post(s_flags, flags + (__syncthreads_or(shared) ? 1 : 0));
   post(s_free, free_here);
   cluster_sync();
@@ -363,11 +370,13 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads)
     compact_plan_kernel(tv_page_pool P, Workspace W, int32_t* __restrict__ moves,
                         int32_t* __restrict__ n_moves) {
   __shared__ int64_t s_used[kCluster], s_hole[kCluster], s_move[kCluster], s_part[kWarps];
+  cluster_arrive();  // (as above)
   begin();
   const int tid = threadIdx.x, rank = (int)cluster_rank();
   Run run = run_of(P.num_pages);
   const auto is_used = [&](int p) { return ld(P.refcount + p) > 0; };
   const int64_t here = block_sum(mark(run, is_used), s_part);
+  cluster_wait();
   post(s_used, here);
   cluster_sync();
   const int used = (int)collect(s_used).total;
