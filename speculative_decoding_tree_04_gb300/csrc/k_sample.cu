@@ -43,8 +43,8 @@
 // distributed shared memory, and every CTA takes the same decisions from the same numbers.
 //
 // Measured (calls in a loop, inputs beyond L2).  One sequence of 9 nodes, 32000 bf16 logits:
-// 9.2 us, 7.9 in a graph; 32 x 33 nodes, 163840 floats: 34-42 us; with the drafter's rows, 8 x 9
-// nodes, 163840 bf16: 25-32 us, and 64 x 17 nodes, 50257 floats: 51-62 us.  The bytes alone
+// 9-13 us, 7.9 in a graph; 32 x 33 nodes, 163840 floats: 34-42 us; with the drafter's rows, 8 x 9
+// nodes, 163840 bf16: 25-32 us, and 64 x 17 nodes, 50257 floats: 47-62 us.  The bytes alone
 // would take below 0.1, 6.2, 1.5 and 5.7 us: what bounds it is the walk, one visited row after
 // another, and the sequences with a draw or test that needs the exact sums (about 25000
 // clocks).  With exact sums for every row: 22, 184, 65 and 188 us.
