@@ -52,16 +52,17 @@ constexpr float kRescale = 8.0f;                // log2: see attend_kernel
 constexpr float kMaxV = 65504.f;                // the largest fp16
 
 // ---- workspace --------------------------------------------------------------------------
-// counts {query tiles, key tiles, pieces of an item}; query tiles {first row of q, rows left,
-// position of the first row, first expanded key}; key tiles {sequence, first key, expanded row,
-// rows left}; then K [H][cap][128] in bf16, V [H][cap][128] in fp16 and the rope keys [cap][64]; and,
+// counts {query tiles, key tiles, pieces, whether any tile is cut}; query tiles {first row of
+// q, rows left, position of the first row, first expanded key}; key tiles {sequence, first key,
+// expanded row, rows left}; where items may be cut, pieces {query tile, number, of how many}
+// and each query tile's {first piece, pieces}; then K [H][cap][128] in bf16, V [H][cap][128] in fp16 and the rope keys [cap][64]; and,
 // where items may be cut, a piece's unnormalised output [256][128] and its rows' maximum and
 // sum [256][2], in floats, for each SM.
 struct Layout {
   int64_t cap;               // expanded key rows
   int64_t max_q, max_k;      // tiles at most
   bool cut;                  // few items: their keys may be cut into pieces
-  size_t q_tiles, k_tiles, k, v, kr, part_o, part_ml, total;
+  size_t q_tiles, k_tiles, pieces, tile_pieces, k, v, kr, part_o, part_ml, total;
 };
 size_t align1k(size_t n) { return (n + 1023) / 1024 * 1024; }
 Layout layout(const tv_prefill_args* a, int sm_count) {
@@ -74,13 +75,17 @@ Layout layout(const tv_prefill_args* a, int sm_count) {
   n += align1k((size_t)l.max_q * sizeof(int4));
   l.k_tiles = n;
   n += align1k((size_t)l.max_k * sizeof(int4));
+  l.cut = l.max_q * a->H < sm_count;
+  l.pieces = n;
+  if (l.cut) n += align1k((size_t)sm_count * sizeof(int4));
+  l.tile_pieces = n;
+  if (l.cut) n += align1k((size_t)sm_count * sizeof(int2));
   l.k = n;
   n += (size_t)l.cap * a->H * kDN * 2;
   l.v = n;
   n += (size_t)l.cap * a->H * kDV * 2;
   l.kr = n;
   n += (size_t)l.cap * kDR * 2;
-  l.cut = l.max_q * a->H < sm_count;
   l.part_o = n;
   if (l.cut) n += (size_t)sm_count * kPair * kDV * 4;
   l.part_ml = n;
@@ -98,11 +103,18 @@ struct PlanArgs {
   int32_t* counts;
   int4* q_tiles;
   int4* k_tiles;
+  int4* pieces;
+  int2* tile_pieces;
   int32_t* status;
 };
 
+// Key blocks that a query tile's rows see.
+__device__ __forceinline__ int blocks_of(int4 q_tile) {
+  return (q_tile.z + min(q_tile.y, kPair) + kBlock - 1) / kBlock;
+}
+
 __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
-  __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost, s_longest;
+  __shared__ int s_q[32], s_k[32], s_max[32], s_base_q, s_base_k, s_base_max, s_lost;
   __shared__ int s_weight[1024];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();  // the expansion may set itself up meanwhile
@@ -191,33 +203,64 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
   if (tid == 0) {
     p.counts[0] = total_q;
     p.counts[1] = total_k;
-    s_longest = 0;
+    if (!p.slots) {
+      p.counts[2] = total_q;
+      p.counts[3] = 0;
+    }
   }
   // longest sweeps first, so that the short ones fill the end (up to 1024 tiles)
-  __syncthreads();
-  for (int i = tid; p.slots && i < total_q; i += 1024) {
-    const int4 t = p.q_tiles[i];
-    atomicMax(&s_longest, (t.z + min(t.y, kPair) + kBlock - 1) / kBlock);
-  }
-  __syncthreads();
-  // pieces: one per SM, of at least four blocks in the longest item
-  if (tid == 0)
-    p.counts[2] = total_q > 0 && p.slots
-                      ? max(1, min(p.slots / (total_q * p.H), s_longest / 4))
-                      : 1;
   if (total_q > 1024) return;
   int4 mine = make_int4(0, 0, 0, 0);
+  __syncthreads();
   if (tid < total_q) {
     mine = p.q_tiles[tid];
     s_weight[tid] = mine.z + min(mine.y, kPair);
   }
   __syncthreads();
+  int rank = 0;
   if (tid < total_q) {
-    int rank = 0;
     const int w = s_weight[tid];
     for (int i = 0; i < total_q; ++i)
       rank += s_weight[i] > w || (s_weight[i] == w && i < tid);
     p.q_tiles[rank] = mine;
+  }
+  if (!p.slots) return;
+  // Few items (total_q * H < slots): the least length, of four blocks at least, at which all
+  // pieces have an SM each; then every tile in equal pieces of that length at most.  (The same
+  // number of pieces for every tile left the longest one's twice the mean: 4 chunks of 256
+  // queries after 2048 to 6000 keys, 16 heads: attend 62 us, 47 with this.)
+  __syncthreads();
+  if (tid < total_q) s_weight[rank] = blocks_of(mine);
+  __syncthreads();
+  if (warp > 0) return;
+  const int most = p.slots / p.H;
+  auto count = [&](int length) {
+    int n = 0;
+    for (int i = lane; i < total_q; i += 32) n += (s_weight[i] + length - 1) / length;
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  int lo = 4, hi = max(4, total_q > 0 ? s_weight[0] : 0);  // at hi, a piece per tile
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (count(mid) <= most) hi = mid;
+    else lo = mid + 1;
+  }
+  int first = 0;
+  for (int i0 = 0; i0 < total_q; i0 += 32) {
+    const int i = i0 + lane, n = i < total_q ? (s_weight[i] + hi - 1) / hi : 0;
+    int up_to = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(0xffffffffu, up_to, o);
+      if (lane >= o) up_to += below;
+    }
+    if (i < total_q) p.tile_pieces[i] = make_int2(first + up_to - n, n);
+    for (int k = 0; k < n; ++k) p.pieces[first + up_to - n + k] = make_int4(i, k, n, 0);
+    first += __shfl_sync(0xffffffffu, up_to, 31);
+  }
+  if (lane == 0) {
+    p.counts[2] = first;
+    p.counts[3] = first > total_q;
   }
 }
 
@@ -502,6 +545,8 @@ static_assert(kAttSmem <= 232448, "shared memory of an SM");
 struct AttendArgs {
   const int32_t* counts;
   const int4* q_tiles;
+  const int4* pieces;  // null: a piece per tile
+  const int2* tile_pieces;
   int32_t H;
   float scale_log2;
   __nv_bfloat16* out;
@@ -510,24 +555,31 @@ struct AttendArgs {
   int32_t* status;
 };
 
-// The r-th item of this CTA.  Items are listed longest first and dealt in rounds of
-// alternating direction; an item that is cut is as many items, one a CTA.
+// The r-th item of this CTA: a head of a query tile's piece.  Items are listed longest first
+// and dealt in rounds of alternating direction.
 struct Item {
   bool some;
   int slot;                       // its place in the list
+  int pieces;                     // of its query tile
   int h, row0, rows, pos0, key0, tiles;
   int j0, n0, n1;                 // first key block; blocks from there that a tile's rows see
 };
-__device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int pieces, int r) {
+__device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int r) {
   Item it;
   const int64_t i =
       (int64_t)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   it.some = i < total;
   if (!it.some) return it;
   it.slot = (int)i;
-  const int whole = it.slot / pieces, piece = it.slot - whole * pieces;
-  const int tile = whole / p.H;
-  it.h = whole - tile * p.H;
+  int tile = it.slot / p.H, piece = 0;
+  it.h = it.slot - tile * p.H;
+  it.pieces = 1;
+  if (p.pieces) {
+    const int4 e = p.pieces[tile];
+    tile = e.x;
+    piece = e.y;
+    it.pieces = e.z;
+  }
   const int4 qt = p.q_tiles[tile];
   it.row0 = qt.x;
   it.rows = min(qt.y, kPair);
@@ -535,8 +587,8 @@ __device__ __forceinline__ Item item_of(const AttendArgs& p, int total, int piec
   it.tiles = it.rows > kBlock ? 2 : 1;
   const int n0 = (it.pos0 + min(it.rows, kBlock) + kBlock - 1) / kBlock;
   const int n1 = it.tiles > 1 ? (it.pos0 + it.rows + kBlock - 1) / kBlock : 0;
-  const int n = max(n0, n1), j1 = (int)((int64_t)n * (piece + 1) / pieces);
-  it.j0 = (int)((int64_t)n * piece / pieces);
+  const int n = max(n0, n1), j1 = (int)((int64_t)n * (piece + 1) / it.pieces);
+  it.j0 = (int)((int64_t)n * piece / it.pieces);
   it.n0 = max(0, min(n0, j1) - it.j0);
   it.n1 = max(0, min(n1, j1) - it.j0);
   it.key0 = qt.w + it.j0 * kBlock;
@@ -610,7 +662,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const uint32_t tmem = sh.tmem;
   griddep_launch_dependents();
   griddep_wait();  // the plan and the expanded keys
-  const int pieces = p.counts[2], total = p.counts[0] * p.H * pieces;
+  const int total = p.counts[2] * p.H;
 
   if (warp == 0 && lane == 0) {
     fence_proxy_async_global();
@@ -621,9 +673,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     bool ok = true;
     int g = 0, items = 0, armed_k = 0, armed_v = 0;
     for (int r = 0; ok; ++r) {
-      const Item it = item_of(p, total, pieces, r);
+      const Item it = item_of(p, total, r);
       if (!it.some) break;
-      if (max(it.n0, it.n1) == 0) continue;  // (a piece of a short item: one item a CTA then)
       // the last block of scores of the item before frees the queries
       if (g > 0) ok = wait_for(sh.abort, &sh.k_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       if (!ok) break;
@@ -713,7 +764,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     };
     bool ok = tmem == 0;  // 512 of 512 columns: the addresses above are absolute
     for (int r = 0; ok; ++r) {
-      const Item it = item_of(p, total, pieces, r);
+      const Item it = item_of(p, total, r);
       if (!it.some) break;
       const int n0 = __reduce_max_sync(0xffffffffu, it.n0);
       const int n1 = __reduce_max_sync(0xffffffffu, it.n1);
@@ -796,12 +847,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     for (int r = 0; ok; ++r) {
       int nt, tile_first;  // every row of the tile sees the sweep's keys 0 .. tile_first
       {
-        const Item it = item_of(p, total, pieces, r);
+        const Item it = item_of(p, total, r);
         if (!it.some) break;
         nt = t ? it.n1 : it.n0;
         tile_first = it.pos0 + (t - it.j0) * kBlock;
         if (nt == 0) {
-          if (pieces > 1 && t < it.tiles && (lane & 3) == 0) {  // nothing of these rows here
+          if (it.pieces > 1 && t < it.tiles && (lane & 3) == 0) {  // nothing of these rows here
             float* ml = p.part_ml + ((int64_t)it.slot * kPair + t * kBlock + ra) * 2;
             ml[1] = ml[17] = 0.f;  // rows ra and ra + 8
           }
@@ -911,9 +962,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (!ok) break;
       ++oc;
       tc_fence_after();
-      const Item it = item_of(p, total, pieces, r);  // (again: not kept through the sweep)
+      const Item it = item_of(p, total, r);  // (again: not kept through the sweep)
       const int q = t * kBlock + ra;                 // rows q and q + 8 of the item
-      if (pieces > 1) {
+      if (it.pieces > 1) {
         const int64_t at = (int64_t)it.slot * kPair + q;
         if ((lane & 3) == 0) {
           *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(ma, la);
@@ -971,27 +1022,29 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // most, from L2.
 __global__ void __launch_bounds__(256) join_kernel(AttendArgs p) {
   griddep_wait();
-  const int pieces = p.counts[2];
-  if (pieces == 1) return;
+  if (!p.counts[3]) return;
   const int lane = threadIdx.x & 31;
   const int64_t units = (int64_t)p.counts[0] * p.H * kPair;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += 8 * gridDim.x) {
     const int whole = (int)(u / kPair), q = (int)(u % kPair);
     const int tile = whole / p.H, h = whole - tile * p.H;
     const int4 qt = p.q_tiles[tile];
-    if (q >= qt.y) continue;
-    const int64_t at = (int64_t)whole * pieces * kPair + q;  // piece k: + k * kPair
+    const int2 tp = p.tile_pieces[tile];
+    const int pieces = tp.y;
+    if (q >= qt.y || pieces == 1) continue;  // (a tile in one piece is written already)
+    const int64_t at = ((int64_t)tp.x * p.H + h) * kPair + q, next = (int64_t)p.H * kPair;
     float M = -INFINITY;
     for (int k = 0; k < pieces; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * kPair) * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * next) * 2);
       if (ml.y > 0.f) M = fmaxf(M, ml.x);
     }
     float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < pieces; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * kPair) * 2);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * next) * 2);
       if (!(ml.y > 0.f)) continue;  // no key of it is visible (its output may not exist)
       const float f = ex2(ml.x - M);
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (at + k * kPair) * kDV + 4 * lane);
+      const float4 x =
+          *reinterpret_cast<const float4*>(p.part_o + (at + k * next) * kDV + 4 * lane);
       l = fmaf(ml.y, f, l);
       o[0] = fmaf(x.x, f, o[0]);
       o[1] = fmaf(x.y, f, o[1]);
@@ -1075,7 +1128,7 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
 
   PlanArgs pa{a->q_start, a->prefix_len, a->B,    a->T,    a->max_q_len, a->max_kv_len,
               (int)l.max_q, (int)l.max_k, a->H, l.cut ? sm_count : 0, counts, q_tiles, k_tiles,
-              a->status};
+              (int4*)(base + l.pieces), (int2*)(base + l.tile_pieces), a->status};
   plan_kernel<<<1, 1024, 0, st>>>(pa);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1112,7 +1165,8 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   xa.V = (__half*)(base + l.v);
   xa.KR = (__nv_bfloat16*)(base + l.kr);
   xa.status = a->status;
-  AttendArgs aa{counts, q_tiles, a->H, (float)((double)a->scale * 1.4426950408889634),
+  AttendArgs aa{counts, q_tiles, l.cut ? (const int4*)(base + l.pieces) : nullptr,
+                (const int2*)(base + l.tile_pieces), a->H, (float)((double)a->scale * 1.4426950408889634),
                 (__nv_bfloat16*)a->out, (float*)(base + l.part_o), (float*)(base + l.part_ml),
                 a->status};
 

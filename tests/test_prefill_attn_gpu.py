@@ -179,6 +179,16 @@ def test_few_items_are_cut_along_the_keys(H, prefix):
     check(make(19 + H, H, [256, 200, 1, 129, 300], [prefix, 100, 0, 200, 900], DL=64))
 
 
+@pytest.mark.parametrize("H,lens,prefixes", [
+    (50, [130, 5], [1500, 3]),                     # one tile in two pieces, one written at once
+    (16, [256, 256, 256, 256], [6000, 3840, 2048, 511]),
+    (75, [129, 7], [700, 700]),                    # two pieces in all: nothing is cut
+])
+def test_cut_and_whole_tiles_side_by_side(H, lens, prefixes):
+    out = check(make(24, H, lens, prefixes, DL=64))
+    assert np.array_equal(run(make(24, H, lens, prefixes, DL=64)), out)
+
+
 def test_cut_items_rescale_and_repeat():
     s = make(21, 2, [140], [2500], DL=64, q_scale=8.0)
     ramp = torch.linspace(0.1, 2, 2640)[:, None]
