@@ -556,7 +556,9 @@ struct AttendArgs {
 };
 
 // The r-th item of this CTA: a head of a query tile's piece.  Items are listed longest first
-// and dealt in rounds of alternating direction.
+// and dealt in rounds of alternating direction.  (Dealt from a counter as CTAs become free, a
+// ragged batch's attend took 134 us instead of 136, but 4096 queries of 64 heads 265 instead of
+// 257.)
 struct Item {
   bool some;
   int slot;                       // its place in the list

@@ -44,7 +44,7 @@
 //
 // Measured (calls in a loop, inputs beyond L2).  One sequence of 9 nodes, 32000 bf16 logits:
 // 9-13 us, 7.9 in a graph; 32 x 33 nodes, 163840 floats: 34-42 us; with the drafter's rows, 8 x 9
-// nodes, 163840 bf16: 25-32 us, and 64 x 17 nodes, 50257 floats: 47-62 us.  The bytes alone
+// nodes, 163840 bf16: 25-35 us, and 64 x 17 nodes, 50257 floats: 47-66 us.  The bytes alone
 // would take below 0.1, 6.2, 1.5 and 5.7 us: what bounds it is the walk, one visited row after
 // another, and the sequences with a draw or test that needs the exact sums (about 25000
 // clocks).  With exact sums for every row: 22, 184, 65 and 188 us.
@@ -944,7 +944,8 @@ cudaError_t launch(const SampleParams& p, int C, int sm_count, cudaStream_t st) 
 }  // namespace
 
 // CTAs per sequence: at most 16, about 2048 vocabulary entries each at least, and no more than
-// four per SM in all.
+// four per SM in all.  (32 x 33 nodes of 163840 floats, and 64 x 17 of 50257 with the drafter's
+// rows: 36-40 and 52-54 us with four, 39-41 and 81-85 with three, 43-47 and 57-61 with two.)
 int sample_cluster(int B, int64_t V, int sm_count) {
   int C = kMaxCluster;
   while (C > 1 && ((int64_t)B * C > 4 * (int64_t)sm_count || V < 2048ll * C)) C /= 2;
