@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
         n = (int)(e - s);
         P = (int)pre;
         nq = (n + kPair - 1) / kPair;
-        nk = (P + n + kBlock - 1) / kBlock;
+        nk = (int)((pre + n + kBlock - 1) / kBlock);  // (of up to 2^31 - 1 keys)
       }
     }
     int cq = nq, ck = nk;  // inclusive sums within the warp
