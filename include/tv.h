@@ -196,12 +196,15 @@ typedef struct {
                                pieces (tensor cores: each 128-row tile's sweep) */
   int32_t paged_view;       /* tv_paged_view; TV_PAGED_AUTO normally */
   int32_t mask_mode;        /* tv_mask_mode; TV_MASK_TREE for tree verification */
-  int32_t overlap_prev;     /* 0 normally.  1: the work queued on the stream before this call
-                               writes none of prefix_len and the page table (as for
+  int32_t overlap_prev;     /* 0 normally.  1: the call queued on the stream just before this
+                               one writes none of prefix_len and the page table (as for
                                tv_verify_prologue, which writes q_pe, cache rows and anc);
                                the tensor-core path's preparation kernel (work schedule,
-                               per-step tensor maps) may then run while that work finishes.
-                               The attention itself still starts only after all of it. */
+                               per-step tensor maps) may then run while that call finishes.
+                               Calls before that one may write them (tv_pages_reserve, say,
+                               with tv_pages_copy between): this library's calls let it start
+                               only once the call before them has ended.  The attention itself
+                               still starts only after all of it. */
 } tv_attn_args;
 
 /* Bytes of workspace tv_verify_attn needs for these arguments (0 if none).  The size

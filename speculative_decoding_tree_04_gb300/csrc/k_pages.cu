@@ -32,10 +32,13 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 
 // Every kernel here is launched as a programmatic dependent of the one before it on the
-// stream, so that its launch overlaps that one, and waits for it before anything else.
+// stream, so that its launch overlaps that one, and waits for it before anything else.  It
+// lets the next kernel start only then: one that works before its own wait (an attention
+// call's preparation under overlap_prev, which reads the page table) overlaps this kernel
+// alone, and not the writers of the table before it.
 __device__ __forceinline__ void begin() {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
 }
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), int64_t grid, int block, cudaStream_t st,

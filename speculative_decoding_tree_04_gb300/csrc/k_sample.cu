@@ -442,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
   const int rank = C > 1 ? (int)cluster_rank() : 0;
   int32_t* path = p.path + (int64_t)b * Q;
   int32_t* emit = p.new_tokens + (int64_t)b * Q;
-  // (launched as a programmatic dependent of the kernel before it)
-  griddep_launch_dependents();
+  // (launched as a programmatic dependent of the kernel before it; the next one may start once
+  // that has ended, so that it overlaps this kernel alone)
   griddep_wait();
+  griddep_launch_dependents();
   // warp 0 holds the tree: node lane and node lane + 32
   int par[2] = {-2, -2}, tok[2] = {-1, -1};
   float uni[2] = {0.f, 0.f};

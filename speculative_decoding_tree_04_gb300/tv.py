@@ -360,7 +360,7 @@ def verify_attn(q_latent, q_pe, c_kv, k_pe, prefix_len, anc, out, lse, scale, ma
     """Tree-verify attention; out [B,Q,H,DL] and lse [B,Q,H] (float32) are written.
 
     ``workspace`` (a CUDA uint8 tensor) is allocated through torch and cached per device
-    when not given.  ``overlap_prev=1`` declares that the work queued before the call
+    when not given.  ``overlap_prev=1`` declares that the call queued just before this one
     writes neither prefix_len nor the page table (tv_attn_args.overlap_prev)."""
     a = attn_args(q_latent, q_pe, c_kv, k_pe, prefix_len, anc, out, lse, scale,
                   max_prefix_len, page_table, page_size, kv_stride_b, status, path, num_splits,

@@ -1,0 +1,122 @@
+"""GPU tests of the serving calls next to an attention call whose preparation may overlap the
+call before it (overlap_prev), and inside captured graphs.
+
+Each kernel of a pool or sampling call waits for the one before it and only then lets the next
+start, so the preparation overlaps the call just before it and nothing earlier."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_tree_04_gb300 import tv
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("tvlib")]
+
+B, Q, H, DL, DR, PS, MOST, V = 24, 9, 64, 512, 64, 64, 12, 900
+SCALE = 192 ** -0.5
+
+
+def i32(v):
+    return torch.from_numpy(np.ascontiguousarray(v, np.int32)).cuda()
+
+
+class Batch:
+    """Rows of one to ten pages over a pool with every cache row filled, and a causal attention
+    call over what the rows hold and the Q keys behind it."""
+
+    def __init__(self, seed):
+        r = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def randn(*shape, s=1.0):
+            return (torch.randn(shape, generator=g, device="cuda") * s).bfloat16()
+
+        # whole pages, so that the keys written next need a page that no table names yet
+        self.length = PS * r.integers(1, 11, B)
+        have = self.length // PS
+        num = int(have.sum()) + 5 * B + 20000     # (many counts to scan: reserve takes longer)
+        perm = r.permutation(num)
+        table, ref, at = np.full((B, MOST), -1), np.zeros(num), 0
+        for b in range(B):
+            table[b, :have[b]] = perm[at:at + have[b]]
+            ref[perm[at:at + have[b]]] = 1
+            at += have[b]
+        self.before = [i32(ref), i32(table), i32(have)]
+        self.ref, self.table, self.n = (t.clone() for t in self.before)
+        self.pool = tv.make_page_pool(self.ref, self.table, self.n, PS)
+        self.c_kv, self.k_pe = randn(num * PS, DL), randn(num * PS, DR)
+        self.ql, self.qr = randn(B, Q, H, DL, s=0.3), randn(B, Q, H, DR, s=0.3)
+        self.len, self.new = i32(self.length), i32(self.length + Q)
+        self.copies = torch.zeros((B, 3), dtype=torch.int32, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.anc = torch.full((B, Q), (1 << Q) - 1, dtype=torch.int64, device="cuda")
+        self.out = torch.zeros((B, Q, H, DL), device="cuda")
+        self.lse = torch.zeros((B, Q, H), device="cuda")
+
+    def restore(self):
+        for t, e in zip((self.ref, self.table, self.n), self.before):
+            t.copy_(e)
+        torch.cuda.synchronize()
+
+    def reserve(self):
+        tv.pages_reserve(self.pool, self.len, self.new, self.copies, status=self.status)
+
+    def copy(self):
+        tv.pages_copy(self.c_kv, self.k_pe, PS, self.copies, status=self.status)
+
+    def attend(self, overlap, prefix=None, workspace=None):
+        tv.verify_attn(self.ql, self.qr, self.c_kv, self.k_pe, self.len if prefix is None else prefix,
+                       self.anc, self.out, self.lse, SCALE, 10 * PS, page_table=self.table,
+                       status=self.status, overlap_prev=overlap, workspace=workspace,
+                       path=tv.PATH_TCGEN05)
+
+
+@pytest.fixture(scope="module")
+def batch():
+    return Batch(1)
+
+
+def test_reserve_then_copy_then_overlapped_attention(batch):
+    """The preparation may overlap the copy, not the reservation that wrote the tables."""
+    s = batch
+    s.restore()
+    s.reserve()
+    s.copy()
+    torch.cuda.synchronize()
+    s.attend(0)
+    torch.cuda.synchronize()
+    out, lse = s.out.clone(), s.lse.clone()
+    assert int(s.status.item()) == 0 and torch.isfinite(out).all()
+    for _ in range(20):
+        s.restore()
+        s.out.zero_()
+        s.reserve()
+        s.copy()
+        s.attend(1)
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0
+        assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
+
+
+def test_sampling_between_reserve_and_overlapped_attention(batch):
+    s = batch
+    s.restore()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    logits = torch.randn((B, Q, V), generator=g, device="cuda")
+    parent = i32(np.tile(np.arange(-1, Q - 1), (B, 1)))
+    tokens = torch.randint(0, V, (B, Q), generator=g, device="cuda", dtype=torch.int32)
+    uni = torch.rand((B, Q), generator=g, device="cuda")
+    acc, path, emit = (torch.empty(x, dtype=torch.int32, device="cuda")
+                       for x in ((B,), (B, Q), (B, Q)))
+    s.reserve()
+    torch.cuda.synchronize()
+    s.attend(0)
+    torch.cuda.synchronize()
+    out = s.out.clone()
+    for _ in range(10):
+        s.restore()
+        s.out.zero_()
+        s.reserve()
+        tv.tree_sample(logits, parent, tokens, uni, acc, path, emit, status=s.status)
+        s.attend(1)
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0 and torch.equal(s.out, out)
