@@ -662,7 +662,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  griddep_launch_dependents();
+  // Only the join may start beside this kernel.  Where none follows, the next kernel is another
+  // call's, and one that works before its own wait (an attention call's preparation under
+  // overlap_prev) may have been given the same workspace.
+  if (p.pieces) griddep_launch_dependents();
   griddep_wait();  // the plan and the expanded keys
   const int total = p.counts[2] * p.H;
 

@@ -120,3 +120,44 @@ def test_sampling_between_reserve_and_overlapped_attention(batch):
         s.attend(1)
         torch.cuda.synchronize()
         assert int(s.status.item()) == 0 and torch.equal(s.out, out)
+
+
+def test_prompts_and_overlapped_attention_share_a_workspace(batch):
+    """A workspace is free once the call's work on the stream is done: the next call's
+    preparation must not write to it while the prompts' attention still reads it."""
+    s = batch
+    s.restore()
+    s.reserve()
+    torch.cuda.synchronize()
+    T, H2 = 700, 64                                 # more items than SMs: no join at the end
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def randn(*shape, k=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * k).bfloat16()
+
+    q, qp, w = randn(T, H2, 128), randn(T, H2, 64), randn(H2, 256, DL, k=DL ** -0.5)
+    start, pre = i32([0, 300, 700]), i32([0, 0])
+    keys = randn(20 * PS, DL), randn(20 * PS, DR)
+    pages = i32(np.arange(24).reshape(2, 12) % 20)
+    out = torch.zeros((T, H2, 128), dtype=torch.bfloat16, device="cuda")
+    args = tv.prefill_args(q, qp, w, *keys, start, pre, out, SCALE, 400, 400, 700, pages)
+    need = max(tv.prefill_workspace_size(args),
+               tv.workspace_size(tv.attn_args(s.ql, s.qr, s.c_kv, s.k_pe, s.len, s.anc, s.out,
+                                              s.lse, SCALE, 10 * PS, s.table)))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def both(overlap):
+        tv.prefill_attn(q, qp, w, *keys, start, pre, out, SCALE, 400, 400, 700, page_table=pages,
+                        status=s.status, workspace=ws)
+        if not overlap:
+            torch.cuda.synchronize()
+        s.attend(overlap, workspace=ws)
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0
+        return out.clone(), s.out.clone()
+
+    want = both(0)
+    for _ in range(10):
+        out.zero_()
+        s.out.zero_()
+        assert all(torch.equal(a, b) for a, b in zip(both(1), want))
