@@ -1023,8 +1023,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 }
 
 // ---- join ---------------------------------------------------------------------------------
-// A warp per (item, query): the pieces' outputs weighted by 2^(m - M).  16 MB of partials at
-// most, from L2.
+// A warp per (item, query): the pieces' outputs weighted by 2^(m - M).  At most 128 KB of
+// partials for each SM (20 MB), from L2.
 __global__ void __launch_bounds__(256) join_kernel(AttendArgs p) {
   griddep_wait();
   if (!p.counts[3]) return;
@@ -1041,12 +1041,12 @@ __global__ void __launch_bounds__(256) join_kernel(AttendArgs p) {
     float M = -INFINITY;
     for (int k = 0; k < pieces; ++k) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * next) * 2);
-      if (ml.y > 0.f) M = fmaxf(M, ml.x);
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);
     }
     float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < pieces; ++k) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (at + k * next) * 2);
-      if (!(ml.y > 0.f)) continue;  // no key of it is visible (its output may not exist)
+      if (ml.y == 0.f) continue;  // nothing visible there (its output may not exist)
       const float f = ex2(ml.x - M);
       const float4 x =
           *reinterpret_cast<const float4*>(p.part_o + (at + k * next) * kDV + 4 * lane);

@@ -27,3 +27,36 @@ def test_a_prefix_at_the_end_of_the_integers(where):
     out = d["out"].double().cpu().numpy()
     done = 40 * where
     assert np.array_equal(out[:done], good[:done]) and (out[done:] == -77).all()
+
+
+def output(s):
+    d = base.device(s)
+    base.launch(s, d)
+    torch.cuda.synchronize()
+    return d["out"].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("H,lens,prefixes", [
+    (1, [200], [1500]),      # cut along the keys: a dozen pieces
+    (80, [200, 40], [600, 3]),  # whole items
+])
+def test_a_nan_reaches_the_rows_that_see_it_and_no_other(H, lens, prefixes):
+    """Cut or whole, a NaN score makes the row NaN; the other rows keep their bits."""
+    s = base.make(32, H, lens, prefixes, DL=64)
+    good = output(s)
+    q = s["q_nope"].clone()
+    s["q_nope"][7, 0, 3] = float("nan")
+    out = output(s)
+    assert np.isnan(out[7, 0]).all()
+    out[7, 0] = good[7, 0]
+    assert np.array_equal(out, good)
+    s["q_nope"] = q
+    for key in (0, 130, prefixes[0] + 50):      # a rope key: of the first piece, another, the last
+        k = s["k_pe"].clone()
+        s["k_pe"][s["rows"][0][key]] = float("nan")
+        out = output(s)
+        first = max(0, key - prefixes[0])        # the first query of the sequence that sees it
+        assert np.isnan(out[first:lens[0]]).all()
+        out[first:lens[0]] = good[first:lens[0]]
+        assert np.array_equal(out, good)
+        s["k_pe"] = k
