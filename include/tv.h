@@ -591,7 +591,8 @@ int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  * prompt's own rows included).  For the tensor cores expanded keys are rounded to bf16,
  * expanded values and the softmax weights to fp16 (so a value's magnitude must stay within
  * 65504: a larger one is clamped and reported); sums and statistics are 32-bit.  The inputs
- * must be finite.
+ * must be finite.  A score that is NaN makes the rows that see it NaN and no others; an expanded
+ * value that is NaN is reported.
  */
 typedef struct {
   uint32_t struct_size;      /* sizeof(tv_prefill_args): ABI check */
@@ -619,7 +620,7 @@ typedef struct {
                                 q_start is negative, above its end or below an earlier one
                                 (its rows are left as they were), or a page of
                                 it outside the cache (that page reads as zeros), or an expanded
-                                value past 65504. */
+                                value past 65504 or NaN. */
 } tv_prefill_args;
 
 /* Bytes of workspace (the expanded keys and values: about 512 * H + 128 bytes per key, and up

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         for (int k = 0; k < 16; ++k) {
           float a = __uint_as_float(x[2 * k]), b = __uint_as_float(x[2 * k + 1]);
           if (c >= kDN) {
-            big = fmax3(big, fabsf(a), fabsf(b));
+            big = abs_max3_nan(big, a, b);
             a = fminf(fmaxf(a, -kMaxV), kMaxV);
             b = fminf(fmaxf(b, -kMaxV), kMaxV);
           }
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
         st_global_32(dst, y);
         st_global_32((char*)dst + 32, y + 8);
       }
-      if (live && big > kMaxV) report(p.status, TV_ERR_BOUNDS);
+      if (live && !(big <= kMaxV)) report(p.status, TV_ERR_BOUNDS);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);

@@ -60,3 +60,17 @@ def test_a_nan_reaches_the_rows_that_see_it_and_no_other(H, lens, prefixes):
         out[first:lens[0]] = good[first:lens[0]]
         assert np.array_equal(out, good)
         s["k_pe"] = k
+
+
+def test_values_that_are_nan_are_reported():
+    """From the weights: the scores do not show it.  From a key's row: they do as well."""
+    s = base.make(33, 2, [90], [40], DL=64)
+    good = output(s)
+    w = s["w_kv"].clone()
+    s["w_kv"][1, 128 + 5, 7] = float("nan")
+    out = base.run(s, tv.TV_ERR_BOUNDS)
+    assert np.array_equal(out[:, 0], good[:, 0])
+    s["w_kv"] = w
+    s["c_kv"][s["rows"][0][50], 3] = float("nan")
+    out = base.run(s, tv.TV_ERR_BOUNDS)
+    assert np.array_equal(out[:10], good[:10]) and np.isnan(out[10:]).all()
