@@ -590,7 +590,8 @@ int tv_pages_copy(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  * q_nope, q_pe and out.  Its keys 0 .. prefix_len[b] + q_len - 1 are all in the cache (the
  * prompt's own rows included).  For the tensor cores expanded keys are rounded to bf16,
  * expanded values and the softmax weights to fp16 (so a value's magnitude must stay within
- * 65504: a larger one is clamped and reported); sums and statistics are 32-bit.  The inputs
+ * 65504: a larger one is clamped and reported; a weight is off by at most 2^-11 of itself or
+ * 2^-32 of its row's largest, whichever is more); sums and statistics are 32-bit.  The inputs
  * must be finite.  A score that is NaN makes the rows that see it NaN and no others; an expanded
  * value that is NaN is reported.
  */

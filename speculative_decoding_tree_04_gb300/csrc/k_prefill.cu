@@ -48,7 +48,7 @@ constexpr int kBlock = 128;                     // keys per block, queries per t
 constexpr int kPair = 2 * kBlock;               // queries per CTA
 constexpr int kChunk = kBlock * 128;            // 128 rows of 64 bf16: 16 KB
 constexpr long long kDeadline = 4000000000ll;   // clocks of a wait: about 2 s
-constexpr float kRescale = 8.0f;                // log2: see attend_kernel
+constexpr float kLift = 7.0f, kRescale = 15.0f;  // log2: see attend_kernel
 constexpr float kMaxV = 65504.f;                // the largest fp16
 
 // ---- workspace --------------------------------------------------------------------------
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           continue;
         }
       }
-      float ma = 0.f, mb = 0.f;                     // running maxima (of scores times c)
+      float ma = 0.f, mb = 0.f;                     // 2^ma is one unit of a row's weights
       float la = 0.f, lb = 0.f;                     // sums over this thread's columns
       for (int j = 0; j < nt; ++j, ++sc) {
         ok = __all_sync(0xffffffffu, wait_for(sh.abort, &sh.s_full[t], sc & 1));
@@ -898,14 +898,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
         xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2)) * c;
         xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2)) * c;
-        // The maximum only moves when a block exceeds it by 2^8: weights stay below 2^8 and
-        // the accumulator is rescaled rarely.  (A piece's first block may hide all its keys
-        // from a row: the maximum is -inf then, and taken as 0 for the weights, all zero.)
+        // Weights are 2^(x - m) with m a maximum's 2^-7, so that the largest is 2^7 or more and
+        // those below fp16's normal range are held to 2^-32 of it (with m the maximum itself
+        // they vanished below 2^-25).  m only moves when a block's weights would exceed 2^15:
+        // fp16 holds them, and the accumulator is rescaled rarely.  (A piece's first block may
+        // hide all its keys from a row: m is -inf then, and taken as 0 for the weights, all
+        // zero.)
         if (j == 0) {
-          ma = xa;
-          mb = xb;
+          ma = xa - kLift;
+          mb = xb - kLift;
         } else if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
-          const float na = xa > ma + kRescale ? xa : ma, nb = xb > mb + kRescale ? xb : mb;
+          const float na = xa > ma + kRescale ? xa - kLift : ma;
+          const float nb = xb > mb + kRescale ? xb - kLift : mb;
           const float fa = na == ma ? 1.f : ex2(ma - na), fb = nb == mb ? 1.f : ex2(mb - nb);
           ma = na;
           mb = nb;
@@ -928,7 +932,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         uint64_t l2a = 0, l2b = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[16];  // V's type; weights stay below 2^8
+          uint32_t pk[16];  // V's type
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t* x = s + 32 * half + 4 * i;

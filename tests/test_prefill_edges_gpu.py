@@ -74,3 +74,47 @@ def test_values_that_are_nan_are_reported():
     s["c_kv"][s["rows"][0][50], 3] = float("nan")
     out = base.run(s, tv.TV_ERR_BOUNDS)
     assert np.array_equal(out[:10], good[:10]) and np.isnan(out[10:]).all()
+
+
+def exact_scores(H, x, v, prefix, extra=0):
+    """A batch of one query row whose scores are x[j] exactly, in units of log2, and whose
+    values are v[j] in the first of 56 columns: keys 0 .. prefix + extra are one latent column,
+    values others, both taken over by weights of zeros and ones.  x and v are bf16 numbers."""
+    s = base.make(34, H, [1 + extra], [prefix], DL=64)
+    for k in ("q_nope", "q_pe", "w_kv"):
+        s[k].zero_()
+    s["q_nope"][:, :, 0] = 1.0
+    s["w_kv"][:, 0, 0] = 1.0
+    for d in range(56):
+        s["w_kv"][:, 128 + d, 8 + d] = 1.0
+    at = s["rows"][0]
+    s["c_kv"][at] = 0.0
+    s["k_pe"][at] = 0.0
+    s["c_kv"][at, 0] = torch.from_numpy(x).bfloat16()
+    s["c_kv"][at, 8] = torch.from_numpy(v).bfloat16()
+    assert np.array_equal(s["c_kv"][at, 0].double().numpy(), x)
+    assert np.array_equal(s["c_kv"][at, 8].double().numpy(), v)
+    s["scale"] = float(np.float32(np.log(2.0)))
+    return s
+
+
+@pytest.mark.parametrize("H", [1, 160])     # cut along the keys, whole items
+@pytest.mark.parametrize("low", [-22.0, -26.0, -29.0])
+def test_many_small_weights_add_up(H, low):
+    """One key takes nearly all the weight and has the value 0; 4200 keys at 2^low have 1.
+
+    A weight is off by at most 2^-11 of itself or 2^-32 of the largest, a score's exponent by
+    2^-22 of it (the scale's two roundings and the product's), the output's rounding 2^-8."""
+    r = np.random.default_rng(40)
+    n = 4201
+    x = low - 0.25 * r.integers(0, 4, n)
+    x[n // 3] = 0.0
+    v = np.ones(n)
+    v[n // 3] = 0.0
+    s = exact_scores(H, x, v, n - 1)
+    p = np.exp(x * s["scale"])
+    ref = (p * v).sum() / p.sum()
+    tol = ((np.maximum(2.0 ** -11 * p, 2.0 ** -32) + 2.0 ** -21 * np.abs(x) * p) * v).sum() / p.sum()
+    out = base.run(s)[0]
+    assert (np.abs(out[:, 0] - ref) <= tol * 1.01 + 2.0 ** -8 * ref).all(), (out[0, 0], ref, tol)
+    assert (out[:, 1:] == 0).all()
