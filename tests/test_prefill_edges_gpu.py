@@ -118,3 +118,43 @@ def test_many_small_weights_add_up(H, low):
     out = base.run(s)[0]
     assert (np.abs(out[:, 0] - ref) <= tol * 1.01 + 2.0 ** -8 * ref).all(), (out[0, 0], ref, tol)
     assert (out[:, 1:] == 0).all()
+
+
+def staircase(H, n=200, prefix=1400, block=128):
+    """Scores that climb by 10, 5 or 20 (in log2) from a block of keys to the next, or fall by
+    10, by groups of eight rows: the accumulator is rescaled at every block, at every second
+    one, or never, for rows that share a warp.  Value column k is zero outside block k of the
+    keys, so every block's share of the output is compared by itself.
+
+    Scores and values are exact; a weight is off by 2^-11 of itself or 2^-32 of the row's
+    largest, exponents by 2^-22 of the largest score (in a weight and in the sum), the output's
+    rounding is 2^-8.  Returns the batch, its scores (log2), values, output and tolerance."""
+    r = np.random.default_rng(41)
+    keys = n + prefix
+    j = np.arange(keys)
+    x = 10.0 * (j // block) + r.integers(0, 4, keys)
+    s = exact_scores(H, x, np.zeros(keys), prefix, n - 1)
+    at = s["rows"][0]
+    v = torch.from_numpy(r.uniform(0.5, 2.0, keys)).bfloat16()
+    s["c_kv"][at, 8 + torch.from_numpy(j // block)] = v
+    a = np.array([1.0, 0.5, 2.0, -1.0])[np.arange(n) // 8 % 4]
+    s["q_nope"][:, :, 0] = torch.from_numpy(a).bfloat16()[:, None]
+    y = a[:, None] * x[None] * s["scale"] / np.log(2.0)
+    y[j[None] > prefix + np.arange(n)[:, None]] = -np.inf
+    p = np.exp2(y - y.max(1, keepdims=True))
+    V = np.zeros((keys, 56))
+    V[j, j // block] = v.double().numpy()
+    l = p.sum(1, keepdims=True)
+    ref = p @ V / l
+    rel = 2.0 ** -11 + 2.0 ** -20 * np.abs(a[:, None] * x.max())
+    tol = (rel * (p @ V) + (p > 0).astype(float) @ V * 2.0 ** -32) / l * 1.01 + 2.0 ** -8 * ref
+    return s, y, V, ref, tol
+
+
+@pytest.mark.parametrize("H", [1, 160])     # cut along the keys, whole items
+def test_moving_maxima_block_by_block(H):
+    s, _, _, ref, tol = staircase(H)
+    out = base.run(s)
+    for h in (0, H - 1):
+        assert (np.abs(out[:, h, :56] - ref) <= tol).all(), (h, np.abs(out[:, h, :56] - ref).max())
+        assert (out[:, h, 56:] == 0).all()
