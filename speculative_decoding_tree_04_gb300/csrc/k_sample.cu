@@ -33,7 +33,7 @@
 // Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
 // that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
 // are as many boundaries as tokens.  Weights are therefore held as integers in units of
-// 2^-44 of the row's largest (rounded from an exponential good to about 2^-38, built from
+// 2^-44 of the row's largest (rounded from an exponential good to about 2^-37, built from
 // pairs of floats: this part's double-precision units are slow).  Their sums are exact,
 // whatever order they are taken in, so splits, tests and the final search agree with one
 // another to the last unit.  A vocabulary of 2^18 tokens sums to below 2^63.
@@ -129,8 +129,8 @@ struct Shared {
 // 2^((x - m) c) in units of 2^-44, as high * 2^22 + low; c = ch + cl.
 // With y = (x - m) c = k/64 + f: 2^y = 2^(k/64) e^(f ln 2), the first factor from the
 // table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).  Floats
-// become integers by adding 1.5 * 2^23, whose last place is 1: conversions run at a quarter
-// of the rate.
+// become integers by adding 1.5 * 2^23, whose last place is 1, which takes magnitudes up to
+// 2^22: conversions run at a quarter of the rate.
 struct Weight {
   int high, low;
 };
@@ -155,9 +155,11 @@ __device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
   const float el = fmaf(zh, zl, zl) + p;
   const float2 t = table[(ki & (kTable - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
   const float ph = t.x * zh;
-  const float pl = fmaf(t.x, zh, -ph) + fmaf(t.x, el, t.y);
-  const float hi = t.x + ph;
-  const float lo = ((t.x - hi) + ph) + pl;
+  const float pl = fmaf(t.x, zh, -ph) + fmaf(t.x, el, fmaf(t.y, zh, t.y));
+  // (summed once more, so that the low part is a rounding of the high one, 2^20 units at most:
+  // without that it holds z^2 / 2, up to 2^28 units, past what the sum below can take)
+  const float h1 = t.x + ph, l1 = ((t.x - h1) + ph) + pl;
+  const float hi = h1 + l1, lo = (h1 - hi) + l1;
   const int e = (ki >> 6) << 23;
   const float a = hi * __int_as_float(e + ((22 + 127) << 23));
   const float ra = a + magic;
