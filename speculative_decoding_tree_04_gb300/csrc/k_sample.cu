@@ -19,16 +19,21 @@
 //
 // Passes.  A visited row is streamed once for its maximum and a float sum of exponentials
 // relative to a running one; what else it takes (a residual's sum, the draw) reads it from L2.
-// Floats decide first: every sum carries a bound on its error (about 4e-6 of the row's sum), a
+// Floats decide first: every sum carries a bound on its error (about 5e-6 of the row's sum), a
 // test whose two sides differ by more than the bounds is decided, and so is a draw that lands
 // that far inside a token.  Whatever is closer sends the node back to be done with the exact
 // sums below: a few tests in 10^6, and as many draws as the distribution has mass near
 // boundaries (one in 100 for a language model's, all of them for a flat one).  An exact weight
 // costs about eight times a float one.
-//   The bound: 2^((x - m) c) has a relative error of 2^-23 ln 2 |y| from the roundings of its
-// exponent y and 2^-22 from the exponential; a distribution's mean |y| is its entropy less
-// log2 Z, at most 18 (2^18 tokens), so that the sum's error is below 1.8e-6 of it; and every
-// addition on the way from a value to the row's sum adds 2^-24.
+//   The bound, with e = 2^-24, a rounding.  The exponent y = (x - m) log2(e) / T carries four
+// (the difference, log2(e) to a float, the quotient, the product), 3.3 e |y| in all, also where
+// it is reached in steps, as a thread's, a warp's, a CTA's and the row's maximum take over one
+// from another: the steps' |y| add up.  The weights' mean |y| is at most 13.4 (2^18 tokens, the
+// worst being one at 1 and all others at 2^-14.8), which makes 3.3 e ln 2 13.4 = 1.83e-6 of the
+// sum; the exponential adds 4 e, the exact sums' own units 2^18 2^-45 (twice in a residual):
+// 2.1e-6 in all.  Each step to another maximum adds 5 e (an exponential and a product), each
+// addition on the way from a value to the row's sum e.  What is then computed from the sums
+// counts its roundings where it is done.
 //
 // Exactness.  The drawn token turns on a running sum over the vocabulary: an error of d in
 // that sum moves a boundary past u_0 W with probability 2 d for each boundary, and there
@@ -66,6 +71,8 @@ constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
 constexpr int kTable = 64;
 constexpr double kLn2 = 0.693147180559945309417;
 constexpr int kCopies = 16;     // of the table, one for each lane of a half warp: no conflicts
+constexpr float kEps = 6e-8f;   // a rounding, 2^-24
+constexpr float kWeightError = 2.1e-6f;  // of a row's sum (see above)
 
 // 2^(j/64) as the sum of two floats, from the exponential's Taylor series in double.
 struct ExpTable {
@@ -652,9 +659,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
                              : 0.f;  // lane r: slice r's sum
       phase ^= 1;
       const float Z = warp_sum(part);
-      // additions from a value to the row's sum: a vector, a thread, a warp, a CTA, a cluster
-      const float adds = 6e-8f * (float)(N + (per_w + 31) / 32 + 16);
-      float W = Z, dW = (1.8e-6f + adds) * Z, S = 0.f, dS = 0.f, G = 1.f;
+      // additions from a value to the row's sum (in a vector, a thread, a warp, a CTA, a
+      // cluster), and changes of maximum, of which a thread's first costs nothing
+      const int ends = (e0 > 0) + (e1 < row.n_vec);
+      const int moves = (per_w + 32 * kUnroll - 1) / (32 * kUnroll) + ends + 2;
+      const float adds = kEps * (float)(N + (per_w + 31) / 32 + ends + 15 + 5 * moves);
+      float W = Z, dW = (kWeightError + adds) * Z, S = 0.f, dS = 0.f, G = 1.f, dG = 0.f;
       uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
       float ew[2] = {0.f, 0.f};
       if (warp == 0) {
@@ -682,7 +692,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             const float g = !p.draft ? 1.f : again ? 0.f : pick(child_q, i);
             const float w = again ? 0.f : p.draft ? fmaxf(fmaf(-g, S, e), 0.f) : e;
             const float over = u * g * W - w * G;
-            const float error = u * g * dW + G * (1e-6f * e + g * (dS + 1e-6f * S));
+            // (6e-14: the exact residual's units)
+            const float error = u * g * (dW + 3.f * kEps * W) + w * (dG + 2.f * kEps * G) +
+                                G * (1e-6f * e + g * (dS + 1e-6f * S) + 6e-14f);
             if (over < -error) {
               cmd = kAccept;
               next = i;
@@ -694,6 +706,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             }
             if (!p.draft) {
               refused |= 1ull << i;
+              dW += 2.f * kEps * W;
               W -= w;
               if (!again) {
                 if (row.in_part(x, per, lane)) part -= w;
@@ -704,8 +717,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             }
             refused |= 1ull << i;
             S += W / G;
-            dS += (dW + W * (1e-6f + 1e-6f / G)) / G + 1e-7f * S;
+            dS += (dW + W * (1.01f * dG / G + 2.f * kEps)) / G + 2.f * kEps * S;
             G -= g;
+            dG += kEps * G;
             cmd = G > 1e-3f ? kResidual : kExact;
           }
           if (cmd == kDraw) {
@@ -736,7 +750,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             next = owner;
             if (lane == 0) {
               sh.target_f = t;
-              sh.margin = 3.f * dW;  // the target's error and the sums' of both passes
+              // the target's error, the sums' (every weight is in those of one pass), and the
+              // roundings of the target on its way: a product, subtractions and scans
+              const int steps = (per_w + 32 * kWarps - 1) / (32 * kWarps);
+              sh.margin = 2.f * dW + kEps * (float)(32 + N + 2 * n + steps) * W;
               sh.range0 = min(c1, c0 + w * per_w);
               sh.range1 = min(c1, sh.range0 + per_w);
             }
@@ -767,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
         if (warp == 0) {
           part = lane < C ? sh.parts[phase][lane] : 0.f;
           W = warp_sum(part);
-          dW = 1.9e-6f * Z + 1e-7f * S + adds * W + dS;
+          dW = kWeightError * Z + (adds + kEps) * W + 1.01f * dS;  // (the g sum to 1)
         }
         phase ^= 1;
       }

@@ -38,8 +38,9 @@ def compare(s, **kw):
         assert got[0][b] == want[0] and np.array_equal(got[2][b], want[2]), b
 
 
-def draws(x, T, seed):
-    """Inputs whose only work is a draw next to a boundary of the row's running sum."""
+def draws(x, T, seed, near=None):
+    """Inputs whose only work is a draw next to a boundary of the row's running sum, or up to
+    2^near away from it."""
     B, V = x.shape
     r = np.random.default_rng(seed)
     u = np.zeros((B, 1), np.float32)
@@ -49,7 +50,8 @@ def draws(x, T, seed):
         inner = np.flatnonzero(w[:-1] > 2.0 ** -24 * total[-1])
         # (a token next to the boundary on either side)
         at = r.choice(inner) if len(inner) else 0
-        v = beside(total[at] / total[-1], int(r.integers(0, 2)))
+        far = FAR if near is None else 2.0 ** r.uniform(-26, near)
+        v = beside(total[at] / total[-1], int(r.integers(0, 2)), far)
         u[b, 0] = r.random() if v is None else v
     return dict(logits=x[:, None], parent=torch.full((B, 1), -1, dtype=torch.int32),
                 tokens=torch.zeros((B, 1), dtype=torch.int32), uniforms=torch.from_numpy(u),
@@ -118,3 +120,15 @@ def test_tests_and_residual_draws_next_to_a_boundary(draft, seed):
             u[0] = u[0] if v is None else v
         s["uniforms"][b] = torch.from_numpy(u)
     compare(s)
+
+
+@pytest.mark.parametrize("T", [0.7, 1.3, 0.30103])
+@pytest.mark.parametrize("rise", [1, -1, 0])
+def test_draws_at_any_distance_from_a_boundary(T, rise):
+    """2^-26 to 2^-16: where floats leave off and the exact sums take over."""
+    B, V = 640, 8192
+    r = np.random.default_rng(70 + rise)
+    x = 2.0 * r.normal(size=(B, V))
+    if rise:
+        x = 0.005 * x + np.linspace(-15, 0, V)[::rise] * np.log(2.0) * T
+    compare(draws(torch.from_numpy(x.astype(np.float32)), float(np.float32(T)), V, near=-16))
