@@ -416,12 +416,15 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  *       after all (w and g are then equal but for rounding).
  * With no child accepted (any more) the walk ends and the bonus token is the smallest v
  * with w[0] + .. + w[v] > uniforms[b,0] * W.  T_b = 0 is greedy: w is 1 at the largest
- * logit (the smallest index among equals) and 0 elsewhere; the result then equals
- * tv_tree_accept's.
+ * logit (the smallest index among equals) and 0 elsewhere, and draft_probs are not read; the
+ * result then equals tv_tree_accept's (on rows that either call takes: see status).  A T_b > 0
+ * below 1.5e-30 or above 1.4e30 counts as that.
  *
  * Weights are integers in units of 2^-44 of the row's largest and their sums are exact, so
- * results do not depend on how a row is split, and equal those of the rule in 64-bit
- * arithmetic unless a uniform number falls within about 2^-38 of a boundary.
+ * results do not depend on how a row is split.  A weight is off by at most 2^-37 of itself and
+ * half a unit.  Results equal those of the rule in 64-bit arithmetic unless a uniform number
+ * falls as near to a boundary as these move it: a draw's boundary by about 2^-37 (by 2^-27 if
+ * 2^18 half units all went one way), a test's by the share that they are of the child's weight.
  */
 typedef enum { TV_DRAFT_BY_DEPTH = 0, TV_DRAFT_BY_NODE = 1 } tv_draft_mode;
 
@@ -455,7 +458,7 @@ typedef struct {
                                 outputs), or a visited row with a NaN, a +inf or nothing
                                 but -inf (the walk ends there without a bonus token: -1).
                                 TV_ERR_BOUNDS: depth(n) >= draft_rows at a visited node
-                                with children (they are not tested). */
+                                with children and T_b > 0 (they are not tested). */
 } tv_sample_args;
 
 /* Returns TV_ERR_UNSUPPORTED for Q > 64 or vocab > 2^18, TV_ERR_INVALID_ARG for bad sizes,

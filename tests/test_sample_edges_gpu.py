@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+from speculative_decoding_tree_04_gb300 import tv
 from tests import serving_model as sm
 from tests.test_sample_gpu import call, make
 
@@ -132,3 +133,21 @@ def test_draws_at_any_distance_from_a_boundary(T, rise):
     if rise:
         x = 0.005 * x + np.linspace(-15, 0, V)[::rise] * np.log(2.0) * T
     compare(draws(torch.from_numpy(x.astype(np.float32)), float(np.float32(T)), V, near=-16))
+
+
+def test_greedy_rows_need_no_drafter():
+    """At temperature 0 the drafter's rows are not read: a depth without one is no error, and
+    what the rows hold does not matter."""
+    s = make(80, 4, 6, 50, draft="depth", wide=1)
+    s["temperature"][:] = 0.0
+    top = s["logits"].float().argmax(-1).to(torch.int32)
+    s["tokens"][:, 1:] = top[:, :-1]                # the whole chain is the target's own
+    s["draft"] = torch.full((4, 1, 50), float("nan"))
+    got, status = call(s)
+    assert status == 0 and (got[0] == 5).all()
+    assert np.array_equal(got[2], top.numpy())
+    s["temperature"][1] = 1.0                       # a sampled row of the batch does need one
+    s["draft"] = torch.full((4, 1, 50), 1.0 / 50)
+    s["uniforms"][:, 1] = 0.0
+    got, status = call(s)
+    assert status == tv.TV_ERR_BOUNDS and got[0].tolist() == [5, 1, 5, 5]
