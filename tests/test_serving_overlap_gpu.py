@@ -161,3 +161,63 @@ def test_prompts_and_overlapped_attention_share_a_workspace(batch):
         out.zero_()
         s.out.zero_()
         assert all(torch.equal(a, b) for a, b in zip(both(1), want))
+
+
+def sampling(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return dict(logits=torch.randn((B, Q, V), generator=g, device="cuda"),
+                parent=i32(np.tile(np.arange(-1, Q - 1), (B, 1))),
+                tokens=torch.randint(0, V, (B, Q), generator=g, device="cuda", dtype=torch.int32),
+                uniforms=torch.rand((B, Q), generator=g, device="cuda"),
+                out=[torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((B,), (B, Q), (B, Q))])
+
+
+def sample(d, status, **kw):
+    tv.tree_sample(d["logits"], d["parent"], d["tokens"], d["uniforms"], *d["out"], status=status,
+                   **kw)
+
+
+@pytest.mark.parametrize("branch", [False, True])
+def test_captured_behind_copies_fills_and_another_stream(batch, branch):
+    """In a graph the calls' kernels come first in it, behind memory copies and fills, and behind
+    the join of a second stream that samples; replayed, they give what eager calls give."""
+    s, d, e = batch, sampling(7), sampling(8)
+
+    def go():
+        main = torch.cuda.current_stream()
+        if branch:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                sample(e, s.status)
+        for t, v in zip((s.ref, s.table, s.n), s.before):
+            t.copy_(v)
+        s.reserve()
+        s.copies_seen.copy_(s.copies)
+        s.copy()
+        d["out"][0].zero_()
+        sample(d, s.status)
+        if branch:
+            main.wait_stream(side)
+        s.attend(0)
+        s.release_all.fill_(0)
+        tv.pages_release(s.pool, s.release_all, status=s.status)
+
+    s.copies_seen, s.release_all = torch.zeros_like(s.copies), torch.zeros_like(s.n)
+    side = torch.cuda.Stream()
+    go()
+    torch.cuda.synchronize()
+    seen = (s.ref, s.table, s.n, s.copies_seen, s.out, s.lse, *d["out"], *e["out"])
+    want = [t.clone() for t in seen]
+    assert int(s.status.item()) == 0 and int(s.ref.sum()) == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go()
+    for _ in range(3):
+        for t in (s.out, s.lse, *d["out"], *e["out"]):
+            t.fill_(-3)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(seen[:-3], want))
+        if branch:
+            assert all(torch.equal(a, b) for a, b in zip(e["out"], want[-3:]))
