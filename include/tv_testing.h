@@ -35,6 +35,26 @@ extern "C" {
  */
 int tv_testing_set_wait_fault(int skip_key_loads, uint64_t deadline_ns, int32_t* exit_counts);
 
+/*
+ * tv_testing_set_prompt_fault -- the same for the two tensor-core kernels of tv_prefill_attn.
+ *
+ * Their waits end at a deadline too, after which a CTA reports TV_ERR_TIMEOUT, waits for its
+ * own copies and MMAs in flight, frees its tensor memory and returns.
+ *   expand_loads : every CTA of the expansion issues at most this many loads (a step of 64
+ *                  latent columns each) and then none; negative: no limit.
+ *   attend_loads : every CTA of the attention issues at most this many loads of keys or values
+ *                  (a block's keys, then its values, and so on); negative: no limit.
+ *   deadline_ns  : deadline of every wait in nanoseconds (of a 2 GHz clock), 2 s at most; 0
+ *                  restores the default (2 s).
+ *   exit_counts  : device int32[4] or NULL: CTAs that left the expansion, those of them that
+ *                  gave up, and the same two of the attention.
+ * Process-wide, for every later tv_prefill_attn call until reset with (-1, -1, 0, NULL); calls
+ * whose CTAs give up produce no valid output.  Returns TV_OK, or TV_ERR_INVALID_ARG for a
+ * deadline above 2 s.
+ */
+int tv_testing_set_prompt_fault(int expand_loads, int attend_loads, uint64_t deadline_ns,
+                                int32_t* exit_counts);
+
 #ifdef __cplusplus
 }
 #endif

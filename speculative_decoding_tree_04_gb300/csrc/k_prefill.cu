@@ -48,6 +48,7 @@ constexpr int kBlock = 128;                     // keys per block, queries per t
 constexpr int kPair = 2 * kBlock;               // queries per CTA
 constexpr int kChunk = kBlock * 128;            // 128 rows of 64 bf16: 16 KB
 constexpr long long kDeadline = 4000000000ll;   // clocks of a wait: about 2 s
+constexpr int kAllLoads = INT_MAX;
 constexpr float kLift = 7.0f, kRescale = 15.0f;  // log2: see attend_kernel
 constexpr float kMaxV = 65504.f;                // the largest fp16
 
@@ -265,10 +266,23 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs p) {
 }
 
 // ---- bounded waits ------------------------------------------------------------------------
+// What a test may change (tv_testing_set_prompt_fault): how many loads a CTA issues, the
+// waits' deadline, and where CTAs count as they leave, {all, those that gave up}.
+struct WaitFault {
+  int32_t loads;
+  long long deadline;
+  int32_t* exits;
+};
 struct Abort {
   volatile int flag;
   int32_t* status;
+  long long deadline;
 };
+__device__ __forceinline__ void count_exit(const WaitFault& f, const Abort& ab) {
+  if (!f.exits || threadIdx.x != 0) return;
+  atomicAdd(f.exits, 1);
+  if (ab.flag) atomicAdd(f.exits + 1, 1);
+}
 
 __device__ __noinline__ bool wait_slow(Abort& ab, uint32_t a, uint32_t parity) {
   // the SM's own clock: reading the global timer takes about as long as these waits do
@@ -278,7 +292,7 @@ __device__ __noinline__ bool wait_slow(Abort& ab, uint32_t a, uint32_t parity) {
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait_plain(a, parity)) return true;
     if (ab.flag) return false;
-    if (clock64() - t0 > kDeadline) {
+    if (clock64() - t0 > ab.deadline) {
       ab.flag = 1;
       report(ab.status, TV_ERR_TIMEOUT);
       return false;
@@ -355,6 +369,7 @@ struct ExpandArgs {
   __nv_bfloat16 *K, *KR;
   __half* V;
   int32_t* status;
+  WaitFault fault;
 };
 
 // First cache row of 64 keys, or a row past the end (TMA then reads zeros) for a page that
@@ -387,6 +402,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     mbar_init(&sh.last, 1);
     sh.abort.flag = 0;
     sh.abort.status = p.status;
+    sh.abort.deadline = p.fault.deadline;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -415,7 +431,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                                  : (int)p.num_rows;
       for (int c = 0; c < p.k_chunks; ++c, ++u) {
         const uint32_t s = u % kExpStages;
-        if (!wait_for(sh.abort, &sh.empty[s], ((u / kExpStages) & 1) ^ 1)) {
+        if (u >= (uint32_t)p.fault.loads ||
+            !wait_for(sh.abort, &sh.empty[s], ((u / kExpStages) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -511,6 +528,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  count_exit(p.fault, sh.abort);
 }
 
 // ---- attend -------------------------------------------------------------------------------
@@ -553,6 +571,7 @@ struct AttendArgs {
   float* part_o;   // [piece][256][128]
   float* part_ml;  // [piece][256][2]
   int32_t* status;
+  WaitFault fault;
 };
 
 // The r-th item of this CTA: a head of a query tile's piece.  Items are listed longest first
@@ -652,6 +671,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     sh.abort.flag = 0;
     sh.abort.status = p.status;
+    sh.abort.deadline = p.fault.deadline;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -700,6 +720,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 5; ++c) {
           const uint32_t u = 5u * g + c;
+          if ((c == 0 || c == 3) && armed_k + armed_v >= p.fault.loads) ok = false;
           if (ok && u >= (uint32_t)kRing) {
             const uint32_t before = u - kRing, gb = before / 5;
             uint64_t* done = before - 5 * gb < 3 ? &sh.k_done[gb & 1] : &sh.v_done[gb & 1];
@@ -1024,6 +1045,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  count_exit(p.fault, sh.abort);
 }
 
 // ---- join ---------------------------------------------------------------------------------
@@ -1071,6 +1093,10 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 std::mutex g_mu;
 bool g_ready[64] = {};
+// Testing hook (tv_testing_set_prompt_fault): off unless a test turns it on.
+std::mutex g_fault_mu;
+WaitFault g_expand_fault = {kAllLoads, kDeadline, nullptr};
+WaitFault g_attend_fault = {kAllLoads, kDeadline, nullptr};
 
 cudaError_t setup() {
   std::call_once(g_encode_once, [] {
@@ -1177,7 +1203,12 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
   AttendArgs aa{counts, q_tiles, l.cut ? (const int4*)(base + l.pieces) : nullptr,
                 (const int2*)(base + l.tile_pieces), a->H, (float)((double)a->scale * 1.4426950408889634),
                 (__nv_bfloat16*)a->out, (float*)(base + l.part_o), (float*)(base + l.part_ml),
-                a->status};
+                a->status, {}};
+  {
+    std::lock_guard<std::mutex> lock(g_fault_mu);
+    xa.fault = g_expand_fault;
+    aa.fault = g_attend_fault;
+  }
 
   // each kernel's set-up runs beside the one before it (programmatic dependent launch)
   cudaLaunchConfig_t cfg = {};
@@ -1204,3 +1235,15 @@ cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cud
 }
 
 }  // namespace tv
+
+extern "C" int tv_testing_set_prompt_fault(int expand_loads, int attend_loads,
+                                           uint64_t deadline_ns, int32_t* exit_counts) {
+  if (deadline_ns > 2000000000ull) return TV_ERR_INVALID_ARG;
+  // two clocks a nanosecond
+  const long long deadline = deadline_ns ? 2ll * (long long)deadline_ns : tv::kDeadline;
+  std::lock_guard<std::mutex> lock(tv::g_fault_mu);
+  tv::g_expand_fault = {expand_loads < 0 ? tv::kAllLoads : expand_loads, deadline, exit_counts};
+  tv::g_attend_fault = {attend_loads < 0 ? tv::kAllLoads : attend_loads, deadline,
+                        exit_counts ? exit_counts + 2 : nullptr};
+  return TV_OK;
+}

@@ -166,6 +166,7 @@ def load():
     lib.tv_last_error.restype = ctypes.c_char_p
     lib.tv_version.restype = ctypes.c_int
     lib.tv_testing_set_wait_fault.argtypes = [i32, ctypes.c_uint64, P]
+    lib.tv_testing_set_prompt_fault.argtypes = [i32, i32, ctypes.c_uint64, P]
     lib.tv_build_tree.argtypes = [P, P, P, i32, i32, i32, i32, P, P, P, P, P, P]
     lib.tv_verify_prologue.argtypes = [ctypes.POINTER(PrologueArgs), P]
     lib.tv_tree_accept_workspace_size.argtypes = [i32, i32, i64]
