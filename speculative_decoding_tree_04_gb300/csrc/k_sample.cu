@@ -22,9 +22,10 @@
 // Floats decide first: every sum carries a bound on its error (about 5e-6 of the row's sum), a
 // test whose two sides differ by more than the bounds is decided, and so is a draw that lands
 // that far inside a token.  Whatever is closer sends the node back to be done with the exact
-// sums below: a few tests in 10^6, and as many draws as the distribution has mass near
-// boundaries (one in 100 for a language model's, all of them for a flat one).  An exact weight
-// costs about eight times a float one.
+// sums below: a few tests in 10^4, and as many draws as the distribution has mass near
+// boundaries (with weights that fall off as rank^-2.2: 9 in 1000 of 163840 tokens, 24 in 1000
+// after a rejection of 50257; all of them for a flat one).  An exact weight costs about eight
+// times a float one, and a node with k drafted children refused pays k + 1 passes of them.
 //   The bound, with e = 2^-24, a rounding.  The exponent y = (x - m) log2(e) / T carries four
 // (the difference, log2(e) to a float, the quotient, the product), 3.3 e |y| in all, also where
 // it is reached in steps, as a thread's, a warp's, a CTA's and the row's maximum take over one
@@ -48,11 +49,13 @@
 // distributed shared memory, and every CTA takes the same decisions from the same numbers.
 //
 // Measured (calls in a loop, inputs beyond L2).  One sequence of 9 nodes, 32000 bf16 logits:
-// 9-13 us, 7.9 in a graph; 32 x 33 nodes, 163840 floats: 34-42 us; with the drafter's rows, 8 x 9
-// nodes, 163840 bf16: 25-35 us, and 64 x 17 nodes, 50257 floats: 47-66 us.  The bytes alone
+// 9-14 us, 7.9 in a graph; 32 x 33 nodes, 163840 floats: 33-41 us; with the drafter's rows, 8 x 9
+// nodes, 163840 bf16: 27-43 us, and 64 x 17 nodes, 50257 floats: 48-65 us.  The bytes alone
 // would take below 0.1, 6.2, 1.5 and 5.7 us: what bounds it is the walk, one visited row after
-// another, and the sequences with a draw or test that needs the exact sums (about 25000
-// clocks).  With exact sums for every row: 22, 184, 65 and 188 us.
+// another, the sequences with a draw or test that needs the exact sums (about 25000 clocks),
+// and, from 456 CTAs on, a second round of them.  The dear ends, from a cold cache: 32 x 33
+// nodes of 163840 equal floats, every draw done twice, 56 us; wide normal logits, most of them,
+// 103; 16 drafted children refused one after another, 8 sequences of 163840 bf16, 314.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -951,8 +954,10 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, tree_sample_kernel<T, kThreads>, p, log2_C);
 }
 
-// Threads per CTA: 1024 or 512 where the CTAs leave an SM that much room and a thread still
-// has eight values to read.
+// Threads per CTA: 1024 or 512 where the CTAs are few and a thread still has eight values to
+// read.  An SM's registers hold one CTA of 1024 threads, one of 512 (119-124 registers each) or
+// three of 256 (80): between one and two CTAs of 512 per SM, the last ones start when the first
+// have ended, and so do those of 256 past three.
 template <typename T>
 cudaError_t launch(const SampleParams& p, int C, int sm_count, cudaStream_t st) {
   const int64_t ctas = (int64_t)p.B * C, slice = p.V / C;
@@ -964,8 +969,10 @@ cudaError_t launch(const SampleParams& p, int C, int sm_count, cudaStream_t st) 
 }  // namespace
 
 // CTAs per sequence: at most 16, about 2048 vocabulary entries each at least, and no more than
-// four per SM in all.  (32 x 33 nodes of 163840 floats, and 64 x 17 of 50257 with the drafter's
-// rows: 36-40 and 52-54 us with four, 39-41 and 81-85 with three, 43-47 and 57-61 with two.)
+// four per SM in all, of which three are resident.  (32 x 33 nodes of 163840 floats, and 64 x 17
+// of 50257 with the drafter's rows: 36-40 and 52-54 us with four, 39-41 and 81-85 with three,
+// 43-47 and 57-61 with two.  A power of two each: 512 CTAs, 256 and 256 of more threads; the
+// number of rounds was not varied by itself.)
 int sample_cluster(int B, int64_t V, int sm_count) {
   int C = kMaxCluster;
   while (C > 1 && ((int64_t)B * C > 4 * (int64_t)sm_count || V < 2048ll * C)) C /= 2;
