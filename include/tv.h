@@ -413,7 +413,9 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  *       child c is accepted iff  uniforms[b,c] * g[x_c] * W < w[x_c] * G; else
  *       w = max(w - g * W/G, 0), G = G - g[x_c], g[x_c] = 0; no child is tested any more
  *       once G <= 0, and if no weight is left after a rejection the child is accepted
- *       after all (w and g are then equal but for rounding).
+ *       after all (w and g are then equal but for rounding).  If the target gives that child
+ *       no weight at all, the bonus token is drawn from what was left before its rejection
+ *       instead.
  * With no child accepted (any more) the walk ends and the bonus token is the smallest v
  * with w[0] + .. + w[v] > uniforms[b,0] * W.  T_b = 0 is greedy: w is 1 at the largest
  * logit (the smallest index among equals) and 0 elsewhere, and draft_probs are not read; the
@@ -423,8 +425,10 @@ int tv_compact_kv(void* c_kv, void* k_pe, tv_dtype kv_dt, int64_t ckv_row_stride
  * Weights are integers in units of 2^-44 of the row's largest and their sums are exact, so
  * results do not depend on how a row is split.  A weight is off by at most 2^-37 of itself and
  * half a unit.  Results equal those of the rule in 64-bit arithmetic unless a uniform number
- * falls as near to a boundary as these move it: a draw's boundary by about 2^-37 (by 2^-27 if
- * 2^18 half units all went one way), a test's by the share that they are of the child's weight.
+ * falls as near to a boundary as these move it.  The sums of a draw move by about 2^-37 of the
+ * row's (by 2^-27 if 2^18 half units all went one way), which is a larger share of what
+ * rejections have left; a test's sides move by the share that a half unit is of the child's
+ * weight; and what rejections leave counts as nothing once it is below half a unit everywhere.
  */
 typedef enum { TV_DRAFT_BY_DEPTH = 0, TV_DRAFT_BY_NODE = 1 } tv_draft_mode;
 

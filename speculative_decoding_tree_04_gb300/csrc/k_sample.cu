@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
       // ---- exact sums of the weights, the tests by them, and residuals after rejections ----
       sc.s_hi = 0.f;
       // warp 0's: S and G, the children left, the tokens refused, the child whose rejection
-      // the residual that is being summed belongs to
-      double S = 0.0, G = 1.0;
+      // the residual that is being summed belongs to, and S before that
+      double S = 0.0, G = 1.0, S_before = 0.0;
       uint64_t left = p.draft && !has_q ? 0ull : children, refused = 0;
       int refusing = -1;
       for (;;) {
@@ -834,9 +834,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
           int64_t W = warp_sum(part);
           int cmd = kDraw, next = -1, n = 0;
           if (refusing >= 0 && W == 0) {
-            // the drafter covers all that p has left: the two are equal but for rounding
-            cmd = kAccept;
-            next = refusing;
+            if (pick(child_e, refusing) > 0) {
+              // the drafter covers all that p has left: the two are equal but for rounding
+              cmd = kAccept;
+              next = refusing;
+            } else {  // a token that p excludes: the draw is from what was left before it
+              cmd = kResidual;
+              S = S_before;
+              left = 0;
+              refusing = -1;
+            }
           }
           while (cmd == kDraw && left && (!p.draft || G > 0.0)) {
             const int i = __ffsll((long long)left) - 1;
@@ -868,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
             }
             cmd = kResidual;
             refusing = i;
+            S_before = S;
             S += (double)W * (1.0 / (double)kUnit) / G;
             G -= g;
           }

@@ -151,3 +151,24 @@ def test_greedy_rows_need_no_drafter():
     s["uniforms"][:, 1] = 0.0
     got, status = call(s)
     assert status == tv.TV_ERR_BOUNDS and got[0].tolist() == [5, 1, 5, 5]
+
+
+@pytest.mark.parametrize("mass", [0.9, 0.999])
+def test_masked_children_are_never_taken(mass):
+    """The target allows one token, of which the drafter is nearly sure, and the children are
+    others: every rejection leaves a tenth (or a thousandth) of the weight, down to less than the
+    exact sums hold, and the allowed token has to be drawn all the same."""
+    B, V, Q = 4, 64, 24
+    r = np.random.default_rng(90)
+    s = make(90, B, Q, V, draft="depth")
+    s["parent"][:, 1:] = 0
+    s["logits"][:, 0] = float("-inf")
+    s["draft"] = torch.full((B, Q, V), (1 - mass) / (V - 1))
+    for b in range(B):
+        order = r.permutation(V).astype(np.int32)
+        s["logits"][b, 0, int(order[0])] = 1.5
+        s["draft"][b, :, int(order[0])] = mass
+        s["tokens"][b, 1:] = torch.from_numpy(order[1:Q])
+    compare(s)
+    got, _ = call(s)
+    assert (got[0] == 0).all() and (got[2][:, 0] == s["logits"][:, 0].argmax(-1).numpy()).all()
