@@ -196,9 +196,10 @@ typedef struct {
                                pieces (tensor cores: each 128-row tile's sweep) */
   int32_t paged_view;       /* tv_paged_view; TV_PAGED_AUTO normally */
   int32_t mask_mode;        /* tv_mask_mode; TV_MASK_TREE for tree verification */
-  int32_t overlap_prev;     /* 0 normally.  1: the call queued on the stream just before this
-                               one writes none of prefix_len and the page table (as for
-                               tv_verify_prologue, which writes q_pe, cache rows and anc);
+  int32_t overlap_prev;     /* 0 normally.  1: the call that queued the stream's last work before
+                               this one (one with nothing to do, such as a copy of an empty
+                               list, queues none) writes none of prefix_len and the page table
+                               (as for tv_verify_prologue, which writes q_pe, cache rows, anc);
                                the tensor-core path's preparation kernel (work schedule,
                                per-step tensor maps) may then run while that call finishes.
                                Calls before that one may write them (tv_pages_reserve, say,
