@@ -978,9 +978,8 @@ cudaError_t launch(const SampleParams& p, int C, int sm_count, cudaStream_t st) 
 
 // CTAs per sequence: at most 16, about 2048 vocabulary entries each at least, and no more than
 // four per SM in all, of which three are resident.  (32 x 33 nodes of 163840 floats, and 64 x 17
-// of 50257 with the drafter's rows: 36-40 and 52-54 us with four, 39-41 and 81-85 with three,
-// 43-47 and 57-61 with two.  A power of two each: 512 CTAs, 256 and 256 of more threads; the
-// number of rounds was not varied by itself.)
+// of 50257 with the drafter's rows, 512 CTAs: 36-40 and 52-54 us.  A limit of three or of two
+// both comes to 256 CTAs of 512 threads: 39-47 and 57-85 over seeds.)
 int sample_cluster(int B, int64_t V, int sm_count) {
   int C = kMaxCluster;
   while (C > 1 && ((int64_t)B * C > 4 * (int64_t)sm_count || V < 2048ll * C)) C /= 2;
