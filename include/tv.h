@@ -639,6 +639,216 @@ size_t tv_prefill_attn_workspace_size(const tv_prefill_args* a);
 /* workspace: device memory of at least that size, 256-byte aligned; scratch. */
 int tv_prefill_attn(const tv_prefill_args* a, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * Rotary positions: which elements make a pair, and how its angle depends on the position.
+ *
+ * Pair k < rot_dim/2 of a rotated part x is (x[k], x[k + rot_dim/2]) with TV_ROPE_HALF (as
+ * tv_rope_neox), (x[2k], x[2k+1]) with TV_ROPE_INTERLEAVED.  It turns by pos * f_k, and cos and
+ * sin are multiplied by the magnitude.  With e_k = base^(-2k/rot_dim) and c the original
+ * context:
+ *   TV_ROPE_PLAIN       f_k = e_k
+ *   TV_ROPE_LINEAR      f_k = e_k / factor
+ *   TV_ROPE_NTK         f_k = base'^(-2k/rot_dim), base' = base * factor^(rot_dim/(rot_dim-2))
+ *   TV_ROPE_YARN        f_k = e_k (1 - r_k) + e_k/factor * r_k, r_k rising from 0 to 1 between
+ *                       the pairs floor(d(high)) and ceil(d(low)), d(n) = rot_dim
+ *                       ln(c / (2 pi n)) / (2 ln base) being the pair that turns n times over
+ *                       c positions (the two are kept within 0 .. rot_dim-1, and 0.001 apart)
+ *   TV_ROPE_WAVELENGTH  the same with 1 - r_k = (n_k - low) / (high - low), cut off at 0 and 1,
+ *                       where n_k = c e_k / (2 pi) is how often pair k turns over c positions
+ */
+typedef enum { TV_ROPE_HALF = 0, TV_ROPE_INTERLEAVED = 1 } tv_rope_layout;
+typedef enum {
+  TV_ROPE_PLAIN = 0,
+  TV_ROPE_LINEAR = 1,
+  TV_ROPE_NTK = 2,
+  TV_ROPE_YARN = 3,
+  TV_ROPE_WAVELENGTH = 4
+} tv_rope_kind;
+
+typedef struct {
+  double base;               /* > 1 */
+  int32_t kind;              /* tv_rope_kind */
+  double factor;             /* >= 1: how far the context is stretched (PLAIN: not read) */
+  double original_context;   /* > 0 (YARN, WAVELENGTH) */
+  double low, high;          /* turns, 0 < low < high (YARN, WAVELENGTH) */
+  double magnitude;          /* factor on cos and sin; 0: 0.1 ln(factor) + 1 for YARN, else 1 */
+} tv_rope_scaling;
+
+/* The f_k of rot_dim/2 pairs and the magnitude (host memory), as the calls below take them.
+ * TV_ERR_INVALID_ARG for a bad scaling or a rot_dim that is odd, below 2 or above 512. */
+int tv_rope_frequencies(const tv_rope_scaling* scaling, int rot_dim, double* frequencies,
+                        double* magnitude);
+
+/*
+ * tv_rope -- rotate a part of every head at given positions.
+ *
+ * Head h of token t is x = in + t*in_stride_token + h*in_stride_head, d_head elements of which
+ * [rot_offset, rot_offset + rot_dim) are rotated: pair (a, b) at angle t_k becomes
+ *     a cos t_k - b sin t_k,   b cos t_k + a sin t_k;
+ * the other elements are copied.  `inverse` turns by -t_k (the gradient of the forward turn; or
+ * a way back to un-rotated keys, at magnitude 1).  The angle runs in double.  float32 results
+ * are within one unit of the last place of the formula in double, and equal tv_rope_neox's where
+ * that can express them; bf16 results are rounded once from a value within 2^-20 (|a| + |b|)
+ * times the magnitude.
+ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_rope_args): ABI check */
+  int32_t T, n_heads;        /* tokens, heads */
+  int32_t d_head;            /* elements of a head, at most 65536 */
+  int32_t rot_offset, rot_dim; /* rot_dim even, 2 .. 512 */
+  int32_t layout;            /* tv_rope_layout */
+  int32_t inverse;           /* 0 or 1 */
+  tv_dtype dt;               /* F32 or BF16, of in and out */
+  const void* in;
+  void* out;                 /* in itself (with the same strides), or memory apart from it */
+  int64_t in_stride_token, in_stride_head, out_stride_token, out_stride_head; /* elements */
+  const int32_t* positions;  /* device [T] */
+  tv_rope_scaling scaling;
+} tv_rope_args;
+
+int tv_rope(const tv_rope_args* a, void* stream);
+
+/*
+ * tv_norm_rope -- norms of queries and keys, rotation, and the append to the cache, in one pass.
+ *
+ * The tokens are packed as for tv_prefill_attn: sequence b has tokens q_start[b] ..
+ * q_start[b+1]-1, the i-th of them at key prefix_len[b] + i and at position prefix_len[b] + i,
+ * or prefix_len[b] + depth[t] for a draft tree.  With N(x; w) = x / sqrt(mean(x^2) + eps) * w,
+ * or x where w is NULL, and R the rotation of the first rot_dim elements:
+ *     q[t,h] = (q_nope, q_pe):  N(q[t,h]; q_weight), its last d_rope elements through R
+ *     kv[t] = (latent, rope):   c_kv row = N(latent; kv_weight),  k_pe row = R N(rope; k_weight)
+ * Sums, products and the rotation are 32-bit (the angle in double), rounded once.  q_nope and
+ * q_pe are what tv_prefill_attn takes; with d_nope = 0 only q_pe is written, for queries that
+ * were taken into the latent space.
+ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_norm_rope_args): ABI check */
+  int32_t B, T, H;           /* sequences, packed tokens, query heads */
+  int32_t d_nope, d_rope, d_latent; /* d_nope >= 0; together at most 65536 */
+  int32_t rot_dim;           /* even, 2 .. min(d_rope, 512) */
+  int32_t layout;            /* tv_rope_layout */
+  tv_dtype dt;               /* F32 or BF16, of every tensor */
+  float eps;                 /* >= 0 */
+  const void* q;             /* device, [t, h] at q + t*q_stride_token + h*q_stride_head; NULL:
+                                no queries (nor their outputs) */
+  int64_t q_stride_token, q_stride_head;
+  const void* kv;            /* device, [t] at kv + t*kv_stride_token; NULL: no keys (the cache is
+                                not read) */
+  int64_t kv_stride_token;
+  const void* q_weight;      /* device [d_nope + d_rope], nullable */
+  const void* kv_weight;     /* device [d_latent], nullable */
+  const void* k_weight;      /* device [d_rope], nullable */
+  const int32_t* q_start;    /* device [B + 1], ascending */
+  const int32_t* prefix_len; /* device [B] */
+  const int32_t* depth;      /* device [T], nullable; a negative one leaves its token alone */
+  void* q_nope;              /* device [T, H, d_nope] contiguous out */
+  void* q_pe;                /* device [T, H, d_rope] contiguous out */
+  void* c_kv;                /* cache arrays, rows of d_latent and d_rope elements */
+  void* k_pe;
+  int64_t ckv_row_stride, kpe_row_stride;
+  tv_cache_layout cache;     /* any page size; num_rows > 0 */
+  tv_rope_scaling scaling;
+  int32_t* status;           /* device int32, nullable.  TV_ERR_BOUNDS: a negative prefix_len
+                                (its tokens are left alone), or a key outside the cache (its rows
+                                are not written).  Tokens of no sequence are left as they were. */
+} tv_norm_rope_args;
+
+int tv_norm_rope(const tv_norm_rope_args* a, void* stream);
+
+/*
+ * tv_shared_attn -- attention of sequences that share a long prefix.
+ *
+ * tv_verify_attn for a batch in which neighbouring sequences hold the same first keys, as rows
+ * forked from one prompt do (tv_pages_fork): group g is the sequences group_start[g] ..
+ * group_start[g+1]-1, and their keys 0 .. shared_len[g]-1 are the same.  The scores of those keys
+ * are taken for the rows of all of a group's sequences together, from the pages of its first
+ * one, and joined with every sequence's own keys by their softmax sums, where that takes fewer
+ * 128-row tiles.  Every row's result is that of the attention over all of its keys:
+ *     s_j = scale * ( q_latent . c_kv_j + q_pe . k_pe_j ),  out = sum_j softmax(s)_j c_kv_j,
+ *     lse = ln sum_j exp(s_j)
+ * over the prefix keys j < prefix_len[b], shared or not, and of the Q own ones the
+ * ancestors-or-self in anc, or with anc NULL the row's token and those before it.  A row that
+ * sees no key gets out = 0 and lse = -inf.
+ *
+ * Softmax weights are rounded to bf16 for the tensor cores (2^-8 of themselves at most), sums and
+ * statistics are 32-bit.  The keys 0 .. prefix_len[b]+Q-1 must be finite for rows that do not
+ * see them, too; what lies behind them in the cache may be anything.
+ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_shared_args): ABI check */
+  int32_t B, H, Q;           /* sequences, heads, queries of a sequence (1 .. 64) */
+  int32_t d_latent, d_rope;  /* 512, 64 */
+  float scale;               /* > 0 */
+  tv_dtype dt;               /* TV_BF16: queries and cache */
+  tv_dtype out_dt;           /* F32 or BF16 */
+  const void* q_latent;      /* device [B, Q, H, d_latent] contiguous */
+  const void* q_pe;          /* device [B, Q, H, d_rope] contiguous, RoPE applied */
+  const void* c_kv;          /* cache rows, as tv_attn_args */
+  const void* k_pe;
+  int64_t ckv_row_stride, kpe_row_stride;
+  tv_cache_layout cache;     /* 64-token pages, or contiguous; num_rows > 0, < 2^31 - 64 */
+  const int32_t* prefix_len; /* device [B] */
+  int32_t max_prefix_len;    /* host bound on prefix_len */
+  int32_t G;                 /* groups, 0 .. B (0: nothing is shared) */
+  const int32_t* group_start; /* device [G + 1]: 0 = first, ascending, B = last */
+  const int32_t* shared_len; /* device [G], 0 .. the group's smallest prefix_len */
+  const uint64_t* anc;       /* device [B, Q] from tv_build_visibility, nullable */
+  void* out;                 /* device [B, Q, H, d_latent] out */
+  float* lse;                /* device [B, Q, H] out, nullable */
+  int32_t* status;           /* device int32, nullable.  TV_ERR_BOUNDS: a sequence whose
+                                prefix_len is negative, above the bound or past the cache (its
+                                rows get out = 0, lse = -inf); groups that are not as above (they
+                                are not shared: every sequence reads its own pages); a page
+                                outside the cache (it reads as zeros). */
+} tv_shared_args;
+
+/* Bytes of workspace (partial results: 2 KB for each row of the batch, twice, and about 22 MB);
+ * depends on B, H, Q, G and the device.  0 for invalid arguments. */
+size_t tv_shared_attn_workspace_size(const tv_shared_args* a);
+
+/* workspace: device memory of at least that size, 256-byte aligned; scratch. */
+int tv_shared_attn(const tv_shared_args* a, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * tv_token_sample -- the next token of each row, from given uniform numbers.
+ *
+ * For a row with temperature T > 0, let w_v = exp((x_v - max x) / T) and order the tokens by
+ * falling logit, equal ones by index.  Kept is the longest beginning of that order in which
+ * every token passes each filter that is on (the first one always does):
+ *     top_k k > 0    it is among the first k;
+ *     top_p p < 1    the tokens before it weigh less than p times those that top_k keeps;
+ *     min_p m > 0    w_v >= m (an m below 2^-44 counts as that).
+ * The token is the smallest kept v whose kept weights up to v sum to more than uniforms[b] times
+ * the sum of all of them.  T = 0 is greedy: the largest logit, the smallest index among equals;
+ * the filters are not read.  A T > 0 below 1.5e-30 or above 1.4e30 counts as that.
+ *
+ * Weights are integers in units of 2^-44 of the largest, off by at most 2^-37 of themselves and
+ * half a unit, as in tv_tree_sample, and their sums are exact: results equal those of the rule in
+ * 64-bit arithmetic unless a sum or a weight falls as near to a border as these move it, and do
+ * not depend on how a row is split.
+ */
+typedef struct {
+  uint32_t struct_size;      /* sizeof(tv_token_args): ABI check */
+  int32_t B;                 /* rows */
+  int64_t vocab;             /* 1 .. 2^18 */
+  const void* logits;        /* device, row b at logits + b*logits_row_stride elements; -inf masks
+                                a token: it is never kept */
+  tv_dtype logits_dt;        /* F32 or BF16 */
+  int64_t logits_row_stride; /* >= vocab */
+  const float* temperature;  /* device [B], nullable (1 for every row) */
+  const int32_t* top_k;      /* device [B], nullable; <= 0: off */
+  const float* top_p;        /* device [B], nullable; >= 1: off; <= 0: only the first token */
+  const float* min_p;        /* device [B], nullable; <= 0: off; above 1: as 1 */
+  const float* uniforms;     /* device [B] in [0, 1) (clamped into it; a NaN counts as 0) */
+  int32_t* tokens;           /* device [B] out */
+  int32_t* kept;             /* device [B] out, nullable: how many tokens are kept */
+  int32_t* status;           /* device int32, nullable.  TV_ERR_INVALID_ARG: a negative or NaN
+                                temperature, a NaN top_p or min_p where the row samples, or a row
+                                with a NaN, a +inf or nothing but -inf (token -1, kept 0). */
+} tv_token_args;
+
+int tv_token_sample(const tv_token_args* a, void* stream);
+
 /* Text for a tv_status code (static storage). */
 const char* tv_status_string(int code);
 

@@ -55,6 +55,12 @@ int tv_testing_set_wait_fault(int skip_key_loads, uint64_t deadline_ns, int32_t*
 int tv_testing_set_prompt_fault(int expand_loads, int attend_loads, uint64_t deadline_ns,
                                 int32_t* exit_counts);
 
+/*
+ * tv_testing_set_shared_fault -- tv_testing_set_wait_fault for the kernel of tv_shared_attn: the
+ * same arguments and effects, for every later tv_shared_attn call until reset with (0, 0, NULL).
+ */
+int tv_testing_set_shared_fault(int skip_key_loads, uint64_t deadline_ns, int32_t* exit_counts);
+
 #ifdef __cplusplus
 }
 #endif

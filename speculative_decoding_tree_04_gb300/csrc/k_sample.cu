@@ -60,6 +60,7 @@
 
 #include <algorithm>
 
+#include "sample_math.h"
 #include "sm100_ptx.h"
 #include "tv_internal.h"
 
@@ -70,32 +71,8 @@ using namespace ptx;
 
 constexpr int kMaxWarps = 32;
 constexpr int kMaxCluster = 16;
-constexpr float kUnit = 17592186044416.f;  // 2^44 units per largest weight
-constexpr int kTable = 64;
-constexpr double kLn2 = 0.693147180559945309417;
-constexpr int kCopies = 16;     // of the table, one for each lane of a half warp: no conflicts
 constexpr float kEps = 6e-8f;   // a rounding, 2^-24
 constexpr float kWeightError = 2.1e-6f;  // of a row's sum (see above)
-
-// 2^(j/64) as the sum of two floats, from the exponential's Taylor series in double.
-struct ExpTable {
-  float hi[kTable], lo[kTable];
-};
-constexpr ExpTable make_exp_table() {
-  ExpTable t{};
-  for (int j = 0; j < kTable; ++j) {
-    const double x = kLn2 * j / kTable;
-    double term = 1.0, sum = 1.0;
-    for (int k = 1; k < 24; ++k) {
-      term *= x / k;
-      sum += term;
-    }
-    t.hi[j] = (float)sum;
-    t.lo[j] = (float)(sum - (double)t.hi[j]);
-  }
-  return t;
-}
-__device__ const ExpTable d_exp = make_exp_table();
 
 struct SampleParams {
   const void* logits;
@@ -136,50 +113,6 @@ struct Shared {
   int range0, range1;
 };
 
-// 2^((x - m) c) in units of 2^-44, as high * 2^22 + low; c = ch + cl.
-// With y = (x - m) c = k/64 + f: 2^y = 2^(k/64) e^(f ln 2), the first factor from the
-// table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).  Floats
-// become integers by adding 1.5 * 2^23, whose last place is 1, which takes magnitudes up to
-// 2^22: conversions run at a quarter of the rate.
-struct Weight {
-  int high, low;
-};
-__device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
-                                         const float2* __restrict__ table) {
-  const float dh = x - m;
-  const float y0 = dh * ch;
-  const bool some = y0 > -46.f;  // else below half a unit; -inf (masked) too
-  const float yh = some ? y0 : 0.f;
-  const float bb = dh - x;
-  const float dl = (x - (dh - bb)) - (m + bb);
-  const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-  constexpr float magic = 12582912.f;
-  const float kr = fmaf(yh, (float)kTable, magic);
-  const int ki = __float_as_int(kr) - __float_as_int(magic);
-  const float f = fmaf(kr - magic, -1.f / kTable, yh);  // exact
-  constexpr float ln2h = (float)kLn2, ln2l = (float)(kLn2 - (double)ln2h);
-  const float zh = f * ln2h;
-  const float zl = fmaf(f, ln2h, -zh) + fmaf(f, ln2l, yl * ln2h);
-  const float p =
-      zh * zh * fmaf(zh, fmaf(zh, fmaf(zh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
-  const float el = fmaf(zh, zl, zl) + p;
-  const float2 t = table[(ki & (kTable - 1)) * kCopies + (threadIdx.x & (kCopies - 1))];
-  const float ph = t.x * zh;
-  const float pl = fmaf(t.x, zh, -ph) + fmaf(t.x, el, fmaf(t.y, zh, t.y));
-  // (summed once more, so that the low part is a rounding of the high one, 2^20 units at most:
-  // without that it holds z^2 / 2, up to 2^28 units, past what the sum below can take)
-  const float h1 = t.x + ph, l1 = ((t.x - h1) + ph) + pl;
-  const float hi = h1 + l1, lo = (h1 - hi) + l1;
-  const int e = (ki >> 6) << 23;
-  const float a = hi * __int_as_float(e + ((22 + 127) << 23));
-  const float ra = a + magic;
-  const float rb = fmaf(a - (ra - magic), 4194304.f,
-                        lo * __int_as_float(e + ((44 + 127) << 23))) + magic;
-  return {some ? __float_as_int(ra) - __float_as_int(magic) : 0,
-          some ? __float_as_int(rb) - __float_as_int(magic) : 0};
-}
-__device__ __forceinline__ int64_t units(Weight w) { return ((int64_t)w.high << 22) + w.low; }
-
 // max(e - q S, 0) in the same units.
 __device__ __forceinline__ int64_t residual(int64_t e, float q, float sh, float sl) {
   constexpr float magic = 12582912.f;
@@ -192,93 +125,6 @@ __device__ __forceinline__ int64_t residual(int64_t e, float q, float sh, float 
   const int64_t r = e - units({__float_as_int(ra) - __float_as_int(magic),
                                __float_as_int(rb) - __float_as_int(magic)});
   return r > 0 ? r : 0;
-}
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int N = 4, kUnroll = 8;  // elements per 16 bytes, loads in flight
-  static constexpr uint32_t kMasked = 0xFF800000u;  // a word of -inf
-  __device__ static void unpack(const uint4& w, float* x) {
-    x[0] = __uint_as_float(w.x);
-    x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z);
-    x[3] = __uint_as_float(w.w);
-  }
-  __device__ static float one(const float* p) { return __ldg(p); }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int N = 8, kUnroll = 4;
-  static constexpr uint32_t kMasked = 0xFF80FF80u;
-  __device__ static void unpack(const uint4& w, float* x) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(v[i] << 16);
-      x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
-};
-
-// A row as 16-byte vectors on 16-byte boundaries: vector j holds elements j*N - off ..,
-// where the row starts `off` elements past a boundary.  Elements outside the row read as
-// -inf, whose weight is zero.
-template <typename T>
-struct Row {
-  const T* x;
-  int64_t V;
-  int off, n_vec;
-  __device__ Row(const T* row, int64_t vocab) : x(row), V(vocab) {
-    off = (int)(((uintptr_t)row & 15u) / sizeof(T));
-    n_vec = (int)((V + off + Vec<T>::N - 1) / Vec<T>::N);
-  }
-  // Whether token v lies in the i-th of the parts of `per` vectors that start at `from`.
-  __device__ bool in_part(int64_t v, int per, int i, int from = 0) const {
-    const int j = (int)((v + off) / Vec<T>::N) - from;
-    return j >= i * per && j < (i + 1) * per;
-  }
-  __device__ int64_t first(int j) const { return (int64_t)j * Vec<T>::N - off; }
-  __device__ bool whole(int j) const { return first(j) >= 0 && first(j) + Vec<T>::N <= V; }
-  // The vectors that lie in the row whole, [first_whole, end_whole).
-  __device__ int first_whole() const { return off > 0 ? 1 : 0; }
-  __device__ int end_whole() const { return (int)((V + off) / Vec<T>::N); }
-  __device__ uint4 raw(int j) const {  // of those
-    return __ldg(reinterpret_cast<const uint4*>(x + first(j)));
-  }
-  __device__ void load(int j, float* v) const {
-    const int64_t a = first(j);
-    if (whole(j)) {
-      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(x + a)), v);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i)
-      v[i] = a + i >= 0 && a + i < V ? Vec<T>::one(x + a + i) : -INFINITY;
-  }
-};
-
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
-__device__ __forceinline__ void st_cluster_u32(const void* local, uint32_t rank, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "r"(v)
-               : "memory");
-}
-__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "f"(v)
-               : "memory");
-}
-__device__ __forceinline__ void st_cluster_u64(const void* local, uint32_t rank, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_u32(local), rank)), "l"(v)
-               : "memory");
 }
 
 // What turns a row's logits into weights: the row's maximum, the scale 1/T (of log2) and,
@@ -332,13 +178,6 @@ __device__ __forceinline__ void weights(const Row<T>& row, const Scale& c, int j
   }
 }
 
-template <typename S>
-__device__ __forceinline__ S warp_sum(S s) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
 // Sum of the weights of vectors [j0, j1), by one warp.
 template <typename S, typename T>
 __device__ __forceinline__ S sum_range(const Row<T>& row, const Scale& c, int j0, int j1) {
@@ -357,29 +196,6 @@ __device__ __forceinline__ S sum_range(const Row<T>& row, const Scale& c, int j0
 template <typename U>
 __device__ __forceinline__ U pick(const U* two, int i) {  // slot i / 32 of lane i % 32
   return __shfl_sync(0xffffffffu, (i >> 5) ? two[1] : two[0], i & 31);
-}
-// Largest of one 64-bit key per lane.
-__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
-  const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
-  const uint32_t low =
-      __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == high ? (uint32_t)k : 0u);
-  return ((uint64_t)high << 32) | low;
-}
-// Where `target` lies among one part per lane: the lane, and what is left of the target there.
-// The last lane below `parts` takes what rounding might leave over.
-template <typename S>
-__device__ __forceinline__ int locate(S part, int parts, S* target) {
-  const int lane = threadIdx.x & 31;
-  S up_to = lane < parts ? part : (S)0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const S below = __shfl_up_sync(0xffffffffu, up_to, o);
-    if (lane >= o) up_to += below;
-  }
-  const uint32_t past = __ballot_sync(0xffffffffu, lane < parts && up_to > *target);
-  const int at = past ? __ffs(past) - 1 : parts - 1;
-  *target -= __shfl_sync(0xffffffffu, up_to - part, at);
-  return at;
 }
 __device__ __forceinline__ int64_t& target_of(Shared& sh, int64_t) { return sh.target; }
 __device__ __forceinline__ float& target_of(Shared& sh, float) { return sh.target_f; }

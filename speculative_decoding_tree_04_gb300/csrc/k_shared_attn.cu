@@ -1,0 +1,1490 @@
+// k_shared_attn.cu -- attention of sequences that share a long prefix (tv_shared_attn).
+//
+// For every (sequence, query, head) row: softmax over the visible keys of
+// scale * (q_latent . c_kv + q_pe . k_pe), then the softmax-weighted sum of c_kv rows.  The sum
+// over keys is split where the keys' owner changes: with Z_1, o_1 the sum of exponentials and
+// the weighted mean over the shared keys and Z_2, o_2 those over a sequence's own keys,
+//     out = (Z_1 o_1 + Z_2 o_2) / (Z_1 + Z_2).
+//
+// Segments and tiles.  A segment is a run of keys with the rows that read it: a group's shared
+// keys with the rows of all its sequences (consecutive in memory, since the sequences are), or a
+// sequence's own keys with its Q*H rows.  A segment's rows are cut into tiles of 128, the rows of
+// one tensor-core product; a sequence with 16 rows that sweeps the shared keys alone leaves 112
+// of them idle at every step, 64 such sequences together none.  Whole pages of the prefix are
+// shared; what is left of it in a partly filled page goes with the own keys (a fork copies that
+// page).  A group is swept together only where that saves steps (see `prepare`): with full tiles
+// anyway, 128 or more rows a sequence, it would only add partial results to join.
+//
+// A tile runs on a pair of SMs as in tv_verify_attn's tensor-core kernel (k_attn_tc.cu), whose
+// division of labour this is: 128 x 512 fp32 outputs fill an SM's tensor memory, so that
+//   rank 0 ("S side") holds the queries (latent part in TMEM, rope part in shared memory), takes
+//     S = Q K^T for 128 keys a step into one of two TMEM buffers, and the online softmax (the
+//     maximum moves only when a block exceeds it by 2^8), and ships every 64-key half's P (bf16)
+//     with the rows' rescale factors and sums to rank 1;
+//   rank 1 ("O side") accumulates O += P V in all 512 TMEM columns and writes the result.
+// Warps of a CTA: 0 loads (TMA), 1 issues MMAs, 4-7 hold a row per thread, and on rank 1 warp 2
+// clears what lies behind a segment's last key (below).  Differences from that kernel:
+//   - Keys are read page by page ({64 elements, 64 rows} boxes, two chunks of two pages per ring
+//     stage), so that no tensor maps have to be built for each call's pages.
+//   - The work is one line of (tile, step) pairs, cut into equal runs, one for each cluster:
+//     tiles of any number of keys balance to a step, and every cluster gets a contiguous run.
+//   - Every tile of a row that has more than one piece writes a partial result; join_kernel
+//     adds them up by rows.
+//
+// Keys that no row sees.  A weight of zero times a value that is not finite is NaN, and what
+// lies in a page behind the last key may be anything.  The O side clears those rows of the last
+// block in shared memory before the MMAs read it; the S side's scores of them are masked.
+//
+// Every wait is bounded, as in k_attn_tc.cu: on expiry the kernel records TV_ERR_TIMEOUT, tells
+// the peer CTA, drains its copies and tensor-core work, frees its TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "sm100_ptx.h"
+#include "tv_internal.h"
+#include "tv_testing.h"
+
+namespace tv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kDL = 512, kDR = 64, kBN = 64, kStep = 128, kRows = 128;
+constexpr int kBoxS = kBN * 128;                // a page's 64 rows x 64 bf16
+constexpr int kChunkS = 2 * kBoxS;              // 128 keys x 64 bf16 (S side)
+constexpr int kStageS = 2 * kChunkS;            // 2 latent chunks
+constexpr int kNLS = 5;                         // S-side latent ring stages
+constexpr int kChunkO = kBN * 128;              // 64 keys x 64 bf16 (O side)
+constexpr int kHalfO = 4 * kChunkO;             // 4 latent chunks of a 64-key block
+constexpr int kNLO = 4;                         // O-side latent ring stages
+// A message carries one 64-key block: P (128 rows x 64 keys bf16), then per row the
+// rescale factor and running row sum (fp32), then one flags word padded to 16 bytes.
+constexpr int kMsgAlpha = 16384, kMsgL = 16896, kMsgFlags = 17408;
+constexpr uint32_t kMsgBytes = 17424;
+constexpr int kMsgStride = 18432;               // inbox buffers (P 1024-byte aligned)
+constexpr int kNInbox = 4;
+constexpr int kNStg = 2;                        // S-side staging buffers (one step)
+constexpr int kThreads = 256;
+// Shared memory, from offset 0 in each CTA.  Rank 0: latent ring, rope stage, the tile's
+// rope queries, staging.  Rank 1: latent ring, inbox, the epilogue's staging chunks.
+constexpr int kRopeOff = kNLS * kStageS;
+constexpr int kQropeOff = kRopeOff + kChunkS;
+constexpr int kStgOff = kQropeOff + kRows * 128;
+constexpr int kSideA = kStgOff + kNStg * (int)kMsgBytes;
+constexpr int kInboxOff = kNLO * kHalfO;
+constexpr int kEpiOff = kInboxOff + kNInbox * kMsgStride;
+constexpr int kSideMax = kSideA;
+static_assert(kEpiOff + 4 * 32 * 32 * 4 <= kSideMax, "epilogue staging must fit");
+
+constexpr uint32_t kTmQ = 0, kTmS0 = 256, kTmS1 = 384;       // S-side TMEM columns
+constexpr uint32_t kFlagRescale = 2;
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // deadline of every wait (wall clock)
+constexpr uint64_t kDrainNs = 2000000000ull;    // deadline of the exit drains
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 256, 0, 1);
+
+constexpr int kMaxClusters = 256;
+
+struct Params {
+  const int32_t* page_table;  // null: contiguous
+  int64_t kv_stride;
+  int32_t max_pages, num_pages, num_rows;
+  int32_t B, H, Q, R;  // R = Q * H rows of a sequence
+  const uint64_t* anc;
+  void* out;
+  int32_t out_bf16;
+  float* lse;
+  float* part_out;     // partial results [part row][512]
+  float* part_lse;
+  int32_t* status;
+  const int4* items;   // three records each, see Item
+  const int32_t* cl_start;  // cluster c takes items cl_start[c] .. cl_start[c+1]-1
+  float scale_log2;
+  uint64_t timeout_ns;        // deadline of every wait
+  int32_t test_skip_loads;    // testing hook: the S-side producer issues no key loads
+  int32_t* test_exit_counts;  // testing hook: [CTAs that left, CTAs that left aborted]
+};
+
+struct Shared {
+  uint64_t slat_full[kNLS], slat_empty[kNLS];
+  uint64_t olat_full[kNLO], olat_empty[kNLO];
+  uint64_t rope_full, rope_empty;
+  uint64_t s_full[2], s_empty[2];
+  uint64_t qr_full, q_free, pdst_free[kNInbox];
+  uint64_t p_full[kNInbox];
+  uint64_t drain, job_full, corr_done, epi_done, dirty, clean, final_bar;
+  uint64_t timeout_ns;
+  uint32_t tmem_base;
+  volatile int abort;
+  volatile int job_type, job_buf;
+};
+constexpr int kSmemBytes = kSideMax + (int)((sizeof(Shared) + 15) / 16 * 16);
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+
+// A work item: steps s0 .. s1-1 (128 keys each) of a segment for one tile of its rows.
+//   record 0: {first row, rows, sequence whose pages hold the keys, first 64-key block}
+//   record 1: {s0, s1, keys of the segment, 1: the row's only piece, written to the output}
+//   record 2: {first part row, keys every row sees, sequence of the rows (-1: a group's), 0}
+struct Item {
+  int row0, nrows, seq, blk0;  // blk0: block of the sequence's keys where this item starts
+  int key0, nkeys;             // first key within the segment, keys of the segment
+  int nb, ns;                  // 64-key blocks and steps of this item
+  int direct, part, pv, mseq;
+  int tail;                    // keys of its last block if that is the segment's and not full
+};
+
+__device__ __noinline__ Item decode(const Params& p, int item) {
+  const int4 a = __ldg(p.items + 3 * item), b = __ldg(p.items + 3 * item + 1),
+             c = __ldg(p.items + 3 * item + 2);
+  Item it;
+  it.row0 = a.x;
+  it.nrows = a.y;
+  it.seq = a.z;
+  it.blk0 = a.w + 2 * b.x;
+  it.key0 = b.x * kStep;
+  it.nkeys = b.z;
+  const int blocks = (b.z + kBN - 1) / kBN;
+  it.nb = min(2 * b.y, blocks) - 2 * b.x;
+  it.ns = b.y - b.x;
+  it.direct = b.w;
+  it.part = c.x;
+  it.pv = c.y;
+  it.mseq = c.z;
+  it.tail = 2 * b.y >= blocks ? b.z % kBN : 0;
+  return it;
+}
+
+// Item taken by cluster `cid` in round r, or -1 when it has none left.
+__device__ __forceinline__ int item_at(const Params& p, int r, int cid) {
+  const int k = __ldg(p.cl_start + cid) + r;
+  return k < __ldg(p.cl_start + cid + 1) ? k : -1;
+}
+
+// Cache row of the first key of the item's block j.  A page outside the cache gives a row past
+// its end, which a TMA load reads as zeros.
+__device__ __forceinline__ int block_row(const Params& p, const Item& it, int j) {
+  const int blk = it.blk0 + j;
+  if (!p.page_table) return (int)(it.seq * p.kv_stride + (int64_t)blk * kBN);
+  const int pg = __ldg(p.page_table + (int64_t)it.seq * p.max_pages + blk);
+  if (pg >= 0 && pg < p.num_pages) return pg * kBN;
+  report(p.status, TV_ERR_BOUNDS);
+  return p.num_rows;
+}
+
+__device__ __forceinline__ void raise_abort(Shared& sh, int32_t* status, int code) {
+  if (!sh.abort) {
+    sh.abort = 1;
+    report(status, code);
+    // tell the peer CTA so that its waits end quickly too
+    const uint32_t peer = map_to_rank(smem_u32((const void*)&sh.abort), cluster_rank() ^ 1u);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer), "r"(1) : "memory");
+  }
+}
+
+// Bounded wait on phase `parity` of a local mbarrier: one inline probe, then an out-of-line
+// polling loop with a wall-clock deadline (kept out of line to keep hot loops small).
+__device__ __noinline__ bool wait_bar_slow(Shared& sh, uint32_t a, uint32_t parity,
+                                           int32_t* status) {
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(a, parity)) return true;
+    if (sh.abort) return false;
+    if (globaltimer() - t0 > sh.timeout_ns) {
+      raise_abort(sh, status, TV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// Exit drain: wait for phase `parity` of a barrier that asynchronous work (a TMA load, the
+// tensor cores) still has to complete, whether or not the kernel is aborting, so that no
+// copy or MMA is in flight when the CTA frees its tensor memory and leaves.  Bounded by its
+// own deadline; if that runs out the kernel reports TV_ERR_TIMEOUT and leaves anyway.
+__device__ __noinline__ void drain_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer() - t0 > kDrainNs) {
+      report(status, TV_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// Drain a ring of n stages whose full barriers got `count` loads so far: the last issue of
+// each stage may still be in flight (earlier ones were consumed before it was re-armed).
+__device__ __noinline__ void drain_ring(uint64_t* full, uint32_t n, uint32_t count,
+                                        int32_t* status) {
+  for (uint32_t k = 0; k < n && k < count; ++k) {
+    const uint32_t u = count - 1 - k;
+    drain_wait(&full[u % n], (u / n) & 1, status);
+  }
+}
+
+__device__ __forceinline__ bool wait_bar(Shared& sh, uint64_t* bar, uint32_t parity,
+                                         int32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  return wait_bar_slow(sh, a, parity, status);
+}
+
+// Same, for a barrier that only this CTA's threads, TMA loads and MMAs complete.
+__device__ __forceinline__ bool wait_bar_cta(Shared& sh, uint64_t* bar, uint32_t parity,
+                                             int32_t* status) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_cta(a, parity)) return true;
+  return wait_bar_slow(sh, a, parity, status);
+}
+
+// Visibility of keys key0 .. key0+63 for a row whose node has ancestor bitset `anc`: bit k
+// set iff key0 + k < k1 and (key0 + k is a prefix key, or the tree node key0 + k - P is an
+// ancestor-or-self of the row's node).
+__device__ __forceinline__ uint64_t block_vis(int64_t key0, int64_t P, int64_t k1, uint64_t anc) {
+  const int64_t np = P - key0;
+  const uint64_t pm = np >= 64 ? ~0ull : (np <= 0 ? 0ull : ((1ull << np) - 1));
+  const int64_t sh = key0 - P;
+  const uint64_t tm = sh >= 0 ? (sh >= 64 ? 0ull : (anc >> sh)) : (-sh >= 64 ? 0ull : (anc << (-sh)));
+  const int64_t nr = k1 - key0;
+  const uint64_t rm = nr >= 64 ? ~0ull : (nr <= 0 ? 0ull : ((1ull << nr) - 1));
+  return (pm | tm) & rm;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// One 64-key half of a step: p = 2^(s*c - mr) for the 64 scores (masked ones are -inf),
+// packed to bf16 into this row of a staging buffer (swizzled K-major layout); returns the
+// sum.
+__device__ __forceinline__ float emit_half(const float* t, float c, float mr, unsigned char* row,
+                                           uint32_t sw) {
+  const uint64_t cc = f2_pack(c, c), nm = f2_pack(-mr, -mr);
+  uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x0, x1;
+      f2_unpack(f2_fma(f2_pack(t[8 * q + 2 * e], t[8 * q + 2 * e + 1]), cc, nm), x0, x1);
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      s2[e & 1] = f2_add(s2[e & 1], f2_pack(p0, p1));
+      w[e] = pack_bf16(p0, p1);
+    }
+    *reinterpret_cast<uint4*>(row + (((uint32_t)q ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  float a0, a1, b0, b1;
+  f2_unpack(s2[0], a0, a1);
+  f2_unpack(s2[1], b0, b1);
+  return (a0 + a1) + (b0 + b1);
+}
+
+// Masked keys of a 64-key half get score -inf.
+__device__ __forceinline__ void apply_mask(float* t, uint64_t vis) {
+  if (vis == ~0ull) return;
+  const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) t[k] = ((lo >> k) & 1u) ? t[k] : -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) t[32 + k] = ((hi >> k) & 1u) ? t[32 + k] : -INFINITY;
+}
+
+// ===================================================================================
+// rank 0: QK^T + softmax
+// ===================================================================================
+__device__ void s_side(const Params& p, const CUtensorMap* map_lat, const CUtensorMap* map_kpe,
+                       const CUtensorMap* map_q, const CUtensorMap* map_qr, Shared& sh,
+                       unsigned char* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* lat = smem;
+  unsigned char* rope = smem + kRopeOff;
+  unsigned char* qrope = smem + kQropeOff;
+  const int cid = (int)cluster_id_x();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 0) {
+    // ---------------- TMA producer: two latent chunks of two pages per stage ------------
+    // Each item starts with its latent queries, which pass through the key ring on their way
+    // into TMEM, and its rope queries, which go straight to their buffer once the previous
+    // item's MMAs are done with it.
+    if (lane == 0) {
+      prefetch_tensormap(map_lat);
+      prefetch_tensormap(map_kpe);
+      prefetch_tensormap(map_q);
+      prefetch_tensormap(map_qr);
+      uint32_t u = 0, rc = 0, qi = 0;
+      auto produce = [&]() {
+        for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
+          const Item it = decode(p, item);
+          // rows of the pages are looked up a step ahead
+          int next0 = block_row(p, it, 0), next1 = it.nb > 1 ? block_row(p, it, 1) : 0;
+          for (int h = 0; h < 4; ++h, ++u) {
+            const uint32_t st = u % kNLS;
+            if (!wait_bar(sh, &sh.slat_empty[st], ((u / kNLS) & 1) ^ 1, p.status)) return;
+            mbar_arrive_expect_tx(&sh.slat_full[st], kStageS);
+            tma_load_3d(lat + st * kStageS, map_q, 0, it.row0, 2 * h, &sh.slat_full[st]);
+          }
+          if (!wait_bar_cta(sh, &sh.q_free, (qi & 1) ^ 1, p.status)) return;
+          ++qi;
+          mbar_arrive_expect_tx(&sh.qr_full, kRows * 128);
+          tma_load_2d(qrope, map_qr, 0, it.row0, &sh.qr_full);
+          for (int j = 0; j < it.ns; ++j, ++rc) {
+            const int row0 = next0, row1 = next1;
+            const bool two = 2 * j + 1 < it.nb;
+            if (j + 1 < it.ns) {
+              next0 = block_row(p, it, 2 * j + 2);
+              if (2 * j + 3 < it.nb) next1 = block_row(p, it, 2 * j + 3);
+            }
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h, ++u) {
+              const uint32_t st = u % kNLS;
+              if (!wait_bar(sh, &sh.slat_empty[st], ((u / kNLS) & 1) ^ 1, p.status)) return;
+              unsigned char* dst = lat + st * kStageS;
+              mbar_arrive_expect_tx(&sh.slat_full[st], two ? kStageS : kStageS / 2);
+              tma_load_3d(dst, map_lat, 0, row0, 2 * h, &sh.slat_full[st]);
+              tma_load_3d(dst + kChunkS, map_lat, 0, row0, 2 * h + 1, &sh.slat_full[st]);
+              if (two) {
+                tma_load_3d(dst + kBoxS, map_lat, 0, row1, 2 * h, &sh.slat_full[st]);
+                tma_load_3d(dst + kChunkS + kBoxS, map_lat, 0, row1, 2 * h + 1, &sh.slat_full[st]);
+              }
+            }
+            if (!wait_bar(sh, &sh.rope_empty, (rc & 1) ^ 1, p.status)) return;
+            mbar_arrive_expect_tx(&sh.rope_full, two ? kChunkS : kBoxS);
+            tma_load_2d(rope, map_kpe, 0, row0, &sh.rope_full);
+            if (two) tma_load_2d(rope + kBoxS, map_kpe, 0, row1, &sh.rope_full);
+          }
+        }
+      };
+      if (!p.test_skip_loads) produce();
+      // leave no load in flight (after an abort the consumers stop taking stages; in a
+      // normal run these phases have completed already)
+      drain_ring(sh.slat_full, kNLS, u, p.status);
+      drain_ring(&sh.rope_full, 1, rc, p.status);
+      drain_ring(&sh.qr_full, 1, qi, p.status);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: S = Q K^T, 128 keys per step ----------------------
+    if (lane == 0) {
+      // The issuing thread must keep the tensor pipe's queue fed, so its loop is kept lean:
+      // stage index, phase and descriptor advance incrementally, and the MMAs of a stage
+      // add constant offsets to one descriptor (address bits 4..17 sit in its low field,
+      // which these offsets never overflow).
+      uint32_t sc = 0, qc = 0, rc = 0, st = 0, sph = 0;
+      const uint64_t dq = smem_desc(smem_u32(qrope), 16, 1024, 2);
+      const uint64_t dr = smem_desc(smem_u32(rope), 16, 1024, 2);
+      const uint64_t dl0 = smem_desc(smem_u32(lat), 16, 1024, 2);
+      uint64_t db = dl0;
+      for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
+        const Item it = decode(p, item);
+        // The tile's latent queries arrive through the key ring as four stages; they are
+        // copied into TMEM once the previous tile's MMAs have finished reading it.
+        if (!wait_bar_cta(sh, &sh.q_free, (qc & 1) ^ 1, p.status)) break;
+        tc_fence_after();
+        bool okq = true;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          if (!wait_bar_cta(sh, &sh.slat_full[st], sph, p.status)) { okq = false; break; }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tmem_cp_128x256b(tmem + kTmQ + 32 * (2 * h + c) + 8 * kk,
+                               db + (uint64_t)((c * kChunkS + 32 * kk) >> 4));
+          mma_commit(&sh.slat_empty[st]);
+          db += kStageS >> 4;
+          if (++st == kNLS) {
+            st = 0;
+            sph ^= 1;
+            db = dl0;
+          }
+        }
+        if (!okq || !wait_bar_cta(sh, &sh.qr_full, qc & 1, p.status)) break;
+        // (no abort test in the loop condition: every wait below returns false once the
+        // abort flag is up, and a shared-memory load per step on this thread's critical
+        // path cost about 3 % of the whole kernel)
+        for (int j = 0; j < it.ns; ++j, ++sc, ++rc) {
+          const uint32_t sb = sc & 1;
+          if (!wait_bar_cta(sh, &sh.s_empty[sb], ((sc >> 1) & 1) ^ 1, p.status)) break;
+          tc_fence_after();  // the softmax warps' TMEM reads of this S buffer come first
+          const uint32_t d = tmem + (sb ? kTmS1 : kTmS0);
+          bool ok = true;
+          // (one stage per iteration, not unrolled: see the note on code size in the softmax)
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            if (!wait_bar_cta(sh, &sh.slat_full[st], sph, p.status)) { ok = false; break; }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(d, tmem + kTmQ + 32 * (2 * h + c) + 8 * kk,
+                       db + (uint64_t)((c * kChunkS + 32 * kk) >> 4), kIdescQK, (h | c | kk) != 0);
+            mma_commit(&sh.slat_empty[st]);
+            db += kStageS >> 4;
+            if (++st == kNLS) {
+              st = 0;
+              sph ^= 1;
+              db = dl0;
+            }
+          }
+          if (!ok || !wait_bar_cta(sh, &sh.rope_full, rc & 1, p.status)) break;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(d, dq + (uint64_t)((32 * kk) >> 4), dr + (uint64_t)((32 * kk) >> 4), kIdescQK, 1);
+          mma_commit(&sh.rope_empty);
+          mma_commit(&sh.s_full[sb]);
+        }
+        mma_commit(&sh.q_free);
+        ++qc;
+      }
+      // every MMA and TMEM copy this thread issued completes before tensor memory is freed
+      mma_commit(&sh.final_bar);
+      drain_wait(&sh.final_bar, 0, p.status);
+    }
+  } else if (warp >= 4) {
+    // ---------------- softmax warpgroup: thread r owns tile row r ------------------
+    const int wq = warp - 4;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const float c = p.scale_log2;
+    const uint32_t peer = cluster_rank() ^ 1u;
+    // the peer's inbox; this row's place in a message (swizzled K-major P)
+    const uint32_t inbox_peer = map_to_rank(smem_u32(smem + kInboxOff), peer);
+    unsigned char* stg = smem + kStgOff;
+    const uint32_t row_off = (uint32_t)((r >> 3) * 1024 + (r & 7) * 128);
+    const uint32_t sw = (uint32_t)(r & 7);
+    bool ok0 = true;  // thread 0: its last inbox waits and copies went through
+    // The four warps leave their loops only together, at a 128-thread barrier that agrees
+    // on the outcome of the waits before it (a warp that left alone would strand the
+    // others at the next barrier).
+    uint32_t sc = 0, mc = 0;
+    bool live = true;
+    int item_next = item_at(p, 0, cid);
+    for (int rr = 0; item_next >= 0 && live; ++rr) {
+      const Item it = decode(p, item_next);
+      item_next = item_at(p, rr + 1, cid);
+      const bool vrow = r < it.nrows;
+      // the only piece's lse goes to the output, others to their part
+      float* lse_dst = !it.direct ? p.part_lse + it.part + r : p.lse ? p.lse + it.row0 + r : nullptr;
+      uint64_t anc = 0;
+      int64_t pv = it.pv;
+      if (vrow && it.mseq >= 0) {
+        // own keys: the prefix and the row's ancestors, or (no anc) all up to its own token
+        const int node = (it.row0 + r - it.mseq * p.R) / p.H;
+        if (p.anc) anc = p.anc[(int64_t)it.mseq * p.Q + node];
+        else pv += node + 1;
+      }
+      const int64_t k1 = it.nkeys;
+
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.ns; ++j, ++sc) {
+        const uint32_t sb = sc & 1;
+        // each warp agrees before its warp-collective TMEM loads
+        const bool okf =
+            __all_sync(0xffffffffu, wait_bar(sh, &sh.s_full[sb], (sc >> 1) & 1, p.status));
+        float t[128];
+        if (!okf) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) t[k] = 0.f;
+        } else {
+          tc_fence_after();
+          uint32_t sr[128];
+          const uint32_t ta = tmem + lane_base + (sb ? kTmS1 : kTmS0);
+          tmem_ld32(ta, sr);
+          tmem_ld32(ta + 32, sr + 32);
+          tmem_ld32(ta + 64, sr + 64);
+          tmem_ld32(ta + 96, sr + 96);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 128; ++k) t[k] = __uint_as_float(sr[k]);
+        }
+        const bool two = 2 * j + 1 < it.nb;
+        const int64_t key0 = it.key0 + (int64_t)j * kStep;
+        const uint64_t vis0 =
+            (key0 + kBN > pv || key0 + kBN > k1) ? block_vis(key0, pv, k1, anc) : ~0ull;
+        const uint64_t vis1 =
+            !two ? 0ull
+                 : ((key0 + 2 * kBN > pv || key0 + 2 * kBN > k1)
+                        ? block_vis(key0 + kBN, pv, k1, anc)
+                        : ~0ull);
+        apply_mask(t, vis0);
+        apply_mask(t + 64, vis1);
+        float mx;
+        {
+          // 128 -> 43 -> 15 -> 5 -> 2 -> 1 with three-input maxima
+          float a[43];
+#pragma unroll
+          for (int i = 0; i < 42; ++i) a[i] = fmax3(t[3 * i], t[3 * i + 1], t[3 * i + 2]);
+          a[42] = fmaxf(t[126], t[127]);
+#pragma unroll
+          for (int i = 0; i < 14; ++i) a[i] = fmax3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+          a[14] = a[42];
+#pragma unroll
+          for (int i = 0; i < 5; ++i) a[i] = fmax3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+          mx = fmax3(a[0], a[1], fmaxf(a[2], fmaxf(a[3], a[4]))) * c;  // block max in log2 units
+        }
+        // The running max m moves only when the block max exceeds it by more than 2^8;
+        // then O and l are rescaled by alpha = 2^(m_old - m_new).
+        float alpha = 1.f;
+        if (mx > (m == -INFINITY ? -INFINITY : m + kRescaleThreshold)) {
+          if (l > 0.f) alpha = ex2(m - mx);
+          m = mx;
+        }
+        const float mr = m == -INFINITY ? 0.f : m;
+
+        // ---- messages: P, alpha, l into the two staging buffers, then bulk copies ----
+        // Thread 0 issued the previous step's copies; once they have read the staging
+        // buffers, the barrier below lets everyone overwrite them.  The barriers also OR
+        // the rescale flag and agree on whether to go on.
+        if (r == 0) bulk_wait_read<0>();
+        const bool resc = named_sync_or(1, 128, alpha != 1.f);
+        if (!named_sync_and(2, 128, okf && ok0 && !sh.abort)) {
+          live = false;
+          break;
+        }
+        unsigned char* stg1 = stg + kMsgBytes;
+        // Code size matters here: the S side's hot loops (producer, MMA issue, softmax) run
+        // on one SM at once, and when they outgrow its instruction cache the misses of all
+        // its SMs queue at the GPC's shared cache (measured: 80 % of that cache's request
+        // rate, 25 % of fetches missing, every SM pair slowed by where it sits in the GPC).
+        // So the two 64-key halves go through one copy of the exponent code, each half's
+        // scores read from tensor memory again (the registers above are only for the max);
+        // the S buffer is released after that second read.
+        float sum = 0.f;
+        {
+          const uint32_t ta = tmem + lane_base + (sb ? kTmS1 : kTmS0);
+#pragma unroll 1
+          for (int hh = 0; hh < (two ? 2 : 1); ++hh) {
+            uint32_t hr[64];
+            float h64[64];
+            const uint32_t col = hh ? 64u : 0u;
+            tmem_ld32(ta + col, hr);
+            tmem_ld32(ta + col + 32, hr + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 64; ++k) h64[k] = __uint_as_float(hr[k]);
+            apply_mask(h64, hh ? vis1 : vis0);
+            sum += emit_half(h64, c, mr, stg + hh * kMsgBytes + row_off, sw);
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.s_empty[sb]);
+        }
+        l = l * alpha + sum;
+        reinterpret_cast<float*>(stg + kMsgAlpha)[r] = alpha;
+        reinterpret_cast<float*>(stg + kMsgL)[r] = l;
+        if (r == 0) *reinterpret_cast<uint4*>(stg + kMsgFlags) = make_uint4(resc ? kFlagRescale : 0u, 0u, 0u, 0u);
+        if (two) {
+          reinterpret_cast<float*>(stg1 + kMsgAlpha)[r] = 1.f;
+          reinterpret_cast<float*>(stg1 + kMsgL)[r] = l;
+          if (r == 0) *reinterpret_cast<uint4*>(stg1 + kMsgFlags) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (j == it.ns - 1 && vrow && lse_dst)  // the piece's log-sum-exp (a NaN stays one)
+          *lse_dst = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        fence_proxy_async_smem();  // the bulk copies read the staging through the async proxy
+        named_sync(3, 128);
+        if (r == 0) {
+          // each message goes to the next inbox buffer once rank 1 has released it
+          for (int k = 0; k < (two ? 2 : 1) && ok0; ++k) {
+            const uint32_t mk = mc + k, ib = mk % kNInbox;
+            ok0 = wait_bar(sh, &sh.pdst_free[ib], ((mk / kNInbox) & 1) ^ 1, p.status);
+            if (ok0)
+              bulk_copy_to_cluster(inbox_peer + ib * kMsgStride, stg + k * kMsgBytes, kMsgBytes,
+                                   map_to_rank(smem_u32(&sh.p_full[ib]), peer));
+          }
+          bulk_commit();
+        }
+        mc += two ? 2 : 1;
+      }
+      if (!live) break;
+    }
+    if (r == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+}
+
+// ===================================================================================
+// rank 1: O += P V, rescale, epilogue
+// ===================================================================================
+__device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
+                       unsigned char* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* lat = smem;
+  unsigned char* inbox = smem + kInboxOff;
+  const int cid = (int)cluster_id_x();
+  const uint32_t tmem = sh.tmem_base;
+
+  if (warp == 0) {
+    // ---------------- TMA producer: each 64-key block's latent chunks, in message order --
+    if (lane == 0) {
+      prefetch_tensormap(map_lat);
+      uint32_t u = 0;
+      auto produce = [&]() {
+        for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
+          const Item it = decode(p, item);
+          // cache rows of the blocks are looked up two ahead
+          int next0 = block_row(p, it, 0), next1 = it.nb > 1 ? block_row(p, it, 1) : 0;
+          for (int j = 0; j < it.nb; ++j) {
+            const int row0 = next0;
+            next0 = next1;
+            if (j + 2 < it.nb) next1 = block_row(p, it, j + 2);
+            for (int h = 0; h < 2; ++h, ++u) {
+              const uint32_t ls = u % kNLO;
+              if (!wait_bar(sh, &sh.olat_empty[ls], ((u / kNLO) & 1) ^ 1, p.status)) return;
+              mbar_arrive_expect_tx(&sh.olat_full[ls], kHalfO);
+              tma_load_3d(lat + ls * kHalfO, map_lat, 0, row0, 4 * h, &sh.olat_full[ls]);
+            }
+          }
+        }
+      };
+      produce();
+      drain_ring(sh.olat_full, kNLO, u, p.status);  // no load left in flight
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer: O += P V ------------------------------------------
+    if (lane == 0) {
+      const uint32_t peer = cluster_rank() ^ 1u;
+      uint32_t vc = 0, mc = 0, ic = 0, dc = 0, cc = 0, nc = 0, last_pb = 0;
+      for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
+        const Item it = decode(p, item);
+        if (ic > 0) {
+          // the previous tile's epilogue has read its last message: hand that buffer back
+          if (!wait_bar(sh, &sh.epi_done, (ic - 1) & 1, p.status)) break;
+          mbar_arrive_remote(map_to_rank(smem_u32(&sh.pdst_free[last_pb]), peer));
+        }
+        tc_fence_after();
+        bool ok = true;
+        for (int j = 0; j < it.nb && ok; ++j, ++mc) {
+          const uint32_t pb = mc % kNInbox;
+          last_pb = pb;
+          if (!wait_bar(sh, &sh.p_full[pb], (mc / kNInbox) & 1, p.status)) { ok = false; break; }
+          // arm the buffer's next phase now: its next message is only sent after the MMAs
+          // below have read this one
+          mbar_arrive_expect_tx(&sh.p_full[pb], kMsgBytes);
+          // The message arrived by a bulk copy, in the async proxy the MMAs read through, so
+          // this fence is not required for ordering; a variant without it (flags loaded
+          // before the re-arm) measured about 1 % slower, so it stays.
+          fence_proxy_async_smem();
+          const uint32_t flags =
+              *reinterpret_cast<volatile uint32_t*>(inbox + pb * kMsgStride + kMsgFlags);
+          if (j > 0 && (flags & kFlagRescale)) {
+            mma_commit(&sh.drain);
+            if (!wait_bar(sh, &sh.drain, dc & 1, p.status)) { ok = false; break; }
+            ++dc;
+            sh.job_type = 1;
+            sh.job_buf = (int)pb;
+            mbar_arrive(&sh.job_full);
+            if (!wait_bar(sh, &sh.corr_done, cc & 1, p.status)) { ok = false; break; }
+            ++cc;
+            tc_fence_after();
+          }
+          if (j == it.nb - 1 && it.tail) {
+            // the last block: warp 2 clears the rows behind the last key
+            for (uint32_t w = vc; w < vc + 2 && ok; ++w)
+              ok = wait_bar(sh, &sh.olat_full[w % kNLO], (w / kNLO) & 1, p.status);
+            if (!ok) break;
+            mbar_arrive(&sh.dirty);
+            if (!wait_bar(sh, &sh.clean, nc & 1, p.status)) { ok = false; break; }
+            ++nc;
+          }
+          const uint32_t pa = smem_u32(inbox + pb * kMsgStride);
+          for (int h = 0; h < 2; ++h, ++vc) {
+            const uint32_t st = vc % kNLO;
+            if (!wait_bar(sh, &sh.olat_full[st], (vc / kNLO) & 1, p.status)) { ok = false; break; }
+            const uint32_t va = smem_u32(lat + st * kHalfO);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss(tmem + 256 * h, smem_desc(pa + 32 * kk, 16, 1024, 2),
+                     smem_desc(va + 2048 * kk, 8192, 1024, 2), kIdescPV, (j | kk) != 0);
+            mma_commit(&sh.olat_empty[st]);
+          }
+          // once the MMAs have read the message, the buffer goes straight back to rank 0's
+          // softmax; a tile's last message stays until the epilogue has read its row sums
+          if (j < it.nb - 1) mma_commit_multicast(&sh.pdst_free[pb], (uint16_t)(1u << peer));
+        }
+        if (!ok) break;
+        mma_commit(&sh.drain);
+        if (!wait_bar(sh, &sh.drain, dc & 1, p.status)) break;
+        ++dc;
+        sh.job_type = 2;
+        sh.job_buf = (int)last_pb;
+        mbar_arrive(&sh.job_full);
+        ++ic;
+      }
+      if (!sh.abort && ic > 0) wait_bar(sh, &sh.epi_done, (ic - 1) & 1, p.status);
+      sh.job_type = 0;  // exit
+      mbar_arrive(&sh.job_full);
+      mma_commit(&sh.final_bar);
+      drain_wait(&sh.final_bar, 0, p.status);
+    }
+  } else if (warp == 2) {
+    // ---------------- clears the rows behind a segment's last key ----------------------
+    uint32_t vc = 0, nc = 0;  // ring stages before this item; blocks cleared
+    for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0; ++rr) {
+      const Item it = decode(p, item);
+      vc += 2 * it.nb;
+      if (!it.tail) continue;
+      // (the MMA thread has seen both stages of the block arrive)
+      if (!__all_sync(0xffffffffu, lane != 0 || wait_bar(sh, &sh.dirty, nc & 1, p.status))) return;
+      ++nc;
+      const int pieces = (kBN - it.tail) * 8;
+      for (uint32_t u = vc - 2; u < vc; ++u) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // (the swizzle moves 16-byte pieces within a row: whole rows are cleared)
+          uint4* rows = reinterpret_cast<uint4*>(lat + (u % kNLO) * kHalfO + c * kChunkO +
+                                                 it.tail * 128);
+          for (int i = lane; i < pieces; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();  // the MMAs read through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.clean);
+    }
+  } else if (warp >= 4) {
+    // ---------------- rescale / epilogue warpgroup: thread r owns tile row r -------
+    const int wq = warp - 4;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    uint32_t jc = 0;
+    for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
+      const Item it = decode(p, item);
+      for (;;) {
+        // the four warps work on disjoint TMEM lanes; each warp agrees on the outcome
+        if (!__all_sync(0xffffffffu, wait_bar(sh, &sh.job_full, jc & 1, p.status))) return;
+        ++jc;
+        const int type = sh.job_type, pb = sh.job_buf;
+        tc_fence_after();
+        if (type == 1) {
+          const float alpha = reinterpret_cast<const float*>(inbox + pb * kMsgStride + kMsgAlpha)[r];
+          // warp-uniform decision: the TMEM loads and stores below are warp-collective
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              uint32_t v[32];
+              __syncwarp();
+              tmem_ld32(tmem + lane_base + 32 * c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st32(tmem + lane_base + 32 * c, v);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.corr_done);
+        } else if (type == 2) {
+          const float lr = reinterpret_cast<const float*>(inbox + pb * kMsgStride + kMsgL)[r];
+          const float inv = lr == 0.f ? 0.f : 1.f / lr;  // (a NaN stays one)
+          // Each thread holds its own row (TMEM lane), so storing straight from registers
+          // would make every warp store touch 32 rows.  Each 32-row x 32-column chunk is
+          // staged in shared memory instead (16-byte pieces XOR-swizzled by row, so that both
+          // the writes and the reads below are free of bank conflicts) and written back with
+          // lanes along the columns: every store instruction fills four whole 128-byte lines.
+          float* stg = reinterpret_cast<float*>(smem + kEpiOff) + wq * 1024;
+          const int rows_ok = it.nrows - wq * 32;    // valid rows of the warp's 32
+          // the output's row of lane 0 (its only piece), or the part's
+          const int64_t row0 = (int64_t)(it.direct ? it.row0 : it.part) + wq * 32;
+          float* dst0 = (it.direct ? (float*)p.out : p.part_out) + row0 * kDL;
+          __nv_bfloat16* dst16 =
+              it.direct && p.out_bf16 ? (__nv_bfloat16*)p.out + row0 * kDL : nullptr;
+          const int rr4 = lane >> 3, jj = lane & 7;
+          auto put_chunk = [&](const uint32_t* v, int c) {
+            __syncwarp();  // the previous chunk's reads of the staging are done
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(stg + lane * 32 + ((e ^ (lane & 7)) << 2)) =
+                  make_float4(__uint_as_float(v[4 * e]) * inv, __uint_as_float(v[4 * e + 1]) * inv,
+                              __uint_as_float(v[4 * e + 2]) * inv, __uint_as_float(v[4 * e + 3]) * inv);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 4 * i + rr4;
+              const float4 x = *reinterpret_cast<const float4*>(stg + row * 32 + ((jj ^ (row & 7)) << 2));
+              if (row >= rows_ok) continue;
+              const int64_t at = (int64_t)row * kDL + 32 * c + 4 * jj;
+              if (dst16)
+                *reinterpret_cast<uint2*>(dst16 + at) =
+                    make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+              else
+                *reinterpret_cast<float4*>(dst0 + at) = x;
+            }
+          };
+          // two chunks in flight: each TMEM load overlaps the previous chunk's stores
+          uint32_t va[32], vb[32];
+          tmem_ld32(tmem + lane_base, va);
+          tmem_wait_ld_regs(va);
+#pragma unroll 1
+          for (int c = 0; c < 16; c += 2) {
+            tmem_ld32(tmem + lane_base + 32 * (c + 1), vb);
+            put_chunk(va, c);
+            tmem_wait_ld_regs(vb);
+            if (c + 2 < 16) tmem_ld32(tmem + lane_base + 32 * (c + 2), va);
+            put_chunk(vb, c + 1);
+            if (c + 2 < 16) tmem_wait_ld_regs(va);
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.epi_done);
+          break;
+        } else {
+          return;  // exit job (only after an abort)
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s,
+               const __grid_constant__ CUtensorMap map_kpe_s,
+               const __grid_constant__ CUtensorMap map_lat_o,
+               const __grid_constant__ CUtensorMap map_q,
+               const __grid_constant__ CUtensorMap map_qr) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023u) {  // both CTAs see the same layout, so both leave here
+    if (threadIdx.x == 0) report(p.status, TV_ERR_UNSUPPORTED);
+    return;
+  }
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kSideMax);
+  const uint32_t rank = cluster_rank();
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNLS; ++i) {
+      mbar_init(&sh.slat_full[i], 1);
+      mbar_init(&sh.slat_empty[i], 1);
+    }
+    for (int i = 0; i < kNLO; ++i) {
+      mbar_init(&sh.olat_full[i], 1);
+      mbar_init(&sh.olat_empty[i], 1);
+    }
+    mbar_init(&sh.rope_full, 1);
+    mbar_init(&sh.rope_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], 128);
+    }
+    for (int i = 0; i < kNInbox; ++i) {
+      mbar_init(&sh.pdst_free[i], 1);
+      mbar_init(&sh.p_full[i], 1);
+    }
+    mbar_init(&sh.qr_full, 1);
+    mbar_init(&sh.q_free, 1);
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.job_full, 1);
+    mbar_init(&sh.corr_done, 128);
+    mbar_init(&sh.epi_done, 128);
+    mbar_init(&sh.dirty, 1);
+    mbar_init(&sh.clean, 1);
+    mbar_init(&sh.final_bar, 1);
+    sh.abort = 0;
+    sh.timeout_ns = p.timeout_ns;
+    sh.job_type = 0;
+    sh.job_buf = 0;
+    if (rank == 1) {
+      // every inbox buffer starts armed for its first message
+      for (int i = 0; i < kNInbox; ++i) mbar_arrive_expect_tx(&sh.p_full[i], kMsgBytes);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();  // barriers of both CTAs exist before any remote arrive or store
+  // The kernel may start while prepare_kernel (just before it in the stream) still runs
+  // (programmatic dependent launch): the set-up above overlaps it, and everything below
+  // reads its work records only after this wait.
+  griddep_wait();
+
+  if (rank == 0)
+    s_side(p, &map_lat_s, &map_kpe_s, &map_q, &map_qr, sh, smem);
+  else
+    o_side(p, &map_lat_o, sh, smem);
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(sh.tmem_base, 512);
+  if (p.test_exit_counts && threadIdx.x == 0) {
+    atomicAdd(p.test_exit_counts, 1);
+    if (sh.abort) atomicAdd(p.test_exit_counts + 1, 1);
+  }
+  cluster_sync();  // neither CTA leaves while the other may still touch its memory
+}
+
+// ---- the work: segments, tiles, runs ----------------------------------------------------
+// Segments are the groups (those swept together) and then the sequences; tile t of a segment
+// holds its rows 128 t .., all tiles of a segment sweep the same steps.  The tiles lie on a line,
+// each as long as its steps and kTileCost more (what starting and finishing one costs, in
+// steps); the line is cut into equal runs, one per cluster.  A cut less than kMinPiece steps from
+// an end of a tile moves there.
+// A tile's first piece, or whole tile, writes its partial result to part row (its own row, with
+// B*R rows each for the groups' and the sequences' segments); the piece that starts at cut c
+// writes to part rows 2*B*R + 128 c ...
+constexpr int kTileCost = 4;
+constexpr int kMinPiece = 2;
+constexpr int kPrepThreads = 1024;
+
+struct Segment {
+  int row0, nrows, steps, nkeys;  // rows, 128-key steps and keys
+  int seq, blk0;                  // sequence whose pages hold them, from which block on
+  int tile0;                      // tiles before this segment
+  int direct;                     // the only segment of its rows
+};
+
+struct PrepArgs {
+  const int32_t* prefix_len;
+  const int32_t* group_start;
+  const int32_t* shared_len;
+  int B, R, Q, G, T, max_prefix, ncl, max_tiles;  // T: tiles of a sequence's rows
+  int64_t seq_cap;
+  int32_t* group_of;    // [B]
+  int32_t* group_bad;   // [G]
+  Segment* seg;         // [G + B]
+  int64_t* cost;        // [G + B + 1]: of the tiles before
+  int4* seq_rec;        // [B]: {first tile of the group's segment or -1, its first row,
+                        //       first tile of the sequence's, 1: out of bounds}
+  int2* tile_rec;       // [max_tiles]: {pieces, cut at which the second one starts}
+  int4* items;
+  int32_t* cl_start;    // [ncl + 1]
+  int32_t* status;
+};
+
+// Exclusive prefix sums over the block of one (cost, tiles) pair a thread; returns the totals.
+__device__ __forceinline__ void scan_pair(int64_t& a, int& b, int64_t* sa, int* sb, int64_t& ta, int& tb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t ia = a;
+  int ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, ia, o);
+    const int y = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += x;
+      ib += y;
+    }
+  }
+  if (lane == 31) {
+    sa[warp] = ia;
+    sb[warp] = ib;
+  }
+  __syncthreads();
+  const int64_t wa = sa[lane];
+  const int wb = sb[lane];
+  int64_t pa = wa;
+  int pb = wb;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, pa, o);
+    const int y = __shfl_up_sync(0xffffffffu, pb, o);
+    if (lane >= o) {
+      pa += x;
+      pb += y;
+    }
+  }
+  ta = __shfl_sync(0xffffffffu, pa, 31);
+  tb = __shfl_sync(0xffffffffu, pb, 31);
+  a = ia - a + (warp > 0 ? __shfl_sync(0xffffffffu, pa, max(warp - 1, 0)) : 0);
+  b = ib - b + (warp > 0 ? __shfl_sync(0xffffffffu, pb, max(warp - 1, 0)) : 0);
+  __syncthreads();
+}
+
+// Last i in [0, n) with v[i] <= x (v ascends, v[0] <= x).
+template <typename V, typename X>
+__device__ __forceinline__ int last_at_most(const V* v, int n, X x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((X)v[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a) {
+  __shared__ int64_t sa[32];
+  __shared__ int sb[32];
+  __shared__ int cut_tile[kMaxClusters + 1], cut_step[kMaxClusters + 1], first[kMaxClusters + 1];
+  griddep_launch_dependents();  // the attention kernel may start its set-up now
+  const int tid = threadIdx.x, B = a.B, G = a.G, n_seg = G + B;
+  // ---- groups: which are sound ----
+  bool ok = true;
+  for (int g = tid; g < G; g += kPrepThreads) {
+    const int s = a.group_start[g], e = a.group_start[g + 1];
+    ok = ok && s >= 0 && s <= e && e <= B && (g > 0 || s == 0) && (g < G - 1 || e == B);
+    const int n = a.shared_len[g];
+    a.group_bad[g] = n < 0 || n > a.max_prefix || n > a.seq_cap;
+  }
+  const bool groups = __syncthreads_and(ok) && G > 0;
+  if (!ok) report(a.status, TV_ERR_BOUNDS);
+  auto out_of_bounds = [&](int P) {
+    return P < 0 || P > a.max_prefix || (int64_t)P + a.Q > a.seq_cap;
+  };
+  if (groups) {
+    for (int b = tid; b < B; b += kPrepThreads) {
+      // (of groups that start at b, empty ones among them, the last)
+      const int g = last_at_most(a.group_start, G, b);
+      a.group_of[b] = g;
+      if (a.shared_len[g] > a.prefix_len[b]) atomicOr(&a.group_bad[g], 1);
+    }
+  }
+  __syncthreads();
+  // ---- segments ----
+  // Together where it saves more steps than the partial results cost: a tile of the group adds
+  // about kTileCost steps, and every sequence's tile becomes a partial result as well.
+  auto shared_steps = [&](int g) {
+    if (!groups) return 0;
+    const int n = a.group_start[g + 1] - a.group_start[g];
+    if (a.group_bad[g]) return 0;
+    const int64_t steps = (a.shared_len[g] / kBN + 1) / 2;
+    const int64_t tiles = ((int64_t)n * a.R + kRows - 1) / kRows;
+    return ((int64_t)n * a.T - tiles) * steps > kTileCost * (tiles + 2) ? (int)steps : 0;
+  };
+  int64_t run_cost = 0;
+  int run_tiles = 0;
+  for (int base = 0; base < n_seg; base += kPrepThreads) {
+    const int i = base + tid;
+    Segment s{};
+    int tiles = 0;
+    if (i < G) {
+      s.steps = shared_steps(i);
+      if (groups && a.group_bad[i]) report(a.status, TV_ERR_BOUNDS);
+      if (s.steps > 0) {
+        s.seq = a.group_start[i];
+        s.row0 = s.seq * a.R;
+        s.nrows = (a.group_start[i + 1] - s.seq) * a.R;
+        s.nkeys = a.shared_len[i] / kBN * kBN;
+        tiles = (s.nrows + kRows - 1) / kRows;
+      }
+    } else if (i < n_seg) {
+      const int b = i - G, P = a.prefix_len[b];
+      if (out_of_bounds(P)) {
+        report(a.status, TV_ERR_BOUNDS);
+      } else {
+        const int g = groups ? a.group_of[b] : 0;
+        const bool shared = groups && shared_steps(g) > 0;
+        const int from = shared ? a.shared_len[g] / kBN : 0;
+        s.seq = b;
+        s.row0 = b * a.R;
+        s.nrows = a.R;
+        s.blk0 = from;
+        s.nkeys = P + a.Q - from * kBN;
+        s.steps = (s.nkeys + kStep - 1) / kStep;
+        s.direct = !shared;
+        tiles = a.T;
+      }
+    }
+    int64_t cost = (int64_t)tiles * (s.steps + kTileCost), all_cost;
+    int before = tiles, all_tiles;
+    scan_pair(cost, before, sa, sb, all_cost, all_tiles);
+    if (i < n_seg) {
+      s.tile0 = run_tiles + before;
+      a.seg[i] = s;
+      a.cost[i] = run_cost + cost;
+      if (i >= G) a.seq_rec[i - G] = make_int4(-1, 0, s.tile0, tiles == 0);
+    }
+    run_cost += all_cost;
+    run_tiles += all_tiles;
+  }
+  const int64_t total = run_cost;
+  const int n_tiles = run_tiles;
+  __syncthreads();
+  if (groups) {
+    for (int b = tid; b < B; b += kPrepThreads) {
+      const Segment& s = a.seg[a.group_of[b]];
+      if (s.steps > 0) {
+        a.seq_rec[b].x = s.tile0;
+        a.seq_rec[b].y = s.row0;
+      }
+    }
+  }
+  // ---- cuts ----
+  // runs of at least a few steps each: with less work, fewer clusters
+  const int64_t run = max((total + a.ncl - 1) / a.ncl, (int64_t)(2 * kTileCost));
+  for (int c = tid; c <= a.ncl; c += kPrepThreads) {
+    int tile = n_tiles, step = 0;
+    const int64_t at = c * run;
+    if (at < total) {
+      // (segments without tiles are as long as nothing: the last one at a place has tiles)
+      const int i = last_at_most(a.cost, n_seg, at);
+      const Segment& s = a.seg[i];
+      const int64_t in = at - a.cost[i], len = s.steps + kTileCost;
+      tile = s.tile0 + (int)(in / len);
+      step = max((int)(in % len) - kTileCost, 0);
+      if (step < kMinPiece) step = 0;
+      else if (s.steps - step < kMinPiece) {
+        step = 0;
+        ++tile;
+      }
+    }
+    cut_tile[c] = tile;
+    cut_step[c] = step;
+  }
+  __syncthreads();
+  // ---- each cluster's items ----
+  auto count_of = [&](int c) {
+    const int n = cut_tile[c + 1] - cut_tile[c];
+    return cut_step[c + 1] > (n == 0 ? cut_step[c] : 0) ? n + 1 : n;
+  };
+  if (tid < 32) {
+    int carry = 0;
+    for (int c0 = 0; c0 < a.ncl; c0 += 32) {
+      const int c = c0 + tid, n = c < a.ncl ? count_of(c) : 0;
+      int up_to = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, up_to, o);
+        if (tid >= o) up_to += x;
+      }
+      if (c < a.ncl) first[c] = carry + up_to - n;
+      carry += __shfl_sync(0xffffffffu, up_to, 31);
+    }
+    if (tid == 0) first[a.ncl] = carry;
+  }
+  __syncthreads();
+  for (int c = tid; c <= a.ncl; c += kPrepThreads) a.cl_start[c] = first[c];
+  const int part2 = 2 * B * a.R;
+  for (int k = tid; k < first[a.ncl]; k += kPrepThreads) {
+    // (of clusters that start at k, empty ones among them, the last)
+    const int c = last_at_most(first, a.ncl, k), j = k - first[c];
+    const int tile = cut_tile[c] + j;
+    int lo = 0, hi = n_seg - 1;  // the segment: the last that starts at the tile or before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seg[mid].tile0 <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const Segment s = a.seg[lo];
+    const int s0 = j == 0 ? cut_step[c] : 0;
+    const int s1 = tile == cut_tile[c + 1] ? cut_step[c + 1] : s.steps;
+    int pieces = 1;  // (known to the tile's first piece)
+    if (s0 == 0) {
+      for (int d = c + 1; d <= a.ncl && cut_tile[d] == tile && cut_step[d] > 0; ++d) ++pieces;
+      a.tile_rec[tile] = make_int2(pieces, c + 1);
+    }
+    const int r0 = (tile - s.tile0) * kRows, row0 = s.row0 + r0;
+    const bool group = lo < G;
+    const int part = s0 > 0 ? part2 + c * kRows : (group ? row0 : B * a.R + row0);
+    const bool direct = s.direct && s0 == 0 && s1 == s.steps;
+    a.items[3 * k] = make_int4(row0, min(kRows, s.nrows - r0), s.seq, s.blk0);
+    a.items[3 * k + 1] = make_int4(s0, s1, s.nkeys, direct);
+    a.items[3 * k + 2] = make_int4(part, group ? s.nkeys : s.nkeys - a.Q, group ? -1 : s.seq, 0);
+  }
+}
+
+// The pieces of every row that has more than one, in order of keys, by a warp:
+//   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k
+// and the rows of sequences out of bounds: out = 0, lse = -inf.
+__global__ void __launch_bounds__(256)
+    join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
+                int R, int64_t part2, const float* __restrict__ part_out,
+                const float* __restrict__ part_lse, void* __restrict__ out, int out_bf16,
+                float* __restrict__ lse) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
+  const int4 rec = __ldg(seq_rec + b);
+  int n1 = 0, c1 = 0, n2 = 0, c2 = 0, in1 = 0;
+  const int in2 = r % kRows;
+  if (!rec.w) {
+    const int2 own = __ldg(tile_rec + rec.z + r / kRows);
+    n2 = own.x;
+    c2 = own.y;
+    if (rec.x >= 0) {
+      const int g = (int)row - rec.y;
+      const int2 t = __ldg(tile_rec + rec.x + g / kRows);
+      n1 = t.x;
+      c1 = t.y;
+      in1 = g % kRows;
+    }
+    if (n1 == 0 && n2 == 1) return;  // written by the attention kernel
+  }
+  const int n = n1 + n2;
+  auto part_row = [&](int k) -> int64_t {
+    if (k < n1) return k == 0 ? row : part2 + (int64_t)(c1 + k - 1) * kRows + in1;
+    k -= n1;
+    return k == 0 ? part2 / 2 + row : part2 + (int64_t)(c2 + k - 1) * kRows + in2;
+  };
+  float mx = -INFINITY;
+  bool is_nan = false;
+  for (int k = lane; k < n; k += 32) {
+    const float l = part_lse[part_row(k)];
+    is_nan |= l != l;
+    mx = fmaxf(mx, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (__any_sync(0xffffffffu, is_nan)) mx = NAN;
+  float sum = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mx != -INFINITY) {
+    for (int k0 = 0; k0 < n; k0 += 4) {  // four pieces' loads in flight
+      float w[4];
+      float4 v[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        w[q] = 0.f;
+        if (k0 + q >= n) continue;
+        const int64_t pr = part_row(k0 + q);
+        w[q] = part_lse[pr];
+        const float4* src = reinterpret_cast<const float4*>(part_out + pr * kDL);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[q][i] = __ldcs(src + lane + 32 * i);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (k0 + q >= n || w[q] == -INFINITY) continue;  // (a piece without a visible key)
+        const float e = expf(w[q] - mx);
+        sum += e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i].x = fmaf(e, v[q][i].x, acc[i].x);
+          acc[i].y = fmaf(e, v[q][i].y, acc[i].y);
+          acc[i].z = fmaf(e, v[q][i].z, acc[i].z);
+          acc[i].w = fmaf(e, v[q][i].w, acc[i].w);
+        }
+      }
+    }
+  }
+  const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+    if (out_bf16)
+      reinterpret_cast<uint2*>((__nv_bfloat16*)out + row * kDL)[lane + 32 * i] =
+          make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+    else
+      reinterpret_cast<float4*>((float*)out + row * kDL)[lane + 32 * i] = x;
+  }
+  if (lane == 0 && lse) lse[row] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+}
+
+// ---- host side -----------------------------------------------------------------------
+// Testing hook (tv_testing_set_shared_fault): off unless a test turns it on.
+std::mutex g_test_mu;
+int g_test_skip_loads = 0;
+uint64_t g_test_deadline_ns = 0;
+int32_t* g_test_exit_counts = nullptr;
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+int g_clusters[64] = {};
+std::mutex g_mu;
+
+bool get_encode() {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return g_encode != nullptr;
+}
+
+// Rows viewed as [64 elements][rows][chunks of 64 elements]: one box is `box_chunks` chunks of
+// `box_rows` rows, chunk by chunk in shared memory as 128-byte-swizzled tiles.
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t chunks,
+              uint32_t box_rows, uint32_t box_chunks) {
+  cuuint64_t dims[3] = {64, rows, chunks};
+  cuuint64_t strides[2] = {row_bytes, 128};
+  cuuint32_t box[3] = {64, box_rows, box_chunks};
+  cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, chunks > 1 ? 3 : 2, const_cast<void*>(base),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of two CTAs that the current device holds at once (0: cannot run here).
+int max_clusters() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_clusters[dev] == 0) {
+    if (cudaFuncSetAttribute(shared_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 256);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, shared_attn_kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = current_sm_count() / 2;
+    }
+    g_clusters[dev] = std::min(n, kMaxClusters);
+  }
+  return g_clusters[dev];
+}
+
+// Clusters that the workspace and the schedule are laid out for (76 where there is no device).
+int planned_clusters() {
+  const int n = max_clusters();
+  return n > 0 ? n : 76;
+}
+
+struct Layout {
+  int64_t max_tiles, part_rows;
+  size_t group_of, group_bad, seg, cost, seq_rec, tile_rec, items, cl_start, part_out, part_lse, total;
+};
+Layout layout(const tv_shared_args* a, int ncl) {
+  const int64_t R = (int64_t)a->Q * a->H, B = a->B, G = a->G;
+  const int64_t T = (R + kRows - 1) / kRows;
+  Layout w{};
+  w.max_tiles = B * T + (B * R) / kRows + G;
+  w.part_rows = 2 * B * R + (int64_t)kRows * ncl;
+  size_t n = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = n;
+    n += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  w.group_of = take(B * 4);
+  w.group_bad = take(G * 4);
+  w.seg = take((G + B) * sizeof(Segment));
+  w.cost = take((G + B + 1) * 8);
+  w.seq_rec = take(B * 16);
+  w.tile_rec = take(w.max_tiles * 8);
+  w.items = take((w.max_tiles + ncl) * 48);
+  w.cl_start = take((ncl + 1) * 4);
+  w.part_out = take(w.part_rows * kDL * 4);
+  w.part_lse = take(w.part_rows * 4);
+  w.total = n;
+  return w;
+}
+
+}  // namespace
+
+size_t shared_workspace(const tv_shared_args* a) { return layout(a, planned_clusters()).total; }
+
+cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t st) {
+  if (!get_encode()) return cudaErrorNotSupported;
+  const int ncl = max_clusters();
+  if (ncl <= 0) return cudaErrorNotSupported;
+  const Layout w = layout(a, ncl);
+  char* base = (char*)ws;
+  const int64_t R = (int64_t)a->Q * a->H, rows = a->B * R;
+  const tv_cache_layout& cache = a->cache;
+  const bool paged = cache.page_table != nullptr;
+  CUtensorMap lat_s, kpe, lat_o, q, qr;
+  const uint64_t lat_bytes = (uint64_t)a->ckv_row_stride * 2, kpe_bytes = (uint64_t)a->kpe_row_stride * 2;
+  if (!make_map(&lat_s, a->c_kv, cache.num_rows, lat_bytes, kDL / 64, kBN, 1) ||
+      !make_map(&kpe, a->k_pe, cache.num_rows, kpe_bytes, 1, kBN, 1) ||
+      !make_map(&lat_o, a->c_kv, cache.num_rows, lat_bytes, kDL / 64, kBN, 4) ||
+      !make_map(&q, a->q_latent, rows, kDL * 2, kDL / 64, kRows, 2) ||
+      !make_map(&qr, a->q_pe, rows, kDR * 2, 1, kRows, 1))
+    return cudaErrorInvalidValue;
+
+  PrepArgs pa{};
+  pa.prefix_len = a->prefix_len;
+  pa.group_start = a->group_start;
+  pa.shared_len = a->shared_len;
+  pa.B = a->B;
+  pa.R = (int)R;
+  pa.Q = a->Q;
+  pa.G = a->G;
+  pa.T = (int)((R + kRows - 1) / kRows);
+  pa.max_prefix = a->max_prefix_len;
+  pa.ncl = ncl;
+  pa.max_tiles = (int)w.max_tiles;
+  pa.seq_cap = paged ? (int64_t)cache.max_pages * kBN : cache.kv_stride_b;
+  pa.group_of = (int32_t*)(base + w.group_of);
+  pa.group_bad = (int32_t*)(base + w.group_bad);
+  pa.seg = (Segment*)(base + w.seg);
+  pa.cost = (int64_t*)(base + w.cost);
+  pa.seq_rec = (int4*)(base + w.seq_rec);
+  pa.tile_rec = (int2*)(base + w.tile_rec);
+  pa.items = (int4*)(base + w.items);
+  pa.cl_start = (int32_t*)(base + w.cl_start);
+  pa.status = a->status;
+  prepare_kernel<<<1, kPrepThreads, 0, st>>>(pa);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  Params p{};
+  p.page_table = cache.page_table;
+  p.kv_stride = cache.kv_stride_b;
+  p.max_pages = cache.max_pages;
+  p.num_pages = (int32_t)(cache.num_rows / kBN);
+  p.num_rows = (int32_t)cache.num_rows;
+  p.B = a->B;
+  p.H = a->H;
+  p.Q = a->Q;
+  p.R = (int)R;
+  p.anc = a->anc;
+  p.out = a->out;
+  p.out_bf16 = a->out_dt == TV_BF16;
+  p.lse = a->lse;
+  p.part_out = (float*)(base + w.part_out);
+  p.part_lse = (float*)(base + w.part_lse);
+  p.status = a->status;
+  p.items = pa.items;
+  p.cl_start = pa.cl_start;
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  p.timeout_ns = kTimeoutNs;
+  {
+    std::lock_guard<std::mutex> lock(g_test_mu);
+    p.test_skip_loads = g_test_skip_loads;
+    if (g_test_deadline_ns) p.timeout_ns = g_test_deadline_ns;
+    p.test_exit_counts = g_test_exit_counts;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * ncl);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, shared_attn_kernel, p, lat_s, kpe, lat_o, q, qr);
+  if (e != cudaSuccess) return e;
+  join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
+      pa.seq_rec, pa.tile_rec, rows, (int)R, 2 * rows, p.part_out, p.part_lse, a->out, p.out_bf16,
+      a->lse);
+  return cudaGetLastError();
+}
+
+}  // namespace tv
+
+extern "C" int tv_testing_set_shared_fault(int skip_key_loads, uint64_t deadline_ns,
+                                           int32_t* exit_counts) {
+  if (skip_key_loads < 0 || skip_key_loads > 1) return TV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lock(tv::g_test_mu);
+  tv::g_test_skip_loads = skip_key_loads;
+  tv::g_test_deadline_ns = deadline_ns;
+  tv::g_test_exit_counts = exit_counts;
+  return TV_OK;
+}

@@ -129,6 +129,18 @@ cudaError_t launch_pages_copy(void* c_kv, void* k_pe, int64_t ckv_stride, int64_
 size_t prefill_workspace(const tv_prefill_args* a, int sm_count);
 cudaError_t launch_prefill(const tv_prefill_args* a, void* ws, int sm_count, cudaStream_t st);
 
+// Rotary positions and norms (k_norm_rope.cu).
+void rope_frequencies(const tv_rope_scaling& sc, int rot, double* inv, double* mag);
+cudaError_t launch_rope_any(const tv_rope_args* a, cudaStream_t st);
+cudaError_t launch_norm_rope(const tv_norm_rope_args* a, cudaStream_t st);
+
+// Attention over a shared prefix (k_shared_attn.cu).
+size_t shared_workspace(const tv_shared_args* a);
+cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t st);
+
+// Next tokens (k_token.cu).
+cudaError_t launch_token_sample(const tv_token_args* a, int sm_count, cudaStream_t st);
+
 // Set the thread-local text returned by tv_last_error() (defined in tv_api.cu).
 void set_last_error(const char* msg);
 

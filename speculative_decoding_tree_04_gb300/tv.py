@@ -17,6 +17,11 @@ this module raises.
     pages_release(pool, keep), pages_compact(pool, moves, n_moves),
     pages_copy(c_kv, k_pe, page_size, copies, ...)
     prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale, ...)
+    rope(x, out, positions, layout, rot_offset, rot_dim, scaling, inverse), rope_scaling(...),
+    rope_frequencies(scaling, rot_dim),
+    norm_rope(q, kv, q_start, prefix_len, q_nope, q_pe, c_kv, k_pe, ...)
+    shared_attn(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len, out, lse, ...)
+    token_sample(logits, uniforms, tokens, temperature, top_k, top_p, min_p, ...)
 """
 from __future__ import annotations
 
@@ -38,6 +43,8 @@ PATH_AUTO, PATH_SIMT, PATH_TCGEN05 = 0, 1, 2
 PAGED_AUTO, PAGED_STEP_MAPS, PAGED_GATHER = 0, 1, 2
 MASK_TREE, MASK_CAUSAL = 0, 1
 DRAFT_BY_DEPTH, DRAFT_BY_NODE = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_WAVELENGTH = 0, 1, 2, 3, 4
 
 
 class TVError(RuntimeError):
@@ -138,6 +145,84 @@ class PagePool(ctypes.Structure):
     ]
 
 
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("kind", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("T", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("d_head", ctypes.c_int32),
+        ("rot_offset", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32), ("dt", ctypes.c_int),
+        ("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("in_stride_token", ctypes.c_int64), ("in_stride_head", ctypes.c_int64),
+        ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("scaling", RopeScaling),
+    ]
+
+
+class NormRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("d_nope", ctypes.c_int32), ("d_rope", ctypes.c_int32), ("d_latent", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("dt", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("q", ctypes.c_void_p),
+        ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("kv", ctypes.c_void_p), ("kv_stride_token", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p), ("kv_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+        ("depth", ctypes.c_void_p),
+        ("q_nope", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("ckv_row_stride", ctypes.c_int64), ("kpe_row_stride", ctypes.c_int64),
+        ("cache", CacheLayout),
+        ("scaling", RopeScaling),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class SharedArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Q", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32), ("d_rope", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("dt", ctypes.c_int), ("out_dt", ctypes.c_int),
+        ("q_latent", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("ckv_row_stride", ctypes.c_int64), ("kpe_row_stride", ctypes.c_int64),
+        ("cache", CacheLayout),
+        ("prefix_len", ctypes.c_void_p), ("max_prefix_len", ctypes.c_int32),
+        ("G", ctypes.c_int32),
+        ("group_start", ctypes.c_void_p), ("shared_len", ctypes.c_void_p),
+        ("anc", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class TokenArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("B", ctypes.c_int32), ("vocab", ctypes.c_int64),
+        ("logits", ctypes.c_void_p), ("logits_dt", ctypes.c_int),
+        ("logits_row_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+        ("uniforms", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -188,6 +273,14 @@ def load():
     lib.tv_prefill_attn_workspace_size.argtypes = [ctypes.POINTER(PrefillArgs)]
     lib.tv_prefill_attn_workspace_size.restype = sz
     lib.tv_prefill_attn.argtypes = [ctypes.POINTER(PrefillArgs), P, sz, P]
+    lib.tv_rope_frequencies.argtypes = [ctypes.POINTER(RopeScaling), i32, P, P]
+    lib.tv_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+    lib.tv_norm_rope.argtypes = [ctypes.POINTER(NormRopeArgs), P]
+    lib.tv_shared_attn_workspace_size.argtypes = [ctypes.POINTER(SharedArgs)]
+    lib.tv_shared_attn_workspace_size.restype = sz
+    lib.tv_shared_attn.argtypes = [ctypes.POINTER(SharedArgs), P, sz, P]
+    lib.tv_token_sample.argtypes = [ctypes.POINTER(TokenArgs), P]
+    lib.tv_testing_set_shared_fault.argtypes = [i32, ctypes.c_uint64, P]
     _lib = lib
     return lib
 
@@ -724,3 +817,210 @@ def prefill_attn(q_nope, q_pe, w_kv, c_kv, k_pe, q_start, prefix_len, out, scale
         workspace = _scratch("prefill", dev, stream, handle, prefill_workspace_size, a)
     _call(dev, "tv_prefill_attn", ctypes.byref(a), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), handle)
+
+
+def rope_scaling(base=10000.0, kind=ROPE_PLAIN, factor=1.0, original_context=4096, low=None,
+                 high=None, magnitude=0.0) -> RopeScaling:
+    """Frequencies of rotary positions.  low and high: turns over the original context, by
+    default 1 and 32 (ROPE_YARN) or 1 and 4 (ROPE_WAVELENGTH)."""
+    return RopeScaling(float(base), int(kind), float(factor), float(original_context),
+                       1.0 if low is None else float(low),
+                       (4.0 if kind == ROPE_WAVELENGTH else 32.0) if high is None
+                       else float(high), float(magnitude))
+
+
+_plain_scaling = rope_scaling()
+
+
+def rope_frequencies(scaling: RopeScaling, rot_dim: int):
+    """The angles per position of rot_dim/2 pairs, and the factor on cos and sin."""
+    f = (ctypes.c_double * max(1, rot_dim // 2))()
+    mag = ctypes.c_double()
+    _check(load().tv_rope_frequencies(ctypes.byref(scaling), rot_dim, f, ctypes.byref(mag)),
+           "tv_rope_frequencies")
+    return list(f), mag.value
+
+
+def rope(x, out, positions, layout=ROPE_HALF, rot_offset=0, rot_dim=None, scaling=None,
+         inverse=False, stream=None):
+    """Rotate elements rot_offset .. rot_offset+rot_dim-1 (default: all behind the offset) of
+    x [T,H,D] (or [T,D], one head) into out of the same shape, which may be x, at positions [T]
+    int32; the other elements are copied.  inverse: by the opposite angle."""
+    dev = _on_device(x, out, positions)
+    if x.dim() == 2:
+        x, out = x.unsqueeze(1), out.unsqueeze(1)
+    T, H, D = x.shape
+    if out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    if (x.stride(2) != 1 or out.stride(2) != 1) and D > 1:
+        raise ValueError("innermost dimension must be contiguous")
+    _i32("positions", positions, (T,))
+    # (a dimension of one has no stride of its own)
+    st = [s if n > 1 else D for t in (x, out) for s, n in zip(t.stride(), (T, H))]
+    a = RopeArgs(ctypes.sizeof(RopeArgs), T, H, D, int(rot_offset),
+                 D - int(rot_offset) if rot_dim is None else int(rot_dim), int(layout),
+                 int(bool(inverse)), _dt(x), x.data_ptr(), out.data_ptr(), *st,
+                 positions.data_ptr(), scaling or _plain_scaling)
+    _call(dev, "tv_rope", ctypes.byref(a), _raw_stream(dev, stream))
+
+
+def norm_rope(q, kv, q_start, prefix_len, q_nope, q_pe, c_kv, k_pe, q_weight=None,
+              kv_weight=None, k_weight=None, eps=1e-6, layout=ROPE_HALF, rot_dim=None,
+              scaling=None, depth=None, page_table=None, page_size=64, kv_stride_b=0,
+              status=None, stream=None):
+    """Norms, rotation and cache append of packed tokens in one pass: queries q [T,H,DN+DR] ->
+    q_nope [T,H,DN] (None when DN is 0) and q_pe [T,H,DR]; key rows kv [T,DL+DR] -> cache rows
+    c_kv [rows,DL] and k_pe [rows,DR].  q_start [B+1], prefix_len [B], depth [T] int32.  A weight
+    of None: no norm.  Either q or kv (with its outputs and weights) may be None."""
+    dev = _on_device(q, kv, q_start, prefix_len, q_nope, q_pe, c_kv, k_pe, q_weight, kv_weight,
+                     k_weight, depth, page_table, status)
+    if q is None and kv is None:
+        raise ValueError("neither q nor kv")
+    B, T = prefix_len.shape[0], (kv if q is None else q).shape[0]
+    dt = (kv if q is None else q).dtype
+    if q is None:
+        q_weight = None
+    if kv is None:
+        kv_weight = k_weight = None
+    DR = (k_pe if q is None else q_pe).shape[-1]
+    H, DN, DL, q_st, kv_st, rows = 1, 0, 1, (0, 0), 0, 0
+    cache = CacheLayout(None, page_size, 0, kv_stride_b, 0)
+    if q is not None:
+        H, DN = q.shape[1], q.shape[2] - DR
+        if q.stride(2) != 1:
+            raise ValueError("innermost dimension of q must be contiguous")
+        q_st = (q.stride(0), q.stride(1))
+        outs = [("q_pe", q_pe, (T, H, DR))]
+        if DN > 0:
+            outs.append(("q_nope", q_nope, (T, H, DN)))
+        for name, t, shape in outs:
+            if t.shape != shape or t.dtype is not dt or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dt} of shape {shape}")
+    if kv is not None:
+        DL = c_kv.shape[1]
+        if kv.shape != (T, DL + DR) or kv.stride(1) != 1 or kv.dtype is not dt:
+            raise ValueError(f"kv must be {dt} [{T}, {DL + DR}] with contiguous rows")
+        for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
+            if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
+                raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
+        kv_st, rows = kv.stride(0), min(c_kv.shape[0], k_pe.shape[0])
+        if page_table is not None:
+            _i32("page_table", page_table, (B, page_table.shape[1]))
+            cache = CacheLayout(page_table.data_ptr(), page_size, page_table.shape[1], 0, rows)
+        else:
+            cache = CacheLayout(None, page_size, 0, kv_stride_b, rows)
+    for name, w, d in (("q_weight", q_weight, DN + DR), ("kv_weight", kv_weight, DL),
+                       ("k_weight", k_weight, DR)):
+        if w is not None and (w.shape != (d,) or w.dtype is not dt or not w.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous {dt} of {d} elements")
+    _i32("q_start", q_start, (B + 1,))
+    _i32("prefix_len", prefix_len, (B,))
+    if depth is not None:
+        _i32("depth", depth, (T,))
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+    a = NormRopeArgs(ctypes.sizeof(NormRopeArgs), B, T, H, DN, DR, DL,
+                     DR if rot_dim is None else int(rot_dim), int(layout),
+                     _dt(kv if q is None else q), float(eps), ptr(q), q_st[0], q_st[1], ptr(kv), kv_st, ptr(q_weight),
+                     ptr(kv_weight), ptr(k_weight), q_start.data_ptr(), prefix_len.data_ptr(),
+                     ptr(depth), ptr(q_nope) if q is not None and DN > 0 else None,
+                     ptr(q_pe) if q is not None else None, ptr(c_kv) if kv is not None else None,
+                     ptr(k_pe) if kv is not None else None,
+                     c_kv.stride(0) if kv is not None else 0,
+                     k_pe.stride(0) if kv is not None else 0, cache,
+                     scaling or _plain_scaling, _status_arg(status))
+    _call(dev, "tv_norm_rope", ctypes.byref(a), _raw_stream(dev, stream))
+
+
+def shared_args(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len, out, lse, scale,
+                max_prefix_len, anc=None, page_table=None, page_size=64, kv_stride_b=0,
+                status=None) -> SharedArgs:
+    B, Q, H, DL = q_latent.shape
+    DR = q_pe.shape[3]
+    dt = q_latent.dtype
+    if dt is not torch.bfloat16:
+        raise TypeError(f"shared_attn takes bfloat16 queries and cache, not {dt}")
+    for name, t, shape, want in (("q_latent", q_latent, (B, Q, H, DL), dt),
+                                 ("q_pe", q_pe, (B, Q, H, DR), dt),
+                                 ("out", out, (B, Q, H, DL), out.dtype)):
+        if t.shape != shape or t.dtype is not want or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {want} of shape {shape}")
+    for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
+        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
+            raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
+    if lse is not None and (lse.shape != (B, Q, H) or lse.dtype is not torch.float32 or
+                            not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 of shape {(B, Q, H)}")
+    if anc is not None and (anc.shape != (B, Q) or not anc.is_contiguous() or
+                            anc.dtype not in (torch.int64, torch.uint64)):
+        raise ValueError(f"anc must be contiguous int64 of shape {(B, Q)}")
+    _i32("prefix_len", prefix_len, (B,))
+    G = 0
+    if group_start is not None:
+        G = group_start.shape[0] - 1
+        _i32("group_start", group_start, (G + 1,))
+        _i32("shared_len", shared_len, (G,))
+    rows = min(c_kv.shape[0], k_pe.shape[0])
+    if page_table is not None:
+        _i32("page_table", page_table, (B, page_table.shape[1]))
+        cache = CacheLayout(page_table.data_ptr(), page_size, page_table.shape[1], 0, rows)
+    else:
+        cache = CacheLayout(None, page_size, 0, kv_stride_b, rows)
+    return SharedArgs(ctypes.sizeof(SharedArgs), B, H, Q, DL, DR, float(scale), TV_BF16,
+                      _dt(out), q_latent.data_ptr(), q_pe.data_ptr(), c_kv.data_ptr(),
+                      k_pe.data_ptr(), c_kv.stride(0), k_pe.stride(0), cache,
+                      prefix_len.data_ptr(), int(max_prefix_len), G,
+                      group_start.data_ptr() if G else None,
+                      shared_len.data_ptr() if G else None,
+                      None if anc is None else anc.data_ptr(), out.data_ptr(),
+                      None if lse is None else lse.data_ptr(), _status_arg(status))
+
+
+def shared_workspace_size(a: SharedArgs) -> int:
+    return int(load().tv_shared_attn_workspace_size(ctypes.byref(a)))
+
+
+def shared_attn(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len, out, lse, scale,
+                max_prefix_len, anc=None, page_table=None, page_size=64, kv_stride_b=0,
+                status=None, workspace=None, stream=None):
+    """Attention of q_latent [B,Q,H,512] and q_pe [B,Q,H,64] (bf16) over the latent cache, where
+    the sequences group_start[g] .. group_start[g+1]-1 ([G+1] int32, None: nothing is shared)
+    hold the same first shared_len[g] keys.  out [B,Q,H,512] (float32 or bf16) and lse [B,Q,H]
+    (float32 or None) are written.  anc [B,Q]: the draft trees' ancestors; None: a chain."""
+    dev = _on_device(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len, out, lse,
+                     anc, page_table, status, workspace)
+    a = shared_args(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len, out, lse,
+                    scale, max_prefix_len, anc, page_table, page_size, kv_stride_b, status)
+    handle = _raw_stream(dev, stream)
+    if workspace is None:
+        workspace = _scratch("shared", dev, stream, handle, shared_workspace_size, a)
+    _call(dev, "tv_shared_attn", ctypes.byref(a), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), handle)
+
+
+def token_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
+                 kept=None, status=None, stream=None):
+    """Next tokens: logits [B,V] (float32 or bf16, rows contiguous) and uniforms [B] float32 ->
+    tokens [B] int32 (and kept [B] int32: how many tokens the filters leave).  temperature
+    (0 = greedy), top_p and min_p [B] float32, top_k [B] int32; None: off."""
+    dev = _on_device(logits, uniforms, tokens, temperature, top_k, top_p, min_p, kept, status)
+    B, V = logits.shape
+    if V > 1 and B > 0 and logits.stride(1) != 1:
+        raise ValueError("logits rows must be contiguous")
+    for name, t in (("uniforms", uniforms), ("temperature", temperature), ("top_p", top_p),
+                    ("min_p", min_p)):
+        if t is not None and (t.shape != (B,) or t.dtype is not torch.float32 or
+                              not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous float32 of shape {(B,)}")
+    for name, t in (("tokens", tokens), ("kept", kept), ("top_k", top_k)):
+        if t is not None:
+            _i32(name, t, (B,))
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+    a = TokenArgs(ctypes.sizeof(TokenArgs), B, V, logits.data_ptr(), _dt(logits),
+                  logits.stride(0) if B > 1 else V, ptr(temperature), ptr(top_k), ptr(top_p),
+                  ptr(min_p), uniforms.data_ptr(), tokens.data_ptr(), ptr(kept),
+                  _status_arg(status))
+    _call(dev, "tv_token_sample", ctypes.byref(a), _raw_stream(dev, stream))
