@@ -9,12 +9,14 @@
 // (2k, 2k+1) in the interleaved one.  The norm's sum, the product and the rotation are taken in
 // 32 bits and rounded once.
 //
-// What bounds it: bytes for prompts, latency for single tokens.  A warp holds one vector (up to
-// four short ones) in registers, 16 bytes a lane, so that the norm costs a shuffle reduction
-// and no second read; in the half layout a lane loads its partners too, from lines that the
-// warp's own loads have brought.  A block serves one token, or a part of its heads where the
-// tokens are few (about two blocks per SM), and takes the angles' cosines and sines once, while
-// the first vectors are on their way.
+// What bounds it: bytes for prompts, latency for single tokens.  A head is held in registers by a
+// group of 1 to 32 lanes, up to four 16-byte vectors a lane, as few lanes idle as that allows (192
+// bf16: 8 lanes of three), so that the norm costs a few shuffles and no second read; in the half
+// layout a lane loads its vectors' partners too, from
+// lines that the warp's own loads bring.  A block serves up to eight tokens, their heads one
+// list that its warps go through without meeting again once the tokens' cosines and sines are
+// there (taken while the first heads are on their way), or where the tokens are few a part of
+// one token's heads.
 //
 // Angles.  The product pos * f_k and its reduction by multiples of pi/2 (Cody and Waite's
 // two-part subtraction) run in double; float32 tensors take cos and sin in double, too, as
@@ -41,7 +43,7 @@ namespace {
 using namespace rope;
 
 constexpr int kMaxThreads = 256;
-constexpr int kMaxVecs = 4;  // 16-byte vectors of one head that a lane holds
+constexpr int kMaxVecs = 4;  // 16-byte vectors of one head that a lane holds at most
 
 // cos and sin of one pair's angle as the rotation takes them.
 template <typename T>
@@ -134,26 +136,23 @@ struct Kind {
   float eps;  // with a weight: the norm's
 };
 
-// A vector's addresses.
-template <typename T>
-struct Place {
-  const T* src;
-  T* low;        // element e < split at low + e
-  T* high;       // element e >= split at high + e - split
-  const T* w;    // norm weights, or null for no norm
-};
-
-// Where pair k's turn lies: the turns that a lane reads in step i (of one vector's eight or
-// four elements) are consecutive over the lanes, so that no two of them meet in a bank.
+// Where pair k's turn lies: a lane reads two turns of one vector's pairs at a time, and those that
+// the lanes read together are consecutive, so that no two of them meet in a bank.
 template <typename T>
 __device__ __forceinline__ int turn_slot(int k, int half, bool pairs) {
   constexpr int N = Vec16<T>::N;
   const int per = pairs ? N / 2 : N;  // pairs of one vector
-  return half % per ? k : (k % per) * (half / per) + k / per;
+  if (half % per) return k;           // (no vectors: read one by one)
+  const int j = k % per;
+  return 2 * ((j / 2) * (half / per) + k / per) + (j & 1);
 }
+template <typename T>
+struct alignas(16) TwoTurns {
+  Turn<T> t[2];
+};
 
-// One vector in 16-byte pieces by the `width` lanes of a group (lane `l` of it).  Loads first,
-// then, by `finish`, the norm, the rotation and the stores.
+// A head in 16-byte pieces by the `width` lanes of a group (lane `l` of it, vectors l, l + width,
+// ..).  Loads first, then, by `finish`, the norm, the rotation and the stores.
 template <typename T, int NV>
 struct Held {
   uint4 own[NV], other[NV];
@@ -161,7 +160,7 @@ struct Held {
     constexpr int N = Vec16<T>::N;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = l + i * width, e = v * N;
+      const int e = (l + i * width) * N;
       if (!on || e >= k.n) continue;
       own[i] = *reinterpret_cast<const uint4*>(src + e);
       if (!pairs && e >= k.at && e < k.at + k.rot) {
@@ -170,12 +169,13 @@ struct Held {
       }
     }
   }
-  __device__ __forceinline__ void finish(const Place<T>& p, const Kind& k, bool pairs, bool on, int l,
-                                         int width, const Turn<T>* turns) {
+  // w: the norm's weights, null for none (the same for a whole warp, whose lanes meet in the sum).
+  __device__ __forceinline__ void finish(T* low, T* high, const Kind& k, bool pairs, const T* w, bool on,
+                                         int l, int width, const Turn<T>* turns) {
     constexpr int N = Vec16<T>::N;
     const int half = k.rot / 2;
     float r = 1.f;
-    if (p.w) {  // the same for the whole warp
+    if (w) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -194,43 +194,44 @@ struct Held {
       if (!on || e >= k.n) continue;
       float x[N];
       Vec16<T>::unpack(own[i], x);
-      if (p.w) {
-        float w[N];
-        Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(p.w + e)), w);
+      if (w) {
+        float f[N];
+        Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(w + e)), f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = x[j] * r * w[j];
+        for (int j = 0; j < N; ++j) x[j] = x[j] * r * f[j];
       }
       if (e >= k.at && e < k.at + k.rot) {
         const int q = e - k.at;
+        const TwoTurns<T>* two = reinterpret_cast<const TwoTurns<T>*>(turns);
         if (pairs) {
-          const int per = N / 2, step = half / per;
+          const int step = half / (N / 2), v = q / N;
 #pragma unroll
           for (int j = 0; j < N / 2; ++j) {
-            const Turn<T> t = turns[j * step + q / N];
+            const Turn<T>& t = two[(j / 2) * step + v].t[j & 1];
             const float a = x[2 * j], b = x[2 * j + 1];
             x[2 * j] = t.out(a, b);
             x[2 * j + 1] = t.out(b, -a);
           }
         } else {
           const bool first = q < half;
-          const int step = half / N, k0 = (first ? q : q - half) / N;
+          const int step = half / N, v = (first ? q : q - half) / N;
           float y[N];
           Vec16<T>::unpack(other[i], y);
-          if (p.w) {
-            float w[N];
+          if (w) {
+            float f[N];
             Vec16<T>::unpack(
-                __ldg(reinterpret_cast<const uint4*>(p.w + (first ? e + half : e - half))), w);
+                __ldg(reinterpret_cast<const uint4*>(w + (first ? e + half : e - half))), f);
 #pragma unroll
-            for (int j = 0; j < N; ++j) y[j] = y[j] * r * w[j];
+            for (int j = 0; j < N; ++j) y[j] = y[j] * r * f[j];
           }
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            const Turn<T> t = turns[j * step + k0];
-            x[j] = first ? t.out(x[j], y[j]) : t.out(x[j], -y[j]);
+            const Turn<T>& t = two[(j / 2) * step + v].t[j & 1];
+            x[j] = t.out(x[j], first ? y[j] : -y[j]);
           }
         }
       }
-      T* dst = e < k.split ? p.low + e : p.high + (e - k.split);
+      T* dst = e < k.split ? low + e : high + (e - k.split);
       *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(x);
     }
   }
@@ -239,22 +240,23 @@ struct Held {
 // The same for one vector of any size and alignment, an element (or a pair) at a time; a lane
 // reads both elements of a pair before it writes either, so the vector may be turned in place.
 template <typename T>
-__device__ void one_by_one(const Place<T>& p, const Kind& k, bool pairs, const Turn<T>* turns, int lane) {
+__device__ void one_by_one(const T* src, T* low, T* high, const T* w, const Kind& k, bool pairs,
+                           const Turn<T>* turns, int lane) {
   float r = 1.f;
-  if (p.w) {
+  if (w) {
     float sum = 0.f;
     for (int e = lane; e < k.n; e += 32) {
-      const float x = to_float(p.src[e]);
+      const float x = to_float(src[e]);
       sum = fmaf(x, x, sum);
     }
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     r = 1.f / sqrtf(sum / (float)k.n + k.eps);
   }
   auto get = [&](int e) {
-    const float x = to_float(p.src[e]);
-    return p.w ? x * r * to_float(p.w[e]) : x;
+    const float x = to_float(src[e]);
+    return w ? x * r * to_float(w[e]) : x;
   };
-  auto put = [&](int e, float y) { store_float(e < k.split ? p.low + e : p.high + (e - k.split), y); };
+  auto put = [&](int e, float y) { store_float(e < k.split ? low + e : high + (e - k.split), y); };
   for (int e = lane; e < k.n; e += 32)
     if (e < k.at || e >= k.at + k.rot) put(e, get(e));
   const int half = k.rot / 2;
@@ -267,87 +269,111 @@ __device__ void one_by_one(const Place<T>& p, const Kind& k, bool pairs, const T
   }
 }
 
-// The heads a block turns for its token: heads h0 .. h0+nh-1 of `kind`, from src + h*stride,
-// to low + h*low_stride and high + h*high_stride.
+// Heads [h0, h0 + nh) of tokens [t0, t0 + nt), one list.
 template <typename T>
 struct Heads {
   const T* src;
   T* low;
   T* high;
   const T* w;
-  int64_t stride, low_stride, high_stride;
-  __device__ Place<T> place(int h) const {
-    return {src + h * stride, low + h * low_stride, high + h * high_stride, w};
-  }
+  int64_t token, stride, low_token, low_stride, high_token, high_stride;
+  int64_t t0;
+  int h0, nh, nt;
 };
 
-constexpr int kAhead = 4;  // vectors of a warp's that are on their way at once
-
-// Turns the block's heads with warps [w0, w0 + nw); `ready` is called once, between the first
-// loads and their use, and returns whether to go on (all threads alike).
+// Turns the list with all of the block's warps.  `ready` is called once by every thread, between
+// the first loads and their use; on[i] then says whether token t0 + i takes part, and its turns
+// start at turns + i * half.
 template <typename T, int NV, typename Ready>
-__device__ __forceinline__ bool turn_heads(const Heads<T>& hd, const Kind& k, bool pairs, bool vec, int nh,
-                                           int width, const Turn<T>* turns, Ready ready) {
+__device__ __forceinline__ void turn_heads(const Heads<T>& hd, const Kind& k, bool pairs, int width,
+                                           const Turn<T>* turns, const bool* on, Ready ready) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  if (!vec) {
-    if (!ready()) return false;
-    for (int h = warp; h < nh; h += nw) one_by_one<T>(hd.place(h), k, pairs, turns, lane);
-    return true;
+  const int half = k.rot / 2, n = hd.nh * hd.nt;
+  auto src = [&](int i, int h) { return hd.src + (hd.t0 + i) * hd.token + (hd.h0 + h) * hd.stride; };
+  auto low = [&](int i, int h) { return hd.low + (hd.t0 + i) * hd.low_token + (hd.h0 + h) * hd.low_stride; };
+  auto high = [&](int i, int h) { return hd.high + (hd.t0 + i) * hd.high_token + (hd.h0 + h) * hd.high_stride; };
+  if (width == 0) {
+    ready();
+    for (int q = warp; q < n; q += nw) {
+      const int i = q / hd.nh, h = q - i * hd.nh;
+      if (on[i]) one_by_one<T>(src(i, h), low(i, h), high(i, h), hd.w, k, pairs, turns + i * half, lane);
+    }
+    return;
   }
   const int groups = 32 / width, l = lane & (width - 1), g = lane / width;
-  constexpr int kHold = NV == 1 ? kAhead : 1;
+  constexpr int kHold = NV == 1 ? 4 : NV == 2 ? 2 : 1;  // heads of a group on their way at once
   Held<T, NV> held[kHold];
-  bool first = true;
   const int step = nw * groups;
+  bool first = true;
   // (the bound is the same for a whole warp: its lanes meet in the norm's shuffles)
-  for (int h0 = warp * groups; first || h0 < nh; h0 += kHold * step) {
+  for (int q0 = warp * groups; first || q0 < n; q0 += kHold * step) {
+    int ti[kHold], hi[kHold];
 #pragma unroll
     for (int u = 0; u < kHold; ++u) {
-      const int h = h0 + u * step + g;
-      held[u].load(hd.src + h * hd.stride, k, pairs, h < nh, l, width);
+      const int q = q0 + u * step + g;
+      ti[u] = q / hd.nh;
+      hi[u] = q - ti[u] * hd.nh;
+      held[u].load(src(ti[u], hi[u]), k, pairs, q < n, l, width);
     }
-    if (first && !ready()) return false;
+    if (first) ready();
     first = false;
     __syncwarp();  // in place: every lane's loads come before any lane's stores
 #pragma unroll
     for (int u = 0; u < kHold; ++u) {
-      const int h = h0 + u * step + g;
-      if (h0 + u * step < nh) held[u].finish(hd.place(h), k, pairs, h < nh, l, width, turns);
+      if (q0 + u * step >= n) continue;
+      const bool is = q0 + u * step + g < n && on[ti[u]];
+      held[u].finish(low(ti[u], hi[u]), high(ti[u], hi[u]), k, pairs, hd.w, is, l, width,
+                     turns + ti[u] * half);
     }
   }
-  return true;
+}
+
+constexpr int kMaxTokens = 8;  // of a block
+
+// Angles of the block's tokens, all at once.
+template <typename T>
+__device__ __forceinline__ void make_turns(Turn<T>* turns, const double* pos, const bool* on, int nt,
+                                           int half, bool pairs, const InvFreq& inv, double mag) {
+  for (int x = threadIdx.x; x < nt * half; x += blockDim.x) {
+    const int i = x / half, k = x - i * half;
+    if (on[i]) turns[i * half + turn_slot<T>(k, half, pairs)] = Turn<T>::make(__dmul_rn(pos[i], inv.v[k]), mag);
+  }
 }
 
 struct RopeParams {
   const void* in;
   void* out;
   int64_t in_token, in_head, out_token, out_head;
-  int heads, per_block;
+  int T, heads, per_block, tokens;
   Kind kind;
-  int pairs, vec, width;
+  int pairs, width;
   const int32_t* positions;
   double sign, mag;
 };
 
-template <typename T>
+template <typename T, int NV>
 __global__ void __launch_bounds__(kMaxThreads)
     rope_kernel(const RopeParams p, const __grid_constant__ InvFreq inv) {
   extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ double pos[kMaxTokens];
+  __shared__ bool on[kMaxTokens];
   Turn<T>* turns = reinterpret_cast<Turn<T>*>(smem);
-  const int64_t t = blockIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+  const int nt = (int)min((int64_t)p.tokens, p.T - t0);
   const int h0 = (int)blockIdx.y * p.per_block, nh = min(p.per_block, p.heads - h0);
-  const T* src = (const T*)p.in + t * p.in_token + h0 * p.in_head;
-  T* dst = (T*)p.out + t * p.out_token + h0 * p.out_head;
-  const Heads<T> hd{src, dst, dst, nullptr, p.in_head, p.out_head, p.out_head};
+  const Heads<T> hd{(const T*)p.in, (T*)p.out,   (T*)p.out,  nullptr,     p.in_token, p.in_head,
+                    p.out_token,    p.out_head, p.out_token, p.out_head, t0,          h0,
+                    nh,             nt};
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const double pos = (double)p.positions[t] * p.sign;
-  turn_heads<T, 1>(hd, p.kind, p.pairs, p.vec, nh, p.width, turns, [&]() {
-    const int half = p.kind.rot / 2;
-    for (int k = threadIdx.x; k < half; k += blockDim.x)
-      turns[turn_slot<T>(k, half, p.pairs)] = Turn<T>::make(__dmul_rn(pos, inv.v[k]), p.mag);
+  turn_heads<T, NV>(hd, p.kind, p.pairs, p.width, turns, on, [&]() {
+    if (threadIdx.x < nt) {
+      pos[threadIdx.x] = (double)p.positions[t0 + threadIdx.x] * p.sign;
+      on[threadIdx.x] = true;
+    }
     __syncthreads();
-    return true;
+    make_turns<T>(turns, pos, on, nt, p.kind.rot / 2, p.pairs, inv, p.mag);
+    __syncthreads();
   });
 }
 
@@ -356,9 +382,9 @@ struct NormRopeParams {
   void *q_nope, *q_pe, *c_kv, *k_pe;
   int64_t q_token, q_head, kv_token, ckv_row, kpe_row;
   int64_t nope_token, nope_head, pe_token, pe_head;
-  int T, B, H, per_block, groups;
+  int T, B, H, per_block, tokens;
   Kind q_kind, c_kind, k_kind;
-  int pairs, q_vec, q_width, c_vec, k_vec, k_width;
+  int pairs, q_width, c_vec, k_vec;
   CacheGeom cache;
   int64_t num_rows;
   const int32_t* q_start;
@@ -370,7 +396,7 @@ struct NormRopeParams {
 
 // The sequence of packed token t: the last b with q_start[b] <= t (-1 if there is none, B past
 // the last), by one warp in rounds of 32 probes.
-__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ q_start, int B, int t, int lane) {
+__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ q_start, int B, int64_t t, int lane) {
   int lo = 0, n = B + 1;  // the answer is lo - 1 .. lo + n - 1
   while (n > 0) {
     const int step = (n + 31) / 32, i = lo + lane * step;
@@ -386,101 +412,80 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ q_start, 
   return lo - 1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kMaxThreads)
+template <typename T, int NV>
+__global__ void __launch_bounds__(kMaxThreads, 3)
     norm_rope_kernel(const NormRopeParams p, const __grid_constant__ InvFreq inv) {
   extern __shared__ __align__(16) unsigned char smem[];
   Turn<T>* turns = reinterpret_cast<Turn<T>*>(smem);
-  __shared__ int64_t s_row;     // the token's cache row, -1: none
-  __shared__ double s_pos;
-  __shared__ int s_on;
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int64_t rows[kMaxTokens];  // the tokens' cache rows, -1: none
+  __shared__ double pos[kMaxTokens];
+  __shared__ bool on[kMaxTokens];
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+  const int nt = (int)min((int64_t)p.tokens, p.T - t0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int h0 = (int)blockIdx.y * p.per_block, nh = max(0, min(p.per_block, p.H - h0));
   const bool keys = p.kv && blockIdx.y == gridDim.y - 1;
-  const Heads<T> hd{(const T*)p.q + t * p.q_token + h0 * p.q_head,
-                    (T*)p.q_nope + t * p.nope_token + h0 * p.nope_head,
-                    (T*)p.q_pe + t * p.pe_token + h0 * p.pe_head,
-                    (const T*)p.q_w,
-                    p.q_head,
-                    p.nope_head,
-                    p.pe_head};
+  const Heads<T> hd{(const T*)p.q, (T*)p.q_nope, (T*)p.q_pe,  (const T*)p.q_w, p.q_token, p.q_head,
+                    p.nope_token,  p.nope_head,  p.pe_token, p.pe_head,       t0,        h0,
+                    max(nh, 1),    nh > 0 ? nt : 0};
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   auto ready = [&]() {
-    if (warp == 0) {
-      const int b = sequence_of(p.q_start, p.B, (int)t, lane);
-      if (lane == 0) {
-        bool on = b >= 0 && b < p.B;
-        int64_t row = -1;
-        if (on) {
-          const int64_t i = t - p.q_start[b];
-          const int64_t dep = p.depth ? p.depth[t] : i;
-          const int P = p.prefix_len[b];
-          if (dep < 0) on = false;  // a node of an invalid tree: the row is left alone
-          if (on && P < 0) {
-            on = false;
-            report(p.status, TV_ERR_BOUNDS);
+    for (int i = warp; i < nt; i += nw) {
+      const int64_t t = t0 + i;
+      const int b = sequence_of(p.q_start, p.B, t, lane);
+      if (lane > 0) continue;
+      bool is = b >= 0 && b < p.B;
+      int64_t row = -1;
+      if (is) {
+        const int64_t at = t - p.q_start[b];
+        const int64_t dep = p.depth ? p.depth[t] : at;
+        const int P = p.prefix_len[b];
+        if (P < 0) report(p.status, TV_ERR_BOUNDS);
+        is = dep >= 0 && P >= 0;  // (a node of an invalid tree is left alone)
+        pos[i] = (double)P + (double)dep;
+        if (is && keys) {
+          const int64_t j = (int64_t)P + at;
+          if (p.cache.page_table) {
+            const int64_t pg =
+                j / p.cache.page_size < p.cache.max_pages
+                    ? p.cache.page_table[(int64_t)b * p.cache.max_pages + j / p.cache.page_size]
+                    : -1;
+            if (pg >= 0) row = pg * p.cache.page_size + j % p.cache.page_size;
+          } else if (j < p.cache.kv_stride_b) {
+            row = (int64_t)b * p.cache.kv_stride_b + j;
           }
-          if (on) {
-            s_pos = (double)P + (double)dep;
-            const int64_t j = (int64_t)P + i;
-            if (keys) {
-              if (p.cache.page_table) {
-                const int64_t pg = j / p.cache.page_size < p.cache.max_pages
-                                       ? p.cache.page_table[(int64_t)b * p.cache.max_pages +
-                                                            j / p.cache.page_size]
-                                       : -1;
-                if (pg >= 0) row = pg * p.cache.page_size + j % p.cache.page_size;
-              } else if (j < p.cache.kv_stride_b) {
-                row = (int64_t)b * p.cache.kv_stride_b + j;
-              }
-              if (row >= p.num_rows) row = -1;
-              if (row < 0) report(p.status, TV_ERR_BOUNDS);
-            }
-          }
+          if (row >= p.num_rows) row = -1;
+          if (row < 0) report(p.status, TV_ERR_BOUNDS);
         }
-        s_on = on;
-        s_row = row;
       }
+      on[i] = is;
+      rows[i] = row;
     }
     __syncthreads();
-    if (!s_on) return false;
-    const int half = p.k_kind.rot / 2;
-    const double pos = s_pos;
-    for (int k = threadIdx.x; k < half; k += blockDim.x)
-      turns[turn_slot<T>(k, half, p.pairs)] = Turn<T>::make(__dmul_rn(pos, inv.v[k]), p.mag);
+    make_turns<T>(turns, pos, on, nt, p.k_kind.rot / 2, p.pairs, inv, p.mag);
     __syncthreads();
-    return true;
   };
-  if (!turn_heads<T, 1>(hd, p.q_kind, p.pairs, p.q_vec, nh, p.q_width, turns, ready)) return;
-  const int64_t row = s_row;
-  if (!keys || row < 0) return;
-  const int nw = blockDim.x >> 5;
-  const T* src = (const T*)p.kv + t * p.kv_token;
-  // the last warp takes the latent row, the one before it (if there is one) the rope part
-  if (warp == nw - 1) {
-    T* dst = (T*)p.c_kv + row * p.ckv_row;
-    const Place<T> pl{src, dst, dst, (const T*)p.kv_w};
-    if (p.c_vec) {
+  turn_heads<T, NV>(hd, p.q_kind, p.pairs, p.q_width, turns, on, ready);
+  if (!keys) return;
+  // the tokens' latent rows and rope parts, a warp each
+  const int half = p.k_kind.rot / 2;
+  for (int x = nw - 1 - warp; x < 2 * nt; x += nw) {
+    const int i = x >> 1;
+    const int64_t row = rows[i];
+    if (row < 0) continue;
+    const bool latent = (x & 1) == 0;
+    const Kind& k = latent ? p.c_kind : p.k_kind;
+    const T* src = (const T*)p.kv + (t0 + i) * p.kv_token + (latent ? 0 : p.c_kind.n);
+    T* dst = latent ? (T*)p.c_kv + row * p.ckv_row : (T*)p.k_pe + row * p.kpe_row;
+    const T* w = (const T*)(latent ? p.kv_w : p.k_w);
+    const Turn<T>* tt = turns + i * half;
+    if (latent ? p.c_vec : p.k_vec) {
       Held<T, kMaxVecs> held;
-      held.load(src, p.c_kind, true, true, lane, 32);
-      held.finish(pl, p.c_kind, true, true, lane, 32, turns);
+      held.load(src, k, p.pairs, true, lane, 32);
+      held.finish(dst, dst, k, p.pairs, w, true, lane, 32, tt);
     } else {
-      one_by_one<T>(pl, p.c_kind, true, turns, lane);
-    }
-  }
-  if (warp == max(0, nw - 2)) {
-    T* dst = (T*)p.k_pe + row * p.kpe_row;
-    const T* s = src + p.c_kind.n;
-    const Place<T> pl{s, dst, dst, (const T*)p.k_w};
-    if (p.k_vec) {
-      Held<T, 1> held;
-      const bool on = lane < p.k_width;
-      held.load(s, p.k_kind, p.pairs, on, lane, 32);
-      held.finish(pl, p.k_kind, p.pairs, on, lane, 32, turns);
-    } else {
-      one_by_one<T>(pl, p.k_kind, p.pairs, turns, lane);
+      one_by_one<T>(src, dst, dst, w, k, p.pairs, tt, lane);
     }
   }
 }
@@ -490,30 +495,42 @@ bool fits(const void* p) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// Whether a kind of vector can be handled 16 bytes at a time by at most `vecs` per lane, and by
-// how many lanes (a power of two).
+// Lanes that hold a head of a kind (a power of two) and their vectors, with as few lanes idle as
+// up to `vecs` vectors a lane allow, fewer vectors first; 0: it has to go one by one.
 template <typename T>
-bool whole_vectors(const Kind& k, bool pairs, int vecs, int* width) {
+int lanes_for(const Kind& k, bool pairs, int vecs, int* per_lane) {
   constexpr int N = Vec16<T>::N;
-  const int part = pairs ? k.rot : k.rot / 2;
-  *width = 32;
-  if (k.n % N || k.split % N || k.at % N || part % N || k.n > 32 * N * vecs) return false;
-  while (*width > 1 && (*width / 2) * N >= k.n) *width /= 2;
-  return true;
+  const int part = pairs ? k.rot : k.rot / 2, n = k.n / N;
+  *per_lane = 1;
+  if (k.n % N || k.split % N || k.at % N || part % N) return 0;
+  int best = 0, waste = 1 << 30;
+  for (int v = 1; v <= vecs; ++v)
+    for (int w = 1; w <= 32; w *= 2)
+      if (w * v >= n && w * v - n < waste) {
+        waste = w * v - n;
+        best = w;
+        *per_lane = v;
+      }
+  return best;
 }
 
-// Heads per block and threads: where the tokens are few their heads go to several blocks, about
-// two per SM in all; a warp has `vectors` heads at a time.
-struct Shape {
-  int per_block, groups, threads;
+// Tokens and heads per block, and threads.  `fit` blocks of 256 threads fit an SM: a block takes as
+// many tokens as fill the GPU once (eight at most), and where the tokens are fewer than two per SM
+// their heads go to several blocks.
+struct Grid {
+  int tokens, per_block, groups, threads;
 };
-Shape shape(int64_t tokens, int heads, int per_warp) {
-  const int64_t want = 2ll * current_sm_count();
-  const int groups = tokens >= want ? 1 : (int)std::min<int64_t>(std::max(heads, 1), (want + tokens - 1) / tokens);
-  Shape s;
+Grid grid_for(int64_t tokens, int heads, int per_warp, int half, int turn_bytes, int fit) {
+  const int64_t sms = current_sm_count();
+  Grid s;
+  const int room = std::max(1, 16384 / (half * turn_bytes));  // 16 KB of turns
+  s.tokens = (int)std::min<int64_t>(std::min(kMaxTokens, room), (tokens + fit * sms - 1) / (fit * sms));
+  const int64_t want = 2 * sms;
+  const int groups =
+      tokens >= want ? 1 : (int)std::min<int64_t>(std::max(heads, 1), (want + tokens - 1) / tokens);
   s.per_block = std::max(1, (heads + groups - 1) / groups);
   s.groups = std::max(1, (heads + s.per_block - 1) / s.per_block);
-  const int warps = (s.per_block + 2 * per_warp - 1) / (2 * per_warp);
+  const int warps = (s.per_block * s.tokens + per_warp - 1) / per_warp;
   s.threads = 32 * std::min(kMaxThreads / 32, std::max(2, warps));
   return s;
 }
@@ -573,15 +590,25 @@ cudaError_t launch_rope_t(const tv_rope_args* a, cudaStream_t st) {
     p.kind = {a->rot_dim, 0, a->rot_dim, a->rot_dim, 0.f};
   }
   p.pairs = a->layout == TV_ROPE_INTERLEAVED;
-  p.vec = whole_vectors<T>(p.kind, p.pairs, 1, &p.width) && fits<T>(p.in) && fits<T>(p.out) &&
-          p.in_token % N == 0 && p.in_head % N == 0 && p.out_token % N == 0 && p.out_head % N == 0;
+  int vecs = 1;
+  p.width = lanes_for<T>(p.kind, p.pairs, kMaxVecs, &vecs);
+  if (!(fits<T>(p.in) && fits<T>(p.out) && p.in_token % N == 0 && p.in_head % N == 0 &&
+        p.out_token % N == 0 && p.out_head % N == 0))
+    p.width = 0;
+  p.T = a->T;
   p.positions = a->positions;
   p.sign = a->inverse ? -1.0 : 1.0;
   const InvFreq& inv = table_of(a->scaling, a->rot_dim, &p.mag);
-  const Shape s = shape(a->T, a->n_heads, p.vec ? 32 / p.width * kAhead / 2 : 1);
+  const Grid s = grid_for(a->T, a->n_heads, p.width ? 32 / p.width : 1, a->rot_dim / 2, sizeof(Turn<T>), 4);
   p.per_block = s.per_block;
-  return start(rope_kernel<T>, dim3((unsigned)a->T, (unsigned)s.groups), s.threads,
-               sizeof(Turn<T>) * (a->rot_dim / 2), st, p, inv);
+  p.tokens = s.tokens;
+  const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
+  const size_t smem = sizeof(Turn<T>) * (a->rot_dim / 2) * s.tokens;
+  auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
+  return vecs == 1   ? go(rope_kernel<T, 1>)
+         : vecs == 2 ? go(rope_kernel<T, 2>)
+         : vecs == 3 ? go(rope_kernel<T, 3>)
+                     : go(rope_kernel<T, 4>);
 }
 
 template <typename T>
@@ -613,13 +640,15 @@ cudaError_t launch_norm_rope_t(const tv_norm_rope_args* a, cudaStream_t st) {
   p.c_kind = {a->d_latent, 0, 0, a->d_latent, a->eps};
   p.k_kind = {a->d_rope, 0, a->rot_dim, a->d_rope, a->eps};
   p.pairs = a->layout == TV_ROPE_INTERLEAVED;
-  int w;
-  p.q_vec = whole_vectors<T>(p.q_kind, p.pairs, 1, &p.q_width) && fits<T>(a->q) && fits<T>(a->q_nope) &&
-            fits<T>(a->q_pe) && fits<T>(a->q_weight) && p.q_token % N == 0 && p.q_head % N == 0;
+  int vecs = 1, kv_vecs;
+  p.q_width = a->q ? lanes_for<T>(p.q_kind, p.pairs, kMaxVecs, &vecs) : 0;
+  if (!(fits<T>(a->q) && fits<T>(a->q_nope) && fits<T>(a->q_pe) && fits<T>(a->q_weight) &&
+        p.q_token % N == 0 && p.q_head % N == 0))
+    p.q_width = 0;
   const bool kv_ok = fits<T>(a->kv) && p.kv_token % N == 0 && a->d_latent % N == 0;
-  p.c_vec = whole_vectors<T>(p.c_kind, true, kMaxVecs, &w) && kv_ok && fits<T>(a->c_kv) &&
+  p.c_vec = lanes_for<T>(p.c_kind, true, kMaxVecs, &kv_vecs) && kv_ok && fits<T>(a->c_kv) &&
             p.ckv_row % N == 0 && fits<T>(a->kv_weight);
-  p.k_vec = whole_vectors<T>(p.k_kind, p.pairs, 1, &p.k_width) && kv_ok && fits<T>(a->k_pe) &&
+  p.k_vec = lanes_for<T>(p.k_kind, p.pairs, kMaxVecs, &kv_vecs) && kv_ok && fits<T>(a->k_pe) &&
             p.kpe_row % N == 0 && fits<T>(a->k_weight);
   p.cache = {a->cache.page_table, a->cache.page_size, a->cache.max_pages, a->cache.kv_stride_b};
   p.num_rows = a->cache.num_rows;
@@ -628,10 +657,16 @@ cudaError_t launch_norm_rope_t(const tv_norm_rope_args* a, cudaStream_t st) {
   p.depth = a->depth;
   p.status = a->status;
   const InvFreq& inv = table_of(a->scaling, a->rot_dim, &p.mag);
-  const Shape s = shape(a->T, p.H, p.q_vec ? 32 / p.q_width * kAhead / 2 : 1);
+  const Grid s = grid_for(a->T, p.H, p.q_width ? 32 / p.q_width : 1, a->rot_dim / 2, sizeof(Turn<T>), 3);
   p.per_block = s.per_block;
-  return start(norm_rope_kernel<T>, dim3((unsigned)a->T, (unsigned)s.groups), s.threads,
-               sizeof(Turn<T>) * (a->rot_dim / 2), st, p, inv);
+  p.tokens = s.tokens;
+  const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
+  const size_t smem = sizeof(Turn<T>) * (a->rot_dim / 2) * s.tokens;
+  auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
+  return vecs == 1   ? go(norm_rope_kernel<T, 1>)
+         : vecs == 2 ? go(norm_rope_kernel<T, 2>)
+         : vecs == 3 ? go(norm_rope_kernel<T, 3>)
+                     : go(norm_rope_kernel<T, 4>);
 }
 
 }  // namespace
