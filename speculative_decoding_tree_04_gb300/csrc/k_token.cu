@@ -1,25 +1,34 @@
 // k_token.cu -- next tokens with temperature, top-k, top-p and min-p (tv_token_sample).
 //
 // All filters keep a beginning of one order, falling logit and then index, so what they leave
-// is a cut: every token above a logit, and the first few (by index) of those equal to it.
-// top_k's cut is the k-th token's; top_p's the token at which the running sum of weights reaches
-// p W, W the sum of what top_k keeps; min_p is a bound on the weight itself.  The token is then
-// drawn in index order from what is kept.
+// ends at one token, the cut: top_k's is the k-th; top_p's the token at which the running sum of
+// weights reaches p W, W the sum of what top_k keeps; min_p bounds the weight itself.  The token
+// is then drawn in index order from what is kept.
 //
-// Finding a cut.  A row's tokens are counted (top_k) or their weights summed (top_p) in kBins
-// bins of falling logit; the bin in which the running total passes the target is found, and its
-// tokens are binned again, finer, until a bin is a single logit.  The first bins are linear in
-// the logit (kSpan units of log2 of the weight, and one bin for all below), which spreads a
-// model's logits evenly; the next ones cut the ordered bit patterns between that bin's smallest
-// and largest: one level more for bf16, mostly two for float32, four at worst.  Weights are the
-// exact integers of tv_tree_sample (sample_math.h), added in three parts of 15 bits, whose sums
-// over a slice of 2^16 tokens stay within 32 bits: sums in any order, results that do not depend
-// on it.
+// Weights are the exact integers of tv_tree_sample (sample_math.h), and all decisions are taken
+// on exact sums.  An exact weight costs some 45 instructions, so the passes over a row are
+// arranged to take each at most about once:
+//   1. the maximum;
+//   2. counts of the tokens in kBins bins that are linear in the logit (kSpan units of log2 of
+//      the weight, the last bin for all below);
+//   top_k: the counts say in which bin the k-th token lies;
+//   top_p: a bin's weights lie within a factor 2^(kSpan / kBins), so the counts bound the running
+//      sums to about 1 %, and the cut to a window of bins;
+//   3. (top_p) exact sums: of the row, of the tokens above the window by warp, and of the
+//      window's tokens in kFine finer bins, one of which then holds the cut;
+//   4. the tokens of the cut's bin go into a list, and are compared with one another.
+//   5. the kept tokens' sums by warp (after top_p alone: the window's, added to those of 3), and
+//      the draw within one warp's slice.
+// Where the bins down to the cut hold few tokens altogether (top_k of common sizes, peaked
+// distributions) all of them go into the list and the rest happens there.  Where the cut's own
+// bin holds too many for the list (equal logits) it is cut by ordered bit patterns, level by
+// level, until a bin is one value.
 //
-// Work.  A cluster of CTAs shares a row.  Every CTA reads its contiguous slice once into shared
-// memory and works on it there.  Per level the CTAs' bins are added up by parts (each CTA the
-// same share of bins, through distributed shared memory), the parts' totals exchanged, and the
-// owner of the passing bin tells the others.
+// Work.  A cluster of CTAs shares a row, each CTA a contiguous slice, each warp a part of it;
+// after the first pass the row comes from L2.  Bins are added up over the cluster through
+// distributed shared memory, each CTA the same share of them, and given to every CTA, which all
+// take the same decisions from the same numbers.  Sums are of integers: no result depends on the
+// order they are taken in, or on how a row is split.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -34,10 +43,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kMaxCluster = 16;
-constexpr int kMaxWarps = 16;
-constexpr int kBins = 1024;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 4096, kFine = 2048;
 constexpr float kSpan = 48.f;  // log2 units of the linear bins: below, weights are zero
-constexpr int kSliceBytes = 64 * 1024;  // of a row per CTA: 2^18 floats by 16 CTAs
+constexpr int kList = 512;     // tokens of a list at most
+constexpr int kSmall = 256;    // of one that holds every kept token
 
 struct TokenParams {
   const void* logits;
@@ -54,31 +64,25 @@ struct TokenParams {
 
 struct Shared {
   float2 exp2_table[kTable * kCopies];
-  uint32_t bins[3][kBins];        // counts, or 15-bit parts of the weights' sums
-  int64_t own[kBins];             // this CTA's share of the bins, over all CTAs
+  uint32_t bins[3 * kFine];       // this CTA's: counts (kBins), or 15-bit parts of weights' sums
+  int64_t all[kFine];             // the cluster's: counts (kBins of 32 bits), or sums
+  uint64_t list[kList];           // this CTA's tokens: key, complemented index
+  uint64_t merged[kList];         // the cluster's,
+  int64_t merged_w[kList];        // and their weights
+  int32_t list_n;
   uint64_t keys[kMaxCluster];     // exchanged: the slices' maxima,
-  int64_t totals[kMaxCluster];    // their sums of a share of bins,
-  int64_t found[2];               // the bin that a target lies in, and what is left of it,
-  int64_t mass[kMaxCluster];      // sums of the kept tokens above the cut,
-  int32_t count[kMaxCluster];     // how many they are,
-  int32_t ties[kMaxCluster];      // and how many tokens lie on it
-  uint64_t warp_key[kMaxWarps];
-  int64_t warp_mass[kMaxWarps];
-  int32_t warp_count[kMaxWarps], warp_ties[kMaxWarps];
+  int32_t lists[kMaxCluster];     // lengths of lists,
+  int64_t mass[2][kMaxCluster];   // sums,
+  int32_t count[kMaxCluster];     // and counts
+  uint64_t warp_key[kWarps];
+  int64_t warp_mass[kWarps];
+  int32_t warp_count[kWarps];
+  float warp_lo[kWarps], warp_hi[kWarps];
+  int64_t found[2];               // a bin, and the total before it
+  int32_t window[2];
+  uint64_t cut;
 };
-
-// Ordered keys of a type's values: 32 bits, or the upper 16 of a bf16.
-template <typename T>
-struct Key {
-  static constexpr int kShift = sizeof(T) == 2 ? 16 : 0;
-  __device__ static uint32_t of(float v) { return ordered(v) >> kShift; }
-  __device__ static float value(uint32_t k) {
-    const bool pos = k >> (31 - kShift);
-    return unordered(sizeof(T) == 2 ? (k << 16) | (pos ? 0u : 0xFFFFu) : k);
-  }
-  static constexpr uint32_t kMasked = 0x007FFFFFu >> kShift;  // of -inf
-  static constexpr uint32_t kTop = 0xFF800000u >> kShift;     // of +inf
-};
+static_assert(kBins <= 2 * kFine && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(const void* local, uint32_t rank) {
   uint32_t v;
@@ -86,13 +90,35 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* local, uint32_t r
   return v;
 }
 
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
-    token_sample_kernel(const TokenParams p, int log2_C) {
-  constexpr int kWarps = kThreads / 32, N = Vec<T>::N;
+__device__ __forceinline__ uint64_t ld_cluster_u64(const void* local, uint32_t rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_u32(local), rank)) : "memory");
+  return v;
+}
+
+// Exclusive prefix sum of one value a thread over the block; *total is the sum.
+template <typename S>
+__device__ __forceinline__ S block_scan(S v, S* warps, S* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  S up_to = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const S below = __shfl_up_sync(0xffffffffu, up_to, o);
+    if (lane >= o) up_to += below;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = up_to;
+  __syncthreads();
+  const S mine = lane < kWarps ? warps[lane] : (S)0;
+  *total = warp_sum(mine);
+  return up_to - v + warp_sum(lane < warp ? mine : (S)0);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenParams p, int log2_C) {
+  constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  uint4* slice = reinterpret_cast<uint4*>(smem + (sizeof(Shared) + 15) / 16 * 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = 1 << log2_C, b = blockIdx.x >> log2_C;
   const int rank = C > 1 ? (int)cluster_rank() : 0;
@@ -113,77 +139,85 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
   // (a CTA's shared memory may be written once it is known to have started)
   if (C > 1) cluster_arrive();
-  for (int i = tid; i < kTable * kCopies; i += kThreads)
-    sh.exp2_table[i] = make_float2(d_exp.hi[i / kCopies], d_exp.lo[i / kCopies]);
+  auto sync = [&]() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  };
   constexpr float l2e = (float)(1.0 / kLn2), l2e_low = (float)(1.0 / kLn2 - (double)l2e);
   const float cq = l2e / T0;
   const float ch = fminf(fmaxf(cq, 1e-30f), 1e30f);
   const float cl = ch == cq ? (fmaf(-cq, T0, l2e) + l2e_low) / T0 : 0.f;
 
-  // ---- the slice into shared memory, and the row's maximum with its first index ----
+  // This warp's vectors, and what it does with every one of them: fn(values, index of the first).
   const Row<T> row((const T*)p.logits + (int64_t)b * p.stride, p.V);
-  const int per = (row.n_vec + C - 1) >> log2_C;
-  const int c0 = min(row.n_vec, rank * per), n_vec = min(row.n_vec, c0 + per) - c0;
+  const int per = (row.n_vec + C - 1) >> log2_C, per_w = (per + kWarps - 1) / kWarps;
+  const int c0 = min(row.n_vec, rank * per), c1 = min(row.n_vec, c0 + per);
+  const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
+  const int e0 = row.first_whole(), e1 = row.end_whole();
+  auto vector = [&](int j) {
+    if (j >= e0 && j < e1) return row.raw(j);
+    alignas(16) T v[N];  // an end of the row
+    const int64_t a = row.first(j);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = a + i >= 0 && a + i < p.V ? row.x[a + i] : (T)-INFINITY;
+    return *reinterpret_cast<const uint4*>(v);
+  };
+  auto each = [&](auto fn) {
+    constexpr int kUnroll = 4;
+#pragma unroll 1
+    for (int j0 = w0 + lane; j0 < w1; j0 += 32 * kUnroll) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (j0 + 32 * k < w1) w[k] = vector(j0 + 32 * k);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (j0 + 32 * k >= w1) break;
+        float v[N];
+        Vec<T>::unpack(w[k], v);
+        fn(v, (int)row.first(j0 + 32 * k));
+      }
+    }
+  };
+
+  // ---- the row's maximum, with its first index ----
+  uint64_t top;
   {
     float best = -INFINITY;
     int best_at = 0;
     bool is_nan = false;
-    constexpr int kUnroll = 8;
-    for (int j0 = tid; j0 < n_vec; j0 += kUnroll * kThreads) {
-      uint4 w[kUnroll];
+    each([&](const float* v, int a) {
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int j = j0 + k * kThreads;
-        if (j >= n_vec) break;
-        if (row.whole(c0 + j)) {
-          w[k] = row.raw(c0 + j);
-        } else {  // an end of the row
-          const int64_t a = row.first(c0 + j);
-          alignas(16) T v[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            v[i] = a + i >= 0 && a + i < p.V ? row.x[a + i] : (T)-INFINITY;
-          w[k] = *reinterpret_cast<const uint4*>(v);
+      for (int i = 0; i < N; ++i) {
+        is_nan |= v[i] != v[i];
+        if (v[i] > best) {
+          best = v[i];
+          best_at = a + i;
         }
       }
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int j = j0 + k * kThreads;
-        if (j >= n_vec) break;
-        slice[j] = w[k];
-        float v[N];
-        Vec<T>::unpack(w[k], v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          is_nan |= v[i] != v[i];
-          if (v[i] > best) {
-            best = v[i];
-            best_at = (int)row.first(c0 + j) + i;
-          }
-        }
-      }
-    }
+    });
+    for (int i = tid; i < kTable * kCopies; i += kThreads)
+      sh.exp2_table[i] = make_float2(d_exp.hi[i / kCopies], d_exp.lo[i / kCopies]);
     // order-preserving value bits, then the complemented index; a NaN beats every value
-    uint64_t key = best > -INFINITY
-                       ? ((uint64_t)ordered(best) << 32) | (0xFFFFFFFFu - (uint32_t)best_at)
-                       : 0ull;
-    key = warp_max(key);
-    if (__any_sync(0xffffffffu, is_nan)) key = ~0ull;
-    if (lane == 0) sh.warp_key[warp] = key;
+    top = best > -INFINITY
+              ? ((uint64_t)ordered(best) << 32) | (0xFFFFFFFFu - (uint32_t)best_at)
+              : 0ull;
+    top = warp_max(top);
+    if (__any_sync(0xffffffffu, is_nan)) top = ~0ull;
+    if (lane == 0) sh.warp_key[warp] = top;
     if (C > 1) cluster_wait();
     __syncthreads();
     if (warp == 0) {
-      key = warp_max(lane < kWarps ? sh.warp_key[lane] : 0ull);
+      top = warp_max(lane < kWarps ? sh.warp_key[lane] : 0ull);
       if (C == 1) {
-        if (lane == 0) sh.keys[0] = key;
+        if (lane == 0) sh.keys[0] = top;
       } else if (lane < C) {
-        st_cluster_u64(&sh.keys[rank], (uint32_t)lane, key);
+        st_cluster_u64(&sh.keys[rank], (uint32_t)lane, top);
       }
     }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
+    sync();
+    top = warp_max(lane < C ? sh.keys[lane] : 0ull);
   }
-  const uint64_t top = warp_max(lane < C ? sh.keys[lane] : 0ull);
   const float m = unordered((uint32_t)(top >> 32));
   const bool none = top == 0 || top == ~0ull || m == INFINITY;
   if (none || greedy) {
@@ -196,118 +230,175 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     return;
   }
 
-  // ---- the cut: keys above cut_key are kept, and the first `ties` tokens at it ----
-  uint32_t cut_key = Key<T>::kMasked;
-  int64_t ties = 0;
   const float per_bin = ch * ((float)(kBins - 1) / kSpan);
   auto weight_of = [&](float v) { return units(weight(v, m, ch, cl, sh.exp2_table)); };
-  // the linear bin of a value: falling in it, so that a bin is a range of keys
+  // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
+  // a bin is a range of keys).
+  auto place = [&](float v, int index) {
+    return ((uint64_t)ordered(v) << 32) | (0xFFFFFFFFu - (uint32_t)index);
+  };
   auto linear = [&](float v) { return min((int)((m - v) * per_bin), kBins - 1); };
+  constexpr uint64_t kMasked = (uint64_t)0x007FFFFFu << 32 | 0xFFFFFFFFu;  // -inf, any index
+  uint64_t cut = kMasked + 1;  // tokens at or above it are kept
+  const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
+  const int64_t least = (int64_t)ceil((double)mp * (double)kUnit);
+  // (a token this far below the maximum is lighter than min_p without more ado)
+  const float far = mp > 0.f ? fminf(-__log2f(mp) * 1.0001f + 0.01f, 64.f) : INFINITY;
 
-  // Adds up the bins of the tokens above cut_key whose keys lie in [lo, hi]: counts (mass false)
-  // or weights.  Returns the total; then sh.totals holds the shares' and sh.own this one's.
-  const int share = kBins >> log2_C;
-  auto collect = [&](bool mass, bool first, uint32_t lo, uint32_t hi, int shift) {
-    const int words = mass ? 3 : 1;
-    for (int i = tid; i < words * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0u;
+  auto clear = [&](int n) {
+    for (int i = tid; i < n; i += kThreads) sh.bins[i] = 0u;
     __syncthreads();
-    for (int j = tid; j < n_vec; j += kThreads) {
-      float v[N];
-      Vec<T>::unpack(slice[j], v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t key = Key<T>::of(v[i]);
-        if (key <= cut_key || key < lo || key > hi) continue;
-        const int bin = first ? linear(v[i]) : (int)((hi - key) >> shift);
-        if (!mass) {
-          atomicAdd(&sh.bins[0][bin], 1u);
-          continue;
-        }
-        const uint64_t w = (uint64_t)weight_of(v[i]);
-        if (w == 0) continue;
-        atomicAdd(&sh.bins[0][bin], (uint32_t)w & 0x7FFFu);
-        atomicAdd(&sh.bins[1][bin], (uint32_t)(w >> 15) & 0x7FFFu);
-        atomicAdd(&sh.bins[2][bin], (uint32_t)(w >> 30));
+  };
+  auto add_mass = [&](int bin, uint64_t w) {
+    atomicAdd(&sh.bins[bin], (uint32_t)w & 0x7FFFu);
+    atomicAdd(&sh.bins[kFine + bin], (uint32_t)(w >> 15) & 0x7FFFu);
+    atomicAdd(&sh.bins[2 * kFine + bin], (uint32_t)(w >> 30));
+  };
+  // The cluster's bins from the CTAs': every CTA adds up its share and gives it to all.
+  auto merge_counts = [&]() {
+    sync();
+    uint32_t* all = reinterpret_cast<uint32_t*>(sh.all);
+    const int share = kBins >> log2_C;
+    for (int i = tid; i < share; i += kThreads) {
+      const int at = rank * share + i;
+      if (C == 1) {
+        all[at] = sh.bins[at];
+        continue;
       }
+      uint32_t s = 0;
+      for (int r = 0; r < C; ++r) s += ld_cluster_u32(&sh.bins[at], (uint32_t)r);
+      for (int r = 0; r < C; ++r) st_cluster_u32(&all[at], (uint32_t)r, s);
     }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    // this CTA's share of the bins: P threads a bin, each adding C / P of the CTAs'
-    const int P = min(C, max(1, kThreads / share));
-    int64_t total = 0;
-    for (int i = tid / P; i < share; i += kThreads / P) {
+    sync();
+  };
+  auto merge_mass = [&]() {
+    sync();
+    const int share = kFine >> log2_C;
+    for (int i = tid; i < share; i += kThreads) {
       const int at = rank * share + i;
       int64_t s = 0;
-      for (int r = tid % P; r < C; r += P) {
-        if (C == 1) {
-          s += sh.bins[0][at];
-          if (mass) s += ((int64_t)sh.bins[1][at] << 15) + ((int64_t)sh.bins[2][at] << 30);
-        } else {
-          s += ld_cluster_u32(&sh.bins[0][at], (uint32_t)r);
-          if (mass)
-            s += ((int64_t)ld_cluster_u32(&sh.bins[1][at], (uint32_t)r) << 15) +
-                 ((int64_t)ld_cluster_u32(&sh.bins[2][at], (uint32_t)r) << 30);
-        }
+      for (int part = 0; part < 3; ++part) {
+        int64_t x = 0;
+        if (C == 1) x = sh.bins[part * kFine + at];
+        else
+          for (int r = 0; r < C; ++r) x += ld_cluster_u32(&sh.bins[part * kFine + at], (uint32_t)r);
+        s += x << (15 * part);
       }
-      for (int o = P / 2; o > 0; o >>= 1) s += __shfl_xor_sync(__activemask(), s, o);
-      if (tid % P == 0) {
-        sh.own[i] = s;
-        total += s;
-      }
+      if (C == 1) sh.all[at] = s;
+      else
+        for (int r = 0; r < C; ++r) st_cluster_u64(&sh.all[at], (uint32_t)r, (uint64_t)s);
     }
-    total = warp_sum(total);
-    if (lane == 0) sh.warp_mass[warp] = total;
-    __syncthreads();
-    if (warp == 0) {
-      total = warp_sum(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0);
-      if (C == 1) {
-        if (lane == 0) sh.totals[0] = total;
-      } else if (lane < C) {
-        st_cluster_u64(&sh.totals[rank], (uint32_t)lane, (uint64_t)total);
-      }
-    }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    return warp_sum(lane < C ? sh.totals[lane] : (int64_t)0);
+    sync();
   };
-  // The bin in which the running total passes `target`, which becomes what is left of it there.
-  auto find = [&](int64_t* target) {
-    int64_t t = *target;
-    const int owner = locate(lane < C ? sh.totals[lane] : (int64_t)0, C, &t);
-    if (owner == rank && warp == 0) {
-      int bin = 0;
-      for (int i0 = 0; i0 < share; i0 += 32) {
-        const int n = min(32, share - i0);
-        const int64_t part = lane < n ? sh.own[i0 + lane] : 0;
-        const int64_t all = warp_sum(part);
-        if (t >= all && i0 + 32 < share) {
-          t -= all;
-          continue;
-        }
-        bin = i0 + locate(part, n, &t);
-        break;
-      }
-      if (C == 1) {
-        if (lane == 0) {
-          sh.found[0] = bin;
-          sh.found[1] = t;
-        }
-      } else if (lane < C) {
-        st_cluster_u64(&sh.found[0], (uint32_t)lane, (uint64_t)(rank * share + bin));
-        st_cluster_u64(&sh.found[1], (uint32_t)lane, (uint64_t)t);
-      }
+  // The bin of n in which the running total of get(bin) passes target; *before: the total up to it.
+  auto find = [&](int n, auto get, int64_t target, int64_t* before, int64_t* total) {
+    const int each_n = n / kThreads;
+    int64_t s = 0;
+    for (int i = 0; i < each_n; ++i) s += get(tid * each_n + i);
+    int64_t at = block_scan(s, sh.warp_mass, total);
+    if (at <= target && target < at + s) {
+      int i = tid * each_n;
+      for (int64_t x; at + (x = get(i)) <= target; ++i) at += x;
+      sh.found[0] = i;
+      sh.found[1] = at;
     }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-    *target = sh.found[1];
+    __syncthreads();
+    *before = sh.found[1];
     return (int)sh.found[0];
+  };
+  auto count_at = [&](int i) { return (int64_t) reinterpret_cast<const uint32_t*>(sh.all)[i]; };
+  auto mass_at = [&](int i) { return sh.all[i]; };
+  // The sum of one value a thread over the cluster.
+  int turn = 0;
+  auto total_of = [&](int64_t v) {
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sh.warp_mass[warp] = v;
+    __syncthreads();
+    v = warp_sum(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0);
+    if (C == 1) return v;
+    if (warp == 0 && lane < C) st_cluster_u64(&sh.mass[turn][rank], (uint32_t)lane, (uint64_t)v);
+    sync();
+    v = warp_sum(lane < C ? sh.mass[turn][lane] : (int64_t)0);
+    turn ^= 1;
+    return v;
+  };
+  // The cluster's list of the tokens that `take` says (kList at most), in any order, in sh.merged
+  // with their weights.  Returns its length.
+  auto gather = [&](auto take) {
+    __syncthreads();
+    if (tid == 0) sh.list_n = 0;
+    __syncthreads();
+    each([&](const float* v, int a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (!(v[i] > -INFINITY) || !take(v[i], a + i)) continue;
+        const int at = atomicAdd(&sh.list_n, 1);
+        if (at < kList) sh.list[at] = place(v[i], a + i);
+      }
+    });
+    __syncthreads();
+    if (C == 1) {
+      if (tid == 0) sh.lists[0] = sh.list_n;
+    } else if (warp == 0 && lane < C) {
+      st_cluster_u32(&sh.lists[rank], (uint32_t)lane, (uint32_t)sh.list_n);
+    }
+    sync();
+    int n = 0;
+    for (int r = 0; r < C; ++r) {
+      const int k = min(sh.lists[r], kList - n);
+      for (int i = tid; i < k; i += kThreads) {
+        const uint64_t x = C == 1 ? sh.list[i] : ld_cluster_u64(&sh.list[i], (uint32_t)r);
+        sh.merged[n + i] = x;
+        sh.merged_w[n + i] = weight_of(unordered((uint32_t)(x >> 32)));
+      }
+      n += k;
+    }
+    __syncthreads();
+    return n;
+  };
+  // Tokens of the list, P threads each: fn(token, its part), with P a power of two within a warp.
+  auto threads_per = [&](int n) {
+    int P = 32;
+    while (P > 1 && P * n > kThreads) P >>= 1;
+    return P;
+  };
+  // How many of the list's tokens come before token x, and their weights' sum.
+  auto before_in_list = [&](int n, int P, uint64_t x, int64_t* mass) {
+    int64_t count = 0, sum = 0;
+    for (int j = tid & (P - 1); j < n; j += P) {
+      const bool is = sh.merged[j] > x;
+      count += is;
+      sum += is ? sh.merged_w[j] : 0;
+    }
+    for (int o = P / 2; o > 0; o >>= 1) {
+      count += __shfl_xor_sync(0xffffffffu, count, o);
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    *mass = sum;
+    return count;
+  };
+  // The cut from a list that holds it: the token with `target` tokens (or weight up to it) before.
+  auto cut_in_list = [&](int n, bool mass, int64_t target) {
+    const int P = threads_per(n);
+    for (int e0_ = 0; e0_ < n; e0_ += kThreads / P) {
+      const int e = e0_ + tid / P;
+      const uint64_t x = e < n ? sh.merged[e] : ~0ull;
+      int64_t sum;
+      const int64_t count = before_in_list(n, P, x, &sum);
+      if (e < n && (tid & (P - 1)) == 0 &&
+          (mass ? sum <= target && target < sum + sh.merged_w[e] : count == target))
+        sh.cut = x;
+    }
+    __syncthreads();
+    return sh.cut;
   };
   // The smallest key whose linear bin is at most `bin`, by one probe a lane.
   auto first_key = [&](int bin) {
-    uint32_t lo = Key<T>::kMasked + 1, hi = Key<T>::of(m);  // linear(hi) = 0
+    uint32_t lo = 0x00800000u, hi = (uint32_t)(top >> 32);  // linear(hi) = 0
     while (lo < hi) {
       const uint32_t step = (hi - lo + 31) / 32, probe = min(hi, lo + (uint32_t)lane * step);
-      const uint32_t in = __ballot_sync(0xffffffffu, linear(Key<T>::value(probe)) <= bin);
+      const uint32_t in = __ballot_sync(0xffffffffu, linear(unordered(probe)) <= bin);
       const int at = __ffs(in) - 1;  // (none: the answer lies above the last probe)
       if (at == 0) return lo;
       const uint32_t below = lo + (uint32_t)(at < 0 ? 31 : at - 1) * step;
@@ -316,169 +407,323 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     }
     return lo;
   };
-  // Moves the cut to where the running total passes `target`, given the linear bins' totals.
-  auto narrow = [&](bool mass, int64_t target) {
-    const int bin = find(&target);
-    uint32_t lo = first_key(bin), hi = bin > 0 ? first_key(bin - 1) - 1 : Key<T>::of(m);
+  // The cut among more tokens than a list holds, of bins b0 .. b1, `target` tokens (or weight)
+  // into them: by key, level by level, then the first tokens at the last key by index.
+  auto refine = [&](bool mass, int b0, int b1, int64_t target) {
+    uint32_t lo = first_key(b1), hi = b0 > 0 ? first_key(b0 - 1) - 1 : (uint32_t)(top >> 32);
+    const uint64_t limit = cut;
     for (;;) {
       int shift = 0;
-      while (((hi - lo) >> shift) >= (uint32_t)kBins) ++shift;
-      collect(mass, false, lo, hi, shift);
-      const uint32_t at = (uint32_t)find(&target);
+      while (((hi - lo) >> shift) >= (uint32_t)kFine) ++shift;
+      clear(3 * kFine);
+      each([&](const float* v, int a) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t key = ordered(v[i]);
+          if (key < lo || key > hi || place(v[i], a + i) < limit) continue;
+          add_mass((int)((hi - key) >> shift), mass ? (uint64_t)weight_of(v[i]) : 1ull);
+        }
+      });
+      merge_mass();
+      int64_t before, total;
+      const uint32_t at = (uint32_t)find(kFine, mass_at, target, &before, &total);
+      target -= before;
       hi -= at << shift;
       if (shift == 0) break;
       const uint32_t width = (1u << shift) - 1;
       lo = hi - lo > width ? hi - width : lo;
     }
-    cut_key = hi;
-    // target: what the tokens at the cut may sum to before the last kept one
-    ties = mass ? target / weight_of(Key<T>::value(hi)) + 1 : target + 1;
-  };
-
-  if (top_k > 0 && top_k < p.V) {
-    const int64_t n = collect(false, true, 0u, Key<T>::kTop, 0);
-    if (top_k < n) narrow(false, (int64_t)top_k - 1);
-  }
-  if (top_p < 1.f) {
-    const int64_t above = collect(true, true, 0u, Key<T>::kTop, 0);
-    const int64_t tie = ties > 0 ? weight_of(Key<T>::value(cut_key)) : 0;
-    const int64_t W = above + ties * tie;
-    const int64_t share_of = (int64_t)ceil((double)fmaxf(top_p, 0.f) * (double)W);
-    const int64_t target = min(max(share_of, (int64_t)1), W) - 1;
-    if (target < above) narrow(true, target);
-    else ties = min(ties, (target - above) / tie + 1);
-  }
-  const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
-  const int64_t least = (int64_t)ceil((double)mp * (double)kUnit);
-  // (a token this far below the maximum is lighter than min_p without more ado)
-  const float far = mp > 0.f ? fminf(-__log2f(mp) * 1.0001f + 0.01f, 64.f) : INFINITY;
-  const int64_t tie = ties > 0 ? weight_of(Key<T>::value(cut_key)) : 0;
-  if (tie < least) ties = 0;
-
-  // ---- the kept tokens' sums by warps' slices, then the draw in index order ----
-  const int per_w = (per + kWarps - 1) / kWarps;
-  const int w0 = min(n_vec, warp * per_w), w1 = min(n_vec, w0 + per_w);
-  auto above = [&](float v, uint32_t key) {  // weight of a token above the cut, -1: not kept
-    if (key <= cut_key || (m - v) * ch > far) return (int64_t)-1;
-    const int64_t w = weight_of(v);
-    return w >= least ? w : (int64_t)-1;
-  };
-  {
-    int64_t mass = 0;
-    int count = 0, on_cut = 0;
-    for (int j = w0 + lane; j < w1; j += 32) {
-      float v[N];
-      Vec<T>::unpack(slice[j], v);
+    // the tokens at this key before the last kept one; then its index
+    int64_t n = mass ? target / weight_of(unordered(hi)) : target;
+    int64_t mine = 0;
+    each([&](const float* v, int a) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t key = Key<T>::of(v[i]);
-        on_cut += key == cut_key && ties > 0;
-        const int64_t w = above(v[i], key);
-        if (w < 0) continue;
-        mass += w;
-        ++count;
+      for (int i = 0; i < N; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
+    });
+    mine = warp_sum(mine);
+    __syncthreads();
+    if (lane == 0) sh.warp_count[warp] = (int)mine;
+    __syncthreads();
+    const int64_t all = warp_sum(lane < kWarps ? (int64_t)sh.warp_count[lane] : 0);
+    if (warp == 0 && lane < C) {
+      if (C == 1) sh.count[0] = (int)all;
+      else st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)all);
+    }
+    sync();
+    n -= warp_sum(lane < rank ? (int64_t)sh.count[lane] : (int64_t)0);
+    n -= warp_sum(lane < warp ? (int64_t)sh.warp_count[lane & (kWarps - 1)] : (int64_t)0);
+    if (n >= 0 && n < mine) {  // in this warp's slice
+      for (int j0 = w0; j0 < w1; j0 += 32) {
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = NAN;
+        if (j0 + lane < w1) Vec<T>::unpack(vector(j0 + lane), v);
+        const int a = (int)row.first(j0 + lane);
+        int64_t k = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) k += ordered(v[i]) == hi && v[i] == v[i] && place(v[i], a + i) >= limit;
+        const int64_t here = warp_sum(k);
+        if (n >= here) {
+          n -= here;
+          continue;
+        }
+        if (lane == locate(k, 32, &n)) {
+          uint64_t x = 0;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (ordered(v[i]) == hi && place(v[i], a + i) >= limit && n-- == 0) x = place(v[i], a + i);
+          for (int r = 0; r < C; ++r) {
+            if (C == 1) sh.cut = x;
+            else st_cluster_u64(&sh.cut, (uint32_t)r, x);
+          }
+        }
+        break;
       }
     }
+    sync();
+    return sh.cut;
+  };
+  // Counts of the kept tokens in the linear bins.
+  auto count = [&](bool limited) {
+    clear(kBins);
+    each([&](const float* v, int a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (v[i] > -INFINITY && (!limited || place(v[i], a + i) >= cut)) atomicAdd(&sh.bins[linear(v[i])], 1u);
+    });
+    merge_counts();
+  };
+  // The whole rest from a list of every token that can be kept: the first k of them, those with
+  // less than `share` before (of the first k's sum, p < 1, where share is 0), the min_p ones.
+  auto finish_in_list = [&](int n, int k, float q, int64_t share) {
+    if (rank != 0) return;
+    const int P = threads_per(n), e = tid / P;  // (n <= kSmall: a round)
+    const bool is = e < n, one = is && (tid & (P - 1)) == 0;
+    const uint64_t x = is ? sh.merged[e] : ~0ull;
+    const int64_t w = is ? sh.merged_w[e] : 0;
+    int64_t sum, total;
+    bool keep = before_in_list(n, P, x, &sum) < (k > 0 ? (int64_t)k : (int64_t)n) && is;
+    if (q < 1.f) {
+      if (share == 0) {
+        block_scan(one && keep ? w : (int64_t)0, sh.warp_mass, &total);
+        share = max((int64_t)ceil((double)fmaxf(q, 0.f) * (double)total), (int64_t)1);
+      }
+      keep = keep && sum < share;
+    }
+    keep = keep && w >= least;
+    int64_t n_kept;
+    block_scan(one && keep ? (int64_t)1 : (int64_t)0, sh.warp_mass, &n_kept);
+    block_scan(one && keep ? w : (int64_t)0, sh.warp_mass, &total);
+    if (one && !keep) sh.merged_w[e] = 0;
+    __syncthreads();
+    const int64_t t = min((int64_t)((double)u * (double)total), total - 1);
+    sum = 0;  // of the kept ones with a lower index
+    for (int j = tid & (P - 1); j < n; j += P)
+      sum += (uint32_t)sh.merged[j] > (uint32_t)x ? sh.merged_w[j] : 0;
+    for (int o = P / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (one && keep && sum <= t && t < sum + w) p.tokens[b] = (int)(0xFFFFFFFFu - (uint32_t)x);
+    if (tid == 0 && p.kept) p.kept[b] = (int)n_kept;
+  };
+
+  bool limited = false, counted = false, done = false;
+  if (top_k > 0 && top_k < p.V) {
+    count(false);
+    counted = true;
+    int64_t before, total;
+    const int bin = find(kBins, count_at, (int64_t)top_k - 1, &before, &total);
+    if (top_k < total) {
+      const int64_t here = count_at(bin);
+      if (before + here <= kSmall) {
+        const int n = gather([&](float v, int) { return linear(v) <= bin; });
+        finish_in_list(n, top_k, top_p, 0);
+        done = true;
+      } else if (here <= kList) {
+        const int n = gather([&](float v, int) { return linear(v) == bin; });
+        cut = cut_in_list(n, false, (int64_t)top_k - 1 - before);
+      } else {
+        cut = refine(false, bin, bin, (int64_t)top_k - 1 - before);
+      }
+      limited = true;
+      counted = false;
+    }
+  }
+  // ---- top_p; saved: the warps' sums of the tokens above the window are there ----
+  bool saved = false;
+  int64_t above = 0;
+  int n_above = 0, b0 = 0, b1 = kBins - 1;
+  if (top_p < 1.f && !done) {
+    if (!counted) count(limited);
+    // bounds of the running sums from the counts (1e-3: roundings of bins and of these sums)
+    constexpr int kEach = kBins / kThreads;
+    constexpr float kWidth = kSpan / (float)(kBins - 1);
+    float lo = 0.f, hi = 0.f, all_lo, all_hi;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int bin = tid * kEach + i;
+      const float n = (float)count_at(bin);
+      hi += n * ex2(-kWidth * (float)bin);
+      lo += bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f;
+    }
+    float up_lo = block_scan(lo, sh.warp_lo, &all_lo), up_hi = block_scan(hi, sh.warp_hi, &all_hi);
+    const float q = fmaxf(top_p, 0.f);
+    const float t_lo = q * all_lo * 0.999f, t_hi = q * all_hi * 1.001f;
+    if (tid < 2) sh.window[tid] = kBins - 1;
+    __syncthreads();
+    // the first bins whose bounds reach the share: the window's ends
+    int at_lo = kBins - 1, at_hi = kBins - 1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int bin = tid * kEach + i;
+      const float n = (float)count_at(bin);
+      up_hi += n * ex2(-kWidth * (float)bin);
+      up_lo += bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f;
+      if (up_hi >= t_lo) at_lo = min(at_lo, bin);
+      if (up_lo >= t_hi) at_hi = min(at_hi, bin);
+    }
+    at_lo = __reduce_min_sync(0xffffffffu, at_lo);
+    at_hi = __reduce_min_sync(0xffffffffu, at_hi);
+    if (lane == 0) {
+      atomicMin(&sh.window[0], at_lo);
+      atomicMin(&sh.window[1], at_hi);
+    }
+    __syncthreads();
+    b0 = sh.window[0];
+    b1 = max(sh.window[1], b0);
+    int64_t n_cand;
+    {
+      int64_t n = 0;
+      for (int i = tid; i <= b1; i += kThreads) n += count_at(i);
+      block_scan(n, sh.warp_mass, &n_cand);
+    }
+    const bool small = n_cand <= kSmall;
+    // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
+    // (linear over b0 .. b1)
+    const float scale = (float)kFine / (float)(b1 - b0 + 1);
+    auto fine = [&](float v) {
+      return min(max((int)(fmaf(m - v, per_bin, -(float)b0) * scale), 0), kFine - 1);
+    };
+    int64_t sum = 0;
+    if (!small) clear(3 * kFine);
+    each([&](const float* v, int a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (limited && place(v[i], a + i) < cut) continue;
+        const int64_t w = weight_of(v[i]);
+        sum += w;
+        if (small || w == 0) continue;
+        const int bin = linear(v[i]);
+        if (bin < b0) {
+          above += w;
+          ++n_above;
+        } else if (bin <= b1) {
+          add_mass(fine(v[i]), (uint64_t)w);
+        }
+      }
+    });
+    const int64_t W = total_of(sum);
+    const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
+    if (small) {
+      const int n = gather([&](float v, int a) {
+        return linear(v) <= b1 && (!limited || place(v, a) >= cut);
+      });
+      finish_in_list(n, 0, top_p, share);
+      done = true;
+    } else {
+      const int64_t target = share - 1 - total_of(above);
+      merge_mass();
+      int64_t before, total;
+      const int bin = find(kFine, mass_at, target, &before, &total);
+      const uint64_t limit = cut;
+      auto in_bin = [&](float v, int a) {
+        const int x = linear(v);
+        return x >= b0 && x <= b1 && fine(v) == bin && place(v, a) >= limit;
+      };
+      const int n = gather(in_bin);
+      int total_n = 0;
+      for (int r = 0; r < C; ++r) total_n += sh.lists[r];
+      cut = total_n <= kList ? cut_in_list(n, true, target - before) : refine(true, b0, b1, target);
+      saved = mp == 0.f;
+    }
+  }
+  if (!done) {
+    // ---- the kept tokens' sums by warps, then the draw in index order ----
+    auto kept_weight = [&](float v, int index) {  // -1: not kept
+      if (place(v, index) < cut || (m - v) * ch > far) return (int64_t)-1;
+      const int64_t w = weight_of(v);
+      return w >= least ? w : (int64_t)-1;
+    };
+    int64_t mass = saved ? above : 0;
+    int n_kept = saved ? n_above : 0;
+    each([&](const float* v, int a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        // (after top_p the tokens above the window are in the sums)
+        if (saved && linear(v[i]) < b0) continue;
+        const int64_t w = kept_weight(v[i], a + i);
+        if (w < 0) continue;
+        mass += w;
+        ++n_kept;
+      }
+    });
     mass = warp_sum(mass);
-    count = warp_sum(count);
-    on_cut = warp_sum(on_cut);
+    n_kept = warp_sum(n_kept);
+    __syncthreads();
     if (lane == 0) {
       sh.warp_mass[warp] = mass;
-      sh.warp_count[warp] = count;
-      sh.warp_ties[warp] = on_cut;
+      sh.warp_count[warp] = n_kept;
     }
     __syncthreads();
     if (warp == 0) {
       mass = warp_sum(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0);
-      count = warp_sum(lane < kWarps ? sh.warp_count[lane] : 0);
-      on_cut = warp_sum(lane < kWarps ? sh.warp_ties[lane] : 0);
+      n_kept = warp_sum(lane < kWarps ? sh.warp_count[lane] : 0);
       if (C == 1) {
         if (lane == 0) {
-          sh.mass[0] = mass;
-          sh.count[0] = count;
-          sh.ties[0] = on_cut;
+          sh.mass[turn][0] = mass;
+          sh.count[0] = n_kept;
         }
       } else if (lane < C) {
-        st_cluster_u64(&sh.mass[rank], (uint32_t)lane, (uint64_t)mass);
-        st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)count);
-        st_cluster_u32(&sh.ties[rank], (uint32_t)lane, (uint32_t)on_cut);
+        st_cluster_u64(&sh.mass[turn][rank], (uint32_t)lane, (uint64_t)mass);
+        st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)n_kept);
       }
     }
-    if (C > 1) cluster_sync();
-    else __syncthreads();
-  }
-  if (warp == 0) {
-    // of parts in index order, lane i holding part i's tokens on the cut: how many are kept,
-    // with `before` of them taken already
-    auto kept_ties = [&](int on_cut, int64_t before) {
-      int64_t up_to = on_cut;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t below = __shfl_up_sync(0xffffffffu, up_to, o);
-        if (lane >= o) up_to += below;
-      }
-      return min(max(ties - before - (up_to - on_cut), (int64_t)0), (int64_t)on_cut);
-    };
-    const int q = lane < C ? sh.ties[lane] : 0;
-    int64_t k = kept_ties(q, 0);
-    int64_t part = lane < C ? sh.mass[lane] + k * tie : 0;
+    sync();
+    const int64_t part = lane < C ? sh.mass[turn][lane] : 0;
     const int64_t W = warp_sum(part);
-    const int64_t n = warp_sum((lane < C ? (int64_t)sh.count[lane] : 0) + k);
     int64_t t = min((int64_t)((double)u * (double)W), W - 1);
     const int owner = locate(part, C, &t);
-    if (rank == 0 && lane == 0 && p.kept) p.kept[b] = (int)n;
-    if (owner == rank) {
-      int64_t before = warp_sum(lane < rank ? (int64_t)q : (int64_t)0);
-      const int qw = lane < kWarps ? sh.warp_ties[lane] : 0;
-      k = kept_ties(qw, before);
-      part = lane < kWarps ? sh.warp_mass[lane] + k * tie : 0;
-      const int w = locate(part, kWarps, &t);
-      before += warp_sum(lane < w ? (int64_t)qw : (int64_t)0);
-      const int y0 = min(n_vec, w * per_w), y1 = min(n_vec, y0 + per_w);
-      for (int j0 = y0; j0 < y1; j0 += 32) {  // a vector per lane
-        const int j = j0 + lane;
+    n_kept = warp_sum(lane < C ? sh.count[lane] : 0);
+    if (rank == 0 && tid == 0 && p.kept) p.kept[b] = n_kept;
+    // the owner's warp that holds the place looks through its vectors, one a lane
+    if (owner == rank && locate(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0, kWarps, &t) == warp) {
+      for (int j0 = w0; j0 < w1; j0 += 32) {
         float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = -INFINITY;
+        if (j0 + lane < w1) Vec<T>::unpack(vector(j0 + lane), v);
+        const int a = (int)row.first(j0 + lane);
         int64_t e[N], sum = 0;
-        int on_cut = 0;
-        if (j < y1) {
-          Vec<T>::unpack(slice[j], v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[i] = -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) on_cut += Key<T>::of(v[i]) == cut_key && ties > 0;
-        k = kept_ties(on_cut, before);
-        int64_t left = k;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const uint32_t key = Key<T>::of(v[i]);
-          e[i] = max(above(v[i], key), (int64_t)0);
-          if (key == cut_key && left > 0) {
-            e[i] = tie;
-            --left;
-          }
+          e[i] = max(kept_weight(v[i], a + i), (int64_t)0);
           sum += e[i];
         }
         const int64_t all = warp_sum(sum);
-        if (t >= all && j0 + 32 < y1) {
+        if (t >= all && j0 + 32 < w1) {
           t -= all;
-          before += warp_sum((int64_t)on_cut);
           continue;
         }
-        const int at = locate(sum, 32, &t);
-        if (lane == at) {
-          int i = 0;
+        if (lane == locate(sum, 32, &t)) {
+          int at = 0;
           bool hit = false;
 #pragma unroll
-          for (int x = 0; x < N; ++x) {
-            if (!hit && t < e[x]) {
+          for (int i = 0; i < N; ++i) {
+            if (!hit && t < e[i]) {
               hit = true;
-              i = x;
+              at = i;
             }
-            if (!hit) t -= e[x];
+            if (!hit) t -= e[i];
           }
-          p.tokens[b] = (int)row.first(c0 + j) + i;
+          p.tokens[b] = a + at;
         }
         break;
       }
@@ -487,13 +732,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   if (C > 1) cluster_sync();  // no CTA leaves while another may still read from it
 }
 
-template <typename T, int kThreads>
-cudaError_t launch(const TokenParams& p, int B, int C, size_t smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(token_sample_kernel<T, kThreads>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T>
+cudaError_t launch(const TokenParams& p, int B, int C, cudaStream_t st) {
+  constexpr int smem = (int)sizeof(Shared);
+  cudaError_t e = cudaFuncSetAttribute(token_sample_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && C > 8)
-    e = cudaFuncSetAttribute(token_sample_kernel<T, kThreads>,
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(token_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)B * (unsigned)C);
@@ -510,20 +755,7 @@ cudaError_t launch(const TokenParams& p, int B, int C, size_t smem, cudaStream_t
   cfg.numAttrs = 2;
   int log2_C = 0;
   while ((1 << log2_C) < C) ++log2_C;
-  return cudaLaunchKernelEx(&cfg, token_sample_kernel<T, kThreads>, p, log2_C);
-}
-
-template <typename T>
-cudaError_t launch(const TokenParams& p, int B, int sm_count, cudaStream_t st) {
-  constexpr int N = Vec<T>::N;
-  // CTAs per row: enough that a slice fits, then more while the GPU is not full and a thread has
-  // several vectors to read
-  auto per = [&](int C) { return ((p.V + N - 1) / N + 1 + C - 1) / C; };  // vectors of a slice
-  int C = 1;
-  while (C < kMaxCluster && per(C) * 16 > kSliceBytes) C *= 2;
-  while (C < kMaxCluster && (int64_t)B * C * 2 <= 2ll * sm_count && per(C) >= 512) C *= 2;
-  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (size_t)per(C) * 16;
-  return launch<T, 512>(p, B, C, smem, st);
+  return cudaLaunchKernelEx(&cfg, token_sample_kernel<T>, p, log2_C);
 }
 
 }  // namespace
@@ -542,8 +774,10 @@ cudaError_t launch_token_sample(const tv_token_args* a, int sm_count, cudaStream
   p.tokens = a->tokens;
   p.kept = a->kept;
   p.status = a->status;
-  return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, a->B, sm_count, st)
-                                 : launch<float>(p, a->B, sm_count, st);
+  // CTAs per row: up to the two per SM that fit at once, 2048 tokens each at least
+  int C = 1;
+  while (C < kMaxCluster && (int64_t)a->B * C * 2 <= 2ll * sm_count && a->vocab >= 4096ll * C) C *= 2;
+  return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, a->B, C, st) : launch<float>(p, a->B, C, st);
 }
 
 }  // namespace tv
