@@ -14,11 +14,12 @@
 //   top_k: the counts say in which bin the k-th token lies;
 //   top_p: a bin's weights lie within a factor 2^(kSpan / kBins), so the counts bound the running
 //      sums to about 1 %, and the cut to a window of bins;
-//   3. (top_p) exact sums: of the row, of the tokens above the window by warp, and of the
-//      window's tokens in kFine finer bins, one of which then holds the cut;
-//   4. the tokens of the cut's bin go into a list, and are compared with one another.
-//   5. the kept tokens' sums by warp (after top_p alone: the window's, added to those of 3), and
-//      the draw within one warp's slice.
+//   3. (top_p) exact sums of the row and, by warp, of the tokens above the window; the warps keep
+//      the window's tokens (where they are too many, the row is read again instead), which are
+//      summed in kFine finer bins, one of which holds the cut;
+//   4. the tokens of the cut's bin go into a list, and are compared with one another;
+//   5. the kept tokens' sums by warp, unless 3 has left them, and the draw within one warp's
+//      slice.
 // Where the bins down to the cut hold few tokens altogether (top_k of common sizes, peaked
 // distributions) all of them go into the list and the rest happens there.  Where the cut's own
 // bin holds too many for the list (equal logits) it is cut by ordered bit patterns, level by
@@ -48,6 +49,8 @@ constexpr int kBins = 4096, kFine = 2048;
 constexpr float kSpan = 48.f;  // log2 units of the linear bins: below, weights are zero
 constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
+constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
+constexpr int kAhead = 3;      // vectors of a lane's that are on their way
 
 struct TokenParams {
   const void* logits;
@@ -63,33 +66,66 @@ struct TokenParams {
 };
 
 struct Shared {
-  float2 exp2_table[kTable * kCopies];
-  uint32_t bins[3 * kFine];       // this CTA's: counts (kBins), or 15-bit parts of weights' sums
-  int64_t all[kFine];             // the cluster's: counts (kBins of 32 bits), or sums
+  PairTable exp2;
+  alignas(16) uint32_t bins[3 * kFine];  // this CTA's: counts (kBins), or 15-bit parts of weights' sums
+  alignas(16) int64_t all[kFine]; // the cluster's: counts (kBins of 32 bits), or sums
+  uint64_t window_of[kWarps][kWindow];  // the warps' tokens of the window
   uint64_t list[kList];           // this CTA's tokens: key, complemented index
   uint64_t merged[kList];         // the cluster's,
   int64_t merged_w[kList];        // and their weights
   int32_t list_n;
   uint64_t keys[kMaxCluster];     // exchanged: the slices' maxima,
   int32_t lists[kMaxCluster];     // lengths of lists,
-  int64_t mass[2][kMaxCluster];   // sums,
+  int64_t mass[4][kMaxCluster];   // sums,
   int32_t count[kMaxCluster];     // and counts
   uint64_t warp_key[kWarps];
-  int64_t warp_mass[kWarps];
+  int64_t warp_mass[kWarps], warp_three[3][kWarps];
   int32_t warp_count[kWarps];
   float warp_lo[kWarps], warp_hi[kWarps];
   int64_t found[2];               // a bin, and the total before it
-  int32_t window[2];
+  int32_t window[2], too_many;
   uint64_t cut;
 };
-static_assert(kBins <= 2 * kFine && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
+static_assert(kBins <= 2 * kFine && kFine / kMaxCluster % 4 == 0 && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(const void* local, uint32_t rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(local), rank)) : "memory");
+__device__ __forceinline__ uint4 ld_cluster_v4(const void* local, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(map_to_rank(smem_u32(local), rank))
+               : "memory");
   return v;
 }
-
+__device__ __forceinline__ void st_cluster_v4(const void* local, uint32_t rank, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_rank(smem_u32(local), rank)),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Four consecutive words of all C CTAs of the cluster (a power of two), added up.
+__device__ __forceinline__ uint4 add_up(const uint32_t* local, int C) {
+  if (C == 1) return *reinterpret_cast<const uint4*>(local);
+  uint4 s = make_uint4(0u, 0u, 0u, 0u);
+  for (int r0 = 0; r0 < C; r0 += 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = r0 + k < C ? ld_cluster_v4(local, (uint32_t)(r0 + k)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s.x += v[k].x;
+      s.y += v[k].y;
+      s.z += v[k].z;
+      s.w += v[k].w;
+    }
+  }
+  return s;
+}
+// To the same place in every CTA of the cluster.
+__device__ __forceinline__ void give(void* local, int C, uint4 v) {
+  if (C == 1) *reinterpret_cast<uint4*>(local) = v;
+  else
+    for (int r = 0; r < C; ++r) st_cluster_v4(local, (uint32_t)r, v);
+}
 __device__ __forceinline__ uint64_t ld_cluster_u64(const void* local, uint32_t rank) {
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_u32(local), rank)) : "memory");
@@ -112,6 +148,20 @@ __device__ __forceinline__ S block_scan(S v, S* warps, S* total) {
   const S mine = lane < kWarps ? warps[lane] : (S)0;
   *total = warp_sum(mine);
   return up_to - v + warp_sum(lane < warp ? mine : (S)0);
+}
+
+// A vector of a row at one of its ends (out of line: the passes are many and code is dear).
+template <typename T>
+__device__ __noinline__ uint4 end_vector(const T* x, int64_t V, int64_t a) {
+  constexpr int N = Vec<T>::N;
+  alignas(16) T v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = a + i >= 0 && a + i < V ? x[a + i] : (T)-INFINITY;
+  return *reinterpret_cast<const uint4*>(v);
+}
+// One exact weight, out of line too.
+__device__ __noinline__ int64_t one_weight(float v, float m, float ch, float cl, const PairTable& table) {
+  return units(weight_pair(v, v, PairScale(m, ch, cl), table).a);
 }
 
 template <typename T>
@@ -155,15 +205,37 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
   const int e0 = row.first_whole(), e1 = row.end_whole();
   auto vector = [&](int j) {
-    if (j >= e0 && j < e1) return row.raw(j);
-    alignas(16) T v[N];  // an end of the row
-    const int64_t a = row.first(j);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = a + i >= 0 && a + i < p.V ? row.x[a + i] : (T)-INFINITY;
-    return *reinterpret_cast<const uint4*>(v);
+    return j >= e0 && j < e1 ? row.raw(j) : end_vector<T>(row.x, p.V, row.first(j));
   };
+  // All lanes call it together, those past the last vector with -inf.
+  // (One copy of fn's code, the next vectors on their way: unrolled, the passes outgrow the
+  // instruction cache.  The first pass, which waits for memory, is a loop of its own.)
   auto each = [&](auto fn) {
-    constexpr int kUnroll = 4;
+    auto fetch = [&](int j) {
+      return j < w1 ? vector(j)
+                    : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+    };
+    uint4 next[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = fetch(w0 + lane + 32 * k);
+#pragma unroll 1
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      float v[N];
+      Vec<T>::unpack(next[0], v);
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) next[k] = next[k + 1];
+      next[kAhead - 1] = fetch(j0 + lane + 32 * kAhead);
+      fn(v, (int)row.first(j0 + lane));
+    }
+  };
+
+  // ---- the row's maximum, with its first index ----
+  uint64_t top;
+  {
+    float best = -INFINITY;
+    int best_at = 0;
+    bool is_nan = false;
+    constexpr int kUnroll = 8;
 #pragma unroll 1
     for (int j0 = w0 + lane; j0 < w1; j0 += 32 * kUnroll) {
       uint4 w[kUnroll];
@@ -175,29 +247,20 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         if (j0 + 32 * k >= w1) break;
         float v[N];
         Vec<T>::unpack(w[k], v);
-        fn(v, (int)row.first(j0 + 32 * k));
-      }
-    }
-  };
-
-  // ---- the row's maximum, with its first index ----
-  uint64_t top;
-  {
-    float best = -INFINITY;
-    int best_at = 0;
-    bool is_nan = false;
-    each([&](const float* v, int a) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        is_nan |= v[i] != v[i];
-        if (v[i] > best) {
-          best = v[i];
-          best_at = a + i;
+        for (int i = 0; i < N; ++i) {
+          is_nan |= v[i] != v[i];
+          if (v[i] > best) {
+            best = v[i];
+            best_at = (int)row.first(j0 + 32 * k) + i;
+          }
         }
       }
-    });
-    for (int i = tid; i < kTable * kCopies; i += kThreads)
-      sh.exp2_table[i] = make_float2(d_exp.hi[i / kCopies], d_exp.lo[i / kCopies]);
+    }
+    for (int i = tid; i < kTable * 32; i += kThreads) {
+      sh.exp2.hi[i] = d_exp.hi[i / 32];
+      sh.exp2.lo[i] = d_exp.lo[i / 32];
+    }
     // order-preserving value bits, then the complemented index; a NaN beats every value
     top = best > -INFINITY
               ? ((uint64_t)ordered(best) << 32) | (0xFFFFFFFFu - (uint32_t)best_at)
@@ -231,13 +294,26 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   }
 
   const float per_bin = ch * ((float)(kBins - 1) / kSpan);
-  auto weight_of = [&](float v) { return units(weight(v, m, ch, cl, sh.exp2_table)); };
+  const PairScale scale2(m, ch, cl);
+  auto weight_of = [&](float v) { return one_weight(v, m, ch, cl, sh.exp2); };
+  // The weights of a vector's values.
+  auto weights_of = [&](const float* v, Weight* w) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const WeightPair two = weight_pair(v[i], v[i + 1], scale2, sh.exp2);
+      w[i] = two.a;
+      w[i + 1] = two.b;
+    }
+  };
   // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
   // a bin is a range of keys).
   auto place = [&](float v, int index) {
     return ((uint64_t)ordered(v) << 32) | (0xFFFFFFFFu - (uint32_t)index);
   };
-  auto linear = [&](float v) { return min((int)((m - v) * per_bin), kBins - 1); };
+  auto position = [&](float v) { return fminf((m - v) * per_bin, 1e30f); };
+  auto linear = [&](float v) { return min((int)position(v), kBins - 1); };
+  // (bins up to `bin` are the positions below this)
+  auto end_of = [&](int bin) { return bin < kBins - 1 ? (float)(bin + 1) : INFINITY; };
   constexpr uint64_t kMasked = (uint64_t)0x007FFFFFu << 32 | 0xFFFFFFFFu;  // -inf, any index
   uint64_t cut = kMasked + 1;  // tokens at or above it are kept
   const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
@@ -257,36 +333,27 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   // The cluster's bins from the CTAs': every CTA adds up its share and gives it to all.
   auto merge_counts = [&]() {
     sync();
-    uint32_t* all = reinterpret_cast<uint32_t*>(sh.all);
     const int share = kBins >> log2_C;
-    for (int i = tid; i < share; i += kThreads) {
+    for (int i = 4 * tid; i < share; i += 4 * kThreads) {
       const int at = rank * share + i;
-      if (C == 1) {
-        all[at] = sh.bins[at];
-        continue;
-      }
-      uint32_t s = 0;
-      for (int r = 0; r < C; ++r) s += ld_cluster_u32(&sh.bins[at], (uint32_t)r);
-      for (int r = 0; r < C; ++r) st_cluster_u32(&all[at], (uint32_t)r, s);
+      give(reinterpret_cast<uint32_t*>(sh.all) + at, C, add_up(&sh.bins[at], C));
     }
     sync();
   };
   auto merge_mass = [&]() {
     sync();
     const int share = kFine >> log2_C;
-    for (int i = tid; i < share; i += kThreads) {
+    for (int i = 4 * tid; i < share; i += 4 * kThreads) {
       const int at = rank * share + i;
-      int64_t s = 0;
-      for (int part = 0; part < 3; ++part) {
-        int64_t x = 0;
-        if (C == 1) x = sh.bins[part * kFine + at];
-        else
-          for (int r = 0; r < C; ++r) x += ld_cluster_u32(&sh.bins[part * kFine + at], (uint32_t)r);
-        s += x << (15 * part);
-      }
-      if (C == 1) sh.all[at] = s;
-      else
-        for (int r = 0; r < C; ++r) st_cluster_u64(&sh.all[at], (uint32_t)r, (uint64_t)s);
+      const uint4 a = add_up(&sh.bins[at], C), b_ = add_up(&sh.bins[kFine + at], C),
+                  c = add_up(&sh.bins[2 * kFine + at], C);
+      auto sum = [](uint32_t x, uint32_t y, uint32_t z) {
+        return (uint64_t)x + ((uint64_t)y << 15) + ((uint64_t)z << 30);
+      };
+      const uint64_t s0 = sum(a.x, b_.x, c.x), s1 = sum(a.y, b_.y, c.y), s2 = sum(a.z, b_.z, c.z),
+                     s3 = sum(a.w, b_.w, c.w);
+      give(&sh.all[at], C, make_uint4((uint32_t)s0, (uint32_t)(s0 >> 32), (uint32_t)s1, (uint32_t)(s1 >> 32)));
+      give(&sh.all[at + 2], C, make_uint4((uint32_t)s2, (uint32_t)(s2 >> 32), (uint32_t)s3, (uint32_t)(s3 >> 32)));
     }
     sync();
   };
@@ -308,35 +375,42 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   };
   auto count_at = [&](int i) { return (int64_t) reinterpret_cast<const uint32_t*>(sh.all)[i]; };
   auto mass_at = [&](int i) { return sh.all[i]; };
-  // The sum of one value a thread over the cluster.
-  int turn = 0;
-  auto total_of = [&](int64_t v) {
-    v = warp_sum(v);
+  // The sums of three values a thread over the cluster.
+  auto totals_of = [&](int64_t& x, int64_t& y, int64_t& z) {
+    int64_t v[3] = {x, y, z};
     __syncthreads();
-    if (lane == 0) sh.warp_mass[warp] = v;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      v[i] = warp_sum(v[i]);
+      if (lane == 0) sh.warp_three[i][warp] = v[i];
+    }
     __syncthreads();
-    v = warp_sum(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0);
-    if (C == 1) return v;
-    if (warp == 0 && lane < C) st_cluster_u64(&sh.mass[turn][rank], (uint32_t)lane, (uint64_t)v);
-    sync();
-    v = warp_sum(lane < C ? sh.mass[turn][lane] : (int64_t)0);
-    turn ^= 1;
-    return v;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      v[i] = warp_sum(lane < kWarps ? sh.warp_three[i][lane] : (int64_t)0);
+      if (C > 1 && warp == i && lane < C) st_cluster_u64(&sh.mass[i][rank], (uint32_t)lane, (uint64_t)v[i]);
+    }
+    if (C > 1) {
+      sync();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) v[i] = warp_sum(lane < C ? sh.mass[i][lane] : (int64_t)0);
+    }
+    x = v[0];
+    y = v[1];
+    z = v[2];
   };
-  // The cluster's list of the tokens that `take` says (kList at most), in any order, in sh.merged
-  // with their weights.  Returns its length.
-  auto gather = [&](auto take) {
+  // Lists: tokens are put on the CTA's (kList at most are kept, all are counted), which are then
+  // joined in sh.merged with their weights, in any order.  join_lists returns how many there are.
+  auto start_list = [&]() {
     __syncthreads();
     if (tid == 0) sh.list_n = 0;
     __syncthreads();
-    each([&](const float* v, int a) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (!(v[i] > -INFINITY) || !take(v[i], a + i)) continue;
-        const int at = atomicAdd(&sh.list_n, 1);
-        if (at < kList) sh.list[at] = place(v[i], a + i);
-      }
-    });
+  };
+  auto put_on_list = [&](float v, int index) {
+    const int at = atomicAdd(&sh.list_n, 1);
+    if (at < kList) sh.list[at] = place(v, index);
+  };
+  auto join_lists = [&]() {
     __syncthreads();
     if (C == 1) {
       if (tid == 0) sh.lists[0] = sh.list_n;
@@ -344,18 +418,33 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       st_cluster_u32(&sh.lists[rank], (uint32_t)lane, (uint32_t)sh.list_n);
     }
     sync();
-    int n = 0;
-    for (int r = 0; r < C; ++r) {
-      const int k = min(sh.lists[r], kList - n);
-      for (int i = tid; i < k; i += kThreads) {
-        const uint64_t x = C == 1 ? sh.list[i] : ld_cluster_u64(&sh.list[i], (uint32_t)r);
-        sh.merged[n + i] = x;
-        sh.merged_w[n + i] = weight_of(unordered((uint32_t)(x >> 32)));
+    const int n = warp_sum(lane < C ? sh.lists[lane] : 0);
+    if (n <= kList) {
+      int at = 0;
+      for (int r = 0; r < C; ++r) {
+        const int k = sh.lists[r];
+        for (int i = tid; i < k; i += kThreads) {
+          const uint64_t x = C == 1 ? sh.list[i] : ld_cluster_u64(&sh.list[i], (uint32_t)r);
+          sh.merged[at + i] = x;
+          sh.merged_w[at + i] = weight_of(unordered((uint32_t)(x >> 32)));
+        }
+        at += k;
       }
-      n += k;
+      __syncthreads();
     }
-    __syncthreads();
     return n;
+  };
+  // The list of the tokens at positions from lo up to hi (and not before the cut).
+  auto gather = [&](float lo, float hi) {
+    start_list();
+    each([&](const float* v, int a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float y = position(v[i]);
+        if (y >= lo && y < hi && place(v[i], a + i) >= cut) put_on_list(v[i], a + i);
+      }
+    });
+    return join_lists();
   };
   // Tokens of the list, P threads each: fn(token, its part), with P a power of two within a warp.
   auto threads_per = [&](int n) {
@@ -534,11 +623,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     if (top_k < total) {
       const int64_t here = count_at(bin);
       if (before + here <= kSmall) {
-        const int n = gather([&](float v, int) { return linear(v) <= bin; });
+        const int n = gather(0.f, end_of(bin));
         finish_in_list(n, top_k, top_p, 0);
         done = true;
       } else if (here <= kList) {
-        const int n = gather([&](float v, int) { return linear(v) == bin; });
+        const int n = gather((float)bin, end_of(bin));
         cut = cut_in_list(n, false, (int64_t)top_k - 1 - before);
       } else {
         cut = refine(false, bin, bin, (int64_t)top_k - 1 - before);
@@ -598,51 +687,98 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     const bool small = n_cand <= kSmall;
     // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
     // (linear over b0 .. b1)
+    const float from = (float)b0, to = end_of(b1);
     const float scale = (float)kFine / (float)(b1 - b0 + 1);
-    auto fine = [&](float v) {
-      return min(max((int)(fmaf(m - v, per_bin, -(float)b0) * scale), 0), kFine - 1);
-    };
+    auto fine = [&](float y) { return min((int)((y - from) * scale), kFine - 1); };
+    if (tid == 0) sh.too_many = 0;
+    __syncthreads();
     int64_t sum = 0;
-    if (!small) clear(3 * kFine);
+    int n_window = 0;  // the warp's tokens of the window
     each([&](const float* v, int a) {
+      // (a vector's parts of weights are added as ints: eight of 2^22)
+      Weight w[N];
+      weights_of(v, w);
+      int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (limited && place(v[i], a + i) < cut) continue;
-        const int64_t w = weight_of(v[i]);
-        sum += w;
-        if (small || w == 0) continue;
-        const int bin = linear(v[i]);
-        if (bin < b0) {
-          above += w;
+        const bool is = !limited || place(v[i], a + i) >= cut;
+        all_h += is ? w[i].high : 0;
+        all_l += is ? w[i].low : 0;
+        const float y = position(v[i]);
+        if (is && y < from) {
+          up_h += w[i].high;
+          up_l += w[i].low;
           ++n_above;
-        } else if (bin <= b1) {
-          add_mass(fine(v[i]), (uint64_t)w);
         }
+        const bool in = is && y >= from && y < to && v[i] > -INFINITY;
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        if (who == 0) continue;
+        const int at = n_window + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kWindow) sh.window_of[warp][at] = place(v[i], a + i);
+        n_window += __popc(who);
       }
+      sum += units({all_h, all_l});
+      above += units({up_h, up_l});
     });
-    const int64_t W = total_of(sum);
+    if (n_window > kWindow && lane == 0) sh.too_many = 1;
+    __syncwarp();
+    int64_t W = sum, all_above = above, too_many = 0;
+    __syncthreads();
+    if (tid == 0) too_many = sh.too_many;
+    totals_of(W, all_above, too_many);
     const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
     if (small) {
-      const int n = gather([&](float v, int a) {
-        return linear(v) <= b1 && (!limited || place(v, a) >= cut);
-      });
+      const int n = gather(0.f, to);
       finish_in_list(n, 0, top_p, share);
       done = true;
     } else {
-      const int64_t target = share - 1 - total_of(above);
+      // the window's tokens: what the warps have kept, or the row once more
+      auto each_in_window = [&](auto fn) {
+        if (too_many == 0) {
+#pragma unroll 1
+          for (int i = lane; i < n_window; i += 32) {
+            const uint64_t x = sh.window_of[warp][i];
+            fn(unordered((uint32_t)(x >> 32)), (int)(0xFFFFFFFFu - (uint32_t)x));
+          }
+          return;
+        }
+        each([&](const float* v, int a) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float y = position(v[i]);
+            if (y >= from && y < to && place(v[i], a + i) >= cut) fn(v[i], a + i);
+          }
+        });
+      };
+      const int64_t target = share - 1 - all_above;
+      clear(3 * kFine);
+      each_in_window([&](float v, int) {
+        const int64_t w = weight_of(v);
+        if (w > 0) add_mass(fine(position(v)), (uint64_t)w);
+      });
       merge_mass();
       int64_t before, total;
       const int bin = find(kFine, mass_at, target, &before, &total);
-      const uint64_t limit = cut;
-      auto in_bin = [&](float v, int a) {
-        const int x = linear(v);
-        return x >= b0 && x <= b1 && fine(v) == bin && place(v, a) >= limit;
-      };
-      const int n = gather(in_bin);
-      int total_n = 0;
-      for (int r = 0; r < C; ++r) total_n += sh.lists[r];
-      cut = total_n <= kList ? cut_in_list(n, true, target - before) : refine(true, b0, b1, target);
-      saved = mp == 0.f;
+      // those before the cut's bin are kept, those in it go on a list
+      int64_t more = 0;
+      int n_more = 0;
+      start_list();
+      each_in_window([&](float v, int index) {
+        const int f = fine(position(v));
+        if (f == bin) put_on_list(v, index);
+        if (f >= bin) return;
+        more += weight_of(v);
+        ++n_more;
+      });
+      const int n = join_lists();
+      if (n <= kList) {
+        cut = cut_in_list(n, true, target - before);
+        saved = mp == 0.f;
+        above += more;
+        n_above += n_more;
+      } else {
+        cut = refine(true, b0, b1, target);
+      }
     }
   }
   if (!done) {
@@ -654,17 +790,40 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     };
     int64_t mass = saved ? above : 0;
     int n_kept = saved ? n_above : 0;
-    each([&](const float* v, int a) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        // (after top_p the tokens above the window are in the sums)
-        if (saved && linear(v[i]) < b0) continue;
-        const int64_t w = kept_weight(v[i], a + i);
-        if (w < 0) continue;
-        mass += w;
+    const bool whole = cut == kMasked + 1 && mp == 0.f;  // no filter
+    if (saved) {
+      // (after top_p all but the kept tokens of this CTA's list are in the sums)
+      for (int i = lane; i < sh.list_n; i += 32) {
+        const uint64_t x = sh.list[i];
+        const int j = (int)((0xFFFFFFFFu - (uint32_t)x + row.off) / N);
+        if (x < cut || j < w0 || j >= w1) continue;
+        mass += weight_of(unordered((uint32_t)(x >> 32)));
         ++n_kept;
       }
-    });
+    } else {
+      each([&](const float* v, int a) {
+        if (whole) {
+          Weight w[N];
+          weights_of(v, w);
+          int h = 0, l = 0;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            h += w[i].high;
+            l += w[i].low;
+            n_kept += v[i] > -INFINITY;
+          }
+          mass += units({h, l});
+          return;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int64_t w = kept_weight(v[i], a + i);
+          if (w < 0) continue;
+          mass += w;
+          ++n_kept;
+        }
+      });
+    }
     mass = warp_sum(mass);
     n_kept = warp_sum(n_kept);
     __syncthreads();
@@ -678,54 +837,53 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       n_kept = warp_sum(lane < kWarps ? sh.warp_count[lane] : 0);
       if (C == 1) {
         if (lane == 0) {
-          sh.mass[turn][0] = mass;
+          sh.mass[3][0] = mass;
           sh.count[0] = n_kept;
         }
       } else if (lane < C) {
-        st_cluster_u64(&sh.mass[turn][rank], (uint32_t)lane, (uint64_t)mass);
+        st_cluster_u64(&sh.mass[3][rank], (uint32_t)lane, (uint64_t)mass);
         st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)n_kept);
       }
     }
     sync();
-    const int64_t part = lane < C ? sh.mass[turn][lane] : 0;
+    const int64_t part = lane < C ? sh.mass[3][lane] : 0;
     const int64_t W = warp_sum(part);
     int64_t t = min((int64_t)((double)u * (double)W), W - 1);
     const int owner = locate(part, C, &t);
     n_kept = warp_sum(lane < C ? sh.count[lane] : 0);
     if (rank == 0 && tid == 0 && p.kept) p.kept[b] = n_kept;
-    // the owner's warp that holds the place looks through its vectors, one a lane
-    if (owner == rank && locate(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0, kWarps, &t) == warp) {
-      for (int j0 = w0; j0 < w1; j0 += 32) {
-        float v[N];
+    // the owner's threads look through the slice of the warp that holds the place, a vector each
+    if (owner == rank) {
+      const int at_w = locate(lane < kWarps ? sh.warp_mass[lane] : (int64_t)0, kWarps, &t);
+      const int y0 = min(c1, c0 + at_w * per_w), y1 = min(c1, y0 + per_w);
+      for (int j0 = y0; j0 < y1; j0 += kThreads) {
+        const int j = j0 + tid, a = (int)row.first(j);
+        int64_t e[N], sum = 0, all;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = -INFINITY;
-        if (j0 + lane < w1) Vec<T>::unpack(vector(j0 + lane), v);
-        const int a = (int)row.first(j0 + lane);
-        int64_t e[N], sum = 0;
+        for (int i = 0; i < N; ++i) e[i] = 0;
+        if (j < y1) {
+          float v[N];
+          Vec<T>::unpack(vector(j), v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          e[i] = max(kept_weight(v[i], a + i), (int64_t)0);
-          sum += e[i];
+          for (int i = 0; i < N; ++i) e[i] = max(kept_weight(v[i], a + i), (int64_t)0);
         }
-        const int64_t all = warp_sum(sum);
-        if (t >= all && j0 + 32 < w1) {
-          t -= all;
-          continue;
-        }
-        if (lane == locate(sum, 32, &t)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += e[i];
+        int64_t here = t - block_scan(sum, sh.warp_mass, &all);
+        t -= all;
+        if (here >= 0 && here < sum) {
           int at = 0;
           bool hit = false;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            if (!hit && t < e[i]) {
+            if (!hit && here < e[i]) {
               hit = true;
               at = i;
             }
-            if (!hit) t -= e[i];
+            if (!hit) here -= e[i];
           }
           p.tokens[b] = a + at;
         }
-        break;
       }
     }
   }
