@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sample_math.h"
 #include "sm100_ptx.h"
@@ -50,7 +51,7 @@ constexpr float kSpan = 48.f;  // log2 units of the linear bins: below, weights 
 constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
 constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
-constexpr int kAhead = 3;      // vectors of a lane's that are on their way
+constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
 struct TokenParams {
   const void* logits;
@@ -83,10 +84,10 @@ struct Shared {
   int32_t warp_count[kWarps];
   float warp_lo[kWarps], warp_hi[kWarps];
   int64_t found[2];               // a bin, and the total before it
-  int32_t window[2], too_many;
+  int32_t window[4], too_many;
   uint64_t cut;
 };
-static_assert(kBins <= 2 * kFine && kFine / kMaxCluster % 4 == 0 && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
+static_assert(kBins <= 2 * kFine && kFine / 4 >= kThreads && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
 
 __device__ __forceinline__ uint4 ld_cluster_v4(const void* local, uint32_t rank) {
   uint4 v;
@@ -101,30 +102,23 @@ __device__ __forceinline__ void st_cluster_v4(const void* local, uint32_t rank, 
                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
-// Four consecutive words of all C CTAs of the cluster (a power of two), added up.
-__device__ __forceinline__ uint4 add_up(const uint32_t* local, int C) {
-  if (C == 1) return *reinterpret_cast<const uint4*>(local);
-  uint4 s = make_uint4(0u, 0u, 0u, 0u);
-  for (int r0 = 0; r0 < C; r0 += 4) {
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = r0 + k < C ? ld_cluster_v4(local, (uint32_t)(r0 + k)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s.x += v[k].x;
-      s.y += v[k].y;
-      s.z += v[k].z;
-      s.w += v[k].w;
-    }
+// Four words of the C CTAs of the cluster (a power of two), lane r of a group of C holding CTA r's,
+// added up: the sum in every lane.
+__device__ __forceinline__ uint4 add_up(uint4 v, int C) {
+  for (int o = C / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
   }
-  return s;
+  return v;
 }
-// To the same place in every CTA of the cluster.
-__device__ __forceinline__ void give(void* local, int C, uint4 v) {
+__device__ __forceinline__ uint4 get(const uint32_t* local, int C, int r) {
+  return C == 1 ? *reinterpret_cast<const uint4*>(local) : ld_cluster_v4(local, (uint32_t)r);
+}
+__device__ __forceinline__ void give(void* local, int C, int r, uint4 v) {
   if (C == 1) *reinterpret_cast<uint4*>(local) = v;
-  else
-    for (int r = 0; r < C; ++r) st_cluster_v4(local, (uint32_t)r, v);
+  else st_cluster_v4(local, (uint32_t)r, v);
 }
 __device__ __forceinline__ uint64_t ld_cluster_u64(const void* local, uint32_t rank) {
   uint64_t v;
@@ -203,31 +197,50 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   const int per = (row.n_vec + C - 1) >> log2_C, per_w = (per + kWarps - 1) / kWarps;
   const int c0 = min(row.n_vec, rank * per), c1 = min(row.n_vec, c0 + per);
   const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
-  const int e0 = row.first_whole(), e1 = row.end_whole();
+  const int e0 = row.first_whole();
+  const uint32_t n_whole = (uint32_t)max(row.end_whole() - e0, 0);
+  const uint4* vectors = reinterpret_cast<const uint4*>(row.x - row.off);  // (read where they are whole)
   auto vector = [&](int j) {
-    return j >= e0 && j < e1 ? row.raw(j) : end_vector<T>(row.x, p.V, row.first(j));
+    return (uint32_t)(j - e0) < n_whole ? __ldg(vectors + j) : end_vector<T>(row.x, p.V, row.first(j));
   };
-  // All lanes call it together, those past the last vector with -inf.
-  // (One copy of fn's code, the next vectors on their way: unrolled, the passes outgrow the
-  // instruction cache.  The first pass, which waits for memory, is a loop of its own.)
-  auto each = [&](auto fn) {
-    auto fetch = [&](int j) {
-      return j < w1 ? vector(j)
-                    : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
-    };
-    uint4 next[kAhead];
+  auto fetch = [&](int j) {
+    return j < w1 ? vector(j)
+                  : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
+  };
+  // All lanes call it together, those past the last vector with -inf.  `dear`: one copy of fn's
+  // code, the next vectors on their way (unrolled, such passes outgrow the instruction cache).
+  auto each = [&](auto dear, auto fn) {
+    if constexpr (decltype(dear)::value) {
+      uint4 next[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) next[k] = fetch(w0 + lane + 32 * k);
+      for (int k = 0; k < kAhead; ++k) next[k] = fetch(w0 + lane + 32 * k);
 #pragma unroll 1
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-      float v[N];
-      Vec<T>::unpack(next[0], v);
+      for (int j0 = w0; j0 < w1; j0 += 32) {
+        float v[N];
+        Vec<T>::unpack(next[0], v);
 #pragma unroll
-      for (int k = 0; k + 1 < kAhead; ++k) next[k] = next[k + 1];
-      next[kAhead - 1] = fetch(j0 + lane + 32 * kAhead);
-      fn(v, (int)row.first(j0 + lane));
+        for (int k = 0; k + 1 < kAhead; ++k) next[k] = next[k + 1];
+        next[kAhead - 1] = fetch(j0 + lane + 32 * kAhead);
+        fn(v, (j0 + lane) * N - row.off);
+      }
+    } else {
+      constexpr int kUnroll = 4;
+#pragma unroll 1
+      for (int j0 = w0; j0 < w1; j0 += 32 * kUnroll) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) w[k] = fetch(j0 + lane + 32 * k);
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+          float v[N];
+          Vec<T>::unpack(w[k], v);
+          fn(v, (j0 + lane + 32 * k) * N - row.off);
+        }
+      }
     }
   };
+  constexpr std::true_type kDear{};
+  constexpr std::false_type kLight{};
 
   // ---- the row's maximum, with its first index ----
   uint64_t top;
@@ -310,10 +323,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   auto place = [&](float v, int index) {
     return ((uint64_t)ordered(v) << 32) | (0xFFFFFFFFu - (uint32_t)index);
   };
-  auto position = [&](float v) { return fminf((m - v) * per_bin, 1e30f); };
+  auto position = [&](float v) { return (m - v) * per_bin; };
   auto linear = [&](float v) { return min((int)position(v), kBins - 1); };
-  // (bins up to `bin` are the positions below this)
-  auto end_of = [&](int bin) { return bin < kBins - 1 ? (float)(bin + 1) : INFINITY; };
+  // Bins b0 .. b1 are the positions y >= b0 that are not at or past the end of b1 (NaN: none is).
+  auto end_of = [&](int bin) { return bin < kBins - 1 ? (float)(bin + 1) : NAN; };
   constexpr uint64_t kMasked = (uint64_t)0x007FFFFFu << 32 | 0xFFFFFFFFu;  // -inf, any index
   uint64_t cut = kMasked + 1;  // tokens at or above it are kept
   const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
@@ -330,30 +343,38 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     atomicAdd(&sh.bins[kFine + bin], (uint32_t)(w >> 15) & 0x7FFFu);
     atomicAdd(&sh.bins[2 * kFine + bin], (uint32_t)(w >> 30));
   };
-  // The cluster's bins from the CTAs': every CTA adds up its share and gives it to all.
+  // The cluster's bins from the CTAs': every CTA adds up its share and gives it to all, a thread
+  // for four bins and one CTA to read from and to give to (whole warps: kFine / 4 is at least a
+  // block's threads).
+  const int give_to = tid & (C - 1), first_bin = 4 * (tid >> log2_C), step = 4 * (kThreads >> log2_C);
   auto merge_counts = [&]() {
     sync();
     const int share = kBins >> log2_C;
-    for (int i = 4 * tid; i < share; i += 4 * kThreads) {
+    for (int i = first_bin; i < share; i += step) {
       const int at = rank * share + i;
-      give(reinterpret_cast<uint32_t*>(sh.all) + at, C, add_up(&sh.bins[at], C));
+      give(reinterpret_cast<uint32_t*>(sh.all) + at, C, give_to, add_up(get(&sh.bins[at], C, give_to), C));
     }
     sync();
   };
   auto merge_mass = [&]() {
     sync();
     const int share = kFine >> log2_C;
-    for (int i = 4 * tid; i < share; i += 4 * kThreads) {
+    for (int i = first_bin; i < share; i += step) {
       const int at = rank * share + i;
-      const uint4 a = add_up(&sh.bins[at], C), b_ = add_up(&sh.bins[kFine + at], C),
-                  c = add_up(&sh.bins[2 * kFine + at], C);
-      auto sum = [](uint32_t x, uint32_t y, uint32_t z) {
-        return (uint64_t)x + ((uint64_t)y << 15) + ((uint64_t)z << 30);
+      uint4 x = get(&sh.bins[at], C, give_to), y = get(&sh.bins[kFine + at], C, give_to),
+            z = get(&sh.bins[2 * kFine + at], C, give_to);
+      x = add_up(x, C);
+      y = add_up(y, C);
+      z = add_up(z, C);
+      auto sum = [](uint32_t a, uint32_t b_, uint32_t c) {
+        return (uint64_t)a + ((uint64_t)b_ << 15) + ((uint64_t)c << 30);
       };
-      const uint64_t s0 = sum(a.x, b_.x, c.x), s1 = sum(a.y, b_.y, c.y), s2 = sum(a.z, b_.z, c.z),
-                     s3 = sum(a.w, b_.w, c.w);
-      give(&sh.all[at], C, make_uint4((uint32_t)s0, (uint32_t)(s0 >> 32), (uint32_t)s1, (uint32_t)(s1 >> 32)));
-      give(&sh.all[at + 2], C, make_uint4((uint32_t)s2, (uint32_t)(s2 >> 32), (uint32_t)s3, (uint32_t)(s3 >> 32)));
+      const uint64_t s0 = sum(x.x, y.x, z.x), s1 = sum(x.y, y.y, z.y), s2 = sum(x.z, y.z, z.z),
+                     s3 = sum(x.w, y.w, z.w);
+      give(&sh.all[at], C, give_to,
+           make_uint4((uint32_t)s0, (uint32_t)(s0 >> 32), (uint32_t)s1, (uint32_t)(s1 >> 32)));
+      give(&sh.all[at + 2], C, give_to,
+           make_uint4((uint32_t)s2, (uint32_t)(s2 >> 32), (uint32_t)s3, (uint32_t)(s3 >> 32)));
     }
     sync();
   };
@@ -437,11 +458,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   // The list of the tokens at positions from lo up to hi (and not before the cut).
   auto gather = [&](float lo, float hi) {
     start_list();
-    each([&](const float* v, int a) {
+    each(kLight, [&](const float* v, int a) {
+      bool any = false;  // (few vectors have one)
+#pragma unroll
+      for (int i = 0; i < N; ++i) any |= position(v[i]) >= lo && !(position(v[i]) >= hi);
+      if (!any) return;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float y = position(v[i]);
-        if (y >= lo && y < hi && place(v[i], a + i) >= cut) put_on_list(v[i], a + i);
+        if (y >= lo && !(y >= hi) && place(v[i], a + i) >= cut) put_on_list(v[i], a + i);
       }
     });
     return join_lists();
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       int shift = 0;
       while (((hi - lo) >> shift) >= (uint32_t)kFine) ++shift;
       clear(3 * kFine);
-      each([&](const float* v, int a) {
+      each(kDear, [&](const float* v, int a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const uint32_t key = ordered(v[i]);
@@ -525,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     // the tokens at this key before the last kept one; then its index
     int64_t n = mass ? target / weight_of(unordered(hi)) : target;
     int64_t mine = 0;
-    each([&](const float* v, int a) {
+    each(kDear, [&](const float* v, int a) {
 #pragma unroll
       for (int i = 0; i < N; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
     });
@@ -572,13 +597,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     sync();
     return sh.cut;
   };
-  // Counts of the kept tokens in the linear bins.
-  auto count = [&](bool limited) {
+  // Counts of the kept tokens in the linear bins, those at positions below hi.
+  auto count = [&](bool limited, float hi) {
     clear(kBins);
-    each([&](const float* v, int a) {
+    each(kLight, [&](const float* v, int a) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (v[i] > -INFINITY && (!limited || place(v[i], a + i) >= cut)) atomicAdd(&sh.bins[linear(v[i])], 1u);
+        if (v[i] > -INFINITY && !(position(v[i]) >= hi) && (!limited || place(v[i], a + i) >= cut))
+          atomicAdd(&sh.bins[linear(v[i])], 1u);
     });
     merge_counts();
   };
@@ -616,11 +642,16 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
 
   bool limited = false, counted = false, done = false;
   if (top_k > 0 && top_k < p.V) {
-    count(false);
-    counted = true;
+    // (mostly a third of the span holds k tokens, and most of the others need no count)
     int64_t before, total;
-    const int bin = find(kBins, count_at, (int64_t)top_k - 1, &before, &total);
-    if (top_k < total) {
+    count(false, (float)(kBins / 3));
+    int bin = find(kBins, count_at, (int64_t)top_k - 1, &before, &total);
+    if (total < top_k) {
+      count(false, NAN);
+      bin = find(kBins, count_at, (int64_t)top_k - 1, &before, &total);
+      counted = true;
+    }
+    if (top_k <= total) {
       const int64_t here = count_at(bin);
       if (before + here <= kSmall) {
         const int n = gather(0.f, end_of(bin));
@@ -641,50 +672,66 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   int64_t above = 0;
   int n_above = 0, b0 = 0, b1 = kBins - 1;
   if (top_p < 1.f && !done) {
-    if (!counted) count(limited);
-    // bounds of the running sums from the counts (1e-3: roundings of bins and of these sums)
+    if (!counted) count(limited, NAN);
+    // The cut's window from the counts: bounds of the running sums (their weights lie within a
+    // bin's; 1e-3: roundings of bins and of these sums), and an estimate from the bins' middles.
+    // Of a float row's many tokens in a bin the errors cancel, a bf16 row's in one bin are equal:
+    // nine times the estimate's deviation (0.0024 of a bin's, evenly spread) are a window some
+    // twenty times narrower than the bounds.  A cut outside it is seen, and the bounds taken.
     constexpr int kEach = kBins / kThreads;
     constexpr float kWidth = kSpan / (float)(kBins - 1);
-    float lo = 0.f, hi = 0.f, all_lo, all_hi;
+    auto low_mass = [&](int bin, float n) { return bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f; };
+    auto high_mass = [&](int bin, float n) { return n * ex2(-kWidth * (float)bin); };
+    auto mid_mass = [&](int bin, float n) { return n * ex2(-kWidth * ((float)bin + 0.5f)); };
+    float lo = 0.f, hi = 0.f, mid = 0.f, var = 0.f, all_lo, all_hi, all_mid, all_var;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int bin = tid * kEach + i;
-      const float n = (float)count_at(bin);
-      hi += n * ex2(-kWidth * (float)bin);
-      lo += bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f;
+      const float n = (float)count_at(bin), w = mid_mass(bin, n);
+      hi += high_mass(bin, n);
+      lo += low_mass(bin, n);
+      mid += w;
+      var += sizeof(T) == 2 ? w * w : w * w / fmaxf(n, 1.f);
     }
     float up_lo = block_scan(lo, sh.warp_lo, &all_lo), up_hi = block_scan(hi, sh.warp_hi, &all_hi);
+    float up_mid = block_scan(mid, sh.warp_lo, &all_mid);
+    block_scan(var, sh.warp_hi, &all_var);
     const float q = fmaxf(top_p, 0.f);
-    const float t_lo = q * all_lo * 0.999f, t_hi = q * all_hi * 1.001f;
-    if (tid < 2) sh.window[tid] = kBins - 1;
+    const float margin = 9.f * 0.0024f * sqrtf(all_var) + 1e-5f * all_mid;
+    // the first bins at which a running sum reaches a place: the bounds' ends, the estimate's
+    const float t[4] = {q * all_lo * 0.999f, q * all_hi * 1.001f, q * all_mid - margin, q * all_mid + margin};
+    if (tid < 4) sh.window[tid] = kBins - 1;
     __syncthreads();
-    // the first bins whose bounds reach the share: the window's ends
-    int at_lo = kBins - 1, at_hi = kBins - 1;
+    int at[4] = {kBins - 1, kBins - 1, kBins - 1, kBins - 1};
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int bin = tid * kEach + i;
       const float n = (float)count_at(bin);
-      up_hi += n * ex2(-kWidth * (float)bin);
-      up_lo += bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f;
-      if (up_hi >= t_lo) at_lo = min(at_lo, bin);
-      if (up_lo >= t_hi) at_hi = min(at_hi, bin);
+      up_hi += high_mass(bin, n);
+      up_lo += low_mass(bin, n);
+      up_mid += mid_mass(bin, n);
+      if (up_hi >= t[0]) at[0] = min(at[0], bin);
+      if (up_lo >= t[1]) at[1] = min(at[1], bin);
+      if (up_mid >= t[2]) at[2] = min(at[2], bin);
+      if (up_mid >= t[3]) at[3] = min(at[3], bin);
     }
-    at_lo = __reduce_min_sync(0xffffffffu, at_lo);
-    at_hi = __reduce_min_sync(0xffffffffu, at_hi);
-    if (lane == 0) {
-      atomicMin(&sh.window[0], at_lo);
-      atomicMin(&sh.window[1], at_hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at[i] = __reduce_min_sync(0xffffffffu, at[i]);
+      if (lane == 0) atomicMin(&sh.window[i], at[i]);
     }
     __syncthreads();
-    b0 = sh.window[0];
-    b1 = max(sh.window[1], b0);
+    const int bound0 = sh.window[0], bound1 = max(sh.window[1], bound0);
     int64_t n_cand;
     {
       int64_t n = 0;
-      for (int i = tid; i <= b1; i += kThreads) n += count_at(i);
+      for (int i = tid; i <= bound1; i += kThreads) n += count_at(i);
       block_scan(n, sh.warp_mass, &n_cand);
     }
     const bool small = n_cand <= kSmall;
+    b0 = small ? bound0 : min(max(sh.window[2], bound0), bound1);
+    b1 = small ? bound1 : min(max(sh.window[3], b0), bound1);
+    for (;;) {
     // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
     // (linear over b0 .. b1)
     const float from = (float)b0, to = end_of(b1);
@@ -693,12 +740,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     if (tid == 0) sh.too_many = 0;
     __syncthreads();
     int64_t sum = 0;
+    above = 0;
+    n_above = 0;
     int n_window = 0;  // the warp's tokens of the window
-    each([&](const float* v, int a) {
+    each(kDear, [&](const float* v, int a) {
       // (a vector's parts of weights are added as ints: eight of 2^22)
       Weight w[N];
       weights_of(v, w);
       int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
+      bool any = false;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const bool is = !limited || place(v[i], a + i) >= cut;
@@ -710,18 +760,22 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           up_l += w[i].low;
           ++n_above;
         }
-        const bool in = is && y >= from && y < to && v[i] > -INFINITY;
-        const uint32_t who = __ballot_sync(0xffffffffu, in);
-        if (who == 0) continue;
-        const int at = n_window + __popc(who & ((1u << lane) - 1u));
-        if (in && at < kWindow) sh.window_of[warp][at] = place(v[i], a + i);
-        n_window += __popc(who);
+        any |= y >= from && !(y >= to);
       }
       sum += units({all_h, all_l});
       above += units({up_h, up_l});
+      if (!__any_sync(0xffffffffu, any)) return;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float y = position(v[i]);
+        const bool in = y >= from && !(y >= to) && place(v[i], a + i) >= cut;
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
+        if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
+        n_window += __popc(who);
+      }
     });
     if (n_window > kWindow && lane == 0) sh.too_many = 1;
-    __syncwarp();
     int64_t W = sum, all_above = above, too_many = 0;
     __syncthreads();
     if (tid == 0) too_many = sh.too_many;
@@ -742,11 +796,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           }
           return;
         }
-        each([&](const float* v, int a) {
+        each(kDear, [&](const float* v, int a) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const float y = position(v[i]);
-            if (y >= from && y < to && place(v[i], a + i) >= cut) fn(v[i], a + i);
+            if (y >= from && !(y >= to) && place(v[i], a + i) >= cut) fn(v[i], a + i);
           }
         });
       };
@@ -759,6 +813,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       merge_mass();
       int64_t before, total;
       const int bin = find(kFine, mass_at, target, &before, &total);
+      if ((target < 0 || target >= total) && (b0 != bound0 || b1 != bound1)) {
+        b0 = bound0;
+        b1 = bound1;
+        continue;
+      }
       // those before the cut's bin are kept, those in it go on a list
       int64_t more = 0;
       int n_more = 0;
@@ -780,6 +839,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         cut = refine(true, b0, b1, target);
       }
     }
+    break;
+    }
   }
   if (!done) {
     // ---- the kept tokens' sums by warps, then the draw in index order ----
@@ -790,7 +851,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     };
     int64_t mass = saved ? above : 0;
     int n_kept = saved ? n_above : 0;
-    const bool whole = cut == kMasked + 1 && mp == 0.f;  // no filter
     if (saved) {
       // (after top_p all but the kept tokens of this CTA's list are in the sums)
       for (int i = lane; i < sh.list_n; i += 32) {
@@ -800,21 +860,26 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         mass += weight_of(unordered((uint32_t)(x >> 32)));
         ++n_kept;
       }
-    } else {
-      each([&](const float* v, int a) {
-        if (whole) {
-          Weight w[N];
-          weights_of(v, w);
-          int h = 0, l = 0;
+    } else if (cut == kMasked + 1 && mp == 0.f) {  // no filter
+      each(kDear, [&](const float* v, int) {
+        Weight w[N];
+        weights_of(v, w);
+        int h = 0, l = 0;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            h += w[i].high;
-            l += w[i].low;
-            n_kept += v[i] > -INFINITY;
-          }
-          mass += units({h, l});
-          return;
+        for (int i = 0; i < N; ++i) {
+          h += w[i].high;
+          l += w[i].low;
+          n_kept += v[i] > -INFINITY;
         }
+        mass += units({h, l});
+      });
+    } else {
+      const float cut_value = unordered((uint32_t)(cut >> 32));
+      each(kLight, [&](const float* v, int a) {
+        bool any = false;  // (few vectors have one)
+#pragma unroll
+        for (int i = 0; i < N; ++i) any |= v[i] >= cut_value && !((m - v[i]) * ch > far);
+        if (!any) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int64_t w = kept_weight(v[i], a + i);
@@ -863,9 +928,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         for (int i = 0; i < N; ++i) e[i] = 0;
         if (j < y1) {
           float v[N];
+          Weight w[N];
           Vec<T>::unpack(vector(j), v);
+          weights_of(v, w);
 #pragma unroll
-          for (int i = 0; i < N; ++i) e[i] = max(kept_weight(v[i], a + i), (int64_t)0);
+          for (int i = 0; i < N; ++i) {
+            e[i] = units(w[i]);
+            if (e[i] < least || place(v[i], a + i) < cut) e[i] = 0;
+          }
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) sum += e[i];

@@ -105,6 +105,21 @@ def test_ties_at_the_cut_go_to_the_lowest_index():
     check(x.bfloat16(), u, k=3000 + 100 * i, p=0.3 + 0.02 * i)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_shares_next_to_the_edge_of_ties(dt):
+    # two values, many times each: estimates of the sums from few bins are off by up to 0.4 %,
+    # and the share falls that near to where the first value's tokens end
+    g = torch.Generator().manual_seed(15)
+    for gap in (0.5, 0.503, 0.5078125, 1.25, 3.0):
+        x = torch.full((16, 9000), 2.0)
+        x[:, torch.randperm(9000, generator=g)[:5000]] = 2.0 - gap
+        x = x.to(dt)
+        w = np.exp(x.double().numpy()[0])
+        first = w[w == w.max()].sum() / w.sum()
+        p = first * (1 + np.linspace(-0.004, 0.004, 16))
+        check(x, torch.rand(16, generator=g).numpy(), p=p)
+
+
 def test_around_zero_and_far_apart():
     # the cut falls between values whose bit patterns lie far apart, signed zeros among them
     g = torch.Generator().manual_seed(6)
