@@ -793,7 +793,7 @@ typedef struct {
   const int32_t* group_start; /* device [G + 1]: 0 = first, ascending, B = last */
   const int32_t* shared_len; /* device [G], 0 .. the group's smallest prefix_len */
   const uint64_t* anc;       /* device [B, Q] from tv_build_visibility, nullable */
-  void* out;                 /* device [B, Q, H, d_latent] out */
+  void* out;                 /* device [B, Q, H, d_latent] out, 32-byte aligned */
   float* lse;                /* device [B, Q, H] out, nullable */
   int32_t* status;           /* device int32, nullable.  TV_ERR_BOUNDS: a sequence whose
                                 prefix_len is negative, above the bound or past the cache (its

@@ -71,15 +71,14 @@ constexpr int kNInbox = 4;
 constexpr int kNStg = 2;                        // S-side staging buffers (one step)
 constexpr int kThreads = 256;
 // Shared memory, from offset 0 in each CTA.  Rank 0: latent ring, rope stage, the tile's
-// rope queries, staging.  Rank 1: latent ring, inbox, the epilogue's staging chunks.
+// rope queries, staging.  Rank 1: latent ring, inbox.
 constexpr int kRopeOff = kNLS * kStageS;
 constexpr int kQropeOff = kRopeOff + kChunkS;
 constexpr int kStgOff = kQropeOff + kRows * 128;
 constexpr int kSideA = kStgOff + kNStg * (int)kMsgBytes;
 constexpr int kInboxOff = kNLO * kHalfO;
-constexpr int kEpiOff = kInboxOff + kNInbox * kMsgStride;
 constexpr int kSideMax = kSideA;
-static_assert(kEpiOff + 4 * 32 * 32 * 4 <= kSideMax, "epilogue staging must fit");
+static_assert(kInboxOff + kNInbox * kMsgStride <= kSideMax, "rank 1's buffers must fit");
 
 constexpr uint32_t kTmQ = 0, kTmS0 = 256, kTmS1 = 384;       // S-side TMEM columns
 constexpr uint32_t kFlagRescale = 2;
@@ -119,7 +118,7 @@ struct Shared {
   uint64_t s_full[2], s_empty[2];
   uint64_t qr_full, q_free, pdst_free[kNInbox];
   uint64_t p_full[kNInbox];
-  uint64_t drain, job_full, corr_done, epi_done, dirty, clean, final_bar;
+  uint64_t drain, job_full, corr_done, epi_done[2], dirty, clean, final_bar;
   uint64_t timeout_ns;
   uint32_t tmem_base;
   volatile int abort;
@@ -655,13 +654,17 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
       for (int rr = 0, item; (item = item_at(p, rr, cid)) >= 0 && !sh.abort; ++rr) {
         const Item it = decode(p, item);
         if (ic > 0) {
-          // the previous tile's epilogue has read its last message: hand that buffer back
-          if (!wait_bar(sh, &sh.epi_done, (ic - 1) & 1, p.status)) break;
+          // the previous item's epilogue has read its last message: hand that buffer back
+          if (!wait_bar(sh, &sh.epi_done[0], (ic - 1) & 1, p.status)) break;
           mbar_arrive_remote(map_to_rank(smem_u32(&sh.pdst_free[last_pb]), peer));
         }
         tc_fence_after();
         bool ok = true;
         for (int j = 0; j < it.nb && ok; ++j, ++mc) {
+          // Two blocks before the end: warp 2 may wait for the last block (whose ring stages'
+          // earlier loads have all been seen here) and clear what lies behind its last key.
+          const bool last = j == it.nb - 1;
+          if (it.tail && j == max(it.nb - 2, 0)) mbar_arrive(&sh.dirty);
           const uint32_t pb = mc % kNInbox;
           last_pb = pb;
           if (!wait_bar(sh, &sh.p_full[pb], (mc / kNInbox) & 1, p.status)) { ok = false; break; }
@@ -685,29 +688,29 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
             ++cc;
             tc_fence_after();
           }
-          if (j == it.nb - 1 && it.tail) {
-            // the last block: warp 2 clears the rows behind the last key
-            for (uint32_t w = vc; w < vc + 2 && ok; ++w)
-              ok = wait_bar(sh, &sh.olat_full[w % kNLO], (w / kNLO) & 1, p.status);
-            if (!ok) break;
-            mbar_arrive(&sh.dirty);
+          if (last && it.tail) {
             if (!wait_bar(sh, &sh.clean, nc & 1, p.status)) { ok = false; break; }
             ++nc;
           }
+          const int nk = last && it.tail ? (it.tail + 15) / 16 : 4;  // 16 keys each
           const uint32_t pa = smem_u32(inbox + pb * kMsgStride);
           for (int h = 0; h < 2; ++h, ++vc) {
             const uint32_t st = vc % kNLO;
             if (!wait_bar(sh, &sh.olat_full[st], (vc / kNLO) & 1, p.status)) { ok = false; break; }
             const uint32_t va = smem_u32(lat + st * kHalfO);
+            if (h == 1 && j == 0 && ic > 0) {
+              if (!wait_bar(sh, &sh.epi_done[1], (ic - 1) & 1, p.status)) { ok = false; break; }
+              tc_fence_after();
+            }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ss(tmem + 256 * h, smem_desc(pa + 32 * kk, 16, 1024, 2),
+              if (kk < nk) mma_ss(tmem + 256 * h, smem_desc(pa + 32 * kk, 16, 1024, 2),
                      smem_desc(va + 2048 * kk, 8192, 1024, 2), kIdescPV, (j | kk) != 0);
             mma_commit(&sh.olat_empty[st]);
           }
           // once the MMAs have read the message, the buffer goes straight back to rank 0's
           // softmax; a tile's last message stays until the epilogue has read its row sums
-          if (j < it.nb - 1) mma_commit_multicast(&sh.pdst_free[pb], (uint16_t)(1u << peer));
+          if (!last) mma_commit_multicast(&sh.pdst_free[pb], (uint16_t)(1u << peer));
         }
         if (!ok) break;
         mma_commit(&sh.drain);
@@ -718,7 +721,7 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
         mbar_arrive(&sh.job_full);
         ++ic;
       }
-      if (!sh.abort && ic > 0) wait_bar(sh, &sh.epi_done, (ic - 1) & 1, p.status);
+      if (!sh.abort && ic > 0) wait_bar(sh, &sh.epi_done[1], (ic - 1) & 1, p.status);
       sh.job_type = 0;  // exit
       mbar_arrive(&sh.job_full);
       mma_commit(&sh.final_bar);
@@ -731,14 +734,20 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
       const Item it = decode(p, item);
       vc += 2 * it.nb;
       if (!it.tail) continue;
-      // (the MMA thread has seen both stages of the block arrive)
-      if (!__all_sync(0xffffffffu, lane != 0 || wait_bar(sh, &sh.dirty, nc & 1, p.status))) return;
+      bool ok = true;
+      if (lane == 0) {
+        ok = wait_bar(sh, &sh.dirty, nc & 1, p.status);
+        for (uint32_t u = vc - 2; u < vc && ok; ++u)
+          ok = wait_bar(sh, &sh.olat_full[u % kNLO], (u / kNLO) & 1, p.status);
+      }
+      if (!__all_sync(0xffffffffu, ok)) return;
       ++nc;
-      const int pieces = (kBN - it.tail) * 8;
+      // up to the next 16 keys, where the MMAs end (the swizzle moves 16-byte pieces within a row:
+      // whole rows are cleared)
+      const int pieces = (-it.tail & 15) * 8;
       for (uint32_t u = vc - 2; u < vc; ++u) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          // (the swizzle moves 16-byte pieces within a row: whole rows are cleared)
           uint4* rows = reinterpret_cast<uint4*>(lat + (u % kNLO) * kHalfO + c * kChunkO +
                                                  it.tail * 128);
           for (int i = lane; i < pieces; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -783,55 +792,59 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
         } else if (type == 2) {
           const float lr = reinterpret_cast<const float*>(inbox + pb * kMsgStride + kMsgL)[r];
           const float inv = lr == 0.f ? 0.f : 1.f / lr;  // (a NaN stays one)
-          // Each thread holds its own row (TMEM lane), so storing straight from registers
-          // would make every warp store touch 32 rows.  Each 32-row x 32-column chunk is
-          // staged in shared memory instead (16-byte pieces XOR-swizzled by row, so that both
-          // the writes and the reads below are free of bank conflicts) and written back with
-          // lanes along the columns: every store instruction fills four whole 128-byte lines.
-          float* stg = reinterpret_cast<float*>(smem + kEpiOff) + wq * 1024;
-          const int rows_ok = it.nrows - wq * 32;    // valid rows of the warp's 32
-          // the output's row of lane 0 (its only piece), or the part's
-          const int64_t row0 = (int64_t)(it.direct ? it.row0 : it.part) + wq * 32;
-          float* dst0 = (it.direct ? (float*)p.out : p.part_out) + row0 * kDL;
-          __nv_bfloat16* dst16 =
-              it.direct && p.out_bf16 ? (__nv_bfloat16*)p.out + row0 * kDL : nullptr;
-          const int rr4 = lane >> 3, jj = lane & 7;
+          // Each thread holds its own row (TMEM lane) and stores it 32 bytes, a whole sector, at a
+          // time; nothing is staged.  The columns are read in halves, each handed back to the
+          // MMAs of the next item once it is.
+          const bool warp_rows = wq * 32 < it.nrows, ok_row = r < it.nrows;
+          // the output's row (its only piece), or the part's
+          const int64_t row = (int64_t)(it.direct ? it.row0 : it.part) + r;
+          const bool half_out = it.direct && p.out_bf16;
+          unsigned char* dst = half_out ? (unsigned char*)p.out + row * (kDL * 2)
+                                        : (unsigned char*)(it.direct ? p.out : (void*)p.part_out) +
+                                              row * (kDL * 4);
           auto put_chunk = [&](const uint32_t* v, int c) {
-            __syncwarp();  // the previous chunk's reads of the staging are done
+            if (!ok_row) return;
+            if (half_out) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(stg + lane * 32 + ((e ^ (lane & 7)) << 2)) =
-                  make_float4(__uint_as_float(v[4 * e]) * inv, __uint_as_float(v[4 * e + 1]) * inv,
-                              __uint_as_float(v[4 * e + 2]) * inv, __uint_as_float(v[4 * e + 3]) * inv);
-            __syncwarp();
+              for (int e = 0; e < 2; ++e) {
+                uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = 4 * i + rr4;
-              const float4 x = *reinterpret_cast<const float4*>(stg + row * 32 + ((jj ^ (row & 7)) << 2));
-              if (row >= rows_ok) continue;
-              const int64_t at = (int64_t)row * kDL + 32 * c + 4 * jj;
-              if (dst16)
-                *reinterpret_cast<uint2*>(dst16 + at) =
-                    make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-              else
-                *reinterpret_cast<float4*>(dst0 + at) = x;
+                for (int i = 0; i < 8; ++i)
+                  w[i] = pack_bf16(__uint_as_float(v[16 * e + 2 * i]) * inv,
+                                   __uint_as_float(v[16 * e + 2 * i + 1]) * inv);
+                st_global_v8(dst + 64 * c + 32 * e, w);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(v[8 * e + i]) * inv);
+                st_global_v8(dst + 128 * c + 32 * e, w);
+              }
             }
           };
-          // two chunks in flight: each TMEM load overlaps the previous chunk's stores
-          uint32_t va[32], vb[32];
-          tmem_ld32(tmem + lane_base, va);
-          tmem_wait_ld_regs(va);
 #pragma unroll 1
-          for (int c = 0; c < 16; c += 2) {
-            tmem_ld32(tmem + lane_base + 32 * (c + 1), vb);
-            put_chunk(va, c);
-            tmem_wait_ld_regs(vb);
-            if (c + 2 < 16) tmem_ld32(tmem + lane_base + 32 * (c + 2), va);
-            put_chunk(vb, c + 1);
-            if (c + 2 < 16) tmem_wait_ld_regs(va);
+          for (int h = 0; h < 2; ++h) {
+            if (warp_rows) {
+              // two chunks in flight: each TMEM load overlaps the previous chunk's stores
+              const uint32_t ta = tmem + lane_base + 256 * h;
+              uint32_t va[32], vb[32];
+              tmem_ld32(ta, va);
+              tmem_wait_ld_regs(va);
+#pragma unroll 1
+              for (int c = 0; c < 8; c += 2) {
+                tmem_ld32(ta + 32 * (c + 1), vb);
+                put_chunk(va, 8 * h + c);
+                tmem_wait_ld_regs(vb);
+                if (c + 2 < 8) tmem_ld32(ta + 32 * (c + 2), va);
+                put_chunk(vb, 8 * h + c + 1);
+                if (c + 2 < 8) tmem_wait_ld_regs(va);
+              }
+            }
+            tc_fence_before();
+            mbar_arrive(&sh.epi_done[h]);
           }
-          tc_fence_before();
-          mbar_arrive(&sh.epi_done);
           break;
         } else {
           return;  // exit job (only after an abort)
@@ -880,7 +893,8 @@ shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.job_full, 1);
     mbar_init(&sh.corr_done, 128);
-    mbar_init(&sh.epi_done, 128);
+    mbar_init(&sh.epi_done[0], 128);
+    mbar_init(&sh.epi_done[1], 128);
     mbar_init(&sh.dirty, 1);
     mbar_init(&sh.clean, 1);
     mbar_init(&sh.final_bar, 1);
@@ -906,6 +920,7 @@ shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s
   // (programmatic dependent launch): the set-up above overlaps it, and everything below
   // reads its work records only after this wait.
   griddep_wait();
+  griddep_launch_dependents();  // the join's blocks wait where there is room for them
 
   if (rank == 0)
     s_side(p, &map_lat_s, &map_kpe_s, &map_q, &map_qr, sh, smem);
@@ -1186,13 +1201,15 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
 // The pieces of every row that has more than one, in order of keys, by a warp:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k
 // and the rows of sequences out of bounds: out = 0, lse = -inf.
-__global__ void __launch_bounds__(256)
+constexpr int kJoinThreads = 128;  // (blocks that fit beside the attention's, by registers)
+__global__ void __launch_bounds__(kJoinThreads, 5)
     join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
                 int R, int64_t part2, const float* __restrict__ part_out,
                 const float* __restrict__ part_lse, void* __restrict__ out, int out_bf16,
                 float* __restrict__ lse) {
+  griddep_wait();  // (launched early, see the attention kernel)
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
   const int4 rec = __ldg(seq_rec + b);
@@ -1217,50 +1234,56 @@ __global__ void __launch_bounds__(256)
     k -= n1;
     return k == 0 ? part2 / 2 + row : part2 + (int64_t)(c2 + k - 1) * kRows + in2;
   };
-  float mx = -INFINITY;
-  bool is_nan = false;
-  for (int k = lane; k < n; k += 32) {
-    const float l = part_lse[part_row(k)];
-    is_nan |= l != l;
-    mx = fmaxf(mx, l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (__any_sync(0xffffffffu, is_nan)) mx = NAN;
-  float sum = 0.f;
+  // a running maximum over four pieces at a time, their loads in flight together
+  float mx = -INFINITY, sum = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (mx != -INFINITY) {
-    for (int k0 = 0; k0 < n; k0 += 4) {  // four pieces' loads in flight
-      float w[4];
-      float4 v[4][4];
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    float w[4];
+    float4 v[4][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        w[q] = 0.f;
-        if (k0 + q >= n) continue;
-        const int64_t pr = part_row(k0 + q);
-        w[q] = part_lse[pr];
-        const float4* src = reinterpret_cast<const float4*>(part_out + pr * kDL);
+    for (int q = 0; q < 4; ++q) {
+      w[q] = -INFINITY;
+      if (k0 + q >= n) continue;
+      const int64_t pr = part_row(k0 + q);
+      w[q] = part_lse[pr];
+      const float4* src = reinterpret_cast<const float4*>(part_out + pr * kDL);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[q][i] = __ldcs(src + lane + 32 * i);
-      }
+      for (int i = 0; i < 4; ++i) v[q][i] = __ldcs(src + lane + 32 * i);
+    }
+    float m = mx;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (k0 + q >= n || w[q] == -INFINITY) continue;  // (a piece without a visible key)
-        const float e = expf(w[q] - mx);
-        sum += e;
+    for (int q = 0; q < 4; ++q) m = fmaxf(m, w[q]);
+    if (m == -INFINITY) {  // pieces without a visible key, or NaN, which is nobody's maximum
+      if (!(w[0] != w[0] || w[1] != w[1] || w[2] != w[2] || w[3] != w[3])) continue;
+      m = 0.f;
+    }
+    const float old = expf(mx - m);
+    sum *= old;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i].x = fmaf(e, v[q][i].x, acc[i].x);
-          acc[i].y = fmaf(e, v[q][i].y, acc[i].y);
-          acc[i].z = fmaf(e, v[q][i].z, acc[i].z);
-          acc[i].w = fmaf(e, v[q][i].w, acc[i].w);
-        }
+    for (int i = 0; i < 4; ++i) {
+      acc[i].x *= old;
+      acc[i].y *= old;
+      acc[i].z *= old;
+      acc[i].w *= old;
+    }
+    mx = m;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (w[q] == -INFINITY) continue;
+      const float e = expf(w[q] - mx);
+      sum += e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x = fmaf(e, v[q][i].x, acc[i].x);
+        acc[i].y = fmaf(e, v[q][i].y, acc[i].y);
+        acc[i].z = fmaf(e, v[q][i].z, acc[i].z);
+        acc[i].w = fmaf(e, v[q][i].w, acc[i].w);
       }
     }
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 x = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
@@ -1270,7 +1293,7 @@ __global__ void __launch_bounds__(256)
     else
       reinterpret_cast<float4*>((float*)out + row * kDL)[lane + 32 * i] = x;
   }
-  if (lane == 0 && lse) lse[row] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+  if (lane == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -1471,10 +1494,14 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, shared_attn_kernel, p, lat_s, kpe, lat_o, q, qr);
   if (e != cudaSuccess) return e;
-  join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
-      pa.seq_rec, pa.tile_rec, rows, (int)R, 2 * rows, p.part_out, p.part_lse, a->out, p.out_bf16,
-      a->lse);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  at[0] = at[1];  // no clusters; launched early as well
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, (const int4*)pa.seq_rec, (const int2*)pa.tile_rec, rows,
+                            (int)R, 2 * rows, (const float*)p.part_out, (const float*)p.part_lse, a->out,
+                            p.out_bf16, a->lse);
 }
 
 }  // namespace tv

@@ -1002,9 +1002,12 @@ cudaError_t launch_token_sample(const tv_token_args* a, int sm_count, cudaStream
   p.tokens = a->tokens;
   p.kept = a->kept;
   p.status = a->status;
-  // CTAs per row: up to the two per SM that fit at once, 2048 tokens each at least
+  // CTAs per row: up to the two per SM that fit at once, while a thread has 28 tokens or more (16 x
+  // 50257 floats, top-k: 4 CTAs of a row 17 us, 8 CTAs 19); 16 only for a few rows: clusters of
+  // that size hardly fit side by side (16 x 50257: 38 us; 1 x 163840, top-p: 34 against 40 with 8).
   int C = 1;
-  while (C < kMaxCluster && (int64_t)a->B * C * 2 <= 2ll * sm_count && a->vocab >= 4096ll * C) C *= 2;
+  const int most = a->B <= 4 ? kMaxCluster : kMaxCluster / 2;
+  while (C < most && (int64_t)a->B * C <= sm_count && a->vocab >= 28ll * kThreads * C) C *= 2;
   return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, a->B, C, st) : launch<float>(p, a->B, C, st);
 }
 

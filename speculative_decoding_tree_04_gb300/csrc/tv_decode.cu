@@ -201,8 +201,8 @@ int check_shared(const tv_shared_args* a) {
   if (a->ckv_row_stride < 512 || a->kpe_row_stride < 64 || a->ckv_row_stride >= (1ll << 31) ||
       a->kpe_row_stride >= (1ll << 31) || a->ckv_row_stride % 8 || a->kpe_row_stride % 8 ||
       !aligned(a->c_kv, 16) || !aligned(a->k_pe, 16) || !aligned(a->q_latent, 16) ||
-      !aligned(a->q_pe, 16) || !aligned(a->out, 16) || !aligned(a->lse, 4))
-    return refuse(TV_ERR_INVALID_ARG, who, "tensors and cache rows must be 16-byte aligned");
+      !aligned(a->q_pe, 16) || !aligned(a->out, 32) || !aligned(a->lse, 4))
+    return refuse(TV_ERR_INVALID_ARG, who, "tensors and cache rows must be 16-byte aligned (out: 32)");
   if (c.page_table) {
     if (c.page_size != 64) return refuse(TV_ERR_UNSUPPORTED, who, "needs 64-token pages");
     if (c.max_pages < 1 || (int64_t)c.max_pages * 64 >= (1ll << 31))
