@@ -28,8 +28,7 @@
 //     stage), so that no tensor maps have to be built for each call's pages.
 //   - The work is one line of (tile, step) pairs, cut into equal runs, one for each cluster:
 //     tiles of any number of keys balance to a step, and every cluster gets a contiguous run.
-//   - Every tile of a row that has more than one piece writes a partial result; join_kernel
-//     adds them up by rows.
+//   - A tile whose rows have more than one piece writes partial results; join_kernel adds them up.
 //
 // Keys that no row sees.  A weight of zero times a value that is not finite is NaN, and what
 // lies in a page behind the last key may be anything.  The O side clears those rows of the last
@@ -100,7 +99,7 @@ struct Params {
   void* out;
   int32_t out_bf16;
   float* lse;
-  float* part_out;     // partial results [part row][512]
+  float* part_out;     // partial results: a tile's from part row `part` on
   float* part_lse;
   int32_t* status;
   const int4* items;   // three records each, see Item
@@ -792,19 +791,25 @@ __device__ void o_side(const Params& p, const CUtensorMap* map_lat, Shared& sh,
         } else if (type == 2) {
           const float lr = reinterpret_cast<const float*>(inbox + pb * kMsgStride + kMsgL)[r];
           const float inv = lr == 0.f ? 0.f : 1.f / lr;  // (a NaN stays one)
-          // Each thread holds its own row (TMEM lane) and stores it 32 bytes, a whole sector, at a
-          // time; nothing is staged.  The columns are read in halves, each handed back to the
-          // MMAs of the next item once it is.
+          // Each thread holds its own row (TMEM lane).  A partial result lies with four columns
+          // of all the tile's rows side by side, [128 column groups][rows][4], so that a warp's
+          // 16-byte stores fill whole lines; an output row is stored 32 bytes, a whole sector, at a
+          // time.  The columns are read in halves, each handed back to the MMAs of the next item
+          // once it is.
           const bool warp_rows = wq * 32 < it.nrows, ok_row = r < it.nrows;
-          // the output's row (its only piece), or the part's
-          const int64_t row = (int64_t)(it.direct ? it.row0 : it.part) + r;
           const bool half_out = it.direct && p.out_bf16;
-          unsigned char* dst = half_out ? (unsigned char*)p.out + row * (kDL * 2)
-                                        : (unsigned char*)(it.direct ? p.out : (void*)p.part_out) +
-                                              row * (kDL * 4);
+          unsigned char* dst = half_out ? (unsigned char*)p.out + ((int64_t)it.row0 + r) * (kDL * 2)
+                                        : (unsigned char*)p.out + ((int64_t)it.row0 + r) * (kDL * 4);
+          float4* part = reinterpret_cast<float4*>(p.part_out + (int64_t)it.part * kDL) + r;
           auto put_chunk = [&](const uint32_t* v, int c) {
             if (!ok_row) return;
-            if (half_out) {
+            if (!it.direct) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                part[(8 * c + e) * it.nrows] =
+                    make_float4(__uint_as_float(v[4 * e]) * inv, __uint_as_float(v[4 * e + 1]) * inv,
+                                __uint_as_float(v[4 * e + 2]) * inv, __uint_as_float(v[4 * e + 3]) * inv);
+            } else if (half_out) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 uint32_t w[8];
@@ -941,204 +946,204 @@ shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s
 // ---- the work: segments, tiles, runs ----------------------------------------------------
 // Segments are the groups (those swept together) and then the sequences; tile t of a segment
 // holds its rows 128 t .., all tiles of a segment sweep the same steps.  The tiles lie on a line,
-// each as long as its steps and kTileCost more (what starting and finishing one costs, in
-// steps); the line is cut into equal runs, one per cluster.  A cut less than kMinPiece steps from
-// an end of a tile moves there.
-// A tile's first piece, or whole tile, writes its partial result to part row (its own row, with
-// B*R rows each for the groups' and the sequences' segments); the piece that starts at cut c
+// which is cut into equal runs, one per cluster.  A tile takes its steps and the cost of a piece,
+// what starting and finishing one takes in steps (measured: the next piece's queries 2 to 3, and
+// what is not overlapped of a full tile's output; 1.6 us a step).  Cutting a tile adds pieces: with
+// runs of length L a tile of s steps is cut s / L times on average, so that its steps count
+// 1 + cost / L each, and L itself follows from C L = N cost + S (1 + cost / L), with N tiles, S
+// steps and C clusters.  A cut less than kMinPiece steps from an end of a tile moves there.
+// A tile's first piece, or whole tile, writes its partial result to part rows of its own (its
+// rows, with B*R each for the groups' and the sequences' segments); the piece that starts at cut c
 // writes to part rows 2*B*R + 128 c ...
-constexpr int kTileCost = 4;
 constexpr int kMinPiece = 2;
 constexpr int kPrepThreads = 1024;
+constexpr int kFixed = 1024;  // lengths on the line are in units of a step / 1024
+__host__ __device__ constexpr int piece_cost(int rows) { return rows <= 32 ? 3 : 5; }
 
+// A segment's part of the line, and what its items need.
 struct Segment {
-  int row0, nrows, steps, nkeys;  // rows, 128-key steps and keys
-  int seq, blk0;                  // sequence whose pages hold them, from which block on
-  int tile0;                      // tiles before this segment
-  int direct;                     // the only segment of its rows
+  int64_t steps0, cost0;  // steps and costs of the tiles before
+  int tile0;              // tiles before
+  int steps, nkeys;       // 128-key steps (0: no tiles) and keys
+  int blk0;               // first 64-key block
 };
+constexpr int kFitSegments = 1024;  // that fit the block's shared memory
 
 struct PrepArgs {
   const int32_t* prefix_len;
   const int32_t* group_start;
   const int32_t* shared_len;
-  int B, R, Q, G, T, max_prefix, ncl, max_tiles;  // T: tiles of a sequence's rows
+  int B, R, Q, G, T, max_prefix, ncl;  // T: tiles of a sequence's rows
   int64_t seq_cap;
   int32_t* group_of;    // [B]
   int32_t* group_bad;   // [G]
-  Segment* seg;         // [G + B]
-  int64_t* cost;        // [G + B + 1]: of the tiles before
+  Segment* seg;         // [G + B], where they do not fit the shared memory
   int4* seq_rec;        // [B]: {first tile of the group's segment or -1, its first row,
-                        //       first tile of the sequence's, 1: out of bounds}
-  int2* tile_rec;       // [max_tiles]: {pieces, cut at which the second one starts}
+                        //       first tile of the sequence's, rows of the group; -1: out of bounds}
+  int2* tile_rec;       // [tiles]: {pieces, cut at which the second one starts}
   int4* items;
   int32_t* cl_start;    // [ncl + 1]
   int32_t* status;
 };
 
-// Exclusive prefix sums over the block of one (cost, tiles) pair a thread; returns the totals.
-__device__ __forceinline__ void scan_pair(int64_t& a, int& b, int64_t* sa, int* sb, int64_t& ta, int& tb) {
+// Exclusive prefix sums over the block of three values a thread, and their totals.
+__device__ __forceinline__ void scan_three(int64_t* v, int64_t (*sums)[32], int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t ia = a;
-  int ib = b;
+  int64_t up[3];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, ia, o);
-    const int y = __shfl_up_sync(0xffffffffu, ib, o);
-    if (lane >= o) {
-      ia += x;
-      ib += y;
+  for (int i = 0; i < 3; ++i) {
+    up[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, up[i], o);
+      if (lane >= o) up[i] += x;
     }
-  }
-  if (lane == 31) {
-    sa[warp] = ia;
-    sb[warp] = ib;
+    if (lane == 31) sums[i][warp] = up[i];
   }
   __syncthreads();
-  const int64_t wa = sa[lane];
-  const int wb = sb[lane];
-  int64_t pa = wa;
-  int pb = wb;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, pa, o);
-    const int y = __shfl_up_sync(0xffffffffu, pb, o);
-    if (lane >= o) {
-      pa += x;
-      pb += y;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t mine = sums[i][lane];
+    int64_t w = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
     }
+    total[i] = __shfl_sync(0xffffffffu, w, 31);
+    v[i] = up[i] - v[i] + __shfl_sync(0xffffffffu, w - mine, warp);
   }
-  ta = __shfl_sync(0xffffffffu, pa, 31);
-  tb = __shfl_sync(0xffffffffu, pb, 31);
-  a = ia - a + (warp > 0 ? __shfl_sync(0xffffffffu, pa, max(warp - 1, 0)) : 0);
-  b = ib - b + (warp > 0 ? __shfl_sync(0xffffffffu, pb, max(warp - 1, 0)) : 0);
   __syncthreads();
 }
 
-// Last i in [0, n) with v[i] <= x (v ascends, v[0] <= x).
-template <typename V, typename X>
-__device__ __forceinline__ int last_at_most(const V* v, int n, X x) {
+// Last i in [0, n) with at(i) <= x (at ascends, at(0) <= x).
+template <typename At, typename X>
+__device__ __forceinline__ int last_at_most(At at, int n, X x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((X)v[mid] <= x) lo = mid;
+    if (at(mid) <= x) lo = mid;
     else hi = mid - 1;
   }
   return lo;
 }
 
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a) {
-  __shared__ int64_t sa[32];
-  __shared__ int sb[32];
+  extern __shared__ __align__(16) unsigned char prep_smem[];
+  __shared__ int64_t sums[3][32];
   __shared__ int cut_tile[kMaxClusters + 1], cut_step[kMaxClusters + 1], first[kMaxClusters + 1];
   griddep_launch_dependents();  // the attention kernel may start its set-up now
   const int tid = threadIdx.x, B = a.B, G = a.G, n_seg = G + B;
+  const bool fits = n_seg <= kFitSegments;
+  Segment* seg = fits ? reinterpret_cast<Segment*>(prep_smem) : a.seg;
+  int32_t* group_of = fits ? reinterpret_cast<int32_t*>(seg + n_seg) : a.group_of;
+  int32_t* group_bad = fits ? group_of + B : a.group_bad;
   // ---- groups: which are sound ----
   bool ok = true;
   for (int g = tid; g < G; g += kPrepThreads) {
-    const int s = a.group_start[g], e = a.group_start[g + 1];
+    const int s = a.group_start[g], e = a.group_start[g + 1], n = a.shared_len[g];
     ok = ok && s >= 0 && s <= e && e <= B && (g > 0 || s == 0) && (g < G - 1 || e == B);
-    const int n = a.shared_len[g];
-    a.group_bad[g] = n < 0 || n > a.max_prefix || n > a.seq_cap;
+    group_bad[g] = n < 0 || n > a.max_prefix || n > a.seq_cap;
   }
   const bool groups = __syncthreads_and(ok) && G > 0;
   if (!ok) report(a.status, TV_ERR_BOUNDS);
-  auto out_of_bounds = [&](int P) {
-    return P < 0 || P > a.max_prefix || (int64_t)P + a.Q > a.seq_cap;
-  };
   if (groups) {
     for (int b = tid; b < B; b += kPrepThreads) {
       // (of groups that start at b, empty ones among them, the last)
-      const int g = last_at_most(a.group_start, G, b);
-      a.group_of[b] = g;
-      if (a.shared_len[g] > a.prefix_len[b]) atomicOr(&a.group_bad[g], 1);
+      const int g = last_at_most([&](int i) { return a.group_start[i]; }, G, b);
+      group_of[b] = g;
+      if (a.shared_len[g] > a.prefix_len[b]) atomicOr(&group_bad[g], 1);
     }
   }
   __syncthreads();
   // ---- segments ----
-  // Together where it saves more steps than the partial results cost: a tile of the group adds
-  // about kTileCost steps, and every sequence's tile becomes a partial result as well.
+  // Together where it saves more steps than the partial results cost: a tile of the group is a
+  // piece more, and every sequence's tile becomes a partial result as well.
   auto shared_steps = [&](int g) {
-    if (!groups) return 0;
+    if (!groups || group_bad[g]) return 0;
     const int n = a.group_start[g + 1] - a.group_start[g];
-    if (a.group_bad[g]) return 0;
     const int64_t steps = (a.shared_len[g] / kBN + 1) / 2;
     const int64_t tiles = ((int64_t)n * a.R + kRows - 1) / kRows;
-    return ((int64_t)n * a.T - tiles) * steps > kTileCost * (tiles + 2) ? (int)steps : 0;
+    return ((int64_t)n * a.T - tiles) * steps > piece_cost(kRows) * (tiles + 2) ? (int)steps : 0;
   };
-  int64_t run_cost = 0;
-  int run_tiles = 0;
+  int64_t run[3] = {0, 0, 0};  // tiles, steps, costs so far
   for (int base = 0; base < n_seg; base += kPrepThreads) {
     const int i = base + tid;
     Segment s{};
-    int tiles = 0;
+    int64_t v[3] = {0, 0, 0}, all[3];
     if (i < G) {
       s.steps = shared_steps(i);
-      if (groups && a.group_bad[i]) report(a.status, TV_ERR_BOUNDS);
+      if (groups && group_bad[i]) report(a.status, TV_ERR_BOUNDS);
       if (s.steps > 0) {
-        s.seq = a.group_start[i];
-        s.row0 = s.seq * a.R;
-        s.nrows = (a.group_start[i + 1] - s.seq) * a.R;
+        const int rows = (a.group_start[i + 1] - a.group_start[i]) * a.R;
         s.nkeys = a.shared_len[i] / kBN * kBN;
-        tiles = (s.nrows + kRows - 1) / kRows;
+        v[0] = (rows + kRows - 1) / kRows;
+        v[2] = v[0] * piece_cost(kRows);
       }
     } else if (i < n_seg) {
       const int b = i - G, P = a.prefix_len[b];
-      if (out_of_bounds(P)) {
+      if (P < 0 || P > a.max_prefix || (int64_t)P + a.Q > a.seq_cap) {
         report(a.status, TV_ERR_BOUNDS);
       } else {
-        const int g = groups ? a.group_of[b] : 0;
-        const bool shared = groups && shared_steps(g) > 0;
-        const int from = shared ? a.shared_len[g] / kBN : 0;
-        s.seq = b;
-        s.row0 = b * a.R;
-        s.nrows = a.R;
-        s.blk0 = from;
-        s.nkeys = P + a.Q - from * kBN;
+        const int g = groups ? group_of[b] : 0;
+        s.blk0 = groups && shared_steps(g) > 0 ? a.shared_len[g] / kBN : 0;
+        s.nkeys = P + a.Q - s.blk0 * kBN;
         s.steps = (s.nkeys + kStep - 1) / kStep;
-        s.direct = !shared;
-        tiles = a.T;
+        v[0] = a.T;
+        v[2] = v[0] * piece_cost(min(a.R, kRows));
       }
     }
-    int64_t cost = (int64_t)tiles * (s.steps + kTileCost), all_cost;
-    int before = tiles, all_tiles;
-    scan_pair(cost, before, sa, sb, all_cost, all_tiles);
+    v[1] = v[0] * s.steps;
+    scan_three(v, sums, all);
     if (i < n_seg) {
-      s.tile0 = run_tiles + before;
-      a.seg[i] = s;
-      a.cost[i] = run_cost + cost;
-      if (i >= G) a.seq_rec[i - G] = make_int4(-1, 0, s.tile0, tiles == 0);
+      s.tile0 = (int)(run[0] + v[0]);
+      s.steps0 = run[1] + v[1];
+      s.cost0 = run[2] + v[2];
+      seg[i] = s;
     }
-    run_cost += all_cost;
-    run_tiles += all_tiles;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) run[k] += all[k];
   }
-  const int64_t total = run_cost;
-  const int n_tiles = run_tiles;
+  const int n_tiles = (int)run[0];
   __syncthreads();
-  if (groups) {
-    for (int b = tid; b < B; b += kPrepThreads) {
-      const Segment& s = a.seg[a.group_of[b]];
-      if (s.steps > 0) {
-        a.seq_rec[b].x = s.tile0;
-        a.seq_rec[b].y = s.row0;
+  for (int b = tid; b < B; b += kPrepThreads) {
+    const Segment& own = seg[G + b];
+    int4 rec = make_int4(-1, 0, own.tile0, own.steps > 0 ? 0 : -1);
+    if (groups && own.steps > 0) {
+      const int g = group_of[b];
+      if (seg[g].steps > 0) {
+        rec.x = seg[g].tile0;
+        rec.y = a.group_start[g] * a.R;
+        rec.w = (a.group_start[g + 1] - a.group_start[g]) * a.R;
       }
     }
+    a.seq_rec[b] = rec;
   }
   // ---- cuts ----
-  // runs of at least a few steps each: with less work, fewer clusters
-  const int64_t run = max((total + a.ncl - 1) / a.ncl, (int64_t)(2 * kTileCost));
+  // the length of a run (see above), at least a few steps: with less work, fewer clusters
+  int64_t length;
+  {
+    const float c = (float)piece_cost(kRows), C = (float)a.ncl, w = (float)(run[1] + run[2]);
+    const float l = (w + sqrtf(w * w + 4.f * C * c * (float)run[1])) / (2.f * C);
+    length = (int64_t)(fmaxf(l, 2.f * c) * (float)kFixed) + 1;
+  }
+  const int64_t per_step = kFixed + (int64_t)piece_cost(kRows) * kFixed * kFixed / length;
+  auto place = [&](int i) { return seg[i].cost0 * kFixed + seg[i].steps0 * per_step; };
+  const int64_t end = run[2] * kFixed + run[1] * per_step;
   for (int c = tid; c <= a.ncl; c += kPrepThreads) {
     int tile = n_tiles, step = 0;
-    const int64_t at = c * run;
-    if (at < total) {
+    const int64_t at = c * length;
+    if (at < end && c < a.ncl) {
       // (segments without tiles are as long as nothing: the last one at a place has tiles)
-      const int i = last_at_most(a.cost, n_seg, at);
-      const Segment& s = a.seg[i];
-      const int64_t in = at - a.cost[i], len = s.steps + kTileCost;
+      const int i = last_at_most(place, n_seg, at);
+      const Segment& s = seg[i];
+      const int64_t cost = (int64_t)piece_cost(i < G ? kRows : min(a.R, kRows)) * kFixed;
+      const int64_t len = s.steps * per_step + cost, in = at - place(i);
       tile = s.tile0 + (int)(in / len);
-      step = max((int)(in % len) - kTileCost, 0);
-      if (step < kMinPiece) step = 0;
-      else if (s.steps - step < kMinPiece) {
+      step = (int)(max(in % len - cost, (int64_t)0) / per_step);
+      if (step < kMinPiece) {
+        step = 0;
+      } else if (s.steps - step < kMinPiece) {
         step = 0;
         ++tile;
       }
@@ -1162,138 +1167,124 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
         const int x = __shfl_up_sync(0xffffffffu, up_to, o);
         if (tid >= o) up_to += x;
       }
-      if (c < a.ncl) first[c] = carry + up_to - n;
+      if (c < a.ncl) a.cl_start[c] = first[c] = carry + up_to - n;
       carry += __shfl_sync(0xffffffffu, up_to, 31);
     }
-    if (tid == 0) first[a.ncl] = carry;
+    if (tid == 0) a.cl_start[a.ncl] = first[a.ncl] = carry;
   }
   __syncthreads();
-  for (int c = tid; c <= a.ncl; c += kPrepThreads) a.cl_start[c] = first[c];
   const int part2 = 2 * B * a.R;
   for (int k = tid; k < first[a.ncl]; k += kPrepThreads) {
     // (of clusters that start at k, empty ones among them, the last)
-    const int c = last_at_most(first, a.ncl, k), j = k - first[c];
+    const int c = last_at_most([&](int i) { return first[i]; }, a.ncl, k), j = k - first[c];
     const int tile = cut_tile[c] + j;
-    int lo = 0, hi = n_seg - 1;  // the segment: the last that starts at the tile or before it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.seg[mid].tile0 <= tile) lo = mid;
-      else hi = mid - 1;
-    }
-    const Segment s = a.seg[lo];
+    // the segment: the last that starts at the tile or before it
+    const int i = last_at_most([&](int x) { return seg[x].tile0; }, n_seg, tile);
+    const Segment s = seg[i];
+    const bool group = i < G;
+    const int seq = group ? a.group_start[i] : i - G;
+    const int rows = group ? (a.group_start[i + 1] - seq) * a.R : a.R;
     const int s0 = j == 0 ? cut_step[c] : 0;
     const int s1 = tile == cut_tile[c + 1] ? cut_step[c + 1] : s.steps;
-    int pieces = 1;  // (known to the tile's first piece)
-    if (s0 == 0) {
+    if (s0 == 0) {  // the tile's first piece knows how many there are
+      int pieces = 1;
       for (int d = c + 1; d <= a.ncl && cut_tile[d] == tile && cut_step[d] > 0; ++d) ++pieces;
       a.tile_rec[tile] = make_int2(pieces, c + 1);
     }
-    const int r0 = (tile - s.tile0) * kRows, row0 = s.row0 + r0;
-    const bool group = lo < G;
+    const int r0 = (tile - s.tile0) * kRows, row0 = seq * a.R + r0;
     const int part = s0 > 0 ? part2 + c * kRows : (group ? row0 : B * a.R + row0);
-    const bool direct = s.direct && s0 == 0 && s1 == s.steps;
-    a.items[3 * k] = make_int4(row0, min(kRows, s.nrows - r0), s.seq, s.blk0);
+    // the only piece of its rows
+    const bool direct = !group && s.blk0 == 0 && s0 == 0 && s1 == s.steps;
+    a.items[3 * k] = make_int4(row0, min(kRows, rows - r0), seq, s.blk0);
     a.items[3 * k + 1] = make_int4(s0, s1, s.nkeys, direct);
-    a.items[3 * k + 2] = make_int4(part, group ? s.nkeys : s.nkeys - a.Q, group ? -1 : s.seq, 0);
+    a.items[3 * k + 2] = make_int4(part, group ? s.nkeys : s.nkeys - a.Q, group ? -1 : seq, 0);
   }
 }
 
-// The pieces of every row that has more than one, in order of keys, by a warp:
+// The pieces of every row that has more than one, in order of keys:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k
-// and the rows of sequences out of bounds: out = 0, lse = -inf.
+// and the rows of sequences out of bounds: out = 0, lse = -inf.  A warp takes 32 rows, one a lane,
+// and 32 of the 512 columns: eight 16-byte loads a piece, which lie side by side over the lanes.
 constexpr int kJoinThreads = 128;  // (blocks that fit beside the attention's, by registers)
 __global__ void __launch_bounds__(kJoinThreads, 5)
     join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
-                int R, int64_t part2, const float* __restrict__ part_out,
-                const float* __restrict__ part_lse, void* __restrict__ out, int out_bf16,
-                float* __restrict__ lse) {
+                int R, const float* __restrict__ part_out, const float* __restrict__ part_lse,
+                void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
   griddep_wait();  // (launched early, see the attention kernel)
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = (int)(w & 15);
+  const int64_t row = (w >> 4) * 32 + (threadIdx.x & 31);
   if (row >= rows) return;
+  const int64_t part2 = 2 * rows;
   const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
   const int4 rec = __ldg(seq_rec + b);
-  int n1 = 0, c1 = 0, n2 = 0, c2 = 0, in1 = 0;
-  const int in2 = r % kRows;
-  if (!rec.w) {
+  int n1 = 0, n2 = 0, cut1 = 0, cut2 = 0, in1 = 0, rows1 = 0;
+  const int in2 = r % kRows, rows2 = min(kRows, R - (r - in2));
+  if (rec.w >= 0) {
     const int2 own = __ldg(tile_rec + rec.z + r / kRows);
     n2 = own.x;
-    c2 = own.y;
+    cut2 = own.y;
     if (rec.x >= 0) {
       const int g = (int)row - rec.y;
       const int2 t = __ldg(tile_rec + rec.x + g / kRows);
       n1 = t.x;
-      c1 = t.y;
+      cut1 = t.y;
       in1 = g % kRows;
+      rows1 = min(kRows, rec.w - (g - in1));
     }
     if (n1 == 0 && n2 == 1) return;  // written by the attention kernel
   }
   const int n = n1 + n2;
-  auto part_row = [&](int k) -> int64_t {
-    if (k < n1) return k == 0 ? row : part2 + (int64_t)(c1 + k - 1) * kRows + in1;
-    k -= n1;
-    return k == 0 ? part2 / 2 + row : part2 + (int64_t)(c2 + k - 1) * kRows + in2;
-  };
-  // a running maximum over four pieces at a time, their loads in flight together
   float mx = -INFINITY, sum = 0.f;
-  float4 acc[4];
+  float acc[32];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < n; k0 += 4) {
-    float w[4];
-    float4 v[4][4];
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    const bool group = k < n1;
+    const int j = group ? k : k - n1, in = group ? in1 : in2, n_rows = group ? rows1 : rows2;
+    // the piece's first part row
+    const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
+                             : (group ? row : part2 / 2 + row) - in;
+    const float l = __ldg(part_lse + p0 + in);
+    const float4* src = reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)8 * chunk * n_rows + in;
+    float4 v[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      w[q] = -INFINITY;
-      if (k0 + q >= n) continue;
-      const int64_t pr = part_row(k0 + q);
-      w[q] = part_lse[pr];
-      const float4* src = reinterpret_cast<const float4*>(part_out + pr * kDL);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[q][i] = __ldcs(src + lane + 32 * i);
-    }
-    float m = mx;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m = fmaxf(m, w[q]);
-    if (m == -INFINITY) {  // pieces without a visible key, or NaN, which is nobody's maximum
-      if (!(w[0] != w[0] || w[1] != w[1] || w[2] != w[2] || w[3] != w[3])) continue;
-      m = 0.f;
-    }
-    const float old = expf(mx - m);
-    sum *= old;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i].x *= old;
-      acc[i].y *= old;
-      acc[i].z *= old;
-      acc[i].w *= old;
-    }
+    for (int e = 0; e < 8; ++e) v[e] = __ldcs(src + e * n_rows);
+    if (l == -INFINITY) continue;  // a piece without a visible key
+    const float m = fmaxf(mx, l);  // (a NaN is nobody's maximum; its weight is NaN)
+    const float old = expf(mx - m), e1 = expf(l - m);
     mx = m;
+    sum = sum * old + e1;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (w[q] == -INFINITY) continue;
-      const float e = expf(w[q] - mx);
-      sum += e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i].x = fmaf(e, v[q][i].x, acc[i].x);
-        acc[i].y = fmaf(e, v[q][i].y, acc[i].y);
-        acc[i].z = fmaf(e, v[q][i].z, acc[i].z);
-        acc[i].w = fmaf(e, v[q][i].w, acc[i].w);
-      }
+    for (int e = 0; e < 8; ++e) {
+      acc[4 * e] = acc[4 * e] * old + e1 * v[e].x;
+      acc[4 * e + 1] = acc[4 * e + 1] * old + e1 * v[e].y;
+      acc[4 * e + 2] = acc[4 * e + 2] * old + e1 * v[e].z;
+      acc[4 * e + 3] = acc[4 * e + 3] * old + e1 * v[e].w;
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t word[8];
+  if (out_bf16) {
+    unsigned char* dst = (unsigned char*)out + row * (kDL * 2) + 64 * chunk;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
-    if (out_bf16)
-      reinterpret_cast<uint2*>((__nv_bfloat16*)out + row * kDL)[lane + 32 * i] =
-          make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-    else
-      reinterpret_cast<float4*>((float*)out + row * kDL)[lane + 32 * i] = x;
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        word[i] = pack_bf16(acc[16 * e + 2 * i] * inv, acc[16 * e + 2 * i + 1] * inv);
+      st_global_v8(dst + 32 * e, word);
+    }
+  } else {
+    unsigned char* dst = (unsigned char*)out + row * (kDL * 4) + 128 * chunk;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) word[i] = __float_as_uint(acc[8 * e + i] * inv);
+      st_global_v8(dst + 32 * e, word);
+    }
   }
-  if (lane == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
+  if (chunk == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -1376,7 +1367,7 @@ int planned_clusters() {
 
 struct Layout {
   int64_t max_tiles, part_rows;
-  size_t group_of, group_bad, seg, cost, seq_rec, tile_rec, items, cl_start, part_out, part_lse, total;
+  size_t group_of, group_bad, seg, seq_rec, tile_rec, items, cl_start, part_out, part_lse, total;
 };
 Layout layout(const tv_shared_args* a, int ncl) {
   const int64_t R = (int64_t)a->Q * a->H, B = a->B, G = a->G;
@@ -1393,7 +1384,6 @@ Layout layout(const tv_shared_args* a, int ncl) {
   w.group_of = take(B * 4);
   w.group_bad = take(G * 4);
   w.seg = take((G + B) * sizeof(Segment));
-  w.cost = take((G + B + 1) * 8);
   w.seq_rec = take(B * 16);
   w.tile_rec = take(w.max_tiles * 8);
   w.items = take((w.max_tiles + ncl) * 48);
@@ -1437,18 +1427,18 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   pa.T = (int)((R + kRows - 1) / kRows);
   pa.max_prefix = a->max_prefix_len;
   pa.ncl = ncl;
-  pa.max_tiles = (int)w.max_tiles;
   pa.seq_cap = paged ? (int64_t)cache.max_pages * kBN : cache.kv_stride_b;
   pa.group_of = (int32_t*)(base + w.group_of);
   pa.group_bad = (int32_t*)(base + w.group_bad);
   pa.seg = (Segment*)(base + w.seg);
-  pa.cost = (int64_t*)(base + w.cost);
   pa.seq_rec = (int4*)(base + w.seq_rec);
   pa.tile_rec = (int2*)(base + w.tile_rec);
   pa.items = (int4*)(base + w.items);
   pa.cl_start = (int32_t*)(base + w.cl_start);
   pa.status = a->status;
-  prepare_kernel<<<1, kPrepThreads, 0, st>>>(pa);
+  const int n_seg = a->G + a->B;
+  const size_t prep_smem = n_seg <= kFitSegments ? n_seg * sizeof(Segment) + (a->B + a->G) * 4 : 0;
+  prepare_kernel<<<1, kPrepThreads, prep_smem, st>>>(pa);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -1494,14 +1484,15 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, shared_attn_kernel, p, lat_s, kpe, lat_o, q, qr);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  const int64_t join_warps = (rows + 31) / 32 * 16;
+  cfg.gridDim = dim3((unsigned)((join_warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   at[0] = at[1];  // no clusters; launched early as well
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, join_kernel, (const int4*)pa.seq_rec, (const int2*)pa.tile_rec, rows,
-                            (int)R, 2 * rows, (const float*)p.part_out, (const float*)p.part_lse, a->out,
-                            p.out_bf16, a->lse);
+                            (int)R, (const float*)p.part_out, (const float*)p.part_lse, a->out, p.out_bf16,
+                            a->lse);
 }
 
 }  // namespace tv
