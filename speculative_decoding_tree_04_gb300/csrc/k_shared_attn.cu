@@ -958,7 +958,7 @@ shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s
 constexpr int kMinPiece = 2;
 constexpr int kPrepThreads = 1024;
 constexpr int kFixed = 1024;  // lengths on the line are in units of a step / 1024
-__host__ __device__ constexpr int piece_cost(int rows) { return rows <= 32 ? 3 : 5; }
+__host__ __device__ constexpr int piece_cost(int rows) { return rows <= 32 ? 2 : 3; }
 
 // A segment's part of the line, and what its items need.
 struct Segment {
@@ -1204,7 +1204,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
 // The pieces of every row that has more than one, in order of keys:
 //   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) out_k
 // and the rows of sequences out of bounds: out = 0, lse = -inf.  A warp takes 32 rows, one a lane,
-// and 32 of the 512 columns: eight 16-byte loads a piece, which lie side by side over the lanes.
+// and 16 of the 512 columns: four 16-byte loads a piece, which lie side by side over the lanes, four
+// pieces' on their way at once.
 constexpr int kJoinThreads = 128;  // (blocks that fit beside the attention's, by registers)
 __global__ void __launch_bounds__(kJoinThreads, 5)
     join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
@@ -1212,8 +1213,8 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
                 void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
   griddep_wait();  // (launched early, see the attention kernel)
   const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int chunk = (int)(w & 15);
-  const int64_t row = (w >> 4) * 32 + (threadIdx.x & 31);
+  const int chunk = (int)(w & 31);
+  const int64_t row = (w >> 5) * 32 + (threadIdx.x & 31);
   if (row >= rows) return;
   const int64_t part2 = 2 * rows;
   const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
@@ -1236,52 +1237,56 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
   }
   const int n = n1 + n2;
   float mx = -INFINITY, sum = 0.f;
-  float acc[32];
+  float acc[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll 1
-  for (int k = 0; k < n; ++k) {
-    const bool group = k < n1;
-    const int j = group ? k : k - n1, in = group ? in1 : in2, n_rows = group ? rows1 : rows2;
-    // the piece's first part row
-    const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
-                             : (group ? row : part2 / 2 + row) - in;
-    const float l = __ldg(part_lse + p0 + in);
-    const float4* src = reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)8 * chunk * n_rows + in;
-    float4 v[8];
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    float l[4];
+    float4 v[4][4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __ldcs(src + e * n_rows);
-    if (l == -INFINITY) continue;  // a piece without a visible key
-    const float m = fmaxf(mx, l);  // (a NaN is nobody's maximum; its weight is NaN)
-    const float old = expf(mx - m), e1 = expf(l - m);
-    mx = m;
-    sum = sum * old + e1;
+    for (int q = 0; q < 4; ++q) {
+      l[q] = -INFINITY;
+      if (k0 + q >= n) continue;
+      const bool group = k0 + q < n1;
+      const int j = group ? k0 + q : k0 + q - n1, in = group ? in1 : in2, n_rows = group ? rows1 : rows2;
+      // the piece's first part row
+      const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
+                               : (group ? row : part2 / 2 + row) - in;
+      l[q] = __ldg(part_lse + p0 + in);
+      const float4* src =
+          reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)4 * chunk * n_rows + in;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      acc[4 * e] = acc[4 * e] * old + e1 * v[e].x;
-      acc[4 * e + 1] = acc[4 * e + 1] * old + e1 * v[e].y;
-      acc[4 * e + 2] = acc[4 * e + 2] * old + e1 * v[e].z;
-      acc[4 * e + 3] = acc[4 * e + 3] * old + e1 * v[e].w;
+      for (int e = 0; e < 4; ++e) v[q][e] = __ldcs(src + e * n_rows);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (l[q] == -INFINITY) continue;  // a piece without a visible key, or none
+      const float m = fmaxf(mx, l[q]);  // (a NaN is nobody's maximum; its weight is NaN)
+      const float old = expf(mx - m), e1 = expf(l[q] - m);
+      mx = m;
+      sum = sum * old + e1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[4 * e] = acc[4 * e] * old + e1 * v[q][e].x;
+        acc[4 * e + 1] = acc[4 * e + 1] * old + e1 * v[q][e].y;
+        acc[4 * e + 2] = acc[4 * e + 2] * old + e1 * v[q][e].z;
+        acc[4 * e + 3] = acc[4 * e + 3] * old + e1 * v[q][e].w;
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t word[8];
   if (out_bf16) {
-    unsigned char* dst = (unsigned char*)out + row * (kDL * 2) + 64 * chunk;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    st_global_v8((unsigned char*)out + row * (kDL * 2) + 32 * chunk, word);
+  } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        word[i] = pack_bf16(acc[16 * e + 2 * i] * inv, acc[16 * e + 2 * i + 1] * inv);
-      st_global_v8(dst + 32 * e, word);
-    }
-  } else {
-    unsigned char* dst = (unsigned char*)out + row * (kDL * 4) + 128 * chunk;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
       for (int i = 0; i < 8; ++i) word[i] = __float_as_uint(acc[8 * e + i] * inv);
-      st_global_v8(dst + 32 * e, word);
+      st_global_v8((unsigned char*)out + row * (kDL * 4) + 64 * chunk + 32 * e, word);
     }
   }
   if (chunk == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
@@ -1484,7 +1489,7 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, shared_attn_kernel, p, lat_s, kpe, lat_o, q, qr);
   if (e != cudaSuccess) return e;
-  const int64_t join_warps = (rows + 31) / 32 * 16;
+  const int64_t join_warps = (rows + 31) / 32 * 32;
   cfg.gridDim = dim3((unsigned)((join_warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
