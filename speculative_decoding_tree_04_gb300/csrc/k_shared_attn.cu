@@ -1211,13 +1211,14 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
     join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
                 int R, const float* __restrict__ part_out, const float* __restrict__ part_lse,
                 void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
-  griddep_wait();  // (launched early, see the attention kernel)
   const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int chunk = (int)(w & 31);
   const int64_t row = (w >> 5) * 32 + (threadIdx.x & 31);
   if (row >= rows) return;
   const int64_t part2 = 2 * rows;
-  const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
+  const int b = (int)((uint32_t)row / (uint32_t)R), r = (int)row - b * R;
+  // (the records are prepare_kernel's, which has ended: the attention kernel lets this one start
+  // after that, and only its results have to be waited for)
   const int4 rec = __ldg(seq_rec + b);
   int n1 = 0, n2 = 0, cut1 = 0, cut2 = 0, in1 = 0, rows1 = 0;
   const int in2 = r % kRows, rows2 = min(kRows, R - (r - in2));
@@ -1235,6 +1236,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
     }
     if (n1 == 0 && n2 == 1) return;  // written by the attention kernel
   }
+  griddep_wait();
   const int n = n1 + n2;
   float mx = -INFINITY, sum = 0.f;
   float acc[16];
