@@ -956,18 +956,18 @@ shared_attn_kernel(const Params p, const __grid_constant__ CUtensorMap map_lat_s
 // rows, with B*R each for the groups' and the sequences' segments); the piece that starts at cut c
 // writes to part rows 2*B*R + 128 c ...
 constexpr int kMinPiece = 2;
-constexpr int kPrepThreads = 1024;
+constexpr int kPrepThreads = 256;
 constexpr int kFixed = 1024;  // lengths on the line are in units of a step / 1024
 __host__ __device__ constexpr int piece_cost(int rows) { return rows <= 32 ? 2 : 3; }
 
 // A segment's part of the line, and what its items need.
 struct Segment {
-  int64_t steps0, cost0;  // steps and costs of the tiles before
-  int tile0;              // tiles before
-  int steps, nkeys;       // 128-key steps (0: no tiles) and keys
-  int blk0;               // first 64-key block
+  int64_t place;     // where it starts on the line; before that is known, steps of the tiles before
+  int cost0, tile0;  // costs of and tiles before
+  int steps, nkeys;  // 128-key steps (0: no tiles) and keys
+  int blk0, pad;     // first 64-key block
 };
-constexpr int kFitSegments = 1024;  // that fit the block's shared memory
+constexpr int kFitSequences = 512;  // whose lists fit the block's shared memory
 
 struct PrepArgs {
   const int32_t* prefix_len;
@@ -975,9 +975,9 @@ struct PrepArgs {
   const int32_t* shared_len;
   int B, R, Q, G, T, max_prefix, ncl;  // T: tiles of a sequence's rows
   int64_t seq_cap;
-  int32_t* group_of;    // [B]
-  int32_t* group_bad;   // [G]
-  Segment* seg;         // [G + B], where they do not fit the shared memory
+  int32_t* lists;       // where they do not fit the shared memory: [G + 1] starts, [G] steps of
+                        // shared keys, [B] groups
+  Segment* seg;         // [G + B] likewise
   int4* seq_rec;        // [B]: {first tile of the group's segment or -1, its first row,
                         //       first tile of the sequence's, rows of the group; -1: out of bounds}
   int2* tile_rec;       // [tiles]: {pieces, cut at which the second one starts}
@@ -985,35 +985,45 @@ struct PrepArgs {
   int32_t* cl_start;    // [ncl + 1]
   int32_t* status;
 };
+constexpr size_t prep_lists(int64_t B, int64_t G) { return (size_t)(2 * G + 2 + B) * 4; }
 
-// Exclusive prefix sums over the block of three values a thread, and their totals.
-__device__ __forceinline__ void scan_three(int64_t* v, int64_t (*sums)[32], int64_t* total) {
+// Exclusive prefix sums over the block of tiles, steps and costs, one of each a thread; totals.
+__device__ __forceinline__ void scan_three(int& tiles, int64_t& steps, int& costs, int64_t (*sums)[3],
+                                           int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t up[3];
+  int up_t = tiles, up_c = costs;
+  int64_t up_s = steps;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    up[i] = v[i];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, up[i], o);
-      if (lane >= o) up[i] += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, up_t, o), c = __shfl_up_sync(0xffffffffu, up_c, o);
+    const int64_t x = __shfl_up_sync(0xffffffffu, up_s, o);
+    if (lane >= o) {
+      up_t += t;
+      up_c += c;
+      up_s += x;
     }
-    if (lane == 31) sums[i][warp] = up[i];
   }
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int64_t mine = sums[i][lane];
-    int64_t w = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += x;
-    }
-    total[i] = __shfl_sync(0xffffffffu, w, 31);
-    v[i] = up[i] - v[i] + __shfl_sync(0xffffffffu, w - mine, warp);
+  if (lane == 31) {
+    sums[warp][0] = up_t;
+    sums[warp][1] = up_s;
+    sums[warp][2] = up_c;
   }
   __syncthreads();
+  int64_t before[3] = {0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    total[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+      const int64_t x = sums[w][i];
+      if (w < warp) before[i] += x;
+      total[i] += x;
+    }
+  }
+  tiles = up_t - tiles + (int)before[0];
+  steps = up_s - steps + before[1];
+  costs = up_c - costs + (int)before[2];
 }
 
 // Last i in [0, n) with at(i) <= x (at ascends, at(0) <= x).
@@ -1027,32 +1037,43 @@ __device__ __forceinline__ int last_at_most(At at, int n, X x) {
   }
   return lo;
 }
+// x / y for 0 <= x, 0 < y, quotient below 2^24 (a float's error there is at most one).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  int64_t q = (int64_t)((float)x / (float)y);
+  if (q * y > x) --q;
+  if ((q + 1) * y <= x) ++q;
+  return q;
+}
 
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a) {
   extern __shared__ __align__(16) unsigned char prep_smem[];
-  __shared__ int64_t sums[3][32];
+  __shared__ int64_t sums[kPrepThreads / 32][3];
   __shared__ int cut_tile[kMaxClusters + 1], cut_step[kMaxClusters + 1], first[kMaxClusters + 1];
   griddep_launch_dependents();  // the attention kernel may start its set-up now
   const int tid = threadIdx.x, B = a.B, G = a.G, n_seg = G + B;
-  const bool fits = n_seg <= kFitSegments;
+  const bool fits = B <= kFitSequences;  // (G is at most B)
   Segment* seg = fits ? reinterpret_cast<Segment*>(prep_smem) : a.seg;
-  int32_t* group_of = fits ? reinterpret_cast<int32_t*>(seg + n_seg) : a.group_of;
-  int32_t* group_bad = fits ? group_of + B : a.group_bad;
+  int32_t* start = fits ? reinterpret_cast<int32_t*>(seg + n_seg) : a.lists;
+  int32_t* shared = start + G + 1;   // 64-key blocks of a group that are shared, -1: a bad group
+  int32_t* group_of = shared + G;
   // ---- groups: which are sound ----
   bool ok = true;
   for (int g = tid; g < G; g += kPrepThreads) {
     const int s = a.group_start[g], e = a.group_start[g + 1], n = a.shared_len[g];
     ok = ok && s >= 0 && s <= e && e <= B && (g > 0 || s == 0) && (g < G - 1 || e == B);
-    group_bad[g] = n < 0 || n > a.max_prefix || n > a.seq_cap;
+    start[g] = s;
+    if (g == G - 1) start[G] = e;
+    shared[g] = n < 0 || n > a.max_prefix || n > a.seq_cap ? -1 : n;
   }
   const bool groups = __syncthreads_and(ok) && G > 0;
   if (!ok) report(a.status, TV_ERR_BOUNDS);
   if (groups) {
     for (int b = tid; b < B; b += kPrepThreads) {
+      const int P = a.prefix_len[b];
       // (of groups that start at b, empty ones among them, the last)
-      const int g = last_at_most([&](int i) { return a.group_start[i]; }, G, b);
+      const int g = last_at_most([&](int i) { return start[i]; }, G, b);
       group_of[b] = g;
-      if (a.shared_len[g] > a.prefix_len[b]) atomicOr(&group_bad[g], 1);
+      if (shared[g] > P) atomicExch(&shared[g], -1);
     }
   }
   __syncthreads();
@@ -1060,25 +1081,24 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
   // Together where it saves more steps than the partial results cost: a tile of the group is a
   // piece more, and every sequence's tile becomes a partial result as well.
   auto shared_steps = [&](int g) {
-    if (!groups || group_bad[g]) return 0;
-    const int n = a.group_start[g + 1] - a.group_start[g];
-    const int64_t steps = (a.shared_len[g] / kBN + 1) / 2;
-    const int64_t tiles = ((int64_t)n * a.R + kRows - 1) / kRows;
-    return ((int64_t)n * a.T - tiles) * steps > piece_cost(kRows) * (tiles + 2) ? (int)steps : 0;
+    if (!groups || shared[g] < 0) return 0;
+    const int rows = (start[g + 1] - start[g]) * a.R, steps = (shared[g] / kBN + 1) / 2;
+    const int tiles = (rows + kRows - 1) / kRows, apart = (start[g + 1] - start[g]) * a.T;
+    return (int64_t)(apart - tiles) * steps > (int64_t)piece_cost(kRows) * (tiles + 2) ? steps : 0;
   };
   int64_t run[3] = {0, 0, 0};  // tiles, steps, costs so far
   for (int base = 0; base < n_seg; base += kPrepThreads) {
     const int i = base + tid;
     Segment s{};
-    int64_t v[3] = {0, 0, 0}, all[3];
+    int tiles = 0, costs = 0;
+    int64_t steps, all[3];
     if (i < G) {
       s.steps = shared_steps(i);
-      if (groups && group_bad[i]) report(a.status, TV_ERR_BOUNDS);
+      if (groups && shared[i] < 0) report(a.status, TV_ERR_BOUNDS);
       if (s.steps > 0) {
-        const int rows = (a.group_start[i + 1] - a.group_start[i]) * a.R;
-        s.nkeys = a.shared_len[i] / kBN * kBN;
-        v[0] = (rows + kRows - 1) / kRows;
-        v[2] = v[0] * piece_cost(kRows);
+        s.nkeys = shared[i] / kBN * kBN;
+        tiles = ((start[i + 1] - start[i]) * a.R + kRows - 1) / kRows;
+        costs = tiles * piece_cost(kRows);
       }
     } else if (i < n_seg) {
       const int b = i - G, P = a.prefix_len[b];
@@ -1086,25 +1106,36 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
         report(a.status, TV_ERR_BOUNDS);
       } else {
         const int g = groups ? group_of[b] : 0;
-        s.blk0 = groups && shared_steps(g) > 0 ? a.shared_len[g] / kBN : 0;
+        s.blk0 = shared_steps(g) > 0 ? shared[g] / kBN : 0;
         s.nkeys = P + a.Q - s.blk0 * kBN;
         s.steps = (s.nkeys + kStep - 1) / kStep;
-        v[0] = a.T;
-        v[2] = v[0] * piece_cost(min(a.R, kRows));
+        tiles = a.T;
+        costs = tiles * piece_cost(min(a.R, kRows));
       }
     }
-    v[1] = v[0] * s.steps;
-    scan_three(v, sums, all);
+    steps = (int64_t)tiles * s.steps;
+    scan_three(tiles, steps, costs, sums, all);
     if (i < n_seg) {
-      s.tile0 = (int)(run[0] + v[0]);
-      s.steps0 = run[1] + v[1];
-      s.cost0 = run[2] + v[2];
+      s.tile0 = (int)run[0] + tiles;
+      s.place = run[1] + steps;
+      s.cost0 = (int)run[2] + costs;
       seg[i] = s;
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) run[k] += all[k];
   }
   const int n_tiles = (int)run[0];
+  // the length of a run (see above), at least a few steps: with less work, fewer clusters
+  int64_t length;
+  {
+    const float c = (float)piece_cost(kRows), C = (float)a.ncl, w = (float)(run[1] + run[2]);
+    const float l = (w + sqrtf(w * w + 4.f * C * c * (float)run[1])) / (2.f * C);
+    length = (int64_t)(fmaxf(l, 2.f * c) * (float)kFixed) + 1;
+  }
+  const int64_t per_step = kFixed + (int64_t)((float)(piece_cost(kRows) * kFixed) * (float)kFixed / (float)length);
+  for (int i = tid; i < n_seg; i += kPrepThreads)  // (each thread its own)
+    seg[i].place = seg[i].place * per_step + (int64_t)seg[i].cost0 * kFixed;
+  const int64_t end = run[2] * kFixed + run[1] * per_step;
   __syncthreads();
   for (int b = tid; b < B; b += kPrepThreads) {
     const Segment& own = seg[G + b];
@@ -1113,34 +1144,24 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
       const int g = group_of[b];
       if (seg[g].steps > 0) {
         rec.x = seg[g].tile0;
-        rec.y = a.group_start[g] * a.R;
-        rec.w = (a.group_start[g + 1] - a.group_start[g]) * a.R;
+        rec.y = start[g] * a.R;
+        rec.w = (start[g + 1] - start[g]) * a.R;
       }
     }
     a.seq_rec[b] = rec;
   }
   // ---- cuts ----
-  // the length of a run (see above), at least a few steps: with less work, fewer clusters
-  int64_t length;
-  {
-    const float c = (float)piece_cost(kRows), C = (float)a.ncl, w = (float)(run[1] + run[2]);
-    const float l = (w + sqrtf(w * w + 4.f * C * c * (float)run[1])) / (2.f * C);
-    length = (int64_t)(fmaxf(l, 2.f * c) * (float)kFixed) + 1;
-  }
-  const int64_t per_step = kFixed + (int64_t)piece_cost(kRows) * kFixed * kFixed / length;
-  auto place = [&](int i) { return seg[i].cost0 * kFixed + seg[i].steps0 * per_step; };
-  const int64_t end = run[2] * kFixed + run[1] * per_step;
   for (int c = tid; c <= a.ncl; c += kPrepThreads) {
     int tile = n_tiles, step = 0;
     const int64_t at = c * length;
     if (at < end && c < a.ncl) {
       // (segments without tiles are as long as nothing: the last one at a place has tiles)
-      const int i = last_at_most(place, n_seg, at);
+      const int i = last_at_most([&](int x) { return seg[x].place; }, n_seg, at);
       const Segment& s = seg[i];
       const int64_t cost = (int64_t)piece_cost(i < G ? kRows : min(a.R, kRows)) * kFixed;
-      const int64_t len = s.steps * per_step + cost, in = at - place(i);
-      tile = s.tile0 + (int)(in / len);
-      step = (int)(max(in % len - cost, (int64_t)0) / per_step);
+      const int64_t len = s.steps * per_step + cost, in = at - s.place, t = quotient(in, len);
+      tile = s.tile0 + (int)t;
+      step = (int)quotient(max(in - t * len - cost, (int64_t)0), per_step);
       if (step < kMinPiece) {
         step = 0;
       } else if (s.steps - step < kMinPiece) {
@@ -1182,8 +1203,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
     const int i = last_at_most([&](int x) { return seg[x].tile0; }, n_seg, tile);
     const Segment s = seg[i];
     const bool group = i < G;
-    const int seq = group ? a.group_start[i] : i - G;
-    const int rows = group ? (a.group_start[i + 1] - seq) * a.R : a.R;
+    const int seq = group ? start[i] : i - G;
+    const int rows = group ? (start[i + 1] - seq) * a.R : a.R;
     const int s0 = j == 0 ? cut_step[c] : 0;
     const int s1 = tile == cut_tile[c + 1] ? cut_step[c + 1] : s.steps;
     if (s0 == 0) {  // the tile's first piece knows how many there are
@@ -1374,7 +1395,7 @@ int planned_clusters() {
 
 struct Layout {
   int64_t max_tiles, part_rows;
-  size_t group_of, group_bad, seg, seq_rec, tile_rec, items, cl_start, part_out, part_lse, total;
+  size_t lists, seg, seq_rec, tile_rec, items, cl_start, part_out, part_lse, total;
 };
 Layout layout(const tv_shared_args* a, int ncl) {
   const int64_t R = (int64_t)a->Q * a->H, B = a->B, G = a->G;
@@ -1388,8 +1409,7 @@ Layout layout(const tv_shared_args* a, int ncl) {
     n += (bytes + 255) / 256 * 256;
     return at;
   };
-  w.group_of = take(B * 4);
-  w.group_bad = take(G * 4);
+  w.lists = take(prep_lists(B, G));
   w.seg = take((G + B) * sizeof(Segment));
   w.seq_rec = take(B * 16);
   w.tile_rec = take(w.max_tiles * 8);
@@ -1435,16 +1455,15 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   pa.max_prefix = a->max_prefix_len;
   pa.ncl = ncl;
   pa.seq_cap = paged ? (int64_t)cache.max_pages * kBN : cache.kv_stride_b;
-  pa.group_of = (int32_t*)(base + w.group_of);
-  pa.group_bad = (int32_t*)(base + w.group_bad);
+  pa.lists = (int32_t*)(base + w.lists);
   pa.seg = (Segment*)(base + w.seg);
   pa.seq_rec = (int4*)(base + w.seq_rec);
   pa.tile_rec = (int2*)(base + w.tile_rec);
   pa.items = (int4*)(base + w.items);
   pa.cl_start = (int32_t*)(base + w.cl_start);
   pa.status = a->status;
-  const int n_seg = a->G + a->B;
-  const size_t prep_smem = n_seg <= kFitSegments ? n_seg * sizeof(Segment) + (a->B + a->G) * 4 : 0;
+  const size_t prep_smem =
+      a->B <= kFitSequences ? (a->G + a->B) * sizeof(Segment) + prep_lists(a->B, a->G) : 0;
   prepare_kernel<<<1, kPrepThreads, prep_smem, st>>>(pa);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
