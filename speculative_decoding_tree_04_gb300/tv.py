@@ -864,6 +864,26 @@ def rope(x, out, positions, layout=ROPE_HALF, rot_offset=0, rot_dim=None, scalin
     _call(dev, "tv_rope", ctypes.byref(a), _raw_stream(dev, stream))
 
 
+def _dense(name, t, dt, shape):
+    if t.shape != shape or t.dtype is not dt or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dt} of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _cache_rows(name, t, dt, d):
+    if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
+        raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
+    return t.data_ptr()
+
+
+def _cache_of(B, rows, page_table, page_size, kv_stride_b):
+    if page_table is None:
+        return CacheLayout(None, page_size, 0, kv_stride_b, rows)
+    most = page_table.shape[1]
+    return CacheLayout(_dense("page_table", page_table, torch.int32, (B, most)), page_size, most,
+                       0, rows)
+
+
 def norm_rope(q, kv, q_start, prefix_len, q_nope, q_pe, c_kv, k_pe, q_weight=None,
               kv_weight=None, k_weight=None, eps=1e-6, layout=ROPE_HALF, rot_dim=None,
               scaling=None, depth=None, page_table=None, page_size=64, kv_stride_b=0,
@@ -876,60 +896,45 @@ def norm_rope(q, kv, q_start, prefix_len, q_nope, q_pe, c_kv, k_pe, q_weight=Non
                      k_weight, depth, page_table, status)
     if q is None and kv is None:
         raise ValueError("neither q nor kv")
-    B, T = prefix_len.shape[0], (kv if q is None else q).shape[0]
-    dt = (kv if q is None else q).dtype
-    if q is None:
-        q_weight = None
-    if kv is None:
-        kv_weight = k_weight = None
+    x = kv if q is None else q
+    dt, T = x.dtype, x.shape[0]
+    B = prefix_len.shape[0]
     DR = (k_pe if q is None else q_pe).shape[-1]
-    H, DN, DL, q_st, kv_st, rows = 1, 0, 1, (0, 0), 0, 0
-    cache = CacheLayout(None, page_size, 0, kv_stride_b, 0)
+    H, DN, DL = 1, 0, 1
+    qp = qt = qh = nope = pe = qw = None
+    kp = kt = ck = kr = ckw = krw = cs = ks = None
     if q is not None:
-        H, DN = q.shape[1], q.shape[2] - DR
-        if q.stride(2) != 1:
+        _, H, d = q.shape
+        DN = d - DR
+        qt, qh, e = q.stride()
+        if e != 1:
             raise ValueError("innermost dimension of q must be contiguous")
-        q_st = (q.stride(0), q.stride(1))
-        outs = [("q_pe", q_pe, (T, H, DR))]
+        qp, pe = q.data_ptr(), _dense("q_pe", q_pe, dt, (T, H, DR))
         if DN > 0:
-            outs.append(("q_nope", q_nope, (T, H, DN)))
-        for name, t, shape in outs:
-            if t.shape != shape or t.dtype is not dt or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {dt} of shape {shape}")
+            nope = _dense("q_nope", q_nope, dt, (T, H, DN))
+        if q_weight is not None:
+            qw = _dense("q_weight", q_weight, dt, (d,))
     if kv is not None:
         DL = c_kv.shape[1]
-        if kv.shape != (T, DL + DR) or kv.stride(1) != 1 or kv.dtype is not dt:
+        kt, e = kv.stride()
+        if kv.shape != (T, DL + DR) or e != 1 or kv.dtype is not dt:
             raise ValueError(f"kv must be {dt} [{T}, {DL + DR}] with contiguous rows")
-        for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
-            if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
-                raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
-        kv_st, rows = kv.stride(0), min(c_kv.shape[0], k_pe.shape[0])
-        if page_table is not None:
-            _i32("page_table", page_table, (B, page_table.shape[1]))
-            cache = CacheLayout(page_table.data_ptr(), page_size, page_table.shape[1], 0, rows)
-        else:
-            cache = CacheLayout(None, page_size, 0, kv_stride_b, rows)
-    for name, w, d in (("q_weight", q_weight, DN + DR), ("kv_weight", kv_weight, DL),
-                       ("k_weight", k_weight, DR)):
-        if w is not None and (w.shape != (d,) or w.dtype is not dt or not w.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous {dt} of {d} elements")
-    _i32("q_start", q_start, (B + 1,))
-    _i32("prefix_len", prefix_len, (B,))
-    if depth is not None:
-        _i32("depth", depth, (T,))
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
+        kp, ck, kr = kv.data_ptr(), _cache_rows("c_kv", c_kv, dt, DL), \
+            _cache_rows("k_pe", k_pe, dt, DR)
+        cs, ks = c_kv.stride(0), k_pe.stride(0)
+        cache = _cache_of(B, min(c_kv.shape[0], k_pe.shape[0]), page_table, page_size, kv_stride_b)
+        if kv_weight is not None:
+            ckw = _dense("kv_weight", kv_weight, dt, (DL,))
+        if k_weight is not None:
+            krw = _dense("k_weight", k_weight, dt, (DR,))
+    else:
+        cache = CacheLayout(None, page_size, 0, kv_stride_b, 0)
     a = NormRopeArgs(ctypes.sizeof(NormRopeArgs), B, T, H, DN, DR, DL,
-                     DR if rot_dim is None else int(rot_dim), int(layout),
-                     _dt(kv if q is None else q), float(eps), ptr(q), q_st[0], q_st[1], ptr(kv), kv_st, ptr(q_weight),
-                     ptr(kv_weight), ptr(k_weight), q_start.data_ptr(), prefix_len.data_ptr(),
-                     ptr(depth), ptr(q_nope) if q is not None and DN > 0 else None,
-                     ptr(q_pe) if q is not None else None, ptr(c_kv) if kv is not None else None,
-                     ptr(k_pe) if kv is not None else None,
-                     c_kv.stride(0) if kv is not None else 0,
-                     k_pe.stride(0) if kv is not None else 0, cache,
-                     scaling or _plain_scaling, _status_arg(status))
+                     DR if rot_dim is None else rot_dim, layout, _dt(x), eps, qp, qt or 0, qh or 0,
+                     kp, kt or 0, qw, ckw, krw, _dense("q_start", q_start, torch.int32, (B + 1,)),
+                     _dense("prefix_len", prefix_len, torch.int32, (B,)),
+                     None if depth is None else _dense("depth", depth, torch.int32, (T,)), nope, pe,
+                     ck, kr, cs or 0, ks or 0, cache, scaling or _plain_scaling, _status_arg(status))
     _call(dev, "tv_norm_rope", ctypes.byref(a), _raw_stream(dev, stream))
 
 
@@ -937,44 +942,27 @@ def shared_args(q_latent, q_pe, c_kv, k_pe, prefix_len, group_start, shared_len,
                 max_prefix_len, anc=None, page_table=None, page_size=64, kv_stride_b=0,
                 status=None) -> SharedArgs:
     B, Q, H, DL = q_latent.shape
-    DR = q_pe.shape[3]
-    dt = q_latent.dtype
+    DR, dt = q_pe.shape[3], q_latent.dtype
     if dt is not torch.bfloat16:
         raise TypeError(f"shared_attn takes bfloat16 queries and cache, not {dt}")
-    for name, t, shape, want in (("q_latent", q_latent, (B, Q, H, DL), dt),
-                                 ("q_pe", q_pe, (B, Q, H, DR), dt),
-                                 ("out", out, (B, Q, H, DL), out.dtype)):
-        if t.shape != shape or t.dtype is not want or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {want} of shape {shape}")
-    for name, t, d in (("c_kv", c_kv, DL), ("k_pe", k_pe, DR)):
-        if t.dim() != 2 or t.shape[1] != d or t.stride(1) != 1 or t.dtype is not dt:
-            raise ValueError(f"{name} must be rows of {d} contiguous {dt}")
-    if lse is not None and (lse.shape != (B, Q, H) or lse.dtype is not torch.float32 or
-                            not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 of shape {(B, Q, H)}")
-    if anc is not None and (anc.shape != (B, Q) or not anc.is_contiguous() or
-                            anc.dtype not in (torch.int64, torch.uint64)):
-        raise ValueError(f"anc must be contiguous int64 of shape {(B, Q)}")
-    _i32("prefix_len", prefix_len, (B,))
-    G = 0
-    if group_start is not None:
-        G = group_start.shape[0] - 1
-        _i32("group_start", group_start, (G + 1,))
-        _i32("shared_len", shared_len, (G,))
-    rows = min(c_kv.shape[0], k_pe.shape[0])
-    if page_table is not None:
-        _i32("page_table", page_table, (B, page_table.shape[1]))
-        cache = CacheLayout(page_table.data_ptr(), page_size, page_table.shape[1], 0, rows)
-    else:
-        cache = CacheLayout(None, page_size, 0, kv_stride_b, rows)
-    return SharedArgs(ctypes.sizeof(SharedArgs), B, H, Q, DL, DR, float(scale), TV_BF16,
-                      _dt(out), q_latent.data_ptr(), q_pe.data_ptr(), c_kv.data_ptr(),
-                      k_pe.data_ptr(), c_kv.stride(0), k_pe.stride(0), cache,
-                      prefix_len.data_ptr(), int(max_prefix_len), G,
-                      group_start.data_ptr() if G else None,
-                      shared_len.data_ptr() if G else None,
-                      None if anc is None else anc.data_ptr(), out.data_ptr(),
-                      None if lse is None else lse.data_ptr(), _status_arg(status))
+    ql = _dense("q_latent", q_latent, dt, (B, Q, H, DL))
+    qp = _dense("q_pe", q_pe, dt, (B, Q, H, DR))
+    ck, kp = _cache_rows("c_kv", c_kv, dt, DL), _cache_rows("k_pe", k_pe, dt, DR)
+    if anc is not None and anc.dtype not in (torch.int64, torch.uint64):
+        raise ValueError("anc must be int64")
+    G, starts, lens = 0, None, None
+    if group_start is not None and shared_len is not None and shared_len.shape[0] > 0:
+        G = shared_len.shape[0]
+        starts = _dense("group_start", group_start, torch.int32, (G + 1,))
+        lens = _dense("shared_len", shared_len, torch.int32, (G,))
+    cache = _cache_of(B, min(c_kv.shape[0], k_pe.shape[0]), page_table, page_size, kv_stride_b)
+    return SharedArgs(ctypes.sizeof(SharedArgs), B, H, Q, DL, DR, scale, TV_BF16, _dt(out), ql, qp,
+                      ck, kp, c_kv.stride(0), k_pe.stride(0), cache,
+                      _dense("prefix_len", prefix_len, torch.int32, (B,)), max_prefix_len, G, starts,
+                      lens, None if anc is None else _dense("anc", anc, anc.dtype, (B, Q)),
+                      _dense("out", out, out.dtype, (B, Q, H, DL)),
+                      None if lse is None else _dense("lse", lse, torch.float32, (B, Q, H)),
+                      _status_arg(status))
 
 
 def shared_workspace_size(a: SharedArgs) -> int:
