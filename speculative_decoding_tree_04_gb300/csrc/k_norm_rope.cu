@@ -41,6 +41,7 @@ namespace tv {
 namespace {
 
 using namespace rope;
+using namespace ptx;
 
 constexpr int kMaxThreads = 256;
 constexpr int kMaxVecs = 4;  // 16-byte vectors of one head that a lane holds at most
@@ -133,34 +134,67 @@ struct Vec16<__nv_bfloat16> {
 // to the first output, the others to the second.
 struct Kind {
   int n, at, rot, split;
-  float eps;  // with a weight: the norm's
+  float eps, inv_n;  // with a weight: the norm's; 1 / n
 };
 
-// Where pair k's turn lies: a lane reads two turns of one vector's pairs at a time, and those that
-// the lanes read together are consecutive, so that no two of them meet in a bank.
+// The turns of one token's pairs in shared memory, as the vectors' lanes read them: those of one
+// vector in 16-byte pieces, and the pieces that the lanes read together consecutive, so that no two
+// of them meet in a bank.  Where there are no vectors (`half` pairs do not fill them) turns are
+// read one by one, in order.
 template <typename T>
-__device__ __forceinline__ int turn_slot(int k, int half, bool pairs) {
-  constexpr int N = Vec16<T>::N;
-  const int per = pairs ? N / 2 : N;  // pairs of one vector
-  if (half % per) return k;           // (no vectors: read one by one)
-  const int j = k % per;
-  return 2 * ((j / 2) * (half / per) + k / per) + (j & 1);
-}
-template <typename T>
-struct alignas(16) TwoTurns {
-  Turn<T> t[2];
+struct Turns;
+template <>
+struct Turns<float> {
+  Turn<float> t[1];  // half of them
+  __device__ static int slot(int k, int half, bool pairs) {
+    const int per = pairs ? 2 : 4;  // pairs of one vector
+    return half % per ? k : k % per * (half / per) + k / per;
+  }
+  static constexpr size_t bytes(int half) { return half * sizeof(Turn<float>); }
+  __device__ void set(int k, int half, bool pairs, const Turn<float>& x) { t[slot(k, half, pairs)] = x; }
+  __device__ Turn<float> get(int k, int half, bool pairs) const { return t[slot(k, half, pairs)]; }
 };
+// bf16: (cos, cos, sin, sin) of two pairs whose elements lie in the same halves of neighbouring
+// words, for packed arithmetic.
+template <>
+struct Turns<__nv_bfloat16> {
+  float f[4];
+  __device__ static int slot(int k, int half, bool pairs) {
+    if (half % (pairs ? 4 : 8)) return 4 * (k / 2) + (k & 1);
+    // pairs: pair j of a vector is word j.  half layout: the vector's elements 2 j and 2 j + 1
+    const int j = pairs ? k & 3 : k & 7, v = pairs ? k >> 2 : k >> 3, n = pairs ? half >> 2 : half >> 3;
+    const int word = pairs ? j : j >> 1, piece = pairs ? word >> 1 : 2 * (word >> 1) + (j & 1);
+    return 4 * (piece * n + v) + (word & 1);
+  }
+  static constexpr size_t bytes(int half) { return (half + 1) / 2 * 16; }
+  __device__ void set(int k, int half, bool pairs, const Turn<__nv_bfloat16>& x) {
+    float* at = f + slot(k, half, pairs);
+    at[0] = x.c;
+    at[2] = x.s;
+  }
+  __device__ Turn<__nv_bfloat16> get(int k, int half, bool pairs) const {
+    const float* at = f + slot(k, half, pairs);
+    return {at[0], at[2]};
+  }
+};
+template <typename T>
+__device__ __forceinline__ const Turns<T>* turns_of(const unsigned char* all, int token, int half) {
+  return reinterpret_cast<const Turns<T>*>(all + token * Turns<T>::bytes(half));
+}
 
 // A head in 16-byte pieces by the `width` lanes of a group (lane `l` of it, vectors l, l + width,
-// ..).  Loads first, then, by `finish`, the norm, the rotation and the stores.
-template <typename T, int NV>
-struct Held {
+// ..).  Loads first, then, by `finish`, the norm, the rotation and the stores.  `other` holds the
+// partners in the half layout; kSwap: they are `swap` lanes away instead (or in the same vector).
+template <typename T, int NV, bool kSwap>
+struct Held;
+
+template <int NV, bool kSwap>
+struct Held<float, NV, kSwap> {
   uint4 own[NV], other[NV];
-  __device__ __forceinline__ void load(const T* src, const Kind& k, bool pairs, bool on, int l, int width) {
-    constexpr int N = Vec16<T>::N;
+  __device__ __forceinline__ void load(const float* src, const Kind& k, bool pairs, bool on, int l, int width) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (l + i * width) * N;
+      const int e = (l + i * width) * 4;
       if (!on || e >= k.n) continue;
       own[i] = *reinterpret_cast<const uint4*>(src + e);
       if (!pairs && e >= k.at && e < k.at + k.rot) {
@@ -170,69 +204,192 @@ struct Held {
     }
   }
   // w: the norm's weights, null for none (the same for a whole warp, whose lanes meet in the sum).
-  __device__ __forceinline__ void finish(T* low, T* high, const Kind& k, bool pairs, const T* w, bool on,
-                                         int l, int width, const Turn<T>* turns) {
-    constexpr int N = Vec16<T>::N;
+  __device__ __forceinline__ void finish(float* low, float* high, const Kind& k, bool pairs, int,
+                                         const float* w, bool on, int l, int width,
+                                         const Turns<float>* turns) {
     const int half = k.rot / 2;
     float r = 1.f;
     if (w) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (!on || (l + i * width) * N >= k.n) continue;
-        float x[N];
-        Vec16<T>::unpack(own[i], x);
+        if (!on || (l + i * width) * 4 >= k.n) continue;
+        float x[4];
+        Vec16<float>::unpack(own[i], x);
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum = fmaf(x[j], x[j], sum);
+        for (int j = 0; j < 4; ++j) sum = fmaf(x[j], x[j], sum);
       }
       for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       r = 1.f / sqrtf(sum / (float)k.n + k.eps);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = (l + i * width) * N;
+      const int e = (l + i * width) * 4;
       if (!on || e >= k.n) continue;
-      float x[N];
-      Vec16<T>::unpack(own[i], x);
+      float x[4];
+      Vec16<float>::unpack(own[i], x);
       if (w) {
-        float f[N];
-        Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4*>(w + e)), f);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = x[j] * r * f[j];
+        for (int j = 0; j < 4; ++j) x[j] = x[j] * r * __ldg(w + e + j);
       }
       if (e >= k.at && e < k.at + k.rot) {
         const int q = e - k.at;
-        const TwoTurns<T>* two = reinterpret_cast<const TwoTurns<T>*>(turns);
         if (pairs) {
-          const int step = half / (N / 2), v = q / N;
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j) {
-            const Turn<T>& t = two[(j / 2) * step + v].t[j & 1];
+          for (int j = 0; j < 2; ++j) {
+            const Turn<float>& t = turns->t[j * (half / 2) + q / 4];
             const float a = x[2 * j], b = x[2 * j + 1];
             x[2 * j] = t.out(a, b);
             x[2 * j + 1] = t.out(b, -a);
           }
         } else {
           const bool first = q < half;
-          const int step = half / N, v = (first ? q : q - half) / N;
-          float y[N];
-          Vec16<T>::unpack(other[i], y);
+          const int v = (first ? q : q - half) / 4;
+          float y[4];
+          Vec16<float>::unpack(other[i], y);
           if (w) {
-            float f[N];
-            Vec16<T>::unpack(
-                __ldg(reinterpret_cast<const uint4*>(w + (first ? e + half : e - half))), f);
 #pragma unroll
-            for (int j = 0; j < N; ++j) y[j] = y[j] * r * f[j];
+            for (int j = 0; j < 4; ++j) y[j] = y[j] * r * __ldg(w + (first ? e + half : e - half) + j);
           }
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const Turn<T>& t = two[(j / 2) * step + v].t[j & 1];
-            x[j] = t.out(x[j], first ? y[j] : -y[j]);
+          for (int j = 0; j < 4; ++j)
+            x[j] = turns->t[j * (half / 4) + v].out(x[j], first ? y[j] : -y[j]);
+        }
+      }
+      *reinterpret_cast<uint4*>(e < k.split ? low + e : high + (e - k.split)) = Vec16<float>::pack(x);
+    }
+  }
+};
+
+// Eight bf16 as four pairs of floats for packed arithmetic: {elements 0 and 2, 1 and 3, 4 and 6, 5
+// and 7} (the same halves of neighbouring words).
+__device__ __forceinline__ void unpack_pairs(const uint4& u, uint64_t* x) {
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = f2_pack(__uint_as_float(v[2 * i] << 16), __uint_as_float(v[2 * i + 1] << 16));
+    x[2 * i + 1] =
+        f2_pack(__uint_as_float(v[2 * i] & 0xffff0000u), __uint_as_float(v[2 * i + 1] & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t* x) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a0, a1, b0, b1;
+    f2_unpack(x[2 * i], a0, a1);
+    f2_unpack(x[2 * i + 1], b0, b1);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a0, b0), q = __floats2bfloat162_rn(a1, b1);
+    v[2 * i] = *reinterpret_cast<const uint32_t*>(&p);
+    v[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&q);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint64_t f2_swap_lanes(uint64_t x, int lanes) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(__shfl_xor_sync(0xffffffffu, a, lanes), __shfl_xor_sync(0xffffffffu, b, lanes));
+}
+
+template <int NV, bool kSwap>
+struct Held<__nv_bfloat16, NV, kSwap> {
+  using T = __nv_bfloat16;
+  uint4 own[NV], other[kSwap ? 1 : NV];
+  __device__ __forceinline__ void load(const T* src, const Kind& k, bool pairs, bool on, int l, int width) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (l + i * width) * 8;
+      own[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!on || e >= k.n) continue;
+      own[i] = *reinterpret_cast<const uint4*>(src + e);
+      if (!kSwap && !pairs && e >= k.at && e < k.at + k.rot) {
+        const int half = k.rot / 2;
+        other[i] = *reinterpret_cast<const uint4*>(src + (e < k.at + half ? e + half : e - half));
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(T* low, T* high, const Kind& k, bool pairs, int swap, const T* w,
+                                         bool on, int l, int width, const Turns<T>* turns) {
+    const int half = k.rot / 2;
+    uint64_t r2 = 0;
+    if (w) {
+      uint64_t s2 = f2_pack(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        uint64_t x[4];
+        unpack_pairs(own[i], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2 = f2_fma(x[j], x[j], s2);
+      }
+      float s0, s1;
+      f2_unpack(s2, s0, s1);
+      float sum = s0 + s1;
+      for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float mean = fmaf(sum, k.inv_n, k.eps);
+      float r = rsqrtf(mean);                        // and a step of Newton's iteration
+      r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.f), r);
+      // (a mean of 0, its square root infinite, or past the step's range: the plain value)
+      if (!(mean > 1e-30f && mean < 1e30f)) r = 1.f / sqrtf(mean);
+      r2 = f2_pack(r, r);
+    }
+    const int at = k.at, end = k.at + k.rot;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (l + i * width) * 8;
+      const bool valid = on && e < k.n;
+      uint64_t x[4];
+      unpack_pairs(own[i], x);
+      if (w) {
+        uint64_t f[4];
+        unpack_pairs(valid ? __ldg(reinterpret_cast<const uint4*>(w + e)) : make_uint4(0u, 0u, 0u, 0u), f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = f2_mul(f2_mul(x[j], r2), f[j]);
+      }
+      // (a vector of the warp's is rotated: where lanes swap, all of them take part)
+      if (i * width * 8 < end && (i + 1) * width * 8 > at) {
+        const bool turned = valid && e >= at && e < end;
+        const int q = e - at;
+        if (pairs) {
+          if (turned) {
+            const float4* t = reinterpret_cast<const float4*>(turns->f) + (q >> 3);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 cs = t[j * (half >> 2)];
+              const uint64_t c = f2_pack(cs.x, cs.y), sn = f2_pack(cs.z, cs.w),
+                             neg = f2_pack(-cs.z, -cs.w);
+              const uint64_t a = x[2 * j], b = x[2 * j + 1];
+              x[2 * j] = f2_fma(a, c, f2_mul(b, neg));
+              x[2 * j + 1] = f2_fma(b, c, f2_mul(a, sn));
+            }
+          }
+        } else {
+          const bool first = q < half;
+          uint64_t y[4];
+          if (kSwap) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = f2_swap_lanes(x[j], swap);
+          } else if (turned) {
+            unpack_pairs(other[i], y);
+            if (w) {
+              uint64_t f[4];
+              unpack_pairs(__ldg(reinterpret_cast<const uint4*>(w + (first ? e + half : e - half))), f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = f2_mul(f2_mul(y[j], r2), f[j]);
+            }
+          }
+          if (turned) {
+            const float4* t = reinterpret_cast<const float4*>(turns->f) + ((first ? q : q - half) >> 3);
+            const float sg = first ? -1.f : 1.f;
+            const uint64_t sign = f2_pack(sg, sg);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 cs = t[j * (half >> 3)];
+              x[j] = f2_fma(x[j], f2_pack(cs.x, cs.y), f2_mul(f2_mul(y[j], sign), f2_pack(cs.z, cs.w)));
+            }
           }
         }
       }
-      T* dst = e < k.split ? low + e : high + (e - k.split);
-      *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(x);
+      if (valid) *reinterpret_cast<uint4*>(e < k.split ? low + e : high + (e - k.split)) = pack_pairs(x);
     }
   }
 };
@@ -241,7 +398,7 @@ struct Held {
 // reads both elements of a pair before it writes either, so the vector may be turned in place.
 template <typename T>
 __device__ void one_by_one(const T* src, T* low, T* high, const T* w, const Kind& k, bool pairs,
-                           const Turn<T>* turns, int lane) {
+                           const Turns<T>* turns, int lane) {
   float r = 1.f;
   if (w) {
     float sum = 0.f;
@@ -263,7 +420,7 @@ __device__ void one_by_one(const T* src, T* low, T* high, const T* w, const Kind
   for (int i = lane; i < half; i += 32) {
     const int ea = k.at + (pairs ? 2 * i : i), eb = pairs ? ea + 1 : ea + half;
     const float a = get(ea), b = get(eb);
-    const Turn<T> t = turns[turn_slot<T>(i, half, pairs)];
+    const Turn<T> t = turns->get(i, half, pairs);
     put(ea, t.out(a, b));
     put(eb, t.out(b, -a));
   }
@@ -283,47 +440,60 @@ struct Heads {
 
 // Turns the list with all of the block's warps.  `ready` is called once by every thread, between
 // the first loads and their use; on[i] then says whether token t0 + i takes part, and its turns
-// start at turns + i * half.
-template <typename T, int NV, typename Ready>
+// are the i-th.
+template <typename T, int NV, bool kSwap, typename Ready>
 __device__ __forceinline__ void turn_heads(const Heads<T>& hd, const Kind& k, bool pairs, int width,
-                                           const Turn<T>* turns, const bool* on, Ready ready) {
+                                           int swap, const unsigned char* turns, const bool* on, Ready ready) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int half = k.rot / 2, n = hd.nh * hd.nt;
-  auto src = [&](int i, int h) { return hd.src + (hd.t0 + i) * hd.token + (hd.h0 + h) * hd.stride; };
-  auto low = [&](int i, int h) { return hd.low + (hd.t0 + i) * hd.low_token + (hd.h0 + h) * hd.low_stride; };
-  auto high = [&](int i, int h) { return hd.high + (hd.t0 + i) * hd.high_token + (hd.h0 + h) * hd.high_stride; };
+  const T* src0 = hd.src + hd.t0 * hd.token + hd.h0 * hd.stride;
+  T* low0 = hd.low + hd.t0 * hd.low_token + hd.h0 * hd.low_stride;
+  T* high0 = hd.high + hd.t0 * hd.high_token + hd.h0 * hd.high_stride;
+  auto src = [&](int i, int h) { return src0 + i * hd.token + h * hd.stride; };
+  auto low = [&](int i, int h) { return low0 + i * hd.low_token + h * hd.low_stride; };
+  auto high = [&](int i, int h) { return high0 + i * hd.high_token + h * hd.high_stride; };
   if (width == 0) {
     ready();
     for (int q = warp; q < n; q += nw) {
       const int i = q / hd.nh, h = q - i * hd.nh;
-      if (on[i]) one_by_one<T>(src(i, h), low(i, h), high(i, h), hd.w, k, pairs, turns + i * half, lane);
+      if (on[i])
+        one_by_one<T>(src(i, h), low(i, h), high(i, h), hd.w, k, pairs, turns_of<T>(turns, i, half), lane);
     }
     return;
   }
   const int groups = 32 / width, l = lane & (width - 1), g = lane / width;
   constexpr int kHold = NV == 1 ? 4 : NV == 2 ? 2 : 1;  // heads of a group on their way at once
-  Held<T, NV> held[kHold];
+  Held<T, NV, kSwap> held[kHold];
   const int step = nw * groups;
-  bool first = true;
-  // (the bound is the same for a whole warp: its lanes meet in the norm's shuffles)
-  for (int q0 = warp * groups; first || q0 < n; q0 += kHold * step) {
-    int ti[kHold], hi[kHold];
+  int ti[kHold], hi[kHold];
 #pragma unroll
-    for (int u = 0; u < kHold; ++u) {
-      const int q = q0 + u * step + g;
-      ti[u] = q / hd.nh;
-      hi[u] = q - ti[u] * hd.nh;
-      held[u].load(src(ti[u], hi[u]), k, pairs, q < n, l, width);
-    }
+  for (int u = 0; u < kHold; ++u) {
+    const int q = warp * groups + u * step + g;
+    ti[u] = q / hd.nh;
+    hi[u] = q - ti[u] * hd.nh;
+  }
+  bool first = true;
+  // (the bound is the same for a whole warp: its lanes meet in shuffles)
+  for (int q0 = warp * groups; first || q0 < n; q0 += kHold * step) {
+#pragma unroll
+    for (int u = 0; u < kHold; ++u)
+      held[u].load(src(ti[u], hi[u]), k, pairs, q0 + u * step + g < n, l, width);
     if (first) ready();
     first = false;
     __syncwarp();  // in place: every lane's loads come before any lane's stores
 #pragma unroll
     for (int u = 0; u < kHold; ++u) {
-      if (q0 + u * step >= n) continue;
-      const bool is = q0 + u * step + g < n && on[ti[u]];
-      held[u].finish(low(ti[u], hi[u]), high(ti[u], hi[u]), k, pairs, hd.w, is, l, width,
-                     turns + ti[u] * half);
+      if (q0 + u * step < n) {
+        const bool is = q0 + u * step + g < n && on[ti[u]];
+        held[u].finish(low(ti[u], hi[u]), high(ti[u], hi[u]), k, pairs, swap, hd.w, is, l, width,
+                       turns_of<T>(turns, ti[u], half));
+      }
+      // the next head of this lane's
+      hi[u] += kHold * step;
+      while (hi[u] >= hd.nh) {
+        hi[u] -= hd.nh;
+        ++ti[u];
+      }
     }
   }
 }
@@ -332,11 +502,13 @@ constexpr int kMaxTokens = 8;  // of a block
 
 // Angles of the block's tokens, all at once.
 template <typename T>
-__device__ __forceinline__ void make_turns(Turn<T>* turns, const double* pos, const bool* on, int nt,
+__device__ __forceinline__ void make_turns(unsigned char* turns, const double* pos, const bool* on, int nt,
                                            int half, bool pairs, const InvFreq& inv, double mag) {
   for (int x = threadIdx.x; x < nt * half; x += blockDim.x) {
     const int i = x / half, k = x - i * half;
-    if (on[i]) turns[i * half + turn_slot<T>(k, half, pairs)] = Turn<T>::make(__dmul_rn(pos[i], inv.v[k]), mag);
+    if (on[i])
+      const_cast<Turns<T>*>(turns_of<T>(turns, i, half))
+          ->set(k, half, pairs, Turn<T>::make(__dmul_rn(pos[i], inv.v[k]), mag));
   }
 }
 
@@ -346,27 +518,26 @@ struct RopeParams {
   int64_t in_token, in_head, out_token, out_head;
   int T, heads, per_block, tokens;
   Kind kind;
-  int pairs, width;
+  int pairs, width, swap;
   const int32_t* positions;
   double sign, mag;
 };
 
-template <typename T, int NV>
+template <typename T, int NV, bool kSwap>
 __global__ void __launch_bounds__(kMaxThreads)
     rope_kernel(const RopeParams p, const __grid_constant__ InvFreq inv) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(16) unsigned char turns[];
   __shared__ double pos[kMaxTokens];
   __shared__ bool on[kMaxTokens];
-  Turn<T>* turns = reinterpret_cast<Turn<T>*>(smem);
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
   const int nt = (int)min((int64_t)p.tokens, p.T - t0);
   const int h0 = (int)blockIdx.y * p.per_block, nh = min(p.per_block, p.heads - h0);
   const Heads<T> hd{(const T*)p.in, (T*)p.out,   (T*)p.out,  nullptr,     p.in_token, p.in_head,
                     p.out_token,    p.out_head, p.out_token, p.out_head, t0,          h0,
                     nh,             nt};
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  turn_heads<T, NV>(hd, p.kind, p.pairs, p.width, turns, on, [&]() {
+  griddep_wait();
+  griddep_launch_dependents();
+  turn_heads<T, NV, kSwap>(hd, p.kind, p.pairs, p.width, p.swap, turns, on, [&]() {
     if (threadIdx.x < nt) {
       pos[threadIdx.x] = (double)p.positions[t0 + threadIdx.x] * p.sign;
       on[threadIdx.x] = true;
@@ -384,7 +555,7 @@ struct NormRopeParams {
   int64_t nope_token, nope_head, pe_token, pe_head;
   int T, B, H, per_block, tokens;
   Kind q_kind, c_kind, k_kind;
-  int pairs, q_width, c_vec, k_vec;
+  int pairs, q_width, q_swap, c_vec, k_vec;
   CacheGeom cache;
   int64_t num_rows;
   const int32_t* q_start;
@@ -412,11 +583,10 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ q_start, 
   return lo - 1;
 }
 
-template <typename T, int NV>
+template <typename T, int NV, bool kSwap>
 __global__ void __launch_bounds__(kMaxThreads, 3)
     norm_rope_kernel(const NormRopeParams p, const __grid_constant__ InvFreq inv) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  Turn<T>* turns = reinterpret_cast<Turn<T>*>(smem);
+  extern __shared__ __align__(16) unsigned char turns[];
   __shared__ int64_t rows[kMaxTokens];  // the tokens' cache rows, -1: none
   __shared__ double pos[kMaxTokens];
   __shared__ bool on[kMaxTokens];
@@ -428,8 +598,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
   const Heads<T> hd{(const T*)p.q, (T*)p.q_nope, (T*)p.q_pe,  (const T*)p.q_w, p.q_token, p.q_head,
                     p.nope_token,  p.nope_head,  p.pe_token, p.pe_head,       t0,        h0,
                     max(nh, 1),    nh > 0 ? nt : 0};
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
+  griddep_wait();
+  griddep_launch_dependents();
   auto ready = [&]() {
     for (int i = warp; i < nt; i += nw) {
       const int64_t t = t0 + i;
@@ -466,7 +636,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     make_turns<T>(turns, pos, on, nt, p.k_kind.rot / 2, p.pairs, inv, p.mag);
     __syncthreads();
   };
-  turn_heads<T, NV>(hd, p.q_kind, p.pairs, p.q_width, turns, on, ready);
+  turn_heads<T, NV, kSwap>(hd, p.q_kind, p.pairs, p.q_width, p.q_swap, turns, on, ready);
   if (!keys) return;
   // the tokens' latent rows and rope parts, a warp each
   const int half = p.k_kind.rot / 2;
@@ -479,11 +649,11 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     const T* src = (const T*)p.kv + (t0 + i) * p.kv_token + (latent ? 0 : p.c_kind.n);
     T* dst = latent ? (T*)p.c_kv + row * p.ckv_row : (T*)p.k_pe + row * p.kpe_row;
     const T* w = (const T*)(latent ? p.kv_w : p.k_w);
-    const Turn<T>* tt = turns + i * half;
+    const Turns<T>* tt = turns_of<T>(turns, i, half);
     if (latent ? p.c_vec : p.k_vec) {
-      Held<T, kMaxVecs> held;
+      Held<T, kMaxVecs, false> held;
       held.load(src, k, p.pairs, true, lane, 32);
-      held.finish(dst, dst, k, p.pairs, w, true, lane, 32, tt);
+      held.finish(dst, dst, k, p.pairs, 0, w, true, lane, 32, tt);
     } else {
       one_by_one<T>(src, dst, dst, w, k, p.pairs, tt, lane);
     }
@@ -514,16 +684,29 @@ int lanes_for(const Kind& k, bool pairs, int vecs, int* per_lane) {
   return best;
 }
 
+// How many lanes away the partners of a rotated part are, if one exchange of lanes brings them (1
+// where they are in the lane's own vector), else 0: the part lies in one of a lane's vectors, at a
+// multiple of its size, a power of two.
+template <typename T>
+int swap_lanes(const Kind& k, bool pairs, int width) {
+  constexpr int N = Vec16<T>::N;
+  if (sizeof(T) == 4 || width == 0) return 0;
+  if (pairs) return 1;
+  const int at = k.at / N, n = k.rot / N;
+  if ((n & (n - 1)) || at % n || at / width != (at + n - 1) / width) return 0;
+  return n / 2;
+}
+
 // Tokens and heads per block, and threads.  `fit` blocks of 256 threads fit an SM: a block takes as
 // many tokens as fill the GPU once (eight at most), and where the tokens are fewer than two per SM
 // their heads go to several blocks.
 struct Grid {
   int tokens, per_block, groups, threads;
 };
-Grid grid_for(int64_t tokens, int heads, int per_warp, int half, int turn_bytes, int fit) {
+Grid grid_for(int64_t tokens, int heads, int per_warp, int turn_bytes, int fit) {
   const int64_t sms = current_sm_count();
   Grid s;
-  const int room = std::max(1, 16384 / (half * turn_bytes));  // 16 KB of turns
+  const int room = std::max(1, 16384 / turn_bytes);  // 16 KB of turns
   s.tokens = (int)std::min<int64_t>(std::min(kMaxTokens, room), (tokens + fit * sms - 1) / (fit * sms));
   const int64_t want = 2 * sms;
   const int groups =
@@ -582,12 +765,12 @@ cudaError_t launch_rope_t(const tv_rope_args* a, cudaStream_t st) {
   p.out_token = a->out_stride_token;
   p.out_head = a->out_stride_head;
   p.heads = a->n_heads;
-  p.kind = {a->d_head, a->rot_offset, a->rot_dim, a->d_head, 0.f};
+  p.kind = {a->d_head, a->rot_offset, a->rot_dim, a->d_head, 0.f, 0.f};
   const bool in_place = a->in == a->out;
   if (in_place) {  // the elements outside the rotated part are there already
     p.in = (const T*)a->in + a->rot_offset;
     p.out = (T*)a->out + a->rot_offset;
-    p.kind = {a->rot_dim, 0, a->rot_dim, a->rot_dim, 0.f};
+    p.kind = {a->rot_dim, 0, a->rot_dim, a->rot_dim, 0.f, 0.f};
   }
   p.pairs = a->layout == TV_ROPE_INTERLEAVED;
   int vecs = 1;
@@ -595,20 +778,27 @@ cudaError_t launch_rope_t(const tv_rope_args* a, cudaStream_t st) {
   if (!(fits<T>(p.in) && fits<T>(p.out) && p.in_token % N == 0 && p.in_head % N == 0 &&
         p.out_token % N == 0 && p.out_head % N == 0))
     p.width = 0;
+  p.swap = swap_lanes<T>(p.kind, p.pairs, p.width);
   p.T = a->T;
   p.positions = a->positions;
   p.sign = a->inverse ? -1.0 : 1.0;
   const InvFreq& inv = table_of(a->scaling, a->rot_dim, &p.mag);
-  const Grid s = grid_for(a->T, a->n_heads, p.width ? 32 / p.width : 1, a->rot_dim / 2, sizeof(Turn<T>), 4);
+  const Grid s = grid_for(a->T, a->n_heads, p.width ? 32 / p.width : 1, (int)Turns<T>::bytes(a->rot_dim / 2), 4);
   p.per_block = s.per_block;
   p.tokens = s.tokens;
   const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
-  const size_t smem = sizeof(Turn<T>) * (a->rot_dim / 2) * s.tokens;
+  const size_t smem = Turns<T>::bytes(a->rot_dim / 2) * s.tokens;
   auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
-  return vecs == 1   ? go(rope_kernel<T, 1>)
-         : vecs == 2 ? go(rope_kernel<T, 2>)
-         : vecs == 3 ? go(rope_kernel<T, 3>)
-                     : go(rope_kernel<T, 4>);
+  if constexpr (sizeof(T) == 2)
+    if (p.swap > 0)
+      return vecs == 1   ? go(rope_kernel<T, 1, true>)
+             : vecs == 2 ? go(rope_kernel<T, 2, true>)
+             : vecs == 3 ? go(rope_kernel<T, 3, true>)
+                         : go(rope_kernel<T, 4, true>);
+  return vecs == 1   ? go(rope_kernel<T, 1, false>)
+         : vecs == 2 ? go(rope_kernel<T, 2, false>)
+         : vecs == 3 ? go(rope_kernel<T, 3, false>)
+                     : go(rope_kernel<T, 4, false>);
 }
 
 template <typename T>
@@ -636,15 +826,16 @@ cudaError_t launch_norm_rope_t(const tv_norm_rope_args* a, cudaStream_t st) {
   p.T = a->T;
   p.B = a->B;
   p.H = a->q ? a->H : 0;
-  p.q_kind = {a->d_nope + a->d_rope, a->d_nope, a->rot_dim, a->d_nope, a->eps};
-  p.c_kind = {a->d_latent, 0, 0, a->d_latent, a->eps};
-  p.k_kind = {a->d_rope, 0, a->rot_dim, a->d_rope, a->eps};
+  p.q_kind = {a->d_nope + a->d_rope, a->d_nope, a->rot_dim, a->d_nope, a->eps, 1.f / (float)(a->d_nope + a->d_rope)};
+  p.c_kind = {a->d_latent, 0, 0, a->d_latent, a->eps, 1.f / (float)a->d_latent};
+  p.k_kind = {a->d_rope, 0, a->rot_dim, a->d_rope, a->eps, 1.f / (float)a->d_rope};
   p.pairs = a->layout == TV_ROPE_INTERLEAVED;
   int vecs = 1, kv_vecs;
   p.q_width = a->q ? lanes_for<T>(p.q_kind, p.pairs, kMaxVecs, &vecs) : 0;
   if (!(fits<T>(a->q) && fits<T>(a->q_nope) && fits<T>(a->q_pe) && fits<T>(a->q_weight) &&
         p.q_token % N == 0 && p.q_head % N == 0))
     p.q_width = 0;
+  p.q_swap = swap_lanes<T>(p.q_kind, p.pairs, p.q_width);
   const bool kv_ok = fits<T>(a->kv) && p.kv_token % N == 0 && a->d_latent % N == 0;
   p.c_vec = lanes_for<T>(p.c_kind, true, kMaxVecs, &kv_vecs) && kv_ok && fits<T>(a->c_kv) &&
             p.ckv_row % N == 0 && fits<T>(a->kv_weight);
@@ -657,16 +848,22 @@ cudaError_t launch_norm_rope_t(const tv_norm_rope_args* a, cudaStream_t st) {
   p.depth = a->depth;
   p.status = a->status;
   const InvFreq& inv = table_of(a->scaling, a->rot_dim, &p.mag);
-  const Grid s = grid_for(a->T, p.H, p.q_width ? 32 / p.q_width : 1, a->rot_dim / 2, sizeof(Turn<T>), 3);
+  const Grid s = grid_for(a->T, p.H, p.q_width ? 32 / p.q_width : 1, (int)Turns<T>::bytes(a->rot_dim / 2), 3);
   p.per_block = s.per_block;
   p.tokens = s.tokens;
   const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
-  const size_t smem = sizeof(Turn<T>) * (a->rot_dim / 2) * s.tokens;
+  const size_t smem = Turns<T>::bytes(a->rot_dim / 2) * s.tokens;
   auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
-  return vecs == 1   ? go(norm_rope_kernel<T, 1>)
-         : vecs == 2 ? go(norm_rope_kernel<T, 2>)
-         : vecs == 3 ? go(norm_rope_kernel<T, 3>)
-                     : go(norm_rope_kernel<T, 4>);
+  if constexpr (sizeof(T) == 2)
+    if (p.q_swap > 0)
+      return vecs == 1   ? go(norm_rope_kernel<T, 1, true>)
+             : vecs == 2 ? go(norm_rope_kernel<T, 2, true>)
+             : vecs == 3 ? go(norm_rope_kernel<T, 3, true>)
+                         : go(norm_rope_kernel<T, 4, true>);
+  return vecs == 1   ? go(norm_rope_kernel<T, 1, false>)
+         : vecs == 2 ? go(norm_rope_kernel<T, 2, false>)
+         : vecs == 3 ? go(norm_rope_kernel<T, 3, false>)
+                     : go(norm_rope_kernel<T, 4, false>);
 }
 
 }  // namespace
