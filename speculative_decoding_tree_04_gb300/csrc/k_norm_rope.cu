@@ -462,7 +462,8 @@ __device__ __forceinline__ void turn_heads(const Heads<T>& hd, const Kind& k, bo
     return;
   }
   const int groups = 32 / width, l = lane & (width - 1), g = lane / width;
-  constexpr int kHold = NV == 1 ? 4 : NV == 2 ? 2 : 1;  // heads of a group on their way at once
+  // heads of a group on their way at once (float32 rotations are long: fewer copies of them)
+  constexpr int kHold = sizeof(T) == 4 ? (NV == 1 ? 2 : 1) : NV == 1 ? 4 : NV == 2 ? 2 : 1;
   Held<T, NV, kSwap> held[kHold];
   const int step = nw * groups;
   int ti[kHold], hi[kHold];
