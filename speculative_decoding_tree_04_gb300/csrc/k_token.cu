@@ -153,9 +153,14 @@ __device__ __noinline__ uint4 end_vector(const T* x, int64_t V, int64_t a) {
   for (int i = 0; i < N; ++i) v[i] = a + i >= 0 && a + i < V ? x[a + i] : (T)-INFINITY;
   return *reinterpret_cast<const uint4*>(v);
 }
-// One exact weight, out of line too.
-__device__ __noinline__ int64_t one_weight(float v, float m, float ch, float cl, const PairTable& table) {
-  return units(weight_pair(v, v, PairScale(m, ch, cl), table).a);
+// One exact weight, out of line too.  `lowest` as of PairScale; NaN: neighbouring floats lie so far
+// apart that all below the maximum weigh nothing.
+__device__ __noinline__ int64_t one_weight(float v, float m, float ch, float cl, float lowest,
+                                           const PairTable& table) {
+  if (lowest != lowest) return v == m ? (int64_t)kUnit : 0;
+  v = fmaxf(v, lowest);
+  const WeightPair w = weight_pair(v, v, PairScale{m, ch, cl}, table);
+  return units({w.high0 - kPart, w.low0 - kPart});
 }
 
 template <typename T>
@@ -307,15 +312,22 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   }
 
   const float per_bin = ch * ((float)(kBins - 1) / kSpan);
-  const PairScale scale2(m, ch, cl);
-  auto weight_of = [&](float v) { return one_weight(v, m, ch, cl, sh.exp2); };
+  const PairScale scale2{m, ch, cl};
+  const float lowest = scale2.lowest();
+  const bool apart = lowest != lowest;
+  auto weight_of = [&](float v) { return one_weight(v, m, ch, cl, lowest, sh.exp2); };
   // The weights of a vector's values.
   auto weights_of = [&](const float* v, Weight* w) {
+    if (apart) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = {v[i] == m ? 1 << 22 : 0, 0};
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const WeightPair two = weight_pair(v[i], v[i + 1], scale2, sh.exp2);
-      w[i] = two.a;
-      w[i + 1] = two.b;
+      const WeightPair two = weight_pair(fmaxf(v[i], lowest), fmaxf(v[i + 1], lowest), scale2, sh.exp2);
+      w[i] = {two.high0 - kPart, two.low0 - kPart};
+      w[i + 1] = {two.high1 - kPart, two.low1 - kPart};
     }
   };
   // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
@@ -521,10 +533,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     }
     return lo;
   };
-  // The cut among more tokens than a list holds, of bins b0 .. b1, `target` tokens (or weight)
+  // The cut among more tokens than a list holds, of keys lo .. hi, `target` tokens (or weight)
   // into them: by key, level by level, then the first tokens at the last key by index.
-  auto refine = [&](bool mass, int b0, int b1, int64_t target) {
-    uint32_t lo = first_key(b1), hi = b0 > 0 ? first_key(b0 - 1) - 1 : (uint32_t)(top >> 32);
+  auto refine = [&](bool mass, uint32_t lo, uint32_t hi, int64_t target) {
     const uint64_t limit = cut;
     for (;;) {
       int shift = 0;
@@ -661,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         const int n = gather((float)bin, end_of(bin));
         cut = cut_in_list(n, false, (int64_t)top_k - 1 - before);
       } else {
-        cut = refine(false, bin, bin, (int64_t)top_k - 1 - before);
+        cut = refine(false, first_key(bin), bin > 0 ? first_key(bin - 1) - 1 : (uint32_t)(top >> 32),
+                     (int64_t)top_k - 1 - before);
       }
       limited = true;
       counted = false;
@@ -733,10 +745,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     b1 = small ? bound1 : min(max(sh.window[3], b0), bound1);
     for (;;) {
     // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
-    // (linear over b0 .. b1)
-    const float from = (float)b0, to = end_of(b1);
-    const float scale = (float)kFine / (float)(b1 - b0 + 1);
-    auto fine = [&](float y) { return min((int)((y - from) * scale), kFine - 1); };
+    // (linear over b0 .. b1).  The window as logits: over is the largest, under the smallest in it.
+    const float from = (float)b0, scale = (float)kFine / (float)(b1 - b0 + 1);
+    const float over = b0 > 0 ? unordered(first_key(b0 - 1) - 1) : INFINITY;
+    const float under = unordered(first_key(b1));
+    auto fine = [&](float v) { return min(max((int)((position(v) - from) * scale), 0), kFine - 1); };
+    auto in_window = [&](float v) { return v <= over && v >= under; };
     if (tid == 0) sh.too_many = 0;
     __syncthreads();
     int64_t sum = 0;
@@ -747,28 +761,30 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       // (a vector's parts of weights are added as ints: eight of 2^22)
       Weight w[N];
       weights_of(v, w);
+      if (limited) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (place(v[i], a + i) < cut) w[i] = {0, 0};
+      }
       int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
       bool any = false;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const bool is = !limited || place(v[i], a + i) >= cut;
-        all_h += is ? w[i].high : 0;
-        all_l += is ? w[i].low : 0;
-        const float y = position(v[i]);
-        if (is && y < from) {
+        all_h += w[i].high;
+        all_l += w[i].low;
+        if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
           up_h += w[i].high;
           up_l += w[i].low;
           ++n_above;
         }
-        any |= y >= from && !(y >= to);
+        any |= in_window(v[i]);
       }
       sum += units({all_h, all_l});
       above += units({up_h, up_l});
       if (!__any_sync(0xffffffffu, any)) return;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float y = position(v[i]);
-        const bool in = y >= from && !(y >= to) && place(v[i], a + i) >= cut;
+        const bool in = in_window(v[i]) && place(v[i], a + i) >= cut;
         const uint32_t who = __ballot_sync(0xffffffffu, in);
         const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
         if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
@@ -782,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     totals_of(W, all_above, too_many);
     const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
     if (small) {
-      const int n = gather(0.f, to);
+      const int n = gather(0.f, end_of(b1));
       finish_in_list(n, 0, top_p, share);
       done = true;
     } else {
@@ -799,8 +815,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         each(kDear, [&](const float* v, int a) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const float y = position(v[i]);
-            if (y >= from && !(y >= to) && place(v[i], a + i) >= cut) fn(v[i], a + i);
+            if (in_window(v[i]) && place(v[i], a + i) >= cut) fn(v[i], a + i);
           }
         });
       };
@@ -808,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       clear(3 * kFine);
       each_in_window([&](float v, int) {
         const int64_t w = weight_of(v);
-        if (w > 0) add_mass(fine(position(v)), (uint64_t)w);
+        if (w > 0) add_mass(fine(v), (uint64_t)w);
       });
       merge_mass();
       int64_t before, total;
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       int n_more = 0;
       start_list();
       each_in_window([&](float v, int index) {
-        const int f = fine(position(v));
+        const int f = fine(v);
         if (f == bin) put_on_list(v, index);
         if (f >= bin) return;
         more += weight_of(v);
@@ -836,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         above += more;
         n_above += n_more;
       } else {
-        cut = refine(true, b0, b1, target);
+        cut = refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
       }
     }
     break;

@@ -82,62 +82,65 @@ __device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
 }
 __device__ __forceinline__ int64_t units(Weight w) { return ((int64_t)w.high << 22) + w.low; }
 
-// The same for two logits at once, the same bits, in packed float operations (half the
-// instructions).  The table: the two floats in arrays of their own, a copy for each lane.
+// The same for two logits at once, in packed float operations (half the instructions; the float
+// pipe's work is the same, which is why they are fewer than above: 44 a logit).  The bits may differ
+// from those of `weight`: the two parts are summed before the low one is rounded, which is off by
+// 5/8 of a unit at most.  The logits lie between lowest() and m: below it weights are zero.
+// The table: the two floats in arrays of their own, a copy for each lane.
 struct PairTable {
   float hi[kTable * 32], lo[kTable * 32];
 };
-struct PairScale {  // -m, m, ch, cl twice each
-  uint64_t neg_m, m, ch, cl;
-  __device__ PairScale(float m_, float ch_, float cl_)
-      : neg_m(f2_pack(-m_, -m_)), m(f2_pack(m_, m_)), ch(f2_pack(ch_, ch_)), cl(f2_pack(cl_, cl_)) {}
+struct PairScale {
+  float m, ch, cl;
+  // What smaller logits may be raised to: a logit of weight zero, 46 .. 140 log2 units below m; NaN
+  // where there is none, the float before m being farther away.
+  __device__ float lowest() const {
+    float x = m - 60.f / ch;
+    if ((x - m) * ch > -46.f) x = nextafterf(x, -INFINITY);
+    const float y = (x - m) * ch;
+    return y <= -46.f && y >= -140.f ? x : NAN;
+  }
 };
-struct WeightPair {
-  Weight a, b;
+struct WeightPair {  // the high and low parts as they leave the float pipe: kPart more each
+  int high0, low0, high1, low1;
 };
+constexpr int kPart = 0x4B400000;  // the bits of 1.5 * 2^23
 __device__ __forceinline__ WeightPair weight_pair(float x0, float x1, const PairScale& c,
                                                   const PairTable& table) {
   auto two = [](float v) { return f2_pack(v, v); };
   auto sub = [&](uint64_t a, uint64_t b) { return f2_fma(b, two(-1.f), a); };  // a - b
   constexpr float magic = 12582912.f;
   constexpr float ln2h = (float)kLn2, ln2l = (float)(kLn2 - (double)ln2h);
-  const uint64_t x = f2_pack(x0, x1), dh = f2_add(x, c.neg_m), y0 = f2_mul(dh, c.ch);
-  float y00, y01;
-  f2_unpack(y0, y00, y01);
-  const bool some0 = y00 > -46.f, some1 = y01 > -46.f;
-  const uint64_t yh = f2_pack(some0 ? y00 : 0.f, some1 ? y01 : 0.f);
+  const uint64_t x = f2_pack(x0, x1), dh = f2_add(x, two(-c.m)), yh = f2_mul(dh, two(c.ch));
   const uint64_t bb = sub(dh, x);
-  const uint64_t dl = sub(sub(x, sub(dh, bb)), f2_add(c.m, bb));
-  const uint64_t yl = f2_add(f2_fma(dh, c.ch, f2_mul(yh, two(-1.f))), f2_fma(dh, c.cl, f2_mul(dl, c.ch)));
+  const uint64_t dl = sub(sub(x, sub(dh, bb)), f2_add(two(c.m), bb));
+  const uint64_t yl = sub(f2_fma(dh, two(c.cl), f2_mul(dl, two(c.ch))), f2_fma(dh, two(-c.ch), yh));
   const uint64_t kr = f2_fma(yh, two((float)kTable), two(magic));
-  float k0, k1;
-  f2_unpack(kr, k0, k1);
-  const int i0 = __float_as_int(k0) - __float_as_int(magic), i1 = __float_as_int(k1) - __float_as_int(magic);
   const uint64_t f = f2_fma(f2_add(kr, two(-magic)), two(-1.f / kTable), yh);
   const uint64_t zh = f2_mul(f, two(ln2h));
-  const uint64_t zl = f2_add(f2_fma(f, two(ln2h), f2_mul(zh, two(-1.f))),
-                             f2_fma(f, two(ln2l), f2_mul(yl, two(ln2h))));
-  const uint64_t q = f2_fma(zh, f2_fma(zh, f2_fma(zh, two(1.f / 120.f), two(1.f / 24.f)), two(1.f / 6.f)),
-                            two(0.5f));
-  const uint64_t el = f2_add(f2_fma(zh, zl, zl), f2_mul(f2_mul(zh, zh), q));
-  const int lane = threadIdx.x & 31, t0 = (i0 & (kTable - 1)) * 32 + lane, t1 = (i1 & (kTable - 1)) * 32 + lane;
+  const uint64_t zl = sub(f2_fma(f, two(ln2l), f2_mul(yl, two(ln2h))), f2_fma(f, two(-ln2h), zh));
+  const uint64_t q = f2_fma(zh, f2_fma(zh, two(1.f / 24.f), two(1.f / 6.f)), two(0.5f));
+  const uint64_t el = f2_fma(f2_mul(zh, zh), q, f2_fma(zh, zl, zl));
+  float k0, k1;
+  f2_unpack(kr, k0, k1);
+  const int i0 = __float_as_int(k0), i1 = __float_as_int(k1), lane = threadIdx.x & 31;
+  const int t0 = (i0 & (kTable - 1)) * 32 + lane, t1 = (i1 & (kTable - 1)) * 32 + lane;
   const uint64_t th = f2_pack(table.hi[t0], table.hi[t1]), tl = f2_pack(table.lo[t0], table.lo[t1]);
   const uint64_t ph = f2_mul(th, zh);
-  const uint64_t pl = f2_add(f2_fma(th, zh, f2_mul(ph, two(-1.f))), f2_fma(th, el, f2_fma(tl, zh, tl)));
+  const uint64_t pl = sub(f2_fma(th, el, f2_fma(tl, zh, tl)), f2_fma(th, f2_mul(zh, two(-1.f)), ph));
   const uint64_t h1 = f2_add(th, ph), l1 = f2_add(f2_add(sub(th, h1), ph), pl);
   const uint64_t hi = f2_add(h1, l1), lo = f2_add(sub(h1, hi), l1);
-  const int e0 = (i0 >> 6) << 23, e1 = (i1 >> 6) << 23;
-  const uint64_t s22 = f2_pack(__int_as_float(e0 + ((22 + 127) << 23)), __int_as_float(e1 + ((22 + 127) << 23)));
+  // 2^22 times the power of two: the integer part of k0 moved to the exponent
+  constexpr int e = (22 + 127) << 23;
+  const uint64_t s22 = f2_pack(__int_as_float((int)((uint32_t)(i0 & ~(kTable - 1)) << 17) + e),
+                               __int_as_float((int)((uint32_t)(i1 & ~(kTable - 1)) << 17) + e));
   const uint64_t a = f2_mul(hi, s22), ra = f2_add(a, two(magic));
-  const uint64_t rb = f2_add(f2_fma(sub(a, f2_add(ra, two(-magic))), two(4194304.f),
-                                    f2_mul(lo, f2_mul(s22, two(4194304.f)))),
-                             two(magic));
+  const uint64_t rest = f2_fma(lo, s22, sub(a, f2_add(ra, two(-magic))));
+  const uint64_t rb = f2_fma(rest, two(4194304.f), two(magic));
   float a0, a1, b0, b1;
   f2_unpack(ra, a0, a1);
   f2_unpack(rb, b0, b1);
-  constexpr int mi = 0x4B400000;  // the bits of 1.5 * 2^23
-  return {{some0 ? __float_as_int(a0) - mi : 0, some0 ? __float_as_int(b0) - mi : 0},
-          {some1 ? __float_as_int(a1) - mi : 0, some1 ? __float_as_int(b1) - mi : 0}};
+  return {__float_as_int(a0), __float_as_int(b0), __float_as_int(a1), __float_as_int(b1)};
 }
 
 template <typename T>
