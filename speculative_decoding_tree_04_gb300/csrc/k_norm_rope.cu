@@ -612,8 +612,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
         const int64_t at = t - p.q_start[b];
         const int64_t dep = p.depth ? p.depth[t] : at;
         const int P = p.prefix_len[b];
-        if (P < 0) report(p.status, TV_ERR_BOUNDS);
-        is = dep >= 0 && P >= 0;  // (a node of an invalid tree is left alone)
+        const bool sound = P >= 0 && at >= 0;  // (a q_start that does not ascend finds anything)
+        if (!sound) report(p.status, TV_ERR_BOUNDS);
+        is = dep >= 0 && sound;  // (a node of an invalid tree is left alone)
         pos[i] = (double)P + (double)dep;
         if (is && keys) {
           const int64_t j = (int64_t)P + at;

@@ -329,6 +329,36 @@ def test_strided_inputs_share_a_buffer():
         assert np.array_equal(out[k].double().cpu().numpy(), o[k])
 
 
+def test_cache_rows_within_wider_ones():
+    # both arrays are parts of one row of 2 + 64 + 6 + 16 + 8 elements, at any alignment
+    for dt in (torch.bfloat16, torch.float32):
+        for off in (0, 8, 2, 3):
+            s = batch(77, [5, 3], [60, 0], 3, 16, 16, 64, dt)
+            want = apply(s)
+            wide = torch.full((s["rows"], 128), -77.0, dtype=dt, device="cuda")
+            c, k = wide[:, off:off + 64], wide[:, off + 72:off + 88]
+            T, H = s["q"].shape[:2]
+            i32 = dict(dtype=torch.int32, device="cuda")
+            tv.norm_rope(None, s["kv"].cuda(), torch.from_numpy(s["start"]).cuda(),
+                         torch.tensor(s["prefixes"], **i32), None, None, c, k,
+                         kv_weight=s["kv_weight"].cuda(),
+                         page_table=torch.from_numpy(s["table"]).cuda())
+            # (another order of the norm's sum at another alignment: a last place of float32)
+            tol = 2.0 ** -7 if dt is torch.bfloat16 else 2.0 ** -20
+            for got, ref in ((c, want["c_kv"]), (k, want["k_pe"])):
+                got = got.double().cpu().numpy()
+                assert (np.abs(got - ref) <= tol * np.abs(ref) + 1e-30).all()
+            rest = torch.cat([wide[:, :off], wide[:, off + 64:off + 72], wide[:, off + 88:]], -1)
+            assert (rest == -77.0).all()
+
+
+def test_starts_that_do_not_ascend():
+    s = batch(78, [4, 4, 4], [5, 6, 7], 2, 16, 16, 64, torch.bfloat16)
+    s["start"] = np.array([0, 9, 4, 12], np.int32)
+    o = apply(s, status=tv.TV_ERR_BOUNDS)  # what it finds is anything, but within the arrays
+    assert (o["q_pe"] == -77.0).any()
+
+
 def test_captured_and_replayed():
     s = batch(76, [1] * 6, [3, 64, 127, 0, 900, 5], 16, 128, 64, 512, torch.bfloat16)
     want = apply(s)

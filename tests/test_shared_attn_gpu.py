@@ -324,6 +324,35 @@ def test_graph_follows_its_lengths():
     close(t, d)
 
 
+def test_cache_rows_within_wider_ones():
+    s = make(15, [6, 2], [1280, 70], 60, Q=2, H=8)
+    want, d = run(s), device(s)
+    wide = torch.full((len(s["c_kv"]), 608), float("nan"), dtype=torch.bfloat16, device="cuda")
+    d["c_kv"], d["k_pe"] = wide[:, 8:520], wide[:, 536:600]
+    d["c_kv"].copy_(s["c_kv"])
+    d["k_pe"].copy_(s["k_pe"])
+    launch(s, d)
+    torch.cuda.synchronize()
+    assert torch.equal(d["out"], want["out"]) and torch.equal(d["lse"], want["lse"])
+
+
+def test_keys_that_are_not_finite_stay_in_their_sequence():
+    # (own keys of one sequence; the shared ones belong to all)
+    s = make(16, [8], [1280], [90] * 8)
+    d = device(s)
+    page = int(s["table"][3, 21])
+    d["c_kv"][page * 64 + 5] = float("nan")
+    launch(s, d)
+    torch.cuda.synchronize()
+    # (a key's latent row is part of its score, q . c + q_pe . k, so the sum is NaN as well)
+    assert torch.isnan(d["out"][3]).all() and torch.isnan(d["lse"][3]).all()
+    close(s, d, [0, 1, 2, 4, 5, 6, 7])
+    d["k_pe"][page * 64 + 5] = float("inf")
+    launch(s, d)
+    torch.cuda.synchronize()
+    close(s, d, [0, 1, 2, 4, 5, 6, 7])
+
+
 def test_on_another_stream():
     s = make(12, [5], [640], 60)
     a, d = run(s), device(s)

@@ -137,6 +137,27 @@ def test_around_zero_and_far_apart():
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_draws_next_to_boundaries(dt):
+    # uniforms at the two floats around a boundary of the running sums, where they are farther
+    # from it than the weights' errors could move it (2^-36)
+    g = torch.Generator().manual_seed(16)
+    for V, kw in ((3000, {}), (3000, dict(k=700)), (40000, dict(p=0.8))):
+        x = (torch.randn((1, V), generator=g) * 2).to(dt)
+        x64 = x[0].double().numpy()
+        w = np.exp(x64 - x64.max())
+        n = dm.next_token(x64, 0.5, 1.0, kw.get("k", 0), kw.get("p", 1.0))[1]
+        chosen = np.sort(np.argsort(-x64, kind="stable")[:n])
+        edges = (np.cumsum(w[chosen]) / w[chosen].sum())[:-1]
+        edges = edges[:: max(1, len(edges) // 200)]
+        below = edges.astype(np.float32)
+        below = np.where(below > edges, np.nextafter(below, np.float32(0)), below)
+        u = np.concatenate([below, np.nextafter(below, np.float32(1))])
+        far = np.abs(u.astype(np.float64) - np.concatenate([edges, edges])) > 2.0 ** -36
+        u = u[far & (u < 1)]
+        check(x.repeat(len(u), 1), u, **kw)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_masked_tokens(dt):
     x, u = rows(7, 6, 4099, dt)
     x[:, ::2] = -float("inf")
