@@ -823,7 +823,7 @@ int tv_shared_attn(const tv_shared_args* a, void* workspace, size_t ws_bytes, vo
  * the filters are not read.  A T > 0 below 1.5e-30 or above 1.4e30 counts as that.
  *
  * Weights are integers in units of 2^-44 of the largest, off by at most 2^-37 of themselves and
- * half a unit, as in tv_tree_sample, and their sums are exact: results equal those of the rule in
+ * 5/8 of a unit, and their sums are exact: results equal those of the rule in
  * 64-bit arithmetic unless a sum or a weight falls as near to a border as these move it, and do
  * not depend on how a row is split.
  */

@@ -5,9 +5,9 @@
 // weights reaches p W, W the sum of what top_k keeps; min_p bounds the weight itself.  The token
 // is then drawn in index order from what is kept.
 //
-// Weights are the exact integers of tv_tree_sample (sample_math.h), and all decisions are taken
-// on exact sums.  An exact weight costs some 45 instructions, so the passes over a row are
-// arranged to take each at most about once:
+// Weights are integers in units of 2^-44 of the largest (sample_math.h), and all decisions are
+// taken on exact sums of them.  A weight costs 44 float operations, so the passes over a row are
+// arranged to take each about once at most:
 //   1. the maximum;
 //   2. counts of the tokens in kBins bins that are linear in the logit (kSpan units of log2 of
 //      the weight, the last bin for all below);
@@ -744,117 +744,117 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     b0 = small ? bound0 : min(max(sh.window[2], bound0), bound1);
     b1 = small ? bound1 : min(max(sh.window[3], b0), bound1);
     for (;;) {
-    // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
-    // (linear over b0 .. b1).  The window as logits: over is the largest, under the smallest in it.
-    const float from = (float)b0, scale = (float)kFine / (float)(b1 - b0 + 1);
-    const float over = b0 > 0 ? unordered(first_key(b0 - 1) - 1) : INFINITY;
-    const float under = unordered(first_key(b1));
-    auto fine = [&](float v) { return min(max((int)((position(v) - from) * scale), 0), kFine - 1); };
-    auto in_window = [&](float v) { return v <= over && v >= under; };
-    if (tid == 0) sh.too_many = 0;
-    __syncthreads();
-    int64_t sum = 0;
-    above = 0;
-    n_above = 0;
-    int n_window = 0;  // the warp's tokens of the window
-    each(kDear, [&](const float* v, int a) {
-      // (a vector's parts of weights are added as ints: eight of 2^22)
-      Weight w[N];
-      weights_of(v, w);
-      if (limited) {
+      // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
+      // (linear over b0 .. b1).  The window as logits: over is the largest, under the smallest in it.
+      const float from = (float)b0, scale = (float)kFine / (float)(b1 - b0 + 1);
+      const float over = b0 > 0 ? unordered(first_key(b0 - 1) - 1) : INFINITY;
+      const float under = unordered(first_key(b1));
+      auto fine = [&](float v) { return min(max((int)((position(v) - from) * scale), 0), kFine - 1); };
+      auto in_window = [&](float v) { return v <= over && v >= under; };
+      if (tid == 0) sh.too_many = 0;
+      __syncthreads();
+      int64_t sum = 0;
+      above = 0;
+      n_above = 0;
+      int n_window = 0;  // the warp's tokens of the window
+      each(kDear, [&](const float* v, int a) {
+        // (a vector's parts of weights are added as ints: eight of 2^22)
+        Weight w[N];
+        weights_of(v, w);
+        if (limited) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (place(v[i], a + i) < cut) w[i] = {0, 0};
-      }
-      int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        all_h += w[i].high;
-        all_l += w[i].low;
-        if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
-          up_h += w[i].high;
-          up_l += w[i].low;
-          ++n_above;
+          for (int i = 0; i < N; ++i)
+            if (place(v[i], a + i) < cut) w[i] = {0, 0};
         }
-        any |= in_window(v[i]);
-      }
-      sum += units({all_h, all_l});
-      above += units({up_h, up_l});
-      if (!__any_sync(0xffffffffu, any)) return;
+        int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
+        bool any = false;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool in = in_window(v[i]) && place(v[i], a + i) >= cut;
-        const uint32_t who = __ballot_sync(0xffffffffu, in);
-        const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
-        if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
-        n_window += __popc(who);
-      }
-    });
-    if (n_window > kWindow && lane == 0) sh.too_many = 1;
-    int64_t W = sum, all_above = above, too_many = 0;
-    __syncthreads();
-    if (tid == 0) too_many = sh.too_many;
-    totals_of(W, all_above, too_many);
-    const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
-    if (small) {
-      const int n = gather(0.f, end_of(b1));
-      finish_in_list(n, 0, top_p, share);
-      done = true;
-    } else {
-      // the window's tokens: what the warps have kept, or the row once more
-      auto each_in_window = [&](auto fn) {
-        if (too_many == 0) {
-#pragma unroll 1
-          for (int i = lane; i < n_window; i += 32) {
-            const uint64_t x = sh.window_of[warp][i];
-            fn(unordered((uint32_t)(x >> 32)), (int)(0xFFFFFFFFu - (uint32_t)x));
+        for (int i = 0; i < N; ++i) {
+          all_h += w[i].high;
+          all_l += w[i].low;
+          if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
+            up_h += w[i].high;
+            up_l += w[i].low;
+            ++n_above;
           }
-          return;
+          any |= in_window(v[i]);
         }
-        each(kDear, [&](const float* v, int a) {
+        sum += units({all_h, all_l});
+        above += units({up_h, up_l});
+        if (!__any_sync(0xffffffffu, any)) return;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (in_window(v[i]) && place(v[i], a + i) >= cut) fn(v[i], a + i);
-          }
-        });
-      };
-      const int64_t target = share - 1 - all_above;
-      clear(3 * kFine);
-      each_in_window([&](float v, int) {
-        const int64_t w = weight_of(v);
-        if (w > 0) add_mass(fine(v), (uint64_t)w);
+        for (int i = 0; i < N; ++i) {
+          const bool in = in_window(v[i]) && place(v[i], a + i) >= cut;
+          const uint32_t who = __ballot_sync(0xffffffffu, in);
+          const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
+          if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
+          n_window += __popc(who);
+        }
       });
-      merge_mass();
-      int64_t before, total;
-      const int bin = find(kFine, mass_at, target, &before, &total);
-      if ((target < 0 || target >= total) && (b0 != bound0 || b1 != bound1)) {
-        b0 = bound0;
-        b1 = bound1;
-        continue;
-      }
-      // those before the cut's bin are kept, those in it go on a list
-      int64_t more = 0;
-      int n_more = 0;
-      start_list();
-      each_in_window([&](float v, int index) {
-        const int f = fine(v);
-        if (f == bin) put_on_list(v, index);
-        if (f >= bin) return;
-        more += weight_of(v);
-        ++n_more;
-      });
-      const int n = join_lists();
-      if (n <= kList) {
-        cut = cut_in_list(n, true, target - before);
-        saved = mp == 0.f;
-        above += more;
-        n_above += n_more;
+      if (n_window > kWindow && lane == 0) sh.too_many = 1;
+      int64_t W = sum, all_above = above, too_many = 0;
+      __syncthreads();
+      if (tid == 0) too_many = sh.too_many;
+      totals_of(W, all_above, too_many);
+      const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
+      if (small) {
+        const int n = gather(0.f, end_of(b1));
+        finish_in_list(n, 0, top_p, share);
+        done = true;
       } else {
-        cut = refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
+        // the window's tokens: what the warps have kept, or the row once more
+        auto each_in_window = [&](auto fn) {
+          if (too_many == 0) {
+#pragma unroll 1
+            for (int i = lane; i < n_window; i += 32) {
+              const uint64_t x = sh.window_of[warp][i];
+              fn(unordered((uint32_t)(x >> 32)), (int)(0xFFFFFFFFu - (uint32_t)x));
+            }
+            return;
+          }
+          each(kDear, [&](const float* v, int a) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              if (in_window(v[i]) && place(v[i], a + i) >= cut) fn(v[i], a + i);
+            }
+          });
+        };
+        const int64_t target = share - 1 - all_above;
+        clear(3 * kFine);
+        each_in_window([&](float v, int) {
+          const int64_t w = weight_of(v);
+          if (w > 0) add_mass(fine(v), (uint64_t)w);
+        });
+        merge_mass();
+        int64_t before, total;
+        const int bin = find(kFine, mass_at, target, &before, &total);
+        if ((target < 0 || target >= total) && (b0 != bound0 || b1 != bound1)) {
+          b0 = bound0;
+          b1 = bound1;
+          continue;
+        }
+        // those before the cut's bin are kept, those in it go on a list
+        int64_t more = 0;
+        int n_more = 0;
+        start_list();
+        each_in_window([&](float v, int index) {
+          const int f = fine(v);
+          if (f == bin) put_on_list(v, index);
+          if (f >= bin) return;
+          more += weight_of(v);
+          ++n_more;
+        });
+        const int n = join_lists();
+        if (n <= kList) {
+          cut = cut_in_list(n, true, target - before);
+          saved = mp == 0.f;
+          above += more;
+          n_above += n_more;
+        } else {
+          cut = refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
+        }
       }
-    }
-    break;
+      break;
     }
   }
   if (!done) {
