@@ -822,10 +822,10 @@ int tv_shared_attn(const tv_shared_args* a, void* workspace, size_t ws_bytes, vo
  * the sum of all of them.  T = 0 is greedy: the largest logit, the smallest index among equals;
  * the filters are not read.  A T > 0 below 1.5e-30 or above 1.4e30 counts as that.
  *
- * Weights are integers in units of 2^-44 of the largest, off by at most 2^-37 of themselves and
- * 5/8 of a unit, and their sums are exact: results equal those of the rule in
- * 64-bit arithmetic unless a sum or a weight falls as near to a border as these move it, and do
- * not depend on how a row is split.
+ * Weights are integers in units of 2^-44 of the largest, off by at most 5/8 of a unit and 2^-36 of
+ * themselves (2^-46 |max x| / T where that is more), and their sums are exact: results equal those
+ * of the rule in 64-bit arithmetic unless a sum or a weight falls as near to a border as these move
+ * it, and do not depend on how a row is split.
  */
 typedef struct {
   uint32_t struct_size;      /* sizeof(tv_token_args): ABI check */

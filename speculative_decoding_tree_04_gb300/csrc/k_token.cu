@@ -6,7 +6,7 @@
 // is then drawn in index order from what is kept.
 //
 // Weights are integers in units of 2^-44 of the largest (sample_math.h), and all decisions are
-// taken on exact sums of them.  A weight costs 44 float operations, so the passes over a row are
+// taken on exact sums of them.  A weight costs 31 float operations, so the passes over a row are
 // arranged to take each about once at most:
 //   1. the maximum;
 //   2. counts of the tokens in kBins bins that are linear in the logit (kSpan units of log2 of
@@ -51,6 +51,7 @@ constexpr float kSpan = 48.f;  // log2 units of the linear bins: below, weights 
 constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
 constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
+constexpr int kHold = 16;      // vectors of a lane's whose weights' parts, of 2^22, are added as ints
 constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
 struct TokenParams {
@@ -67,7 +68,7 @@ struct TokenParams {
 };
 
 struct Shared {
-  PairTable exp2;
+  ScaledTable exp2;
   alignas(16) uint32_t bins[3 * kFine];  // this CTA's: counts (kBins), or 15-bit parts of weights' sums
   alignas(16) int64_t all[kFine]; // the cluster's: counts (kBins of 32 bits), or sums
   uint64_t window_of[kWarps][kWindow];  // the warps' tokens of the window
@@ -82,7 +83,8 @@ struct Shared {
   uint64_t warp_key[kWarps];
   int64_t warp_mass[kWarps], warp_three[3][kWarps];
   int32_t warp_count[kWarps];
-  float warp_lo[kWarps], warp_hi[kWarps];
+  float warp_up[4][kWarps];       // of the window's search
+  int32_t warp_n[kWarps], n_before[3];
   int64_t found[2];               // a bin, and the total before it
   int32_t window[4], too_many;
   uint64_t cut;
@@ -144,6 +146,23 @@ __device__ __forceinline__ S block_scan(S v, S* warps, S* total) {
   return up_to - v + warp_sum(lane < warp ? mine : (S)0);
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// The largest of a vector's values, NaN where one is.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& w) {
+  if constexpr (sizeof(T) == 4) {
+    return max_or_nan(max_or_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                      max_or_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else {
+    auto two = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    const __nv_bfloat162 y = __hmax2_nan(__hmax2_nan(two(w.x), two(w.y)), __hmax2_nan(two(w.z), two(w.w)));
+    return max_or_nan(__low2float(y), __high2float(y));
+  }
+}
 // A vector of a row at one of its ends (out of line: the passes are many and code is dear).
 template <typename T>
 __device__ __noinline__ uint4 end_vector(const T* x, int64_t V, int64_t a) {
@@ -153,14 +172,11 @@ __device__ __noinline__ uint4 end_vector(const T* x, int64_t V, int64_t a) {
   for (int i = 0; i < N; ++i) v[i] = a + i >= 0 && a + i < V ? x[a + i] : (T)-INFINITY;
   return *reinterpret_cast<const uint4*>(v);
 }
-// One exact weight, out of line too.  `lowest` as of PairScale; NaN: neighbouring floats lie so far
-// apart that all below the maximum weigh nothing.
-__device__ __noinline__ int64_t one_weight(float v, float m, float ch, float cl, float lowest,
-                                           const PairTable& table) {
+// One exact weight, out of line too (m: the maximum).
+__device__ __noinline__ int64_t one_weight(float v, float m, float lowest, const RowScale& scale,
+                                           const ScaledTable& table) {
   if (lowest != lowest) return v == m ? (int64_t)kUnit : 0;
-  v = fmaxf(v, lowest);
-  const WeightPair w = weight_pair(v, v, PairScale{m, ch, cl}, table);
-  return units({w.high0 - kPart, w.low0 - kPart});
+  return units(scaled_weight(fmaxf(v, lowest), scale, table));
 }
 
 template <typename T>
@@ -192,23 +208,22 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     if (C > 1) cluster_sync();
     else __syncthreads();
   };
-  constexpr float l2e = (float)(1.0 / kLn2), l2e_low = (float)(1.0 / kLn2 - (double)l2e);
-  const float cq = l2e / T0;
-  const float ch = fminf(fmaxf(cq, 1e-30f), 1e30f);
-  const float cl = ch == cq ? (fmaf(-cq, T0, l2e) + l2e_low) / T0 : 0.f;
 
   // This warp's vectors, and what it does with every one of them: fn(values, index of the first).
   const Row<T> row((const T*)p.logits + (int64_t)b * p.stride, p.V);
   const int per = (row.n_vec + C - 1) >> log2_C, per_w = (per + kWarps - 1) / kWarps;
   const int c0 = min(row.n_vec, rank * per), c1 = min(row.n_vec, c0 + per);
   const int w0 = min(c1, c0 + warp * per_w), w1 = min(c1, w0 + per_w);
-  const int e0 = row.first_whole();
-  const uint32_t n_whole = (uint32_t)max(row.end_whole() - e0, 0);
-  const uint4* vectors = reinterpret_cast<const uint4*>(row.x - row.off);  // (read where they are whole)
+  // (the row's first and last vector may reach past it)
+  const int e0 = row.first_whole(), e1 = row.end_whole();
+  const int whole0 = max(w0, e0);
+  const uint32_t n_whole = (uint32_t)max(min(w1, e1) - whole0, 0);
+  const uint4* vectors = reinterpret_cast<const uint4*>(row.x - row.off);
   auto vector = [&](int j) {
-    return (uint32_t)(j - e0) < n_whole ? __ldg(vectors + j) : end_vector<T>(row.x, p.V, row.first(j));
+    return j >= e0 && j < e1 ? __ldg(vectors + j) : end_vector<T>(row.x, p.V, row.first(j));
   };
-  auto fetch = [&](int j) {
+  auto fetch = [&](int j) {  // of the warp's, masked past its last one
+    if ((uint32_t)(j - whole0) < n_whole) return __ldg(vectors + j);
     return j < w1 ? vector(j)
                   : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
   };
@@ -250,41 +265,39 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   // ---- the row's maximum, with its first index ----
   uint64_t top;
   {
-    float best = -INFINITY;
-    int best_at = 0;
-    bool is_nan = false;
+    float best = -INFINITY;  // (NaN where one is)
+    int best_j = w0 + lane;
     constexpr int kUnroll = 8;
 #pragma unroll 1
     for (int j0 = w0 + lane; j0 < w1; j0 += 32 * kUnroll) {
       uint4 w[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (j0 + 32 * k < w1) w[k] = vector(j0 + 32 * k);
+      for (int k = 0; k < kUnroll; ++k) w[k] = fetch(j0 + 32 * k);
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
-        if (j0 + 32 * k >= w1) break;
-        float v[N];
-        Vec<T>::unpack(w[k], v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          is_nan |= v[i] != v[i];
-          if (v[i] > best) {
-            best = v[i];
-            best_at = (int)row.first(j0 + 32 * k) + i;
-          }
-        }
+        const float x = largest<T>(w[k]);
+        if (x > best) best_j = j0 + 32 * k;
+        best = max_or_nan(best, x);
       }
     }
+    int best_at = 0;
+    if (greedy && best > -INFINITY) {
+      float v[N];
+      Vec<T>::unpack(fetch(best_j), v);
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i)
+        if (v[i] == best) best_at = best_j * N - row.off + i;
+    }
     for (int i = tid; i < kTable * 32; i += kThreads) {
-      sh.exp2.hi[i] = d_exp.hi[i / 32];
-      sh.exp2.lo[i] = d_exp.lo[i / 32];
+      sh.exp2.hi[i] = d_exp_over_linear.hi[i / 32];
+      sh.exp2.lo[i] = d_exp_over_linear.lo[i / 32];
     }
     // order-preserving value bits, then the complemented index; a NaN beats every value
     top = best > -INFINITY
               ? ((uint64_t)ordered(best) << 32) | (0xFFFFFFFFu - (uint32_t)best_at)
               : 0ull;
     top = warp_max(top);
-    if (__any_sync(0xffffffffu, is_nan)) top = ~0ull;
+    if (__any_sync(0xffffffffu, best != best)) top = ~0ull;
     if (lane == 0) sh.warp_key[warp] = top;
     if (C > 1) cluster_wait();
     __syncthreads();
@@ -311,11 +324,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     return;
   }
 
-  const float per_bin = ch * ((float)(kBins - 1) / kSpan);
-  const PairScale scale2{m, ch, cl};
-  const float lowest = scale2.lowest();
+  float lowest;
+  const RowScale scale(m, T0, &lowest);
+  const float ch = scale.k64 * (1.f / kTable), per_bin = ch * ((float)(kBins - 1) / kSpan);
   const bool apart = lowest != lowest;
-  auto weight_of = [&](float v) { return one_weight(v, m, ch, cl, lowest, sh.exp2); };
+  auto weight_of = [&](float v) { return one_weight(v, m, lowest, scale, sh.exp2); };
   // The weights of a vector's values.
   auto weights_of = [&](const float* v, Weight* w) {
     if (apart) {
@@ -324,11 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       return;
     }
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const WeightPair two = weight_pair(fmaxf(v[i], lowest), fmaxf(v[i + 1], lowest), scale2, sh.exp2);
-      w[i] = {two.high0 - kPart, two.low0 - kPart};
-      w[i + 1] = {two.high1 - kPart, two.low1 - kPart};
-    }
+    for (int i = 0; i < N; ++i) w[i] = scaled_weight(fmaxf(v[i], lowest), scale, sh.exp2);
   };
   // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
   // a bin is a range of keys).
@@ -342,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   constexpr uint64_t kMasked = (uint64_t)0x007FFFFFu << 32 | 0xFFFFFFFFu;  // -inf, any index
   uint64_t cut = kMasked + 1;  // tokens at or above it are kept
   const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
-  const int64_t least = (int64_t)ceil((double)mp * (double)kUnit);
+  // (the maximum's own weight may be off by a unit, and is kept with a min_p of 1 too)
+  const int64_t least = mp > 0.f ? min((int64_t)ceil((double)mp * (double)kUnit), weight_of(m)) : 0;
   // (a token this far below the maximum is lighter than min_p without more ado)
   const float far = mp > 0.f ? fminf(-__log2f(mp) * 1.0001f + 0.01f, 64.f) : INFINITY;
 
@@ -679,10 +689,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       counted = false;
     }
   }
-  // ---- top_p; saved: the warps' sums of the tokens above the window are there ----
+  // ---- top_p; saved: the warps' sums of the tokens before the cut's list are there ----
   bool saved = false;
   int64_t above = 0;
-  int n_above = 0, b0 = 0, b1 = kBins - 1;
+  int n_above = 0, n_own = 0;  // tokens above the window, of the row; more that are kept, the lane's
+  int b0 = 0, b1 = kBins - 1;
   if (top_p < 1.f && !done) {
     if (!counted) count(limited, NAN);
     // The cut's window from the counts: bounds of the running sums (their weights lie within a
@@ -695,37 +706,67 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     auto low_mass = [&](int bin, float n) { return bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f; };
     auto high_mass = [&](int bin, float n) { return n * ex2(-kWidth * (float)bin); };
     auto mid_mass = [&](int bin, float n) { return n * ex2(-kWidth * ((float)bin + 0.5f)); };
-    float lo = 0.f, hi = 0.f, mid = 0.f, var = 0.f, all_lo, all_hi, all_mid, all_var;
+    // prefix sums over the block, a thread for kEach bins: the three masses and the counts; the
+    // variances' sum
+    float up[4] = {0.f, 0.f, 0.f, 0.f}, all[4];
+    int up_n = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int bin = tid * kEach + i;
       const float n = (float)count_at(bin), w = mid_mass(bin, n);
-      hi += high_mass(bin, n);
-      lo += low_mass(bin, n);
-      mid += w;
-      var += sizeof(T) == 2 ? w * w : w * w / fmaxf(n, 1.f);
+      up[0] += low_mass(bin, n);
+      up[1] += high_mass(bin, n);
+      up[2] += w;
+      up[3] += sizeof(T) == 2 ? w * w : w * w / fmaxf(n, 1.f);
+      up_n += (int)count_at(bin);
     }
-    float up_lo = block_scan(lo, sh.warp_lo, &all_lo), up_hi = block_scan(hi, sh.warp_hi, &all_hi);
-    float up_mid = block_scan(mid, sh.warp_lo, &all_mid);
-    block_scan(var, sh.warp_hi, &all_var);
+    {
+      float to[4];
+      int to_n = up_n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[i] = up[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float below = __shfl_up_sync(0xffffffffu, to[i], o);
+          if (lane >= o) to[i] += below;
+        }
+        const int below = __shfl_up_sync(0xffffffffu, to_n, o);
+        if (lane >= o) to_n += below;
+      }
+      if (lane == 31) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sh.warp_up[i][warp] = to[i];
+        sh.warp_n[warp] = to_n;
+      }
+      if (tid < 4) sh.window[tid] = kBins - 1;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float part = lane < kWarps ? sh.warp_up[i][lane] : 0.f;
+        all[i] = warp_sum(part);
+        up[i] = to[i] - up[i] + warp_sum(lane < warp ? part : 0.f);
+      }
+      up_n = to_n - up_n + warp_sum(lane < warp ? sh.warp_n[lane & (kWarps - 1)] : 0);
+    }
     const float q = fmaxf(top_p, 0.f);
-    const float margin = 9.f * 0.0024f * sqrtf(all_var) + 1e-5f * all_mid;
+    const float margin = 9.f * 0.0024f * sqrtf(all[3]) + 1e-5f * all[2];
     // the first bins at which a running sum reaches a place: the bounds' ends, the estimate's
-    const float t[4] = {q * all_lo * 0.999f, q * all_hi * 1.001f, q * all_mid - margin, q * all_mid + margin};
-    if (tid < 4) sh.window[tid] = kBins - 1;
-    __syncthreads();
+    const float t[4] = {q * all[0] * 0.999f, q * all[1] * 1.001f, q * all[2] - margin, q * all[2] + margin};
     int at[4] = {kBins - 1, kBins - 1, kBins - 1, kBins - 1};
+    const int n_first = up_n;  // tokens before this thread's bins
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int bin = tid * kEach + i;
       const float n = (float)count_at(bin);
-      up_hi += high_mass(bin, n);
-      up_lo += low_mass(bin, n);
-      up_mid += mid_mass(bin, n);
-      if (up_hi >= t[0]) at[0] = min(at[0], bin);
-      if (up_lo >= t[1]) at[1] = min(at[1], bin);
-      if (up_mid >= t[2]) at[2] = min(at[2], bin);
-      if (up_mid >= t[3]) at[3] = min(at[3], bin);
+      up[1] += high_mass(bin, n);
+      up[0] += low_mass(bin, n);
+      up[2] += mid_mass(bin, n);
+      if (up[1] >= t[0]) at[0] = min(at[0], bin);
+      if (up[0] >= t[1]) at[1] = min(at[1], bin);
+      if (up[2] >= t[2]) at[2] = min(at[2], bin);
+      if (up[2] >= t[3]) at[3] = min(at[3], bin);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -734,15 +775,26 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     }
     __syncthreads();
     const int bound0 = sh.window[0], bound1 = max(sh.window[1], bound0);
-    int64_t n_cand;
-    {
-      int64_t n = 0;
-      for (int i = tid; i <= bound1; i += kThreads) n += count_at(i);
-      block_scan(n, sh.warp_mass, &n_cand);
+    b0 = min(max(sh.window[2], bound0), bound1);
+    b1 = min(max(sh.window[3], b0), bound1);
+    // tokens before the bounds, in front of the window and up to the bounds' end, by the threads
+    // that have those bins
+    const int ends[3] = {bound0, b0, bound1 + 1};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if ((ends[k] - (k == 2)) / kEach != tid) continue;
+      int n = n_first;
+      for (int bin = tid * kEach; bin < ends[k]; ++bin) n += (int)count_at(bin);
+      sh.n_before[k] = n;
     }
+    __syncthreads();
+    const int n_bound0 = sh.n_before[0], n_cand = sh.n_before[2];
+    n_above = sh.n_before[1];
     const bool small = n_cand <= kSmall;
-    b0 = small ? bound0 : min(max(sh.window[2], bound0), bound1);
-    b1 = small ? bound1 : min(max(sh.window[3], b0), bound1);
+    if (small) {
+      b0 = bound0;
+      b1 = bound1;
+    }
     for (;;) {
       // exact sums: of the row, of the tokens above the window, and of the window's in finer bins
       // (linear over b0 .. b1).  The window as logits: over is the largest, under the smallest in it.
@@ -755,10 +807,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       __syncthreads();
       int64_t sum = 0;
       above = 0;
-      n_above = 0;
       int n_window = 0;  // the warp's tokens of the window
+      int all_h = 0, all_l = 0, up_h = 0, up_l = 0, held = 0;
+      auto widen = [&]() {
+        sum += units({all_h, all_l});
+        above += units({up_h, up_l});
+        all_h = all_l = up_h = up_l = 0;
+      };
       each(kDear, [&](const float* v, int a) {
-        // (a vector's parts of weights are added as ints: eight of 2^22)
         Weight w[N];
         weights_of(v, w);
         if (limited) {
@@ -766,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           for (int i = 0; i < N; ++i)
             if (place(v[i], a + i) < cut) w[i] = {0, 0};
         }
-        int all_h = 0, all_l = 0, up_h = 0, up_l = 0;
+        if ((++held & (kHold - 1)) == 0) widen();
         bool any = false;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -775,12 +831,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
             up_h += w[i].high;
             up_l += w[i].low;
-            ++n_above;
           }
           any |= in_window(v[i]);
         }
-        sum += units({all_h, all_l});
-        above += units({up_h, up_l});
         if (!__any_sync(0xffffffffu, any)) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -791,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           n_window += __popc(who);
         }
       });
+      widen();
       if (n_window > kWindow && lane == 0) sh.too_many = 1;
       int64_t W = sum, all_above = above, too_many = 0;
       __syncthreads();
@@ -831,6 +885,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         if ((target < 0 || target >= total) && (b0 != bound0 || b1 != bound1)) {
           b0 = bound0;
           b1 = bound1;
+          n_above = n_bound0;
           continue;
         }
         // those before the cut's bin are kept, those in it go on a list
@@ -849,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           cut = cut_in_list(n, true, target - before);
           saved = mp == 0.f;
           above += more;
-          n_above += n_more;
+          n_own = n_more;
         } else {
           cut = refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
         }
@@ -865,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       return w >= least ? w : (int64_t)-1;
     };
     int64_t mass = saved ? above : 0;
-    int n_kept = saved ? n_above : 0;
+    int n_kept = saved ? n_own : 0;
     if (saved) {
       // (after top_p all but the kept tokens of this CTA's list are in the sums)
       for (int i = lane; i < sh.list_n; i += 32) {
@@ -876,18 +931,29 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         ++n_kept;
       }
     } else if (cut == kMasked + 1 && mp == 0.f) {  // no filter
+      int h = 0, l = 0, held = 0;
       each(kDear, [&](const float* v, int) {
         Weight w[N];
         weights_of(v, w);
-        int h = 0, l = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           h += w[i].high;
           l += w[i].low;
-          n_kept += v[i] > -INFINITY;
         }
-        mass += units({h, l});
+        float x = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) x = fminf(x, v[i]);
+        n_kept += N;
+        if (x == -INFINITY) {  // (few vectors have a masked token)
+#pragma unroll
+          for (int i = 0; i < N; ++i) n_kept -= v[i] == -INFINITY;
+        }
+        if ((++held & (kHold - 1)) == 0) {
+          mass += units({h, l});
+          h = l = 0;
+        }
       });
+      mass += units({h, l});
     } else {
       const float cut_value = unordered((uint32_t)(cut >> 32));
       each(kLight, [&](const float* v, int a) {
@@ -930,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     const int64_t W = warp_sum(part);
     int64_t t = min((int64_t)((double)u * (double)W), W - 1);
     const int owner = locate(part, C, &t);
-    n_kept = warp_sum(lane < C ? sh.count[lane] : 0);
+    n_kept = warp_sum(lane < C ? sh.count[lane] : 0) + (saved ? n_above : 0);
     if (rank == 0 && tid == 0 && p.kept) p.kept[b] = n_kept;
     // the owner's threads look through the slice of the warp that holds the place, a vector each
     if (owner == rank) {

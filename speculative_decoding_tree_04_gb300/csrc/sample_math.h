@@ -1,5 +1,5 @@
 // sample_math.h -- arithmetic shared by the sampling kernels (tv_tree_sample, tv_token_sample):
-// the exact weights of logits, rows as 16-byte vectors, and reductions over warps.
+// the integer weights of logits, rows as 16-byte vectors, and reductions over warps.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,7 +22,7 @@ constexpr int kCopies = 16;     // of the table, one for each lane of a half war
 struct ExpTable {
   float hi[kTable], lo[kTable];
 };
-constexpr ExpTable make_exp_table() {
+constexpr ExpTable make_exp_table(bool over_linear) {
   ExpTable t{};
   for (int j = 0; j < kTable; ++j) {
     const double x = kLn2 * j / kTable;
@@ -31,14 +31,16 @@ constexpr ExpTable make_exp_table() {
       term *= x / k;
       sum += term;
     }
+    if (over_linear) sum /= 1.0 + (double)j / kTable;
     t.hi[j] = (float)sum;
     t.lo[j] = (float)(sum - (double)t.hi[j]);
   }
   return t;
 }
-__device__ const ExpTable d_exp = make_exp_table();
+__device__ const ExpTable d_exp = make_exp_table(false);
+__device__ const ExpTable d_exp_over_linear = make_exp_table(true);  // 2^(j/64) / (1 + j/64)
 
-// 2^((x - m) c) in units of 2^-44, as high * 2^22 + low; c = ch + cl.
+// 2^((x - m) c) in units of 2^-44 (tv_tree_sample), as high * 2^22 + low; c = ch + cl.
 // With y = (x - m) c = k/64 + f: 2^y = 2^(k/64) e^(f ln 2), the first factor from the
 // table, the second by its series (|f ln 2| < 0.0055: the z^5 term is below 2^-44).  Floats
 // become integers by adding 1.5 * 2^23, whose last place is 1, which takes magnitudes up to
@@ -82,67 +84,71 @@ __device__ __forceinline__ Weight weight(float x, float m, float ch, float cl,
 }
 __device__ __forceinline__ int64_t units(Weight w) { return ((int64_t)w.high << 22) + w.low; }
 
-// The same for two logits at once, in packed float operations (half the instructions; the float
-// pipe's work is the same, which is why they are fewer than above: 44 a logit).  The bits may differ
-// from those of `weight`: the two parts are summed before the low one is rounded, which is off by
-// 5/8 of a unit at most.  The logits lie between lowest() and m: below it weights are zero.
-// The table: the two floats in arrays of their own, a copy for each lane.
-struct PairTable {
+// e^((x - m) / T) in the same units, in 31 float operations.  With d = m - x and
+// d / T = k ln 2 / 64 + q - s, k an integer, q what is left of the rounded quotient (exact: its last
+// place is not below 2^-31 where k is not 0) and s the errors of all roundings,
+//     e^(-d/T) = 2^(-k/64) e^(s - q),   e^(s - q) = 1 - q + s (1 - q) + q^2/2 - q^3/6 + q^4/24
+// up to 2^-44.  The difference's error takes two operations where m is a multiple of every logit's
+// last place (Dekker's sum); m is rounded to one, by 2^-24 of itself or of 60 T, and what that
+// leaves is added to d / T, to 2^-49 of |m| / T.  The bits may differ from those of `weight`: the
+// two parts are summed before the low one is rounded, which is off by 5/8 of a unit at most.  The
+// logits lie between the scale's lowest and the maximum.
+// The power of two: the bits of -k, moved to where an exponent's begin, are a float 2^i (1 + j/64)
+// with -k = 64 i + j, so that the table holds 2^(j/64) / (1 + j/64).  Its two floats are in arrays
+// of their own, a copy for each lane.
+struct ScaledTable {
   float hi[kTable * 32], lo[kTable * 32];
 };
-struct PairScale {
-  float m, ch, cl;
-  // What smaller logits may be raised to: a logit of weight zero, 46 .. 140 log2 units below m; NaN
-  // where there is none, the float before m being farther away.
-  __device__ float lowest() const {
-    float x = m - 60.f / ch;
-    if ((x - m) * ch > -46.f) x = nextafterf(x, -INFINITY);
-    const float y = (x - m) * ch;
-    return y <= -46.f && y >= -140.f ? x : NAN;
+struct RowScale {
+  float m, rest;  // m + rest T: the maximum
+  float th, tl;   // 1 / T as two floats
+  float k64;      // 64 log2(e) / T
+  // largest: the maximum; lowest: what smaller logits may be raised to, a logit of weight zero, 46 ..
+  // 140 log2 units below it; NaN where there is none, the float before the maximum being farther
+  // away: then all others weigh nothing.
+  __device__ RowScale(float largest, float T, float* lowest) {
+    T = fminf(fmaxf(T, 1.5e-30f), 1.4e30f);
+    th = 1.f / T;
+    tl = fmaf(-th, T, 1.f) / T;
+    const float log2e = (float)(1.0 / kLn2);
+    k64 = (float)kTable * log2e * th;
+    auto below = [&](float x) { return (largest - x) * th * log2e; };
+    float x = largest - 60.f / (log2e * th);
+    if (below(x) < 46.f) x = nextafterf(x, -INFINITY);
+    *lowest = below(x) >= 46.f && below(x) <= 140.f ? x : NAN;
+    m = largest;
+    if (fabsf(x) > fabsf(largest)) {  // (then x is finite or there is no lowest)
+      // 1.5 * 2^23 of x's last places
+      const float c = 1.5f * __uint_as_float(__float_as_uint(x) & 0x7F800000u);
+      m = __fadd_rn(__fadd_rn(largest, c), -c);
+    }
+    rest = (largest - m) / T;
   }
 };
-struct WeightPair {  // the high and low parts as they leave the float pipe: kPart more each
-  int high0, low0, high1, low1;
-};
-constexpr int kPart = 0x4B400000;  // the bits of 1.5 * 2^23
-__device__ __forceinline__ WeightPair weight_pair(float x0, float x1, const PairScale& c,
-                                                  const PairTable& table) {
-  auto two = [](float v) { return f2_pack(v, v); };
-  auto sub = [&](uint64_t a, uint64_t b) { return f2_fma(b, two(-1.f), a); };  // a - b
+__device__ __forceinline__ Weight scaled_weight(float x, const RowScale& c, const ScaledTable& table) {
   constexpr float magic = 12582912.f;
-  constexpr float ln2h = (float)kLn2, ln2l = (float)(kLn2 - (double)ln2h);
-  const uint64_t x = f2_pack(x0, x1), dh = f2_add(x, two(-c.m)), yh = f2_mul(dh, two(c.ch));
-  const uint64_t bb = sub(dh, x);
-  const uint64_t dl = sub(sub(x, sub(dh, bb)), f2_add(two(c.m), bb));
-  const uint64_t yl = sub(f2_fma(dh, two(c.cl), f2_mul(dl, two(c.ch))), f2_fma(dh, two(-c.ch), yh));
-  const uint64_t kr = f2_fma(yh, two((float)kTable), two(magic));
-  const uint64_t f = f2_fma(f2_add(kr, two(-magic)), two(-1.f / kTable), yh);
-  const uint64_t zh = f2_mul(f, two(ln2h));
-  const uint64_t zl = sub(f2_fma(f, two(ln2l), f2_mul(yl, two(ln2h))), f2_fma(f, two(-ln2h), zh));
-  const uint64_t q = f2_fma(zh, f2_fma(zh, two(1.f / 24.f), two(1.f / 6.f)), two(0.5f));
-  const uint64_t el = f2_fma(f2_mul(zh, zh), q, f2_fma(zh, zl, zl));
-  float k0, k1;
-  f2_unpack(kr, k0, k1);
-  const int i0 = __float_as_int(k0), i1 = __float_as_int(k1), lane = threadIdx.x & 31;
-  const int t0 = (i0 & (kTable - 1)) * 32 + lane, t1 = (i1 & (kTable - 1)) * 32 + lane;
-  const uint64_t th = f2_pack(table.hi[t0], table.hi[t1]), tl = f2_pack(table.lo[t0], table.lo[t1]);
-  const uint64_t ph = f2_mul(th, zh);
-  const uint64_t pl = sub(f2_fma(th, el, f2_fma(tl, zh, tl)), f2_fma(th, f2_mul(zh, two(-1.f)), ph));
-  const uint64_t h1 = f2_add(th, ph), l1 = f2_add(f2_add(sub(th, h1), ph), pl);
-  const uint64_t hi = f2_add(h1, l1), lo = f2_add(sub(h1, hi), l1);
-  // 2^22 times the power of two: the integer part of k0 moved to the exponent
-  constexpr int e = (22 + 127) << 23;
-  const uint64_t s22 = f2_pack(__int_as_float((int)((uint32_t)(i0 & ~(kTable - 1)) << 17) + e),
-                               __int_as_float((int)((uint32_t)(i1 & ~(kTable - 1)) << 17) + e));
-  const uint64_t a = f2_mul(hi, s22), ra = f2_add(a, two(magic));
-  const uint64_t rest = f2_fma(lo, s22, sub(a, f2_add(ra, two(-magic))));
-  const uint64_t rb = f2_fma(rest, two(4194304.f), two(magic));
-  float a0, a1, b0, b1;
-  f2_unpack(ra, a0, a1);
-  f2_unpack(rb, b0, b1);
-  return {__float_as_int(a0), __float_as_int(b0), __float_as_int(a1), __float_as_int(b1)};
+  constexpr float step = (float)(kLn2 / kTable), step_low = (float)(kLn2 / kTable - (double)step);
+  const float d = __fsub_rn(c.m, x), dl = __fsub_rn(__fsub_rn(c.m, d), x);
+  const float p = fmaf(d, c.th, c.rest);
+  const float kr = fmaf(d, -c.k64, magic), k = __fsub_rn(kr, magic);  // -k
+  const float q = fmaf(k, step, p);
+  float s = fmaf(d, -c.tl, __fsub_rn(fmaf(d, -c.th, p), c.rest));
+  s = fmaf(k, -step_low, fmaf(dl, -c.th, s));
+  const float series = fmaf(q, fmaf(q, 1.f / 24.f, -1.f / 6.f), 0.5f);
+  const float e = fmaf(__fmul_rn(q, q), series, fmaf(s, -q, s));
+  const int i = __float_as_int(kr);
+  const int t = (i & (kTable - 1)) * 32 + (threadIdx.x & 31);
+  const float th = table.hi[t], tl = table.lo[t];
+  const float ph = __fmul_rn(th, q);
+  const float low = __fadd_rn(fmaf(th, e, fmaf(tl, -q, tl)), fmaf(-th, q, ph));
+  const float hi = __fadd_rn(th, __fsub_rn(low, ph));
+  const float lo = __fadd_rn(__fsub_rn(__fsub_rn(th, hi), ph), low);
+  const float s22 = __int_as_float((int)((uint32_t)i << 17) + ((22 + 127) << 23));
+  const float ra = fmaf(hi, s22, magic);
+  const float left = fmaf(lo, s22, fmaf(hi, s22, __fsub_rn(magic, ra)));
+  const float rb = fmaf(left, 4194304.f, magic);
+  return {__float_as_int(ra) - __float_as_int(magic), __float_as_int(rb) - __float_as_int(magic)};
 }
-
 template <typename T>
 struct Vec;
 template <>

@@ -1,7 +1,7 @@
 """GPU tests of tv_token_sample against its rule in 64 bits.
 
-Tokens and counts have to be equal.  The library's weights are off by 2^-37 of themselves and
-half a unit of 2^-44, so a draw or a cut may differ where a uniform number or a share falls that
+Tokens and counts have to be equal.  The library's weights are off by 2^-36 of themselves and
+5/8 of a unit of 2^-44, so a draw or a cut may differ where a uniform number or a share falls that
 near to a boundary: with at most 2^18 boundaries in a row, that is one row in 10^5 or fewer of
 random inputs.  Inputs here are seeded, a few thousand rows in all.
 """
