@@ -51,12 +51,14 @@ constexpr float kSpan = 48.f;  // log2 units of the linear bins: below, weights 
 constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
 constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
-constexpr int kHold = 16;      // vectors of a lane's whose weights' parts, of 2^22, are added as ints
+constexpr int kSome = 4;       // values of a vector that the passes with weights take at once
+constexpr int kHold = 64;      // of these whose weights' parts, of 2^22, are added as ints
 constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
 struct TokenParams {
   const void* logits;
   int64_t V, stride;
+  int B, sorted;
   const float* temperature;
   const int32_t* top_k;
   const float* top_p;
@@ -88,6 +90,7 @@ struct Shared {
   int64_t found[2];               // a bin, and the total before it
   int32_t window[4], too_many;
   uint64_t cut;
+  uint32_t is_long[kWarps];
 };
 static_assert(kBins <= 2 * kFine && kFine / 4 >= kThreads && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
 
@@ -146,6 +149,11 @@ __device__ __forceinline__ S block_scan(S v, S* warps, S* total) {
   return up_to - v + warp_sum(lane < warp ? mine : (S)0);
 }
 
+// 2^-x of a bin's width, from the exponential's series.
+constexpr float bin_ratio(double x) {
+  const double y = -kLn2 * x * (double)kSpan / (kBins - 1);
+  return (float)(1.0 + y * (1.0 + y / 2 * (1.0 + y / 3 * (1.0 + y / 4))));
+}
 __device__ __forceinline__ float max_or_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -179,16 +187,46 @@ __device__ __noinline__ int64_t one_weight(float v, float m, float lowest, const
   return units(scaled_weight(fmaxf(v, lowest), scale, table));
 }
 
+// The i-th row to start: those with a top_p and no top_k, which take two to three times as long as
+// others, before the others, so that no SM is given two of them while another has none (64 rows x
+// 163840, a quarter of them long and 36 rows apart: 75 us in order of rows, 63 sorted; rows alike:
+// 0.7 us more).
+constexpr int kSorted = 32 * kWarps;  // rows at most
+__device__ __forceinline__ int row_in_order(const TokenParams& p, int i, uint32_t* is_long) {
+  const int lane = threadIdx.x & 31, r = threadIdx.x;
+  bool is = false;
+  if (r < p.B) {
+    const int k = p.top_k ? p.top_k[r] : 0;
+    is = p.top_p[r] < 1.f && !(k > 0 && k < p.V) && (!p.temperature || p.temperature[r] != 0.f);
+  }
+  const uint32_t bits = __ballot_sync(0xffffffffu, is);
+  if (lane == 0) is_long[r / 32] = bits;
+  __syncthreads();
+  uint32_t mine = lane < kWarps ? is_long[lane] : 0u;
+  const int n_long = warp_sum(__popc(mine));
+  if (i >= n_long) {
+    i -= n_long;
+    mine = ~mine;
+  }
+  const int c = locate(__popc(mine), 32, &i);
+  uint32_t left = __shfl_sync(0xffffffffu, mine, c);
+  for (; i > 0; --i) left &= left - 1;
+  return 32 * c + __ffs(left) - 1;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenParams p, int log2_C) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = 1 << log2_C, b = blockIdx.x >> log2_C;
+  const int C = 1 << log2_C;
   const int rank = C > 1 ? (int)cluster_rank() : 0;
   griddep_wait();
-  griddep_launch_dependents();
+  const int place_of_row = blockIdx.x >> log2_C;
+  // (a reduction's result is seen to be the same in the whole warp, and needs no registers)
+  const int b = (int)__reduce_max_sync(
+      0xffffffffu, (uint32_t)(p.sorted ? row_in_order(p, place_of_row, sh.is_long) : place_of_row));
   const float T0 = p.temperature ? p.temperature[b] : 1.f;
   const int top_k = p.top_k ? p.top_k[b] : 0;
   const float top_p = p.top_p ? p.top_p[b] : 1.f, min_p = p.min_p ? p.min_p[b] : 0.f;
@@ -228,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
                   : make_uint4(Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked, Vec<T>::kMasked);
   };
   // All lanes call it together, those past the last vector with -inf.  `dear`: one copy of fn's
-  // code, the next vectors on their way (unrolled, such passes outgrow the instruction cache).
+  // code for kSome values, the next vectors on their way (unrolled, such passes outgrow the
+  // registers and the instruction cache).
   auto each = [&](auto dear, auto fn) {
     if constexpr (decltype(dear)::value) {
       uint4 next[kAhead];
@@ -236,12 +275,20 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       for (int k = 0; k < kAhead; ++k) next[k] = fetch(w0 + lane + 32 * k);
 #pragma unroll 1
       for (int j0 = w0; j0 < w1; j0 += 32) {
-        float v[N];
-        Vec<T>::unpack(next[0], v);
+        uint4 w = next[0];
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) next[k] = next[k + 1];
         next[kAhead - 1] = fetch(j0 + lane + 32 * kAhead);
-        fn(v, (j0 + lane) * N - row.off);
+#pragma unroll 1
+        for (int i = 0; i < N; i += kSome) {
+          float v[N];
+          Vec<T>::unpack(w, v);  // (its first kSome values)
+          fn(v, (j0 + lane) * N + i - row.off);
+          if constexpr (N > kSome) {
+            w.x = w.z;
+            w.y = w.w;
+          }
+        }
       }
     } else {
       constexpr int kUnroll = 4;
@@ -329,15 +376,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   const float ch = scale.k64 * (1.f / kTable), per_bin = ch * ((float)(kBins - 1) / kSpan);
   const bool apart = lowest != lowest;
   auto weight_of = [&](float v) { return one_weight(v, m, lowest, scale, sh.exp2); };
-  // The weights of a vector's values.
+  // The weights of kSome values.
   auto weights_of = [&](const float* v, Weight* w) {
     if (apart) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = {v[i] == m ? 1 << 22 : 0, 0};
+      for (int i = 0; i < kSome; ++i) w[i] = {v[i] == m ? 1 << 22 : 0, 0};
       return;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = scaled_weight(fmaxf(v[i], lowest), scale, sh.exp2);
+    for (int i = 0; i < kSome; ++i) w[i] = scaled_weight(fmaxf(v[i], lowest), scale, sh.exp2);
   };
   // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
   // a bin is a range of keys).
@@ -529,9 +576,17 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     __syncthreads();
     return sh.cut;
   };
-  // The smallest key whose linear bin is at most `bin`, by one probe a lane.
+  // The smallest key whose linear bin is at most `bin`, by one probe a lane: first of the 32 keys
+  // around the bins' inverse, which mostly hold it.
   auto first_key = [&](int bin) {
     uint32_t lo = 0x00800000u, hi = (uint32_t)(top >> 32);  // linear(hi) = 0
+    const uint32_t near = min(max(ordered(m - (float)(bin + 1) / per_bin), lo + 16u), hi) - 16u;
+    {
+      const uint32_t in = __ballot_sync(
+          0xffffffffu, near + (uint32_t)lane >= hi || linear(unordered(near + (uint32_t)lane)) <= bin);
+      const int at = __ffs(in) - 1;
+      if (at > 0) return min(near + (uint32_t)at, hi);
+    }
     while (lo < hi) {
       const uint32_t step = (hi - lo + 31) / 32, probe = min(hi, lo + (uint32_t)lane * step);
       const uint32_t in = __ballot_sync(0xffffffffu, linear(unordered(probe)) <= bin);
@@ -553,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       clear(3 * kFine);
       each(kDear, [&](const float* v, int a) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < kSome; ++i) {
           const uint32_t key = ordered(v[i]);
           if (key < lo || key > hi || place(v[i], a + i) < limit) continue;
           add_mass((int)((hi - key) >> shift), mass ? (uint64_t)weight_of(v[i]) : 1ull);
@@ -573,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     int64_t mine = 0;
     each(kDear, [&](const float* v, int a) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
+      for (int i = 0; i < kSome; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
     });
     mine = warp_sum(mine);
     __syncthreads();
@@ -621,12 +676,19 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   // Counts of the kept tokens in the linear bins, those at positions below hi.
   auto count = [&](bool limited, float hi) {
     clear(kBins);
-    each(kLight, [&](const float* v, int a) {
+    if (limited) {
+      each(kLight, [&](const float* v, int a) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (v[i] > -INFINITY && !(position(v[i]) >= hi) && (!limited || place(v[i], a + i) >= cut))
-          atomicAdd(&sh.bins[linear(v[i])], 1u);
-    });
+        for (int i = 0; i < N; ++i)
+          if (place(v[i], a + i) >= cut) atomicAdd(&sh.bins[linear(v[i])], 1u);
+      });
+    } else {
+      each(kLight, [&](const float* v, int) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (v[i] > -INFINITY && !(position(v[i]) >= hi)) atomicAdd(&sh.bins[linear(v[i])], 1u);
+      });
+    }
     merge_counts();
   };
   // The whole rest from a list of every token that can be kept: the first k of them, those with
@@ -702,24 +764,32 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     // nine times the estimate's deviation (0.0024 of a bin's, evenly spread) are a window some
     // twenty times narrower than the bounds.  A cut outside it is seen, and the bounds taken.
     constexpr int kEach = kBins / kThreads;
-    constexpr float kWidth = kSpan / (float)(kBins - 1);
-    auto low_mass = [&](int bin, float n) { return bin < kBins - 1 ? n * ex2(-kWidth * (float)(bin + 1)) : 0.f; };
-    auto high_mass = [&](int bin, float n) { return n * ex2(-kWidth * (float)bin); };
-    auto mid_mass = [&](int bin, float n) { return n * ex2(-kWidth * ((float)bin + 0.5f)); };
-    // prefix sums over the block, a thread for kEach bins: the three masses and the counts; the
-    // variances' sum
+    static_assert(kEach == 8, "two vectors of counts a thread");
+    uint32_t n_of[kEach];
+    *reinterpret_cast<uint4*>(n_of) = reinterpret_cast<const uint4*>(sh.all)[2 * tid];
+    *reinterpret_cast<uint4*>(n_of + 4) = reinterpret_cast<const uint4*>(sh.all)[2 * tid + 1];
+    // 2^-width: the weights at a bin's two ends; from the bin's middle
+    constexpr float kRatio = bin_ratio(1.0), kMiddle = bin_ratio(0.5);
+    const float first = ex2(-(kSpan / (float)(kBins - 1)) * (float)(tid * kEach));
+    // prefix sums over the block, a thread for kEach bins: the masses' bounds and estimate, and the
+    // counts; the variances' sum
     float up[4] = {0.f, 0.f, 0.f, 0.f}, all[4];
     int up_n = 0;
+    auto add_bins = [&](auto fn) {
+      float high = first;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int bin = tid * kEach + i;
-      const float n = (float)count_at(bin), w = mid_mass(bin, n);
-      up[0] += low_mass(bin, n);
-      up[1] += high_mass(bin, n);
-      up[2] += w;
-      up[3] += sizeof(T) == 2 ? w * w : w * w / fmaxf(n, 1.f);
-      up_n += (int)count_at(bin);
-    }
+      for (int i = 0; i < kEach; ++i, high *= kRatio) {
+        const int bin = tid * kEach + i;
+        const float n = (float)n_of[i], w = n * (high * kMiddle);
+        up[0] += bin < kBins - 1 ? n * (high * kRatio) : 0.f;
+        up[1] += n * high;
+        up[2] += w;
+        up[3] += sizeof(T) == 2 ? w * w : w * w / fmaxf(n, 1.f);
+        up_n += (int)n_of[i];
+        fn(bin);
+      }
+    };
+    add_bins([](int) {});
     {
       float to[4];
       int to_n = up_n;
@@ -756,18 +826,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     const float t[4] = {q * all[0] * 0.999f, q * all[1] * 1.001f, q * all[2] - margin, q * all[2] + margin};
     int at[4] = {kBins - 1, kBins - 1, kBins - 1, kBins - 1};
     const int n_first = up_n;  // tokens before this thread's bins
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int bin = tid * kEach + i;
-      const float n = (float)count_at(bin);
-      up[1] += high_mass(bin, n);
-      up[0] += low_mass(bin, n);
-      up[2] += mid_mass(bin, n);
+    add_bins([&](int bin) {
       if (up[1] >= t[0]) at[0] = min(at[0], bin);
       if (up[0] >= t[1]) at[1] = min(at[1], bin);
       if (up[2] >= t[2]) at[2] = min(at[2], bin);
       if (up[2] >= t[3]) at[3] = min(at[3], bin);
-    }
+    });
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       at[i] = __reduce_min_sync(0xffffffffu, at[i]);
@@ -784,7 +848,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     for (int k = 0; k < 3; ++k) {
       if ((ends[k] - (k == 2)) / kEach != tid) continue;
       int n = n_first;
-      for (int bin = tid * kEach; bin < ends[k]; ++bin) n += (int)count_at(bin);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) n += tid * kEach + i < ends[k] ? (int)n_of[i] : 0;
       sh.n_before[k] = n;
     }
     __syncthreads();
@@ -815,17 +880,17 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         all_h = all_l = up_h = up_l = 0;
       };
       each(kDear, [&](const float* v, int a) {
-        Weight w[N];
+        Weight w[kSome];
         weights_of(v, w);
         if (limited) {
 #pragma unroll
-          for (int i = 0; i < N; ++i)
+          for (int i = 0; i < kSome; ++i)
             if (place(v[i], a + i) < cut) w[i] = {0, 0};
         }
         if ((++held & (kHold - 1)) == 0) widen();
         bool any = false;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < kSome; ++i) {
           all_h += w[i].high;
           all_l += w[i].low;
           if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
@@ -836,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         }
         if (!__any_sync(0xffffffffu, any)) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < kSome; ++i) {
           const bool in = in_window(v[i]) && place(v[i], a + i) >= cut;
           const uint32_t who = __ballot_sync(0xffffffffu, in);
           const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
@@ -868,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           }
           each(kDear, [&](const float* v, int a) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < kSome; ++i) {
               if (in_window(v[i]) && place(v[i], a + i) >= cut) fn(v[i], a + i);
             }
           });
@@ -912,6 +977,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       break;
     }
   }
+  // (not earlier: a next call's first CTAs, the long rows', would take their places two by two on the
+  // SMs that are done first; mixed rows, call after call: 78 us that way, 63 this way)
+  griddep_launch_dependents();
   if (!done) {
     // ---- the kept tokens' sums by warps, then the draw in index order ----
     auto kept_weight = [&](float v, int index) {  // -1: not kept
@@ -933,20 +1001,20 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     } else if (cut == kMasked + 1 && mp == 0.f) {  // no filter
       int h = 0, l = 0, held = 0;
       each(kDear, [&](const float* v, int) {
-        Weight w[N];
+        Weight w[kSome];
         weights_of(v, w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < kSome; ++i) {
           h += w[i].high;
           l += w[i].low;
         }
         float x = v[0];
 #pragma unroll
-        for (int i = 1; i < N; ++i) x = fminf(x, v[i]);
-        n_kept += N;
+        for (int i = 1; i < kSome; ++i) x = fminf(x, v[i]);
+        n_kept += kSome;
         if (x == -INFINITY) {  // (few vectors have a masked token)
 #pragma unroll
-          for (int i = 0; i < N; ++i) n_kept -= v[i] == -INFINITY;
+          for (int i = 0; i < kSome; ++i) n_kept -= v[i] == -INFINITY;
         }
         if ((++held & (kHold - 1)) == 0) {
           mass += units({h, l});
@@ -1011,7 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           float v[N];
           Weight w[N];
           Vec<T>::unpack(vector(j), v);
-          weights_of(v, w);
+#pragma unroll
+          for (int i = 0; i < N; i += kSome) weights_of(v + i, w + i);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             e[i] = units(w[i]);
@@ -1089,6 +1158,8 @@ cudaError_t launch_token_sample(const tv_token_args* a, int sm_count, cudaStream
   int C = 1;
   const int most = a->B <= 4 ? kMaxCluster : kMaxCluster / 2;
   while (C < most && (int64_t)a->B * C <= sm_count && a->vocab >= 28ll * kThreads * C) C *= 2;
+  p.B = a->B;
+  p.sorted = p.top_p && a->B <= kSorted && (int64_t)a->B * C > sm_count;
   return a->logits_dt == TV_BF16 ? launch<__nv_bfloat16>(p, a->B, C, st) : launch<float>(p, a->B, C, st);
 }
 

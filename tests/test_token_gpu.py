@@ -79,6 +79,21 @@ def test_mixed_rows(B, V, spread, dt):
           m=np.where(i % 4 == 1, 0.01, 0.0))
 
 
+@pytest.mark.parametrize("B", [200, 512, 513, 1300])
+def test_more_rows_than_fit_at_once(B):
+    # long and short rows in any order, rows that are refused among them
+    logits, u = rows(17, B, 300)
+    g = np.random.default_rng(17)
+    pick = lambda *v: g.choice(v, B)
+    kw = dict(temperature=pick(1.0, 0.7, 0.0), k=pick(0, 0, 7, 400), p=pick(1.0, 0.9, 0.5),
+              m=pick(0.0, 0.0, 0.01))
+    check(logits, u, **kw)
+    kw["temperature"][::3] = -1.0
+    tokens, kept = sample(logits.cuda(), u, status=tv.TV_ERR_INVALID_ARG, **kw)
+    assert (tokens[::3] == -1).all() and (kept[::3] == 0).all()
+    assert (np.delete(kept, np.s_[::3]) > 0).all()
+
+
 @pytest.mark.parametrize("V", [64, 4096, 131072])
 def test_equal_logits(V):
     # n equal weights: sums are exact, a draw is floor(u n), a nucleus ceil(p n), by index
