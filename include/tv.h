@@ -802,7 +802,7 @@ typedef struct {
                                 outside the cache (it reads as zeros). */
 } tv_shared_args;
 
-/* Bytes of workspace (partial results: 2 KB for each row of the batch, twice, and about 22 MB);
+/* Bytes of workspace (partial results: 2 KB for each row of the batch, twice, and about 20 MB);
  * depends on B, H, Q, G and the device.  0 for invalid arguments. */
 size_t tv_shared_attn_workspace_size(const tv_shared_args* a);
 

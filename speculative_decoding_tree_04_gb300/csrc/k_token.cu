@@ -30,6 +30,15 @@
 // distributed shared memory, each CTA the same share of them, and given to every CTA, which all
 // take the same decisions from the same numbers.  Sums are of integers: no result depends on the
 // order they are taken in, or on how a row is split.
+//
+// Measured, in a graph of such calls (64 rows of 163840 floats; 256 of 50257 bf16; 1 of 32000 bf16):
+// greedy 12, 5.8 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 31 and 15; no filter 38, 38 and
+// 10; top_p 81, 82 and 31.  What bounds it: the weights' passes take 12 us for a CTA's 40960 logits
+// (73 % of the issue slots, which the float pipe's 31 operations and some 15 integer ones fill), two
+// CTAs of an SM one after the other, and the 256 CTAs of either batch are 2 on most of the 152
+// SMs; counting, 9 us, its atomics' conflicts; the rest is latency between the cluster's
+// barriers, about 1 us each.  Packed float operations gave the same times (their lanes are the same),
+// and so did counting during the first pass below a guessed maximum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
