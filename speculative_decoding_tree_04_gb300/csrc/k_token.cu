@@ -61,6 +61,8 @@ constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
 constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
 constexpr int kSome = 4;       // values of a vector that the passes with weights take at once
+constexpr int kTabled = 16;    // with at least so many tokens a thread
+constexpr int kValues = 4096;  // values whose weights are taken once
 constexpr int kHold = 64;      // of these whose weights' parts, of 2^22, are added as ints
 constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
@@ -80,8 +82,13 @@ struct TokenParams {
 
 struct Shared {
   ScaledTable exp2;
-  alignas(16) uint32_t bins[3 * kFine];  // this CTA's: counts (kBins), or 15-bit parts of weights' sums
-  alignas(16) int64_t all[kFine]; // the cluster's: counts (kBins of 32 bits), or sums
+  union {
+    struct {
+      alignas(16) uint32_t bins[3 * kFine];  // this CTA's: counts (kBins), or 15-bit parts of weights' sums
+      alignas(16) int64_t all[kFine];        // the cluster's: counts (kBins of 32 bits), or sums
+    };
+    int64_t values[kValues + 1];  // between these uses: the weights of a bf16 row's values, and 0
+  };
   uint64_t window_of[kWarps][kWindow];  // the warps' tokens of the window
   uint64_t list[kList];           // this CTA's tokens: key, complemented index
   uint64_t merged[kList];         // the cluster's,
@@ -395,6 +402,46 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
 #pragma unroll
     for (int i = 0; i < kSome; ++i) w[i] = scaled_weight(fmaxf(v[i], lowest), scale, sh.exp2);
   };
+  // bf16: the weights of all values from the maximum down to `lowest`, but those next to 0, in a
+  // table: the negative ones by falling magnitude (its bits a <= low_a), then the others (a <= high_a),
+  // both of them down to cut_a, which is where they fill the table (for logits of ordinary size
+  // 2^-13 or less).
+  const int low_a = lowest <= 0.f ? (int)(__float_as_uint(lowest) >> 16 & 0x7FFFu) + 1 : -1;
+  const int high_a = m >= 0.f ? (int)(__float_as_uint(m) >> 16 & 0x7FFFu) : -1;
+  const int cut_a = max(low_a < 0 || high_a < 0 ? max(low_a, high_a) + 1 - kValues
+                                                : (low_a + high_a + 3 - kValues) >> 1, 0);
+  const int n_negative = max(low_a - cut_a + 1, 0), top_a = n_negative + high_a;
+  const bool tabled = sizeof(T) == 2 && !apart && per * N >= kTabled * kThreads;
+  auto make_values = [&]() {
+    for (int i = tid; i <= kValues; i += kThreads) {
+      const bool negative = i < n_negative;
+      const int a = (negative ? low_a : top_a) - i;
+      const float v = __uint_as_float((uint32_t)max(a, 0) << 16 | (negative ? 0x80000000u : 0u));
+      const bool is = a >= cut_a && i < kValues && v >= lowest && v <= m;
+      sh.values[i] = is ? units(scaled_weight(v, scale, sh.exp2)) : 0;
+    }
+    __syncthreads();
+  };
+  // (what lies past either end of the table weighs nothing; a value next to 0 is seen by the caller,
+  // who finds the smallest magnitude below next_to_0)
+  const float next_to_0 = __uint_as_float((uint32_t)cut_a << 16);
+  auto value_weight = [&](float v) {
+    const uint32_t u = __float_as_uint(v);
+    const int i = ((int)u < 0 ? low_a : top_a) - (int)(u >> 16 & 0x7FFFu);
+    return sh.values[min((uint32_t)i, (uint32_t)kValues)];
+  };
+  auto value_weights = [&](const float* v, int64_t* w) {
+    float least_of = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < kSome; ++i) least_of = fminf(least_of, fabsf(v[i]));
+    if (least_of < next_to_0) {
+#pragma unroll
+      for (int i = 0; i < kSome; ++i) w[i] = weight_of(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSome; ++i) w[i] = value_weight(v[i]);
+    }
+  };
   // A token's place in the order, larger first; a value's bin, rising as the value falls (so that
   // a bin is a range of keys).
   auto place = [&](float v, int index) {
@@ -402,8 +449,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   };
   auto position = [&](float v) { return (m - v) * per_bin; };
   auto linear = [&](float v) { return min((int)position(v), kBins - 1); };
-  // Bins b0 .. b1 are the positions y >= b0 that are not at or past the end of b1 (NaN: none is).
-  auto end_of = [&](int bin) { return bin < kBins - 1 ? (float)(bin + 1) : NAN; };
   constexpr uint64_t kMasked = (uint64_t)0x007FFFFFu << 32 | 0xFFFFFFFFu;  // -inf, any index
   uint64_t cut = kMasked + 1;  // tokens at or above it are kept
   const float mp = fminf(fmaxf(min_p, 0.f), 1.f);
@@ -533,19 +578,41 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     }
     return n;
   };
-  // The list of the tokens at positions from lo up to hi (and not before the cut).
-  auto gather = [&](float lo, float hi) {
+  // The smallest key whose linear bin is at most `bin`, by one probe a lane: first of the 32 keys
+  // around the bins' inverse, which mostly hold it.
+  auto first_key = [&](int bin) {
+    uint32_t lo = 0x00800000u, hi = (uint32_t)(top >> 32);  // linear(hi) = 0
+    const uint32_t near = min(max(ordered(m - (float)(bin + 1) / per_bin), lo + 16u), hi) - 16u;
+    {
+      const uint32_t in = __ballot_sync(
+          0xffffffffu, near + (uint32_t)lane >= hi || linear(unordered(near + (uint32_t)lane)) <= bin);
+      const int at = __ffs(in) - 1;
+      if (at > 0) return min(near + (uint32_t)at, hi);
+    }
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32, probe = min(hi, lo + (uint32_t)lane * step);
+      const uint32_t in = __ballot_sync(0xffffffffu, linear(unordered(probe)) <= bin);
+      const int at = __ffs(in) - 1;  // (none: the answer lies above the last probe)
+      if (at == 0) return lo;
+      const uint32_t below = lo + (uint32_t)(at < 0 ? 31 : at - 1) * step;
+      hi = at < 0 ? hi : min(hi, lo + (uint32_t)at * step);
+      lo = min(hi, below + 1);
+    }
+    return lo;
+  };
+  // The list of the tokens from the bins first .. last that are not behind the cut.
+  auto gather = [&](int first, int last) {
+    const float above_it = first > 0 ? unordered(first_key(first - 1)) : INFINITY;
+    const float from = unordered(first_key(last));
     start_list();
     each(kLight, [&](const float* v, int a) {
-      bool any = false;  // (few vectors have one)
+      float x = v[0];  // (few vectors have one: of those from the first bin on, by their largest)
 #pragma unroll
-      for (int i = 0; i < N; ++i) any |= position(v[i]) >= lo && !(position(v[i]) >= hi);
-      if (!any) return;
+      for (int i = 1; i < N; ++i) x = fmaxf(x, v[i]);
+      if (!(x >= from)) return;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float y = position(v[i]);
-        if (y >= lo && !(y >= hi) && place(v[i], a + i) >= cut) put_on_list(v[i], a + i);
-      }
+      for (int i = 0; i < N; ++i)
+        if (v[i] >= from && v[i] < above_it && place(v[i], a + i) >= cut) put_on_list(v[i], a + i);
     });
     return join_lists();
   };
@@ -584,28 +651,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     }
     __syncthreads();
     return sh.cut;
-  };
-  // The smallest key whose linear bin is at most `bin`, by one probe a lane: first of the 32 keys
-  // around the bins' inverse, which mostly hold it.
-  auto first_key = [&](int bin) {
-    uint32_t lo = 0x00800000u, hi = (uint32_t)(top >> 32);  // linear(hi) = 0
-    const uint32_t near = min(max(ordered(m - (float)(bin + 1) / per_bin), lo + 16u), hi) - 16u;
-    {
-      const uint32_t in = __ballot_sync(
-          0xffffffffu, near + (uint32_t)lane >= hi || linear(unordered(near + (uint32_t)lane)) <= bin);
-      const int at = __ffs(in) - 1;
-      if (at > 0) return min(near + (uint32_t)at, hi);
-    }
-    while (lo < hi) {
-      const uint32_t step = (hi - lo + 31) / 32, probe = min(hi, lo + (uint32_t)lane * step);
-      const uint32_t in = __ballot_sync(0xffffffffu, linear(unordered(probe)) <= bin);
-      const int at = __ffs(in) - 1;  // (none: the answer lies above the last probe)
-      if (at == 0) return lo;
-      const uint32_t below = lo + (uint32_t)(at < 0 ? 31 : at - 1) * step;
-      hi = at < 0 ? hi : min(hi, lo + (uint32_t)at * step);
-      lo = min(hi, below + 1);
-    }
-    return lo;
   };
   // The cut among more tokens than a list holds, of keys lo .. hi, `target` tokens (or weight)
   // into them: by key, level by level, then the first tokens at the last key by index.
@@ -682,9 +727,18 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     sync();
     return sh.cut;
   };
-  // Counts of the kept tokens in the linear bins, those at positions below hi.
+  // Counts of the kept tokens in the linear bins, those at positions below hi; hi 0: of all,
+  // masked ones too, which are in the last bin.
   auto count = [&](bool limited, float hi) {
     clear(kBins);
+    if (hi == 0.f && !limited) {  // (one atomic after another, without a branch)
+      each(kLight, [&](const float* v, int) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) atomicAdd(&sh.bins[linear(v[i])], 1u);
+      });
+      merge_counts();
+      return;
+    }
     if (limited) {
       each(kLight, [&](const float* v, int a) {
 #pragma unroll
@@ -693,6 +747,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       });
     } else {
       each(kLight, [&](const float* v, int) {
+        float x = v[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) x = fmaxf(x, v[i]);
+        if (position(x) >= hi) return;  // (most vectors)
 #pragma unroll
         for (int i = 0; i < N; ++i)
           if (v[i] > -INFINITY && !(position(v[i]) >= hi)) atomicAdd(&sh.bins[linear(v[i])], 1u);
@@ -734,9 +792,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
 
   bool limited = false, counted = false, done = false;
   if (top_k > 0 && top_k < p.V) {
-    // (mostly a third of the span holds k tokens, and most of the others need no count)
+    // (mostly the first part of the span holds k tokens, and most of the others need no count)
     int64_t before, total;
-    count(false, (float)(kBins / 3));
+    count(false, (float)(top_k <= 128 ? kBins / 6 : kBins / 3));
     int bin = find(kBins, count_at, (int64_t)top_k - 1, &before, &total);
     if (total < top_k) {
       count(false, NAN);
@@ -746,11 +804,11 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     if (top_k <= total) {
       const int64_t here = count_at(bin);
       if (before + here <= kSmall) {
-        const int n = gather(0.f, end_of(bin));
+        const int n = gather(0, bin);
         finish_in_list(n, top_k, top_p, 0);
         done = true;
       } else if (here <= kList) {
-        const int n = gather((float)bin, end_of(bin));
+        const int n = gather(bin, bin);
         cut = cut_in_list(n, false, (int64_t)top_k - 1 - before);
       } else {
         cut = refine(false, first_key(bin), bin > 0 ? first_key(bin - 1) - 1 : (uint32_t)(top >> 32),
@@ -766,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   int n_above = 0, n_own = 0;  // tokens above the window, of the row; more that are kept, the lane's
   int b0 = 0, b1 = kBins - 1;
   if (top_p < 1.f && !done) {
-    if (!counted) count(limited, NAN);
+    if (!counted) count(limited, 0.f);
     // The cut's window from the counts: bounds of the running sums (their weights lie within a
     // bin's; 1e-3: roundings of bins and of these sums), and an estimate from the bins' middles.
     // Of a float row's many tokens in a bin the errors cancel, a bf16 row's in one bin are equal:
@@ -876,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       const float over = b0 > 0 ? unordered(first_key(b0 - 1) - 1) : INFINITY;
       const float under = unordered(first_key(b1));
       auto fine = [&](float v) { return min(max((int)((position(v) - from) * scale), 0), kFine - 1); };
-      auto in_window = [&](float v) { return v <= over && v >= under; };
+      auto in_window = [&](float v) { return (v <= over) & (v >= under); };
       if (tid == 0) sh.too_many = 0;
       __syncthreads();
       int64_t sum = 0;
@@ -888,7 +946,39 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         above += units({up_h, up_l});
         all_h = all_l = up_h = up_l = 0;
       };
-      each(kDear, [&](const float* v, int a) {
+      auto collect = [&](const float* v, int a, bool any) {
+        if (!__any_sync(0xffffffffu, any)) return;
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+          bool in = in_window(v[i]);
+          if (limited) in = in && place(v[i], a + i) >= cut;
+          const uint32_t who = __ballot_sync(0xffffffffu, in);
+          if (who == 0u) continue;
+          const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
+          if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
+          n_window += __popc(who);
+        }
+      };
+      // (of a limited row all tokens above the window are kept: the cut lies in it)
+      if (tabled) {
+        make_values();
+        each(kDear, [&](const float* v, int a) {
+          bool any = false;
+          int64_t w[kSome];
+          value_weights(v, w);
+          if (limited) {
+#pragma unroll
+            for (int i = 0; i < kSome; ++i) w[i] = place(v[i], a + i) < cut ? 0 : w[i];
+          }
+#pragma unroll
+          for (int i = 0; i < kSome; ++i) {
+            sum += w[i];
+            above += v[i] > over ? w[i] : 0;
+            any |= in_window(v[i]);
+          }
+          collect(v, a, any);
+        });
+      } else each(kDear, [&](const float* v, int a) {
         Weight w[kSome];
         weights_of(v, w);
         if (limited) {
@@ -902,21 +992,13 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         for (int i = 0; i < kSome; ++i) {
           all_h += w[i].high;
           all_l += w[i].low;
-          if (v[i] > over) {  // (of a limited row all such are kept: the cut lies in the window)
+          if (v[i] > over) {
             up_h += w[i].high;
             up_l += w[i].low;
           }
           any |= in_window(v[i]);
         }
-        if (!__any_sync(0xffffffffu, any)) return;
-#pragma unroll
-        for (int i = 0; i < kSome; ++i) {
-          const bool in = in_window(v[i]) && place(v[i], a + i) >= cut;
-          const uint32_t who = __ballot_sync(0xffffffffu, in);
-          const int place_of = n_window + __popc(who & ((1u << lane) - 1u));
-          if (in && place_of < kWindow) sh.window_of[warp][place_of] = place(v[i], a + i);
-          n_window += __popc(who);
-        }
+        collect(v, a, any);
       });
       widen();
       if (n_window > kWindow && lane == 0) sh.too_many = 1;
@@ -926,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       totals_of(W, all_above, too_many);
       const int64_t share = min(max((int64_t)ceil((double)q * (double)W), (int64_t)1), W);
       if (small) {
-        const int n = gather(0.f, end_of(b1));
+        const int n = gather(0, b1);
         finish_in_list(n, 0, top_p, share);
         done = true;
       } else {
@@ -1007,7 +1089,18 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         mass += weight_of(unordered((uint32_t)(x >> 32)));
         ++n_kept;
       }
-    } else if (cut == kMasked + 1 && mp == 0.f) {  // no filter
+    } else if (cut == kMasked + 1 && mp == 0.f && tabled) {  // no filter
+      make_values();
+      each(kDear, [&](const float* v, int) {
+        int64_t w[kSome];
+        value_weights(v, w);
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) {
+          mass += w[i];
+          n_kept += v[i] > -INFINITY;
+        }
+      });
+    } else if (cut == kMasked + 1 && mp == 0.f) {
       int h = 0, l = 0, held = 0;
       each(kDear, [&](const float* v, int) {
         Weight w[kSome];

@@ -151,6 +151,23 @@ def test_around_zero_and_far_apart():
     check(y, [0.0, 0.5, 0.99], temperature=1e30, k=4, p=0.8)
 
 
+@pytest.mark.parametrize("f", [dict(), dict(p=0.9), dict(k=900, p=0.8), dict(p=0.99, m=1e-4)])
+def test_bf16_values_of_any_size(f):
+    # the weights of a row's values are taken from a table, those of values next to 0 are not:
+    # negative maxima, tiny ones, rows far from 0, rows around it, wide and narrow ones
+    B, V = 12, 30011
+    logits, u = rows(18, B, V, torch.float32, 1.0)
+    spread = torch.tensor([3, 3, 3, 1e-3, 1e-6, 2, 2, 300, 0.1, 5, 3, 3.0])[:, None]
+    shift = torch.tensor([-20, 0, 40, 0, 0, 1000, -1000, 0, -0.6, 0, 0, -13.2])[:, None]
+    t = np.array([1, 1, 1, 1, 1e-7, 1, 1, 40, 0.05, 0.1, 30, 1.0])
+    x = logits * spread + shift
+    x[9] = x[9] * (torch.arange(V) % 3 == 0)          # zeros
+    x[10, ::2] = torch.randn(len(x[10, ::2]), generator=torch.Generator().manual_seed(1)) * 1e-30
+    x[11] = -x[11].abs() * 1e-3                        # none above 0, the largest next to it
+    x[1, ::5] = float("-inf")
+    check(x.to(torch.bfloat16), u, temperature=t, **f)
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_draws_next_to_boundaries(dt):
     # uniforms at the two floats around a boundary of the running sums, where they are farther
