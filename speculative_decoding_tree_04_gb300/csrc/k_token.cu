@@ -31,14 +31,18 @@
 // take the same decisions from the same numbers.  Sums are of integers: no result depends on the
 // order they are taken in, or on how a row is split.
 //
+// A bf16 row has few values: where it is long their weights are taken once, into a table, and the
+// passes look them up.
+//
 // Measured, in a graph of such calls (64 rows of 163840 floats; 256 of 50257 bf16; 1 of 32000 bf16):
-// greedy 12, 5.8 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 31 and 15; no filter 38, 38 and
-// 10; top_p 81, 82 and 31.  What bounds it: the weights' passes take 12 us for a CTA's 40960 logits
-// (73 % of the issue slots, which the float pipe's 31 operations and some 15 integer ones fill), two
-// CTAs of an SM one after the other, and the 256 CTAs of either batch are 2 on most of the 152
-// SMs; counting, 9 us, its atomics' conflicts; the rest is latency between the cluster's
-// barriers, about 1 us each.  Packed float operations gave the same times (their lanes are the same),
-// and so did counting during the first pass below a guessed maximum.
+// greedy 12, 5.7 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 29 and 15; no filter 38, 30 and
+// 10; top_p 77, 68 and 31.  What bounds it: instructions.  A float's weight takes 31 float operations
+// and some 15 integer ones, 12 us for a CTA's 40960 (73 % of the issue slots); a table's look-up
+// half of that, its window tests and sums included; a count five, and 6.5 cycles for the
+// atomics' conflicts.  Two CTAs of an SM run one after the other, and the 256 CTAs of either batch
+// are two on most of the 152 SMs; the rest is latency between the cluster's barriers, about 1 us
+// each.  Packed float operations gave the same times (their lanes are the same), and so did
+// counting during the first pass below a guessed maximum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -61,8 +65,9 @@ constexpr int kList = 512;     // tokens of a list at most
 constexpr int kSmall = 256;    // of one that holds every kept token
 constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
 constexpr int kSome = 4;       // values of a vector that the passes with weights take at once
-constexpr int kTabled = 16;    // with at least so many tokens a thread
-constexpr int kValues = 4096;  // values whose weights are taken once
+constexpr int kValues = 4096;  // values of a bf16 row whose weights are taken once, where a thread has
+constexpr int kTabled = 28;    // so many tokens (256 rows, top_p, 8192 tokens: 31.0 us without the
+                               // table, 32.9 with it; 16384: 39.3 and 37.7; 50257: 81 and 68)
 constexpr int kHold = 64;      // of these whose weights' parts, of 2^22, are added as ints
 constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
@@ -978,28 +983,30 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           }
           collect(v, a, any);
         });
-      } else each(kDear, [&](const float* v, int a) {
-        Weight w[kSome];
-        weights_of(v, w);
-        if (limited) {
+      } else {
+        each(kDear, [&](const float* v, int a) {
+          Weight w[kSome];
+          weights_of(v, w);
+          if (limited) {
 #pragma unroll
-          for (int i = 0; i < kSome; ++i)
-            if (place(v[i], a + i) < cut) w[i] = {0, 0};
-        }
-        if ((++held & (kHold - 1)) == 0) widen();
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < kSome; ++i) {
-          all_h += w[i].high;
-          all_l += w[i].low;
-          if (v[i] > over) {
-            up_h += w[i].high;
-            up_l += w[i].low;
+            for (int i = 0; i < kSome; ++i)
+              if (place(v[i], a + i) < cut) w[i] = {0, 0};
           }
-          any |= in_window(v[i]);
-        }
-        collect(v, a, any);
-      });
+          if ((++held & (kHold - 1)) == 0) widen();
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < kSome; ++i) {
+            all_h += w[i].high;
+            all_l += w[i].low;
+            if (v[i] > over) {
+              up_h += w[i].high;
+              up_l += w[i].low;
+            }
+            any |= in_window(v[i]);
+          }
+          collect(v, a, any);
+        });
+      }
       widen();
       if (n_window > kWindow && lane == 0) sh.too_many = 1;
       int64_t W = sum, all_above = above, too_many = 0;
@@ -1127,10 +1134,10 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     } else {
       const float cut_value = unordered((uint32_t)(cut >> 32));
       each(kLight, [&](const float* v, int a) {
-        bool any = false;  // (few vectors have one)
+        float x = v[0];  // (few vectors have one: their largest then is)
 #pragma unroll
-        for (int i = 0; i < N; ++i) any |= v[i] >= cut_value && !((m - v[i]) * ch > far);
-        if (!any) return;
+        for (int i = 1; i < N; ++i) x = fmaxf(x, v[i]);
+        if (!(x >= cut_value) || (m - x) * ch > far) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int64_t w = kept_weight(v[i], a + i);
