@@ -17,7 +17,8 @@
 //   3. (top_p) exact sums of the row and, by warp, of the tokens above the window; the warps keep
 //      the window's tokens (where they are too many, the row is read again instead), which are
 //      summed in kFine finer bins, one of which holds the cut;
-//   4. the tokens of the cut's bin go into a list, and are compared with one another;
+//   4. the tokens of the cut's bin go into a list, and are compared with one another; a bf16
+//      row's bin is one value, whose tokens are counted by warp, to find the cut's index;
 //   5. the kept tokens' sums by warp, unless 3 has left them, and the draw within one warp's
 //      slice.
 // Where the bins down to the cut hold few tokens altogether (top_k of common sizes, peaked
@@ -35,14 +36,14 @@
 // passes look them up.
 //
 // Measured, in a graph of such calls (64 rows of 163840 floats; 256 of 50257 bf16; 1 of 32000 bf16):
-// greedy 12, 5.7 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 29 and 15; no filter 38, 30 and
-// 10; top_p 77, 68 and 31.  What bounds it: instructions.  A float's weight takes 31 float operations
-// and some 15 integer ones, 12 us for a CTA's 40960 (73 % of the issue slots); a table's look-up
-// half of that, its window tests and sums included; a count five, and 6.5 cycles for the
-// atomics' conflicts.  Two CTAs of an SM run one after the other, and the 256 CTAs of either batch
-// are two on most of the 152 SMs; the rest is latency between the cluster's barriers, about 1 us
-// each.  Packed float operations gave the same times (their lanes are the same), and so did
-// counting during the first pass below a guessed maximum.
+// greedy 12, 5.8 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 29 and 15; no filter 38, 30 and
+// 10; top_p 75, 64 and 30 (8 rows of 163840 bf16: 37).  What bounds it: instructions.  A float's
+// weight takes 31 float operations and some 15 integer ones, 12 us for a CTA's 40960 (73 % of the issue
+// slots); a table's look-up half of that, its window tests and sums included; a count five, and
+// 6.5 cycles for the atomics' conflicts.  Two CTAs of an SM run one after the other, and the 256
+// CTAs of either batch are two on most of the 152 SMs; the rest is latency between the cluster's
+// barriers, about 1 us each.  Packed float operations gave the same times (their lanes are the
+// same), and so did counting during the first pass below a guessed maximum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -67,7 +68,7 @@ constexpr int kWindow = 256;   // of a window's tokens that a warp keeps
 constexpr int kSome = 4;       // values of a vector that the passes with weights take at once
 constexpr int kValues = 4096;  // values of a bf16 row whose weights are taken once, where a thread has
 constexpr int kTabled = 28;    // so many tokens (256 rows, top_p, 8192 tokens: 31.0 us without the
-                               // table, 32.9 with it; 16384: 39.3 and 37.7; 50257: 81 and 68)
+                               // table, 32.9 with it; 16384: 39.3 and 37.7)
 constexpr int kHold = 64;      // of these whose weights' parts, of 2^22, are added as ints
 constexpr int kAhead = 2;      // vectors of a lane's that are on their way
 
@@ -657,11 +658,80 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     __syncthreads();
     return sh.cut;
   };
+  // The cut at the n-th (from 0) of the tokens with this key, in order of index, those before the
+  // limit aside; kept: how many of the warp's are in window_of, -1: they have to be looked for.
+  auto nth_at = [&](uint32_t hi, int64_t n, uint64_t limit, int kept) {
+    int64_t mine = 0;
+    if (kept >= 0) {
+      for (int i = lane; i < kept; i += 32) mine += (uint32_t)(sh.window_of[warp][i] >> 32) == hi;
+    } else {
+      each(kDear, [&](const float* v, int a) {
+#pragma unroll
+        for (int i = 0; i < kSome; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
+      });
+    }
+    mine = warp_sum(mine);
+    __syncthreads();
+    if (lane == 0) sh.warp_count[warp] = (int)mine;
+    __syncthreads();
+    const int64_t all = warp_sum(lane < kWarps ? (int64_t)sh.warp_count[lane] : 0);
+    if (warp == 0 && lane < C) {
+      if (C == 1) sh.count[0] = (int)all;
+      else st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)all);
+    }
+    sync();
+    n -= warp_sum(lane < rank ? (int64_t)sh.count[lane] : (int64_t)0);
+    n -= warp_sum(lane < warp ? (int64_t)sh.warp_count[lane & (kWarps - 1)] : (int64_t)0);
+    auto found_it = [&](uint64_t x) {
+      for (int r = 0; r < C; ++r) {
+        if (C == 1) sh.cut = x;
+        else st_cluster_u64(&sh.cut, (uint32_t)r, x);
+      }
+    };
+    if (kept >= 0 && n >= 0 && n < mine) {  // on this warp's list
+      for (int i = lane; i < kept; i += 32) {
+        const uint64_t x = sh.window_of[warp][i];
+        if ((uint32_t)(x >> 32) != hi) continue;
+        int before = 0;
+        for (int k = 0; k < kept; ++k) {
+          const uint64_t y = sh.window_of[warp][k];
+          before += (uint32_t)(y >> 32) == hi && y > x;
+        }
+        if (before == n) found_it(x);
+      }
+    } else if (n >= 0 && n < mine) {  // in its slice
+      for (int j0 = w0; j0 < w1; j0 += 32) {
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = NAN;
+        if (j0 + lane < w1) Vec<T>::unpack(vector(j0 + lane), v);
+        const int a = (int)row.first(j0 + lane);
+        int64_t k = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) k += ordered(v[i]) == hi && v[i] == v[i] && place(v[i], a + i) >= limit;
+        const int64_t here = warp_sum(k);
+        if (n >= here) {
+          n -= here;
+          continue;
+        }
+        if (lane == locate(k, 32, &n)) {
+          uint64_t x = 0;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (ordered(v[i]) == hi && place(v[i], a + i) >= limit && n-- == 0) x = place(v[i], a + i);
+          found_it(x);
+        }
+        break;
+      }
+    }
+    sync();
+    return sh.cut;
+  };
   // The cut among more tokens than a list holds, of keys lo .. hi, `target` tokens (or weight)
   // into them: by key, level by level, then the first tokens at the last key by index.
   auto refine = [&](bool mass, uint32_t lo, uint32_t hi, int64_t target) {
     const uint64_t limit = cut;
-    for (;;) {
+    for (int step = 0; step < 3; ++step) {  // (2^32 keys, kFine bins)
       int shift = 0;
       while (((hi - lo) >> shift) >= (uint32_t)kFine) ++shift;
       clear(3 * kFine);
@@ -682,55 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       const uint32_t width = (1u << shift) - 1;
       lo = hi - lo > width ? hi - width : lo;
     }
-    // the tokens at this key before the last kept one; then its index
-    int64_t n = mass ? target / weight_of(unordered(hi)) : target;
-    int64_t mine = 0;
-    each(kDear, [&](const float* v, int a) {
-#pragma unroll
-      for (int i = 0; i < kSome; ++i) mine += ordered(v[i]) == hi && place(v[i], a + i) >= limit;
-    });
-    mine = warp_sum(mine);
-    __syncthreads();
-    if (lane == 0) sh.warp_count[warp] = (int)mine;
-    __syncthreads();
-    const int64_t all = warp_sum(lane < kWarps ? (int64_t)sh.warp_count[lane] : 0);
-    if (warp == 0 && lane < C) {
-      if (C == 1) sh.count[0] = (int)all;
-      else st_cluster_u32(&sh.count[rank], (uint32_t)lane, (uint32_t)all);
-    }
-    sync();
-    n -= warp_sum(lane < rank ? (int64_t)sh.count[lane] : (int64_t)0);
-    n -= warp_sum(lane < warp ? (int64_t)sh.warp_count[lane & (kWarps - 1)] : (int64_t)0);
-    if (n >= 0 && n < mine) {  // in this warp's slice
-      for (int j0 = w0; j0 < w1; j0 += 32) {
-        float v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = NAN;
-        if (j0 + lane < w1) Vec<T>::unpack(vector(j0 + lane), v);
-        const int a = (int)row.first(j0 + lane);
-        int64_t k = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) k += ordered(v[i]) == hi && v[i] == v[i] && place(v[i], a + i) >= limit;
-        const int64_t here = warp_sum(k);
-        if (n >= here) {
-          n -= here;
-          continue;
-        }
-        if (lane == locate(k, 32, &n)) {
-          uint64_t x = 0;
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (ordered(v[i]) == hi && place(v[i], a + i) >= limit && n-- == 0) x = place(v[i], a + i);
-          for (int r = 0; r < C; ++r) {
-            if (C == 1) sh.cut = x;
-            else st_cluster_u64(&sh.cut, (uint32_t)r, x);
-          }
-        }
-        break;
-      }
-    }
-    sync();
-    return sh.cut;
+    return nth_at(hi, mass ? target / weight_of(unordered(hi)) : target, limit, -1);
   };
   // Counts of the kept tokens in the linear bins, those at positions below hi; hi 0: of all,
   // masked ones too, which are in the last bin.
@@ -823,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       counted = false;
     }
   }
-  // ---- top_p; saved: the warps' sums of the tokens before the cut's list are there ----
+  // ---- top_p; saved: the lanes' sums of the kept tokens are there ----
   bool saved = false;
   int64_t above = 0;
   int n_above = 0, n_own = 0;  // tokens above the window, of the row; more that are kept, the lane's
@@ -833,8 +855,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     // The cut's window from the counts: bounds of the running sums (their weights lie within a
     // bin's; 1e-3: roundings of bins and of these sums), and an estimate from the bins' middles.
     // Of a float row's many tokens in a bin the errors cancel, a bf16 row's in one bin are equal:
-    // nine times the estimate's deviation (0.0024 of a bin's, evenly spread) are a window some
-    // twenty times narrower than the bounds.  A cut outside it is seen, and the bounds taken.
+    // five times the estimate's deviation (0.0025 of a bin's, evenly spread) are a window five to
+    // twenty times narrower than the bounds.  A cut outside it (one row in a million; rows whose
+    // logits lie on a grid like the bins') is seen, and the bounds taken.
     constexpr int kEach = kBins / kThreads;
     static_assert(kEach == 8, "two vectors of counts a thread");
     uint32_t n_of[kEach];
@@ -893,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
       up_n = to_n - up_n + warp_sum(lane < warp ? sh.warp_n[lane & (kWarps - 1)] : 0);
     }
     const float q = fmaxf(top_p, 0.f);
-    const float margin = 9.f * 0.0024f * sqrtf(all[3]) + 1e-5f * all[2];
+    const float margin = 5.f * 0.0025f * sqrtf(all[3]) + 1e-5f * all[2];
     // the first bins at which a running sum reaches a place: the bounds' ends, the estimate's
     const float t[4] = {q * all[0] * 0.999f, q * all[1] * 1.001f, q * all[2] - margin, q * all[2] + margin};
     int at[4] = {kBins - 1, kBins - 1, kBins - 1, kBins - 1};
@@ -1036,40 +1059,73 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
             }
           });
         };
-        const int64_t target = share - 1 - all_above;
-        clear(3 * kFine);
-        each_in_window([&](float v, int) {
-          const int64_t w = weight_of(v);
-          if (w > 0) add_mass(fine(v), (uint64_t)w);
-        });
-        merge_mass();
-        int64_t before, total;
-        const int bin = find(kFine, mass_at, target, &before, &total);
-        if ((target < 0 || target >= total) && (b0 != bound0 || b1 != bound1)) {
-          b0 = bound0;
-          b1 = bound1;
-          n_above = n_bound0;
-          continue;
-        }
-        // those before the cut's bin are kept, those in it go on a list
-        int64_t more = 0;
-        int n_more = 0;
-        start_list();
-        each_in_window([&](float v, int index) {
-          const int f = fine(v);
-          if (f == bin) put_on_list(v, index);
-          if (f >= bin) return;
-          more += weight_of(v);
-          ++n_more;
-        });
-        const int n = join_lists();
-        if (n <= kList) {
-          cut = cut_in_list(n, true, target - before);
-          saved = mp == 0.f;
-          above += more;
-          n_own = n_more;
+        int64_t target = share - 1 - all_above, before, total;
+        bool listed = true;
+        auto missed = [&]() { return (target < 0 || target >= total) && (b0 != bound0 || b1 != bound1); };
+        if constexpr (sizeof(T) == 2) {
+          // by value, one a bin (where the window holds values next to 0 in steps)
+          uint32_t first16 = (b0 > 0 ? ordered(over) : (uint32_t)(top >> 32)) >> 16, last16 = ordered(under) >> 16;
+          bool again = false;
+#pragma unroll 1
+          for (int step = 0; step < 2; ++step) {  // (2^16 values, kFine bins)
+            int shift = 0;
+            while (((first16 - last16) >> shift) >= (uint32_t)kFine) ++shift;
+            clear(3 * kFine);
+            each_in_window([&](float v, int) {
+              const uint32_t key16 = ordered(v) >> 16;
+              if (key16 > first16 || key16 < last16) return;
+              const int64_t w = weight_of(v);
+              if (w > 0) add_mass((int)((first16 - key16) >> shift), (uint64_t)w);
+            });
+            merge_mass();
+            const uint32_t at = (uint32_t)find(kFine, mass_at, target, &before, &total);
+            again = missed();
+            if (again) break;
+            target -= before;
+            first16 -= at << shift;
+            if (shift == 0) break;
+            last16 = max(last16, first16 - (1u << shift) + 1);
+          }
+          if (again) {
+            b0 = bound0;
+            b1 = bound1;
+            n_above = n_bound0;
+            continue;
+          }
+          const uint32_t key = first16 << 16 | (first16 & 0x8000u ? 0u : 0xFFFFu);
+          cut = nth_at(key, target / max(weight_of(unordered(key)), (int64_t)1), cut,
+                       too_many == 0 ? n_window : -1);
         } else {
-          cut = refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
+          clear(3 * kFine);
+          each_in_window([&](float v, int) {
+            const int64_t w = weight_of(v);
+            if (w > 0) add_mass(fine(v), (uint64_t)w);
+          });
+          merge_mass();
+          const int bin = find(kFine, mass_at, target, &before, &total);
+          if (missed()) {
+            b0 = bound0;
+            b1 = bound1;
+            n_above = n_bound0;
+            continue;
+          }
+          // the tokens of the cut's bin go on a list
+          start_list();
+          each_in_window([&](float v, int index) {
+            if (fine(v) == bin) put_on_list(v, index);
+          });
+          const int n = join_lists();
+          listed = n <= kList;
+          cut = listed ? cut_in_list(n, true, target - before)
+                       : refine(true, ordered(under), b0 > 0 ? ordered(over) : (uint32_t)(top >> 32), target);
+        }
+        saved = mp == 0.f && listed;
+        if (saved) {
+          each_in_window([&](float v, int index) {
+            if (place(v, index) < cut) return;
+            above += weight_of(v);
+            ++n_own;
+          });
         }
       }
       break;
@@ -1087,16 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     };
     int64_t mass = saved ? above : 0;
     int n_kept = saved ? n_own : 0;
-    if (saved) {
-      // (after top_p all but the kept tokens of this CTA's list are in the sums)
-      for (int i = lane; i < sh.list_n; i += 32) {
-        const uint64_t x = sh.list[i];
-        const int j = (int)((0xFFFFFFFFu - (uint32_t)x + row.off) / N);
-        if (x < cut || j < w0 || j >= w1) continue;
-        mass += weight_of(unordered((uint32_t)(x >> 32)));
-        ++n_kept;
-      }
-    } else if (cut == kMasked + 1 && mp == 0.f && tabled) {  // no filter
+    if (!saved && cut == kMasked + 1 && mp == 0.f && tabled) {  // no filter
       make_values();
       each(kDear, [&](const float* v, int) {
         int64_t w[kSome];
@@ -1107,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           n_kept += v[i] > -INFINITY;
         }
       });
-    } else if (cut == kMasked + 1 && mp == 0.f) {
+    } else if (!saved && cut == kMasked + 1 && mp == 0.f) {
       int h = 0, l = 0, held = 0;
       each(kDear, [&](const float* v, int) {
         Weight w[kSome];
@@ -1131,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         }
       });
       mass += units({h, l});
-    } else {
+    } else if (!saved) {
       const float cut_value = unordered((uint32_t)(cut >> 32));
       each(kLight, [&](const float* v, int a) {
         float x = v[0];  // (few vectors have one: their largest then is)

@@ -5,6 +5,8 @@ Tokens and counts have to be equal.  The library's weights are off by 2^-36 of t
 near to a boundary: with at most 2^18 boundaries in a row, that is one row in 10^5 or fewer of
 random inputs.  Inputs here are seeded, a few thousand rows in all.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -149,6 +151,32 @@ def test_around_zero_and_far_apart():
     y = torch.tensor([[3e38, -3e38, 1e38, 2.0, -2.0]]).repeat(3, 1)
     check(y, [0.0, 0.5, 0.99], k=4)
     check(y, [0.0, 0.5, 0.99], temperature=1e30, k=4, p=0.8)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1.0, 7.0])
+def test_logits_on_a_grid(dt, T):
+    # all of a bin's tokens on the same side of its middle, those of the upper bins on the other
+    # one: the running sums' estimate is off by more than chance would have it
+    g = torch.Generator().manual_seed(19)
+    width = 48 / 4095 * math.log(2) * T
+    j = torch.randint(0, 400, (1, 40000), generator=g).double()
+    x = -(j + torch.where(j < 100, 0.03, 0.97)) * width
+    x[0, 7] = 0.0
+    p = np.concatenate([np.linspace(0.02, 0.98, 40), [0.999, 0.9999]])
+    u = torch.rand(len(p), generator=g).numpy()
+    check(x.to(dt).repeat(len(p), 1), u, p=p, temperature=T)
+
+
+@pytest.mark.parametrize("V", [50257, 200000])
+def test_cuts_among_many_equal_bf16_logits(V):
+    # a few values, each some hundred to some ten thousand times
+    logits, u = rows(20, 10, V, torch.float32, 1.0)
+    x = logits * torch.tensor([0.5, 1, 3, 0.1, 0.02, 1, 1, 3, 0.5, 1])[:, None]
+    x[5:] = (x[5:] * 4).round() / 4 - 2
+    p = np.array([0.9, 0.95, 0.3, 0.5, 0.7, 0.2, 0.99, 0.9, 0.6, 0.01])
+    check(x.to(torch.bfloat16), u, p=p)
+    check(x.to(torch.bfloat16), u, p=p, m=0.01, k=[0, 5000, 0, V // 2, 0, 0, 30000, 0, 900, 0])
 
 
 @pytest.mark.parametrize("f", [dict(), dict(p=0.9), dict(k=900, p=0.8), dict(p=0.99, m=1e-4)])
