@@ -90,8 +90,8 @@ struct Shared {
   ScaledTable exp2;
   union {
     struct {
-      alignas(16) uint32_t bins[3 * kFine];  // this CTA's: counts (kBins), or 15-bit parts of weights' sums
-      alignas(16) int64_t all[kFine];        // the cluster's: counts (kBins of 32 bits), or sums
+      alignas(16) uint32_t bins[kBins];  // this CTA's: counts, or sums (kFine low halves, then high ones)
+      alignas(16) int64_t all[kFine];    // the cluster's: counts (kBins of 32 bits), or sums
     };
     int64_t values[kValues + 1];  // between these uses: the weights of a bf16 row's values, and 0
   };
@@ -114,7 +114,7 @@ struct Shared {
   uint64_t cut;
   uint32_t is_long[kWarps];
 };
-static_assert(kBins <= 2 * kFine && kFine / 4 >= kThreads && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
+static_assert(kBins == 2 * kFine && kFine / 4 >= kThreads && kBins % kThreads == 0 && kFine % kThreads == 0, "bins");
 
 __device__ __forceinline__ uint4 ld_cluster_v4(const void* local, uint32_t rank) {
   uint4 v;
@@ -468,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     __syncthreads();
   };
   auto add_mass = [&](int bin, uint64_t w) {
-    atomicAdd(&sh.bins[bin], (uint32_t)w & 0x7FFFu);
-    atomicAdd(&sh.bins[kFine + bin], (uint32_t)(w >> 15) & 0x7FFFu);
-    atomicAdd(&sh.bins[2 * kFine + bin], (uint32_t)(w >> 30));
+    const uint32_t low = (uint32_t)w, old = atomicAdd(&sh.bins[bin], low);
+    const uint32_t high = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
+    if (high) atomicAdd(&sh.bins[kFine + bin], high);
   };
   // The cluster's bins from the CTAs': every CTA adds up its share and gives it to all, a thread
   // for four bins and one CTA to read from and to give to (whole warps: kFine / 4 is at least a
@@ -490,16 +490,13 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     const int share = kFine >> log2_C;
     for (int i = first_bin; i < share; i += step) {
       const int at = rank * share + i;
-      uint4 x = get(&sh.bins[at], C, give_to), y = get(&sh.bins[kFine + at], C, give_to),
-            z = get(&sh.bins[2 * kFine + at], C, give_to);
-      x = add_up(x, C);
-      y = add_up(y, C);
-      z = add_up(z, C);
-      auto sum = [](uint32_t a, uint32_t b_, uint32_t c) {
-        return (uint64_t)a + ((uint64_t)b_ << 15) + ((uint64_t)c << 30);
+      const uint4 x = get(&sh.bins[at], C, give_to), y = get(&sh.bins[kFine + at], C, give_to);
+      auto sum = [&](uint32_t low, uint32_t high) {
+        uint64_t w = (uint64_t)high << 32 | low;
+        for (int o = C / 2; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        return w;
       };
-      const uint64_t s0 = sum(x.x, y.x, z.x), s1 = sum(x.y, y.y, z.y), s2 = sum(x.z, y.z, z.z),
-                     s3 = sum(x.w, y.w, z.w);
+      const uint64_t s0 = sum(x.x, y.x), s1 = sum(x.y, y.y), s2 = sum(x.z, y.z), s3 = sum(x.w, y.w);
       give(&sh.all[at], C, give_to,
            make_uint4((uint32_t)s0, (uint32_t)(s0 >> 32), (uint32_t)s1, (uint32_t)(s1 >> 32)));
       give(&sh.all[at + 2], C, give_to,
@@ -734,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
     for (int step = 0; step < 3; ++step) {  // (2^32 keys, kFine bins)
       int shift = 0;
       while (((hi - lo) >> shift) >= (uint32_t)kFine) ++shift;
-      clear(3 * kFine);
+      clear(2 * kFine);
       each(kDear, [&](const float* v, int a) {
 #pragma unroll
         for (int i = 0; i < kSome; ++i) {
@@ -1070,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           for (int step = 0; step < 2; ++step) {  // (2^16 values, kFine bins)
             int shift = 0;
             while (((first16 - last16) >> shift) >= (uint32_t)kFine) ++shift;
-            clear(3 * kFine);
+            clear(2 * kFine);
             each_in_window([&](float v, int) {
               const uint32_t key16 = ordered(v) >> 16;
               if (key16 > first16 || key16 < last16) return;
@@ -1096,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
           cut = nth_at(key, target / max(weight_of(unordered(key)), (int64_t)1), cut,
                        too_many == 0 ? n_window : -1);
         } else {
-          clear(3 * kFine);
+          clear(2 * kFine);
           each_in_window([&](float v, int) {
             const int64_t w = weight_of(v);
             if (w > 0) add_mass(fine(v), (uint64_t)w);

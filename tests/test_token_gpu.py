@@ -111,6 +111,29 @@ def test_equal_logits(V):
     assert n.tolist() == [24] * 6 and t.tolist() == [int(np.float32(v) * 24.0) for v in u]
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B", [6, 160])
+def test_as_many_equal_logits_as_there_can_be(B, dt):
+    # the sums of 2^18 of the largest weights need all but two bits; 160 rows: one CTA each
+    V = 1 << 18
+    g = torch.Generator().manual_seed(21)
+    x = torch.full((6, V), 0.5)
+    x[1, ::7] = 0.25
+    x[2] = 0.25 * torch.randint(0, 2, (V,), generator=g)
+    x[3, :3000] = torch.randn(3000, generator=g) - 1
+    x[4, 1::3] = -0.0
+    x[5] = torch.where(torch.rand(V, generator=g) < 0.7, 0.5, -3.0)
+    u = np.array([0.9, 0.3, 0.99999, 0.5, 0.7, 0.1])
+    for kw in (dict(p=[0.9, 0.95, 0.75, 0.99, 0.9999, 0.9999]), dict(k=[200000] * 6),
+               dict(k=[150000, 224695, 140000, 262143, 200000, 190000], p=[0.6] * 6)):
+        want = [dm.next_token(x[b].double().numpy(), u[b], 1.0, kw.get("k", [0] * 6)[b],
+                              kw.get("p", [1.0] * 6)[b], 0.0) for b in range(6)]
+        rep = np.arange(B) % 6
+        kw = {n: np.array(v)[rep] for n, v in kw.items()}
+        got = sample(x.to(dt).cuda()[torch.from_numpy(rep).cuda()], u[rep], **kw)
+        assert [(t, n) for t, n in zip(*got)] == [want[b] for b in rep]
+
+
 def test_ties_at_the_cut_go_to_the_lowest_index():
     # few distinct values, many times each
     g = torch.Generator().manual_seed(5)
