@@ -36,8 +36,8 @@
 // passes look them up.
 //
 // Measured, in a graph of such calls (64 rows of 163840 floats; 256 of 50257 bf16; 1 of 32000 bf16):
-// greedy 12, 5.8 and 4 us (3.5 TB/s of the first's 42 MB); top_k 34, 29 and 15; no filter 38, 30 and
-// 10; top_p 75, 64 and 30 (8 rows of 163840 bf16: 37).  What bounds it: instructions.  A float's
+// greedy 11, 5.3 and 4 us (3.9 TB/s of the first's 42 MB); top_k 30, 29 and 15; no filter 36, 28 and
+// 10; top_p 73, 62 and 28 (8 rows of 163840 bf16: 36).  What bounds it: instructions.  A float's
 // weight takes 31 float operations and some 15 integer ones, 12 us for a CTA's 40960 (73 % of the issue
 // slots); a table's look-up half of that, its window tests and sums included; a count five, and
 // 6.5 cycles for the atomics' conflicts.  Two CTAs of an SM run one after the other, and the 256
@@ -1061,7 +1061,8 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
         auto missed = [&]() { return (target < 0 || target >= total) && (b0 != bound0 || b1 != bound1); };
         if constexpr (sizeof(T) == 2) {
           // by value, one a bin (where the window holds values next to 0 in steps)
-          uint32_t first16 = (b0 > 0 ? ordered(over) : (uint32_t)(top >> 32)) >> 16, last16 = ordered(under) >> 16;
+          uint32_t first16 = (b0 > 0 ? ordered(over) : (uint32_t)(top >> 32)) >> 16;
+          uint32_t last16 = ordered(under) >> 16;
           bool again = false;
 #pragma unroll 1
           for (int step = 0; step < 2; ++step) {  // (2^16 values, kFine bins)
