@@ -1244,29 +1244,35 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
   const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int chunk = (int)(w & 31);
   const int64_t row = (w >> 5) * 32 + (threadIdx.x & 31);
-  if (row >= rows) return;
   const int64_t part2 = 2 * rows;
   const int b = (int)((uint32_t)row / (uint32_t)R), r = (int)row - b * R;
-  // (the records are prepare_kernel's, which has ended: the attention kernel lets this one start
-  // after that, and only its results have to be waited for)
-  const int4 rec = __ldg(seq_rec + b);
   int n1 = 0, n2 = 0, cut1 = 0, cut2 = 0, in1 = 0, rows1 = 0;
   const int in2 = r % kRows, rows2 = min(kRows, R - (r - in2));
-  if (rec.w >= 0) {
-    const int2 own = __ldg(tile_rec + rec.z + r / kRows);
-    n2 = own.x;
-    cut2 = own.y;
-    if (rec.x >= 0) {
-      const int g = (int)row - rec.y;
-      const int2 t = __ldg(tile_rec + rec.x + g / kRows);
-      n1 = t.x;
-      cut1 = t.y;
-      in1 = g % kRows;
-      rows1 = min(kRows, rec.w - (g - in1));
+  bool join = row < rows;
+  if (join) {
+    // (the records are prepare_kernel's, which has ended: the attention kernel lets this one start
+    // after that, and only its results have to be waited for)
+    const int4 rec = __ldg(seq_rec + b);
+    if (rec.w >= 0) {
+      const int2 own = __ldg(tile_rec + rec.z + r / kRows);
+      n2 = own.x;
+      cut2 = own.y;
+      if (rec.x >= 0) {
+        const int g = (int)row - rec.y;
+        const int2 t = __ldg(tile_rec + rec.x + g / kRows);
+        n1 = t.x;
+        cut1 = t.y;
+        in1 = g % kRows;
+        rows1 = min(kRows, rec.w - (g - in1));
+      }
+      join = n1 != 0 || n2 != 1;  // else written by the attention kernel
     }
-    if (n1 == 0 && n2 == 1) return;  // written by the attention kernel
   }
+  // Every thread waits, those with nothing to join as well: the attention kernel lets this one start
+  // before it has done its work, and what comes next in the stream is ordered behind this grid's end
+  // alone, which without the wait may come first (every row in one piece).
   griddep_wait();
+  if (!join) return;
   const int n = n1 + n2;
   float mx = -INFINITY, sum = 0.f;
   float acc[16];
