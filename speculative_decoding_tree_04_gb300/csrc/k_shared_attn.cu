@@ -145,9 +145,10 @@ struct Item {
   int tail;                    // keys of its last block if that is the segment's and not full
 };
 
+// (Ordinary loads: prepare_kernel may write the records while this kernel's blocks are there already,
+// so that the read-only path, for what nobody writes during a kernel, is not open to them.)
 __device__ __noinline__ Item decode(const Params& p, int item) {
-  const int4 a = __ldg(p.items + 3 * item), b = __ldg(p.items + 3 * item + 1),
-             c = __ldg(p.items + 3 * item + 2);
+  const int4 a = p.items[3 * item], b = p.items[3 * item + 1], c = p.items[3 * item + 2];
   Item it;
   it.row0 = a.x;
   it.nrows = a.y;
@@ -168,8 +169,8 @@ __device__ __noinline__ Item decode(const Params& p, int item) {
 
 // Item taken by cluster `cid` in round r, or -1 when it has none left.
 __device__ __forceinline__ int item_at(const Params& p, int r, int cid) {
-  const int k = __ldg(p.cl_start + cid) + r;
-  return k < __ldg(p.cl_start + cid + 1) ? k : -1;
+  const int k = p.cl_start[cid] + r;
+  return k < p.cl_start[cid + 1] ? k : -1;
 }
 
 // Cache row of the first key of the item's block j.  A page outside the cache gives a row past
@@ -1238,9 +1239,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
 // parts and the launch; the parts mostly come from L2.
 constexpr int kJoinThreads = 128;  // (blocks that fit beside the attention's, by registers)
 __global__ void __launch_bounds__(kJoinThreads, 5)
-    join_kernel(const int4* __restrict__ seq_rec, const int2* __restrict__ tile_rec, int64_t rows,
-                int R, const float* __restrict__ part_out, const float* __restrict__ part_lse,
-                void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
+    join_kernel(const int4* seq_rec, const int2* tile_rec, int64_t rows, int R, const float* part_out,
+                const float* part_lse, void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
   const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int chunk = (int)(w & 31);
   const int64_t row = (w >> 5) * 32 + (threadIdx.x & 31);
@@ -1251,15 +1251,15 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
   bool join = row < rows;
   if (join) {
     // (the records are prepare_kernel's, which has ended: the attention kernel lets this one start
-    // after that, and only its results have to be waited for)
-    const int4 rec = __ldg(seq_rec + b);
+    // after that, and only its results have to be waited for.  Read where they were written to, in L2)
+    const int4 rec = __ldcg(seq_rec + b);
     if (rec.w >= 0) {
-      const int2 own = __ldg(tile_rec + rec.z + r / kRows);
+      const int2 own = __ldcg(tile_rec + rec.z + r / kRows);
       n2 = own.x;
       cut2 = own.y;
       if (rec.x >= 0) {
         const int g = (int)row - rec.y;
-        const int2 t = __ldg(tile_rec + rec.x + g / kRows);
+        const int2 t = __ldcg(tile_rec + rec.x + g / kRows);
         n1 = t.x;
         cut1 = t.y;
         in1 = g % kRows;
@@ -1291,7 +1291,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
       // the piece's first part row
       const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
                                : (group ? row : part2 / 2 + row) - in;
-      l[q] = __ldg(part_lse + p0 + in);
+      l[q] = part_lse[p0 + in];  // (written while this grid was there: not by the read-only path)
       const float4* src =
           reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)4 * chunk * n_rows + in;
 #pragma unroll
