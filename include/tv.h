@@ -700,7 +700,9 @@ typedef struct {
   int32_t inverse;           /* 0 or 1 */
   tv_dtype dt;               /* F32 or BF16, of in and out */
   const void* in;
-  void* out;                 /* in itself (with the same strides), or memory apart from it */
+  void* out;                 /* in itself (with the same strides), or memory apart from it: its
+                                vectors may lie between in's where the strides are the same, or
+                                where a period of one stride holds both side by side */
   int64_t in_stride_token, in_stride_head, out_stride_token, out_stride_head; /* elements */
   const int32_t* positions;  /* device [T] */
   tv_rope_scaling scaling;

@@ -42,6 +42,44 @@ int64_t span(int64_t token, int64_t head, int64_t T, int64_t H, int64_t d) {
   return (T - 1) * token + (H - 1) * head + d;
 }
 
+// [T, H] vectors of d elements, `token` and `head` elements apart.
+struct Vectors {
+  int64_t token, head, d;
+};
+// Whether two such sets of one element type that start `off` elements apart share memory.  Slices of
+// one buffer mostly lie between one another's vectors: those of the same strides are told exactly,
+// others by the place in a stride's period that each keeps to (nothing else is: it counts as shared).
+bool meet(Vectors a, Vectors b, int64_t off, int64_t T, int64_t H) {
+  if (T == 1) a.token = b.token = 0;  // (a dimension of one has no stride)
+  if (H == 1) a.head = b.head = 0;
+  if (off >= span(a.token, a.head, T, H, a.d) || -off >= span(b.token, b.head, T, H, b.d)) return false;
+  if (a.token == b.token && a.head == b.head) {
+    // some differences dt and dh of the tokens and heads put b's vector within a's
+    for (int64_t dh = 1 - H; dh < H; ++dh) {
+      const int64_t at = off + dh * a.head;
+      int64_t dt = a.token > 0 ? (a.d - 1 - at) / a.token : 0;  // the largest one not behind a's end,
+      if (a.token > 0 && at + dt * a.token >= a.d) --dt;        // (division rounds to zero)
+      if (dt > T - 1) dt = T - 1;
+      if (dt > -T && at + dt * a.token < a.d && at + dt * a.token > -b.d) return true;
+    }
+    return false;
+  }
+  // multiples of m put aside, a lies in [0, an) and b in [at, at + bn)
+  auto apart_by = [&](int64_t m, int64_t an, int64_t bn) {
+    const int64_t at = (off % m + m) % m;
+    return at >= an && at + bn <= m;
+  };
+  for (const int64_t m : {a.token, b.token})
+    if (m > 0 && a.token % m == 0 && b.token % m == 0 &&
+        apart_by(m, (H - 1) * a.head + a.d, (H - 1) * b.head + b.d))
+      return false;
+  for (const int64_t m : {a.head, b.head})
+    if (m > 0 && a.head % m == 0 && b.head % m == 0 &&
+        apart_by(m, (T - 1) * a.token + a.d, (T - 1) * b.token + b.d))
+      return false;
+  return true;
+}
+
 int check_scaling(const tv_rope_scaling* s, int rot_dim, const char* who) {
   if (!s) return refuse(TV_ERR_INVALID_ARG, who, "scaling is NULL");
   if (rot_dim < 2 || rot_dim > 512 || rot_dim % 2)
@@ -89,6 +127,9 @@ int check_rope(const tv_rope_args* a) {
     if ((T > 1 && a->in_stride_token != a->out_stride_token) ||
         (H > 1 && a->in_stride_head != a->out_stride_head))
       return refuse(TV_ERR_INVALID_ARG, who, "in place needs equal strides");
+  } else if (meet({a->in_stride_token, a->in_stride_head, d}, {a->out_stride_token, a->out_stride_head, d},
+                  ((intptr_t)a->out - (intptr_t)a->in) / es, T, H)) {
+    return refuse(TV_ERR_INVALID_ARG, who, "out overlaps in");
   }
   const int64_t n_out = span(a->out_stride_token, a->out_stride_head, T, H, d) * es;
   if (overlap(a->out, n_out, a->positions, 4 * T))
