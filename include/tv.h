@@ -745,8 +745,8 @@ typedef struct {
   const int32_t* depth;      /* device [T], nullable; a negative one leaves its token alone */
   void* q_nope;              /* device [T, H, d_nope] contiguous out */
   void* q_pe;                /* device [T, H, d_rope] contiguous out */
-  void* c_kv;                /* cache arrays, rows of d_latent and d_rope elements */
-  void* k_pe;
+  void* c_kv;                /* cache arrays, rows of d_latent and d_rope elements; they may be */
+  void* k_pe;                /* slices of one, whose rows do not meet */
   int64_t ckv_row_stride, kpe_row_stride;
   tv_cache_layout cache;     /* any page size; num_rows > 0 */
   tv_rope_scaling scaling;

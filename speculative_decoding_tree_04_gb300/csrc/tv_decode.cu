@@ -192,7 +192,6 @@ int check_norm_rope(const tv_norm_rope_args* a) {
     in(a->kv, ((T - 1) * a->kv_stride_token + a->d_latent + a->d_rope) * es);
     in(a->kv_weight, a->d_latent * es);
     in(a->k_weight, a->d_rope * es);
-    // (the two arrays may be slices of one: each with the other's rows between its own)
     in(c.page_table, 4ll * a->B * c.max_pages);
     out(a->c_kv, (c.num_rows - 1) * a->ckv_row_stride + a->d_latent);
     out(a->k_pe, (c.num_rows - 1) * a->kpe_row_stride + a->d_rope);
@@ -207,6 +206,10 @@ int check_norm_rope(const tv_norm_rope_args* a) {
       if (y < n_query && overlap(outs[x], n_outs[x], outs[y], n_outs[y]))
         return refuse(TV_ERR_INVALID_ARG, who, "two outputs overlap");
   }
+  // (the cache's two arrays may be slices of one: each with the other's rows between its own)
+  if (a->kv && meet({a->ckv_row_stride, 0, a->d_latent}, {a->kpe_row_stride, 0, a->d_rope},
+                    ((intptr_t)a->k_pe - (intptr_t)a->c_kv) / es, a->cache.num_rows, 1))
+    return refuse(TV_ERR_INVALID_ARG, who, "c_kv and k_pe overlap");
   if (!aligned(a->q, es) || !aligned(a->kv, es) || !aligned(a->q_weight, es) ||
       !aligned(a->kv_weight, es) || !aligned(a->k_weight, es))
     return refuse(TV_ERR_INVALID_ARG, who, "tensors not aligned to their element size");

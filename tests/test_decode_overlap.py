@@ -8,6 +8,7 @@ import torch
 
 from speculative_decoding_tree_04_gb300 import tv
 from tests import test_decode_abi as abi
+from tests import test_rope_any_gpu as ropes
 
 BAD = tv.TV_ERR_INVALID_ARG
 IN = abi.FAKE
@@ -35,6 +36,24 @@ IN = abi.FAKE
 def test_rope_refuses_an_overlapping_output(tvlib, kw):
     a = abi.rope_args(**kw)
     assert tv.load().tv_rope(ctypes.byref(a), None) == BAD
+    assert b"overlap" in tv.load().tv_last_error()
+
+
+CKV = abi.FAKE + 6 * abi.M
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_pe=CKV), dict(k_pe=CKV + 4 * 64), dict(k_pe=CKV + 4 * (1023 * 64 + 63)),
+    dict(k_pe=CKV - 4 * 1023 * 16), dict(k_pe=CKV - 4 * 15),
+    # slices of one buffer's rows that meet, of their own row or the next one
+    dict(k_pe=CKV + 4 * 63, ckv_row_stride=80, kpe_row_stride=80),
+    dict(k_pe=CKV + 4 * 65, ckv_row_stride=80, kpe_row_stride=80),
+    dict(k_pe=CKV - 4 * 15, ckv_row_stride=80, kpe_row_stride=80),
+    dict(k_pe=CKV + 4 * 130, ckv_row_stride=200, kpe_row_stride=100),
+])
+def test_norm_rope_refuses_cache_arrays_that_meet(tvlib, kw):
+    a = abi.norm_args(**kw)
+    assert tv.load().tv_norm_rope(ctypes.byref(a), None) == BAD
     assert b"overlap" in tv.load().tv_last_error()
 
 
@@ -85,3 +104,18 @@ def test_slices_of_one_buffer(tvlib, dt):
         assert torch.equal(buf, want)
         taken[1] += 1
     assert (taken > 100).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("at", [(0, 512), (64, 0), (8, 536), (80, 8)])
+def test_cache_arrays_of_one_buffer(tvlib, at):
+    s = ropes.batch(21, [5, 1, 70], [0, 63, 30], 2, 16, 64, 512, torch.bfloat16)
+    want = ropes.apply(s)
+    wide = torch.full((s["rows"], 600), -77.0, dtype=torch.bfloat16, device="cuda")
+    c, k = wide[:, at[0]:at[0] + 512], wide[:, at[1]:at[1] + 64]
+    tv.norm_rope(None, s["kv"].cuda(), torch.from_numpy(s["start"]).cuda(),
+                 torch.tensor(s["prefixes"], dtype=torch.int32, device="cuda"), None, None, c, k,
+                 kv_weight=s["kv_weight"].cuda(), page_table=torch.from_numpy(s["table"]).cuda())
+    torch.cuda.synchronize()
+    assert (c.double().cpu().numpy() == want["c_kv"]).all()
+    assert (k.double().cpu().numpy() == want["k_pe"]).all()
