@@ -796,7 +796,7 @@ cudaError_t launch_rope_t(const tv_rope_args* a, cudaStream_t st) {
   const Grid s = grid_for(a->T, a->n_heads, p.width ? 32 / p.width : 1, (int)Turns<T>::bytes(a->rot_dim / 2), 4);
   p.per_block = s.per_block;
   p.tokens = s.tokens;
-  const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
+  const dim3 grid((unsigned)(((int64_t)a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
   const size_t smem = Turns<T>::bytes(a->rot_dim / 2) * s.tokens;
   auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
   if constexpr (sizeof(T) == 2)
@@ -861,7 +861,7 @@ cudaError_t launch_norm_rope_t(const tv_norm_rope_args* a, cudaStream_t st) {
   const Grid s = grid_for(a->T, p.H, p.q_width ? 32 / p.q_width : 1, (int)Turns<T>::bytes(a->rot_dim / 2), 3);
   p.per_block = s.per_block;
   p.tokens = s.tokens;
-  const dim3 grid((unsigned)((a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
+  const dim3 grid((unsigned)(((int64_t)a->T + s.tokens - 1) / s.tokens), (unsigned)s.groups);
   const size_t smem = Turns<T>::bytes(a->rot_dim / 2) * s.tokens;
   auto go = [&](auto kernel) { return start(kernel, grid, s.threads, smem, st, p, inv); };
   if constexpr (sizeof(T) == 2)

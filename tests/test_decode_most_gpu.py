@@ -1,0 +1,44 @@
+"""GPU tests of the rotations with as many tokens as a call may name."""
+import pytest
+import torch
+
+from speculative_decoding_tree_04_gb300 import tv
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("tvlib")]
+T = 2 ** 31 - 1
+
+
+@pytest.fixture
+def many():
+    """One pair a token, 8.6 GB, and every token's position."""
+    x = torch.empty((T, 1, 2), dtype=torch.bfloat16, device="cuda")
+    x.view(T, 2).copy_(torch.tensor([1.0, -0.5], device="cuda").bfloat16().expand(T, 2))
+    yield x
+    del x
+    torch.cuda.empty_cache()
+
+
+PARTS = [slice(first, first + 5000) for first in (0, 1 << 30, T - 5000)]
+
+
+def test_rope_of_the_most_tokens(many):
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    want = [torch.empty_like(many[part]) for part in PARTS]
+    for part, alone in zip(PARTS, want):
+        tv.rope(many[part], alone, pos[part])
+    tv.rope(many, many, pos)
+    for part, alone in zip(PARTS, want):
+        assert torch.equal(many[part], alone)
+
+
+def test_norms_of_the_most_tokens(many):
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    weight = torch.tensor([1.0, 2.0], device="cuda").bfloat16()
+    out = torch.full_like(many, -77.0)
+    tv.norm_rope(many, None, i32([0, T]), i32([0]), None, out, None, None, q_weight=weight)
+    for part in PARTS:
+        alone = torch.empty_like(many[part])
+        tv.norm_rope(many[part], None, i32([0, 5000]), i32([part.start]), None, alone, None, None,
+                     q_weight=weight)
+        assert torch.equal(out[part], alone)
