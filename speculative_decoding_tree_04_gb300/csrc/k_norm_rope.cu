@@ -577,19 +577,19 @@ struct NormRopeParams {
 // The sequence of packed token t: the last b with q_start[b] <= t (-1 if there is none, B past
 // the last), by one warp in rounds of 32 probes.
 __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ q_start, int B, int64_t t, int lane) {
-  int lo = 0, n = B + 1;  // the answer is lo - 1 .. lo + n - 1
+  uint32_t lo = 0, n = (uint32_t)B + 1;  // the answer is lo - 1 .. lo + n - 1
   while (n > 0) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const bool le = lane * step < n && __ldg(q_start + i) <= t;
+    const uint32_t step = (n + 31) / 32, i = lo + (uint32_t)lane * step;
+    const bool le = (uint32_t)lane * step < n && __ldg(q_start + i) <= t;
     const uint32_t m = __ballot_sync(0xffffffffu, le);
-    const int c = __popc(m);  // probes at or below t (entries ascend)
-    if (c == 0) return lo - 1;
-    const int last = lo + (c - 1) * step;
-    const int end = min(lo + n, last + step);
+    const uint32_t c = (uint32_t)__popc(m);  // probes at or below t (entries ascend)
+    if (c == 0) break;
+    const uint32_t last = lo + (c - 1) * step;
+    const uint32_t end = min(lo + n, last + step);
     lo = last + 1;
     n = end - lo;
   }
-  return lo - 1;
+  return (int)lo - 1;
 }
 
 template <typename T, int NV, bool kSwap>

@@ -1,4 +1,4 @@
-"""GPU tests of the rotations with as many tokens as a call may name."""
+"""GPU tests of the rotations and norms with as many tokens, and sequences, as a call may name."""
 import pytest
 import torch
 
@@ -42,3 +42,23 @@ def test_norms_of_the_most_tokens(many):
         tv.norm_rope(many[part], None, i32([0, 5000]), i32([part.start]), None, alone, None, None,
                      q_weight=weight)
         assert torch.equal(out[part], alone)
+
+
+@pytest.mark.parametrize("B", [2 ** 31 - 1, 2 ** 31 - 32, 2 ** 30 + 5])
+def test_norms_of_the_most_sequences(B):
+    # all but three of them empty, ones before, between and behind
+    i32 = dict(dtype=torch.int32, device="cuda")
+    owner, n = [B // 3, B - 2, B - 1], [4, 1, 6]
+    start, prefix = torch.zeros(B + 1, **i32), torch.zeros(B, **i32)
+    at = 0
+    for b, k in zip(owner, n):
+        at += k
+        start[b + 1:] = at
+        prefix[b] = 100 + k
+    g = torch.Generator(device="cuda").manual_seed(41)
+    q = torch.randn((at + 2, 3, 64), generator=g, device="cuda").bfloat16()
+    out, want = torch.full_like(q, -77.0), torch.full_like(q, -77.0)
+    tv.norm_rope(q, None, start, prefix, None, out, None, None)
+    tv.norm_rope(q, None, torch.tensor([0, 4, 5, 11], **i32), torch.tensor([104, 101, 106], **i32),
+                 None, want, None, None)
+    assert torch.equal(out, want) and (out[at:] == -77.0).all()
