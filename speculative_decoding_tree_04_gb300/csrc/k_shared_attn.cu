@@ -1236,14 +1236,18 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const PrepArgs a)
 // and the rows of sequences out of bounds: out = 0, lse = -inf.  A warp takes 32 rows, one a lane,
 // and 16 of the 512 columns: four 16-byte loads a piece, which lie side by side over the lanes, four
 // pieces' on their way at once.  1024 rows of two to three pieces: 6 us, latency of the records, the
-// parts and the launch; the parts mostly come from L2.
+// parts and the launch; the parts mostly come from L2.  Where there are many rows (kSome) a warp
+// takes `chunks` times 16 columns, one after another: rows in one piece leave it nothing to do, and
+// each warp costs its start (64 sequences of 300 keys, 524288 rows: 636 us, with 16 columns a warp
+// everywhere 780; 73728 rows 111 and 126; where all of 73728 rows are joined, 247 and 255).
 constexpr int kJoinThreads = 128;  // (blocks that fit beside the attention's, by registers)
+template <bool kSome>
 __global__ void __launch_bounds__(kJoinThreads, 5)
     join_kernel(const int4* seq_rec, const int2* tile_rec, int64_t rows, int R, const float* part_out,
-                const float* part_lse, void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
-  const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int chunk = (int)(w & 31);
-  const int64_t row = (w >> 5) * 32 + (threadIdx.x & 31);
+                const float* part_lse, void* __restrict__ out, int out_bf16, float* __restrict__ lse,
+                int chunks) {
+  const int64_t first = ((int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)) * (kSome ? chunks : 1);
+  const int64_t row = (first >> 5) * 32 + (threadIdx.x & 31);
   const int64_t part2 = 2 * rows;
   const int b = (int)((uint32_t)row / (uint32_t)R), r = (int)row - b * R;
   int n1 = 0, n2 = 0, cut1 = 0, cut2 = 0, in1 = 0, rows1 = 0;
@@ -1274,60 +1278,65 @@ __global__ void __launch_bounds__(kJoinThreads, 5)
   griddep_wait();
   if (!join) return;
   const int n = n1 + n2;
-  float mx = -INFINITY, sum = 0.f;
-  float acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  int chunk = (int)(first & 31);
+  const int end = kSome ? chunk + chunks : 0;
 #pragma unroll 1
-  for (int k0 = 0; k0 < n; k0 += 4) {
-    float l[4];
-    float4 v[4][4];
+  do {
+    float mx = -INFINITY, sum = 0.f;
+    float acc[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      l[q] = -INFINITY;
-      if (k0 + q >= n) continue;
-      const bool group = k0 + q < n1;
-      const int j = group ? k0 + q : k0 + q - n1, in = group ? in1 : in2, n_rows = group ? rows1 : rows2;
-      // the piece's first part row
-      const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
-                               : (group ? row : part2 / 2 + row) - in;
-      l[q] = part_lse[p0 + in];  // (written while this grid was there: not by the read-only path)
-      const float4* src =
-          reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)4 * chunk * n_rows + in;
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += 4) {
+      float l[4];
+      float4 v[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[q][e] = __ldcs(src + e * n_rows);
-    }
+      for (int q = 0; q < 4; ++q) {
+        l[q] = -INFINITY;
+        if (k0 + q >= n) continue;
+        const bool group = k0 + q < n1;
+        const int j = group ? k0 + q : k0 + q - n1, in = group ? in1 : in2, n_rows = group ? rows1 : rows2;
+        // the piece's first part row
+        const int64_t p0 = j > 0 ? part2 + (int64_t)((group ? cut1 : cut2) + j - 1) * kRows
+                                 : (group ? row : part2 / 2 + row) - in;
+        l[q] = part_lse[p0 + in];  // (written while this grid was there: not by the read-only path)
+        const float4* src =
+            reinterpret_cast<const float4*>(part_out + p0 * kDL) + (int64_t)4 * chunk * n_rows + in;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (l[q] == -INFINITY) continue;  // a piece without a visible key, or none
-      const float m = fmaxf(mx, l[q]);  // (a NaN is nobody's maximum; its weight is NaN)
-      const float old = expf(mx - m), e1 = expf(l[q] - m);
-      mx = m;
-      sum = sum * old + e1;
+        for (int e = 0; e < 4; ++e) v[q][e] = __ldcs(src + e * n_rows);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[4 * e] = acc[4 * e] * old + e1 * v[q][e].x;
-        acc[4 * e + 1] = acc[4 * e + 1] * old + e1 * v[q][e].y;
-        acc[4 * e + 2] = acc[4 * e + 2] * old + e1 * v[q][e].z;
-        acc[4 * e + 3] = acc[4 * e + 3] * old + e1 * v[q][e].w;
+      for (int q = 0; q < 4; ++q) {
+        if (l[q] == -INFINITY) continue;  // a piece without a visible key, or none
+        const float m = fmaxf(mx, l[q]);  // (a NaN is nobody's maximum; its weight is NaN)
+        const float old = expf(mx - m), e1 = expf(l[q] - m);
+        mx = m;
+        sum = sum * old + e1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[4 * e] = acc[4 * e] * old + e1 * v[q][e].x;
+          acc[4 * e + 1] = acc[4 * e + 1] * old + e1 * v[q][e].y;
+          acc[4 * e + 2] = acc[4 * e + 2] * old + e1 * v[q][e].z;
+          acc[4 * e + 3] = acc[4 * e + 3] * old + e1 * v[q][e].w;
+        }
       }
     }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint32_t word[8];
-  if (out_bf16) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t word[8];
+    if (out_bf16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) word[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    st_global_v8((unsigned char*)out + row * (kDL * 2) + 32 * chunk, word);
-  } else {
+      for (int i = 0; i < 8; ++i) word[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+      st_global_v8((unsigned char*)out + row * (kDL * 2) + 32 * chunk, word);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) word[i] = __float_as_uint(acc[8 * e + i] * inv);
-      st_global_v8((unsigned char*)out + row * (kDL * 4) + 64 * chunk + 32 * e, word);
+        for (int i = 0; i < 8; ++i) word[i] = __float_as_uint(acc[8 * e + i] * inv);
+        st_global_v8((unsigned char*)out + row * (kDL * 4) + 64 * chunk + 32 * e, word);
+      }
     }
-  }
-  if (chunk == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    if (chunk == 0 && lse) lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
+  } while (kSome && ++chunk < end);
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -1525,15 +1534,21 @@ cudaError_t launch_shared_attn(const tv_shared_args* a, void* ws, cudaStream_t s
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, shared_attn_kernel, p, lat_s, kpe, lat_o, q, qr);
   if (e != cudaSuccess) return e;
-  const int64_t join_warps = (rows + 31) / 32 * 32;
+  // sixteen columns a warp, up to eight times the warps that the GPU holds of this kernel; beyond
+  // that more of them, down to a warp for each 32 rows
+  int chunks = 1;
+  while (chunks < 32 && (rows + 31) / 32 * (32 / chunks) > 8ll * 5 * (kJoinThreads / 32) * current_sm_count())
+    chunks *= 2;
+  const int64_t join_warps = (rows + 31) / 32 * (32 / chunks);
   cfg.gridDim = dim3((unsigned)((join_warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   at[0] = at[1];  // no clusters; launched early as well
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, (const int4*)pa.seq_rec, (const int2*)pa.tile_rec, rows,
-                            (int)R, (const float*)p.part_out, (const float*)p.part_lse, a->out, p.out_bf16,
-                            a->lse);
+  return cudaLaunchKernelEx(&cfg, chunks > 1 ? join_kernel<true> : join_kernel<false>,
+                            (const int4*)pa.seq_rec, (const int2*)pa.tile_rec, rows, (int)R,
+                            (const float*)p.part_out, (const float*)p.part_lse, a->out, p.out_bf16,
+                            a->lse, chunks);
 }
 
 }  // namespace tv
