@@ -410,12 +410,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_sample_kernel(const TokenPa
   };
   // bf16: the weights of all values from the maximum down to `lowest`, but those next to 0, in a
   // table: the negative ones by falling magnitude (its bits a <= low_a), then the others (a <= high_a),
-  // both of them down to cut_a, which is where they fill the table (for logits of ordinary size
-  // 2^-13 or less).
+  // both of them down to cut_a, which is where they, or one of them alone, fill the table (for logits
+  // of ordinary size 2^-13 or less).
   const int low_a = lowest <= 0.f ? (int)(__float_as_uint(lowest) >> 16 & 0x7FFFu) + 1 : -1;
   const int high_a = m >= 0.f ? (int)(__float_as_uint(m) >> 16 & 0x7FFFu) : -1;
-  const int cut_a = max(low_a < 0 || high_a < 0 ? max(low_a, high_a) + 1 - kValues
-                                                : (low_a + high_a + 3 - kValues) >> 1, 0);
+  const int alone = max(low_a, high_a) + 1 - kValues;
+  const int cut_a = max(max(alone, low_a < 0 || high_a < 0 ? 0 : (low_a + high_a + 3 - kValues) >> 1), 0);
   const int n_negative = max(low_a - cut_a + 1, 0), top_a = n_negative + high_a;
   const bool tabled = sizeof(T) == 2 && !apart && per * N >= kTabled * kThreads;
   auto make_values = [&]() {
