@@ -689,7 +689,8 @@ int tv_rope_frequencies(const tv_rope_scaling* scaling, int rot_dim, double* fre
  * a way back to un-rotated keys, at magnitude 1).  The angle runs in double.  float32 results
  * are within one unit of the last place of the formula in double, and equal tv_rope_neox's where
  * that can express them; bf16 results are rounded once from a value within 2^-20 (|a| + |b|)
- * times the magnitude.
+ * times the magnitude, so that one in some thousands has another last bit than tv_rope_neox and
+ * tv_verify_prologue store, which round the correctly rounded float32 value.
  */
 typedef struct {
   uint32_t struct_size;      /* sizeof(tv_rope_args): ABI check */
@@ -719,7 +720,9 @@ int tv_rope(const tv_rope_args* a, void* stream);
  * or x where w is NULL, and R the rotation of the first rot_dim elements:
  *     q[t,h] = (q_nope, q_pe):  N(q[t,h]; q_weight), its last d_rope elements through R
  *     kv[t] = (latent, rope):   c_kv row = N(latent; kv_weight),  k_pe row = R N(rope; k_weight)
- * Sums, products and the rotation are 32-bit (the angle in double), rounded once.  q_nope and
+ * Sums, products and the rotation are 32-bit (the angle in double), rounded once: the sum of a
+ * vector's squares, and its mean with eps, have to lie within a float's normal range (elements up
+ * to 10^16 do).  A bf16 rotation is tv_rope's, not to the last bit tv_verify_prologue's.  q_nope and
  * q_pe are what tv_prefill_attn takes; with d_nope = 0 only q_pe is written, for queries that
  * were taken into the latent space.
  */

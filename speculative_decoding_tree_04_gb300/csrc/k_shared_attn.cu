@@ -32,7 +32,7 @@
 //
 // Measured, in a graph of such calls: 64 samples of a prompt of 8192 keys with 300 of their own, 16
 // heads, 48 us (tv_verify_attn: 146); three prompts, 64 sequences, 64 heads, 89 us (153); draft
-// trees of nine nodes, 21 sequences, 69 us (89); four samples of 700 keys 25 us (49).  Of the 48:
+// trees of nine nodes, 21 sequences, 65 us (89); four samples of 700 keys 25 us (49).  Of the 48:
 // prepare_kernel 5.5, the first scores 5 later, steps of 1.45 to 1.65 us (85 % of the bf16 peak while
 // they last), 4 until the last one's sums are out, 2 to 4 for the tile's 256 KB of partial results
 // per cluster, 2 between the kernels and 6 for the join.

@@ -36,14 +36,19 @@
 // passes look them up.
 //
 // Measured, in a graph of such calls (64 rows of 163840 floats; 256 of 50257 bf16; 1 of 32000 bf16):
-// greedy 11, 5.3 and 4 us (3.9 TB/s of the first's 42 MB); top_k 30, 29 and 15; no filter 36, 28 and
-// 10; top_p 73, 62 and 28 (8 rows of 163840 bf16: 36).  What bounds it: instructions.  A float's
-// weight takes 31 float operations and some 15 integer ones, 12 us for a CTA's 40960 (73 % of the issue
-// slots); a table's look-up half of that, its window tests and sums included; a count five, and
-// 6.5 cycles for the atomics' conflicts.  Two CTAs of an SM run one after the other, and the 256
-// CTAs of either batch are two on most of the 152 SMs; the rest is latency between the cluster's
-// barriers, about 1 us each.  Packed float operations gave the same times (their lanes are the
-// same), and so did counting during the first pass below a guessed maximum.
+// greedy 9.7, 5.3 and 4.2 us (4.3 TB/s of the first's 42 MB); top_k 40 31, 30 and 16; no filter 36, 28
+// and 10; top_p 0.95 72, 62 and 29 (8 rows of 163840 bf16: 36).  What bounds it with a filter: a
+// CTA's own chain of passes.  A float's weight takes 31 float operations and some 15 integer ones, 12
+// us for a CTA's 40960 (73 % of the issue slots while it lasts); a table's look-up half of that, its
+// window tests and sums included; a count five, and 6.5 cycles for the atomics' conflicts; then
+// barriers, a cluster's about 1 us each, and what a thread does once.  Over a whole call no unit is
+// full (issue slots 48 % in the bf16 batch, 60 % on the busiest SM): its 256 CTAs are two side by side
+// on 104 of the 152 SMs and one on the others, which take nine tenths of the time of two.
+// Mixed filters: the rows with top_p alone take two to three times the others' time, and the others'
+// SMs wait (SMs active 61 % of the call, issue slots 24 %).  Greedy rows wait for memory (12 of 26
+// cycles between a warp's instructions) and the cluster's start and end.  Packed float operations gave
+// the same times (their lanes are the same), and so did counting during the first pass below a
+// guessed maximum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
