@@ -154,8 +154,8 @@ int check_norm_rope(const tv_norm_rope_args* a) {
     return refuse(TV_ERR_INVALID_ARG, who, "bad layout");
   if (!type_ok(a->dt)) return refuse(TV_ERR_INVALID_ARG, who, "bad dtype");
   if (!(a->eps >= 0.f) || std::isinf(a->eps)) return refuse(TV_ERR_INVALID_ARG, who, "bad eps");
-  if (!a->q && !a->kv) return refuse(TV_ERR_INVALID_ARG, who, "neither q nor kv");
   if (a->B == 0 || a->T == 0) return TV_OK;
+  if (!a->q && !a->kv) return refuse(TV_ERR_INVALID_ARG, who, "neither q nor kv");
   if (!a->q_start || !a->prefix_len) return refuse(TV_ERR_INVALID_ARG, who, "NULL pointer");
   const int64_t es = size_of(a->dt), T = a->T, H = a->H;
   constexpr int64_t kMost = 1ll << 31;
